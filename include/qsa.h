@@ -499,6 +499,180 @@ QSA_API qsa_status qsa_sparse_mla_decode(const qsa_bf16 *q, int32_t n_heads, con
                                          int32_t max_rows, int32_t B, float softmax_scale, qsa_bf16 *out, float *lse,
                                          void *ws, size_t ws_bytes, qsa_stream stream);
 
+/* ------------------------------------------------------------------ paged K/V cache
+ * A cache cut into pages of page_size tokens, for layers that read their whole (or windowed)
+ * history and for serving many requests from one pool. A pool plane is [n_pages][page_size][...]
+ * (token-major inside a page, as the flat caches above); row r of a page table [n_rows][table_ld]
+ * int32 lists the pages of one sequence in order: its token t is at
+ *   slot = table[r * table_ld + t / page_size] * page_size + t % page_size,
+ * and its K row of KV head h at k_cache + (slot * n_kv_heads + h) * head_dim ("3090x3で 314 万
+ * コンテキスト", section "カーネルを書き換えずに済む": the same row address, with the slot in the
+ * token's place). Entries behind a sequence's last page are not read; pages may be shared by
+ * several rows. */
+typedef struct {
+    int32_t n_q_heads;   /* query head h reads KV head h / (n_q_heads / n_kv_heads); at most 16 per KV head */
+    int32_t n_kv_heads;
+    int32_t head_dim;    /* 64, 128 or 256 (FP8 rows: 128 or 256) */
+    int32_t page_size;   /* tokens per page, >= 1 (no power of two needed) */
+    int32_t window;      /* > 0: the new token sees the last `window` cached tokens only; 0: all */
+    float softmax_scale; /* <= 0 selects 1/sqrt(head_dim) */
+} qsa_paged_config;
+
+/* Rotary positions. Pair i (0 <= i < rot_dim / 2) of a head turns by the angle p f_i:
+ *   y[a] = amplitude (x[a] cos(p f_i) - x[b] sin(p f_i)),  y[b] = amplitude (x[b] cos(p f_i) + x[a] sin(p f_i))
+ * with (a, b) = rot_begin + (i, i + rot_dim / 2) (halves) or rot_begin + (2i, 2i + 1) (interleaved);
+ * other dims pass through. f_i = base^(-2i / rot_dim), rescaled for contexts longer than the trained
+ * one by `scaling`:
+ *   LINEAR    f_i / factor;
+ *   NTK       the base becomes base x factor^(rot_dim / (rot_dim - 2));
+ *   BY_PARTS  f_i (1 - g) + g f_i / factor with g = clamp((i - lo) / (hi - lo), 0, 1), lo = max(floor(c(beta_fast)), 0),
+ *             hi = min(ceil(c(beta_slow)), rot_dim / 2 - 1) (hi - lo at least 0.001), c(b) = (rot_dim / 2)
+ *             ln(original_len / (2 pi b)) / ln(base): pairs that turn more than beta_fast times over the
+ *             trained length stay, those that turn less than beta_slow times are slowed;
+ *             amplitude = 0.1 ln(factor) + 1 (factor > 1; else 1). The other scalings have amplitude 1. */
+typedef enum {
+    QSA_ROPE_NONE = 0,
+    QSA_ROPE_LINEAR = 1,
+    QSA_ROPE_NTK = 2,
+    QSA_ROPE_BY_PARTS = 3
+} qsa_rope_scaling;
+
+typedef struct {
+    int32_t head_dim;     /* multiple of 16, at most 1024 */
+    int32_t rot_begin;    /* first turned dim: multiple of 8 */
+    int32_t rot_dim;      /* turned dims: multiple of 16, 0 for none; rot_begin + rot_dim <= head_dim */
+    int32_t interleaved;  /* pairs (2i, 2i+1) instead of (i, i + rot_dim/2) */
+    int32_t scaling;      /* qsa_rope_scaling */
+    int32_t original_len; /* BY_PARTS: trained context length */
+    double base, factor;  /* base > 1; factor > 0 */
+    double beta_fast, beta_slow; /* BY_PARTS: beta_fast > beta_slow > 0 */
+} qsa_rope_config;
+
+/* Host only: the table the rotary kernels read. phase[i] (rot_dim / 2 entries, HOST memory) is f_i / (2 pi)
+ * modulo 1 as a 64-bit binary fraction of a turn, so position x phase modulo 2^64 is the angle exactly:
+ * positions of millions lose nothing. *amplitude as above. Copy phase to the device once and keep it. */
+QSA_API qsa_status qsa_rope_table(const qsa_rope_config *rope, uint64_t *phase, float *amplitude);
+
+/* Turn rows: out[n][h] = rotary(x[n][h], pos[n]) for n < N, h < n_heads, in fp32 with one rounding to bf16.
+ * Negative positions turn backwards (the inverse, and the gradient, of position -p up to amplitude^2).
+ *   x, out: rows of n_heads x head_dim contiguous bf16, x_ld / out_ld elements between rows (multiples of 8,
+ *   at least n_heads head_dim); 16-byte aligned; out may be x (same ld), else they must not overlap;
+ *   phase: the device copy of qsa_rope_table's; pos [N] int32.
+ * No workspace, no device-side errors. N = 0 is a no-op. */
+QSA_API qsa_status qsa_rope(const qsa_rope_config *rope, const uint64_t *phase, float amplitude, const qsa_bf16 *x,
+                            int64_t x_ld, const int32_t *pos, int32_t N, int32_t n_heads, qsa_bf16 *out,
+                            int64_t out_ld, qsa_stream stream);
+
+/* Bytes of a paged call's workspace for these heads (the same for every batch, length and page count; 0 on
+ * unsupported geometry). Zero it once with qsa_workspace_init. */
+QSA_API size_t qsa_paged_workspace_size(const qsa_paged_config *cfg);
+
+/* Append new tokens to a paged cache: for n < N, token n belongs to row r = seq[n] (seq NULL: r = n) at
+ * position p = pos[n]: q_out[n] = rotary(q[n], p), the K row at p becomes rotary(k[n], p) (each value rounded
+ * once to bf16) and the V row v[n]. A token with r < 0 is padding: nothing of it is read or written.
+ *   q [N] rows of n_q_heads x head_dim, q_ld elements apart (NULL: no queries); k, v likewise with n_kv_heads
+ *   (q, k and v may be slices of one projection's rows); lds multiples of 8; 16-byte aligned;
+ *   q_out rows q_out_ld apart (may be q with the same ld); rope->head_dim = cfg->head_dim.
+ * No (row, position) twice in one call, and no page that another row reads at that position: which of two
+ * writes stays is undefined. Device checks (the K/V write is skipped, QSA_ERR_DEVICE_BOUNDS recorded, q_out
+ * still written): r < n_rows, 0 <= p < table_ld page_size, 0 <= page < n_pages. */
+QSA_API qsa_status qsa_rope_append(const qsa_paged_config *cfg, const qsa_rope_config *rope, const uint64_t *phase,
+                                   float amplitude, const qsa_bf16 *q, int64_t q_ld, const qsa_bf16 *k, int64_t k_ld,
+                                   const qsa_bf16 *v, int64_t v_ld, const int32_t *seq, const int32_t *pos, int32_t N,
+                                   qsa_bf16 *q_out, int64_t q_out_ld, qsa_bf16 *k_cache, qsa_bf16 *v_cache,
+                                   int64_t n_pages, const int32_t *table, int64_t table_ld, int32_t n_rows, void *ws,
+                                   size_t ws_bytes, qsa_stream stream);
+
+/* qsa_rope_append into FP8 rows: the turned K row (in fp32, not rounded to bf16 first) and the V row are
+ * quantised per 128 dims as qsa_quantize_kv_fp8 does (scale = max |x| / 448, E4M3(x / scale), scale 0 and
+ * zero codes for zeros).
+ *   codes [n_pages][page_size][n_kv_heads][head_dim] uint8, 16-byte aligned; scales [..][head_dim / 128] fp32,
+ *   8-byte aligned. */
+QSA_API qsa_status qsa_rope_append_fp8kv(const qsa_paged_config *cfg, const qsa_rope_config *rope,
+                                         const uint64_t *phase, float amplitude, const qsa_bf16 *q, int64_t q_ld,
+                                         const qsa_bf16 *k, int64_t k_ld, const qsa_bf16 *v, int64_t v_ld,
+                                         const int32_t *seq, const int32_t *pos, int32_t N, qsa_bf16 *q_out,
+                                         int64_t q_out_ld, uint8_t *k_codes, float *k_scales, uint8_t *v_codes,
+                                         float *v_scales, int64_t n_pages, const int32_t *table, int64_t table_ld,
+                                         int32_t n_rows, void *ws, size_t ws_bytes, qsa_stream stream);
+
+/* Attention of one new token per sequence over its whole paged cache, split over the length and joined by
+ * log-sum-exp (the dense companion of qsa_sparse_decode). Sequence s has n = seq_len[s] cached tokens, the new
+ * one among them, and attends j in [max(0, n - window), n) (all n without a window):
+ *   out[s][h] = sum_j softmax_j(scale q[s][h] . K[j]) V[j],   lse[s][h] = ln sum_j e^(scale q.K[j]).
+ * A sequence with n = 0 gets out = 0 and lse = -inf. fp32 scores, softmax and sums; the weights enter the
+ * second product as the sum of two bf16 values. Pages that no attended token lies in are not read.
+ *   q rows of n_q_heads x head_dim, q_ld elements apart (a multiple of 8), 16-byte aligned; k_cache, v_cache
+ *   16-byte aligned, device memory or mapped pinned host memory; n_pages page_size < 2^31; seq_len [B];
+ *   out [B][n_q_heads][head_dim] bf16, 16-byte aligned; lse [B][n_q_heads] fp32 or NULL.
+ * Device checks: 0 <= n <= table_ld page_size (else the sequence counts as empty), 0 <= page < n_pages (its
+ * tokens are then left out); QSA_ERR_DEVICE_BOUNDS is recorded. Results do not depend on timing: the split
+ * depends on the lengths and the device alone. The first call on a device queries its occupancy and should
+ * precede stream capture. */
+QSA_API qsa_status qsa_paged_decode(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
+                                    const qsa_bf16 *k_cache, const qsa_bf16 *v_cache, int64_t n_pages,
+                                    const int32_t *table, int64_t table_ld, const int32_t *seq_len, int32_t B,
+                                    qsa_bf16 *out, float *lse, void *ws, size_t ws_bytes, qsa_stream stream);
+
+/* qsa_paged_decode over the FP8 rows qsa_rope_append_fp8kv writes (head_dim 128 or 256). */
+QSA_API qsa_status qsa_paged_decode_fp8kv(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
+                                          const uint8_t *k_codes, const float *k_scales, const uint8_t *v_codes,
+                                          const float *v_scales, int64_t n_pages, const int32_t *table,
+                                          int64_t table_ld, const int32_t *seq_len, int32_t B, qsa_bf16 *out,
+                                          float *lse, void *ws, size_t ws_bytes, qsa_stream stream);
+
+/* Planes of a pool that move together: n_planes arrays [n_pages][page_bytes], plane_stride bytes apart (e.g.
+ * the K caches of all layers). page_bytes a multiple of 4, plane_stride of page_bytes's alignment (16 where
+ * page_bytes is a multiple of 16, else 4), bases aligned likewise. */
+typedef struct {
+    void *base;
+    int64_t plane_stride;
+    int64_t page_bytes;
+    int32_t n_planes;
+} qsa_page_planes;
+#define QSA_MAX_PLANE_GROUPS 8
+
+/* Workspace of the page calls for tables of at most n_rows rows and pools of at most n_pages pages. */
+QSA_API size_t qsa_pages_workspace_size(int32_t n_rows, int64_t n_pages);
+
+/* One step of a pool's bookkeeping: fork, extend, free and start sequences. Row i < n_out of the new table
+ * continues row parent[i] of the old one (-1: starts empty) with room for add[i] >= 0 more tokens:
+ *   seq_len_out[i] = seq_len[parent[i]] + add[i];
+ *   full pages of the parent are shared; its partly filled last page stays with the first row that continues
+ *   it if nothing else refers to it (ref 1), and every other row gets a page of its own with the used tokens
+ *   copied in every plane (ceil(used page_bytes / page_size) bytes, rounded up to 16 or 4); then pages for the added tokens.
+ * New pages are the lowest-numbered ones with ref = 0, taken in row order (a row's copied page first).
+ * Old rows that nothing continues give their pages back. ref_out[p] = ref[p] - entries of the old table + entries of
+ * the new table that name page p (other holders' references stay). Entries behind a row's last page are -1.
+ * parent = row, add = 1 is a decode step's extension; a repeated parent is a fork; parent -1, add 0 frees.
+ *   parent, add, seq_len_out [n_out]; seq_len [n_in]; table [n_in][ld], table_out [n_out][ld] (another array);
+ *   ref, ref_out [n_pages] (may be the same array); n_in, n_out <= 65536. planes: n_groups <= 8 groups (HOST
+ *   array; 0 groups: bookkeeping alone).
+ * A row that runs out of pages or of the table's ld, or names a parent outside [0, n_in), becomes empty
+ * and QSA_ERR_DEVICE_BOUNDS is recorded with its index. */
+QSA_API qsa_status qsa_fork_pages(int32_t page_size, const int32_t *parent, const int32_t *add, int32_t n_out,
+                                  const int32_t *table, const int32_t *seq_len, int32_t n_in, int64_t ld,
+                                  const int32_t *ref, int64_t n_pages, int32_t *table_out, int32_t *seq_len_out,
+                                  int32_t *ref_out, const qsa_page_planes *planes, int32_t n_groups, void *ws,
+                                  size_t ws_bytes, qsa_stream stream);
+
+/* Compact a pool: with n_live pages of ref > 0, every live page with id >= n_live moves (in ascending order) into the
+ * free ids below n_live (ascending), in every plane; table_out and ref_out name the new places. The contents of
+ * pages >= n_live are left as they were. table_out may be table, ref_out may be ref. A table entry inside its row's
+ * length that names no live page is recorded (QSA_ERR_DEVICE_BOUNDS, the row) and becomes -1. */
+QSA_API qsa_status qsa_compact_pages(int32_t page_size, const int32_t *table, const int32_t *seq_len, int32_t n_rows,
+                                     int64_t ld, const int32_t *ref, int64_t n_pages, int32_t *table_out,
+                                     int32_t *ref_out, const qsa_page_planes *planes, int32_t n_groups, void *ws,
+                                     size_t ws_bytes, qsa_stream stream);
+
+/* Copy pages: page dst[i] of every destination plane becomes page src[i] of the source plane, i < n; a pair with a
+ * negative id is skipped, one out of range recorded (QSA_ERR_DEVICE_BOUNDS). dst_planes NULL: inside the same pool
+ * (then no dst may be another pair's src or dst). Groups of dst_planes match planes' n_planes and page_bytes; planes may be
+ * device or mapped pinned host memory, e.g. to move a sequence's pages to the host and back. */
+QSA_API qsa_status qsa_copy_pages(const int32_t *src, const int32_t *dst, int32_t n, const qsa_page_planes *planes,
+                                  int64_t n_pages, const qsa_page_planes *dst_planes, int64_t n_dst_pages,
+                                  int32_t n_groups, void *ws, size_t ws_bytes, qsa_stream stream);
+
 /* Static description of a status code. */
 QSA_API const char *qsa_status_string(qsa_status s);
 

@@ -40,6 +40,26 @@ class qsa_config(C.Structure):
                 ("softmax_scale", C.c_float)]
 
 
+class qsa_paged_config(C.Structure):
+    _fields_ = [("n_q_heads", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("page_size", C.c_int32), ("window", C.c_int32), ("softmax_scale", C.c_float)]
+
+
+class qsa_rope_config(C.Structure):
+    _fields_ = [("head_dim", C.c_int32), ("rot_begin", C.c_int32), ("rot_dim", C.c_int32),
+                ("interleaved", C.c_int32), ("scaling", C.c_int32), ("original_len", C.c_int32),
+                ("base", C.c_double), ("factor", C.c_double), ("beta_fast", C.c_double), ("beta_slow", C.c_double)]
+
+
+class qsa_page_planes(C.Structure):
+    _fields_ = [("base", C.c_void_p), ("plane_stride", C.c_int64), ("page_bytes", C.c_int64),
+                ("n_planes", C.c_int32)]
+
+
+ROPE_SCALINGS = ("none", "linear", "ntk", "by_parts")
+MAX_PLANE_GROUPS = 8
+
+
 def make_config(n_q_heads: int, n_kv_heads: int = 2, head_dim: int = 256, idx_dim: int = 128,
                 ratio: int = 4, budget: int = 2048, softmax_scale: float = 0.0) -> qsa_config:
     return qsa_config(n_q_heads, n_kv_heads, head_dim, idx_dim, ratio, budget, softmax_scale)
@@ -50,6 +70,10 @@ _I32 = C.c_int32
 _I64 = C.c_int64
 _SZ = C.c_size_t
 _CFG = C.POINTER(qsa_config)
+_PCFG = C.POINTER(qsa_paged_config)
+_RCFG = C.POINTER(qsa_rope_config)
+_PLANES = C.POINTER(qsa_page_planes)
+_F32 = C.c_float
 
 _SIGNATURES = {
     "qsa_workspace_size": (_SZ, [_I32, _CFG, _I32, _I64]),
@@ -87,6 +111,21 @@ _SIGNATURES = {
                                         _P, _P, _P, _SZ, _P, _SZ, _I64, C.c_uint32, _P]),
     "qsa_sparse_mla_workspace_size": (_SZ, [_I32, _I32, _I32]),
     "qsa_sparse_mla_decode": (_I32, [_P, _I32, _P, _I64, _P, _P, _I32, _I32, C.c_float, _P, _P, _P, _SZ, _P]),
+    "qsa_rope_table": (_I32, [_RCFG, _P, C.POINTER(_F32)]),
+    "qsa_rope": (_I32, [_RCFG, _P, _F32, _P, _I64, _P, _I32, _I32, _P, _I64, _P]),
+    "qsa_paged_workspace_size": (_SZ, [_PCFG]),
+    "qsa_rope_append": (_I32, [_PCFG, _RCFG, _P, _F32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P, _P,
+                               _I64, _P, _I64, _I32, _P, _SZ, _P]),
+    "qsa_rope_append_fp8kv": (_I32, [_PCFG, _RCFG, _P, _F32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _P, _I64,
+                                     _P, _P, _P, _P, _I64, _P, _I64, _I32, _P, _SZ, _P]),
+    "qsa_paged_decode": (_I32, [_PCFG, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _SZ, _P]),
+    "qsa_paged_decode_fp8kv": (_I32, [_PCFG, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _SZ,
+                                      _P]),
+    "qsa_pages_workspace_size": (_SZ, [_I32, _I64]),
+    "qsa_fork_pages": (_I32, [_I32, _P, _P, _I32, _P, _P, _I32, _I64, _P, _I64, _P, _P, _P, _PLANES, _I32, _P, _SZ,
+                              _P]),
+    "qsa_compact_pages": (_I32, [_I32, _P, _P, _I32, _I64, _P, _I64, _P, _P, _PLANES, _I32, _P, _SZ, _P]),
+    "qsa_copy_pages": (_I32, [_P, _P, _I32, _PLANES, _I64, _PLANES, _I64, _I32, _P, _SZ, _P]),
     "qsa_status_string": (C.c_char_p, [_I32]),
     "qsa_last_error": (C.c_char_p, []),
     "qsa_version": (C.c_char_p, []),
@@ -418,6 +457,229 @@ def qsa_sparse_mla_decode(q, kv_rows, rows, n_rows, out, lse, ws, softmax_scale:
                                         _ptr(n_rows, torch.int32, "n_rows"), rows.shape[1], B, float(softmax_scale),
                                         _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"),
                                         *_ws_args(ws), _stream(stream)), "qsa_sparse_mla_decode")
+
+
+# ---------------------------------------------------------------------------- paged K/V cache
+def _cuda(t, dtype, name) -> int:
+    """The address of a contiguous tensor on the current device."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _cache(t, dtype, shape, name) -> int:
+    """The address of a cache array on the current device or in pinned host memory."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
+    if t.get_device() not in (-1, torch.cuda.current_device()):
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _head_rows(t, n, heads, dim, name):
+    """(address, elements between rows) of bf16 [n, heads, dim] with contiguous heads, on the current device."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if tuple(t.shape) != (n, heads, dim):
+        raise ValueError(f"{name} must be [{n}, {heads}, {dim}], got {list(t.shape)}")
+    ld, head, one = t.stride()
+    if one != 1 or (head != dim and heads > 1):
+        raise ValueError(f"the heads of {name} must be contiguous")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr(), ld if n > 1 else heads * dim
+
+
+def _ints(t, shape, name) -> int:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return _cuda(t, torch.int32, name)
+
+
+class RopeTable:
+    """Rotary frequencies on a device: the configuration, the phases and the amplitude qsa_rope_table gives."""
+
+    def __init__(self, cfg: qsa_rope_config, device="cuda"):
+        host = torch.empty(max(cfg.rot_dim // 2, 1), dtype=torch.int64)
+        amplitude = _F32(1.0)
+        _check(load().qsa_rope_table(C.byref(cfg), host.data_ptr(), C.byref(amplitude)), "qsa_rope_table")
+        self.cfg, self.amplitude = cfg, amplitude.value
+        self.phase = host.to(device)
+
+
+def rope_table(head_dim: int, rot_dim: int | None = None, rot_begin: int = 0, interleaved: bool = False,
+               base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original_len: int = 0,
+               beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda") -> RopeTable:
+    """The table of dims [rot_begin, rot_begin + rot_dim) of a head (rot_dim None: the rest of the head);
+    scaling is one of ROPE_SCALINGS."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {ROPE_SCALINGS}, got {scaling!r}")
+    rot = head_dim - rot_begin if rot_dim is None else rot_dim
+    return RopeTable(qsa_rope_config(head_dim, rot_begin, rot, int(interleaved), ROPE_SCALINGS.index(scaling),
+                                     original_len, base, factor, beta_fast, beta_slow), device)
+
+
+def qsa_rope(rope: RopeTable, x, pos, out, stream=None):
+    """out[n, h] = x[n, h] turned to position pos[n]: x, out [N, H, head_dim] bf16 (rows may be strided; out may
+    be x), pos [N] int32."""
+    n, heads = x.shape[0], x.shape[1]
+    x_ptr, x_ld = _head_rows(x, n, heads, rope.cfg.head_dim, "x")
+    out_ptr, out_ld = _head_rows(out, n, heads, rope.cfg.head_dim, "out")
+    _check(load().qsa_rope(C.byref(rope.cfg), _cuda(rope.phase, torch.int64, "phase"), rope.amplitude, x_ptr, x_ld,
+                           _ints(pos, (n,), "pos"), n, heads, out_ptr, out_ld, _stream(stream)), "qsa_rope")
+
+
+def make_paged_config(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, softmax_scale: float = 0.0,
+                      window: int = 0) -> qsa_paged_config:
+    return qsa_paged_config(n_q_heads, n_kv_heads, head_dim, page_size, window, softmax_scale)
+
+
+def _zeroed(nbytes: int, device, stream):
+    ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    off = (-ws.data_ptr()) % 256
+    ws = ws[off:off + nbytes]
+    qsa_workspace_init(ws, stream)
+    return ws
+
+
+def paged_workspace(cfg: qsa_paged_config, device="cuda", stream=None):
+    """A zero-initialised workspace for qsa_rope_append and qsa_paged_decode (any batch and length)."""
+    n = int(load().qsa_paged_workspace_size(C.byref(cfg)))
+    if n == 0:
+        raise QsaError(QSA_ERR_UNSUPPORTED, "unsupported paged geometry: " + load().qsa_last_error().decode())
+    return _zeroed(n, device, stream)
+
+
+def pages_workspace(n_rows: int, n_pages: int, device="cuda", stream=None):
+    """A zero-initialised workspace for the page calls on tables of at most n_rows rows."""
+    n = int(load().qsa_pages_workspace_size(n_rows, n_pages))
+    if n == 0:
+        raise QsaError(QSA_ERR_UNSUPPORTED, "too many rows or pages")
+    return _zeroed(n, device, stream)
+
+
+def _append(fn, name, cfg, rope, q, k, v, pos, seq, q_out, planes, n_pages, table, ws, stream):
+    n, D = k.shape[0], cfg.head_dim
+    q_ptr, q_ld = (None, 0) if q is None else _head_rows(q, n, cfg.n_q_heads, D, "q")
+    q_out_ptr, q_out_ld = (None, 0) if q is None else _head_rows(q_out, n, cfg.n_q_heads, D, "q_out")
+    _check(fn(C.byref(cfg), C.byref(rope.cfg), _cuda(rope.phase, torch.int64, "phase"), rope.amplitude, q_ptr, q_ld,
+              *_head_rows(k, n, cfg.n_kv_heads, D, "k"), *_head_rows(v, n, cfg.n_kv_heads, D, "v"),
+              None if seq is None else _ints(seq, (n,), "seq"), _ints(pos, (n,), "pos"), n, q_out_ptr, q_out_ld,
+              *planes, n_pages, _cuda(table, torch.int32, "table"), table.shape[1], table.shape[0], *_ws_args(ws),
+              _stream(stream)), name)
+
+
+def _bf16_planes(cfg, k_cache, v_cache):
+    shape = (k_cache.shape[0], cfg.page_size, cfg.n_kv_heads, cfg.head_dim)
+    return (_cache(k_cache, torch.bfloat16, shape, "k_cache"), _cache(v_cache, torch.bfloat16, shape, "v_cache"))
+
+
+def _fp8_planes(cfg, kv8):
+    k_codes, k_scales, v_codes, v_scales = kv8
+    shape = (k_codes.shape[0], cfg.page_size, cfg.n_kv_heads, cfg.head_dim)
+    groups = shape[:3] + (cfg.head_dim // 128,)
+    return (_cache(k_codes, torch.uint8, shape, "k_codes"), _cache(k_scales, torch.float32, groups, "k_scales"),
+            _cache(v_codes, torch.uint8, shape, "v_codes"), _cache(v_scales, torch.float32, groups, "v_scales"))
+
+
+def qsa_rope_append(cfg, rope: RopeTable, q, k, v, pos, seq, q_out, k_cache, v_cache, table, ws, stream=None):
+    """New tokens into a paged cache: q [N, Hq, D] turned into q_out (both None: K and V only), k [N, Hkv, D]
+    turned and v stored at position pos[n] of row seq[n] (seq None: row n). k_cache, v_cache
+    [n_pages, page_size, Hkv, D] bf16; table [rows, max_pages] int32. q, k, v may be slices of one tensor."""
+    _append(load().qsa_rope_append, "qsa_rope_append", cfg, rope, q, k, v, pos, seq, q_out,
+            _bf16_planes(cfg, k_cache, v_cache), k_cache.shape[0], table, ws, stream)
+
+
+def qsa_rope_append_fp8kv(cfg, rope: RopeTable, q, k, v, pos, seq, q_out, kv8, table, ws, stream=None):
+    """qsa_rope_append into FP8 rows: kv8 = (k_codes, k_scales, v_codes, v_scales), codes
+    [n_pages, page_size, Hkv, D] uint8 and scales [..., D / 128] fp32."""
+    _append(load().qsa_rope_append_fp8kv, "qsa_rope_append_fp8kv", cfg, rope, q, k, v, pos, seq, q_out,
+            _fp8_planes(cfg, kv8), kv8[0].shape[0], table, ws, stream)
+
+
+def _paged(fn, name, cfg, q, planes, n_pages, table, seq_len, out, lse, ws, stream):
+    B = q.shape[0]
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"table must be [{B}, max_pages], got {list(table.shape)}")
+    if tuple(out.shape) != (B, cfg.n_q_heads, cfg.head_dim):
+        raise ValueError(f"out must be [{B}, {cfg.n_q_heads}, {cfg.head_dim}], got {list(out.shape)}")
+    if lse is not None and tuple(lse.shape) != (B, cfg.n_q_heads):
+        raise ValueError(f"lse must be [{B}, {cfg.n_q_heads}], got {list(lse.shape)}")
+    _check(fn(C.byref(cfg), *_head_rows(q, B, cfg.n_q_heads, cfg.head_dim, "q"), *planes, n_pages,
+              _cuda(table, torch.int32, "table"), table.shape[1], _ints(seq_len, (B,), "seq_len"), B,
+              _cuda(out, torch.bfloat16, "out"), None if lse is None else _cuda(lse, torch.float32, "lse"),
+              *_ws_args(ws), _stream(stream)), name)
+
+
+def qsa_paged_decode(cfg, q, k_cache, v_cache, table, seq_len, out, lse, ws, stream=None):
+    """Attention of one new token per sequence over its seq_len[s] cached tokens: q [B, Hq, D] (rows may be
+    strided), caches [n_pages, page_size, Hkv, D] bf16, table [B, max_pages], out [B, Hq, D], lse [B, Hq] or None."""
+    _paged(load().qsa_paged_decode, "qsa_paged_decode", cfg, q, _bf16_planes(cfg, k_cache, v_cache),
+           k_cache.shape[0], table, seq_len, out, lse, ws, stream)
+
+
+def qsa_paged_decode_fp8kv(cfg, q, kv8, table, seq_len, out, lse, ws, stream=None):
+    """qsa_paged_decode over FP8 rows kv8 = (k_codes, k_scales, v_codes, v_scales)."""
+    _paged(load().qsa_paged_decode_fp8kv, "qsa_paged_decode_fp8kv", cfg, q, _fp8_planes(cfg, kv8), kv8[0].shape[0],
+           table, seq_len, out, lse, ws, stream)
+
+
+def _plane_groups(planes, n_pages):
+    """The C array of pool tensors: each [n_planes, n_pages, ...] with contiguous pages."""
+    groups = (qsa_page_planes * max(len(planes), 1))()
+    for i, t in enumerate(planes):
+        if t.dim() < 3 or t.shape[1] != n_pages or not t[0].is_contiguous():
+            raise ValueError(f"planes[{i}] must be [n_planes, {n_pages}, ...] with contiguous planes")
+        if t.get_device() not in (-1, torch.cuda.current_device()):
+            raise ValueError(f"planes[{i}] is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+        size = t.element_size()
+        groups[i] = qsa_page_planes(t.data_ptr(), t.stride(0) * size if t.shape[0] > 1 else 0,
+                                    t.stride(1) * size if n_pages > 1 else t[0].numel() * size, t.shape[0])
+    return groups
+
+
+def qsa_fork_pages(page_size, parent, add, table, seq_len, ref, table_out, seq_len_out, ref_out, planes, ws,
+                   stream=None):
+    """New table rows that continue old ones (parent[i], -1: none) with room for add[i] more tokens; full pages
+    shared, a shared last page copied in every plane, new pages taken from those with ref 0. planes: a list of
+    pool tensors [n_planes, n_pages, ...]."""
+    n_out, (n_in, ld), n_pages = parent.shape[0], table.shape, ref.shape[0]
+    _check(load().qsa_fork_pages(int(page_size), _ints(parent, (n_out,), "parent"), _ints(add, (n_out,), "add"), n_out,
+                                 _cuda(table, torch.int32, "table"), _ints(seq_len, (n_in,), "seq_len"), n_in, ld,
+                                 _ints(ref, (n_pages,), "ref"), n_pages, _ints(table_out, (n_out, ld), "table_out"),
+                                 _ints(seq_len_out, (n_out,), "seq_len_out"), _ints(ref_out, (n_pages,), "ref_out"),
+                                 _plane_groups(planes, n_pages), len(planes), *_ws_args(ws), _stream(stream)),
+           "qsa_fork_pages")
+
+
+def qsa_compact_pages(page_size, table, seq_len, ref, table_out, ref_out, planes, ws, stream=None):
+    """Move the live pages (ref > 0) to the lowest ids in every plane and rewrite table and ref."""
+    (n_rows, ld), n_pages = table.shape, ref.shape[0]
+    _check(load().qsa_compact_pages(int(page_size), _cuda(table, torch.int32, "table"),
+                                    _ints(seq_len, (n_rows,), "seq_len"), n_rows, ld, _ints(ref, (n_pages,), "ref"),
+                                    n_pages, _ints(table_out, (n_rows, ld), "table_out"),
+                                    _ints(ref_out, (n_pages,), "ref_out"), _plane_groups(planes, n_pages), len(planes),
+                                    *_ws_args(ws), _stream(stream)), "qsa_compact_pages")
+
+
+def qsa_copy_pages(src, dst, planes, ws, dst_planes=None, stream=None):
+    """Page dst[i] becomes page src[i] in every plane (or of dst_planes, which may be pinned host tensors);
+    pairs with a negative id are skipped."""
+    if not planes:
+        return
+    n, n_pages = src.shape[0], planes[0].shape[1]
+    n_dst = n_pages if dst_planes is None else dst_planes[0].shape[1]
+    if dst_planes is not None and len(dst_planes) != len(planes):
+        raise ValueError("dst_planes must match planes")
+    _check(load().qsa_copy_pages(_ints(src, (n,), "src"), _ints(dst, (n,), "dst"), n, _plane_groups(planes, n_pages),
+                                 n_pages, None if dst_planes is None else _plane_groups(dst_planes, n_dst), n_dst,
+                                 len(planes), *_ws_args(ws), _stream(stream)), "qsa_copy_pages")
 
 
 def version() -> str:

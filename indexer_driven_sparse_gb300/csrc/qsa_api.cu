@@ -10,6 +10,7 @@
 
 #include "qsa_internal.cuh"
 #include "kv_fp8.cuh"
+#include "paged.cuh"
 
 using namespace qsa;
 
@@ -111,17 +112,12 @@ qsa_status qsa::host_fail(qsa_status s, const char *what, const char *detail) {
     return fail(s, "%s: %s", what, detail);
 }
 
-extern "C" {
-
-QSA_API size_t qsa_workspace_size(int32_t op, const qsa_config *cfg, int32_t n_rows, int64_t max_blocks) {
-    if (check_config(cfg) != QSA_OK) return 0;
-    return ws_size(op, cfg, n_rows, max_blocks);
-}
+qsa_status qsa::host_ok() { return ok(); }
 
 // The GPU reads p at the same address: device or managed memory, or pinned host memory mapped
 // into the device's address space (cudaHostAlloc; cudaHostRegister with the mapped flag) -
 // the K/V cache may live in host memory and be gathered over the host link.
-static bool device_accessible(const void *p) {
+bool qsa::device_accessible(const void *p) {
     cudaPointerAttributes at{};
     if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -133,6 +129,13 @@ static bool device_accessible(const void *p) {
         case cudaMemoryTypeHost: return at.devicePointer == p;
         default: return false;
     }
+}
+
+extern "C" {
+
+QSA_API size_t qsa_workspace_size(int32_t op, const qsa_config *cfg, int32_t n_rows, int64_t max_blocks) {
+    if (check_config(cfg) != QSA_OK) return 0;
+    return ws_size(op, cfg, n_rows, max_blocks);
 }
 
 QSA_API qsa_status qsa_workspace_init(void *ws, size_t ws_bytes, qsa_stream stream) {

@@ -1,0 +1,255 @@
+// Rotary positions, alone (qsa_rope) and fused with appending K/V to a paged cache (qsa_rope_append).
+//
+// Pair i of a head at position p turns by the angle p f_i. f_i / (2 pi) modulo 1 is held as a 64-bit binary
+// fraction of a turn, so the angle's fraction of a turn is (p x phase_i) mod 2^64: an integer product that is
+// exact at every position (in fp32 the product of a position of millions and f_i is off by tenths of a
+// radian). Its upper 32 bits, as a signed fraction in [-1/2, 1/2), give sin and cos by sincospif.
+//
+// Both kernels stream: one thread owns 16 dims of a token's head (a "slot": 8 pairs, or 16 dims that pass
+// through) for a run of heads, so the 8 sines and cosines are computed once and used for every head of the run.
+#include "paged.cuh"
+
+#include <algorithm>
+
+namespace qsa {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+struct Slot {
+    int a, b;       // first dims of the slot's two 8-element vectors
+    int freq;       // first pair, -1: passes through
+};
+
+// The slots of a head: rot/16 turning ones first, then the dims that pass through in order.
+__device__ __forceinline__ Slot slot_of(const RopeArgs &r, int s) {
+    Slot t;
+    const int turning = r.rot >> 4;
+    if (s < turning) {
+        t.freq = 8 * s;
+        t.a = r.interleaved ? r.begin + 16 * s : r.begin + 8 * s;
+        t.b = r.interleaved ? t.a + 8 : t.a + (r.rot >> 1);
+    } else {
+        const int e = 16 * (s - turning);
+        t.freq = -1;
+        t.a = e < r.begin ? e : e + r.rot;
+        t.b = e + 8 < r.begin ? e + 8 : e + 8 + r.rot;
+    }
+    return t;
+}
+
+__device__ __forceinline__ void turns(const RopeArgs &r, int freq, int pos, float (&co)[8], float (&si)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint64_t turn = (uint64_t)(int64_t)pos * __ldg(r.phase + freq + i);
+        const float half_turns = (float)(int32_t)(turn >> 32) * 0x1p-31f;
+        sincospif(half_turns, &si[i], &co[i]);
+        si[i] *= r.amplitude;
+        co[i] *= r.amplitude;
+    }
+}
+
+// Turn a slot's 16 values: pairs (x[i], x[8 + i]), or neighbours when interleaved.
+__device__ __forceinline__ void turn16(float (&x)[16], const float (&co)[8], const float (&si)[8], bool interleaved) {
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = x[2 * i], w = x[2 * i + 1];
+            x[2 * i] = u * co[i] - w * si[i];
+            x[2 * i + 1] = w * co[i] + u * si[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = x[i], w = x[8 + i];
+            x[i] = u * co[i] - w * si[i];
+            x[8 + i] = w * co[i] + u * si[i];
+        }
+    }
+}
+
+__device__ __forceinline__ void unpack16(const uint4 &a, const uint4 &b, float (&x)[16]) {
+    float f[8], g[8];
+    unpack8(a, f);
+    unpack8(b, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] = f[i];
+        x[8 + i] = g[i];
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float *x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = (uint32_t)float_to_bf16_bits(x[2 * i]) | ((uint32_t)float_to_bf16_bits(x[2 * i + 1]) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Thread (token n, slot s) for heads [h0, h0 + run).
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, RopeRows a, int run) {
+    const int S = r.D >> 4;
+    const int64_t t = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
+    const int64_t n = t / S;
+    if (n >= a.N) return;
+    const Slot sl = slot_of(r, (int)(t - n * S));
+    if (sl.freq < 0 && a.x == a.out) return;       // in place: nothing to do
+    const int h0 = blockIdx.y * run, h1 = min(a.H, h0 + run);
+    const uint16_t *src = a.x + n * a.x_ld + (int64_t)h0 * r.D;
+    uint16_t *dst = a.out + n * a.out_ld + (int64_t)h0 * r.D;
+    float co[8], si[8];
+    if (sl.freq >= 0) turns(r, sl.freq, a.pos[n], co, si);
+#pragma unroll 4
+    for (int h = h0; h < h1; ++h, src += r.D, dst += r.D) {
+        uint4 va = *reinterpret_cast<const uint4 *>(src + sl.a), vb = *reinterpret_cast<const uint4 *>(src + sl.b);
+        if (sl.freq >= 0) {
+            float x[16];
+            unpack16(va, vb, x);
+            turn16(x, co, si, r.interleaved != 0);
+            va = pack8(x);
+            vb = pack8(x + 8);
+        }
+        *reinterpret_cast<uint4 *>(dst + sl.a) = va;
+        *reinterpret_cast<uint4 *>(dst + sl.b) = vb;
+    }
+}
+
+// Eight values of one 128-dim group (or of two groups, g0 != g1) quantised as quantize_kv_fp8_kernel does: the
+// group's |max| over the row's S threads (a power of two <= 16 that starts at a multiple of S in the warp).
+template <int S>
+__device__ __forceinline__ void quantise16(const float (&x)[16], const Slot &sl, int s, uint8_t *codes, float *scales,
+                                           int groups) {
+    const unsigned mask = (S == 32 ? 0xffffffffu : ((1u << S) - 1u)) << ((threadIdx.x & 31) & ~(S - 1));
+    const int ga = sl.a >> 7, gb = sl.b >> 7;
+    float ma = 0.f, mb = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        ma = fmaxf(ma, fabsf(x[i]));
+        mb = fmaxf(mb, fabsf(x[8 + i]));
+    }
+    float m0 = fmaxf(ga == 0 ? ma : 0.f, gb == 0 ? mb : 0.f), m1 = fmaxf(ga == 1 ? ma : 0.f, gb == 1 ? mb : 0.f);
+#pragma unroll
+    for (int o = S / 2; o >= 1; o >>= 1) {
+        m0 = fmaxf(m0, __shfl_xor_sync(mask, m0, o, S));
+        m1 = fmaxf(m1, __shfl_xor_sync(mask, m1, o, S));
+    }
+    const float s0 = __fdiv_rn(m0, kE4m3Max), s1 = __fdiv_rn(m1, kE4m3Max);
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        const float scale = (v ? gb : ga) ? s1 : s0;
+        uint32_t w0 = 0u, w1 = 0u;
+        if (scale > 0.f) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[8 * v + i], scale);
+            w0 = e4m3x2_of(y[0], y[1]) | (e4m3x2_of(y[2], y[3]) << 16);
+            w1 = e4m3x2_of(y[4], y[5]) | (e4m3x2_of(y[6], y[7]) << 16);
+        }
+        *reinterpret_cast<uint2 *>(codes + (v ? sl.b : sl.a)) = make_uint2(w0, w1);
+    }
+    if (s == 0) {
+        scales[0] = s0;
+        if (groups == 2) scales[1] = s1;
+    }
+}
+
+// Thread (token n, slot s) for a run of the token's Hq + 2 Hkv heads: q (turned into q_out), k (turned into the
+// cache), v (into the cache). S = D / 16 threads of one warp carry a head.
+template <int S, bool F8>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, AppendArgs a, int run) {
+    constexpr int D = S * 16;
+    const int64_t t = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
+    const int64_t n = t / S;
+    const int s = (int)(t & (S - 1));
+    if (n >= a.N) return;
+    const int row = a.seq ? a.seq[n] : (int)n;
+    if (row < 0) return;                                     // padding
+    const int pos = a.pos[n];
+    const Slot sl = slot_of(r, s), straight = {16 * s, 16 * s + 8, -1};
+    // heads of q come first; without queries the list starts at k
+    const int total = a.Hq + 2 * a.Hkv;
+    const int h0 = (a.q ? 0 : a.Hq) + blockIdx.y * run, h1 = min(total, h0 + run);
+    if (h0 >= h1) return;
+    int64_t slot = -1;
+    if (h1 > a.Hq) {
+        bool ok = row < a.n_rows && pos >= 0 && pos / a.page_size < a.ld;
+        if (ok) {
+            const int page = a.table[(int64_t)row * a.ld + pos / a.page_size];
+            ok = page >= 0 && page < a.n_pages;
+            slot = (int64_t)page * a.page_size + pos % a.page_size;
+        }
+        if (!ok) {
+            slot = -1;
+            if (s == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereAppend, (int)n);
+        }
+    }
+    float co[8], si[8];
+    if (sl.freq >= 0 && h0 < a.Hq + a.Hkv) turns(r, sl.freq, pos, co, si);
+#pragma unroll 2
+    for (int h = h0; h < h1; ++h) {
+        const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+        if (!is_q && slot < 0) break;
+        const int g = h - a.Hq - (is_v ? a.Hkv : 0);          // KV head
+        const Slot at = is_v ? straight : sl;
+        const uint16_t *src = is_q ? a.q + n * a.q_ld + h * D
+                                   : (is_v ? a.v + n * a.v_ld : a.k + n * a.k_ld) + g * D;
+        uint4 va = *reinterpret_cast<const uint4 *>(src + at.a), vb = *reinterpret_cast<const uint4 *>(src + at.b);
+        const bool turned = at.freq >= 0;
+        float x[16];
+        if (turned || F8) unpack16(va, vb, x);
+        if (turned) turn16(x, co, si, r.interleaved != 0);
+        const int64_t kv = (slot * a.Hkv + g) * D;
+        if (F8 && !is_q) {
+            quantise16<S>(x, at, s, (is_v ? a.v_codes : a.k_codes) + kv,
+                          (is_v ? a.v_scales : a.k_scales) + (slot * a.Hkv + g) * (D / 128), D / 128);
+        } else {
+            if (turned) {
+                va = pack8(x);
+                vb = pack8(x + 8);
+            }
+            uint16_t *dst = is_q ? a.q_out + n * a.q_out_ld + h * D : (is_v ? a.v_cache : a.k_cache) + kv;
+            *reinterpret_cast<uint4 *>(dst + at.a) = va;
+            *reinterpret_cast<uint4 *>(dst + at.b) = vb;
+        }
+    }
+}
+
+// Heads per thread: as long a run as keeps about 150,000 threads (a thousand per SM), since a run shares its sines.
+int run_of(int64_t threads_per_head, int heads) {
+    const int64_t want = 152 * 1024;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(heads, threads_per_head * heads / want));
+}
+
+template <int S, bool F8>
+cudaError_t append(const RopeArgs &r, const AppendArgs &a, cudaStream_t st) {
+    const int heads = (a.q ? a.Hq : 0) + 2 * a.Hkv;
+    const int64_t threads = (int64_t)a.N * S;
+    const int run = run_of(threads, heads);
+    const dim3 grid((unsigned)((threads + kRopeThreads - 1) / kRopeThreads), (heads + run - 1) / run);
+    rope_append_kernel<S, F8><<<grid, kRopeThreads, 0, st>>>(r, a, run);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs &r, const RopeRows &a, cudaStream_t st) {
+    const int64_t threads = (int64_t)a.N * (r.D >> 4);
+    const int run = run_of(threads, a.H);
+    const dim3 grid((unsigned)((threads + kRopeThreads - 1) / kRopeThreads), (a.H + run - 1) / run);
+    rope_kernel<<<grid, kRopeThreads, 0, st>>>(r, a, run);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rope_append(const RopeArgs &r, const AppendArgs &a, cudaStream_t st) {
+    const bool f8 = a.k_codes != nullptr;
+    switch (r.D) {
+        case 64: return f8 ? cudaErrorInvalidValue : append<4, false>(r, a, st);
+        case 128: return f8 ? append<8, true>(r, a, st) : append<8, false>(r, a, st);
+        case 256: return f8 ? append<16, true>(r, a, st) : append<16, false>(r, a, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace qsa

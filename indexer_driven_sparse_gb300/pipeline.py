@@ -232,3 +232,79 @@ def _workspace(nbytes: int, device):
     ws = ws[off:off + nbytes]
     qb.qsa_workspace_init(ws)
     return ws
+
+
+class PagedCache:
+    """K/V of every layer in one pool of pages, and the sequences that share it: row r of `table` lists the
+    pages of sequence r, `seq_len[r]` its tokens and `ref[p]` the rows that name page p.
+
+    A decode step is ``extend`` (room for the new tokens), then per layer ``append`` and ``attend``; ``fork``
+    lets rows continue other rows (beams, shared prompts) or gives their pages back, and ``compact`` moves
+    the live pages to the front of the pool. Nothing here synchronises; ``status`` does."""
+
+    def __init__(self, n_layers: int, n_pages: int, page_size: int, n_rows: int, max_pages: int, n_q_heads: int,
+                 n_kv_heads: int, head_dim: int = 256, fp8: bool = False, softmax_scale: float = 0.0, window: int = 0,
+                 device="cuda"):
+        self.cfg = qb.make_paged_config(n_q_heads, n_kv_heads, head_dim, page_size, softmax_scale, window)
+        self.fp8, self.device, self.n_rows = fp8, device, n_rows
+        shape = (n_layers, n_pages, page_size, n_kv_heads)
+        if fp8:
+            codes = dict(dtype=torch.uint8, device=device)
+            scales = dict(dtype=torch.float32, device=device)
+            self.planes = [torch.zeros(*shape, head_dim, **codes), torch.zeros(*shape, head_dim // 128, **scales),
+                           torch.zeros(*shape, head_dim, **codes), torch.zeros(*shape, head_dim // 128, **scales)]
+        else:
+            self.planes = [torch.zeros(*shape, head_dim, dtype=torch.bfloat16, device=device) for _ in range(2)]
+        i32 = dict(dtype=torch.int32, device=device)
+        # the page calls write a new table beside the old one: two of each, in turn
+        self._tables = [torch.full((n_rows, max_pages), -1, **i32) for _ in range(2)]
+        self._lens = [torch.zeros(n_rows, **i32) for _ in range(2)]
+        self._now = 0
+        self.ref = torch.zeros(n_pages, **i32)
+        self._rows = torch.arange(n_rows, **i32)
+        self._one = torch.ones(n_rows, **i32)
+        self.ws = qb.paged_workspace(self.cfg, device)
+        self.pages_ws = qb.pages_workspace(n_rows, n_pages, device)
+
+    @property
+    def table(self):
+        return self._tables[self._now]
+
+    @property
+    def seq_len(self):
+        return self._lens[self._now]
+
+    def fork(self, parent, add, stream=None):
+        """Row i continues row parent[i] (-1: starts empty) with room for add[i] more tokens (qsa_fork_pages)."""
+        new = 1 - self._now
+        qb.qsa_fork_pages(self.cfg.page_size, parent, add, self.table, self.seq_len, self.ref, self._tables[new],
+                          self._lens[new], self.ref, self.planes, self.pages_ws, stream)
+        self._now = new
+
+    def extend(self, add=None, stream=None):
+        """Room for add[i] more tokens in row i (None: one each)."""
+        self.fork(self._rows, self._one if add is None else add, stream)
+
+    def compact(self, stream=None):
+        qb.qsa_compact_pages(self.cfg.page_size, self.table, self.seq_len, self.ref, self.table, self.ref, self.planes,
+                             self.pages_ws, stream)
+
+    def append(self, layer: int, rope, q, k, v, pos, seq=None, q_out=None, stream=None):
+        """Store k (turned) and v at position pos[n] of row seq[n] (None: row n) of a layer; q turned into q_out."""
+        planes = [p[layer] for p in self.planes]
+        if self.fp8:
+            qb.qsa_rope_append_fp8kv(self.cfg, rope, q, k, v, pos, seq, q_out, planes, self.table, self.ws, stream)
+        else:
+            qb.qsa_rope_append(self.cfg, rope, q, k, v, pos, seq, q_out, *planes, self.table, self.ws, stream)
+
+    def attend(self, layer: int, q, out, lse=None, stream=None):
+        """Attention of each row's newest token over the row's tokens of a layer."""
+        planes = [p[layer] for p in self.planes]
+        if self.fp8:
+            qb.qsa_paged_decode_fp8kv(self.cfg, q, planes, self.table, self.seq_len, out, lse, self.ws, stream)
+        else:
+            qb.qsa_paged_decode(self.cfg, q, *planes, self.table, self.seq_len, out, lse, self.ws, stream)
+
+    def status(self, stream=None):
+        """(status, detail) of the attention and append calls, then of the page calls."""
+        return qb.qsa_read_device_status(self.ws, stream), qb.qsa_read_device_status(self.pages_ws, stream)
