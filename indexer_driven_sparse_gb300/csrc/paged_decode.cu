@@ -1,101 +1,733 @@
 // Attention of one new token over a paged K/V cache (qsa_paged_decode, qsa_paged_decode_fp8kv):
 //   out = sum_j softmax_j(scale q . K[j]) V[j] over the sequence's cached tokens, with their log-sum-exp.
-// Plain form: one CTA per (sequence, query head) walks the tokens in chunks with a running maximum and sum.
+//
+// What bounds it: every K and V row is read once (2 Hkv rows a token) and used by the G <= 16 query heads of
+// its KV head: 4 G flop per value read, a fiftieth of what the tensor cores do per byte of HBM. So the
+// kernel is a stream of rows, and the work goes into keeping enough of them in flight.
+//
+// Split: the batch's tokens, cut into tiles of 64 of one sequence each, form one list; it is dealt to R ranges of
+// equal length (R Hkv CTAs fill the GPU once), so a ragged batch is balanced whatever its lengths. CTA
+// (range, KV head) walks its tiles through a ring of shared-memory stages filled by 16-byte cp.async. A
+// sequence that a range boundary cuts leaves partials (m, l, O), joined by paged_join_kernel; all others are
+// written at once. The two KV heads of a range are neighbouring CTAs, so a token's rows are read together.
+//
+// A tile's products run on mma.sync m16n8k16: M is the G heads padded to 16, which a 128-row tcgen05 tile would
+// fill to an eighth, and its accumulator is a register fragment that becomes the next product's operand
+// without a trip through tensor memory. D / 32 warps: for S = Q K^T a warp takes 64 / warps tokens of the tile
+// and leaves its scores in shared memory; then every warp forms the softmax weights of all 64 tokens in the
+// operand layout of O += P V (16 heads x 64 tokens: 32 exponentials a lane) and multiplies its 32 dims of V. The
+// running maximum and sum are the same in every warp, so nothing is reduced across warps.
+//   bf16 rows: P = P_hi + P_lo, two bf16 values (2^-17 of each weight): one bf16 would add as much error
+//     as the result's own rounding.
+//   FP8 rows: E4M3 codes are exact in f16. Q enters as f16 scaled by a power of two per head (values below 2^-24 of
+//     the head's largest are rounded there: beneath the fp32 sum's own rounding); the K scales multiply the fp32
+//     sums of each 128 dims. V's scales multiply the weights: w = p v_scale, held relative to their running
+//     maximum (so that the largest is 1) and rounded to f16, 2^-11 of each, well under the rows' own 2^-4.
 #include "paged.cuh"
+#include "qsa_ptx.cuh"
+
+#include <cuda_fp16.h>
+
+#include <algorithm>
 
 namespace qsa {
 
 namespace {
 
-constexpr int kPagedThreads = 256;
-constexpr int kPagedChunk = 64;
+constexpr int kTile = 64;                // tokens of a tile
+constexpr int kSPitch = 72;              // floats between two heads' scores: float2 accesses touch every bank once
+constexpr int kJoinThreads = 256;
+constexpr int kMaxRanges = 512;
 
-template <int D, bool F8>
-__global__ void __launch_bounds__(kPagedThreads) paged_plain_kernel(PagedArgs a) {
-    const int s = blockIdx.y, h = blockIdx.x, g = h / a.G, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ float qs[D], w[kPagedChunk];
-    __shared__ int64_t slots[kPagedChunk];
-    int len = a.seq_len[s];
-    if (len < 0 || len > a.ld * a.page_size) {
-        if (tid == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, s);
-        len = 0;
+template <int D_, int GT_, bool F8_>
+struct PagedCfg {
+    static constexpr int D = D_, GT = GT_;          // GT: head rows kept (8 or 16)
+    static constexpr bool F8 = F8_;
+    static constexpr int warps = D / 32, threads = warps * 32;
+    static constexpr int row = D * (F8 ? 1 : 2);    // bytes of a K or V row
+    static constexpr int chunks = row / 16;         // 16-byte chunks of a row
+    static constexpr int rows_per_copy = 32 / chunks;
+    static constexpr int warp_tok = kTile / warps;  // tokens a warp loads and scores
+    static constexpr int groups = F8 ? D / 128 : 0; // scales of a row
+    static constexpr int k_bytes = kTile * row, s_bytes = kTile * groups * 4, q_bytes = GT * D * 2;
+    static constexpr int stage = 2 * k_bytes + 2 * s_bytes + q_bytes;
+    static constexpr int stages = F8 && D == 256 ? 5 : 3;
+    static constexpr int ctas = D == 256 ? 1 : (F8 || D == 64) ? 3 : 2;   // per SM
+    static constexpr int scores = GT * kSPitch * 4;
+    static constexpr int smem = stages * stage + scores;
+};
+
+// Workspace behind the status block: meta [kMaxRanges] {row, parts}, (m, l) and O of the partials; range r has slot
+// 2r for the sequence it continues and 2r + 1 for the one it starts and leaves unfinished.
+struct PagedScratch {
+    int2 *meta;
+    float2 *ml;     // [2 R][Hq]
+    float *o;       // [2 R][Hq][D]
+};
+
+constexpr int max_ctas(int D) { return D == 256 ? 160 : 480; }
+
+__host__ __device__ inline int ranges_for(int ctas, int Hkv) { return ctas / Hkv > 0 ? ctas / Hkv : 1; }
+
+struct Row {
+    int len, lo, t0, t1;    // tokens, first attended token, tiles [t0, t1)
+};
+
+__device__ __forceinline__ Row row_of(const PagedArgs &a, int s) {
+    Row r;
+    r.len = __ldg(a.seq_len + s);
+    if (r.len < 0 || r.len > a.ld * a.page_size) r.len = 0;
+    r.lo = a.window > 0 ? max(0, r.len - a.window) : 0;
+    r.t0 = r.lo / kTile;
+    r.t1 = r.len > 0 ? (r.len + kTile - 1) / kTile : r.t0;
+    return r;
+}
+
+// A place in the tile list: tile t of row s.
+struct Cursor {
+    int s, t;
+    Row r;
+    __device__ __forceinline__ void at(const PagedArgs &a, int row, int skip) {
+        s = row;
+        r = row_of(a, s);
+        t = r.t0 + skip;
     }
-    const int lo = a.window > 0 ? max(0, len - a.window) : 0;
-    if (tid < D) qs[tid] = bf16_bits_to_float(a.q[s * a.q_ld + h * D + tid]) * a.scale_log2;
-    float m = -INFINITY, l = 0.f, acc = 0.f;
-    for (int c0 = lo; c0 < len; c0 += kPagedChunk) {
-        const int n = min(kPagedChunk, len - c0);
-        __syncthreads();
-        if (tid < n) {
-            const int t = c0 + tid, page = a.table[s * a.ld + t / a.page_size];
-            const bool ok = page >= 0 && page < a.n_pages;
-            if (!ok) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, s);
-            slots[tid] = ok ? (int64_t)page * a.page_size + t % a.page_size : -1;
+    __device__ __forceinline__ void next(const PagedArgs &a) {   // never called behind the list's last tile
+        if (++t < r.t1) return;
+        do {
+            ++s;
+            r = row_of(a, s);
+        } while (r.t1 == r.t0);
+        t = r.t0;
+    }
+};
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small_zfill(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(real ? N : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two E4M3 codes (the low or the high half of w) -> f16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t w, int half) {
+    uint32_t r;
+    const uint16_t c = (uint16_t)(half ? w >> 16 : w & 0xFFFFu);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float quad_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+template <typename C>
+__global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedArgs a, PagedScratch ws, int ranges) {
+    constexpr int D = C::D, GT = C::GT, W = C::warps, TW = C::warp_tok, NS = C::stages;
+    constexpr bool F8 = C::F8;
+    constexpr int HR = GT / 8;                     // head rows a lane holds: g and g + 8
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long scan[C::warps + 1];
+    __shared__ int start[2];
+    __shared__ uint32_t real_tok[NS][W];           // bit i: token i of the warp's share exists
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    const int range = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv;
+    const int Hkv = a.Hkv, G = a.G;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- this range's tiles: total over the batch, then the row and tile the range starts at
+    const int per = (a.B + C::threads - 1) / C::threads, s_lo = min(a.B, tid * per), s_hi = min(a.B, s_lo + per);
+    long long mine = 0;
+    for (int s = s_lo; s < s_hi; ++s) {
+        const Row r = row_of(a, s);
+        mine += r.t1 - r.t0;
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) upto += scan[w];
+        total += scan[w];
+    }
+    const int R = (int)min((long long)ranges, max(total, 1ll));
+    const long long x0 = range < R ? total * range / R : 0, x1 = range < R ? total * (range + 1) / R : 0;
+    if (x0 < x1 && upto - mine <= x0 && x0 < upto) {
+        long long at = upto - mine;
+        int s = s_lo;
+        for (;; ++s) {
+            const Row r = row_of(a, s);
+            if (x0 < at + r.t1 - r.t0) break;
+            at += r.t1 - r.t0;
         }
-        __syncthreads();
-        for (int i = warp; i < n; i += kPagedThreads / 32) {
-            float x = 0.f;
-            if (slots[i] >= 0) {
-                const int64_t row = slots[i] * a.Hkv + g;
-                for (int d = lane; d < D; d += 32) {
-                    if (F8) {
-                        float f[16];
-                        const uint32_t c = static_cast<const uint8_t *>(a.k)[row * D + d];
-                        e4m3x16_to_f32(make_uint4(c, 0, 0, 0), f);
-                        x = fmaf(qs[d], f[0] * a.k_scales[row * (D / 128) + d / 128], x);
-                    } else {
-                        x = fmaf(qs[d], bf16_bits_to_float(static_cast<const uint16_t *>(a.k)[row * D + d]), x);
+        start[0] = s;
+        start[1] = (int)(x0 - at);
+    }
+    // rows without a token: zeros
+    for (int s = range; s < a.B; s += ranges) {
+        const Row r = row_of(a, s);
+        if (r.t1 > r.t0) continue;
+        const int len = a.seq_len[s];
+        if (len != 0 && kvh == 0 && tid == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, s);
+        uint16_t *o = a.out + ((int64_t)s * a.Hq + kvh * G) * D;
+        for (int i = tid; i < G * D / 8; i += C::threads) reinterpret_cast<uint4 *>(o)[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse && tid < G) a.lse[(int64_t)s * a.Hq + kvh * G + tid] = -INFINITY;
+    }
+    __syncthreads();
+    const long long n_tiles = x1 - x0;
+    if (kvh == 0 && tid == 0 && range < kMaxRanges) ws.meta[range] = make_int2(-1, 0);
+    if (n_tiles == 0) return;
+
+    const uint32_t base = smem_u32(smem);
+    float *S = reinterpret_cast<float *>(smem + NS * C::stage);
+    Cursor in, at;                                 // the loads' place, and the products'
+    in.at(a, start[0], start[1]);
+    at = in;
+
+    // ---- loads: page ids one tile ahead of the copies
+    int page = -1;
+    auto fetch_page = [&]() {
+        const int tok = in.t * kTile + warp * TW + lane;
+        page = -1;
+        if (lane < TW && tok >= in.r.lo && tok < in.r.len) page = __ldg(a.table + in.s * a.ld + tok / a.page_size);
+    };
+    auto issue = [&](int stage, bool first) {      // tile `in`, whose page ids are in `page`
+        const uint32_t st = base + stage * C::stage;
+        const int tok = in.t * kTile + warp * TW + lane;
+        const bool wanted = lane < TW && tok >= in.r.lo && tok < in.r.len;
+        int slot = -1;
+        if (wanted) {
+            if (page >= 0 && page < a.n_pages)
+                slot = page * a.page_size + tok % a.page_size;
+            else if (kvh == 0)
+                record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, in.s);
+        }
+        const uint32_t real = __ballot_sync(0xffffffffu, slot >= 0);
+        if (lane == 0) real_tok[stage][warp] = real;
+        const char *kp = static_cast<const char *>(a.k), *vp = static_cast<const char *>(a.v);
+        const int chunk = lane % C::chunks;
+#pragma unroll
+        for (int i = 0; i < TW / C::rows_per_copy; ++i) {
+            const int r = i * C::rows_per_copy + lane / C::chunks;
+            const int sl = __shfl_sync(0xffffffffu, slot, r);
+            const int t = warp * TW + r;
+            const int64_t from = sl < 0 ? 0 : ((int64_t)sl * Hkv + kvh) * C::row + chunk * 16;
+            const uint32_t to = st + t * C::row + ((chunk ^ (t & 7)) << 4);
+            cp_async16_zfill(to, kp + from, sl >= 0);
+            cp_async16_zfill(to + C::k_bytes, vp + from, sl >= 0);
+        }
+        if (F8 && lane < TW) {
+            constexpr int SB = F8 ? C::groups * 4 : 4;
+            const int64_t from = slot < 0 ? 0 : ((int64_t)slot * Hkv + kvh) * C::groups;
+            const uint32_t to = st + 2 * C::k_bytes + (warp * TW + lane) * SB;
+            cp_async_small_zfill<SB>(to, a.k_scales + from, slot >= 0);
+            cp_async_small_zfill<SB>(to + C::s_bytes, a.v_scales + from, slot >= 0);
+        }
+        if (first) {                               // the row's queries, heads behind G as zeros
+            const uint16_t *q = a.q + in.s * a.q_ld + (int64_t)kvh * G * D;
+            const uint32_t to = st + 2 * C::k_bytes + 2 * C::s_bytes;
+            for (int i = tid; i < GT * D / 8; i += C::threads) {
+                const int h = i / (D / 8), ch = i % (D / 8);
+                cp_async16_zfill(to + h * D * 2 + ((ch ^ (h & 7)) << 4), q + (h < G ? h * D + ch * 8 : 0), h < G);
+            }
+        }
+    };
+    long long issued = 0;
+    int in_stage = 0;
+    bool in_first = true;
+    auto advance = [&]() {                         // issue the next tile (or an empty group) and step on
+        if (issued < n_tiles) {
+            issue(in_stage, in_first);
+            in_stage = in_stage + 1 == NS ? 0 : in_stage + 1;
+            ++issued;
+            if (issued < n_tiles) {
+                const int was = in.s;
+                in.next(a);
+                in_first = in.s != was;
+                fetch_page();
+            }
+        }
+        cp_async_commit();
+    };
+    fetch_page();
+#pragma unroll 1
+    for (int i = 0; i < NS - 1; ++i) advance();
+
+    // ---- products
+    constexpr int KS = D / 16;
+    uint32_t qf[KS][2 * HR];                       // Q operand: rows g (and g + 8), two k halves
+    float q_scale[HR];                             // logit = score x q_scale (x K scale)
+    float m[HR], l[HR], ref[HR];                   // running maximum, this lane's part of the sum, FP8 weights' reference
+    float o[4][4];
+    bool begins = start[1] == 0;                   // the segment starts its sequence
+    bool first = true;
+    int stage = 0;
+    for (long long i = 0; i < n_tiles; ++i, stage = stage + 1 == NS ? 0 : stage + 1) {
+        cp_async_wait<NS - 2>();
+        __syncthreads();                           // tile i is in; every warp has left tile i - 1
+        advance();
+        const uint32_t st = base + stage * C::stage;
+        if (first) {
+            const uint32_t qa = st + 2 * C::k_bytes + 2 * C::s_bytes;
+            if (!F8) {
+                if (GT == 16) {
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        const int h = (lane & 7) + ((lane >> 3) & 1) * 8, ch = 2 * k + (lane >> 4);
+                        uint32_t r[4];
+                        ldmatrix4(qa + h * D * 2 + ((ch ^ (h & 7)) << 4), r);
+                        qf[k][0] = r[0], qf[k][1] = r[2];
+                        qf[k][2 * HR - 2] = GT == 16 ? r[1] : r[0], qf[k][2 * HR - 1] = GT == 16 ? r[3] : r[2];
                     }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < KS; k += 2) {
+                        const int h = lane & 7, ch = 2 * k + (lane >> 3);
+                        uint32_t r[4];
+                        ldmatrix4(qa + h * D * 2 + ((ch ^ h) << 4), r);
+                        qf[k][0] = r[0], qf[k][1] = r[1];
+                        qf[k + 1][0] = r[2], qf[k + 1][1] = r[3];
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < HR; ++h) q_scale[h] = a.scale_log2;
+            } else {
+                // k index (2c, 2c+1 | 2c+8, 2c+9) of a step stands for dims 16k + 4c .. 4c + 3, as the codes of K lie
+#pragma unroll
+                for (int h = 0; h < HR; ++h) {
+                    const uint32_t qrow = qa + (g + 8 * h) * D * 2;
+                    float top = 0.f;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        uint32_t x, y;
+                        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                                     : "=r"(x), "=r"(y)
+                                     : "r"(qrow + (((2 * k + (c >> 1)) ^ g) << 4) + (c & 1) * 8));
+                        qf[k][2 * h] = x, qf[k][2 * h + 1] = y;
+                        top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(x << 16)), fabsf(__uint_as_float(x & 0xFFFF0000u))),
+                                               fmaxf(fabsf(__uint_as_float(y << 16)), fabsf(__uint_as_float(y & 0xFFFF0000u)))));
+                    }
+                    top = quad_max(top);
+                    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                    q_scale[h] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const uint32_t x = qf[k][2 * h + z];
+                            qf[k][2 * h + z] = f16x2(__uint_as_float(x << 16) * down,
+                                                     __uint_as_float(x & 0xFFFF0000u) * down);
+                        }
                 }
             }
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            if (lane == 0) w[i] = slots[i] >= 0 ? x : -INFINITY;
+            for (int h = 0; h < HR; ++h) m[h] = -INFINITY, l[h] = 0.f, ref[h] = 0.f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[n][k] = 0.f;
+            first = false;
         }
-        __syncthreads();
-        float mn = m;
-        for (int i = 0; i < n; ++i) mn = fmaxf(mn, w[i]);
-        const float ref = mn == -INFINITY ? 0.f : mn, alpha = exp2f(m - ref);
-        l *= alpha;
-        acc *= alpha;
-        for (int i = 0; i < n; ++i) {
-            const float p = exp2f(w[i] - ref);
-            l += p;
-            if (tid < D && slots[i] >= 0) {
-                const int64_t row = slots[i] * a.Hkv + g;
-                float v;
-                if (F8) {
-                    float f[16];
-                    const uint32_t c = static_cast<const uint8_t *>(a.v)[row * D + tid];
-                    e4m3x16_to_f32(make_uint4(c, 0, 0, 0), f);
-                    v = f[0] * a.v_scales[row * (D / 128) + tid / 128];
-                } else {
-                    v = bf16_bits_to_float(static_cast<const uint16_t *>(a.v)[row * D + tid]);
+        // S = Q K^T over this warp's tokens
+        {
+            constexpr int NQ = TW / 8;             // 8-token tiles
+            constexpr int CH = F8 ? C::groups * (NQ == 1 ? 2 : 1) : 4 / NQ;   // independent sums of a tile
+            const uint32_t real = real_tok[stage][warp];
+#pragma unroll
+            for (int nt = 0; nt < NQ; ++nt) {
+                float acc[CH > 0 ? CH : 1][4];
+#pragma unroll
+                for (int x = 0; x < CH; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
+                const uint32_t krow = st + (warp * TW + nt * 8 + (lane & 7)) * C::row;
+#pragma unroll
+                for (int k = 0; k < C::chunks / 4; ++k) {
+                    uint32_t b[4];
+                    ldmatrix4(krow + (((4 * k + (lane >> 3)) ^ (lane & 7)) << 4), b);
+                    if (!F8) {
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const uint32_t qa[4] = {qf[2 * k + z][0], HR == 2 ? qf[2 * k + z][2 * HR - 2] : 0u,
+                                                    qf[2 * k + z][1], HR == 2 ? qf[2 * k + z][2 * HR - 1] : 0u};
+                            mma16816<false>(acc[(2 * k + z) % CH], qa, b[2 * z], b[2 * z + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int step = 4 * k + z;
+                            const uint32_t qa[4] = {qf[step][0], HR == 2 ? qf[step][2 * HR - 2] : 0u, qf[step][1],
+                                                    HR == 2 ? qf[step][2 * HR - 1] : 0u};
+                            constexpr int per_group = CH / (C::groups > 0 ? C::groups : 1);
+                            mma16816<true>(acc[(step / 8) * per_group + (step % 8) % (per_group > 0 ? per_group : 1)], qa,
+                                           e4m3_to_f16x2(b[z], 0), e4m3_to_f16x2(b[z], 1));
+                        }
+                    }
                 }
-                acc = fmaf(p, v, acc);
+                float s[4];
+                const int t = nt * 8 + 2 * c;      // this lane's two tokens of the warp's share
+                if (!F8) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        s[x] = acc[0][x];
+#pragma unroll
+                        for (int y = 1; y < CH; ++y) s[x] += acc[y][x];
+                    }
+                } else {
+                    const float *ks = reinterpret_cast<const float *>(smem + stage * C::stage + 2 * C::k_bytes) +
+                                      (warp * TW + t) * C::groups;
+                    constexpr int per_group = CH / (C::groups > 0 ? C::groups : 1);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        s[x] = 0.f;
+#pragma unroll
+                        for (int gr = 0; gr < C::groups; ++gr) {
+                            float sum = acc[gr * per_group][x];
+#pragma unroll
+                            for (int y = 1; y < per_group; ++y) sum += acc[gr * per_group + y][x];
+                            s[x] = fmaf(sum, ks[(x & 1) * C::groups + gr], s[x]);
+                        }
+                    }
+                }
+                const bool r0 = (real >> t) & 1, r1 = (real >> (t + 1)) & 1;
+#pragma unroll
+                for (int h = 0; h < HR; ++h)
+                    *reinterpret_cast<float2 *>(S + (g + 8 * h) * kSPitch + warp * TW + t) =
+                        make_float2(r0 ? s[2 * h] * q_scale[h] : -INFINITY, r1 ? s[2 * h + 1] * q_scale[h] : -INFINITY);
             }
         }
-        m = mn;
+        __syncthreads();
+        // weights of all 64 tokens, in the operand layout
+        float p[HR][16];
+        float alpha[HR];
+#pragma unroll
+        for (int h = 0; h < HR; ++h) {
+            const float *srow = S + (g + 8 * h) * kSPitch + 2 * c;
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 v = *reinterpret_cast<const float2 *>(srow + 8 * k);
+                p[h][2 * k] = v.x, p[h][2 * k + 1] = v.y;
+                top = fmaxf(top, fmaxf(v.x, v.y));
+            }
+            top = fmaxf(m[h], quad_max(top));
+            const float at_top = top == -INFINITY ? 0.f : top;
+            alpha[h] = ex2(m[h] - at_top);
+            m[h] = top;
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                p[h][k] = ex2(p[h][k] - at_top);
+                sum += p[h][k];
+            }
+            l[h] = fmaf(l[h], alpha[h], sum);
+        }
+        if (F8) {
+            // w = p v_scale relative to their running maximum
+            const float *vs = reinterpret_cast<const float *>(smem + stage * C::stage + 2 * C::k_bytes + C::s_bytes) +
+                              (C::groups == 2 ? warp / 4 : 0);
+            constexpr int VG = C::groups > 0 ? C::groups : 1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float v0 = vs[(8 * k + 2 * c) * VG], v1 = vs[(8 * k + 2 * c + 1) * VG];
+#pragma unroll
+                for (int h = 0; h < HR; ++h) p[h][2 * k] *= v0, p[h][2 * k + 1] *= v1;
+            }
+#pragma unroll
+            for (int h = 0; h < HR; ++h) {
+                float top = 0.f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) top = fmaxf(top, p[h][k]);
+                const float old = ref[h] * alpha[h];
+                ref[h] = fmaxf(old, quad_max(top));
+                const float inv = ref[h] > 0.f ? __fdividef(1.f, ref[h]) : 0.f;
+                alpha[h] = old * inv;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) p[h][k] *= inv;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            o[n][0] *= alpha[0], o[n][1] *= alpha[0];
+            if (HR == 2) o[n][2] *= alpha[HR - 1], o[n][3] *= alpha[HR - 1];
+        }
+        // O += P V over this warp's 32 dims
+        const uint32_t vt = st + C::k_bytes + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::row;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t hi[4], lo[4];
+            hi[1] = hi[3] = lo[1] = lo[3] = 0u;
+#pragma unroll
+            for (int h = 0; h < HR; ++h)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const float u = p[h][4 * k + 2 * z], v = p[h][4 * k + 2 * z + 1];
+                    if (F8) {
+                        hi[2 * z + h] = f16x2(u, v);
+                    } else {
+                        const uint32_t w = bf16x2(u, v);
+                        hi[2 * z + h] = w;
+                        lo[2 * z + h] = bf16x2(u - __uint_as_float(w << 16), v - __uint_as_float(w & 0xFFFF0000u));
+                    }
+                }
+            if (!F8) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t b[4];
+                    ldmatrix4_trans(vt + 16 * k * C::row + (((4 * warp + 2 * j + (lane >> 4)) ^ (lane & 7)) << 4), b);
+                    mma16816<false>(o[2 * j], hi, b[0], b[1]);
+                    mma16816<false>(o[2 * j + 1], hi, b[2], b[3]);
+                    mma16816<false>(o[2 * j], lo, b[0], b[1]);
+                    mma16816<false>(o[2 * j + 1], lo, b[2], b[3]);
+                }
+            } else {
+                // a 16-bit element of the transposed load is two codes, dims 2n and 2n + 1 of a chunk of 16
+                uint32_t b[4];
+                ldmatrix4_trans(vt + 16 * k * C::row + (((2 * warp + (lane >> 4)) ^ (lane & 7)) << 4), b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = __byte_perm(b[j], 0, 0x3120);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int odd = 0; odd < 2; ++odd)
+                        mma16816<true>(o[2 * j + odd], hi, e4m3_to_f16x2(b[2 * j], odd), e4m3_to_f16x2(b[2 * j + 1], odd));
+            }
+        }
+        // the segment's end
+        const bool ends = at.t + 1 == at.r.t1;
+        if (ends || i + 1 == n_tiles) {
+            const bool whole = begins && ends;
+            const int slot = 2 * range + (begins ? 1 : 0);
+#pragma unroll
+            for (int h = 0; h < HR; ++h) {
+                const int row = g + 8 * h;
+                const float sum = quad_sum(l[h]);
+                if (row >= G) continue;
+                const int head = kvh * G + row;
+                float f = F8 ? ref[h] : 1.f;
+                if (whole) f = sum == 0.f ? 0.f : f / sum;
+                float *po = ws.o + ((int64_t)slot * a.Hq + head) * D + warp * 32;
+                uint16_t *out = a.out + ((int64_t)at.s * a.Hq + head) * D + warp * 32;
+#pragma unroll
+                for (int j = 0; j < (F8 ? 2 : 4); ++j) {
+                    if (!F8) {
+                        const float x = o[j][2 * h] * f, y = o[j][2 * h + 1] * f;
+                        if (whole)
+                            *reinterpret_cast<uint32_t *>(out + 8 * j + 2 * c) = bf16x2(x, y);
+                        else
+                            *reinterpret_cast<float2 *>(po + 8 * j + 2 * c) = make_float2(x, y);
+                    } else {
+                        const float4 x = make_float4(o[2 * j][2 * h] * f, o[2 * j + 1][2 * h] * f, o[2 * j][2 * h + 1] * f,
+                                                     o[2 * j + 1][2 * h + 1] * f);
+                        if (whole)
+                            *reinterpret_cast<uint2 *>(out + 16 * j + 4 * c) = make_uint2(bf16x2(x.x, x.y), bf16x2(x.z, x.w));
+                        else
+                            *reinterpret_cast<float4 *>(po + 16 * j + 4 * c) = x;
+                    }
+                }
+                if (warp == 0 && c == 0) {
+                    if (!whole)
+                        ws.ml[(int64_t)slot * a.Hq + head] = make_float2(m[h], sum);
+                    else if (a.lse)
+                        a.lse[(int64_t)at.s * a.Hq + head] = sum == 0.f ? -INFINITY : (m[h] + log2f(sum)) * kLn2;
+                }
+            }
+            if (begins && !ends && kvh == 0 && tid == 0) {
+                // the sequence's last tile is number `end` of the list: how many ranges it spans
+                const long long end = x0 + i + (at.r.t1 - 1 - at.t);
+                ws.meta[range] = make_int2(at.s, (int)(((end + 1) * R - 1) / total) - range + 1);
+            }
+            begins = first = true;
+        }
+        if (i + 1 < n_tiles) at.next(a);
     }
-    if (tid < D) a.out[((int64_t)s * a.Hq + h) * D + tid] = float_to_bf16_bits(l > 0.f ? acc / l : 0.f);
-    if (tid == 0 && a.lse) a.lse[(int64_t)s * a.Hq + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// The partials of a sequence that range `blockIdx.x` starts and leaves unfinished, joined for one head:
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, in the ranges' order.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedArgs a, PagedScratch ws) {
+    constexpr int cols = D / 4, rows = kJoinThreads / cols;
+    __shared__ float w[kMaxRanges], red[kJoinThreads / 32 + 1], red2[kJoinThreads / 32 + 1];
+    __shared__ float4 acc[kJoinThreads];
+    const int range = blockIdx.x, head = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 meta = ws.meta[range];
+    if (meta.x < 0) return;
+    const int n = meta.y;
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * range + 1 : 2 * (range + i)) * a.Hq + head; };
+    float top = -INFINITY;
+    for (int i = tid; i < n; i += kJoinThreads) top = fmaxf(top, ws.ml[slot(i)].x);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, red[i]);
+    const float M = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    for (int i = tid; i < n; i += kJoinThreads) {
+        const float2 ml = ws.ml[slot(i)];
+        w[i] = exp2f(ml.x - M);
+        sum = fmaf(w[i], ml.y, sum);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) red2[warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) sum += red2[i];
+    const int col = tid % cols;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = tid / cols; i < n; i += rows) {
+        const float4 v = *reinterpret_cast<const float4 *>(ws.o + slot(i) * D + 4 * col);
+        x.x = fmaf(w[i], v.x, x.x), x.y = fmaf(w[i], v.y, x.y);
+        x.z = fmaf(w[i], v.z, x.z), x.w = fmaf(w[i], v.w, x.w);
+    }
+    acc[tid] = x;
+    __syncthreads();
+    if (tid >= cols) return;
+#pragma unroll
+    for (int i = 1; i < rows; ++i) {
+        const float4 v = acc[tid + i * cols];
+        x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
+    }
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2 *>(a.out + ((int64_t)meta.x * a.Hq + head) * D + 4 * col) =
+        make_uint2(bf16x2(x.x * f, x.y * f), bf16x2(x.z * f, x.w * f));
+    if (tid == 0 && a.lse)
+        a.lse[(int64_t)meta.x * a.Hq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// CTAs of one wave on the current device (cached per device; 0 on an error).
+template <typename C>
+int wave() {
+    static int cached[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (cached[dev] == 0) {
+        int sms = 0, per_sm = 0;
+        if (cudaFuncSetAttribute(paged_tile_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_tile_kernel<C>, C::threads, C::smem) != cudaSuccess)
+            return 0;
+        cached[dev] = std::min(sms * per_sm, max_ctas(C::D));
+    }
+    return cached[dev];
+}
+
+PagedScratch scratch_of(char *w, int D, int Hq, int Hkv) {
+    const size_t slots = 2 * (size_t)ranges_for(max_ctas(D), Hkv) * Hq;
+    PagedScratch s;
+    s.meta = reinterpret_cast<int2 *>(w);
+    s.ml = reinterpret_cast<float2 *>(w + kMaxRanges * sizeof(int2));
+    s.o = reinterpret_cast<float *>(w + kMaxRanges * sizeof(int2) + (slots * sizeof(float2) + 255) / 256 * 256);
+    return s;
+}
+
+template <typename C>
+cudaError_t launch(const PagedArgs &a, cudaStream_t st) {
+    const int ctas = wave<C>();
+    if (ctas == 0) {
+        const cudaError_t e = cudaGetLastError();
+        return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    }
+    const int ranges = ranges_for(ctas, a.Hkv);
+    const PagedScratch ws = scratch_of(a.scratch, C::D, a.Hq, a.Hkv);
+    paged_tile_kernel<C><<<ranges * a.Hkv, C::threads, C::smem, st>>>(a, ws, ranges);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || ranges == 1) return e;      // one range cuts no sequence
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranges - 1, a.Hq);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::D>, a, ws);
 }
 
 template <int D, bool F8>
-cudaError_t launch(const PagedArgs &a, cudaStream_t st) {
-    paged_plain_kernel<D, F8><<<dim3(a.Hq, a.B), kPagedThreads, 0, st>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_heads(const PagedArgs &a, cudaStream_t st) {
+    return a.G <= 8 ? launch<PagedCfg<D, 8, F8>>(a, st) : launch<PagedCfg<D, 16, F8>>(a, st);
 }
 
 }  // namespace
 
-size_t paged_scratch_bytes(int, int, int) { return 0; }
+size_t paged_scratch_bytes(int D, int Hq, int Hkv) {
+    const size_t slots = 2 * (size_t)ranges_for(max_ctas(D), Hkv) * Hq;
+    return kMaxRanges * sizeof(int2) + (slots * sizeof(float2) + 255) / 256 * 256 + slots * D * sizeof(float);
+}
 
 cudaError_t launch_paged_decode(const PagedArgs &a, int D, bool fp8, cudaStream_t st) {
     switch (D) {
-        case 64: return fp8 ? cudaErrorInvalidValue : launch<64, false>(a, st);
-        case 128: return fp8 ? launch<128, true>(a, st) : launch<128, false>(a, st);
-        case 256: return fp8 ? launch<256, true>(a, st) : launch<256, false>(a, st);
+        case 64: return fp8 ? cudaErrorInvalidValue : launch_heads<64, false>(a, st);
+        case 128: return fp8 ? launch_heads<128, true>(a, st) : launch_heads<128, false>(a, st);
+        case 256: return fp8 ? launch_heads<256, true>(a, st) : launch_heads<256, false>(a, st);
         default: return cudaErrorInvalidValue;
     }
 }
