@@ -460,46 +460,67 @@ def qsa_sparse_mla_decode(q, kv_rows, rows, n_rows, out, lse, ws, softmax_scale:
 
 
 # ---------------------------------------------------------------------------- paged K/V cache
-def _cuda(t, dtype, name) -> int:
-    """The address of a contiguous tensor on the current device."""
+# These calls run once per layer and token: their checks are a chain of cheap comparisons, and what is wrong is
+# only worded (by _refuse) once one of them has failed.
+_bf16, _i32, _u8, _f32, _i64 = torch.bfloat16, torch.int32, torch.uint8, torch.float32, torch.int64
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _refuse(t, dtype, name, dev, shape=None, host=False):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.get_device() != dev and not (host and t.get_device() == -1):
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _on(t, dtype, name, dev):
+    """The address of a contiguous tensor on the current device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype, name, dev)
     return t.data_ptr()
 
 
-def _cache(t, dtype, shape, name) -> int:
+def _ints(t, n, name, dev):
+    """The address of int32 [n]."""
+    if t.dtype is not _i32 or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+        _refuse(t, _i32, name, dev, (n,))
+    return t.data_ptr()
+
+
+def _ints2(t, n, m, name, dev):
+    """The address of int32 [n, m]."""
+    if t.dtype is not _i32 or t.get_device() != dev or t.shape != (n, m) or not t.is_contiguous():
+        _refuse(t, _i32, name, dev, (n, m))
+    return t.data_ptr()
+
+
+def _cache(t, dtype, shape, name, dev):
     """The address of a cache array on the current device or in pinned host memory."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
-    if t.get_device() not in (-1, torch.cuda.current_device()):
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() not in (dev, -1):
+        _refuse(t, dtype, name, dev, shape, host=True)
     return t.data_ptr()
 
 
-def _head_rows(t, n, heads, dim, name):
+def _head_rows(t, n, heads, dim, name, dev):
     """(address, elements between rows) of bf16 [n, heads, dim] with contiguous heads, on the current device."""
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if tuple(t.shape) != (n, heads, dim):
-        raise ValueError(f"{name} must be [{n}, {heads}, {dim}], got {list(t.shape)}")
+    if t.dtype is not _bf16 or t.get_device() != dev or t.shape != (n, heads, dim):
+        if t.dtype is _bf16 and tuple(t.shape) == (n, heads, dim):
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+        _refuse(t, _bf16, name, dev, (n, heads, dim))
     ld, head, one = t.stride()
     if one != 1 or (head != dim and heads > 1):
         raise ValueError(f"the heads of {name} must be contiguous")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
     return t.data_ptr(), ld if n > 1 else heads * dim
 
 
-def _ints(t, shape, name) -> int:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return _cuda(t, torch.int32, name)
+def _stream_of(stream, dev):
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
 class RopeTable:
@@ -528,11 +549,14 @@ def rope_table(head_dim: int, rot_dim: int | None = None, rot_begin: int = 0, in
 def qsa_rope(rope: RopeTable, x, pos, out, stream=None):
     """out[n, h] = x[n, h] turned to position pos[n]: x, out [N, H, head_dim] bf16 (rows may be strided; out may
     be x), pos [N] int32."""
-    n, heads = x.shape[0], x.shape[1]
-    x_ptr, x_ld = _head_rows(x, n, heads, rope.cfg.head_dim, "x")
-    out_ptr, out_ld = _head_rows(out, n, heads, rope.cfg.head_dim, "out")
-    _check(load().qsa_rope(C.byref(rope.cfg), _cuda(rope.phase, torch.int64, "phase"), rope.amplitude, x_ptr, x_ld,
-                           _ints(pos, (n,), "pos"), n, heads, out_ptr, out_ld, _stream(stream)), "qsa_rope")
+    dev, cfg = torch.cuda.current_device(), rope.cfg
+    n, heads, _ = x.shape
+    x_ptr, x_ld = _head_rows(x, n, heads, cfg.head_dim, "x", dev)
+    out_ptr, out_ld = _head_rows(out, n, heads, cfg.head_dim, "out", dev)
+    st = load().qsa_rope(cfg, _on(rope.phase, _i64, "phase", dev), rope.amplitude, x_ptr, x_ld,
+                         _ints(pos, n, "pos", dev), n, heads, out_ptr, out_ld, _stream_of(stream, dev))
+    if st:
+        _check(st, "qsa_rope")
 
 
 def make_paged_config(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, softmax_scale: float = 0.0,
@@ -564,83 +588,101 @@ def pages_workspace(n_rows: int, n_pages: int, device="cuda", stream=None):
     return _zeroed(n, device, stream)
 
 
-def _append(fn, name, cfg, rope, q, k, v, pos, seq, q_out, planes, n_pages, table, ws, stream):
-    n, D = k.shape[0], cfg.head_dim
-    q_ptr, q_ld = (None, 0) if q is None else _head_rows(q, n, cfg.n_q_heads, D, "q")
-    q_out_ptr, q_out_ld = (None, 0) if q is None else _head_rows(q_out, n, cfg.n_q_heads, D, "q_out")
-    _check(fn(C.byref(cfg), C.byref(rope.cfg), _cuda(rope.phase, torch.int64, "phase"), rope.amplitude, q_ptr, q_ld,
-              *_head_rows(k, n, cfg.n_kv_heads, D, "k"), *_head_rows(v, n, cfg.n_kv_heads, D, "v"),
-              None if seq is None else _ints(seq, (n,), "seq"), _ints(pos, (n,), "pos"), n, q_out_ptr, q_out_ld,
-              *planes, n_pages, _cuda(table, torch.int32, "table"), table.shape[1], table.shape[0], *_ws_args(ws),
-              _stream(stream)), name)
+def _append(name, cfg, rope, q, k, v, pos, seq, q_out, planes, n_pages, table, ws, stream, dev):
+    n, D, Hkv = k.shape[0], cfg.head_dim, cfg.n_kv_heads
+    if q is None:
+        q_ptr, q_ld, q_out_ptr, q_out_ld = None, 0, None, 0
+    else:
+        q_ptr, q_ld = _head_rows(q, n, cfg.n_q_heads, D, "q", dev)
+        q_out_ptr, q_out_ld = _head_rows(q_out, n, cfg.n_q_heads, D, "q_out", dev)
+    k_ptr, k_ld = _head_rows(k, n, Hkv, D, "k", dev)
+    v_ptr, v_ld = _head_rows(v, n, Hkv, D, "v", dev)
+    rows, ld = table.shape
+    st = getattr(load(), name)(cfg, rope.cfg, _on(rope.phase, _i64, "phase", dev), rope.amplitude, q_ptr, q_ld, k_ptr,
+                               k_ld, v_ptr, v_ld, None if seq is None else _ints(seq, n, "seq", dev),
+                               _ints(pos, n, "pos", dev), n, q_out_ptr, q_out_ld, *planes, n_pages,
+                               _on(table, _i32, "table", dev), ld, rows, _on(ws, _u8, "ws", dev), ws.numel(),
+                               _stream_of(stream, dev))
+    if st:
+        _check(st, name)
 
 
-def _bf16_planes(cfg, k_cache, v_cache):
+def _bf16_planes(cfg, k_cache, v_cache, dev):
     shape = (k_cache.shape[0], cfg.page_size, cfg.n_kv_heads, cfg.head_dim)
-    return (_cache(k_cache, torch.bfloat16, shape, "k_cache"), _cache(v_cache, torch.bfloat16, shape, "v_cache"))
+    return _cache(k_cache, _bf16, shape, "k_cache", dev), _cache(v_cache, _bf16, shape, "v_cache", dev)
 
 
-def _fp8_planes(cfg, kv8):
+def _fp8_planes(cfg, kv8, dev):
     k_codes, k_scales, v_codes, v_scales = kv8
     shape = (k_codes.shape[0], cfg.page_size, cfg.n_kv_heads, cfg.head_dim)
     groups = shape[:3] + (cfg.head_dim // 128,)
-    return (_cache(k_codes, torch.uint8, shape, "k_codes"), _cache(k_scales, torch.float32, groups, "k_scales"),
-            _cache(v_codes, torch.uint8, shape, "v_codes"), _cache(v_scales, torch.float32, groups, "v_scales"))
+    return (_cache(k_codes, _u8, shape, "k_codes", dev), _cache(k_scales, _f32, groups, "k_scales", dev),
+            _cache(v_codes, _u8, shape, "v_codes", dev), _cache(v_scales, _f32, groups, "v_scales", dev))
 
 
 def qsa_rope_append(cfg, rope: RopeTable, q, k, v, pos, seq, q_out, k_cache, v_cache, table, ws, stream=None):
     """New tokens into a paged cache: q [N, Hq, D] turned into q_out (both None: K and V only), k [N, Hkv, D]
     turned and v stored at position pos[n] of row seq[n] (seq None: row n). k_cache, v_cache
     [n_pages, page_size, Hkv, D] bf16; table [rows, max_pages] int32. q, k, v may be slices of one tensor."""
-    _append(load().qsa_rope_append, "qsa_rope_append", cfg, rope, q, k, v, pos, seq, q_out,
-            _bf16_planes(cfg, k_cache, v_cache), k_cache.shape[0], table, ws, stream)
+    dev = torch.cuda.current_device()
+    _append("qsa_rope_append", cfg, rope, q, k, v, pos, seq, q_out, _bf16_planes(cfg, k_cache, v_cache, dev),
+            k_cache.shape[0], table, ws, stream, dev)
 
 
 def qsa_rope_append_fp8kv(cfg, rope: RopeTable, q, k, v, pos, seq, q_out, kv8, table, ws, stream=None):
     """qsa_rope_append into FP8 rows: kv8 = (k_codes, k_scales, v_codes, v_scales), codes
     [n_pages, page_size, Hkv, D] uint8 and scales [..., D / 128] fp32."""
-    _append(load().qsa_rope_append_fp8kv, "qsa_rope_append_fp8kv", cfg, rope, q, k, v, pos, seq, q_out,
-            _fp8_planes(cfg, kv8), kv8[0].shape[0], table, ws, stream)
+    dev = torch.cuda.current_device()
+    _append("qsa_rope_append_fp8kv", cfg, rope, q, k, v, pos, seq, q_out, _fp8_planes(cfg, kv8, dev),
+            kv8[0].shape[0], table, ws, stream, dev)
 
 
-def _paged(fn, name, cfg, q, planes, n_pages, table, seq_len, out, lse, ws, stream):
-    B = q.shape[0]
-    if table.dim() != 2 or table.shape[0] != B:
-        raise ValueError(f"table must be [{B}, max_pages], got {list(table.shape)}")
-    if tuple(out.shape) != (B, cfg.n_q_heads, cfg.head_dim):
-        raise ValueError(f"out must be [{B}, {cfg.n_q_heads}, {cfg.head_dim}], got {list(out.shape)}")
-    if lse is not None and tuple(lse.shape) != (B, cfg.n_q_heads):
-        raise ValueError(f"lse must be [{B}, {cfg.n_q_heads}], got {list(lse.shape)}")
-    _check(fn(C.byref(cfg), *_head_rows(q, B, cfg.n_q_heads, cfg.head_dim, "q"), *planes, n_pages,
-              _cuda(table, torch.int32, "table"), table.shape[1], _ints(seq_len, (B,), "seq_len"), B,
-              _cuda(out, torch.bfloat16, "out"), None if lse is None else _cuda(lse, torch.float32, "lse"),
-              *_ws_args(ws), _stream(stream)), name)
+def _paged(name, cfg, q, planes, n_pages, table, seq_len, out, lse, ws, stream, dev):
+    B, ld = table.shape
+    Hq, D = cfg.n_q_heads, cfg.head_dim
+    q_ptr, q_ld = _head_rows(q, B, Hq, D, "q", dev)
+    if out.dtype is not _bf16 or out.get_device() != dev or out.shape != (B, Hq, D) or not out.is_contiguous():
+        _refuse(out, _bf16, "out", dev, (B, Hq, D))
+    if lse is not None and (lse.dtype is not _f32 or lse.get_device() != dev or lse.shape != (B, Hq)
+                            or not lse.is_contiguous()):
+        _refuse(lse, _f32, "lse", dev, (B, Hq))
+    st = getattr(load(), name)(cfg, q_ptr, q_ld, *planes, n_pages, _on(table, _i32, "table", dev), ld,
+                               _ints(seq_len, B, "seq_len", dev), B, out.data_ptr(),
+                               None if lse is None else lse.data_ptr(), _on(ws, _u8, "ws", dev), ws.numel(),
+                               _stream_of(stream, dev))
+    if st:
+        _check(st, name)
 
 
 def qsa_paged_decode(cfg, q, k_cache, v_cache, table, seq_len, out, lse, ws, stream=None):
     """Attention of one new token per sequence over its seq_len[s] cached tokens: q [B, Hq, D] (rows may be
     strided), caches [n_pages, page_size, Hkv, D] bf16, table [B, max_pages], out [B, Hq, D], lse [B, Hq] or None."""
-    _paged(load().qsa_paged_decode, "qsa_paged_decode", cfg, q, _bf16_planes(cfg, k_cache, v_cache),
-           k_cache.shape[0], table, seq_len, out, lse, ws, stream)
+    dev = torch.cuda.current_device()
+    _paged("qsa_paged_decode", cfg, q, _bf16_planes(cfg, k_cache, v_cache, dev), k_cache.shape[0], table, seq_len, out,
+           lse, ws, stream, dev)
 
 
 def qsa_paged_decode_fp8kv(cfg, q, kv8, table, seq_len, out, lse, ws, stream=None):
     """qsa_paged_decode over FP8 rows kv8 = (k_codes, k_scales, v_codes, v_scales)."""
-    _paged(load().qsa_paged_decode_fp8kv, "qsa_paged_decode_fp8kv", cfg, q, _fp8_planes(cfg, kv8), kv8[0].shape[0],
-           table, seq_len, out, lse, ws, stream)
+    dev = torch.cuda.current_device()
+    _paged("qsa_paged_decode_fp8kv", cfg, q, _fp8_planes(cfg, kv8, dev), kv8[0].shape[0], table, seq_len, out, lse, ws,
+           stream, dev)
 
 
-def _plane_groups(planes, n_pages):
-    """The C array of pool tensors: each [n_planes, n_pages, ...] with contiguous pages."""
-    groups = (qsa_page_planes * max(len(planes), 1))()
-    for i, t in enumerate(planes):
-        if t.dim() < 3 or t.shape[1] != n_pages or not t[0].is_contiguous():
-            raise ValueError(f"planes[{i}] must be [n_planes, {n_pages}, ...] with contiguous planes")
-        if t.get_device() not in (-1, torch.cuda.current_device()):
-            raise ValueError(f"planes[{i}] is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _plane_groups(planes, n_pages, dev):
+    """The C array of pool tensors: each [n_planes, n_pages, ...] with contiguous planes."""
+    groups = (qsa_page_planes * (len(planes) or 1))()
+    for t, g in zip(planes, groups):
+        count, pages = t.shape[:2]
         size = t.element_size()
-        groups[i] = qsa_page_planes(t.data_ptr(), t.stride(0) * size if t.shape[0] > 1 else 0,
-                                    t.stride(1) * size if n_pages > 1 else t[0].numel() * size, t.shape[0])
+        strides = t.stride()
+        page = t.numel() // (count * pages or 1) * size
+        if pages != n_pages or not (t.is_contiguous() or t[0].is_contiguous()):
+            raise ValueError(f"planes must be [n_planes, {n_pages}, ...] with contiguous planes, got {list(t.shape)}")
+        if t.get_device() not in (dev, -1):
+            raise ValueError(f"a plane is on {t.device}, the current device is cuda:{dev}")
+        g.base, g.page_bytes, g.n_planes = t.data_ptr(), page, count
+        g.plane_stride = strides[0] * size if count > 1 else 0
     return groups
 
 
@@ -649,23 +691,29 @@ def qsa_fork_pages(page_size, parent, add, table, seq_len, ref, table_out, seq_l
     """New table rows that continue old ones (parent[i], -1: none) with room for add[i] more tokens; full pages
     shared, a shared last page copied in every plane, new pages taken from those with ref 0. planes: a list of
     pool tensors [n_planes, n_pages, ...]."""
+    dev = torch.cuda.current_device()
     n_out, (n_in, ld), n_pages = parent.shape[0], table.shape, ref.shape[0]
-    _check(load().qsa_fork_pages(int(page_size), _ints(parent, (n_out,), "parent"), _ints(add, (n_out,), "add"), n_out,
-                                 _cuda(table, torch.int32, "table"), _ints(seq_len, (n_in,), "seq_len"), n_in, ld,
-                                 _ints(ref, (n_pages,), "ref"), n_pages, _ints(table_out, (n_out, ld), "table_out"),
-                                 _ints(seq_len_out, (n_out,), "seq_len_out"), _ints(ref_out, (n_pages,), "ref_out"),
-                                 _plane_groups(planes, n_pages), len(planes), *_ws_args(ws), _stream(stream)),
-           "qsa_fork_pages")
+    st = load().qsa_fork_pages(page_size, _ints(parent, n_out, "parent", dev), _ints(add, n_out, "add", dev), n_out,
+                               _on(table, _i32, "table", dev), _ints(seq_len, n_in, "seq_len", dev), n_in, ld,
+                               _ints(ref, n_pages, "ref", dev), n_pages, _ints2(table_out, n_out, ld, "table_out", dev),
+                               _ints(seq_len_out, n_out, "seq_len_out", dev), _ints(ref_out, n_pages, "ref_out", dev),
+                               _plane_groups(planes, n_pages, dev), len(planes), _on(ws, _u8, "ws", dev), ws.numel(),
+                               _stream_of(stream, dev))
+    if st:
+        _check(st, "qsa_fork_pages")
 
 
 def qsa_compact_pages(page_size, table, seq_len, ref, table_out, ref_out, planes, ws, stream=None):
     """Move the live pages (ref > 0) to the lowest ids in every plane and rewrite table and ref."""
+    dev = torch.cuda.current_device()
     (n_rows, ld), n_pages = table.shape, ref.shape[0]
-    _check(load().qsa_compact_pages(int(page_size), _cuda(table, torch.int32, "table"),
-                                    _ints(seq_len, (n_rows,), "seq_len"), n_rows, ld, _ints(ref, (n_pages,), "ref"),
-                                    n_pages, _ints(table_out, (n_rows, ld), "table_out"),
-                                    _ints(ref_out, (n_pages,), "ref_out"), _plane_groups(planes, n_pages), len(planes),
-                                    *_ws_args(ws), _stream(stream)), "qsa_compact_pages")
+    st = load().qsa_compact_pages(page_size, _on(table, _i32, "table", dev), _ints(seq_len, n_rows, "seq_len", dev),
+                                  n_rows, ld, _ints(ref, n_pages, "ref", dev), n_pages,
+                                  _ints2(table_out, n_rows, ld, "table_out", dev),
+                                  _ints(ref_out, n_pages, "ref_out", dev), _plane_groups(planes, n_pages, dev),
+                                  len(planes), _on(ws, _u8, "ws", dev), ws.numel(), _stream_of(stream, dev))
+    if st:
+        _check(st, "qsa_compact_pages")
 
 
 def qsa_copy_pages(src, dst, planes, ws, dst_planes=None, stream=None):
@@ -673,13 +721,16 @@ def qsa_copy_pages(src, dst, planes, ws, dst_planes=None, stream=None):
     pairs with a negative id are skipped."""
     if not planes:
         return
+    dev = torch.cuda.current_device()
     n, n_pages = src.shape[0], planes[0].shape[1]
     n_dst = n_pages if dst_planes is None else dst_planes[0].shape[1]
     if dst_planes is not None and len(dst_planes) != len(planes):
         raise ValueError("dst_planes must match planes")
-    _check(load().qsa_copy_pages(_ints(src, (n,), "src"), _ints(dst, (n,), "dst"), n, _plane_groups(planes, n_pages),
-                                 n_pages, None if dst_planes is None else _plane_groups(dst_planes, n_dst), n_dst,
-                                 len(planes), *_ws_args(ws), _stream(stream)), "qsa_copy_pages")
+    _check(load().qsa_copy_pages(_ints(src, n, "src", dev), _ints(dst, n, "dst", dev), n,
+                                 _plane_groups(planes, n_pages, dev), n_pages,
+                                 None if dst_planes is None else _plane_groups(dst_planes, n_dst, dev), n_dst,
+                                 len(planes), _on(ws, _u8, "ws", dev), ws.numel(), _stream_of(stream, dev)),
+           "qsa_copy_pages")
 
 
 def version() -> str:

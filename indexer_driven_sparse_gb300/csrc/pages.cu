@@ -1,11 +1,11 @@
 // Bookkeeping and copying of a paged cache's pages: fork / extend / free (qsa_fork_pages), compaction
 // (qsa_compact_pages) and plain copies (qsa_copy_pages).
 //
-// The whole numbers are settled by one cluster of 8 CTAs (its hardware barrier joins the phases; the counts
-// and lists between them live in the workspace), since every phase needs the one before it over all rows or
-// pages: the lowest free pages are found by counting each CTA's share of ref first and numbering it after.
-// A second kernel, launched as its programmatic dependent, writes the tables and copies the pages with every
-// SM: that part is bound by HBM, the first by the latency of its dependent loads.
+// The whole numbers are settled by one cluster of 8 CTAs: each thread counts the free (or live) pages of its run of
+// ref, one scan numbers the runs inside a CTA, and one cluster barrier makes the CTAs' counts known; meanwhile CTA 0
+// plans the rows of a fork. That kernel is a chain of dependent loads and is bound by their latency: it has one pass
+// before the barrier and one after it. A second kernel, its programmatic dependent, writes the tables and copies
+// the pages with every SM: that part is bound by HBM.
 #include "paged.cuh"
 
 #include <algorithm>
@@ -17,29 +17,28 @@ namespace {
 constexpr int kCluster = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBytes = 16384;      // one CTA's share of a page copy at a time
+constexpr int kMoveBytes = 4096;       // one warp's share of a page copy at a time: eight 16-byte words a lane
+constexpr int kSharedRows = 4096;      // per-parent words kept in shared memory up to this many rows
 
-struct RowCopy {                       // row `row`'s first new page becomes page src's first `used` tokens
-    int32_t src, row, used;
+struct RowCopy {                       // new page fresh[off] becomes page src's first `used` tokens
+    int32_t src, off, used;
 };
 
 // Counts at the front of the scratch area.
 struct PlanHead {
     int32_t per_cta[kCluster];         // free (fork) or live (compact) pages in each CTA's share
-    int32_t extra[kCluster];           // compact: moving pages in each share
-    int32_t holes[kCluster];           // compact: free pages below n_live in each share
-    int32_t n_pairs, n_live, need, pad;
+    int32_t n_pairs, n_live;
 };
 static_assert(sizeof(PlanHead) <= 256, "PlanHead fits its 256 bytes");
 
 // Scratch: head, then arrays of int32 sized by rows and pages.
 struct ForkScratch {
     PlanHead *head;
-    int32_t *first, *children;         // [n_in] lowest child row, rows that continue it
-    int32_t *off;                      // [n_out] first of its new pages in `fresh`, -1: row is empty or failed
+    int32_t *first, *children;         // [n_in] lowest row that continues it, how many do
+    int32_t *off;                      // [n_out] first of its new pages in `fresh`, -1: row failed
     int32_t *keeps;                    // [n_out] keeps the parent's last page
     int32_t *fresh;                    // [n_pages] new pages in the order they are handed out
-    RowCopy *pairs;                   // [n_out]
+    RowCopy *pairs;                    // [n_out]
 };
 
 __host__ __device__ inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -107,114 +106,135 @@ __device__ __forceinline__ RowPlan row_plan(const ForkArgs &a, int i) {
     return p;
 }
 
-// Phases (cluster barriers between them):
-//   1 count free pages per CTA share, copy ref, clear the per-parent words;
-//   2 each row: lowest child of its parent;
-//   3 CTA 0: pages each row needs, scanned over the rows -> off, pairs; rows that find no page fail;
-//   4 every CTA: number its free pages -> fresh; children of each parent.
+// A thread's run of page ids [lo, hi) in its CTA's share.
+struct Run {
+    int lo, hi;
+};
+__device__ __forceinline__ Run run_of_thread(int n_pages) {
+    const int share = (n_pages + kCluster - 1) / kCluster, per = (share + kPlanThreads - 1) / kPlanThreads;
+    const int end = min(n_pages, ((int)blockIdx.x + 1) * share);
+    Run r;
+    r.lo = min(end, (int)blockIdx.x * share + (int)threadIdx.x * per);
+    r.hi = min(end, r.lo + per);
+    return r;
+}
+
+// Before the barrier: every CTA numbers its free pages and copies ref; CTA 0 plans the rows (lowest row that
+// continues each parent, pages each row needs, scanned over the rows). After it: the free pages that are handed out go
+// to `fresh`; CTA 0, now knowing how many there are, strikes out the rows that find none and lists the copies.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     fork_plan_kernel(ForkArgs a, ForkScratch s) {
     __shared__ long long sh[33];
+    __shared__ int first_sh[kSharedRows], children_sh[kSharedRows];
     const int cta = blockIdx.x, tid = threadIdx.x;
-    const int all = kCluster * kPlanThreads, me = cta * kPlanThreads + tid;
     launch_dependents();
-    const int share = (a.n_pages + kCluster - 1) / kCluster;
-    const int lo = min(a.n_pages, cta * share), hi = min(a.n_pages, lo + share);
+    const Run run = run_of_thread(a.n_pages);
     int free_here = 0;
-    for (int p = lo + tid; p < hi; p += kPlanThreads) {
+    for (int p = run.lo; p < run.hi; ++p) {
         const int r = a.ref[p];
         free_here += r == 0;
         a.ref_out[p] = r;
     }
     long long total;
-    block_scan<long long>(free_here, sh, &total);
+    int rank = (int)block_scan<long long>(free_here, sh, &total) - free_here;
     if (tid == 0) s.head->per_cta[cta] = (int)total;
-    for (int p = me; p < a.n_in; p += all) {
-        s.first[p] = INT32_MAX;
-        s.children[p] = 0;
-    }
-    cluster_sync();
-    for (int i = me; i < a.n_out; i += all) {
-        const RowPlan p = row_plan(a, i);
-        if (!p.ok) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
-        if (p.parent >= 0) atomicMin(s.first + p.parent, i);
-    }
-    cluster_sync();
+
+    // CTA 0's rows: first and children live in shared memory, or in the workspace when there are many
+    int *first = a.n_in <= kSharedRows ? first_sh : s.first;
+    int *children = a.n_in <= kSharedRows ? children_sh : s.children;
+    RowPlan plan{};                    // of row tid, the only one of this thread up to kPlanThreads rows
+    long long need = 0;
     if (cta == 0) {
-        long long n_free = 0;
-#pragma unroll
-        for (int c = 0; c < kCluster; ++c) n_free += s.head->per_cta[c];
-        long long carry = 0;           // pages handed out in the low half, copies in the high half
+        for (int p = tid; p < a.n_in; p += kPlanThreads) {
+            first[p] = INT32_MAX;
+            children[p] = 0;
+        }
+        __syncthreads();
+        for (int i = tid; i < a.n_out; i += kPlanThreads) {
+            const RowPlan p = row_plan(a, i);
+            if (i == tid) plan = p;
+            if (!p.ok) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
+            if (p.parent >= 0) atomicMin(first + p.parent, i);
+        }
+        __syncthreads();
         for (int i0 = 0; i0 < a.n_out; i0 += kPlanThreads) {
             const int i = i0 + tid;
             long long mine = 0;
-            RowPlan p{};
-            bool keep = false, copy = false;
-            int last = -1;
             if (i < a.n_out) {
-                p = row_plan(a, i);
+                const RowPlan p = i == tid ? plan : row_plan(a, i);
+                int keep = 0;
                 if (p.used > 0) {
-                    last = a.table[(int64_t)p.parent * a.ld + p.full];
+                    const int last = a.table[(int64_t)p.parent * a.ld + p.full];
                     const bool named = last >= 0 && last < a.n_pages;
                     if (!named) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
-                    keep = s.first[p.parent] == i && named && a.ref[last] == 1;
-                    copy = !keep;
-                    if (!named) last = -1;
+                    keep = named && first[p.parent] == i && a.ref[last] == 1;
                 }
-                mine = p.pages - p.full - (keep ? 1 : 0);
+                s.keeps[i] = keep;
+                mine = p.pages - p.full - keep;
             }
             long long sum;
-            const long long upto = carry + block_scan<long long>(mine, sh, &sum);
-            const bool failed = mine > 0 && upto > n_free;
-            carry += sum;
-            if (failed) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
-            if (i < a.n_out) {
-                s.off[i] = failed ? -1 : (int)(upto - mine);
-                s.keeps[i] = keep;
-                a.seq_len_out[i] = failed ? 0 : p.total;
-            }
-            copy = copy && !failed && last >= 0;
-            // the copies' list: rows in order
-            long long copies;
-            const long long rank = block_scan<long long>(copy, sh, &copies);
-            const int before = i0 == 0 ? 0 : s.head->n_pairs;
-            if (copy) s.pairs[before + (int)rank - 1] = {last, i, p.used};
-            __syncthreads();
-            if (tid == 0) s.head->n_pairs = before + (int)copies;
-            __syncthreads();
-        }
-        if (tid == 0) {
-            s.head->need = (int)min(carry, n_free);
-            if (a.n_out == 0) s.head->n_pairs = 0;
+            const long long upto = need + block_scan<long long>(mine, sh, &sum);
+            if (i < a.n_out) s.off[i] = (int)min(upto - mine, (long long)INT32_MAX);
+            need += sum;
         }
     }
     cluster_sync();
-    for (int i = me; i < a.n_out; i += all)
-        if (s.off[i] >= 0) {
-            const int p = row_plan(a, i).parent;
-            if (p >= 0) atomicAdd(s.children + p, 1);
-        }
-    const int need = s.head->need;
-    int base = 0;
+    long long n_free = 0;
 #pragma unroll
-    for (int c = 0; c < kCluster; ++c) base += c < cta ? s.head->per_cta[c] : 0;
-    for (int p0 = lo; p0 < hi && base < need; p0 += kPlanThreads) {
-        const int p = p0 + tid;
-        const bool is_free = p < hi && a.ref[p] == 0;
-        long long sum;
-        const int rank = base + (int)block_scan<long long>(is_free, sh, &sum) - 1;
-        if (is_free && rank < need) s.fresh[rank] = p;
-        base += (int)sum;
+    for (int c = 0; c < kCluster; ++c) {
+        const int n = s.head->per_cta[c];
+        rank += c < cta ? n : 0;
+        n_free += n;
     }
+    // every free page has a place in the order; pages behind what is handed out are written and not read
+    for (int p = run.lo; p < run.hi; ++p)
+        if (a.ref[p] == 0) s.fresh[rank++] = p;
+    if (cta != 0) return;
+    int n_pairs = 0;
+    for (int i0 = 0; i0 < a.n_out; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        bool copy = false;
+        RowCopy c{};
+        if (i < a.n_out) {
+            const RowPlan p = i == tid ? plan : row_plan(a, i);
+            const int keep = s.keeps[i], off = s.off[i], mine = p.pages - p.full - keep;
+            const bool failed = mine > 0 && (long long)off + mine > n_free;
+            if (failed) {
+                record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
+                s.off[i] = -1;
+            } else if (p.parent >= 0) {
+                atomicAdd(children + p.parent, 1);
+            }
+            a.seq_len_out[i] = failed ? 0 : p.total;
+            if (!failed && p.used > 0 && !keep) {
+                const int last = a.table[(int64_t)p.parent * a.ld + p.full];
+                c = {last, off, p.used};
+                copy = last >= 0 && last < a.n_pages;
+            }
+        }
+        long long copies;
+        const long long at = block_scan<long long>(copy, sh, &copies);
+        if (copy) s.pairs[n_pairs + (int)at - 1] = c;
+        n_pairs += (int)copies;
+    }
+    if (tid == 0) s.head->n_pairs = n_pairs;
+    __syncthreads();
+    if (a.n_in <= kSharedRows)
+        for (int p = tid; p < a.n_in; p += kPlanThreads) {
+            s.first[p] = first[p];
+            s.children[p] = children[p];
+        }
 }
 
 // ---------------------------------------------------------------------------- copies
-// Words of 16 or 4 bytes of one plane's page, [begin, end) bytes, by the CTA's threads.
+// A warp's number with neighbours in different CTAs, so that a little work spreads over the SMs.
+__device__ __forceinline__ int warp_spread() { return (int)(threadIdx.x >> 5) * gridDim.x + blockIdx.x; }
+
+// Words of 16 or 4 bytes of one plane's page, [begin, end) bytes, by one warp.
 template <typename W>
 __device__ __forceinline__ void move_words(const char *src, char *dst, int64_t begin, int64_t end) {
-    constexpr int U = 4;
-    const int64_t step = (int64_t)kMoveThreads * sizeof(W);
-    for (int64_t b = begin + threadIdx.x * (int64_t)sizeof(W); b < end; b += U * step) {
+    constexpr int U = 8, step = 32 * (int)sizeof(W);
+    for (int64_t b = begin + (threadIdx.x & 31) * (int)sizeof(W); b < end; b += U * step) {
         W v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -225,14 +245,20 @@ __device__ __forceinline__ void move_words(const char *src, char *dst, int64_t b
     }
 }
 
-// Every plane's pages of n pairs; pair k by `pair`, which returns the used tokens (0: skip).
+// Every plane's pages of n pairs, a warp for each kMoveBytes; pair k by `pair`, which returns the used tokens
+// (0: skip).
 template <typename Pair>
 __device__ __forceinline__ void move_pages(const PlaneGroups &pg, int n, int page_size, Pair pair) {
+    const int warps = gridDim.x * (kMoveThreads / 32);
     for (int gi = 0; gi < pg.n; ++gi) {
         const PlaneGroup &g = pg.g[gi];
         const int64_t parts = (g.page_bytes + kMoveBytes - 1) / kMoveBytes;
         const int64_t items = parts * g.n_planes * n;
-        for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+        // a CTA's warps take neighbouring parts (2.1 GB of pages: 396 us, spread 417 us); fewer parts than warps are
+        // spread, from the end that has no table rows
+        const int warp = items < warps ? warps - 1 - warp_spread()
+                                       : (int)((blockIdx.x * kMoveThreads + threadIdx.x) >> 5);
+        for (int64_t w = warp; w < items; w += warps) {
             const int64_t part = w % parts, rest = w / parts;
             const int plane = (int)(rest % g.n_planes), k = (int)(rest / g.n_planes);
             int src, dst;
@@ -253,10 +279,10 @@ __device__ __forceinline__ void move_pages(const PlaneGroups &pg, int n, int pag
 }
 
 // The new table's rows (a warp each), the references, then the copies.
-__global__ void __launch_bounds__(kMoveThreads) fork_move_kernel(ForkArgs a, ForkScratch s, PlaneGroups pg) {
+__global__ void __launch_bounds__(kMoveThreads, 4) fork_move_kernel(ForkArgs a, ForkScratch s, PlaneGroups pg) {
     wait_for_primary();
     const int lane = threadIdx.x & 31;
-    const int warp = (blockIdx.x * kMoveThreads + threadIdx.x) >> 5, warps = gridDim.x * (kMoveThreads / 32);
+    const int warps = gridDim.x * (kMoveThreads / 32), warp = warp_spread();
     for (int i = warp; i < a.n_out; i += warps) {
         const RowPlan p = row_plan(a, i);
         const int off = s.off[i];
@@ -276,7 +302,8 @@ __global__ void __launch_bounds__(kMoveThreads) fork_move_kernel(ForkArgs a, For
     }
     // an old row's full pages: its own entry goes, each row that continues it adds one; its last, partly
     // filled page stays only with a row that keeps it
-    for (int p = warp; p < a.n_in; p += warps) {
+    const int skip = a.n_out % warps;              // on from where the new rows ended
+    for (int p = warp >= skip ? warp - skip : warp - skip + warps; p < a.n_in; p += warps) {
         const int len = a.seq_len[p];
         if (len <= 0 || pages_of(len, a.page_size) > a.ld) continue;
         const int full = len / a.page_size, pages = pages_of(len, a.page_size), children = s.children[p];
@@ -294,7 +321,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_move_kernel(ForkArgs a, For
     move_pages(pg, s.head->n_pairs, a.page_size, [&](int k, int &src, int &dst) {
         const RowCopy c = s.pairs[k];
         src = c.src;
-        dst = s.fresh[s.off[c.row]];
+        dst = s.fresh[c.off];
         return c.used;
     });
 }
@@ -302,79 +329,61 @@ __global__ void __launch_bounds__(kMoveThreads) fork_move_kernel(ForkArgs a, For
 // ---------------------------------------------------------------------------- compaction
 struct CompactScratch {
     PlanHead *head;
-    int32_t *to;                       // [n_pages] new id of a live page, -1: free
-    int32_t *movers, *holes;           // [n_pages] ascending
+    int32_t *rank;                     // [n_pages] of a page that moves: its place among them from the last, -1: free
+    int32_t *movers, *holes;           // [n_pages] from the last: mover i goes to hole i
 };
 
-// Phases: 1 count live pages; 2 with n_live known, count the pages that move and the holes; 3 number them;
-// 4 `to` and ref_out where pages move. (ref_out above n_live is cleared by the second kernel.)
+// With L(p) live pages below p and n_live in all, a free page p < n_live is hole number p - L(p), and the page that
+// moves into the last hole is the one with L(p) = n_live - 1: numbered from the last, mover p has place
+// n_live - 1 - L(p). So one pass of live counts gives both lists; M = n_live - L(n_live) pages move, and hole number h
+// has place M - 1 - h, which the second kernel, knowing M, resolves.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     compact_plan_kernel(CompactArgs a, CompactScratch s) {
     __shared__ long long sh[33];
     const int cta = blockIdx.x, tid = threadIdx.x;
     launch_dependents();
-    const int share = (a.n_pages + kCluster - 1) / kCluster;
-    const int lo = min(a.n_pages, cta * share), hi = min(a.n_pages, lo + share);
-    long long total;
+    const Run run = run_of_thread(a.n_pages);
     int live = 0;
-    for (int p = lo + tid; p < hi; p += kPlanThreads) live += a.ref[p] > 0;
-    block_scan<long long>(live, sh, &total);
+    for (int p = run.lo; p < run.hi; ++p) live += a.ref[p] > 0;
+    long long total;
+    int below = (int)block_scan<long long>(live, sh, &total) - live;
     if (tid == 0) s.head->per_cta[cta] = (int)total;
     cluster_sync();
     int n_live = 0;
 #pragma unroll
-    for (int c = 0; c < kCluster; ++c) n_live += s.head->per_cta[c];
-    long long both = 0;                // movers in the high half, holes in the low half
-    for (int p = lo + tid; p < hi; p += kPlanThreads) {
-        const bool is_live = a.ref[p] > 0;
-        both += ((long long)(is_live && p >= n_live) << 32) + (!is_live && p < n_live);
-    }
-    block_scan<long long>(both, sh, &total);
-    if (tid == 0) {
-        s.head->extra[cta] = (int)(total >> 32);
-        s.head->holes[cta] = (int)(total & 0xffffffff);
-    }
-    cluster_sync();
-    long long base = 0;
-    int moving = 0;
-#pragma unroll
     for (int c = 0; c < kCluster; ++c) {
-        moving += s.head->extra[c];
-        if (c < cta) base += ((long long)s.head->extra[c] << 32) + s.head->holes[c];
+        const int n = s.head->per_cta[c];
+        below += c < cta ? n : 0;
+        n_live += n;
     }
-    for (int p0 = lo; p0 < hi; p0 += kPlanThreads) {
-        const int p = p0 + tid;
-        const bool is_live = p < hi && a.ref[p] > 0;
-        const bool mover = is_live && p >= n_live, hole = p < hi && !is_live && p < n_live;
-        const long long upto =
-            base + block_scan<long long>(((long long)mover << 32) + (long long)hole, sh, &total);
-        if (mover) s.movers[(int)(upto >> 32) - 1] = p;
-        if (hole) s.holes[(int)(upto & 0xffffffff) - 1] = p;
-        if (p < hi && !mover) {
-            s.to[p] = is_live ? p : -1;
-            if (is_live) a.ref_out[p] = a.ref[p];
+    for (int p = run.lo; p < run.hi; ++p) {
+        const int r = a.ref[p];
+        if (p == n_live) s.head->n_pairs = n_live - below;
+        if (r > 0) {
+            if (p >= n_live) {
+                s.rank[p] = n_live - 1 - below;
+                s.movers[n_live - 1 - below] = p;
+            } else {
+                s.rank[p] = 0;
+                a.ref_out[p] = r;
+            }
+            ++below;
+        } else {
+            s.rank[p] = -1;
+            if (p < n_live) s.holes[p - below] = p;
         }
-        base += total;
-    }
-    cluster_sync();
-    const int all = kCluster * kPlanThreads, me = cta * kPlanThreads + tid;
-    for (int k = me; k < moving; k += all) {
-        s.to[s.movers[k]] = s.holes[k];
-        a.ref_out[s.holes[k]] = a.ref[s.movers[k]];
     }
     if (cta == 0 && tid == 0) {
-        s.head->n_pairs = moving;
         s.head->n_live = n_live;
+        if (n_live == a.n_pages) s.head->n_pairs = 0;
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(CompactArgs a, CompactScratch s, PlaneGroups pg) {
+__global__ void __launch_bounds__(kMoveThreads, 4) compact_move_kernel(CompactArgs a, CompactScratch s, PlaneGroups pg) {
     wait_for_primary();
     const int lane = threadIdx.x & 31;
-    const int warp = (blockIdx.x * kMoveThreads + threadIdx.x) >> 5, warps = gridDim.x * (kMoveThreads / 32);
-    const int n_live = s.head->n_live;
-    for (int p = n_live + blockIdx.x * kMoveThreads + threadIdx.x; p < a.n_pages; p += gridDim.x * kMoveThreads)
-        a.ref_out[p] = 0;
+    const int warps = gridDim.x * (kMoveThreads / 32), warp = warp_spread();
+    const int n_live = s.head->n_live, moving = s.head->n_pairs;
     for (int i = warp; i < a.n_rows; i += warps) {
         int len = a.seq_len[i];
         if (len < 0 || pages_of(len, a.page_size) > a.ld) {
@@ -386,20 +395,28 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(CompactArgs 
             int e = -1;
             if (j < pages) {
                 e = a.table[(int64_t)i * a.ld + j];
-                e = e >= 0 && e < a.n_pages ? s.to[e] : -1;
-                if (e < 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
+                const int rank = e >= 0 && e < a.n_pages ? s.rank[e] : -1;
+                if (rank < 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
+                e = rank < 0 ? -1 : e < n_live ? e : s.holes[moving - 1 - rank];
             }
             a.table_out[(int64_t)i * a.ld + j] = e;
         }
     }
-    move_pages(pg, s.head->n_pairs, 1, [&](int k, int &src, int &dst) {
+    // references: a page that moves takes its count along, the rest above n_live have none
+    for (int p = blockIdx.x * kMoveThreads + threadIdx.x; p < a.n_pages; p += gridDim.x * kMoveThreads) {
+        if (p < n_live) continue;
+        const int rank = s.rank[p];
+        if (rank >= 0) a.ref_out[s.holes[moving - 1 - rank]] = a.ref[p];
+        a.ref_out[p] = 0;
+    }
+    move_pages(pg, moving, 1, [&](int k, int &src, int &dst) {
         src = s.movers[k];
-        dst = s.holes[k];
+        dst = s.holes[moving - 1 - k];
         return 1;
     });
 }
 
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, 4)
     copy_pages_kernel(const int32_t *src_ids, const int32_t *dst_ids, int n, PlaneGroups pg, int64_t n_src, int64_t n_dst,
                       WsHeader *hdr) {
     move_pages(pg, n, 1, [&](int k, int &src, int &dst) {
@@ -407,7 +424,7 @@ __global__ void __launch_bounds__(kMoveThreads)
         dst = dst_ids[k];
         if (src < 0 || dst < 0) return 0;
         if (src >= n_src || dst >= n_dst) {
-            if (threadIdx.x == 0) record_error(hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, k);
+            if ((threadIdx.x & 31) == 0) record_error(hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, k);
             return 0;
         }
         return 1;
@@ -464,7 +481,7 @@ cudaError_t launch_compact_pages(const CompactArgs &a, const PlaneGroups &p, cud
     CompactScratch s;
     s.head = reinterpret_cast<PlanHead *>(w);
     const size_t pages = up256((size_t)a.n_pages * 4);
-    s.to = reinterpret_cast<int32_t *>(w + 256);
+    s.rank = reinterpret_cast<int32_t *>(w + 256);
     s.movers = reinterpret_cast<int32_t *>(w + 256 + pages);
     s.holes = reinterpret_cast<int32_t *>(w + 256 + 2 * pages);
     compact_plan_kernel<<<kCluster, kPlanThreads, 0, st>>>(a, s);

@@ -5,8 +5,9 @@
 // exact at every position (in fp32 the product of a position of millions and f_i is off by tenths of a
 // radian). Its upper 32 bits, as a signed fraction in [-1/2, 1/2), give sin and cos by sincospif.
 //
-// Both kernels stream: one thread owns 16 dims of a token's head (a "slot": 8 pairs, or 16 dims that pass
-// through) for a run of heads, so the 8 sines and cosines are computed once and used for every head of the run.
+// Both kernels stream: one thread owns 16 dims of a token's head (a "slot": 8 pairs, or 16 dims that pass through)
+// for a run of heads, so the 8 sines and cosines are computed once and used for every head of the run. A slot's two
+// 8-element vectors lie half a region apart, so neighbouring threads read and write neighbouring 16 bytes.
 #include "paged.cuh"
 
 #include <algorithm>
@@ -16,33 +17,35 @@ namespace qsa {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kBatch = 4;          // heads whose loads are in flight together
 
 struct Slot {
     int a, b;       // first dims of the slot's two 8-element vectors
-    int freq;       // first pair, -1: passes through
+    int fa, fb;     // first pairs of the slot's two groups of four, fa = -1: passes through
 };
 
 // The slots of a head: rot/16 turning ones first, then the dims that pass through in order.
 __device__ __forceinline__ Slot slot_of(const RopeArgs &r, int s) {
     Slot t;
-    const int turning = r.rot >> 4;
+    const int turning = r.rot >> 4, half = r.rot >> 1;
     if (s < turning) {
-        t.freq = 8 * s;
-        t.a = r.interleaved ? r.begin + 16 * s : r.begin + 8 * s;
-        t.b = r.interleaved ? t.a + 8 : t.a + (r.rot >> 1);
+        t.a = r.begin + 8 * s;
+        t.b = t.a + half;
+        t.fa = r.interleaved ? 4 * s : 8 * s;
+        t.fb = r.interleaved ? 4 * s + (half >> 1) : 8 * s + 4;
     } else {
-        const int e = 16 * (s - turning);
-        t.freq = -1;
+        const int e = 8 * (s - turning), f = e + ((r.D - r.rot) >> 1);
+        t.fa = t.fb = -1;
         t.a = e < r.begin ? e : e + r.rot;
-        t.b = e + 8 < r.begin ? e + 8 : e + 8 + r.rot;
+        t.b = f < r.begin ? f : f + r.rot;
     }
     return t;
 }
 
-__device__ __forceinline__ void turns(const RopeArgs &r, int freq, int pos, float (&co)[8], float (&si)[8]) {
+__device__ __forceinline__ void turns(const RopeArgs &r, const Slot &t, int pos, float (&co)[8], float (&si)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint64_t turn = (uint64_t)(int64_t)pos * __ldg(r.phase + freq + i);
+        const uint64_t turn = (uint64_t)(int64_t)pos * __ldg(r.phase + (i < 4 ? t.fa + i : t.fb + i - 4));
         const float half_turns = (float)(int32_t)(turn >> 32) * 0x1p-31f;
         sincospif(half_turns, &si[i], &co[i]);
         si[i] *= r.amplitude;
@@ -88,31 +91,45 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Thread (token n, slot s) for heads [h0, h0 + run).
+// Thread (token n, slot s) for heads [h0, h0 + run), kBatch at a time: their loads are issued together, which
+// the compiler cannot do by itself since out may be x.
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, RopeRows a, int run) {
     const int S = r.D >> 4;
     const int64_t t = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
     const int64_t n = t / S;
     if (n >= a.N) return;
     const Slot sl = slot_of(r, (int)(t - n * S));
-    if (sl.freq < 0 && a.x == a.out) return;       // in place: nothing to do
+    if (sl.fa < 0 && a.x == a.out) return;         // in place: nothing to do
     const int h0 = blockIdx.y * run, h1 = min(a.H, h0 + run);
-    const uint16_t *src = a.x + n * a.x_ld + (int64_t)h0 * r.D;
-    uint16_t *dst = a.out + n * a.out_ld + (int64_t)h0 * r.D;
+    const uint16_t *src = a.x + n * a.x_ld;
+    uint16_t *dst = a.out + n * a.out_ld;
+    uint4 va[kBatch], vb[kBatch];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (h + i < h1) {
+                va[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)(h + i) * r.D + sl.a);
+                vb[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)(h + i) * r.D + sl.b);
+            }
+    };
+    load(h0);
     float co[8], si[8];
-    if (sl.freq >= 0) turns(r, sl.freq, a.pos[n], co, si);
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h, src += r.D, dst += r.D) {
-        uint4 va = *reinterpret_cast<const uint4 *>(src + sl.a), vb = *reinterpret_cast<const uint4 *>(src + sl.b);
-        if (sl.freq >= 0) {
-            float x[16];
-            unpack16(va, vb, x);
-            turn16(x, co, si, r.interleaved != 0);
-            va = pack8(x);
-            vb = pack8(x + 8);
+    if (sl.fa >= 0) turns(r, sl, a.pos[n], co, si);
+    for (int h = h0; h < h1; h += kBatch) {
+        if (h > h0) load(h);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (h + i >= h1) break;
+            if (sl.fa >= 0) {
+                float x[16];
+                unpack16(va[i], vb[i], x);
+                turn16(x, co, si, r.interleaved != 0);
+                va[i] = pack8(x);
+                vb[i] = pack8(x + 8);
+            }
+            *reinterpret_cast<uint4 *>(dst + (int64_t)(h + i) * r.D + sl.a) = va[i];
+            *reinterpret_cast<uint4 *>(dst + (int64_t)(h + i) * r.D + sl.b) = vb[i];
         }
-        *reinterpret_cast<uint4 *>(dst + sl.a) = va;
-        *reinterpret_cast<uint4 *>(dst + sl.b) = vb;
     }
 }
 
@@ -167,11 +184,27 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, A
     const int row = a.seq ? a.seq[n] : (int)n;
     if (row < 0) return;                                     // padding
     const int pos = a.pos[n];
-    const Slot sl = slot_of(r, s), straight = {16 * s, 16 * s + 8, -1};
+    const Slot sl = slot_of(r, s), straight = {8 * s, D / 2 + 8 * s, -1, -1};
     // heads of q come first; without queries the list starts at k
     const int total = a.Hq + 2 * a.Hkv;
-    const int h0 = (a.q ? 0 : a.Hq) + blockIdx.y * run, h1 = min(total, h0 + run);
+    const int h0 = (a.q ? 0 : a.Hq) + blockIdx.y * run;
+    int h1 = min(total, h0 + run);
     if (h0 >= h1) return;
+    uint4 va[kBatch], vb[kBatch];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int hi = h + i;
+            if (hi >= h1) break;
+            const bool v = hi >= a.Hq + a.Hkv;
+            const uint16_t *src = hi < a.Hq ? a.q + n * a.q_ld + hi * D
+                                  : v       ? a.v + n * a.v_ld + (hi - a.Hq - a.Hkv) * D
+                                            : a.k + n * a.k_ld + (hi - a.Hq) * D;
+            va[i] = *reinterpret_cast<const uint4 *>(src + (v ? straight.a : sl.a));
+            vb[i] = *reinterpret_cast<const uint4 *>(src + (v ? straight.b : sl.b));
+        }
+    };
+    load(h0);
     int64_t slot = -1;
     if (h1 > a.Hq) {
         bool ok = row < a.n_rows && pos >= 0 && pos / a.page_size < a.ld;
@@ -181,44 +214,45 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, A
             slot = (int64_t)page * a.page_size + pos % a.page_size;
         }
         if (!ok) {
-            slot = -1;
             if (s == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereAppend, (int)n);
+            h1 = min(h1, a.Hq);                               // its K and V are left out
         }
     }
     float co[8], si[8];
-    if (sl.freq >= 0 && h0 < a.Hq + a.Hkv) turns(r, sl.freq, pos, co, si);
-#pragma unroll 2
-    for (int h = h0; h < h1; ++h) {
-        const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-        if (!is_q && slot < 0) break;
-        const int g = h - a.Hq - (is_v ? a.Hkv : 0);          // KV head
-        const Slot at = is_v ? straight : sl;
-        const uint16_t *src = is_q ? a.q + n * a.q_ld + h * D
-                                   : (is_v ? a.v + n * a.v_ld : a.k + n * a.k_ld) + g * D;
-        uint4 va = *reinterpret_cast<const uint4 *>(src + at.a), vb = *reinterpret_cast<const uint4 *>(src + at.b);
-        const bool turned = at.freq >= 0;
-        float x[16];
-        if (turned || F8) unpack16(va, vb, x);
-        if (turned) turn16(x, co, si, r.interleaved != 0);
-        const int64_t kv = (slot * a.Hkv + g) * D;
-        if (F8 && !is_q) {
-            quantise16<S>(x, at, s, (is_v ? a.v_codes : a.k_codes) + kv,
-                          (is_v ? a.v_scales : a.k_scales) + (slot * a.Hkv + g) * (D / 128), D / 128);
-        } else {
-            if (turned) {
-                va = pack8(x);
-                vb = pack8(x + 8);
+    if (sl.fa >= 0 && h0 < min(h1, a.Hq + a.Hkv)) turns(r, sl, pos, co, si);
+    for (int h = h0; h < h1; h += kBatch) {
+        if (h > h0) load(h);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int hi = h + i;
+            if (hi >= h1) break;
+            const bool is_q = hi < a.Hq, is_v = hi >= a.Hq + a.Hkv;
+            const int g = hi - a.Hq - (is_v ? a.Hkv : 0);      // KV head
+            const Slot at = is_v ? straight : sl;
+            const bool turned = at.fa >= 0;
+            float x[16];
+            if (turned || F8) unpack16(va[i], vb[i], x);
+            if (turned) turn16(x, co, si, r.interleaved != 0);
+            const int64_t kv = (slot * a.Hkv + g) * D;
+            if (F8 && !is_q) {
+                quantise16<S>(x, at, s, (is_v ? a.v_codes : a.k_codes) + kv,
+                              (is_v ? a.v_scales : a.k_scales) + (slot * a.Hkv + g) * (D / 128), D / 128);
+            } else {
+                if (turned) {
+                    va[i] = pack8(x);
+                    vb[i] = pack8(x + 8);
+                }
+                uint16_t *dst = is_q ? a.q_out + n * a.q_out_ld + hi * D : (is_v ? a.v_cache : a.k_cache) + kv;
+                *reinterpret_cast<uint4 *>(dst + at.a) = va[i];
+                *reinterpret_cast<uint4 *>(dst + at.b) = vb[i];
             }
-            uint16_t *dst = is_q ? a.q_out + n * a.q_out_ld + h * D : (is_v ? a.v_cache : a.k_cache) + kv;
-            *reinterpret_cast<uint4 *>(dst + at.a) = va;
-            *reinterpret_cast<uint4 *>(dst + at.b) = vb;
         }
     }
 }
 
-// Heads per thread: as long a run as keeps about 150,000 threads (a thousand per SM), since a run shares its sines.
+// Heads per thread: as long a run as keeps the GPU's 152 x 2048 threads, since a run shares its sines.
 int run_of(int64_t threads_per_head, int heads) {
-    const int64_t want = 152 * 1024;
+    const int64_t want = 152 * 2048;
     return (int)std::max<int64_t>(1, std::min<int64_t>(heads, threads_per_head * heads / want));
 }
 

@@ -193,16 +193,31 @@ def test_page_calls_refusals(lib):
 def test_binding_refuses_wrong_tensors(lib):
     import torch
     cpu = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    for bad, error in ((cpu.float(), TypeError), (cpu[:, :4], ValueError), (cpu.transpose(0, 1).contiguous().transpose(0, 1),
+                                                                            ValueError), (cpu.double(), TypeError)):
+        with pytest.raises(error):
+            qb._head_rows(bad, 2, 8, 128, "q", -1)
+    assert qb._head_rows(cpu, 2, 8, 128, "q", -1) == (cpu.data_ptr(), 1024)
+    with pytest.raises(ValueError, match="current device"):
+        qb._head_rows(cpu, 2, 8, 128, "q", 0)
+    i32 = torch.zeros(4, 6, dtype=torch.int32)
     with pytest.raises(TypeError):
-        qb._head_rows(cpu.float(), 2, 8, 128, "q")
+        qb._ints(i32[0].long(), 6, "pos", -1)
     with pytest.raises(ValueError):
-        qb._head_rows(cpu, 2, 4, 128, "q")
+        qb._ints(i32[0], 5, "pos", -1)
+    with pytest.raises(ValueError, match="contiguous"):
+        qb._ints(i32[:, 0], 4, "pos", -1)
+    with pytest.raises(ValueError, match="current device"):
+        qb._on(i32, torch.int32, "table", 0)
     with pytest.raises(ValueError):
-        qb._head_rows(cpu.transpose(0, 1), 8, 2, 128, "q")
+        qb._ints2(i32, 6, 4, "table", -1)
     with pytest.raises(ValueError):
-        qb._plane_groups([torch.zeros(3, 5, 4)], 6)
-    with pytest.raises(ValueError):
-        qb._plane_groups([torch.zeros(5, 3, 4).transpose(0, 1)], 5)
+        qb._cache(cpu, torch.bfloat16, (2, 8, 64), "k_cache", 0)
+    for bad in (torch.zeros(3, 5, 4), torch.zeros(6, 3, 4).transpose(0, 1)):
+        with pytest.raises(ValueError):
+            qb._plane_groups([bad], 6, -1)
+    g = qb._plane_groups([torch.zeros(3, 6, 4, 2, dtype=torch.int16), torch.zeros(4, 6, 5)[1:]], 6, -1)
+    assert [(x.plane_stride, x.page_bytes, x.n_planes) for x in g] == [(96, 16, 3), (120, 20, 3)]
     with pytest.raises(ValueError):
         qb.rope_table(128, scaling="other")
     with pytest.raises(qb.QsaError):
