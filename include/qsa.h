@@ -557,7 +557,7 @@ QSA_API qsa_status qsa_rope_table(const qsa_rope_config *rope, uint64_t *phase, 
  * Negative positions turn backwards (the inverse, and the gradient, of position -p up to amplitude^2).
  *   x, out: rows of n_heads x head_dim contiguous bf16, x_ld / out_ld elements between rows (multiples of 8,
  *   at least n_heads head_dim); 16-byte aligned; out may be x (same ld), else they must not overlap;
- *   phase: the device copy of qsa_rope_table's; pos [N] int32.
+ *   phase: the device copy of qsa_rope_table's, 16-byte aligned; pos [N] int32.
  * No workspace, no device-side errors. N = 0 is a no-op. */
 QSA_API qsa_status qsa_rope(const qsa_rope_config *rope, const uint64_t *phase, float amplitude, const qsa_bf16 *x,
                             int64_t x_ld, const int32_t *pos, int32_t N, int32_t n_heads, qsa_bf16 *out,

@@ -160,7 +160,7 @@ QSA_API qsa_status qsa_rope(const qsa_rope_config *rope, const uint64_t *phase, 
     QSA_TRY(check_rows(call, "out", out, out_ld, width));
     QSA_NEED(call, x != out || x_ld == out_ld, "in place needs out_ld = x_ld");
     QSA_NEED(call, pos != nullptr && (phase != nullptr || rope->rot_dim == 0), "NULL tensor pointer");
-    QSA_NEED(call, aligned(pos, 4) && aligned(phase, 8), "pos must be 4-byte and phase 8-byte aligned");
+    QSA_NEED(call, aligned(pos, 4) && aligned(phase, 16), "pos must be 4-byte and phase 16-byte aligned");
     const RopeRows rows{x, out, x_ld, out_ld, pos, N, n_heads};
     return launched(launch_rope(rope_args(rope, phase, amplitude), rows, static_cast<cudaStream_t>(stream)), call);
 }
@@ -196,6 +196,7 @@ qsa_status rope_append(const char *call, const qsa_paged_config *cfg, const qsa_
     QSA_TRY(check_rows(call, "k", a.k, a.k_ld, kv_width));
     QSA_TRY(check_rows(call, "v", a.v, a.v_ld, kv_width));
     QSA_NEED(call, a.pos && a.table && (phase != nullptr || rope->rot_dim == 0), "NULL tensor pointer");
+    QSA_NEED(call, aligned(phase, 16), "phase must be 16-byte aligned");
     if (fp8) {
         QSA_NEED(call, a.k_codes && a.v_codes && a.k_scales && a.v_scales, "NULL tensor pointer");
         QSA_NEED(call, aligned(a.k_codes, 16) && aligned(a.v_codes, 16) && aligned(a.k_scales, 8) && aligned(a.v_scales, 8),

@@ -3,7 +3,7 @@
 // Pair i of a head at position p turns by the angle p f_i. f_i / (2 pi) modulo 1 is held as a 64-bit binary
 // fraction of a turn, so the angle's fraction of a turn is (p x phase_i) mod 2^64: an integer product that is
 // exact at every position (in fp32 the product of a position of millions and f_i is off by tenths of a
-// radian). Its upper 32 bits, as a signed fraction in [-1/2, 1/2), give sin and cos by sincospif.
+// radian). Its upper 32 bits give sin and cos.
 //
 // Both kernels stream: one thread owns 16 dims of a token's head (a "slot": 8 pairs, or 16 dims that pass through)
 // for a run of heads, so the 8 sines and cosines are computed once and used for every head of the run. A slot's two
@@ -16,7 +16,7 @@ namespace qsa {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kBatch = 4;          // heads whose loads are in flight together
 
 struct Slot {
@@ -42,14 +42,37 @@ __device__ __forceinline__ Slot slot_of(const RopeArgs &r, int s) {
     return t;
 }
 
+// sin and cos of a 32-bit fraction of a turn. The nearest quarter turn comes off in integers, exactly; the rest
+// x, at most pi/4, goes into the Taylor series of both (first omitted terms x^11/11! < 2e-9 and x^10/10! < 3e-8,
+// both below fp32's own rounding of the results near 1).
+__device__ __forceinline__ void sincos_turn(uint32_t turn, float &si, float &co) {
+    const uint32_t quarter = (turn + 0x20000000u) >> 30;
+    const float x = (float)(int32_t)(turn - (quarter << 30)) * 1.46291807926715968e-9f;   // 2 pi / 2^32
+    const float z = x * x;
+    float s = fmaf(z, 2.7557319224e-6f, -1.9841269841e-4f);
+    s = fmaf(s, z, 8.3333333333e-3f);
+    s = fmaf(s, z, -1.6666666667e-1f);
+    s = fmaf(s * z, x, x);
+    float c = fmaf(z, 2.4801587302e-5f, -1.3888888889e-3f);
+    c = fmaf(c, z, 4.1666666667e-2f);
+    c = fmaf(c, z, -0.5f);
+    c = fmaf(c, z, 1.f);
+    const float u = quarter & 1u ? c : s, v = quarter & 1u ? s : c;
+    si = quarter & 2u ? -u : u;                             // quarters: (s, c), (c, -s), (-s, -c), (-c, s)
+    co = (quarter + 1u) & 2u ? -v : v;
+}
+
 __device__ __forceinline__ void turns(const RopeArgs &r, const Slot &t, int pos, float (&co)[8], float (&si)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint64_t turn = (uint64_t)(int64_t)pos * __ldg(r.phase + (i < 4 ? t.fa + i : t.fb + i - 4));
-        const float half_turns = (float)(int32_t)(turn >> 32) * 0x1p-31f;
-        sincospif(half_turns, &si[i], &co[i]);
-        si[i] *= r.amplitude;
-        co[i] *= r.amplitude;
+    for (int i = 0; i < 4; ++i) {
+        const ulonglong2 f = __ldg(reinterpret_cast<const ulonglong2 *>(r.phase + (i < 2 ? t.fa : t.fb - 4) + 2 * i));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint64_t turn = (uint64_t)(int64_t)pos * (j ? f.y : f.x);
+            sincos_turn((uint32_t)(turn >> 32), si[2 * i + j], co[2 * i + j]);
+            si[2 * i + j] *= r.amplitude;
+            co[2 * i + j] *= r.amplitude;
+        }
     }
 }
 
@@ -133,6 +156,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, RopeRows
     }
 }
 
+// x / scale for inv = RN(1 / scale): one correction of the product by the reciprocal. For scale = RN(amax / 448) of any
+// bf16 amax and any bf16 x this is the correctly rounded quotient (all 128 x 128 pairs of significands compared in
+// exact arithmetic; powers of two do not matter in the range quantise16 uses it in); for a turned fp32 x it is
+// at most one unit in the last place off.
+__device__ __forceinline__ float quotient(float x, float scale, float inv) {
+    const float q = x * inv;
+    return fmaf(fmaf(-q, scale, x), inv, q);
+}
+
 // Eight values of one 128-dim group (or of two groups, g0 != g1) quantised as quantize_kv_fp8_kernel does: the
 // group's |max| over the row's S threads (a power of two <= 16 that starts at a multiple of S in the warp).
 template <int S>
@@ -159,8 +191,14 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], const Slot &sl,
         uint32_t w0 = 0u, w1 = 0u;
         if (scale > 0.f) {
             float y[8];
+            if (scale > 0x1p-60f && scale < 0x1p60f) {         // no remainder below the normal range
+                const float inv = __frcp_rn(scale);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[8 * v + i], scale);
+                for (int i = 0; i < 8; ++i) y[i] = quotient(x[8 * v + i], scale, inv);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[8 * v + i], scale);
+            }
             w0 = e4m3x2_of(y[0], y[1]) | (e4m3x2_of(y[2], y[3]) << 16);
             w1 = e4m3x2_of(y[4], y[5]) | (e4m3x2_of(y[6], y[7]) << 16);
         }
@@ -250,9 +288,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, A
     }
 }
 
-// Heads per thread: as long a run as keeps the GPU's 152 x 2048 threads, since a run shares its sines.
+// Heads per thread: as long a run as keeps 1024 threads for each of 152 SMs, since a run shares its sines.
 int run_of(int64_t threads_per_head, int heads) {
-    const int64_t want = 152 * 2048;
+    const int64_t want = 152 * 1024;
     return (int)std::max<int64_t>(1, std::min<int64_t>(heads, threads_per_head * heads / want));
 }
 

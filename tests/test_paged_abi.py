@@ -76,7 +76,7 @@ def test_rope_refusals(lib):
     assert call(n=0) == qb.QSA_OK and call(heads=0) == qb.QSA_OK
     for kw in (dict(cfg=None), dict(n=-1), dict(heads=-1), dict(x=0), dict(x=FAKE + 8), dict(x_ld=504), dict(x_ld=516),
                dict(out=0), dict(out=FAKE + 2), dict(out_ld=256), dict(pos=0), dict(pos=FAKE + 2), dict(phase=0),
-               dict(phase=FAKE + 4), dict(out=FAKE, out_ld=520)):
+               dict(phase=FAKE + 8), dict(out=FAKE, out_ld=520)):
         assert call(**kw) == BAD, kw
     assert call(heads=70000, x_ld=70000 * 128, out_ld=70000 * 128) == UNSUPPORTED
 
@@ -139,7 +139,7 @@ def test_rope_append_refusals(lib):
     assert call(n=0) == qb.QSA_OK
     for kw in (dict(cfg=None), dict(rope=None), dict(rope=rope_cfg(head_dim=256)), dict(n=-1), dict(rows=-1),
                dict(q=FAKE + 8), dict(q_ld=8), dict(q_out=0), dict(q_out=FAKE, q_out_ld=1032), dict(k=0), dict(k_ld=248),
-               dict(v=0), dict(v=FAKE + 2), dict(v_ld=260), dict(pos=0), dict(table=0), dict(phase=0), dict(kc=0),
+               dict(v=0), dict(v=FAKE + 2), dict(v_ld=260), dict(pos=0), dict(table=0), dict(phase=0), dict(phase=FAKE + 8), dict(kc=0),
                dict(vc=0), dict(kc=FAKE + 8), dict(ws=0), dict(ws=FAKE + 128), dict(pages=-1), dict(ld=-1)):
         assert call(**kw) == BAD, kw
     for kw in (dict(ks=0), dict(vs=0), dict(ks=FAKE + 4), dict(kc=FAKE + 8)):
