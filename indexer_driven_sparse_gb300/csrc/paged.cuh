@@ -50,6 +50,7 @@ struct PagedArgs {
     int64_t ld;
     const int32_t *seq_len;
     int32_t B, Hq, Hkv, G, page_size, window;
+    int32_t tile_entries, tile_rest;    // a tile's tokens / page_size and the remainder (set by the launcher)
     float scale_log2;
     uint16_t *out;
     float *lse;

@@ -5,24 +5,24 @@
 // its KV head: 4 G flop per value read, a fiftieth of what the tensor cores do per byte of HBM. So the
 // kernel is a stream of rows, and the work goes into keeping enough of them in flight.
 //
-// Split: the batch's tokens, cut into tiles of 64 of one sequence each, form one list; it is dealt to R ranges of
+// Split: the batch's tokens, cut into tiles of 64 or 128 of one sequence each, form one list; it is dealt to R ranges of
 // equal length (R Hkv CTAs fill the GPU once), so a ragged batch is balanced whatever its lengths. CTA
 // (range, KV head) walks its tiles through a ring of shared-memory stages filled by 16-byte cp.async. A
 // sequence that a range boundary cuts leaves partials (m, l, O), joined by paged_join_kernel; all others are
 // written at once. The two KV heads of a range are neighbouring CTAs, so a token's rows are read together.
 //
 // A tile's products run on mma.sync m16n8k16: M is the G heads padded to 16, which a 128-row tcgen05 tile would
-// fill to an eighth, and its accumulator is a register fragment that becomes the next product's operand
-// without a trip through tensor memory. D / 32 warps: for S = Q K^T a warp takes 64 / warps tokens of the tile
-// and leaves its scores in shared memory; then every warp forms the softmax weights of all 64 tokens in the
-// operand layout of O += P V (16 heads x 64 tokens: 32 exponentials a lane) and multiplies its 32 dims of V. The
-// running maximum and sum are the same in every warp, so nothing is reduced across warps.
+// fill to an eighth. D / 32 warps. For S = Q K^T a warp takes its share of the tile's tokens; the warps exchange their
+// maxima, each turns its own scores into weights P (in shared memory), and for O += P V each takes 32 dims of V and
+// all tokens. Every warp keeps the same running maximum; the sum of the weights stays with the warp that formed
+// them until a segment ends.
 //   bf16 rows: P = P_hi + P_lo, two bf16 values (2^-17 of each weight): one bf16 would add as much error
 //     as the result's own rounding.
 //   FP8 rows: E4M3 codes are exact in f16. Q enters as f16 scaled by a power of two per head (values below 2^-24 of
 //     the head's largest are rounded there: beneath the fp32 sum's own rounding); the K scales multiply the fp32
-//     sums of each 128 dims. V's scales multiply the weights: w = p v_scale, held relative to their running
-//     maximum (so that the largest is 1) and rounded to f16, 2^-11 of each, well under the rows' own 2^-4.
+//     sums of each 128 dims. V's scales enter the weights, w = 2^(s + log2 v_scale - m) with m the running maximum of
+//     that exponent (so that the largest is 1), one set of weights for each 128 dims, rounded to f16: 2^-11 of each,
+//     well under the rows' own 2^-4. The softmax's sum is taken without v_scale, relative to the first set's m.
 #include "paged.cuh"
 #include "qsa_ptx.cuh"
 
@@ -34,27 +34,28 @@ namespace qsa {
 
 namespace {
 
-constexpr int kTile = 64;                // tokens of a tile
-constexpr int kSPitch = 72;              // floats between two heads' scores: float2 accesses touch every bank once
 constexpr int kJoinThreads = 256;
-constexpr int kMaxRanges = 512;
+constexpr int kMaxRanges = 640;
 
 template <int D_, int GT_, bool F8_>
 struct PagedCfg {
     static constexpr int D = D_, GT = GT_;          // GT: head rows kept (8 or 16)
     static constexpr bool F8 = F8_;
     static constexpr int warps = D / 32, threads = warps * 32;
+    static constexpr int tile = F8 && D == 128 ? 128 : 64;        // tokens
     static constexpr int row = D * (F8 ? 1 : 2);    // bytes of a K or V row
     static constexpr int chunks = row / 16;         // 16-byte chunks of a row
     static constexpr int rows_per_copy = 32 / chunks;
-    static constexpr int warp_tok = kTile / warps;  // tokens a warp loads and scores
-    static constexpr int groups = F8 ? D / 128 : 0; // scales of a row
-    static constexpr int k_bytes = kTile * row, s_bytes = kTile * groups * 4, q_bytes = GT * D * 2;
-    static constexpr int stage = 2 * k_bytes + 2 * s_bytes + q_bytes;
-    static constexpr int stages = F8 && D == 256 ? 5 : 3;
-    static constexpr int ctas = D == 256 ? 1 : (F8 || D == 64) ? 3 : 2;   // per SM
-    static constexpr int scores = GT * kSPitch * 4;
-    static constexpr int smem = stages * stage + scores;
+    static constexpr int warp_tok = tile / warps;   // tokens a warp loads and scores
+    static constexpr int groups = F8 ? D / 128 : 1; // scales of a row (FP8), sets of weights
+    static constexpr int k_bytes = tile * row, s_bytes = F8 ? tile * groups * 4 : 0, q_bytes = GT * D * 2;
+    static constexpr int stage = 2 * k_bytes + 2 * s_bytes;
+    static constexpr int stages = F8 && D == 128 ? 2 : F8 && D == 256 && GT == 16 ? 5 : 3;
+    static constexpr int ctas = D == 256 ? (F8 && GT == 8 ? 2 : 1) : D == 128 ? (F8 ? 3 : 2) : (GT == 8 ? 4 : 3);   // per SM
+    static constexpr int p_pitch = tile * 2 + 16;   // bytes between two heads' weights: an odd number of 16-byte chunks
+    static constexpr int p_sets = F8 ? groups : 2;  // FP8: one per V scale; bf16: high and low parts
+    static constexpr int q_at = stages * stage, p_at = q_at + (stages - 1) * q_bytes, x_at = p_at + p_sets * GT * p_pitch;
+    static constexpr int smem = x_at + groups * GT * warps * 4;
 };
 
 // Workspace behind the status block: meta [kMaxRanges] {row, parts}, (m, l) and O of the partials; range r has slot
@@ -65,7 +66,7 @@ struct PagedScratch {
     float *o;       // [2 R][Hq][D]
 };
 
-constexpr int max_ctas(int D) { return D == 256 ? 160 : 480; }
+constexpr int max_ctas(int D) { return D == 256 ? 320 : D == 128 ? 480 : 640; }
 
 __host__ __device__ inline int ranges_for(int ctas, int Hkv) { return ctas / Hkv > 0 ? ctas / Hkv : 1; }
 
@@ -73,32 +74,35 @@ struct Row {
     int len, lo, t0, t1;    // tokens, first attended token, tiles [t0, t1)
 };
 
+template <int T>
 __device__ __forceinline__ Row row_of(const PagedArgs &a, int s) {
     Row r;
     r.len = __ldg(a.seq_len + s);
     if (r.len < 0 || r.len > a.ld * a.page_size) r.len = 0;
     r.lo = a.window > 0 ? max(0, r.len - a.window) : 0;
-    r.t0 = r.lo / kTile;
-    r.t1 = r.len > 0 ? (r.len + kTile - 1) / kTile : r.t0;
+    r.t0 = r.lo / T;
+    r.t1 = r.len > 0 ? r.len / T + (r.len % T != 0) : r.t0;
     return r;
 }
 
 // A place in the tile list: tile t of row s.
+template <int T>
 struct Cursor {
     int s, t;
     Row r;
     __device__ __forceinline__ void at(const PagedArgs &a, int row, int skip) {
         s = row;
-        r = row_of(a, s);
+        r = row_of<T>(a, s);
         t = r.t0 + skip;
     }
-    __device__ __forceinline__ void next(const PagedArgs &a) {   // never called behind the list's last tile
-        if (++t < r.t1) return;
+    __device__ __forceinline__ bool next(const PagedArgs &a) {   // never called behind the list's last tile; true: a new row
+        if (++t < r.t1) return false;
         do {
             ++s;
-            r = row_of(a, s);
+            r = row_of<T>(a, s);
         } while (r.t1 == r.t0);
         t = r.t0;
+        return true;
     }
 };
 
@@ -141,6 +145,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -175,13 +184,19 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
+// dst + index x bytes, index >= 0
+__device__ __forceinline__ const char *row_ptr(const char *base, int index, uint32_t bytes) {
+    return base + (uint64_t)(uint32_t)index * bytes;
+}
+
 template <typename C>
 __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedArgs a, PagedScratch ws, int ranges) {
-    constexpr int D = C::D, GT = C::GT, W = C::warps, TW = C::warp_tok, NS = C::stages;
+    constexpr int D = C::D, GT = C::GT, W = C::warps, T = C::tile, TW = C::warp_tok, NS = C::stages, SG = C::groups;
     constexpr bool F8 = C::F8;
     constexpr int HR = GT / 8;                     // head rows a lane holds: g and g + 8
+    constexpr int NQ = TW / 8;                     // 8-token columns of the warp's scores
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long scan[C::warps + 1];
+    __shared__ long long scan[W + 1];
     __shared__ int start[2];
     __shared__ uint32_t real_tok[NS][W];           // bit i: token i of the warp's share exists
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -194,7 +209,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     const int per = (a.B + C::threads - 1) / C::threads, s_lo = min(a.B, tid * per), s_hi = min(a.B, s_lo + per);
     long long mine = 0;
     for (int s = s_lo; s < s_hi; ++s) {
-        const Row r = row_of(a, s);
+        const Row r = row_of<T>(a, s);
         mine += r.t1 - r.t0;
     }
     long long upto = mine;
@@ -217,7 +232,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
         long long at = upto - mine;
         int s = s_lo;
         for (;; ++s) {
-            const Row r = row_of(a, s);
+            const Row r = row_of<T>(a, s);
             if (x0 < at + r.t1 - r.t0) break;
             at += r.t1 - r.t0;
         }
@@ -226,7 +241,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     }
     // rows without a token: zeros
     for (int s = range; s < a.B; s += ranges) {
-        const Row r = row_of(a, s);
+        const Row r = row_of<T>(a, s);
         if (r.t1 > r.t0) continue;
         const int len = a.seq_len[s];
         if (len != 0 && kvh == 0 && tid == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, s);
@@ -236,81 +251,86 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     }
     __syncthreads();
     const long long n_tiles = x1 - x0;
-    if (kvh == 0 && tid == 0 && range < kMaxRanges) ws.meta[range] = make_int2(-1, 0);
+    if (kvh == 0 && tid == 0) ws.meta[range] = make_int2(-1, 0);
     if (n_tiles == 0) return;
 
     const uint32_t base = smem_u32(smem);
-    float *S = reinterpret_cast<float *>(smem + NS * C::stage);
-    Cursor in, at;                                 // the loads' place, and the products'
+    Cursor<T> in, at;                              // the loads' place, and the products'
     in.at(a, start[0], start[1]);
     at = in;
 
-    // ---- loads: page ids one tile ahead of the copies
-    int page = -1;
-    auto fetch_page = [&]() {
-        const int tok = in.t * kTile + warp * TW + lane;
-        page = -1;
-        if (lane < TW && tok >= in.r.lo && tok < in.r.len) page = __ldg(a.table + in.s * a.ld + tok / a.page_size);
-    };
-    auto issue = [&](int stage, bool first) {      // tile `in`, whose page ids are in `page`
-        const uint32_t st = base + stage * C::stage;
-        const int tok = in.t * kTile + warp * TW + lane;
-        const bool wanted = lane < TW && tok >= in.r.lo && tok < in.r.len;
-        int slot = -1;
-        if (wanted) {
-            if (page >= 0 && page < a.n_pages)
-                slot = page * a.page_size + tok % a.page_size;
-            else if (kvh == 0)
-                record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, in.s);
+    // ---- loads. Lane i < TW keeps token i of the warp's share: its page's place in the table and offset in the page,
+    // stepped by a tile at a time, and the page id, fetched one tile ahead of the copies.
+    const int chunk = lane % C::chunks;
+    const uint32_t row_step = (uint32_t)Hkv * C::row;
+    const char *k_rows = static_cast<const char *>(a.k) + kvh * C::row + chunk * 16;
+    const char *v_rows = static_cast<const char *>(a.v) + kvh * C::row + chunk * 16;
+    int entry, offset, page;
+    bool wanted;
+    auto fetch_page = [&](bool new_row) {
+        const int tok = in.t * T + warp * TW + lane;
+        if (new_row) {
+            entry = tok / a.page_size;
+            offset = tok - entry * a.page_size;
+        } else {
+            entry += a.tile_entries;
+            offset += a.tile_rest;
+            if (offset >= a.page_size) offset -= a.page_size, ++entry;
         }
+        wanted = (TW == 32 || lane < TW) && tok >= in.r.lo && tok < in.r.len;
+        page = wanted ? __ldg(a.table + in.s * a.ld + entry) : -1;
+    };
+    auto issue = [&](int stage, int q_slot, bool first) {      // tile `in`
+        const uint32_t st = base + stage * C::stage;
+        const bool ok = (uint32_t)page < (uint32_t)a.n_pages;
+        if (wanted && !ok && kvh == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, in.s);
+        const int slot = wanted && ok ? page * a.page_size + offset : -1;
         const uint32_t real = __ballot_sync(0xffffffffu, slot >= 0);
         if (lane == 0) real_tok[stage][warp] = real;
-        const char *kp = static_cast<const char *>(a.k), *vp = static_cast<const char *>(a.v);
-        const int chunk = lane % C::chunks;
 #pragma unroll
         for (int i = 0; i < TW / C::rows_per_copy; ++i) {
             const int r = i * C::rows_per_copy + lane / C::chunks;
             const int sl = __shfl_sync(0xffffffffu, slot, r);
             const int t = warp * TW + r;
-            const int64_t from = sl < 0 ? 0 : ((int64_t)sl * Hkv + kvh) * C::row + chunk * 16;
             const uint32_t to = st + t * C::row + ((chunk ^ (t & 7)) << 4);
-            cp_async16_zfill(to, kp + from, sl >= 0);
-            cp_async16_zfill(to + C::k_bytes, vp + from, sl >= 0);
+            cp_async16_zfill(to, row_ptr(k_rows, max(sl, 0), row_step), sl >= 0);
+            cp_async16_zfill(to + C::k_bytes, row_ptr(v_rows, max(sl, 0), row_step), sl >= 0);
         }
-        if (F8 && lane < TW) {
-            constexpr int SB = F8 ? C::groups * 4 : 4;
-            const int64_t from = slot < 0 ? 0 : ((int64_t)slot * Hkv + kvh) * C::groups;
+        if (F8 && (TW == 32 || lane < TW)) {
+            constexpr int SB = SG * 4;
+            const int64_t from = ((int64_t)max(slot, 0) * Hkv + kvh) * SG;
             const uint32_t to = st + 2 * C::k_bytes + (warp * TW + lane) * SB;
             cp_async_small_zfill<SB>(to, a.k_scales + from, slot >= 0);
             cp_async_small_zfill<SB>(to + C::s_bytes, a.v_scales + from, slot >= 0);
         }
         if (first) {                               // the row's queries, heads behind G as zeros
             const uint16_t *q = a.q + in.s * a.q_ld + (int64_t)kvh * G * D;
-            const uint32_t to = st + 2 * C::k_bytes + 2 * C::s_bytes;
+            const uint32_t to = base + C::q_at + q_slot * C::q_bytes;
             for (int i = tid; i < GT * D / 8; i += C::threads) {
                 const int h = i / (D / 8), ch = i % (D / 8);
                 cp_async16_zfill(to + h * D * 2 + ((ch ^ (h & 7)) << 4), q + (h < G ? h * D + ch * 8 : 0), h < G);
             }
         }
     };
+    // Queries wait in NS - 1 slots, one for each row in turn: a tile is issued once every warp has taken the queries
+    // of the tile NS - 1 before it, so no slot in use is overwritten.
     long long issued = 0;
-    int in_stage = 0;
+    int in_stage = 0, in_slot = 0;
     bool in_first = true;
     auto advance = [&]() {                         // issue the next tile (or an empty group) and step on
         if (issued < n_tiles) {
-            issue(in_stage, in_first);
+            issue(in_stage, in_slot, in_first);
             in_stage = in_stage + 1 == NS ? 0 : in_stage + 1;
+            if (in_first) in_slot = in_slot + 1 == NS - 1 ? 0 : in_slot + 1;
             ++issued;
             if (issued < n_tiles) {
-                const int was = in.s;
-                in.next(a);
-                in_first = in.s != was;
-                fetch_page();
+                in_first = in.next(a);
+                fetch_page(in_first);
             }
         }
         cp_async_commit();
     };
-    fetch_page();
+    fetch_page(true);
 #pragma unroll 1
     for (int i = 0; i < NS - 1; ++i) advance();
 
@@ -318,18 +338,20 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     constexpr int KS = D / 16;
     uint32_t qf[KS][2 * HR];                       // Q operand: rows g (and g + 8), two k halves
     float q_scale[HR];                             // logit = score x q_scale (x K scale)
-    float m[HR], l[HR], ref[HR];                   // running maximum, this lane's part of the sum, FP8 weights' reference
+    float m[SG][HR], l[HR];                        // running maxima of the sets; this lane's own weights' sum
     float o[4][4];
+    const int my_set = SG == 2 ? warp / 4 : 0;     // the weights this warp's dims use
+    float *const maxima = reinterpret_cast<float *>(smem + C::x_at);    // [SG][GT][W]
     bool begins = start[1] == 0;                   // the segment starts its sequence
     bool first = true;
-    int stage = 0;
+    int stage = 0, q_slot = 0;
     for (long long i = 0; i < n_tiles; ++i, stage = stage + 1 == NS ? 0 : stage + 1) {
         cp_async_wait<NS - 2>();
         __syncthreads();                           // tile i is in; every warp has left tile i - 1
-        advance();
         const uint32_t st = base + stage * C::stage;
         if (first) {
-            const uint32_t qa = st + 2 * C::k_bytes + 2 * C::s_bytes;
+            const uint32_t qa = base + C::q_at + q_slot * C::q_bytes;
+            q_slot = q_slot + 1 == NS - 1 ? 0 : q_slot + 1;
             if (!F8) {
                 if (GT == 16) {
 #pragma unroll
@@ -383,23 +405,28 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                 }
             }
 #pragma unroll
-            for (int h = 0; h < HR; ++h) m[h] = -INFINITY, l[h] = 0.f, ref[h] = 0.f;
+            for (int h = 0; h < HR; ++h) {
+                l[h] = 0.f;
+#pragma unroll
+                for (int gr = 0; gr < SG; ++gr) m[gr][h] = -INFINITY;
+            }
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[n][k] = 0.f;
             first = false;
         }
-        // S = Q K^T over this warp's tokens
+        // S = Q K^T over this warp's tokens; s[nt]: tokens nt x 8 + 2c, + 1 for head rows g (and g + 8)
+        float s[NQ][2 * HR];
+        float lv[SG][NQ][2];                       // FP8: log2 of the tokens' V scales
         {
-            constexpr int NQ = TW / 8;             // 8-token tiles
-            constexpr int CH = F8 ? C::groups * (NQ == 1 ? 2 : 1) : 4 / NQ;   // independent sums of a tile
+            constexpr int CH = F8 ? (NQ <= 2 ? 2 : 1) : 4 / NQ > 0 ? 4 / NQ : 1;   // independent sums (FP8: of each 128 dims)
             const uint32_t real = real_tok[stage][warp];
 #pragma unroll
             for (int nt = 0; nt < NQ; ++nt) {
-                float acc[CH > 0 ? CH : 1][4];
+                float acc[SG * CH][4];
 #pragma unroll
-                for (int x = 0; x < CH; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
+                for (int x = 0; x < SG * CH; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
                 const uint32_t krow = st + (warp * TW + nt * 8 + (lane & 7)) * C::row;
 #pragma unroll
                 for (int k = 0; k < C::chunks / 4; ++k) {
@@ -418,139 +445,150 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                             const int step = 4 * k + z;
                             const uint32_t qa[4] = {qf[step][0], HR == 2 ? qf[step][2 * HR - 2] : 0u, qf[step][1],
                                                     HR == 2 ? qf[step][2 * HR - 1] : 0u};
-                            constexpr int per_group = CH / (C::groups > 0 ? C::groups : 1);
-                            mma16816<true>(acc[(step / 8) * per_group + (step % 8) % (per_group > 0 ? per_group : 1)], qa,
-                                           e4m3_to_f16x2(b[z], 0), e4m3_to_f16x2(b[z], 1));
+                            mma16816<true>(acc[(step / 8) * CH + step % CH], qa, e4m3_to_f16x2(b[z], 0),
+                                           e4m3_to_f16x2(b[z], 1));
                         }
                     }
                 }
-                float s[4];
                 const int t = nt * 8 + 2 * c;      // this lane's two tokens of the warp's share
-                if (!F8) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        s[x] = acc[0][x];
-#pragma unroll
-                        for (int y = 1; y < CH; ++y) s[x] += acc[y][x];
-                    }
-                } else {
+                float sc[2][SG];                   // K scales of the two tokens
+                if (F8) {
                     const float *ks = reinterpret_cast<const float *>(smem + stage * C::stage + 2 * C::k_bytes) +
-                                      (warp * TW + t) * C::groups;
-                    constexpr int per_group = CH / (C::groups > 0 ? C::groups : 1);
+                                      (warp * TW + t) * SG;
+                    const float *vs = ks + C::s_bytes / 4;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        s[x] = 0.f;
+                    for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int gr = 0; gr < C::groups; ++gr) {
-                            float sum = acc[gr * per_group][x];
-#pragma unroll
-                            for (int y = 1; y < per_group; ++y) sum += acc[gr * per_group + y][x];
-                            s[x] = fmaf(sum, ks[(x & 1) * C::groups + gr], s[x]);
+                        for (int gr = 0; gr < SG; ++gr) {
+                            sc[x][gr] = ks[x * SG + gr];
+                            // a scale below 2^-100 counts as that: its row's values are beneath 2^-91
+                            lv[gr][nt][x] = fmaxf(lg2(vs[x * SG + gr]), -100.f);
                         }
-                    }
                 }
-                const bool r0 = (real >> t) & 1, r1 = (real >> (t + 1)) & 1;
 #pragma unroll
-                for (int h = 0; h < HR; ++h)
-                    *reinterpret_cast<float2 *>(S + (g + 8 * h) * kSPitch + warp * TW + t) =
-                        make_float2(r0 ? s[2 * h] * q_scale[h] : -INFINITY, r1 ? s[2 * h + 1] * q_scale[h] : -INFINITY);
+                for (int x = 0; x < 2 * HR; ++x) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int gr = 0; gr < SG; ++gr) {
+                        float sum = acc[gr * CH][x];
+#pragma unroll
+                        for (int y = 1; y < CH; ++y) sum += acc[gr * CH + y][x];
+                        v = F8 ? fmaf(sum, sc[x & 1][gr], v) : sum;
+                    }
+                    s[nt][x] = (real >> (t + (x & 1))) & 1 ? v * q_scale[x / 2] : -INFINITY;
+                }
             }
         }
-        __syncthreads();
-        // weights of all 64 tokens, in the operand layout
-        float p[HR][16];
-        float alpha[HR];
+        // the tile's maximum of every head: over this warp's tokens, then over the warps
 #pragma unroll
-        for (int h = 0; h < HR; ++h) {
-            const float *srow = S + (g + 8 * h) * kSPitch + 2 * c;
-            float top = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float2 v = *reinterpret_cast<const float2 *>(srow + 8 * k);
-                p[h][2 * k] = v.x, p[h][2 * k + 1] = v.y;
-                top = fmaxf(top, fmaxf(v.x, v.y));
-            }
-            top = fmaxf(m[h], quad_max(top));
-            const float at_top = top == -INFINITY ? 0.f : top;
-            alpha[h] = ex2(m[h] - at_top);
-            m[h] = top;
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                p[h][k] = ex2(p[h][k] - at_top);
-                sum += p[h][k];
-            }
-            l[h] = fmaf(l[h], alpha[h], sum);
-        }
-        if (F8) {
-            // w = p v_scale relative to their running maximum
-            const float *vs = reinterpret_cast<const float *>(smem + stage * C::stage + 2 * C::k_bytes + C::s_bytes) +
-                              (C::groups == 2 ? warp / 4 : 0);
-            constexpr int VG = C::groups > 0 ? C::groups : 1;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float v0 = vs[(8 * k + 2 * c) * VG], v1 = vs[(8 * k + 2 * c + 1) * VG];
-#pragma unroll
-                for (int h = 0; h < HR; ++h) p[h][2 * k] *= v0, p[h][2 * k + 1] *= v1;
-            }
+        for (int gr = 0; gr < SG; ++gr)
 #pragma unroll
             for (int h = 0; h < HR; ++h) {
-                float top = 0.f;
+                float top = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) top = fmaxf(top, p[h][k]);
-                const float old = ref[h] * alpha[h];
-                ref[h] = fmaxf(old, quad_max(top));
-                const float inv = ref[h] > 0.f ? __fdividef(1.f, ref[h]) : 0.f;
-                alpha[h] = old * inv;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) p[h][k] *= inv;
+                for (int nt = 0; nt < NQ; ++nt)
+                    top = fmaxf(top, F8 ? fmaxf(s[nt][2 * h] + lv[gr][nt][0], s[nt][2 * h + 1] + lv[gr][nt][1])
+                                        : fmaxf(s[nt][2 * h], s[nt][2 * h + 1]));
+                top = quad_max(top);
+                if (c == 0) maxima[(gr * GT + g + 8 * h) * W + warp] = top;
             }
-        }
+        __syncthreads();
+        advance();
+        float alpha[HR];                           // of this warp's set
+#pragma unroll
+        for (int gr = 0; gr < SG; ++gr)
+#pragma unroll
+            for (int h = 0; h < HR; ++h) {
+                const float *x = maxima + (gr * GT + g + 8 * h) * W;
+                float top = m[gr][h];
+                if (W == 2) {
+                    const float2 v = *reinterpret_cast<const float2 *>(x);
+                    top = fmaxf(top, fmaxf(v.x, v.y));
+                } else {
+#pragma unroll
+                    for (int w = 0; w < W / 4; ++w) {
+                        const float4 v = reinterpret_cast<const float4 *>(x)[w];
+                        top = fmaxf(top, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+                    }
+                }
+                const float ref = top == -INFINITY ? 0.f : top;
+                const float al = ex2(m[gr][h] - ref);
+                m[gr][h] = top;
+                if (gr == 0) l[h] *= al;
+                if (SG == 1 || gr == my_set) alpha[h] = al;
+                // weights of this warp's tokens
+                unsigned char *p = smem + C::p_at + (g + 8 * h) * C::p_pitch + (warp * TW + 2 * c) * 2;
+#pragma unroll
+                for (int nt = 0; nt < NQ; ++nt) {
+                    const float u = s[nt][2 * h] - ref, v = s[nt][2 * h + 1] - ref;
+                    if (F8) {
+                        if (gr == 0) l[h] += ex2(u) + ex2(v);
+                        *reinterpret_cast<uint32_t *>(p + gr * GT * C::p_pitch + nt * 16) =
+                            f16x2(ex2(u + lv[gr][nt][0]), ex2(v + lv[gr][nt][1]));
+                    } else {
+                        const float e = ex2(u), f = ex2(v);
+                        l[h] += e + f;
+                        const uint32_t w = bf16x2(e, f);
+                        *reinterpret_cast<uint32_t *>(p + nt * 16) = w;
+                        *reinterpret_cast<uint32_t *>(p + GT * C::p_pitch + nt * 16) =
+                            bf16x2(e - __uint_as_float(w << 16), f - __uint_as_float(w & 0xFFFF0000u));
+                    }
+                }
+            }
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             o[n][0] *= alpha[0], o[n][1] *= alpha[0];
             if (HR == 2) o[n][2] *= alpha[HR - 1], o[n][3] *= alpha[HR - 1];
         }
+        __syncthreads();
         // O += P V over this warp's 32 dims
         const uint32_t vt = st + C::k_bytes + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::row;
+        const uint32_t pt = base + C::p_at + (F8 ? my_set * GT * C::p_pitch : 0) +
+                            (GT == 16 ? ((lane & 7) + ((lane >> 3) & 1) * 8) * C::p_pitch + (lane >> 4) * 16
+                                      : (lane & 7) * C::p_pitch + (lane >> 3) * 16);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t hi[4], lo[4];
-            hi[1] = hi[3] = lo[1] = lo[3] = 0u;
+        for (int k0 = 0; k0 < T / 16; k0 += 2) {
+            uint32_t pw[2][2][4];                  // [step][high, low]
 #pragma unroll
-            for (int h = 0; h < HR; ++h)
+            for (int z = 0; z < (F8 ? 1 : 2); ++z) {
+                uint32_t r[4];
+                if (GT == 16) {
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const float u = p[h][4 * k + 2 * z], v = p[h][4 * k + 2 * z + 1];
-                    if (F8) {
-                        hi[2 * z + h] = f16x2(u, v);
-                    } else {
-                        const uint32_t w = bf16x2(u, v);
-                        hi[2 * z + h] = w;
-                        lo[2 * z + h] = bf16x2(u - __uint_as_float(w << 16), v - __uint_as_float(w & 0xFFFF0000u));
+                    for (int k = 0; k < 2; ++k) ldmatrix4(pt + z * GT * C::p_pitch + (k0 + k) * 32, pw[k][z]);
+                } else {
+                    ldmatrix4(pt + z * GT * C::p_pitch + k0 * 32, r);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        pw[k][z][0] = r[2 * k], pw[k][z][2] = r[2 * k + 1];
+                        pw[k][z][1] = pw[k][z][3] = 0u;
                     }
                 }
-            if (!F8) {
+            }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+            for (int k = 0; k < 2; ++k) {
+                if (!F8) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t b[4];
+                        ldmatrix4_trans(vt + 16 * (k0 + k) * C::row + (((4 * warp + 2 * j + (lane >> 4)) ^ (lane & 7)) << 4), b);
+                        mma16816<false>(o[2 * j], pw[k][0], b[0], b[1]);
+                        mma16816<false>(o[2 * j + 1], pw[k][0], b[2], b[3]);
+                        mma16816<false>(o[2 * j], pw[k][1], b[0], b[1]);
+                        mma16816<false>(o[2 * j + 1], pw[k][1], b[2], b[3]);
+                    }
+                } else {
+                    // a 16-bit element of the transposed load is two codes, dims 2n and 2n + 1 of a chunk of 16
                     uint32_t b[4];
-                    ldmatrix4_trans(vt + 16 * k * C::row + (((4 * warp + 2 * j + (lane >> 4)) ^ (lane & 7)) << 4), b);
-                    mma16816<false>(o[2 * j], hi, b[0], b[1]);
-                    mma16816<false>(o[2 * j + 1], hi, b[2], b[3]);
-                    mma16816<false>(o[2 * j], lo, b[0], b[1]);
-                    mma16816<false>(o[2 * j + 1], lo, b[2], b[3]);
+                    ldmatrix4_trans(vt + 16 * (k0 + k) * C::row + (((2 * warp + (lane >> 4)) ^ (lane & 7)) << 4), b);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) b[j] = __byte_perm(b[j], 0, 0x3120);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int odd = 0; odd < 2; ++odd)
+                            mma16816<true>(o[2 * j + odd], pw[k][0], e4m3_to_f16x2(b[2 * j], odd),
+                                           e4m3_to_f16x2(b[2 * j + 1], odd));
                 }
-            } else {
-                // a 16-bit element of the transposed load is two codes, dims 2n and 2n + 1 of a chunk of 16
-                uint32_t b[4];
-                ldmatrix4_trans(vt + 16 * k * C::row + (((2 * warp + (lane >> 4)) ^ (lane & 7)) << 4), b);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = __byte_perm(b[j], 0, 0x3120);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int odd = 0; odd < 2; ++odd)
-                        mma16816<true>(o[2 * j + odd], hi, e4m3_to_f16x2(b[2 * j], odd), e4m3_to_f16x2(b[2 * j + 1], odd));
             }
         }
         // the segment's end
@@ -558,14 +596,30 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
         if (ends || i + 1 == n_tiles) {
             const bool whole = begins && ends;
             const int slot = 2 * range + (begins ? 1 : 0);
+            // the sums of every warp's weights, where the maxima were
+#pragma unroll
+            for (int h = 0; h < HR; ++h) {
+                l[h] = quad_sum(l[h]);
+                if (c == 0) maxima[(g + 8 * h) * W + warp] = l[h];
+            }
+            __syncthreads();
 #pragma unroll
             for (int h = 0; h < HR; ++h) {
                 const int row = g + 8 * h;
-                const float sum = quad_sum(l[h]);
                 if (row >= G) continue;
+                float sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) sum += maxima[row * W + w];
                 const int head = kvh * G + row;
-                float f = F8 ? ref[h] : 1.f;
-                if (whole) f = sum == 0.f ? 0.f : f / sum;
+                // bf16: O / sum, or (m, sum, O) as a partial. FP8: O 2^(m_set - log2 of the softmax's denominator), with
+                // (that logarithm, 1) as the partial's pair: the sets' maxima may lie far apart
+                const float lse2 = sum == 0.f ? -INFINITY : m[0][h] + log2f(sum);
+                float f;
+                if (F8)
+                    f = sum == 0.f ? 0.f : ex2(m[SG == 2 ? 1 : 0][h] - lse2);
+                else
+                    f = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                if (SG == 2 && my_set == 0) f = sum == 0.f ? 0.f : 1.f / sum;
                 float *po = ws.o + ((int64_t)slot * a.Hq + head) * D + warp * 32;
                 uint16_t *out = a.out + ((int64_t)at.s * a.Hq + head) * D + warp * 32;
 #pragma unroll
@@ -587,9 +641,9 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                 }
                 if (warp == 0 && c == 0) {
                     if (!whole)
-                        ws.ml[(int64_t)slot * a.Hq + head] = make_float2(m[h], sum);
+                        ws.ml[(int64_t)slot * a.Hq + head] = F8 ? make_float2(lse2, 1.f) : make_float2(m[0][h], sum);
                     else if (a.lse)
-                        a.lse[(int64_t)at.s * a.Hq + head] = sum == 0.f ? -INFINITY : (m[h] + log2f(sum)) * kLn2;
+                        a.lse[(int64_t)at.s * a.Hq + head] = lse2 * kLn2;
                 }
             }
             if (begins && !ends && kvh == 0 && tid == 0) {
@@ -696,7 +750,10 @@ cudaError_t launch(const PagedArgs &a, cudaStream_t st) {
     }
     const int ranges = ranges_for(ctas, a.Hkv);
     const PagedScratch ws = scratch_of(a.scratch, C::D, a.Hq, a.Hkv);
-    paged_tile_kernel<C><<<ranges * a.Hkv, C::threads, C::smem, st>>>(a, ws, ranges);
+    PagedArgs b = a;
+    b.tile_entries = C::tile / a.page_size;
+    b.tile_rest = C::tile % a.page_size;
+    paged_tile_kernel<C><<<ranges * a.Hkv, C::threads, C::smem, st>>>(b, ws, ranges);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || ranges == 1) return e;      // one range cuts no sequence
     cudaLaunchConfig_t cfg = {};
