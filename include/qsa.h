@@ -648,7 +648,7 @@ QSA_API size_t qsa_pages_workspace_size(int32_t n_rows, int64_t n_pages);
  * the new table that name page p (other holders' references stay). Entries behind a row's last page are -1.
  * parent = row, add = 1 is a decode step's extension; a repeated parent is a fork; parent -1, add 0 frees.
  *   parent, add, seq_len_out [n_out]; seq_len [n_in]; table [n_in][ld], table_out [n_out][ld] (another array);
- *   ref, ref_out [n_pages] (may be the same array); n_in, n_out <= 65536. planes: n_groups <= 8 groups (HOST
+ *   ref, ref_out [n_pages] (another array); n_in, n_out <= 65536. planes: n_groups <= 8 groups (HOST
  *   array; 0 groups: bookkeeping alone).
  * A row that runs out of pages or of the table's ld, or names a parent outside [0, n_in), becomes empty
  * and QSA_ERR_DEVICE_BOUNDS is recorded with its index. */
@@ -660,7 +660,7 @@ QSA_API qsa_status qsa_fork_pages(int32_t page_size, const int32_t *parent, cons
 
 /* Compact a pool: with n_live pages of ref > 0, every live page with id >= n_live moves (in ascending order) into the
  * free ids below n_live (ascending), in every plane; table_out and ref_out name the new places. The contents of
- * pages >= n_live are left as they were. table_out may be table, ref_out may be ref. A table entry inside its row's
+ * pages >= n_live are left as they were. table_out may be table; ref_out is another array than ref. A table entry inside its row's
  * length that names no live page is recorded (QSA_ERR_DEVICE_BOUNDS, the row) and becomes -1. */
 QSA_API qsa_status qsa_compact_pages(int32_t page_size, const int32_t *table, const int32_t *seq_len, int32_t n_rows,
                                      int64_t ld, const int32_t *ref, int64_t n_pages, int32_t *table_out,

@@ -1,4 +1,5 @@
-"""ctypes binding of libqsa.so: argument marshalling only.
+"""Binding of libqsa.so: argument marshalling only, by ctypes, and for the paged-cache calls (which run once per
+layer and token) by the compiled qsa_torch module.
 
 Every function named ``qsa_*`` here calls the C entry point of the same name with
 the device pointers of the torch tensors it is given; all work runs in the
@@ -9,11 +10,12 @@ library is missing, :func:`load` raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import os
 
 import torch
 
-from .build import LIB_PATH
+from .build import LIB_PATH, TORCH_PATH
 
 QSA_OK = 0
 QSA_ERR_INVALID_ARGUMENT = 1
@@ -57,7 +59,6 @@ class qsa_page_planes(C.Structure):
 
 
 ROPE_SCALINGS = ("none", "linear", "ntk", "by_parts")
-MAX_PLANE_GROUPS = 8
 
 
 def make_config(n_q_heads: int, n_kv_heads: int = 2, head_dim: int = 256, idx_dim: int = 128,
@@ -460,67 +461,20 @@ def qsa_sparse_mla_decode(q, kv_rows, rows, n_rows, out, lse, ws, softmax_scale:
 
 
 # ---------------------------------------------------------------------------- paged K/V cache
-# These calls run once per layer and token: their checks are a chain of cheap comparisons, and what is wrong is
-# only worded (by _refuse) once one of them has failed.
-_bf16, _i32, _u8, _f32, _i64 = torch.bfloat16, torch.int32, torch.uint8, torch.float32, torch.int64
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_NATIVE = None
 
 
-def _refuse(t, dtype, name, dev, shape=None, host=False):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != dev and not (host and t.get_device() == -1):
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-
-
-def _on(t, dtype, name, dev):
-    """The address of a contiguous tensor on the current device `dev`."""
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, dtype, name, dev)
-    return t.data_ptr()
-
-
-def _ints(t, n, name, dev):
-    """The address of int32 [n]."""
-    if t.dtype is not _i32 or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
-        _refuse(t, _i32, name, dev, (n,))
-    return t.data_ptr()
-
-
-def _ints2(t, n, m, name, dev):
-    """The address of int32 [n, m]."""
-    if t.dtype is not _i32 or t.get_device() != dev or t.shape != (n, m) or not t.is_contiguous():
-        _refuse(t, _i32, name, dev, (n, m))
-    return t.data_ptr()
-
-
-def _cache(t, dtype, shape, name, dev):
-    """The address of a cache array on the current device or in pinned host memory."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() not in (dev, -1):
-        _refuse(t, dtype, name, dev, shape, host=True)
-    return t.data_ptr()
-
-
-def _head_rows(t, n, heads, dim, name, dev):
-    """(address, elements between rows) of bf16 [n, heads, dim] with contiguous heads, on the current device."""
-    if t.dtype is not _bf16 or t.get_device() != dev or t.shape != (n, heads, dim):
-        if t.dtype is _bf16 and tuple(t.shape) == (n, heads, dim):
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-        _refuse(t, _bf16, name, dev, (n, heads, dim))
-    ld, head, one = t.stride()
-    if one != 1 or (head != dim and heads > 1):
-        raise ValueError(f"the heads of {name} must be contiguous")
-    return t.data_ptr(), ld if n > 1 else heads * dim
-
-
-def _stream_of(stream, dev):
-    return _raw_stream(dev) if stream is None else _stream(stream)
+def _native():
+    """The compiled marshalling of the calls below (built beside libqsa.so)."""
+    global _NATIVE
+    if _NATIVE is None:
+        load()
+        if not os.path.exists(TORCH_PATH):
+            raise RuntimeError(f"{TORCH_PATH} is missing: build it with __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("qsa_torch", TORCH_PATH)
+        _NATIVE = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_NATIVE)
+    return _NATIVE
 
 
 class RopeTable:
@@ -549,12 +503,8 @@ def rope_table(head_dim: int, rot_dim: int | None = None, rot_begin: int = 0, in
 def qsa_rope(rope: RopeTable, x, pos, out, stream=None):
     """out[n, h] = x[n, h] turned to position pos[n]: x, out [N, H, head_dim] bf16 (rows may be strided; out may
     be x), pos [N] int32."""
-    dev, cfg = torch.cuda.current_device(), rope.cfg
-    n, heads, _ = x.shape
-    x_ptr, x_ld = _head_rows(x, n, heads, cfg.head_dim, "x", dev)
-    out_ptr, out_ld = _head_rows(out, n, heads, cfg.head_dim, "out", dev)
-    st = load().qsa_rope(cfg, _on(rope.phase, _i64, "phase", dev), rope.amplitude, x_ptr, x_ld,
-                         _ints(pos, n, "pos", dev), n, heads, out_ptr, out_ld, _stream_of(stream, dev))
+    st = (_NATIVE or _native()).rope(rope.cfg, rope.phase, rope.amplitude, x, pos, out,
+                                     None if stream is None else _stream(stream))
     if st:
         _check(st, "qsa_rope")
 
@@ -588,102 +538,40 @@ def pages_workspace(n_rows: int, n_pages: int, device="cuda", stream=None):
     return _zeroed(n, device, stream)
 
 
-def _append(name, cfg, rope, q, k, v, pos, seq, q_out, planes, n_pages, table, ws, stream, dev):
-    n, D, Hkv = k.shape[0], cfg.head_dim, cfg.n_kv_heads
-    if q is None:
-        q_ptr, q_ld, q_out_ptr, q_out_ld = None, 0, None, 0
-    else:
-        q_ptr, q_ld = _head_rows(q, n, cfg.n_q_heads, D, "q", dev)
-        q_out_ptr, q_out_ld = _head_rows(q_out, n, cfg.n_q_heads, D, "q_out", dev)
-    k_ptr, k_ld = _head_rows(k, n, Hkv, D, "k", dev)
-    v_ptr, v_ld = _head_rows(v, n, Hkv, D, "v", dev)
-    rows, ld = table.shape
-    st = getattr(load(), name)(cfg, rope.cfg, _on(rope.phase, _i64, "phase", dev), rope.amplitude, q_ptr, q_ld, k_ptr,
-                               k_ld, v_ptr, v_ld, None if seq is None else _ints(seq, n, "seq", dev),
-                               _ints(pos, n, "pos", dev), n, q_out_ptr, q_out_ld, *planes, n_pages,
-                               _on(table, _i32, "table", dev), ld, rows, _on(ws, _u8, "ws", dev), ws.numel(),
-                               _stream_of(stream, dev))
-    if st:
-        _check(st, name)
-
-
-def _bf16_planes(cfg, k_cache, v_cache, dev):
-    shape = (k_cache.shape[0], cfg.page_size, cfg.n_kv_heads, cfg.head_dim)
-    return _cache(k_cache, _bf16, shape, "k_cache", dev), _cache(v_cache, _bf16, shape, "v_cache", dev)
-
-
-def _fp8_planes(cfg, kv8, dev):
-    k_codes, k_scales, v_codes, v_scales = kv8
-    shape = (k_codes.shape[0], cfg.page_size, cfg.n_kv_heads, cfg.head_dim)
-    groups = shape[:3] + (cfg.head_dim // 128,)
-    return (_cache(k_codes, _u8, shape, "k_codes", dev), _cache(k_scales, _f32, groups, "k_scales", dev),
-            _cache(v_codes, _u8, shape, "v_codes", dev), _cache(v_scales, _f32, groups, "v_scales", dev))
-
-
 def qsa_rope_append(cfg, rope: RopeTable, q, k, v, pos, seq, q_out, k_cache, v_cache, table, ws, stream=None):
     """New tokens into a paged cache: q [N, Hq, D] turned into q_out (both None: K and V only), k [N, Hkv, D]
     turned and v stored at position pos[n] of row seq[n] (seq None: row n). k_cache, v_cache
     [n_pages, page_size, Hkv, D] bf16; table [rows, max_pages] int32. q, k, v may be slices of one tensor."""
-    dev = torch.cuda.current_device()
-    _append("qsa_rope_append", cfg, rope, q, k, v, pos, seq, q_out, _bf16_planes(cfg, k_cache, v_cache, dev),
-            k_cache.shape[0], table, ws, stream, dev)
+    st = (_NATIVE or _native()).rope_append(cfg, rope.cfg, rope.phase, rope.amplitude, q, k, v, pos, seq, q_out,
+                                            (k_cache, v_cache), table, ws, None if stream is None else _stream(stream))
+    if st:
+        _check(st, "qsa_rope_append")
 
 
 def qsa_rope_append_fp8kv(cfg, rope: RopeTable, q, k, v, pos, seq, q_out, kv8, table, ws, stream=None):
     """qsa_rope_append into FP8 rows: kv8 = (k_codes, k_scales, v_codes, v_scales), codes
     [n_pages, page_size, Hkv, D] uint8 and scales [..., D / 128] fp32."""
-    dev = torch.cuda.current_device()
-    _append("qsa_rope_append_fp8kv", cfg, rope, q, k, v, pos, seq, q_out, _fp8_planes(cfg, kv8, dev),
-            kv8[0].shape[0], table, ws, stream, dev)
-
-
-def _paged(name, cfg, q, planes, n_pages, table, seq_len, out, lse, ws, stream, dev):
-    B, ld = table.shape
-    Hq, D = cfg.n_q_heads, cfg.head_dim
-    q_ptr, q_ld = _head_rows(q, B, Hq, D, "q", dev)
-    if out.dtype is not _bf16 or out.get_device() != dev or out.shape != (B, Hq, D) or not out.is_contiguous():
-        _refuse(out, _bf16, "out", dev, (B, Hq, D))
-    if lse is not None and (lse.dtype is not _f32 or lse.get_device() != dev or lse.shape != (B, Hq)
-                            or not lse.is_contiguous()):
-        _refuse(lse, _f32, "lse", dev, (B, Hq))
-    st = getattr(load(), name)(cfg, q_ptr, q_ld, *planes, n_pages, _on(table, _i32, "table", dev), ld,
-                               _ints(seq_len, B, "seq_len", dev), B, out.data_ptr(),
-                               None if lse is None else lse.data_ptr(), _on(ws, _u8, "ws", dev), ws.numel(),
-                               _stream_of(stream, dev))
+    st = (_NATIVE or _native()).rope_append_fp8kv(cfg, rope.cfg, rope.phase, rope.amplitude, q, k, v, pos, seq, q_out,
+                                                  kv8, table, ws, None if stream is None else _stream(stream))
     if st:
-        _check(st, name)
+        _check(st, "qsa_rope_append_fp8kv")
 
 
 def qsa_paged_decode(cfg, q, k_cache, v_cache, table, seq_len, out, lse, ws, stream=None):
     """Attention of one new token per sequence over its seq_len[s] cached tokens: q [B, Hq, D] (rows may be
     strided), caches [n_pages, page_size, Hkv, D] bf16, table [B, max_pages], out [B, Hq, D], lse [B, Hq] or None."""
-    dev = torch.cuda.current_device()
-    _paged("qsa_paged_decode", cfg, q, _bf16_planes(cfg, k_cache, v_cache, dev), k_cache.shape[0], table, seq_len, out,
-           lse, ws, stream, dev)
+    st = (_NATIVE or _native()).paged_decode(cfg, q, (k_cache, v_cache), table, seq_len, out, lse, ws,
+                                             None if stream is None else _stream(stream))
+    if st:
+        _check(st, "qsa_paged_decode")
 
 
 def qsa_paged_decode_fp8kv(cfg, q, kv8, table, seq_len, out, lse, ws, stream=None):
     """qsa_paged_decode over FP8 rows kv8 = (k_codes, k_scales, v_codes, v_scales)."""
-    dev = torch.cuda.current_device()
-    _paged("qsa_paged_decode_fp8kv", cfg, q, _fp8_planes(cfg, kv8, dev), kv8[0].shape[0], table, seq_len, out, lse, ws,
-           stream, dev)
-
-
-def _plane_groups(planes, n_pages, dev):
-    """The C array of pool tensors: each [n_planes, n_pages, ...] with contiguous planes."""
-    groups = (qsa_page_planes * (len(planes) or 1))()
-    for t, g in zip(planes, groups):
-        count, pages = t.shape[:2]
-        size = t.element_size()
-        strides = t.stride()
-        page = t.numel() // (count * pages or 1) * size
-        if pages != n_pages or not (t.is_contiguous() or t[0].is_contiguous()):
-            raise ValueError(f"planes must be [n_planes, {n_pages}, ...] with contiguous planes, got {list(t.shape)}")
-        if t.get_device() not in (dev, -1):
-            raise ValueError(f"a plane is on {t.device}, the current device is cuda:{dev}")
-        g.base, g.page_bytes, g.n_planes = t.data_ptr(), page, count
-        g.plane_stride = strides[0] * size if count > 1 else 0
-    return groups
+    st = (_NATIVE or _native()).paged_decode_fp8kv(cfg, q, kv8, table, seq_len, out, lse, ws,
+                                                   None if stream is None else _stream(stream))
+    if st:
+        _check(st, "qsa_paged_decode_fp8kv")
 
 
 def qsa_fork_pages(page_size, parent, add, table, seq_len, ref, table_out, seq_len_out, ref_out, planes, ws,
@@ -691,27 +579,16 @@ def qsa_fork_pages(page_size, parent, add, table, seq_len, ref, table_out, seq_l
     """New table rows that continue old ones (parent[i], -1: none) with room for add[i] more tokens; full pages
     shared, a shared last page copied in every plane, new pages taken from those with ref 0. planes: a list of
     pool tensors [n_planes, n_pages, ...]."""
-    dev = torch.cuda.current_device()
-    n_out, (n_in, ld), n_pages = parent.shape[0], table.shape, ref.shape[0]
-    st = load().qsa_fork_pages(page_size, _ints(parent, n_out, "parent", dev), _ints(add, n_out, "add", dev), n_out,
-                               _on(table, _i32, "table", dev), _ints(seq_len, n_in, "seq_len", dev), n_in, ld,
-                               _ints(ref, n_pages, "ref", dev), n_pages, _ints2(table_out, n_out, ld, "table_out", dev),
-                               _ints(seq_len_out, n_out, "seq_len_out", dev), _ints(ref_out, n_pages, "ref_out", dev),
-                               _plane_groups(planes, n_pages, dev), len(planes), _on(ws, _u8, "ws", dev), ws.numel(),
-                               _stream_of(stream, dev))
+    st = (_NATIVE or _native()).fork_pages(page_size, parent, add, table, seq_len, ref, table_out, seq_len_out, ref_out,
+                                           planes, ws, None if stream is None else _stream(stream))
     if st:
         _check(st, "qsa_fork_pages")
 
 
 def qsa_compact_pages(page_size, table, seq_len, ref, table_out, ref_out, planes, ws, stream=None):
     """Move the live pages (ref > 0) to the lowest ids in every plane and rewrite table and ref."""
-    dev = torch.cuda.current_device()
-    (n_rows, ld), n_pages = table.shape, ref.shape[0]
-    st = load().qsa_compact_pages(page_size, _on(table, _i32, "table", dev), _ints(seq_len, n_rows, "seq_len", dev),
-                                  n_rows, ld, _ints(ref, n_pages, "ref", dev), n_pages,
-                                  _ints2(table_out, n_rows, ld, "table_out", dev),
-                                  _ints(ref_out, n_pages, "ref_out", dev), _plane_groups(planes, n_pages, dev),
-                                  len(planes), _on(ws, _u8, "ws", dev), ws.numel(), _stream_of(stream, dev))
+    st = (_NATIVE or _native()).compact_pages(page_size, table, seq_len, ref, table_out, ref_out, planes, ws,
+                                              None if stream is None else _stream(stream))
     if st:
         _check(st, "qsa_compact_pages")
 
@@ -719,18 +596,10 @@ def qsa_compact_pages(page_size, table, seq_len, ref, table_out, ref_out, planes
 def qsa_copy_pages(src, dst, planes, ws, dst_planes=None, stream=None):
     """Page dst[i] becomes page src[i] in every plane (or of dst_planes, which may be pinned host tensors);
     pairs with a negative id are skipped."""
-    if not planes:
-        return
-    dev = torch.cuda.current_device()
-    n, n_pages = src.shape[0], planes[0].shape[1]
-    n_dst = n_pages if dst_planes is None else dst_planes[0].shape[1]
-    if dst_planes is not None and len(dst_planes) != len(planes):
-        raise ValueError("dst_planes must match planes")
-    _check(load().qsa_copy_pages(_ints(src, n, "src", dev), _ints(dst, n, "dst", dev), n,
-                                 _plane_groups(planes, n_pages, dev), n_pages,
-                                 None if dst_planes is None else _plane_groups(dst_planes, n_dst, dev), n_dst,
-                                 len(planes), _on(ws, _u8, "ws", dev), ws.numel(), _stream_of(stream, dev)),
-           "qsa_copy_pages")
+    st = (_NATIVE or _native()).copy_pages(src, dst, planes, ws, dst_planes,
+                                           None if stream is None else _stream(stream))
+    if st:
+        _check(st, "qsa_copy_pages")
 
 
 def version() -> str:

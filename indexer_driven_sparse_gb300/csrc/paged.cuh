@@ -7,6 +7,27 @@ namespace qsa {
 
 constexpr int kWhereAppend = 9, kWherePaged = 10, kWherePages = 11;
 
+// Programmatic dependent launch: a kernel launched by launch_dependent may begin while the kernel before it on the
+// stream ends; it waits for that one's memory before its first access and lets the next one begin. Every kernel here
+// does both at its start, so each still follows all that came before it.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 struct RopeArgs {
     const uint64_t *phase;    // turns per token as a 64-bit fraction, one per pair
     float amplitude;

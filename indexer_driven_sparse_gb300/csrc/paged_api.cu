@@ -355,6 +355,7 @@ QSA_API qsa_status qsa_fork_pages(int32_t page_size, const int32_t *parent, cons
     QSA_NEED(call, n_pages == 0 || (ref && ref_out), "NULL tensor pointer");
     QSA_NEED(call, table == nullptr || table_out != table, "table_out must be another array than table");
     QSA_NEED(call, seq_len == nullptr || seq_len_out != seq_len, "seq_len_out must be another array than seq_len");
+    QSA_NEED(call, ref == nullptr || ref_out != ref, "ref_out must be another array than ref");
     if (n_out == 0 && n_in == 0 && n_pages == 0) return host_ok();
     a.parent = parent, a.add = add, a.table = table, a.seq_len = seq_len, a.ref = ref;
     a.table_out = table_out, a.seq_len_out = seq_len_out, a.ref_out = ref_out;
@@ -378,6 +379,7 @@ QSA_API qsa_status qsa_compact_pages(int32_t page_size, const int32_t *table, co
     if (n_pages == 0 && n_rows == 0) return host_ok();
     QSA_NEED(call, n_rows == 0 || (seq_len && ((table && table_out) || ld == 0)), "NULL tensor pointer");
     QSA_NEED(call, n_pages == 0 || (ref && ref_out), "NULL tensor pointer");
+    QSA_NEED(call, ref == nullptr || ref_out != ref, "ref_out must be another array than ref");
     a.table = table, a.seq_len = seq_len, a.ref = ref, a.table_out = table_out, a.ref_out = ref_out;
     a.n_rows = n_rows, a.page_size = page_size, a.n_pages = (int32_t)n_pages, a.ld = ld;
     a.hdr = static_cast<WsHeader *>(ws);

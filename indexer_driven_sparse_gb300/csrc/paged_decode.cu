@@ -42,7 +42,7 @@ struct PagedCfg {
     static constexpr int D = D_, GT = GT_;          // GT: head rows kept (8 or 16)
     static constexpr bool F8 = F8_;
     static constexpr int warps = D / 32, threads = warps * 32;
-    static constexpr int tile = F8 && D == 128 ? 128 : 64;        // tokens
+    static constexpr int tile = F8 ? 128 : 64;      // tokens
     static constexpr int row = D * (F8 ? 1 : 2);    // bytes of a K or V row
     static constexpr int chunks = row / 16;         // 16-byte chunks of a row
     static constexpr int rows_per_copy = 32 / chunks;
@@ -50,8 +50,8 @@ struct PagedCfg {
     static constexpr int groups = F8 ? D / 128 : 1; // scales of a row (FP8), sets of weights
     static constexpr int k_bytes = tile * row, s_bytes = F8 ? tile * groups * 4 : 0, q_bytes = GT * D * 2;
     static constexpr int stage = 2 * k_bytes + 2 * s_bytes;
-    static constexpr int stages = F8 && D == 128 ? 2 : F8 && D == 256 && GT == 16 ? 5 : 3;
-    static constexpr int ctas = D == 256 ? (F8 && GT == 8 ? 2 : 1) : D == 128 ? (F8 ? 3 : 2) : (GT == 8 ? 4 : 3);   // per SM
+    static constexpr int stages = F8 && D == 128 ? 2 : 3;
+    static constexpr int ctas = D == 256 ? 1 : D == 128 ? (F8 ? 3 : 2) : (GT == 8 ? 4 : 3);   // per SM
     static constexpr int p_pitch = tile * 2 + 16;   // bytes between two heads' weights: an odd number of 16-byte chunks
     static constexpr int p_sets = F8 ? groups : 2;  // FP8: one per V scale; bf16: high and low parts
     static constexpr int q_at = stages * stage, p_at = q_at + (stages - 1) * q_bytes, x_at = p_at + p_sets * GT * p_pitch;
@@ -66,7 +66,7 @@ struct PagedScratch {
     float *o;       // [2 R][Hq][D]
 };
 
-constexpr int max_ctas(int D) { return D == 256 ? 320 : D == 128 ? 480 : 640; }
+constexpr int max_ctas(int D) { return D == 256 ? 160 : D == 128 ? 480 : 640; }
 
 __host__ __device__ inline int ranges_for(int ctas, int Hkv) { return ctas / Hkv > 0 ? ctas / Hkv : 1; }
 
@@ -184,6 +184,54 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
+// Partials in order: the first from range r's slot 2r + 1, the others from the slots 2r of the ranges behind it.
+__device__ __forceinline__ int64_t part_slot(int range, int i) { return i == 0 ? 2 * (int64_t)range + 1 : 2 * ((int64_t)range + i); }
+
+// (m, l, 4 dims of O) joined over the partials first, first + step, ... < n.
+template <int D, int U>
+__device__ __forceinline__ void join_parts(const PagedArgs &a, const PagedScratch &ws, int range, int n, int head, int col,
+                                           int first, int step, float &m, float &l, float4 &x) {
+    m = -INFINITY, l = 0.f;
+    x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = first; i0 < n; i0 += U * step) {
+        float2 ml[U];
+        float4 o[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * step;
+            ml[u] = make_float2(-INFINITY, 0.f);
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < n) {
+                const int64_t slot = part_slot(range, i) * a.Hq + head;
+                ml[u] = __ldcg(ws.ml + slot);
+                o[u] = __ldcg(reinterpret_cast<const float4 *>(ws.o + slot * D + 4 * col));
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+        const float ref = top == -INFINITY ? 0.f : top, old = ex2(m - ref);
+        m = top;
+        l *= old;
+        x.x *= old, x.y *= old, x.z *= old, x.w *= old;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float w = ex2(ml[u].x - ref);
+            l = fmaf(w, ml[u].y, l);
+            x.x = fmaf(w, o[u].x, x.x), x.y = fmaf(w, o[u].y, x.y);
+            x.z = fmaf(w, o[u].z, x.z), x.w = fmaf(w, o[u].w, x.w);
+        }
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void write_joined(const PagedArgs &a, int s, int head, int col, float m, float l, const float4 &x) {
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2 *>(a.out + ((int64_t)s * a.Hq + head) * D + 4 * col) =
+        make_uint2(bf16x2(x.x * f, x.y * f), bf16x2(x.z * f, x.w * f));
+    if (col == 0 && a.lse) a.lse[(int64_t)s * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
 // dst + index x bytes, index >= 0
 __device__ __forceinline__ const char *row_ptr(const char *base, int index, uint32_t bytes) {
     return base + (uint64_t)(uint32_t)index * bytes;
@@ -203,7 +251,8 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     const int g = lane >> 2, c = lane & 3;
     const int range = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv;
     const int Hkv = a.Hkv, G = a.G;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_begin();
+    wait_for_previous();
 
     // ---- this range's tiles: total over the batch, then the row and tile the range starts at
     const int per = (a.B + C::threads - 1) / C::threads, s_lo = min(a.B, tid * per), s_hi = min(a.B, s_lo + per);
@@ -658,61 +707,40 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
 }
 
 // The partials of a sequence that range `blockIdx.x` starts and leaves unfinished, joined for one head:
-// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, in the ranges' order.
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. Thread (row, 4 dims) takes every rows-th partial, its (m, l)
+// and O loaded together and merged with a running maximum; then the rows of threads are merged in order. The time is
+// that of two dependent loads (which partials, the partials).
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedArgs a, PagedScratch ws) {
-    constexpr int cols = D / 4, rows = kJoinThreads / cols;
-    __shared__ float w[kMaxRanges], red[kJoinThreads / 32 + 1], red2[kJoinThreads / 32 + 1];
+    constexpr int cols = D / 4, rows = kJoinThreads / cols, U = D == 256 ? 8 : 4;
     __shared__ float4 acc[kJoinThreads];
-    const int range = blockIdx.x, head = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ float2 pair[rows];
+    const int range = blockIdx.x, head = blockIdx.y, tid = threadIdx.x, col = tid % cols, row = tid / cols;
+    let_next_begin();
+    wait_for_previous();
     const int2 meta = ws.meta[range];
     if (meta.x < 0) return;
-    const int n = meta.y;
-    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * range + 1 : 2 * (range + i)) * a.Hq + head; };
-    float top = -INFINITY;
-    for (int i = tid; i < n; i += kJoinThreads) top = fmaxf(top, ws.ml[slot(i)].x);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) red[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, red[i]);
-    const float M = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    for (int i = tid; i < n; i += kJoinThreads) {
-        const float2 ml = ws.ml[slot(i)];
-        w[i] = exp2f(ml.x - M);
-        sum = fmaf(w[i], ml.y, sum);
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) red2[warp] = sum;
-    __syncthreads();
-    sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) sum += red2[i];
-    const int col = tid % cols;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = tid / cols; i < n; i += rows) {
-        const float4 v = *reinterpret_cast<const float4 *>(ws.o + slot(i) * D + 4 * col);
-        x.x = fmaf(w[i], v.x, x.x), x.y = fmaf(w[i], v.y, x.y);
-        x.z = fmaf(w[i], v.z, x.z), x.w = fmaf(w[i], v.w, x.w);
-    }
+    float m, l;
+    float4 x;
+    join_parts<D, U>(a, ws, range, meta.y, head, col, row, rows, m, l, x);
     acc[tid] = x;
+    if (col == 0) pair[row] = make_float2(m, l);
     __syncthreads();
     if (tid >= cols) return;
+    float top = -INFINITY;
 #pragma unroll
-    for (int i = 1; i < rows; ++i) {
-        const float4 v = acc[tid + i * cols];
-        x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
+    for (int i = 0; i < rows; ++i) top = fmaxf(top, pair[i].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < rows; ++i) {
+        const float w = ex2(pair[i].x - ref);
+        const float4 v = acc[i * cols + tid];
+        sum = fmaf(w, pair[i].y, sum);
+        x.x = fmaf(w, v.x, x.x), x.y = fmaf(w, v.y, x.y), x.z = fmaf(w, v.z, x.z), x.w = fmaf(w, v.w, x.w);
     }
-    const float f = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2 *>(a.out + ((int64_t)meta.x * a.Hq + head) * D + 4 * col) =
-        make_uint2(bf16x2(x.x * f, x.y * f), bf16x2(x.z * f, x.w * f));
-    if (tid == 0 && a.lse)
-        a.lse[(int64_t)meta.x * a.Hq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    write_joined<D>(a, meta.x, head, col, top, sum, x);
 }
 
 // CTAs of one wave on the current device (cached per device; 0 on an error).
@@ -753,19 +781,9 @@ cudaError_t launch(const PagedArgs &a, cudaStream_t st) {
     PagedArgs b = a;
     b.tile_entries = C::tile / a.page_size;
     b.tile_rest = C::tile % a.page_size;
-    paged_tile_kernel<C><<<ranges * a.Hkv, C::threads, C::smem, st>>>(b, ws, ranges);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(paged_tile_kernel<C>, dim3(ranges * a.Hkv), C::threads, C::smem, st, b, ws, ranges);
     if (e != cudaSuccess || ranges == 1) return e;      // one range cuts no sequence
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ranges - 1, a.Hq);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::D>, a, ws);
+    return launch_dependent(paged_join_kernel<C::D>, dim3(ranges - 1, a.Hq), kJoinThreads, 0, st, a, ws);
 }
 
 template <int D, bool F8>

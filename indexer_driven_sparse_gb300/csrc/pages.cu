@@ -4,8 +4,13 @@
 // The whole numbers are settled by one cluster of 8 CTAs: each thread counts the free (or live) pages of its run of
 // ref, one scan numbers the runs inside a CTA, and one cluster barrier makes the CTAs' counts known; meanwhile CTA 0
 // plans the rows of a fork. That kernel is a chain of dependent loads and is bound by their latency: it has one pass
-// before the barrier and one after it. A second kernel, its programmatic dependent, writes the tables and copies
+// before the barrier and one after it. A second kernel, launched as its dependent, writes the tables and copies
 // the pages with every SM: that part is bound by HBM.
+//
+// Pools and tables that one CTA can plan in its shared memory (kSmallPages, kSmallRows, kSmallEntries) take a single
+// kernel instead: every CTA makes the whole plan for itself from L2, so none waits for another, and goes on to its
+// share of the tables and copies. Two kernels against one, a call: 9.0 against 6.1 us for a fork of 8 rows, 6.5 against 4.3 us for a
+// small compaction; above the limits the repeated plan would cost more than the second launch.
 #include "paged.cuh"
 
 #include <algorithm>
@@ -17,8 +22,12 @@ namespace {
 constexpr int kCluster = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBytes = 4096;       // one warp's share of a page copy at a time: eight 16-byte words a lane
+constexpr int kMoveBytes = 4096;       // one warp's share of a page copy at a time: eight 16-byte words a lane, in two goes
 constexpr int kSharedRows = 4096;      // per-parent words kept in shared memory up to this many rows
+constexpr int kSmallThreads = 512;
+constexpr int kSmallPages = 16384;     // page ids in 16 bits, at most 64 KB of shared memory
+constexpr int kSmallRows = 1024;
+constexpr int64_t kSmallEntries = 65536;   // table entries whose references one CTA counts
 
 struct RowCopy {                       // new page fresh[off] becomes page src's first `used` tokens
     int32_t src, off, used;
@@ -46,8 +55,6 @@ __host__ __device__ inline size_t up256(size_t n) { return (n + 255) / 256 * 256
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Inclusive sum over the CTA's threads; *total gets the whole. `sh` holds 33 words.
 template <typename T>
@@ -127,7 +134,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     __shared__ long long sh[33];
     __shared__ int first_sh[kSharedRows], children_sh[kSharedRows];
     const int cta = blockIdx.x, tid = threadIdx.x;
-    launch_dependents();
+    let_next_begin();
+    wait_for_previous();
     const Run run = run_of_thread(a.n_pages);
     int free_here = 0;
     for (int p = run.lo; p < run.hi; ++p) {
@@ -233,7 +241,7 @@ __device__ __forceinline__ int warp_spread() { return (int)(threadIdx.x >> 5) * 
 // Words of 16 or 4 bytes of one plane's page, [begin, end) bytes, by one warp.
 template <typename W>
 __device__ __forceinline__ void move_words(const char *src, char *dst, int64_t begin, int64_t end) {
-    constexpr int U = 8, step = 32 * (int)sizeof(W);
+    constexpr int U = 4, step = 32 * (int)sizeof(W);
     for (int64_t b = begin + (threadIdx.x & 31) * (int)sizeof(W); b < end; b += U * step) {
         W v[U];
 #pragma unroll
@@ -247,9 +255,9 @@ __device__ __forceinline__ void move_words(const char *src, char *dst, int64_t b
 
 // Every plane's pages of n pairs, a warp for each kMoveBytes; pair k by `pair`, which returns the used tokens
 // (0: skip).
-template <typename Pair>
+template <int Threads, typename Pair>
 __device__ __forceinline__ void move_pages(const PlaneGroups &pg, int n, int page_size, Pair pair) {
-    const int warps = gridDim.x * (kMoveThreads / 32);
+    const int warps = gridDim.x * (Threads / 32);
     for (int gi = 0; gi < pg.n; ++gi) {
         const PlaneGroup &g = pg.g[gi];
         const int64_t parts = (g.page_bytes + kMoveBytes - 1) / kMoveBytes;
@@ -257,9 +265,11 @@ __device__ __forceinline__ void move_pages(const PlaneGroups &pg, int n, int pag
         // a CTA's warps take neighbouring parts (2.1 GB of pages: 396 us, spread 417 us); fewer parts than warps are
         // spread, from the end that has no table rows
         const int warp = items < warps ? warps - 1 - warp_spread()
-                                       : (int)((blockIdx.x * kMoveThreads + threadIdx.x) >> 5);
+                                       : (int)((blockIdx.x * Threads + threadIdx.x) >> 5);
         for (int64_t w = warp; w < items; w += warps) {
-            const int64_t part = w % parts, rest = w / parts;
+            // the part is turned by the page: a warp that met the same part of every page would copy all of the partly
+            // filled ones (low parts) or none
+            const int64_t rest = w / parts, part = (w - rest * parts + rest % 13) % parts;
             const int plane = (int)(rest % g.n_planes), k = (int)(rest / g.n_planes);
             int src, dst;
             const int used = pair(k, src, dst);
@@ -280,7 +290,8 @@ __device__ __forceinline__ void move_pages(const PlaneGroups &pg, int n, int pag
 
 // The new table's rows (a warp each), the references, then the copies.
 __global__ void __launch_bounds__(kMoveThreads, 4) fork_move_kernel(ForkArgs a, ForkScratch s, PlaneGroups pg) {
-    wait_for_primary();
+    let_next_begin();
+    wait_for_previous();
     const int lane = threadIdx.x & 31;
     const int warps = gridDim.x * (kMoveThreads / 32), warp = warp_spread();
     for (int i = warp; i < a.n_out; i += warps) {
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) fork_move_kernel(ForkArgs a, 
                 atomicAdd(a.ref_out + e, delta);
         }
     }
-    move_pages(pg, s.head->n_pairs, a.page_size, [&](int k, int &src, int &dst) {
+    move_pages<kMoveThreads>(pg, s.head->n_pairs, a.page_size, [&](int k, int &src, int &dst) {
         const RowCopy c = s.pairs[k];
         src = c.src;
         dst = s.fresh[c.off];
@@ -341,7 +352,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     compact_plan_kernel(CompactArgs a, CompactScratch s) {
     __shared__ long long sh[33];
     const int cta = blockIdx.x, tid = threadIdx.x;
-    launch_dependents();
+    let_next_begin();
+    wait_for_previous();
     const Run run = run_of_thread(a.n_pages);
     int live = 0;
     for (int p = run.lo; p < run.hi; ++p) live += a.ref[p] > 0;
@@ -380,7 +392,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
 }
 
 __global__ void __launch_bounds__(kMoveThreads, 4) compact_move_kernel(CompactArgs a, CompactScratch s, PlaneGroups pg) {
-    wait_for_primary();
+    let_next_begin();
+    wait_for_previous();
     const int lane = threadIdx.x & 31;
     const int warps = gridDim.x * (kMoveThreads / 32), warp = warp_spread();
     const int n_live = s.head->n_live, moving = s.head->n_pairs;
@@ -409,7 +422,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) compact_move_kernel(CompactAr
         if (rank >= 0) a.ref_out[s.holes[moving - 1 - rank]] = a.ref[p];
         a.ref_out[p] = 0;
     }
-    move_pages(pg, moving, 1, [&](int k, int &src, int &dst) {
+    move_pages<kMoveThreads>(pg, moving, 1, [&](int k, int &src, int &dst) {
         src = s.movers[k];
         dst = s.holes[moving - 1 - k];
         return 1;
@@ -419,7 +432,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) compact_move_kernel(CompactAr
 __global__ void __launch_bounds__(kMoveThreads, 4)
     copy_pages_kernel(const int32_t *src_ids, const int32_t *dst_ids, int n, PlaneGroups pg, int64_t n_src, int64_t n_dst,
                       WsHeader *hdr) {
-    move_pages(pg, n, 1, [&](int k, int &src, int &dst) {
+    let_next_begin();
+    wait_for_previous();
+    move_pages<kMoveThreads>(pg, n, 1, [&](int k, int &src, int &dst) {
         src = src_ids[k];
         dst = dst_ids[k];
         if (src < 0 || dst < 0) return 0;
@@ -431,22 +446,261 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
     });
 }
 
+// ---------------------------------------------------------------------------- small pools: one kernel
+// Shared memory of a CTA's plan.
+struct SmallFork {
+    int *len, *last, *first, *children;    // [n_in] tokens, last partly filled page (kAlone: nothing else names it; -1: none), ...
+    int *parent, *total, *off;             // [n_out] parent -1: starts empty; off kKeeps: keeps the parent's last page; -1: failed
+    uint16_t *pairs;                       // [n_out] rows that copy a page
+    uint16_t *fresh;                       // [n_pages] free pages in order
+};
+constexpr int kAlone = 1 << 30, kKeeps = 1 << 30;
+
+static_assert(kSmallPages <= 32 * kSmallThreads, "a thread's run of pages fits a word");
+
+// Bit i: test(ref[lo + i]), for a run of at most 32 pages, eight loads at a time.
+template <typename Test>
+__device__ __forceinline__ uint32_t run_mask(const int32_t *ref, int lo, int hi, Test test) {
+    uint32_t m = 0;
+    for (int p0 = lo; p0 < hi; p0 += 8) {
+        int r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (p0 + i < hi) r[i] = ref[p0 + i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (p0 + i < hi && test(r[i])) m |= 1u << (p0 + i - lo);
+    }
+    return m;
+}
+
+size_t small_fork_bytes(int n_in, int n_out, int n_pages) {
+    return (size_t)n_in * 16 + (size_t)n_out * 12 + ((size_t)n_out + n_pages + 8) * 2;
+}
+size_t small_compact_bytes(int n_pages) { return ((size_t)n_pages * 2 + 8) * 2; }
+constexpr int kSmallSmem = 2 * kSmallRows * 16 + kSmallPages * 4;    // 96 KB: above both sums at their limits
+
+// CTA 0 also writes the references: ref and the entries that rows give up or take.
+__global__ void __launch_bounds__(kSmallThreads, 2) fork_small_kernel(ForkArgs a, PlaneGroups pg) {
+    extern __shared__ __align__(16) int small_smem[];
+    __shared__ int sh[33];
+    __shared__ long long sh64[33];
+    let_next_begin();
+    wait_for_previous();
+    const int tid = threadIdx.x, lane = tid & 31;
+    SmallFork s;
+    s.len = small_smem;
+    s.last = s.len + a.n_in;
+    s.first = s.last + a.n_in;
+    s.children = s.first + a.n_in;
+    s.parent = s.children + a.n_in;
+    s.total = s.parent + a.n_out;
+    s.off = s.total + a.n_out;
+    s.pairs = reinterpret_cast<uint16_t *>(s.off + a.n_out);
+    s.fresh = s.pairs + a.n_out;
+    const int per = (a.n_pages + kSmallThreads - 1) / kSmallThreads;
+    const int lo = min(a.n_pages, tid * per), hi = min(a.n_pages, lo + per);
+    const uint32_t is_free = run_mask(a.ref, lo, hi, [](int r) { return r == 0; });
+    const int free_here = __popc(is_free);
+    if (blockIdx.x == 0)
+        for (int p = tid; p < a.n_pages; p += kSmallThreads) a.ref_out[p] = a.ref[p];
+    for (int p = tid; p < a.n_in; p += kSmallThreads) {
+        const int len = a.seq_len[p];
+        int last = -1;
+        if (len > 0 && pages_of(len, a.page_size) <= a.ld && len % a.page_size != 0) {
+            last = a.table[(int64_t)p * a.ld + len / a.page_size];
+            if (last >= 0 && last < a.n_pages)
+                last |= a.ref[last] == 1 ? kAlone : 0;
+            else
+                last = -1;
+        }
+        s.len[p] = len;
+        s.last[p] = last;
+        s.first[p] = INT32_MAX;
+        s.children[p] = 0;
+    }
+    for (int i = tid; i < a.n_out; i += kSmallThreads) {
+        s.parent[i] = a.parent[i];
+        s.total[i] = a.add[i];
+    }
+    int n_free;
+    int rank = block_scan<int>(free_here, sh, &n_free) - free_here;
+    for (uint32_t left = is_free; left != 0; left &= left - 1) s.fresh[rank++] = (uint16_t)(lo + __ffs(left) - 1);
+    for (int i = tid; i < a.n_out; i += kSmallThreads) {
+        const int parent = s.parent[i], add = s.total[i];
+        bool ok = parent >= -1 && parent < a.n_in && add >= 0;
+        const int base = ok && parent >= 0 ? s.len[parent] : 0;
+        const int64_t total = (int64_t)base + add;
+        ok = ok && base >= 0 && pages_of(base, a.page_size) <= a.ld && total <= INT32_MAX &&
+             pages_of((int)total, a.page_size) <= a.ld;
+        if (!ok && blockIdx.x == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
+        s.parent[i] = ok ? parent : -1;
+        s.total[i] = ok ? (int)total : 0;
+        if (ok && parent >= 0) atomicMin(s.first + parent, i);
+    }
+    __syncthreads();
+    long long handed = 0;
+    int n_pairs = 0;
+    for (int i0 = 0; i0 < a.n_out; i0 += kSmallThreads) {
+        const int i = i0 + tid;
+        int mine = 0, keep = 0;
+        bool copies = false;
+        if (i < a.n_out) {
+            const int parent = s.parent[i], base = parent >= 0 ? s.len[parent] : 0;
+            if (base % a.page_size != 0) {
+                const int last = s.last[parent];
+                if (last < 0 && blockIdx.x == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
+                keep = last >= 0 && (last & kAlone) != 0 && s.first[parent] == i;
+                copies = last >= 0 && !keep;
+            }
+            mine = pages_of(s.total[i], a.page_size) - base / a.page_size - keep;
+        }
+        // n_out <= kSmallRows rows of at most 2^31 tokens: their pages may pass 2^31
+        long long sum;
+        const long long upto = handed + block_scan<long long>(mine, sh64, &sum);
+        handed += sum;
+        const bool failed = mine > 0 && upto > n_free;
+        if (i < a.n_out) {
+            if (failed) {
+                if (blockIdx.x == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
+                s.off[i] = -1;
+            } else {
+                s.off[i] = (mine > 0 ? (int)(upto - mine) : 0) | (keep ? kKeeps : 0);
+                if (s.parent[i] >= 0) atomicAdd(s.children + s.parent[i], 1);
+            }
+            if (blockIdx.x == gridDim.x - 1) a.seq_len_out[i] = failed ? 0 : s.total[i];
+        }
+        copies = copies && !failed;
+        int count;
+        const int at = block_scan<int>(copies, sh, &count);
+        if (copies) s.pairs[n_pairs + at - 1] = (uint16_t)i;
+        n_pairs += count;
+    }
+    __syncthreads();
+    const int warps = gridDim.x * (kSmallThreads / 32), warp = warp_spread();
+    if (blockIdx.x == 0) {
+        // every table entry by one thread: the loads of a row do not wait for another row's
+        const int ld = (int)a.ld, entries = a.n_in * ld;
+#pragma unroll 4
+        for (int x = tid; x < entries; x += kSmallThreads) {
+            const int p = x / ld, j = x - p * ld, len = s.len[p];
+            if (len <= 0 || pages_of(len, a.page_size) > ld || j >= pages_of(len, a.page_size)) continue;
+            const int first = s.first[p];
+            const int kept = first < a.n_out && s.off[first] >= 0 && (s.off[first] & kKeeps) != 0;
+            const int e = a.table[x], delta = (j < len / a.page_size ? s.children[p] : kept) - 1;
+            if (e < 0 || e >= a.n_pages)
+                record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, p);
+            else if (delta != 0)
+                atomicAdd(a.ref_out + e, delta);
+        }
+        for (int i = tid; i < a.n_out; i += kSmallThreads) {
+            const int off = s.off[i];
+            if (off < 0) continue;
+            const int base = s.parent[i] >= 0 ? s.len[s.parent[i]] : 0;
+            const int mine = pages_of(s.total[i], a.page_size) - base / a.page_size - (off & kKeeps ? 1 : 0);
+            for (int j = 0; j < mine; ++j) atomicAdd(a.ref_out + s.fresh[(off & ~kKeeps) + j], 1);
+        }
+    }
+    for (int i = warp; i < a.n_out; i += warps) {
+        const int off = s.off[i], parent = s.parent[i], base = parent >= 0 ? s.len[parent] : 0;
+        const int kept = off < 0 ? 0 : base / a.page_size + (off & kKeeps ? 1 : 0);
+        const int pages = off < 0 ? 0 : pages_of(s.total[i], a.page_size);
+        const int32_t *from = a.table + (int64_t)max(parent, 0) * a.ld;
+        for (int64_t j = lane; j < a.ld; j += 32)
+            a.table_out[(int64_t)i * a.ld + j] = j < kept ? from[j] : j < pages ? s.fresh[(off & ~kKeeps) + (int)j - kept] : -1;
+    }
+    move_pages<kSmallThreads>(pg, n_pairs, a.page_size, [&](int k, int &src, int &dst) {
+        const int i = s.pairs[k], parent = s.parent[i];
+        src = s.last[parent] & ~kAlone;
+        dst = s.fresh[s.off[i]];                   // a row that copies keeps nothing: no flag
+        return s.len[parent] % a.page_size;
+    });
+}
+
+__global__ void __launch_bounds__(kSmallThreads, 2) compact_small_kernel(CompactArgs a, PlaneGroups pg) {
+    extern __shared__ __align__(16) int small_smem[];
+    __shared__ int sh[33];
+    __shared__ int moving_sh;
+    let_next_begin();
+    wait_for_previous();
+    const int tid = threadIdx.x, lane = tid & 31;
+    // [n_pages] a live page's new id, or a moving page's place from the last; [n_pages / 2] each
+    uint16_t *const map = reinterpret_cast<uint16_t *>(small_smem), *const movers = map + a.n_pages,
+                   *const holes = movers + (a.n_pages + 1) / 2;
+    constexpr uint16_t kFree = 0xFFFF;
+    const int per = (a.n_pages + kSmallThreads - 1) / kSmallThreads;
+    const int lo = min(a.n_pages, tid * per), hi = min(a.n_pages, lo + per);
+    const uint32_t is_live = run_mask(a.ref, lo, hi, [](int r) { return r > 0; });
+    int n_live;
+    int below = block_scan<int>(__popc(is_live), sh, &n_live) - __popc(is_live);
+    if (tid == 0 && n_live == a.n_pages) moving_sh = 0;
+    for (int p = lo; p < hi; ++p) {
+        if (p == n_live) moving_sh = n_live - below;
+        if ((is_live >> (p - lo)) & 1) {
+            map[p] = (uint16_t)(p < n_live ? p : n_live - 1 - below);
+            if (p >= n_live) movers[n_live - 1 - below] = (uint16_t)p;
+            ++below;
+        } else {
+            map[p] = kFree;
+            if (p < n_live) holes[p - below] = (uint16_t)p;
+        }
+    }
+    __syncthreads();
+    const int moving = moving_sh;
+    const int warps = gridDim.x * (kSmallThreads / 32), warp = warp_spread();
+    for (int i = warp; i < a.n_rows; i += warps) {
+        int len = a.seq_len[i];
+        if (len < 0 || pages_of(len, a.page_size) > a.ld) {
+            if (lane == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
+            len = 0;
+        }
+        const int pages = pages_of(len, a.page_size);
+        for (int64_t j = lane; j < a.ld; j += 32) {
+            int e = -1;
+            if (j < pages) {
+                const int old = a.table[(int64_t)i * a.ld + j];
+                const int to = old >= 0 && old < a.n_pages ? map[old] : kFree;
+                if (to == kFree)
+                    record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
+                else
+                    e = old < n_live ? to : holes[moving - 1 - to];
+            }
+            a.table_out[(int64_t)i * a.ld + j] = e;
+        }
+    }
+    for (int p = blockIdx.x * kSmallThreads + tid; p < a.n_pages; p += gridDim.x * kSmallThreads) {
+        if (p >= n_live) {
+            const int to = map[p];
+            if (to != kFree) a.ref_out[holes[moving - 1 - to]] = a.ref[p];
+            a.ref_out[p] = 0;
+        } else if (map[p] != kFree) {
+            a.ref_out[p] = a.ref[p];
+        }
+    }
+    move_pages<kSmallThreads>(pg, moving, 1, [&](int k, int &src, int &dst) {
+        src = movers[k];
+        dst = holes[moving - 1 - k];
+        return 1;
+    });
+}
+
+// CTAs of the small kernels: two for each of 152 SMs. The first call on a device raises the shared-memory limit.
+template <typename K, typename A>
+cudaError_t launch_small(K kern, const A &a, const PlaneGroups &p, size_t bytes, bool (&ready)[64], cudaStream_t st) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+        if (e != cudaSuccess) return e;
+        ready[dev] = true;
+    }
+    return launch_dependent(kern, dim3(152 * 2), kSmallThreads, bytes, st, a, p);
+}
+
 // CTAs of the copying kernels: four for each of 152 SMs.
 constexpr int kMoveCtas = 152 * 4;
-
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kern)(P...), cudaStream_t st, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kMoveCtas);
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
 
 }  // namespace
 
@@ -456,6 +710,10 @@ size_t pages_scratch_bytes(int n_rows, int64_t n_pages) {
 }
 
 cudaError_t launch_fork_pages(const ForkArgs &a, const PlaneGroups &p, cudaStream_t st) {
+    if (a.n_pages <= kSmallPages && a.n_in <= kSmallRows && a.n_out <= kSmallRows && a.n_in * a.ld <= kSmallEntries) {
+        static bool ready[64];
+        return launch_small(fork_small_kernel, a, p, small_fork_bytes(a.n_in, a.n_out, a.n_pages), ready, st);
+    }
     char *w = a.scratch;
     ForkScratch s;
     auto take = [&](size_t bytes) {
@@ -470,13 +728,16 @@ cudaError_t launch_fork_pages(const ForkArgs &a, const PlaneGroups &p, cudaStrea
     s.keeps = reinterpret_cast<int32_t *>(take((size_t)a.n_out * 4));
     s.pairs = reinterpret_cast<RowCopy *>(take((size_t)a.n_out * sizeof(RowCopy)));
     s.fresh = reinterpret_cast<int32_t *>(take((size_t)a.n_pages * 4));
-    fork_plan_kernel<<<kCluster, kPlanThreads, 0, st>>>(a, s);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(fork_plan_kernel, dim3(kCluster), kPlanThreads, 0, st, a, s);
     if (e != cudaSuccess) return e;
-    return launch_after(fork_move_kernel, st, a, s, p);
+    return launch_dependent(fork_move_kernel, dim3(kMoveCtas), kMoveThreads, 0, st, a, s, p);
 }
 
 cudaError_t launch_compact_pages(const CompactArgs &a, const PlaneGroups &p, cudaStream_t st) {
+    if (a.n_pages <= kSmallPages) {
+        static bool ready[64];
+        return launch_small(compact_small_kernel, a, p, small_compact_bytes(a.n_pages), ready, st);
+    }
     char *w = a.scratch;
     CompactScratch s;
     s.head = reinterpret_cast<PlanHead *>(w);
@@ -484,16 +745,14 @@ cudaError_t launch_compact_pages(const CompactArgs &a, const PlaneGroups &p, cud
     s.rank = reinterpret_cast<int32_t *>(w + 256);
     s.movers = reinterpret_cast<int32_t *>(w + 256 + pages);
     s.holes = reinterpret_cast<int32_t *>(w + 256 + 2 * pages);
-    compact_plan_kernel<<<kCluster, kPlanThreads, 0, st>>>(a, s);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(compact_plan_kernel, dim3(kCluster), kPlanThreads, 0, st, a, s);
     if (e != cudaSuccess) return e;
-    return launch_after(compact_move_kernel, st, a, s, p);
+    return launch_dependent(compact_move_kernel, dim3(kMoveCtas), kMoveThreads, 0, st, a, s, p);
 }
 
 cudaError_t launch_copy_pages(const int32_t *src, const int32_t *dst, int n, const PlaneGroups &p, int64_t n_src,
                               int64_t n_dst, WsHeader *hdr, cudaStream_t st) {
-    copy_pages_kernel<<<kMoveCtas, kMoveThreads, 0, st>>>(src, dst, n, p, n_src, n_dst, hdr);
-    return cudaGetLastError();
+    return launch_dependent(copy_pages_kernel, dim3(kMoveCtas), kMoveThreads, 0, st, src, dst, n, p, n_src, n_dst, hdr);
 }
 
 }  // namespace qsa

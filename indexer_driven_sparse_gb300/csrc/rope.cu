@@ -117,6 +117,8 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
 // Thread (token n, slot s) for heads [h0, h0 + run), kBatch at a time: their loads are issued together, which
 // the compiler cannot do by itself since out may be x.
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, RopeRows a, int run) {
+    let_next_begin();
+    wait_for_previous();
     const int S = r.D >> 4;
     const int64_t t = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
     const int64_t n = t / S;
@@ -215,6 +217,8 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], const Slot &sl,
 template <int S, bool F8>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, AppendArgs a, int run) {
     constexpr int D = S * 16;
+    let_next_begin();
+    wait_for_previous();
     const int64_t t = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
     const int64_t n = t / S;
     const int s = (int)(t & (S - 1));
@@ -300,8 +304,7 @@ cudaError_t append(const RopeArgs &r, const AppendArgs &a, cudaStream_t st) {
     const int64_t threads = (int64_t)a.N * S;
     const int run = run_of(threads, heads);
     const dim3 grid((unsigned)((threads + kRopeThreads - 1) / kRopeThreads), (heads + run - 1) / run);
-    rope_append_kernel<S, F8><<<grid, kRopeThreads, 0, st>>>(r, a, run);
-    return cudaGetLastError();
+    return launch_dependent(rope_append_kernel<S, F8>, grid, kRopeThreads, 0, st, r, a, run);
 }
 
 }  // namespace
@@ -310,8 +313,7 @@ cudaError_t launch_rope(const RopeArgs &r, const RopeRows &a, cudaStream_t st) {
     const int64_t threads = (int64_t)a.N * (r.D >> 4);
     const int run = run_of(threads, a.H);
     const dim3 grid((unsigned)((threads + kRopeThreads - 1) / kRopeThreads), (a.H + run - 1) / run);
-    rope_kernel<<<grid, kRopeThreads, 0, st>>>(r, a, run);
-    return cudaGetLastError();
+    return launch_dependent(rope_kernel, grid, kRopeThreads, 0, st, r, a, run);
 }
 
 cudaError_t launch_rope_append(const RopeArgs &r, const AppendArgs &a, cudaStream_t st) {

@@ -256,11 +256,11 @@ class PagedCache:
         else:
             self.planes = [torch.zeros(*shape, head_dim, dtype=torch.bfloat16, device=device) for _ in range(2)]
         i32 = dict(dtype=torch.int32, device=device)
-        # the page calls write a new table beside the old one: two of each, in turn
+        # the page calls write new bookkeeping beside the old: two of each, in turn
         self._tables = [torch.full((n_rows, max_pages), -1, **i32) for _ in range(2)]
         self._lens = [torch.zeros(n_rows, **i32) for _ in range(2)]
-        self._now = 0
-        self.ref = torch.zeros(n_pages, **i32)
+        self._refs = [torch.zeros(n_pages, **i32) for _ in range(2)]
+        self._now, self._ref_now = 0, 0
         self._rows = torch.arange(n_rows, **i32)
         self._one = torch.ones(n_rows, **i32)
         self.ws = qb.paged_workspace(self.cfg, device)
@@ -274,20 +274,26 @@ class PagedCache:
     def seq_len(self):
         return self._lens[self._now]
 
+    @property
+    def ref(self):
+        return self._refs[self._ref_now]
+
     def fork(self, parent, add, stream=None):
         """Row i continues row parent[i] (-1: starts empty) with room for add[i] more tokens (qsa_fork_pages)."""
-        new = 1 - self._now
+        new, new_ref = 1 - self._now, 1 - self._ref_now
         qb.qsa_fork_pages(self.cfg.page_size, parent, add, self.table, self.seq_len, self.ref, self._tables[new],
-                          self._lens[new], self.ref, self.planes, self.pages_ws, stream)
-        self._now = new
+                          self._lens[new], self._refs[new_ref], self.planes, self.pages_ws, stream)
+        self._now, self._ref_now = new, new_ref
 
     def extend(self, add=None, stream=None):
         """Room for add[i] more tokens in row i (None: one each)."""
         self.fork(self._rows, self._one if add is None else add, stream)
 
     def compact(self, stream=None):
-        qb.qsa_compact_pages(self.cfg.page_size, self.table, self.seq_len, self.ref, self.table, self.ref, self.planes,
-                             self.pages_ws, stream)
+        new_ref = 1 - self._ref_now
+        qb.qsa_compact_pages(self.cfg.page_size, self.table, self.seq_len, self.ref, self.table, self._refs[new_ref],
+                             self.planes, self.pages_ws, stream)
+        self._ref_now = new_ref
 
     def append(self, layer: int, rope, q, k, v, pos, seq=None, q_out=None, stream=None):
         """Store k (turned) and v at position pos[n] of row seq[n] (None: row n) of a layer; q turned into q_out."""

@@ -489,7 +489,8 @@ def copied(plane, copies, page):
 
 
 @pytest.mark.parametrize("S,page,high,spare", [(1, 4, 9, 5), (8, 16, 100, 30), (300, 8, 60, 1500), (70, 1, 5, 400),
-                                               (5, 1000, 3000, 12)])
+                                               (5, 1000, 3000, 12), (1030, 4, 20, 4000), (20, 2, 90, 17000),
+                                               (600, 1, 120, 3000)])
 @pytest.mark.parametrize("kind", ["beams", "extend", "any", "free"])
 def test_fork(cuda_lib, S, page, high, spare, kind):
     table, lens, ref = random_pool(S, page, high, spare, seed=S + page)
@@ -517,8 +518,9 @@ def test_fork(cuda_lib, S, page, high, spare, kind):
     for got, w in zip(planes, want_planes):
         assert torch.equal(got, w)
     assert want[4] == [] and status(ws) == (0, 0)
-    qb.qsa_fork_pages(*args, ref_dev, t_out, l_out, ref_dev, [], ws)          # references in place, no planes
-    assert np.array_equal(ref_dev.cpu().numpy(), want[2]) and np.array_equal(t_out.cpu().numpy(), want[0])
+    r_out.fill_(77)
+    qb.qsa_fork_pages(*args, ref_dev, t_out, l_out, r_out, [], ws)            # no planes: bookkeeping alone
+    assert np.array_equal(r_out.cpu().numpy(), want[2]) and np.array_equal(t_out.cpu().numpy(), want[0])
 
 
 def test_fork_rows_that_find_no_page_become_empty(cuda_lib):
@@ -541,7 +543,7 @@ def test_fork_rows_that_find_no_page_become_empty(cuda_lib):
 
 
 @pytest.mark.parametrize("S,page,high,spare", [(1, 4, 9, 5), (8, 16, 100, 30), (300, 8, 60, 1500), (0, 4, 8, 9),
-                                               (40, 2, 700, 9000)])
+                                               (40, 2, 700, 9000), (40, 2, 700, 9), (16, 4, 90, 30000), (1500, 4, 40, 11)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_compact(cuda_lib, S, page, high, spare, in_place):
     table, lens, ref = random_pool(S, page, high, spare, seed=S + 1)
@@ -555,13 +557,15 @@ def test_compact(cuda_lib, S, page, high, spare, in_place):
         want_planes.append(w)
     ws = qb.pages_workspace(max(S, 1), len(ref))
     t, r = ints(table.tolist()).reshape(table.shape), ints(ref.tolist())
-    t_out, r_out = (t, r) if in_place else (torch.full_like(t, 77), torch.full_like(r, 77))
+    t_out, r_out = t if in_place else torch.full_like(t, 77), torch.full_like(r, 77)
     qb.qsa_compact_pages(page, t, ints(lens.tolist()), r, t_out, r_out, planes, ws)
     assert np.array_equal(t_out.cpu().numpy(), want_t) and np.array_equal(r_out.cpu().numpy(), want_r)
     assert all(torch.equal(a, b) for a, b in zip(planes, want_planes))
     assert status(ws) == (0, 0)
     # a compact pool stays as it is
-    qb.qsa_compact_pages(page, t_out, ints(lens.tolist()), r_out, t_out, r_out, planes, ws)
+    again = torch.full_like(r, 77)
+    qb.qsa_compact_pages(page, t_out, ints(lens.tolist()), r_out, t_out, again, planes, ws)
+    assert torch.equal(again, r_out)
     assert np.array_equal(t_out.cpu().numpy(), want_t) and all(torch.equal(a, b) for a, b in zip(planes, want_planes))
 
 

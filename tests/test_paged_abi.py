@@ -155,11 +155,11 @@ def test_page_calls_refusals(lib):
         return (qb.qsa_page_planes * 1)(qb.qsa_page_planes(**base))
 
     def fork(ps=4, parent=FAKE, add=FAKE, n_out=3, table=FAKE, lens=FAKE, n_in=3, ld=4, ref=FAKE, pages=9, t_out=FAKE + 256,
-             l_out=FAKE + 256, r_out=FAKE, groups=None, n=1, ws=FAKE, bytes=1 << 30):
+             l_out=FAKE + 256, r_out=FAKE + 256, groups=None, n=1, ws=FAKE, bytes=1 << 30):
         return lib.qsa_fork_pages(ps, parent, add, n_out, table, lens, n_in, ld, ref, pages, t_out, l_out, r_out,
                                   planes() if groups is None else groups, n, ws, bytes, None)
 
-    def compact(ps=4, table=FAKE, lens=FAKE, rows=3, ld=4, ref=FAKE, pages=9, t_out=FAKE, r_out=FAKE, groups=None, n=1,
+    def compact(ps=4, table=FAKE, lens=FAKE, rows=3, ld=4, ref=FAKE, pages=9, t_out=FAKE, r_out=FAKE + 256, groups=None, n=1,
                 ws=FAKE, bytes=1 << 30):
         return lib.qsa_compact_pages(ps, table, lens, rows, ld, ref, pages, t_out, r_out,
                                      planes() if groups is None else groups, n, ws, bytes, None)
@@ -169,10 +169,10 @@ def test_page_calls_refusals(lib):
                   dict(groups=planes(page_bytes=-16)), dict(groups=planes(page_bytes=36, base=FAKE + 2))]
     for kw in [dict(ps=0), dict(parent=0), dict(add=0), dict(n_out=-1), dict(n_out=65537), dict(n_in=65537), dict(table=0),
                dict(lens=0), dict(ld=-1), dict(ref=0), dict(pages=-1), dict(t_out=0), dict(t_out=FAKE), dict(l_out=0),
-               dict(l_out=FAKE), dict(r_out=0), dict(ws=0), dict(ws=FAKE + 64)] + bad_groups:
+               dict(l_out=FAKE), dict(r_out=0), dict(r_out=FAKE), dict(ws=0), dict(ws=FAKE + 64)] + bad_groups:
         assert fork(**kw) == BAD, kw
     for kw in [dict(ps=0), dict(table=0), dict(lens=0), dict(rows=-1), dict(rows=65537), dict(ld=-1), dict(ref=0),
-               dict(pages=-1), dict(t_out=0), dict(r_out=0), dict(ws=0)] + bad_groups:
+               dict(pages=-1), dict(t_out=0), dict(r_out=0), dict(r_out=FAKE), dict(ws=0)] + bad_groups:
         assert compact(**kw) == BAD, kw
     assert fork(bytes=256) == SMALL and compact(bytes=256) == SMALL
     assert fork(pages=(1 << 30) + 1) == UNSUPPORTED and compact(pages=(1 << 30) + 1) == UNSUPPORTED
@@ -192,32 +192,42 @@ def test_page_calls_refusals(lib):
 
 def test_binding_refuses_wrong_tensors(lib):
     import torch
-    cpu = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
-    for bad, error in ((cpu.float(), TypeError), (cpu[:, :4], ValueError), (cpu.transpose(0, 1).contiguous().transpose(0, 1),
-                                                                            ValueError), (cpu.double(), TypeError)):
-        with pytest.raises(error):
-            qb._head_rows(bad, 2, 8, 128, "q", -1)
-    assert qb._head_rows(cpu, 2, 8, 128, "q", -1) == (cpu.data_ptr(), 1024)
-    with pytest.raises(ValueError, match="current device"):
-        qb._head_rows(cpu, 2, 8, 128, "q", 0)
-    i32 = torch.zeros(4, 6, dtype=torch.int32)
-    with pytest.raises(TypeError):
-        qb._ints(i32[0].long(), 6, "pos", -1)
-    with pytest.raises(ValueError):
-        qb._ints(i32[0], 5, "pos", -1)
-    with pytest.raises(ValueError, match="contiguous"):
-        qb._ints(i32[:, 0], 4, "pos", -1)
-    with pytest.raises(ValueError, match="current device"):
-        qb._on(i32, torch.int32, "table", 0)
-    with pytest.raises(ValueError):
-        qb._ints2(i32, 6, 4, "table", -1)
-    with pytest.raises(ValueError):
-        qb._cache(cpu, torch.bfloat16, (2, 8, 64), "k_cache", 0)
-    for bad in (torch.zeros(3, 5, 4), torch.zeros(6, 3, 4).transpose(0, 1)):
-        with pytest.raises(ValueError):
-            qb._plane_groups([bad], 6, -1)
-    g = qb._plane_groups([torch.zeros(3, 6, 4, 2, dtype=torch.int16), torch.zeros(4, 6, 5)[1:]], 6, -1)
-    assert [(x.plane_stride, x.page_bytes, x.n_planes) for x in g] == [(96, 16, 3), (120, 20, 3)]
+    bf16 = dict(dtype=torch.bfloat16)
+    i32 = dict(dtype=torch.int32)
+    rope = qb.rope_table(128, device="cpu")
+    x, pos = torch.zeros(2, 8, 128, **bf16), torch.zeros(2, **i32)
+
+    def refused(error, text, fn, *args):
+        with pytest.raises(error, match=text):
+            fn(*args)
+
+    # everything right but the device
+    refused(ValueError, "x is on cpu", qb.qsa_rope, rope, x, pos, x)
+    refused(TypeError, "x must be torch.BFloat16", qb.qsa_rope, rope, x.float(), pos, x)
+    refused(TypeError, "x must be a tensor", qb.qsa_rope, rope, None, pos, x)
+    refused(ValueError, "x must be", qb.qsa_rope, rope, x[0], pos, x)
+    refused(ValueError, r"x must be \[2, 8, 128\], got \[2, 8, 64\]", qb.qsa_rope, rope, x[..., :64], pos, x)
+    refused(ValueError, "heads of x", qb.qsa_rope, rope, torch.zeros(8, 2, 128, **bf16).transpose(0, 1), pos, x)
+    refused(ValueError, "heads of x", qb.qsa_rope, rope, torch.zeros(2, 8, 256, **bf16)[..., ::2], pos, x)
+    cfg = paged_cfg(n_q_heads=8, n_kv_heads=2)
+    kv = [torch.zeros(5, 16, 2, 128, **bf16) for _ in range(2)]
+    table, lens, ws = torch.zeros(2, 3, **i32), torch.zeros(2, **i32), torch.zeros(512, dtype=torch.uint8)
+    lse = torch.zeros(2, 8)
+
+    def decode(cfg=cfg, q=x, kv=kv, table=table, lens=lens, out=x, lse=lse, ws=ws):
+        qb.qsa_paged_decode(cfg, q, *kv, table, lens, out, lse, ws)
+
+    for error, text, kw in ((ValueError, "q is on cpu", {}), (TypeError, "qsa_paged_config", dict(cfg=rope.cfg)),
+                            (TypeError, "table must be torch.Int", dict(table=table.long())),
+                            (ValueError, "table must have two", dict(table=lens)),
+                            (ValueError, r"q must be \[3", dict(table=torch.zeros(3, 3, **i32)))):
+        with pytest.raises(error, match=text):
+            decode(**kw)
+    planes = [torch.zeros(3, 6, 4)]
+    ref = torch.zeros(6, **i32)
+    refused(ValueError, "parent is on cpu", qb.qsa_fork_pages, 4, pos, pos, table, lens, ref, table, lens, ref, planes, ws)
+    refused(ValueError, "table is on cpu", qb.qsa_compact_pages, 4, table, lens, ref, table, ref, planes, ws)
+    refused(ValueError, "src is on cpu", qb.qsa_copy_pages, pos, pos, planes, ws)
     with pytest.raises(ValueError):
         qb.rope_table(128, scaling="other")
     with pytest.raises(qb.QsaError):
