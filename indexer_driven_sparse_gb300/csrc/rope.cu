@@ -212,8 +212,8 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], const Slot &sl,
     }
 }
 
-// Thread (token n, slot s) for a run of the token's Hq + 2 Hkv heads: q (turned into q_out), k (turned into the
-// cache), v (into the cache). S = D / 16 threads of one warp carry a head.
+// Thread (token n, slot s) for a run of the token's 2 Hkv + Hq heads: k (turned into the cache), v (into the cache),
+// then q (turned into q_out): the runs with K and V, which take longer, begin first. S = D / 16 threads of one warp carry a head.
 template <int S, bool F8>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, AppendArgs a, int run) {
     constexpr int D = S * 16;
@@ -227,28 +227,26 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, A
     if (row < 0) return;                                     // padding
     const int pos = a.pos[n];
     const Slot sl = slot_of(r, s), straight = {8 * s, D / 2 + 8 * s, -1, -1};
-    // heads of q come first; without queries the list starts at k
-    const int total = a.Hq + 2 * a.Hkv;
-    const int h0 = (a.q ? 0 : a.Hq) + blockIdx.y * run;
-    int h1 = min(total, h0 + run);
-    if (h0 >= h1) return;
+    const int kv_heads = 2 * a.Hkv;
+    const int h1 = min(kv_heads + (a.q ? a.Hq : 0), ((int)blockIdx.y + 1) * run);
+    const int h0 = blockIdx.y * run;
     uint4 va[kBatch], vb[kBatch];
     auto load = [&](int h) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int hi = h + i;
             if (hi >= h1) break;
-            const bool v = hi >= a.Hq + a.Hkv;
-            const uint16_t *src = hi < a.Hq ? a.q + n * a.q_ld + hi * D
-                                  : v       ? a.v + n * a.v_ld + (hi - a.Hq - a.Hkv) * D
-                                            : a.k + n * a.k_ld + (hi - a.Hq) * D;
+            const bool v = hi >= a.Hkv && hi < kv_heads;
+            const uint16_t *src = hi >= kv_heads ? a.q + n * a.q_ld + (hi - kv_heads) * D
+                                  : v            ? a.v + n * a.v_ld + (hi - a.Hkv) * D
+                                                 : a.k + n * a.k_ld + hi * D;
             va[i] = *reinterpret_cast<const uint4 *>(src + (v ? straight.a : sl.a));
             vb[i] = *reinterpret_cast<const uint4 *>(src + (v ? straight.b : sl.b));
         }
     };
     load(h0);
     int64_t slot = -1;
-    if (h1 > a.Hq) {
+    if (h0 < kv_heads) {
         bool ok = row < a.n_rows && pos >= 0 && pos / a.page_size < a.ld;
         if (ok) {
             const int page = a.table[(int64_t)row * a.ld + pos / a.page_size];
@@ -257,19 +255,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, A
         }
         if (!ok) {
             if (s == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereAppend, (int)n);
-            h1 = min(h1, a.Hq);                               // its K and V are left out
+            slot = -1;                                        // its K and V are left out
         }
     }
     float co[8], si[8];
-    if (sl.fa >= 0 && h0 < min(h1, a.Hq + a.Hkv)) turns(r, sl, pos, co, si);
+    if (sl.fa >= 0) turns(r, sl, pos, co, si);
     for (int h = h0; h < h1; h += kBatch) {
         if (h > h0) load(h);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int hi = h + i;
             if (hi >= h1) break;
-            const bool is_q = hi < a.Hq, is_v = hi >= a.Hq + a.Hkv;
-            const int g = hi - a.Hq - (is_v ? a.Hkv : 0);      // KV head
+            const bool is_q = hi >= kv_heads, is_v = hi >= a.Hkv && !is_q;
+            if (!is_q && slot < 0) continue;
+            const int g = hi - (is_v ? a.Hkv : 0);             // KV head
             const Slot at = is_v ? straight : sl;
             const bool turned = at.fa >= 0;
             float x[16];
@@ -284,7 +283,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, A
                     va[i] = pack8(x);
                     vb[i] = pack8(x + 8);
                 }
-                uint16_t *dst = is_q ? a.q_out + n * a.q_out_ld + hi * D : (is_v ? a.v_cache : a.k_cache) + kv;
+                uint16_t *dst = is_q ? a.q_out + n * a.q_out_ld + (hi - kv_heads) * D : (is_v ? a.v_cache : a.k_cache) + kv;
                 *reinterpret_cast<uint4 *>(dst + at.a) = va[i];
                 *reinterpret_cast<uint4 *>(dst + at.b) = vb[i];
             }
