@@ -94,6 +94,7 @@ struct ForkArgs {
     const int32_t *parent, *add, *table, *seq_len, *ref;
     int32_t *table_out, *seq_len_out, *ref_out;
     int32_t n_out, n_in, page_size, n_pages;
+    int32_t page_shift;                 // log2 of page_size, -1: no power of two (set by the launcher)
     int64_t ld;
     WsHeader *hdr;
     char *scratch;

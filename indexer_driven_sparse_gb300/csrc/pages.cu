@@ -25,9 +25,10 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveBytes = 4096;       // one warp's share of a page copy at a time: eight 16-byte words a lane, in two goes
 constexpr int kSharedRows = 4096;      // per-parent words kept in shared memory up to this many rows
 constexpr int kSmallThreads = 512;
-constexpr int kSmallPages = 16384;     // page ids in 16 bits, at most 64 KB of shared memory
+constexpr int kSmallPages = 16384;     // page ids in 16 bits, at most 96 KB of shared memory for the pages
 constexpr int kSmallRows = 1024;
 constexpr int64_t kSmallEntries = 65536;   // table entries whose references one CTA counts
+constexpr int kEntriesAhead = 12;      // ... this many of each thread's loaded before the plan
 
 struct RowCopy {                       // new page fresh[off] becomes page src's first `used` tokens
     int32_t src, off, used;
@@ -113,6 +114,20 @@ __device__ __forceinline__ RowPlan row_plan(const ForkArgs &a, int i) {
     return p;
 }
 
+// f(p, ref[p]) for p in [lo, hi), eight loads at a time: f may store, and the compiler keeps loads behind stores.
+template <typename F>
+__device__ __forceinline__ void for_refs(const int32_t *ref, int lo, int hi, F f) {
+    for (int p0 = lo; p0 < hi; p0 += 8) {
+        int r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (p0 + i < hi) r[i] = ref[p0 + i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (p0 + i < hi) f(p0 + i, r[i]);
+    }
+}
+
 // A thread's run of page ids [lo, hi) in its CTA's share.
 struct Run {
     int lo, hi;
@@ -138,11 +153,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     wait_for_previous();
     const Run run = run_of_thread(a.n_pages);
     int free_here = 0;
-    for (int p = run.lo; p < run.hi; ++p) {
-        const int r = a.ref[p];
+    for_refs(a.ref, run.lo, run.hi, [&](int p, int r) {
         free_here += r == 0;
         a.ref_out[p] = r;
-    }
+    });
     long long total;
     int rank = (int)block_scan<long long>(free_here, sh, &total) - free_here;
     if (tid == 0) s.head->per_cta[cta] = (int)total;
@@ -195,8 +209,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
         n_free += n;
     }
     // every free page has a place in the order; pages behind what is handed out are written and not read
-    for (int p = run.lo; p < run.hi; ++p)
-        if (a.ref[p] == 0) s.fresh[rank++] = p;
+    for_refs(a.ref, run.lo, run.hi, [&](int p, int r) {
+        if (r == 0) s.fresh[rank++] = p;
+    });
     if (cta != 0) return;
     int n_pairs = 0;
     for (int i0 = 0; i0 < a.n_out; i0 += kPlanThreads) {
@@ -356,7 +371,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     wait_for_previous();
     const Run run = run_of_thread(a.n_pages);
     int live = 0;
-    for (int p = run.lo; p < run.hi; ++p) live += a.ref[p] > 0;
+    for_refs(a.ref, run.lo, run.hi, [&](int, int r) { live += r > 0; });
     long long total;
     int below = (int)block_scan<long long>(live, sh, &total) - live;
     if (tid == 0) s.head->per_cta[cta] = (int)total;
@@ -368,8 +383,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
         below += c < cta ? n : 0;
         n_live += n;
     }
-    for (int p = run.lo; p < run.hi; ++p) {
-        const int r = a.ref[p];
+    for_refs(a.ref, run.lo, run.hi, [&](int p, int r) {
         if (p == n_live) s.head->n_pairs = n_live - below;
         if (r > 0) {
             if (p >= n_live) {
@@ -384,7 +398,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
             s.rank[p] = -1;
             if (p < n_live) s.holes[p - below] = p;
         }
-    }
+    });
     if (cta == 0 && tid == 0) {
         s.head->n_live = n_live;
         if (n_live == a.n_pages) s.head->n_pairs = 0;
@@ -449,176 +463,241 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
 // ---------------------------------------------------------------------------- small pools: one kernel
 // Shared memory of a CTA's plan.
 struct SmallFork {
-    int *len, *last, *first, *children;    // [n_in] tokens, last partly filled page (kAlone: nothing else names it; -1: none), ...
-    int *parent, *total, *off;             // [n_out] parent -1: starts empty; off kKeeps: keeps the parent's last page; -1: failed
+    int *len, *full;                       // [n_in] tokens, full pages (-1: an impossible length)
+    int *last;                             // [n_in] the last, partly filled page (kAlone: nothing else names it; -1: none)
+    int *first, *children;                 // [n_in] lowest row that continues it (later: whether one keeps the last page), how many do
+    int *parent, *pages, *off;             // [n_out] parent -1: starts empty; pages in all; off kKeeps: keeps the parent's last page; -1: failed
+    int *delta;                            // [n_pages] CTA 0: references that come and go
     uint16_t *pairs;                       // [n_out] rows that copy a page
     uint16_t *fresh;                       // [n_pages] free pages in order
 };
 constexpr int kAlone = 1 << 30, kKeeps = 1 << 30;
-
-static_assert(kSmallPages <= 32 * kSmallThreads, "a thread's run of pages fits a word");
-
-// Bit i: test(ref[lo + i]), for a run of at most 32 pages, eight loads at a time.
-template <typename Test>
-__device__ __forceinline__ uint32_t run_mask(const int32_t *ref, int lo, int hi, Test test) {
-    uint32_t m = 0;
-    for (int p0 = lo; p0 < hi; p0 += 8) {
-        int r[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (p0 + i < hi) r[i] = ref[p0 + i];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (p0 + i < hi && test(r[i])) m |= 1u << (p0 + i - lo);
-    }
-    return m;
-}
+constexpr int kSmallChunks = kSmallPages / kSmallThreads, kSmallWarps = kSmallThreads / 32;
+static_assert(kSmallChunks <= 32 && kSmallChunks * kSmallWarps <= kSmallThreads, "a thread's pages fit a word, the counts a scan");
 
 size_t small_fork_bytes(int n_in, int n_out, int n_pages) {
-    return (size_t)n_in * 16 + (size_t)n_out * 12 + ((size_t)n_out + n_pages + 8) * 2;
+    return (size_t)n_in * 20 + (size_t)n_out * 12 + (size_t)n_pages * 4 + ((size_t)n_out + n_pages + 8) * 2;
 }
 size_t small_compact_bytes(int n_pages) { return ((size_t)n_pages * 2 + 8) * 2; }
-constexpr int kSmallSmem = 2 * kSmallRows * 16 + kSmallPages * 4;    // 96 KB: above both sums at their limits
+constexpr int kSmallSmem = kSmallRows * 32 + kSmallPages * 6 + 1024;    // above both sums at their limits
 
-// CTA 0 also writes the references: ref and the entries that rows give up or take.
+// test(ref[p]) for the pages p = tid, tid + kSmallThreads, ... as a word; counts[t] becomes the number of pages that
+// pass before chunk t / kSmallWarps of kSmallThreads pages and warp t % kSmallWarps in it, *total all that pass.
+// `also(p, r)` sees every page. Ends with a barrier.
+template <typename Test, typename Also>
+__device__ __forceinline__ uint32_t small_ranks(const int32_t *ref, int n_pages, int *counts, int *sh, int *total, Test test,
+                                                Also also) {
+    const int tid = threadIdx.x, warp = tid >> 5, chunks = (n_pages + kSmallThreads - 1) / kSmallThreads;
+    uint32_t mine = 0;
+    for (int i0 = 0; i0 < chunks; i0 += 16) {
+        int r[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int p = (i0 + i) * kSmallThreads + tid;
+            if (p < n_pages) r[i] = ref[p];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int p = (i0 + i) * kSmallThreads + tid;
+            if (i0 + i >= chunks) break;
+            const bool pass = p < n_pages && test(r[i]);
+            const uint32_t m = __ballot_sync(0xffffffffu, pass);
+            mine |= (uint32_t)pass << (i0 + i);
+            if ((tid & 31) == 0) counts[(i0 + i) * kSmallWarps + warp] = __popc(m);
+            if (p < n_pages) also(p, r[i]);
+        }
+    }
+    __syncthreads();
+    const int n = tid < chunks * kSmallWarps ? counts[tid] : 0;
+    const int upto = block_scan<int>(n, sh, total);
+    if (tid < chunks * kSmallWarps) counts[tid] = upto - n;
+    __syncthreads();
+    return mine;
+}
+
+// f(p, passes, passes before p) for the same pages.
+template <typename F>
+__device__ __forceinline__ void for_ranks(uint32_t mine, int n_pages, const int *counts, F f) {
+    const int tid = threadIdx.x, warp = tid >> 5, chunks = (n_pages + kSmallThreads - 1) / kSmallThreads;
+    const uint32_t lower = (1u << (tid & 31)) - 1u;
+    for (int i = 0; i < chunks; ++i) {
+        const bool pass = (mine >> i) & 1u;
+        const uint32_t m = __ballot_sync(0xffffffffu, pass);
+        const int p = i * kSmallThreads + tid;
+        if (p < n_pages) f(p, pass, counts[i * kSmallWarps + warp] + __popc(m & lower));
+    }
+}
+
+// CTA 0 also writes the references: ref and what rows give up or take, summed in shared memory.
 __global__ void __launch_bounds__(kSmallThreads, 2) fork_small_kernel(ForkArgs a, PlaneGroups pg) {
     extern __shared__ __align__(16) int small_smem[];
+    __shared__ int counts[kSmallThreads];
     __shared__ int sh[33];
     __shared__ long long sh64[33];
     let_next_begin();
     wait_for_previous();
     const int tid = threadIdx.x, lane = tid & 31;
+    const int ps = a.page_size, shift = a.page_shift;
+    auto over = [&](int tokens) { return shift >= 0 ? tokens >> shift : tokens / ps; };     // whole pages
     SmallFork s;
     s.len = small_smem;
-    s.last = s.len + a.n_in;
+    s.full = s.len + a.n_in;
+    s.last = s.full + a.n_in;
     s.first = s.last + a.n_in;
     s.children = s.first + a.n_in;
     s.parent = s.children + a.n_in;
-    s.total = s.parent + a.n_out;
-    s.off = s.total + a.n_out;
-    s.pairs = reinterpret_cast<uint16_t *>(s.off + a.n_out);
+    s.pages = s.parent + a.n_out;
+    s.off = s.pages + a.n_out;
+    s.delta = s.off + a.n_out;
+    s.pairs = reinterpret_cast<uint16_t *>(s.delta + a.n_pages);
     s.fresh = s.pairs + a.n_out;
-    const int per = (a.n_pages + kSmallThreads - 1) / kSmallThreads;
-    const int lo = min(a.n_pages, tid * per), hi = min(a.n_pages, lo + per);
-    const uint32_t is_free = run_mask(a.ref, lo, hi, [](int r) { return r == 0; });
-    const int free_here = __popc(is_free);
-    if (blockIdx.x == 0)
-        for (int p = tid; p < a.n_pages; p += kSmallThreads) a.ref_out[p] = a.ref[p];
+    // CTA 0's table entries come along with the first loads
+    const int ld = (int)a.ld, entries = a.n_in * ld;
+    int entry[kEntriesAhead];
+    if (blockIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < kEntriesAhead; ++i) {
+            const int x = tid + i * kSmallThreads;
+            entry[i] = x < entries ? a.table[x] : -1;
+        }
+    }
+    for (int i = tid; i < a.n_out; i += kSmallThreads) {
+        s.parent[i] = a.parent[i];
+        s.pages[i] = a.add[i];
+    }
     for (int p = tid; p < a.n_in; p += kSmallThreads) {
         const int len = a.seq_len[p];
-        int last = -1;
-        if (len > 0 && pages_of(len, a.page_size) <= a.ld && len % a.page_size != 0) {
-            last = a.table[(int64_t)p * a.ld + len / a.page_size];
+        int last = -1, full = len >= 0 ? over(len) : -1;
+        if (full >= 0 && full + (len != full * ps) > ld) full = -1;
+        if (full >= 0 && len != full * ps) {
+            last = a.table[p * ld + full];
             if (last >= 0 && last < a.n_pages)
                 last |= a.ref[last] == 1 ? kAlone : 0;
             else
                 last = -1;
         }
         s.len[p] = len;
+        s.full[p] = full;
         s.last[p] = last;
         s.first[p] = INT32_MAX;
         s.children[p] = 0;
     }
-    for (int i = tid; i < a.n_out; i += kSmallThreads) {
-        s.parent[i] = a.parent[i];
-        s.total[i] = a.add[i];
-    }
     int n_free;
-    int rank = block_scan<int>(free_here, sh, &n_free) - free_here;
-    for (uint32_t left = is_free; left != 0; left &= left - 1) s.fresh[rank++] = (uint16_t)(lo + __ffs(left) - 1);
+    const uint32_t is_free = small_ranks(a.ref, a.n_pages, counts, sh, &n_free, [](int r) { return r == 0; },
+                                         [&](int p, int r) { s.delta[p] = r; });
+    for_ranks(is_free, a.n_pages, counts, [&](int p, bool free, int rank) {
+        if (free) s.fresh[rank] = (uint16_t)p;
+    });
     for (int i = tid; i < a.n_out; i += kSmallThreads) {
-        const int parent = s.parent[i], add = s.total[i];
-        bool ok = parent >= -1 && parent < a.n_in && add >= 0;
+        const int parent = s.parent[i], add = s.pages[i];
+        bool ok = parent >= -1 && parent < a.n_in && add >= 0 && (parent < 0 || s.full[parent] >= 0);
         const int base = ok && parent >= 0 ? s.len[parent] : 0;
         const int64_t total = (int64_t)base + add;
-        ok = ok && base >= 0 && pages_of(base, a.page_size) <= a.ld && total <= INT32_MAX &&
-             pages_of((int)total, a.page_size) <= a.ld;
+        ok = ok && total <= INT32_MAX;
+        int pages = ok ? over((int)total) : 0;
+        pages += ok && (int)total != pages * ps;
+        ok = ok && pages <= ld;
         if (!ok && blockIdx.x == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
         s.parent[i] = ok ? parent : -1;
-        s.total[i] = ok ? (int)total : 0;
+        s.pages[i] = ok ? pages : 0;
+        if (blockIdx.x == gridDim.x - 1) a.seq_len_out[i] = ok ? (int)total : 0;    // a row that fails later is emptied there
         if (ok && parent >= 0) atomicMin(s.first + parent, i);
     }
     __syncthreads();
-    long long handed = 0;
-    int n_pairs = 0;
+    // pages that each row needs and the copies, scanned together (copies above bit 48: at most kSmallRows)
+    long long before = 0;
     for (int i0 = 0; i0 < a.n_out; i0 += kSmallThreads) {
         const int i = i0 + tid;
-        int mine = 0, keep = 0;
-        bool copies = false;
+        long long mine = 0;
+        int keep = 0;
         if (i < a.n_out) {
-            const int parent = s.parent[i], base = parent >= 0 ? s.len[parent] : 0;
-            if (base % a.page_size != 0) {
+            const int parent = s.parent[i], full = parent >= 0 ? s.full[parent] : 0;
+            long long copies = 0;
+            if (parent >= 0 && s.len[parent] != full * ps) {
                 const int last = s.last[parent];
                 if (last < 0 && blockIdx.x == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
                 keep = last >= 0 && (last & kAlone) != 0 && s.first[parent] == i;
                 copies = last >= 0 && !keep;
             }
-            mine = pages_of(s.total[i], a.page_size) - base / a.page_size - keep;
+            mine = s.pages[i] - full - keep + (copies << 48);
         }
-        // n_out <= kSmallRows rows of at most 2^31 tokens: their pages may pass 2^31
         long long sum;
-        const long long upto = handed + block_scan<long long>(mine, sh64, &sum);
-        handed += sum;
-        const bool failed = mine > 0 && upto > n_free;
+        const long long upto = before + block_scan<long long>(mine, sh64, &sum);
+        constexpr long long kLow = (1ll << 48) - 1;
         if (i < a.n_out) {
+            const int need = (int)(mine & kLow);
+            const bool failed = need > 0 && (upto & kLow) > n_free;
             if (failed) {
                 if (blockIdx.x == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
                 s.off[i] = -1;
+                if (blockIdx.x == gridDim.x - 1) a.seq_len_out[i] = 0;
             } else {
-                s.off[i] = (mine > 0 ? (int)(upto - mine) : 0) | (keep ? kKeeps : 0);
+                s.off[i] = (need > 0 ? (int)((upto & kLow) - need) : 0) | (keep ? kKeeps : 0);
                 if (s.parent[i] >= 0) atomicAdd(s.children + s.parent[i], 1);
             }
-            if (blockIdx.x == gridDim.x - 1) a.seq_len_out[i] = failed ? 0 : s.total[i];
+            if (mine >> 48) s.pairs[(int)(upto >> 48) - 1] = (uint16_t)i;
         }
-        copies = copies && !failed;
-        int count;
-        const int at = block_scan<int>(copies, sh, &count);
-        if (copies) s.pairs[n_pairs + at - 1] = (uint16_t)i;
-        n_pairs += count;
+        before += sum;
     }
+    const int n_pairs = (int)(before >> 48);
     __syncthreads();
-    const int warps = gridDim.x * (kSmallThreads / 32), warp = warp_spread();
+    const int warps = gridDim.x * kSmallWarps, warp = warp_spread();
     if (blockIdx.x == 0) {
-        // every table entry by one thread: the loads of a row do not wait for another row's
-        const int ld = (int)a.ld, entries = a.n_in * ld;
-#pragma unroll 4
-        for (int x = tid; x < entries; x += kSmallThreads) {
-            const int p = x / ld, j = x - p * ld, len = s.len[p];
-            if (len <= 0 || pages_of(len, a.page_size) > ld || j >= pages_of(len, a.page_size)) continue;
+        for (int p = tid; p < a.n_in; p += kSmallThreads) {
             const int first = s.first[p];
-            const int kept = first < a.n_out && s.off[first] >= 0 && (s.off[first] & kKeeps) != 0;
-            const int e = a.table[x], delta = (j < len / a.page_size ? s.children[p] : kept) - 1;
-            if (e < 0 || e >= a.n_pages)
-                record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, p);
-            else if (delta != 0)
-                atomicAdd(a.ref_out + e, delta);
+            s.first[p] = first < a.n_out && s.off[first] >= 0 && (s.off[first] & kKeeps) != 0;
         }
+        __syncthreads();
+        // table entry x = p ld + j, which is page e
+        const int dp = kSmallThreads / max(ld, 1), dj = kSmallThreads - dp * ld;
+        int p = tid / max(ld, 1), j = tid - p * ld;
+        auto count = [&](int e) {
+            const int full = s.full[p];
+            if (full >= 0 && j < full + (s.len[p] != full * ps)) {
+                const int delta = (j < full ? s.children[p] : s.first[p]) - 1;
+                if (e < 0 || e >= a.n_pages)
+                    record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, p);
+                else if (delta != 0)
+                    atomicAdd(s.delta + e, delta);
+            }
+            p += dp;
+            j += dj;
+            if (j >= ld) j -= ld, ++p;
+        };
+#pragma unroll
+        for (int i = 0; i < kEntriesAhead; ++i)
+            if (tid + i * kSmallThreads < entries) count(entry[i]);
+#pragma unroll 4
+        for (int x = tid + kEntriesAhead * kSmallThreads; x < entries; x += kSmallThreads) count(a.table[x]);
+        // new pages were free: each is named once
         for (int i = tid; i < a.n_out; i += kSmallThreads) {
-            const int off = s.off[i];
+            const int off = s.off[i], parent = s.parent[i];
             if (off < 0) continue;
-            const int base = s.parent[i] >= 0 ? s.len[s.parent[i]] : 0;
-            const int mine = pages_of(s.total[i], a.page_size) - base / a.page_size - (off & kKeeps ? 1 : 0);
-            for (int j = 0; j < mine; ++j) atomicAdd(a.ref_out + s.fresh[(off & ~kKeeps) + j], 1);
+            const int mine = s.pages[i] - (parent >= 0 ? s.full[parent] : 0) - (off & kKeeps ? 1 : 0);
+            for (int k = 0; k < mine; ++k) atomicAdd(s.delta + s.fresh[(off & ~kKeeps) + k], 1);
         }
+        __syncthreads();
+        for (int x = tid; x < a.n_pages; x += kSmallThreads) a.ref_out[x] = s.delta[x];
     }
     for (int i = warp; i < a.n_out; i += warps) {
-        const int off = s.off[i], parent = s.parent[i], base = parent >= 0 ? s.len[parent] : 0;
-        const int kept = off < 0 ? 0 : base / a.page_size + (off & kKeeps ? 1 : 0);
-        const int pages = off < 0 ? 0 : pages_of(s.total[i], a.page_size);
+        const int off = s.off[i], parent = s.parent[i];
+        const int kept = off < 0 || parent < 0 ? 0 : s.full[parent] + (off & kKeeps ? 1 : 0), pages = off < 0 ? 0 : s.pages[i];
         const int32_t *from = a.table + (int64_t)max(parent, 0) * a.ld;
         for (int64_t j = lane; j < a.ld; j += 32)
             a.table_out[(int64_t)i * a.ld + j] = j < kept ? from[j] : j < pages ? s.fresh[(off & ~kKeeps) + (int)j - kept] : -1;
     }
     move_pages<kSmallThreads>(pg, n_pairs, a.page_size, [&](int k, int &src, int &dst) {
-        const int i = s.pairs[k], parent = s.parent[i];
+        const int i = s.pairs[k], parent = s.parent[i], off = s.off[i];
+        if (off < 0) return 0;                     // failed
         src = s.last[parent] & ~kAlone;
-        dst = s.fresh[s.off[i]];                   // a row that copies keeps nothing: no flag
-        return s.len[parent] % a.page_size;
+        dst = s.fresh[off];                        // a row that copies keeps nothing: no flag
+        return s.len[parent] - s.full[parent] * ps;
     });
 }
 
 __global__ void __launch_bounds__(kSmallThreads, 2) compact_small_kernel(CompactArgs a, PlaneGroups pg) {
     extern __shared__ __align__(16) int small_smem[];
+    __shared__ int counts[kSmallThreads];
     __shared__ int sh[33];
     __shared__ int moving_sh;
     let_next_begin();
@@ -628,23 +707,19 @@ __global__ void __launch_bounds__(kSmallThreads, 2) compact_small_kernel(Compact
     uint16_t *const map = reinterpret_cast<uint16_t *>(small_smem), *const movers = map + a.n_pages,
                    *const holes = movers + (a.n_pages + 1) / 2;
     constexpr uint16_t kFree = 0xFFFF;
-    const int per = (a.n_pages + kSmallThreads - 1) / kSmallThreads;
-    const int lo = min(a.n_pages, tid * per), hi = min(a.n_pages, lo + per);
-    const uint32_t is_live = run_mask(a.ref, lo, hi, [](int r) { return r > 0; });
     int n_live;
-    int below = block_scan<int>(__popc(is_live), sh, &n_live) - __popc(is_live);
+    const uint32_t is_live = small_ranks(a.ref, a.n_pages, counts, sh, &n_live, [](int r) { return r > 0; }, [](int, int) {});
     if (tid == 0 && n_live == a.n_pages) moving_sh = 0;
-    for (int p = lo; p < hi; ++p) {
+    for_ranks(is_live, a.n_pages, counts, [&](int p, bool live, int below) {
         if (p == n_live) moving_sh = n_live - below;
-        if ((is_live >> (p - lo)) & 1) {
+        if (live) {
             map[p] = (uint16_t)(p < n_live ? p : n_live - 1 - below);
             if (p >= n_live) movers[n_live - 1 - below] = (uint16_t)p;
-            ++below;
         } else {
             map[p] = kFree;
             if (p < n_live) holes[p - below] = (uint16_t)p;
         }
-    }
+    });
     __syncthreads();
     const int moving = moving_sh;
     const int warps = gridDim.x * (kSmallThreads / 32), warp = warp_spread();
@@ -684,7 +759,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) compact_small_kernel(Compact
     });
 }
 
-// CTAs of the small kernels: two for each of 152 SMs. The first call on a device raises the shared-memory limit.
+// CTAs of the small kernels: two for each of 152 SMs where their shared memory allows it. The first call on a device raises the shared-memory limit.
 template <typename K, typename A>
 cudaError_t launch_small(K kern, const A &a, const PlaneGroups &p, size_t bytes, bool (&ready)[64], cudaStream_t st) {
     int dev = 0;
@@ -696,7 +771,7 @@ cudaError_t launch_small(K kern, const A &a, const PlaneGroups &p, size_t bytes,
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    return launch_dependent(kern, dim3(152 * 2), kSmallThreads, bytes, st, a, p);
+    return launch_dependent(kern, dim3(bytes <= 100 * 1024 ? 152 * 2 : 152), kSmallThreads, bytes, st, a, p);
 }
 
 // CTAs of the copying kernels: four for each of 152 SMs.
@@ -712,7 +787,9 @@ size_t pages_scratch_bytes(int n_rows, int64_t n_pages) {
 cudaError_t launch_fork_pages(const ForkArgs &a, const PlaneGroups &p, cudaStream_t st) {
     if (a.n_pages <= kSmallPages && a.n_in <= kSmallRows && a.n_out <= kSmallRows && a.n_in * a.ld <= kSmallEntries) {
         static bool ready[64];
-        return launch_small(fork_small_kernel, a, p, small_fork_bytes(a.n_in, a.n_out, a.n_pages), ready, st);
+        ForkArgs b = a;
+        b.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
+        return launch_small(fork_small_kernel, b, p, small_fork_bytes(a.n_in, a.n_out, a.n_pages), ready, st);
     }
     char *w = a.scratch;
     ForkScratch s;
