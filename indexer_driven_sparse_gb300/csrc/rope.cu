@@ -109,13 +109,13 @@ __device__ __forceinline__ void unpack16(const uint4 &a, const uint4 &b, float (
 __device__ __forceinline__ uint4 pack8(const float *x) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = (uint32_t)float_to_bf16_bits(x[2 * i]) | ((uint32_t)float_to_bf16_bits(x[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Thread (token n, slot s) for heads [h0, h0 + run), kBatch at a time: their loads are issued together, which
 // the compiler cannot do by itself since out may be x.
+template <bool Inter>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, RopeRows a, int run) {
     let_next_begin();
     wait_for_previous();
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, RopeRows
             if (sl.fa >= 0) {
                 float x[16];
                 unpack16(va[i], vb[i], x);
-                turn16(x, co, si, r.interleaved != 0);
+                turn16(x, co, si, Inter);
                 va[i] = pack8(x);
                 vb[i] = pack8(x + 8);
             }
@@ -214,7 +214,7 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], const Slot &sl,
 
 // Thread (token n, slot s) for a run of the token's 2 Hkv + Hq heads: k (turned into the cache), v (into the cache),
 // then q (turned into q_out): the runs with K and V, which take longer, begin first. S = D / 16 threads of one warp carry a head.
-template <int S, bool F8>
+template <int S, bool F8, bool Inter>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, AppendArgs a, int run) {
     constexpr int D = S * 16;
     let_next_begin();
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, A
             const bool turned = at.fa >= 0;
             float x[16];
             if (turned || F8) unpack16(va[i], vb[i], x);
-            if (turned) turn16(x, co, si, r.interleaved != 0);
+            if (turned) turn16(x, co, si, Inter);
             const int64_t kv = (slot * a.Hkv + g) * D;
             if (F8 && !is_q) {
                 quantise16<S>(x, at, s, (is_v ? a.v_codes : a.k_codes) + kv,
@@ -303,7 +303,8 @@ cudaError_t append(const RopeArgs &r, const AppendArgs &a, cudaStream_t st) {
     const int64_t threads = (int64_t)a.N * S;
     const int run = run_of(threads, heads);
     const dim3 grid((unsigned)((threads + kRopeThreads - 1) / kRopeThreads), (heads + run - 1) / run);
-    return launch_dependent(rope_append_kernel<S, F8>, grid, kRopeThreads, 0, st, r, a, run);
+    return launch_dependent(r.interleaved ? rope_append_kernel<S, F8, true> : rope_append_kernel<S, F8, false>, grid, kRopeThreads,
+                            0, st, r, a, run);
 }
 
 }  // namespace
@@ -312,7 +313,7 @@ cudaError_t launch_rope(const RopeArgs &r, const RopeRows &a, cudaStream_t st) {
     const int64_t threads = (int64_t)a.N * (r.D >> 4);
     const int run = run_of(threads, a.H);
     const dim3 grid((unsigned)((threads + kRopeThreads - 1) / kRopeThreads), (a.H + run - 1) / run);
-    return launch_dependent(rope_kernel, grid, kRopeThreads, 0, st, r, a, run);
+    return launch_dependent(r.interleaved ? rope_kernel<true> : rope_kernel<false>, grid, kRopeThreads, 0, st, r, a, run);
 }
 
 cudaError_t launch_rope_append(const RopeArgs &r, const AppendArgs &a, cudaStream_t st) {
