@@ -197,6 +197,7 @@ qsa_status rope_append(const char *call, const qsa_paged_config *cfg, const qsa_
     QSA_TRY(check_rows(call, "v", a.v, a.v_ld, kv_width));
     QSA_NEED(call, a.pos && a.table && (phase != nullptr || rope->rot_dim == 0), "NULL tensor pointer");
     QSA_NEED(call, aligned(phase, 16), "phase must be 16-byte aligned");
+    QSA_NEED(call, aligned(a.pos, 4) && aligned(a.seq, 4) && aligned(a.table, 4), "pos, seq and table must be 4-byte aligned");
     if (fp8) {
         QSA_NEED(call, a.k_codes && a.v_codes && a.k_scales && a.v_scales, "NULL tensor pointer");
         QSA_NEED(call, aligned(a.k_codes, 16) && aligned(a.v_codes, 16) && aligned(a.k_scales, 8) && aligned(a.v_scales, 8),
@@ -221,6 +222,8 @@ qsa_status paged_decode(const char *call, const qsa_paged_config *cfg, PagedArgs
     QSA_NEED(call, aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.out, 16),
              "the K/V rows and out must be 16-byte aligned");
     QSA_NEED(call, !fp8 || (aligned(a.k_scales, 8) && aligned(a.v_scales, 8)), "scales must be 8-byte aligned");
+    QSA_NEED(call, aligned(a.table, 4) && aligned(a.seq_len, 4) && aligned(a.lse, 4),
+             "table, seq_len and lse must be 4-byte aligned");
     QSA_NEED(call, device_accessible(a.k) && device_accessible(a.v) &&
                  (!fp8 || (device_accessible(a.k_scales) && device_accessible(a.v_scales))),
              "the K/V rows (and their scales) must be device memory or mapped pinned host memory");
@@ -356,6 +359,11 @@ QSA_API qsa_status qsa_fork_pages(int32_t page_size, const int32_t *parent, cons
     QSA_NEED(call, table == nullptr || table_out != table, "table_out must be another array than table");
     QSA_NEED(call, seq_len == nullptr || seq_len_out != seq_len, "seq_len_out must be another array than seq_len");
     QSA_NEED(call, ref == nullptr || ref_out != ref, "ref_out must be another array than ref");
+    for (const void *p : {static_cast<const void *>(parent), static_cast<const void *>(add), static_cast<const void *>(table),
+                          static_cast<const void *>(seq_len), static_cast<const void *>(ref),
+                          static_cast<const void *>(table_out), static_cast<const void *>(seq_len_out),
+                          static_cast<const void *>(ref_out)})
+        QSA_NEED(call, aligned(p, 4), "the int32 arrays must be 4-byte aligned");
     if (n_out == 0 && n_in == 0 && n_pages == 0) return host_ok();
     a.parent = parent, a.add = add, a.table = table, a.seq_len = seq_len, a.ref = ref;
     a.table_out = table_out, a.seq_len_out = seq_len_out, a.ref_out = ref_out;
@@ -380,6 +388,9 @@ QSA_API qsa_status qsa_compact_pages(int32_t page_size, const int32_t *table, co
     QSA_NEED(call, n_rows == 0 || (seq_len && ((table && table_out) || ld == 0)), "NULL tensor pointer");
     QSA_NEED(call, n_pages == 0 || (ref && ref_out), "NULL tensor pointer");
     QSA_NEED(call, ref == nullptr || ref_out != ref, "ref_out must be another array than ref");
+    for (const void *p : {static_cast<const void *>(table), static_cast<const void *>(seq_len), static_cast<const void *>(ref),
+                          static_cast<const void *>(table_out), static_cast<const void *>(ref_out)})
+        QSA_NEED(call, aligned(p, 4), "the int32 arrays must be 4-byte aligned");
     a.table = table, a.seq_len = seq_len, a.ref = ref, a.table_out = table_out, a.ref_out = ref_out;
     a.n_rows = n_rows, a.page_size = page_size, a.n_pages = (int32_t)n_pages, a.ld = ld;
     a.hdr = static_cast<WsHeader *>(ws);
@@ -397,6 +408,7 @@ QSA_API qsa_status qsa_copy_pages(const int32_t *src, const int32_t *dst, int32_
     QSA_TRY(check_workspace(call, ws, ws_bytes, kWsHeaderBytes));
     if (n == 0 || n_groups == 0) return host_ok();
     QSA_NEED(call, src && dst, "NULL tensor pointer");
+    QSA_NEED(call, aligned(src, 4) && aligned(dst, 4), "src and dst must be 4-byte aligned");
     for (int i = 0; i < n_groups; ++i)
         QSA_NEED(call, device_accessible(planes[i].base) && (!dst_planes || device_accessible(dst_planes[i].base)),
                  "planes[%d] must be device memory or mapped pinned host memory", i);

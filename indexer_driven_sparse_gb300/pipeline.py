@@ -240,7 +240,8 @@ class PagedCache:
 
     A decode step is ``extend`` (room for the new tokens), then per layer ``append`` and ``attend``; ``fork``
     lets rows continue other rows (beams, shared prompts) or gives their pages back, and ``compact`` moves
-    the live pages to the front of the pool. Nothing here synchronises; ``status`` does."""
+    the live pages to the front of the pool. Nothing here synchronises; ``status`` does. ``fork`` and ``compact``
+    write beside what they read and then change over: a captured CUDA graph holds an even number of each."""
 
     def __init__(self, n_layers: int, n_pages: int, page_size: int, n_rows: int, max_pages: int, n_q_heads: int,
                  n_kv_heads: int, head_dim: int = 256, fp8: bool = False, softmax_scale: float = 0.0, window: int = 0,

@@ -657,3 +657,145 @@ def test_a_decode_loop_with_beams_and_compaction(cuda_lib, fp8):
     cache.fork(ints([-1] * rows), ints([0] * rows))
     assert not cache.ref.any() and cache.seq_len.tolist() == [0] * rows
     assert cache.status() == ((0, 0), (0, 0))
+
+
+def test_captured_decode_steps_replay(cuda_lib):
+    """Two decode steps (the bookkeeping alternates between two sets of arrays) captured with their forks, appends
+    and attention; replays continue the sequences as eager steps do. Another stream, and a kernel of another
+    kind right before and behind."""
+    page, Hq, Hkv, D, rows = 4, 4, 2, 64, 3
+    rope = qb.rope_table(D)
+
+    def build():
+        c = PagedCache(1, 40, page, rows, 8, Hq, Hkv, D)
+        c.fork(ints([-1] * rows), ints([3, 0, 9]))
+        return c
+
+    fused = torch.empty(rows, Hq + 2 * Hkv, D, dtype=torch.bfloat16, device=DEV)
+    q_out = torch.empty(rows, Hq, D, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(q_out)
+    source = randn((rows, Hq + 2 * Hkv, D), 5)
+    grow = torch.ones(1, dtype=torch.bfloat16, device=DEV)
+    parents = [ints([0, 0, 2]), ints([1, 1, 2])]
+
+    def step(c, parent):
+        torch.mul(source, grow, out=fused)                # what the attention input's producer would be
+        grow.mul_(1.5)
+        c.fork(parent, ints_one)
+        c.append(0, rope, fused[:, :Hq], fused[:, Hq:Hq + Hkv], fused[:, Hq + Hkv:], last(c), None, q_out)
+        c.attend(0, q_out, out)
+        return out
+
+    ints_one = ints([1] * rows)
+    pos = torch.empty(rows, dtype=torch.int32, device=DEV)
+
+    def last(c):
+        torch.sub(c.seq_len, 1, out=pos)
+        return pos
+
+    eager = build()
+    want = []
+    for i in range(8):
+        want.append(step(eager, parents[i % 2]).clone())
+    grow.fill_(1.0)
+    cache = build()
+    keep = torch.zeros(2, *out.shape, dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        for i in range(2):
+            keep[i].copy_(step(cache, parents[i]))
+    for i in range(4):
+        with torch.cuda.stream(side):
+            g.replay()
+        side.synchronize()
+        assert torch.equal(keep[0], want[2 * i]) and torch.equal(keep[1], want[2 * i + 1]), i
+    assert torch.equal(cache.table, eager.table) and torch.equal(cache.ref, eager.ref)
+    assert torch.equal(cache.seq_len, eager.seq_len) and cache.status() == ((0, 0), (0, 0))
+
+
+def test_calls_take_a_stream(cuda_lib):
+    side = torch.cuda.Stream()
+    x = randn((5, 2, 128), 1)
+    pos = ints([1, 2, 3, 4, 5])
+    rope = qb.rope_table(128)
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    qb.qsa_rope(rope, x, pos, a)
+    torch.cuda.synchronize()
+    qb.qsa_rope(rope, x, pos, b, stream=side)
+    qb.qsa_rope(rope, b, -pos, b, stream=side.cuda_stream)
+    side.synchronize()
+    again = torch.empty_like(x)
+    qb.qsa_rope(rope, a, -pos, again)
+    assert torch.equal(b, again)
+    q, planes, values, tab, table = paged_inputs([70, 3], 8, 2, 128, 16, False, seed=3)
+    cfg = qb.make_paged_config(8, 2, 128, 16)
+    ws = qb.paged_workspace(cfg)
+    torch.cuda.synchronize()
+    out, lse = torch.empty_like(q), torch.empty(2, 8, device=DEV)
+    lens = ints([70, 3])
+    torch.cuda.synchronize()
+    run_decode(cfg, q, planes, tab, lens, ws, out, lse, stream=side)
+    side.synchronize()
+    check_decode(out, lse, q, values, table, [70, 3], 16, 0, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_far_slots_of_a_large_cache(cuda_lib, fp8):
+    """Rows whose byte offsets pass 2^32 (and 2^33 with bf16 rows): appended, attended, copied and compacted."""
+    page, Hkv, D = 64, 8, 128
+    row = D if fp8 else 2 * D
+    n_pages = (5 << 30) // (page * Hkv * row)             # 5 GB a plane
+    shape = (n_pages, page, Hkv, D)
+    if fp8:
+        pool = [torch.empty(shape, dtype=torch.uint8, device=DEV), torch.empty(shape[:3] + (1,), device=DEV),
+                torch.empty(shape, dtype=torch.uint8, device=DEV), torch.empty(shape[:3] + (1,), device=DEV)]
+    else:
+        pool = [torch.empty(shape, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    cfg = qb.make_paged_config(16, Hkv, D, page)
+    ws = qb.paged_workspace(cfg)
+    n = 3 * page - 5
+    table = ints([[n_pages - 1, n_pages // 2 + 7, n_pages - 3]])
+    fused = randn((n, 16 + 2 * Hkv, D), 8)
+    q_out = torch.empty(n, 16, D, dtype=torch.bfloat16, device=DEV)
+    rope = qb.rope_table(D)
+    args = (cfg, rope, fused[:, :16], fused[:, 16:16 + Hkv], fused[:, 16 + Hkv:],
+            torch.arange(n, dtype=torch.int32, device=DEV), torch.zeros(n, dtype=torch.int32, device=DEV), q_out)
+    q = q_out[-1:]
+
+    def attend(planes, tab):
+        return run_decode(cfg, q, planes, tab, ints([n]), ws)
+
+    if fp8:
+        qb.qsa_rope_append_fp8kv(*args, pool, table, ws)
+        small = [p[table[0].long()].contiguous() for p in pool]
+    else:
+        qb.qsa_rope_append(*args, *pool, table, ws)
+        small = [p[table[0].long()].contiguous() for p in pool]
+    out, lse = attend(pool, table)
+    near, near_lse = attend(small, ints([[0, 1, 2]]))
+    assert torch.equal(out, near) and torch.equal(lse, near_lse)
+    freq, amp = P.rope_frequencies(D, 1e4)
+    K = P.rope(f64(fused[:, 16:16 + Hkv]), np.arange(n), freq, amp, 0, False)
+    want = P.decode(f64(q[0]), K, f64(fused[:, 16 + Hkv:]), 0, D ** -0.5)[0]
+    assert np.abs(f64(out[0]) - want).max() <= (0.25 if fp8 else 0.03)
+    # the page calls over the same planes
+    planes = [p[None] for p in pool]
+    pws = qb.pages_workspace(2, n_pages)
+    ref = torch.zeros(n_pages, dtype=torch.int32, device=DEV)
+    ref[table[0].long()] = 1
+    t2, r2 = torch.empty_like(table), torch.empty_like(ref)
+    qb.qsa_compact_pages(page, table, ints([n]), ref, t2, r2, planes, pws)
+    assert t2.tolist() == [[2, 0, 1]]
+    out, lse = attend(pool, t2)
+    assert torch.equal(out, near)
+    t3, l3, r3 = torch.empty(2, 3, dtype=torch.int32, device=DEV), ints([0, 0]), torch.empty_like(ref)
+    qb.qsa_fork_pages(page, ints([0, 0]), ints([0, 0]), t2, ints([n]), r2, t3, l3, r3, planes, pws)
+    assert t3.tolist() == [[2, 0, 1], [2, 0, 3]]
+    out, lse = attend(pool, t3[1:])
+    assert torch.equal(out, near)
+    qb.qsa_copy_pages(t3[1], ints([n_pages - 2, 5, n_pages - 9]), planes, pws)
+    out, lse = attend(pool, ints([[n_pages - 2, 5, n_pages - 9]]))
+    assert torch.equal(out, near)
+    assert status(ws) == (0, 0) and status(pws) == (0, 0)

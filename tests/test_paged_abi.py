@@ -114,7 +114,8 @@ def test_paged_decode_refusals(lib):
     assert decode(lib, cfg, B=0) == qb.QSA_OK
     for kw in (dict(cfg=None), dict(B=-1), dict(B=65536), dict(q=0), dict(q=FAKE + 8), dict(q_ld=1016), dict(q_ld=1028),
                dict(k=0), dict(v=0), dict(k=FAKE + 8), dict(v=FAKE + 2), dict(table=0), dict(lens=0), dict(out=0),
-               dict(out=FAKE + 4), dict(pages=-1), dict(ld=-1), dict(ws=0), dict(ws=FAKE + 16)):
+               dict(out=FAKE + 4), dict(pages=-1), dict(ld=-1), dict(ws=0), dict(ws=FAKE + 16), dict(table=FAKE + 2),
+               dict(lens=FAKE + 1)):
         assert decode(lib, kw.pop("cfg", cfg), **kw) == BAD, kw
     assert decode(lib, cfg, bytes=255) == SMALL
     assert decode(lib, cfg, pages=1 << 28) == UNSUPPORTED
@@ -140,7 +141,7 @@ def test_rope_append_refusals(lib):
     for kw in (dict(cfg=None), dict(rope=None), dict(rope=rope_cfg(head_dim=256)), dict(n=-1), dict(rows=-1),
                dict(q=FAKE + 8), dict(q_ld=8), dict(q_out=0), dict(q_out=FAKE, q_out_ld=1032), dict(k=0), dict(k_ld=248),
                dict(v=0), dict(v=FAKE + 2), dict(v_ld=260), dict(pos=0), dict(table=0), dict(phase=0), dict(phase=FAKE + 8), dict(kc=0),
-               dict(vc=0), dict(kc=FAKE + 8), dict(ws=0), dict(ws=FAKE + 128), dict(pages=-1), dict(ld=-1)):
+               dict(vc=0), dict(kc=FAKE + 8), dict(ws=0), dict(ws=FAKE + 128), dict(pages=-1), dict(ld=-1), dict(pos=FAKE + 2), dict(table=FAKE + 1)):
         assert call(**kw) == BAD, kw
     for kw in (dict(ks=0), dict(vs=0), dict(ks=FAKE + 4), dict(kc=FAKE + 8)):
         assert call(fp8=True, **kw) == BAD, kw
@@ -169,7 +170,7 @@ def test_page_calls_refusals(lib):
                   dict(groups=planes(page_bytes=-16)), dict(groups=planes(page_bytes=36, base=FAKE + 2))]
     for kw in [dict(ps=0), dict(parent=0), dict(add=0), dict(n_out=-1), dict(n_out=65537), dict(n_in=65537), dict(table=0),
                dict(lens=0), dict(ld=-1), dict(ref=0), dict(pages=-1), dict(t_out=0), dict(t_out=FAKE), dict(l_out=0),
-               dict(l_out=FAKE), dict(r_out=0), dict(r_out=FAKE), dict(ws=0), dict(ws=FAKE + 64)] + bad_groups:
+               dict(l_out=FAKE), dict(r_out=0), dict(r_out=FAKE), dict(parent=FAKE + 2), dict(r_out=FAKE + 1), dict(ws=0), dict(ws=FAKE + 64)] + bad_groups:
         assert fork(**kw) == BAD, kw
     for kw in [dict(ps=0), dict(table=0), dict(lens=0), dict(rows=-1), dict(rows=65537), dict(ld=-1), dict(ref=0),
                dict(pages=-1), dict(t_out=0), dict(r_out=0), dict(r_out=FAKE), dict(ws=0)] + bad_groups:
@@ -184,7 +185,7 @@ def test_page_calls_refusals(lib):
         return lib.qsa_copy_pages(src, dst, n, planes() if groups is None else groups, 9, to, 9, count, ws, bytes, None)
 
     assert copy(n=0) == qb.QSA_OK and copy(count=0) == qb.QSA_OK
-    for kw in [dict(src=0), dict(dst=0), dict(n=-1), dict(ws=0), dict(to=planes(n_planes=3)), dict(to=planes(page_bytes=32)),
+    for kw in [dict(src=0), dict(dst=0), dict(src=FAKE + 2), dict(n=-1), dict(ws=0), dict(to=planes(n_planes=3)), dict(to=planes(page_bytes=32)),
                dict(count=9)] + [dict(groups=g["groups"]) for g in bad_groups if "groups" in g]:
         assert copy(**kw) == BAD, kw
     assert copy(bytes=100) == SMALL
