@@ -8,8 +8,8 @@ namespace qsa {
 constexpr int kWhereAppend = 9, kWherePaged = 10, kWherePages = 11;
 
 // Programmatic dependent launch: a kernel launched by launch_dependent may begin while the kernel before it on the
-// stream ends; it waits for that one's memory before its first access and lets the next one begin. Every kernel here
-// does both at its start, so each still follows all that came before it.
+// stream ends; it waits for that one's memory before its first access. Every kernel here does that at its start, so
+// each still follows all that came before it; the short streaming ones also let the next one begin at once.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -70,6 +70,23 @@ constexpr int max_ctas(int D) { return D == 256 ? 160 : D == 128 ? 480 : 640; }
 
 __host__ __device__ inline int ranges_for(int ctas, int Hkv) { return ctas / Hkv > 0 ? ctas / Hkv : 1; }
 
+// total tiles cut into R ranges: range r begins at floor(total r / R). In 32 bits where they suffice: a 64-bit
+// division takes a quarter of a microsecond of a kernel whose shortest calls take three.
+struct Ranges {
+    long long total, each;
+    int R, rest;
+    __device__ __forceinline__ Ranges(long long total_, int R_) : total(total_), R(R_) {
+        each = total >> 32 ? total / R : (uint32_t)total / (uint32_t)R;
+        rest = (int)(total - each * R);
+    }
+    __device__ __forceinline__ long long begin(int r) const { return each * r + (uint32_t)(rest * r) / (uint32_t)R; }
+    // The range that holds tile x: the last r with begin(r) <= x, so total r < (x + 1) R.
+    __device__ __forceinline__ int of(long long x) const {
+        const long long y = (x + 1) * R - 1;
+        return y >> 32 ? (int)(y / total) : (int)((uint32_t)y / (uint32_t)total);
+    }
+};
+
 struct Row {
     int len, lo, t0, t1;    // tokens, first attended token, tiles [t0, t1)
 };
@@ -237,6 +254,9 @@ __device__ __forceinline__ const char *row_ptr(const char *base, int index, uint
     return base + (uint64_t)(uint32_t)index * bytes;
 }
 
+// Neither this kernel nor the join lets the next one begin early: join CTAs that wait beside it cost a call of 4,096
+// tokens 0.7 us of 7.8, and a tile kernel whose CTAs find no room beside what still runs does not run in one wave, which
+// its equal ranges are made for.
 template <typename C>
 __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedArgs a, PagedScratch ws, int ranges) {
     constexpr int D = C::D, GT = C::GT, W = C::warps, T = C::tile, TW = C::warp_tok, NS = C::stages, SG = C::groups;
@@ -251,7 +271,6 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     const int g = lane >> 2, c = lane & 3;
     const int range = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv;
     const int Hkv = a.Hkv, G = a.G;
-    let_next_begin();
     wait_for_previous();
 
     // ---- this range's tiles: total over the batch, then the row and tile the range starts at
@@ -276,7 +295,8 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
         total += scan[w];
     }
     const int R = (int)min((long long)ranges, max(total, 1ll));
-    const long long x0 = range < R ? total * range / R : 0, x1 = range < R ? total * (range + 1) / R : 0;
+    const Ranges cut(total, R);
+    const long long x0 = range < R ? cut.begin(range) : 0, x1 = range < R ? cut.begin(range + 1) : 0;
     if (x0 < x1 && upto - mine <= x0 && x0 < upto) {
         long long at = upto - mine;
         int s = s_lo;
@@ -698,7 +718,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
             if (begins && !ends && kvh == 0 && tid == 0) {
                 // the sequence's last tile is number `end` of the list: how many ranges it spans
                 const long long end = x0 + i + (at.r.t1 - 1 - at.t);
-                ws.meta[range] = make_int2(at.s, (int)(((end + 1) * R - 1) / total) - range + 1);
+                ws.meta[range] = make_int2(at.s, cut.of(end) - range + 1);
             }
             begins = first = true;
         }
@@ -706,23 +726,44 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     }
 }
 
-// The partials of a sequence that range `blockIdx.x` starts and leaves unfinished, joined for one head:
-// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. Thread (row, 4 dims) takes every rows-th partial, its (m, l)
-// and O loaded together and merged with a running maximum; then the rows of threads are merged in order. The time is
-// that of two dependent loads (which partials, the partials).
+// The partials of the sequences that a range starts and leaves unfinished, joined:
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. CTA (y, head) takes the y-th such range (there are at most as many
+// as sequences). Thread (row, 4 dims) takes every rows-th partial, its (m, l) and O loaded together and merged with a
+// running maximum; then the rows of threads are merged in order. The time is that of two dependent loads.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedArgs a, PagedScratch ws) {
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedArgs a, PagedScratch ws, int ranges) {
     constexpr int cols = D / 4, rows = kJoinThreads / cols, U = D == 256 ? 8 : 4;
     __shared__ float4 acc[kJoinThreads];
     __shared__ float2 pair[rows];
-    const int range = blockIdx.x, head = blockIdx.y, tid = threadIdx.x, col = tid % cols, row = tid / cols;
-    let_next_begin();
+    __shared__ int4 job_sh;                                                 // range, sequence, partials
+    const int head = blockIdx.y, tid = threadIdx.x, col = tid % cols, row = tid / cols;
     wait_for_previous();
-    const int2 meta = ws.meta[range];
-    if (meta.x < 0) return;
+    if (tid < 32) {
+        if (tid == 0) job_sh.x = -1;
+        __syncwarp();
+        int n = 0;
+        for (int r0 = 0; r0 < ranges - 1; r0 += 32 * 8) {
+            int2 meta[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = r0 + 32 * k + tid;
+                meta[k] = r < ranges - 1 ? __ldcg(ws.meta + r) : make_int2(-1, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t some = __ballot_sync(0xffffffffu, meta[k].x >= 0);
+                if (meta[k].x >= 0 && n + __popc(some & ((1u << tid) - 1u)) == (int)blockIdx.x)
+                    job_sh = make_int4(r0 + 32 * k + tid, meta[k].x, meta[k].y, 0);
+                n += __popc(some);
+            }
+        }
+    }
+    __syncthreads();
+    const int4 job = job_sh;
+    if (job.x < 0) return;
     float m, l;
     float4 x;
-    join_parts<D, U>(a, ws, range, meta.y, head, col, row, rows, m, l, x);
+    join_parts<D, U>(a, ws, job.x, job.z, head, col, row, rows, m, l, x);
     acc[tid] = x;
     if (col == 0) pair[row] = make_float2(m, l);
     __syncthreads();
@@ -740,7 +781,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedArgs a, P
         sum = fmaf(w, pair[i].y, sum);
         x.x = fmaf(w, v.x, x.x), x.y = fmaf(w, v.y, x.y), x.z = fmaf(w, v.z, x.z), x.w = fmaf(w, v.w, x.w);
     }
-    write_joined<D>(a, meta.x, head, col, top, sum, x);
+    write_joined<D>(a, job.y, head, col, top, sum, x);
 }
 
 // CTAs of one wave on the current device (cached per device; 0 on an error).
@@ -783,7 +824,7 @@ cudaError_t launch(const PagedArgs &a, cudaStream_t st) {
     b.tile_rest = C::tile % a.page_size;
     const cudaError_t e = launch_dependent(paged_tile_kernel<C>, dim3(ranges * a.Hkv), C::threads, C::smem, st, b, ws, ranges);
     if (e != cudaSuccess || ranges == 1) return e;      // one range cuts no sequence
-    return launch_dependent(paged_join_kernel<C::D>, dim3(ranges - 1, a.Hq), kJoinThreads, 0, st, a, ws);
+    return launch_dependent(paged_join_kernel<C::D>, dim3(std::min(ranges - 1, a.B), a.Hq), kJoinThreads, 0, st, a, ws, ranges);
 }
 
 template <int D, bool F8>
