@@ -625,7 +625,7 @@ QSA_API qsa_status qsa_paged_decode_fp8kv(const qsa_paged_config *cfg, const qsa
 
 /* Planes of a pool that move together: n_planes arrays [n_pages][page_bytes], plane_stride bytes apart (e.g.
  * the K caches of all layers). page_bytes a multiple of 4, plane_stride of page_bytes's alignment (16 where
- * page_bytes is a multiple of 16, else 4), bases aligned likewise. */
+ * page_bytes is a multiple of 16, else 4), bases aligned likewise; device memory or mapped pinned host memory. */
 typedef struct {
     void *base;
     int64_t plane_stride;

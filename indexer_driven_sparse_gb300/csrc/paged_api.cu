@@ -206,6 +206,10 @@ qsa_status rope_append(const char *call, const qsa_paged_config *cfg, const qsa_
         QSA_NEED(call, a.k_cache && a.v_cache, "NULL tensor pointer");
         QSA_NEED(call, aligned(a.k_cache, 16) && aligned(a.v_cache, 16), "k_cache and v_cache must be 16-byte aligned");
     }
+    QSA_NEED(call, fp8 ? device_accessible(a.k_codes) && device_accessible(a.v_codes) && device_accessible(a.k_scales) &&
+                             device_accessible(a.v_scales)
+                       : device_accessible(a.k_cache) && device_accessible(a.v_cache),
+             "the K/V rows (and their scales) must be device memory or mapped pinned host memory");
     return launched(launch_rope_append(rope_args(rope, phase, amplitude), a, static_cast<cudaStream_t>(stream)), call);
 }
 
@@ -267,6 +271,13 @@ qsa_status plane_groups(const char *call, const qsa_page_planes *from, const qsa
         g.n_planes = s.n_planes;
         g.wide = word == 16;
     }
+    return QSA_OK;
+}
+
+qsa_status check_planes_memory(const char *call, const PlaneGroups &p) {
+    for (int i = 0; i < p.n; ++i)
+        QSA_NEED(call, device_accessible(p.g[i].src) && (p.g[i].src == p.g[i].dst || device_accessible(p.g[i].dst)),
+                 "planes[%d] must be device memory or mapped pinned host memory", i);
     return QSA_OK;
 }
 
@@ -365,6 +376,7 @@ QSA_API qsa_status qsa_fork_pages(int32_t page_size, const int32_t *parent, cons
                           static_cast<const void *>(ref_out)})
         QSA_NEED(call, aligned(p, 4), "the int32 arrays must be 4-byte aligned");
     if (n_out == 0 && n_in == 0 && n_pages == 0) return host_ok();
+    QSA_TRY(check_planes_memory(call, groups));
     a.parent = parent, a.add = add, a.table = table, a.seq_len = seq_len, a.ref = ref;
     a.table_out = table_out, a.seq_len_out = seq_len_out, a.ref_out = ref_out;
     a.n_out = n_out, a.n_in = n_in, a.page_size = page_size, a.n_pages = (int32_t)n_pages, a.ld = ld;
@@ -391,6 +403,7 @@ QSA_API qsa_status qsa_compact_pages(int32_t page_size, const int32_t *table, co
     for (const void *p : {static_cast<const void *>(table), static_cast<const void *>(seq_len), static_cast<const void *>(ref),
                           static_cast<const void *>(table_out), static_cast<const void *>(ref_out)})
         QSA_NEED(call, aligned(p, 4), "the int32 arrays must be 4-byte aligned");
+    QSA_TRY(check_planes_memory(call, groups));
     a.table = table, a.seq_len = seq_len, a.ref = ref, a.table_out = table_out, a.ref_out = ref_out;
     a.n_rows = n_rows, a.page_size = page_size, a.n_pages = (int32_t)n_pages, a.ld = ld;
     a.hdr = static_cast<WsHeader *>(ws);
@@ -409,9 +422,7 @@ QSA_API qsa_status qsa_copy_pages(const int32_t *src, const int32_t *dst, int32_
     if (n == 0 || n_groups == 0) return host_ok();
     QSA_NEED(call, src && dst, "NULL tensor pointer");
     QSA_NEED(call, aligned(src, 4) && aligned(dst, 4), "src and dst must be 4-byte aligned");
-    for (int i = 0; i < n_groups; ++i)
-        QSA_NEED(call, device_accessible(planes[i].base) && (!dst_planes || device_accessible(dst_planes[i].base)),
-                 "planes[%d] must be device memory or mapped pinned host memory", i);
+    QSA_TRY(check_planes_memory(call, groups));
     return launched(launch_copy_pages(src, dst, n, groups, n_pages, dst_planes ? n_dst_pages : n_pages,
                                       static_cast<WsHeader *>(ws), static_cast<cudaStream_t>(stream)), call);
 }

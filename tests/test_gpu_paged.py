@@ -799,3 +799,79 @@ def test_far_slots_of_a_large_cache(cuda_lib, fp8):
     out, lse = attend(pool, ints([[n_pages - 2, 5, n_pages - 9]]))
     assert torch.equal(out, near)
     assert status(ws) == (0, 0) and status(pws) == (0, 0)
+
+
+def test_host_checks_reach_python(cuda_lib):
+    """A refused call raises with the library's text and launches nothing: misaligned rows, host memory that the
+    GPU cannot read, a workspace that is too small, arrays that must differ."""
+    rope = qb.rope_table(64)
+    x = torch.zeros(3 * 2 * 64 + 8, dtype=torch.bfloat16, device=DEV)
+    pos = ints([0, 1, 2])
+
+    def refused(text, fn, *args, **kw):
+        with pytest.raises(qb.QsaError, match=text) as e:
+            fn(*args, **kw)
+        assert e.value.status in (qb.QSA_ERR_INVALID_ARGUMENT, qb.QSA_ERR_WORKSPACE_TOO_SMALL)
+
+    off = x[4:4 + 384].view(3, 2, 64)
+    refused("x must be 16-byte aligned", qb.qsa_rope, rope, off, pos, x[:384].view(3, 2, 64))
+    q, planes, values, tab, table = paged_inputs([30, 3], 8, 2, 128, 16, False, seed=2)
+    cfg = qb.make_paged_config(8, 2, 128, 16)
+    ws = qb.paged_workspace(cfg)
+    out = torch.empty_like(q)
+    pageable = [p.cpu() for p in planes]
+    lens = ints([30, 3])
+    refused("pinned", qb.qsa_paged_decode, cfg, q, *pageable, tab, lens, out, None, ws)
+    refused("workspace", qb.qsa_paged_decode, cfg, q, *planes, tab, lens, out, None, ws[:256])
+    r128 = qb.rope_table(128)
+    kv = torch.zeros(2, 4, 128, dtype=torch.bfloat16, device=DEV)
+    refused("pinned", qb.qsa_rope_append, cfg, r128, None, kv[:, :2], kv[:, 2:], ints([0, 1]), None, None, *pageable, tab, ws)
+    refused("head_dim", qb.qsa_rope_append, cfg, rope, None, kv[:, :2], kv[:, 2:], ints([0, 1]), None, None, *planes, tab, ws)
+    n = planes[0].shape[0]
+    pws = qb.pages_workspace(2, n)
+    ref, out_ref, t2, l2 = ints([1] * n), ints([0] * n), torch.zeros_like(tab), ints([0, 0])
+    host = [pageable[0][None]]
+    refused("pinned", qb.qsa_fork_pages, 16, ints([0, 1]), ints([1, 1]), tab, lens, ref, t2, l2, out_ref, host, pws)
+    refused("another array", qb.qsa_fork_pages, 16, ints([0, 1]), ints([1, 1]), tab, lens, ref, tab, l2, out_ref, [], pws)
+    refused("another array", qb.qsa_compact_pages, 16, tab, lens, ref, t2, ref, [], pws)
+    refused("pinned", qb.qsa_compact_pages, 16, tab, lens, ref, t2, out_ref, host, pws)
+    refused("pinned", qb.qsa_copy_pages, ints([0]), ints([1]), host, pws)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        qb.qsa_rope(rope, x[:384].view(3, 2, 64), pos.cpu(), x[:384].view(3, 2, 64))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(160, 160, 256), (620, 310, 128), (700, 700, 64)])
+def test_decode_with_more_kv_heads_than_one_wave(cuda_lib, Hq, Hkv, D):
+    lens = [70, 0, 5, 129]
+    q, planes, values, tab, table = paged_inputs(lens, Hq, Hkv, D, 16, False, seed=13)
+    cfg = qb.make_paged_config(Hq, Hkv, D, 16)
+    ws = qb.paged_workspace(cfg)
+    out, lse = run_decode(cfg, q, planes, tab, ints(lens), ws)
+    check_decode(out, lse, q, values, table, lens, 16, 0, D ** -0.5)
+
+
+def test_workspace_shared_by_other_geometries(cuda_lib):
+    """One allocation, large enough for all, used in turn by batches of other sizes, heads and row types, with other
+    calls of the library writing over it in between: nothing of a call is left for the next."""
+    big = max((qb.paged_workspace(qb.make_paged_config(h, k, d, 16)) for h, k, d in
+               ((16, 2, 256), (32, 8, 128), (8, 8, 64))), key=lambda t: t.numel())
+    cases = []
+    for seed, (Hq, Hkv, D, fp8, lens) in enumerate([(16, 2, 256, False, [3000, 5, 0]), (32, 8, 128, True, [40] * 70),
+                                                    (8, 8, 64, False, [9000]), (16, 2, 256, True, [1, 2, 3, 700])]):
+        cases.append((Hq, Hkv, D, fp8, lens, *paged_inputs(lens, Hq, Hkv, D, 16, fp8, seed=70 + seed)))
+    for turn in range(2):
+        for Hq, Hkv, D, fp8, lens, q, planes, values, tab, table in cases:
+            big[256:].fill_(0xFF if turn else 0x7F)       # what another operator's scratch may look like
+            cfg = qb.make_paged_config(Hq, Hkv, D, 16)
+            out, lse = run_decode(cfg, q, planes, tab, ints(lens), big)
+            check_decode(out, lse, q, values, table, lens, 16, 0, D ** -0.5, fp8)
+    pws = qb.pages_workspace(300, 2000)
+    for S, spare in ((300, 900), (8, 30), (40, 200)):
+        pws[256:].fill_(0xFF)
+        table, lens, ref = random_pool(S, 8, 30, spare, seed=S)
+        want = P.fork(table, lens, ref, list(range(S)), [1] * S, 8)
+        t2, l2, r2 = torch.zeros(table.shape, dtype=torch.int32, device=DEV), ints([0] * S), ints([0] * len(ref))
+        qb.qsa_fork_pages(8, ints(list(range(S))), ints([1] * S), ints(table.tolist()), ints(lens.tolist()),
+                          ints(ref.tolist()), t2, l2, r2, [], pws)
+        assert np.array_equal(t2.cpu().numpy(), want[0]) and np.array_equal(r2.cpu().numpy(), want[2])
+    assert status(big) == (0, 0) and status(pws) == (0, 0)
