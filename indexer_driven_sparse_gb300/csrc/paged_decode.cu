@@ -41,12 +41,18 @@ template <int D_, int GT_, bool F8_>
 struct PagedCfg {
     static constexpr int D = D_, GT = GT_;          // GT: head rows kept (8 or 16)
     static constexpr bool F8 = F8_;
-    static constexpr int warps = D / 32, threads = warps * 32;
+    static constexpr int warps = D / 32;            // that multiply
+    // that load; 0: those that multiply do. With 16 head rows these have enough to do: FP8 rows of 256 dims 125 us with
+    // loading warps, 142 without, 64 dims 108 and 114 (32 sequences of 20,000); with 8 rows 131 and 128, and a call of
+    // 4,096 tokens 7.5 and 7.3. At 128 dims the registers of more warps are not there.
+    static constexpr int loaders = GT == 8 || D == 128 ? 0 : D == 256 ? 4 : 2;
+    static constexpr int threads = (warps + loaders) * 32;
     static constexpr int tile = F8 ? 128 : 64;      // tokens
     static constexpr int row = D * (F8 ? 1 : 2);    // bytes of a K or V row
     static constexpr int chunks = row / 16;         // 16-byte chunks of a row
     static constexpr int rows_per_copy = 32 / chunks;
-    static constexpr int warp_tok = tile / warps;   // tokens a warp loads and scores
+    static constexpr int warp_tok = tile / warps;   // tokens a warp scores
+    static constexpr int load_warps = loaders ? loaders : warps, load_tok = tile / load_warps;   // tokens a warp loads
     static constexpr int groups = F8 ? D / 128 : 1; // scales of a row (FP8), sets of weights
     static constexpr int k_bytes = tile * row, s_bytes = F8 ? tile * groups * 4 : 0, q_bytes = GT * D * 2;
     static constexpr int stage = 2 * k_bytes + 2 * s_bytes;
@@ -249,6 +255,9 @@ __device__ __forceinline__ void write_joined(const PagedArgs &a, int s, int head
     if (col == 0 && a.lse) a.lse[(int64_t)s * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// The block's barrier, from more than one place in the code.
+__device__ __forceinline__ void sync_all() { asm volatile("bar.sync 0;" ::: "memory"); }
+
 // dst + index x bytes, index >= 0
 __device__ __forceinline__ const char *row_ptr(const char *base, int index, uint32_t bytes) {
     return base + (uint64_t)(uint32_t)index * bytes;
@@ -260,13 +269,14 @@ __device__ __forceinline__ const char *row_ptr(const char *base, int index, uint
 template <typename C>
 __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedArgs a, PagedScratch ws, int ranges) {
     constexpr int D = C::D, GT = C::GT, W = C::warps, T = C::tile, TW = C::warp_tok, NS = C::stages, SG = C::groups;
+    constexpr int LT = C::load_tok;
     constexpr bool F8 = C::F8;
     constexpr int HR = GT / 8;                     // head rows a lane holds: g and g + 8
     constexpr int NQ = TW / 8;                     // 8-token columns of the warp's scores
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long scan[W + 1];
+    __shared__ long long scan[W + C::loaders];
     __shared__ int start[2];
-    __shared__ uint32_t real_tok[NS][W];           // bit i: token i of the warp's share exists
+    __shared__ uint32_t real_tok[NS][C::load_warps];       // bit i: token i of the loading warp's share exists
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     const int range = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv;
@@ -290,7 +300,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     __syncthreads();
     long long total = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
+    for (int w = 0; w < W + C::loaders; ++w) {
         if (w < warp) upto += scan[w];
         total += scan[w];
     }
@@ -328,8 +338,9 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     in.at(a, start[0], start[1]);
     at = in;
 
-    // ---- loads. Lane i < TW keeps token i of the warp's share: its page's place in the table and offset in the page,
-    // stepped by a tile at a time, and the page id, fetched one tile ahead of the copies.
+    // ---- loads. Lane i < LT keeps token i of the loading warp's share: its page's place in the table and offset in the
+    // page, stepped by a tile at a time, and the page id, fetched one tile ahead of the copies.
+    const int lw = C::loaders ? warp - W : warp, lt = lw * 32 + lane;      // loading warp, thread among those that load
     const int chunk = lane % C::chunks;
     const uint32_t row_step = (uint32_t)Hkv * C::row;
     const char *k_rows = static_cast<const char *>(a.k) + kvh * C::row + chunk * 16;
@@ -337,7 +348,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     int entry, offset, page;
     bool wanted;
     auto fetch_page = [&](bool new_row) {
-        const int tok = in.t * T + warp * TW + lane;
+        const int tok = in.t * T + lw * LT + lane;
         if (new_row) {
             entry = tok / a.page_size;
             offset = tok - entry * a.page_size;
@@ -346,7 +357,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
             offset += a.tile_rest;
             if (offset >= a.page_size) offset -= a.page_size, ++entry;
         }
-        wanted = (TW == 32 || lane < TW) && tok >= in.r.lo && tok < in.r.len;
+        wanted = (LT == 32 || lane < LT) && tok >= in.r.lo && tok < in.r.len;
         page = wanted ? __ldg(a.table + in.s * a.ld + entry) : -1;
     };
     auto issue = [&](int stage, int q_slot, bool first) {      // tile `in`
@@ -355,27 +366,27 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
         if (wanted && !ok && kvh == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, in.s);
         const int slot = wanted && ok ? page * a.page_size + offset : -1;
         const uint32_t real = __ballot_sync(0xffffffffu, slot >= 0);
-        if (lane == 0) real_tok[stage][warp] = real;
+        if (lane == 0) real_tok[stage][lw] = real;
 #pragma unroll
-        for (int i = 0; i < TW / C::rows_per_copy; ++i) {
+        for (int i = 0; i < LT / C::rows_per_copy; ++i) {
             const int r = i * C::rows_per_copy + lane / C::chunks;
             const int sl = __shfl_sync(0xffffffffu, slot, r);
-            const int t = warp * TW + r;
+            const int t = lw * LT + r;
             const uint32_t to = st + t * C::row + ((chunk ^ (t & 7)) << 4);
             cp_async16_zfill(to, row_ptr(k_rows, max(sl, 0), row_step), sl >= 0);
             cp_async16_zfill(to + C::k_bytes, row_ptr(v_rows, max(sl, 0), row_step), sl >= 0);
         }
-        if (F8 && (TW == 32 || lane < TW)) {
+        if (F8 && (LT == 32 || lane < LT)) {
             constexpr int SB = SG * 4;
             const int64_t from = ((int64_t)max(slot, 0) * Hkv + kvh) * SG;
-            const uint32_t to = st + 2 * C::k_bytes + (warp * TW + lane) * SB;
+            const uint32_t to = st + 2 * C::k_bytes + (lw * LT + lane) * SB;
             cp_async_small_zfill<SB>(to, a.k_scales + from, slot >= 0);
             cp_async_small_zfill<SB>(to + C::s_bytes, a.v_scales + from, slot >= 0);
         }
         if (first) {                               // the row's queries, heads behind G as zeros
             const uint16_t *q = a.q + in.s * a.q_ld + (int64_t)kvh * G * D;
             const uint32_t to = base + C::q_at + q_slot * C::q_bytes;
-            for (int i = tid; i < GT * D / 8; i += C::threads) {
+            for (int i = lt; i < GT * D / 8; i += C::load_warps * 32) {
                 const int h = i / (D / 8), ch = i % (D / 8);
                 cp_async16_zfill(to + h * D * 2 + ((ch ^ (h & 7)) << 4), q + (h < G ? h * D + ch * 8 : 0), h < G);
             }
@@ -399,9 +410,23 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
         }
         cp_async_commit();
     };
-    fetch_page(true);
+    if (!C::loaders || warp >= W) {
+        fetch_page(true);
 #pragma unroll 1
-    for (int i = 0; i < NS - 1; ++i) advance();
+        for (int i = 0; i < NS - 1; ++i) advance();
+    }
+    if (C::loaders && warp >= W) {                 // the barriers of the loop below, and the loads between them
+        for (long long i = 0; i < n_tiles; ++i) {
+            cp_async_wait<NS - 2>();
+            sync_all();
+            sync_all();
+            advance();
+            sync_all();
+            if (at.t + 1 == at.r.t1 || i + 1 == n_tiles) sync_all();
+            if (i + 1 < n_tiles) at.next(a);
+        }
+        return;
+    }
 
     // ---- products
     constexpr int KS = D / 16;
@@ -415,8 +440,8 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     bool first = true;
     int stage = 0, q_slot = 0;
     for (long long i = 0; i < n_tiles; ++i, stage = stage + 1 == NS ? 0 : stage + 1) {
-        cp_async_wait<NS - 2>();
-        __syncthreads();                           // tile i is in; every warp has left tile i - 1
+        if (!C::loaders) cp_async_wait<NS - 2>();
+        sync_all();                                // tile i is in; every warp has left tile i - 1
         const uint32_t st = base + stage * C::stage;
         if (first) {
             const uint32_t qa = base + C::q_at + q_slot * C::q_bytes;
@@ -490,7 +515,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
         float lv[SG][NQ][2];                       // FP8: log2 of the tokens' V scales
         {
             constexpr int CH = F8 ? (NQ <= 2 ? 2 : 1) : 4 / NQ > 0 ? 4 / NQ : 1;   // independent sums (FP8: of each 128 dims)
-            const uint32_t real = real_tok[stage][warp];
+            const uint32_t real = real_tok[stage][warp * TW / LT] >> (warp * TW % LT);
 #pragma unroll
             for (int nt = 0; nt < NQ; ++nt) {
                 float acc[SG * CH][4];
@@ -561,8 +586,8 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                 top = quad_max(top);
                 if (c == 0) maxima[(gr * GT + g + 8 * h) * W + warp] = top;
             }
-        __syncthreads();
-        advance();
+        sync_all();
+        if (!C::loaders) advance();
         float alpha[HR];                           // of this warp's set
 #pragma unroll
         for (int gr = 0; gr < SG; ++gr)
@@ -609,7 +634,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
             o[n][0] *= alpha[0], o[n][1] *= alpha[0];
             if (HR == 2) o[n][2] *= alpha[HR - 1], o[n][3] *= alpha[HR - 1];
         }
-        __syncthreads();
+        sync_all();
         // O += P V over this warp's 32 dims
         const uint32_t vt = st + C::k_bytes + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::row;
         const uint32_t pt = base + C::p_at + (F8 ? my_set * GT * C::p_pitch : 0) +
@@ -671,7 +696,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                 l[h] = quad_sum(l[h]);
                 if (c == 0) maxima[(g + 8 * h) * W + warp] = l[h];
             }
-            __syncthreads();
+            sync_all();
 #pragma unroll
             for (int h = 0; h < HR; ++h) {
                 const int row = g + 8 * h;
