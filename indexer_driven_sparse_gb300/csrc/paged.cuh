@@ -72,6 +72,7 @@ struct PagedArgs {
     const int32_t *seq_len;
     int32_t B, Hq, Hkv, G, page_size, window;
     int32_t tile_entries, tile_rest;    // a tile's tokens / page_size and the remainder (set by the launcher)
+    int32_t page_shift;                 // log2 of page_size, -1: no power of two (set by the launcher)
     float scale_log2;
     uint16_t *out;
     float *lse;

@@ -34,7 +34,7 @@ namespace qsa {
 
 namespace {
 
-constexpr int kJoinThreads = 256;
+constexpr int kFewJoins = 152;           // CTAs of the join up to which they have 512 threads, one for each SM
 constexpr int kMaxRanges = 640;
 
 template <int D_, int GT_, bool F8_>
@@ -76,18 +76,22 @@ constexpr int max_ctas(int D) { return D == 256 ? 160 : D == 128 ? 480 : 640; }
 
 __host__ __device__ inline int ranges_for(int ctas, int Hkv) { return ctas / Hkv > 0 ? ctas / Hkv : 1; }
 
-// total tiles cut into R ranges: range r begins at floor(total r / R). In 32 bits where they suffice: a 64-bit
-// division takes a quarter of a microsecond of a kernel whose shortest calls take three.
+// total tiles cut into R ranges: range r begins at floor(total r / R). In 32 bits where they suffice, and without a
+// division where every range is one tile: a 64-bit division takes a quarter of a microsecond of a kernel whose shortest
+// calls take three.
 struct Ranges {
     long long total, each;
     int R, rest;
     __device__ __forceinline__ Ranges(long long total_, int R_) : total(total_), R(R_) {
-        each = total >> 32 ? total / R : (uint32_t)total / (uint32_t)R;
+        each = total == R ? 1 : total >> 32 ? total / R : (uint32_t)total / (uint32_t)R;
         rest = (int)(total - each * R);
     }
-    __device__ __forceinline__ long long begin(int r) const { return each * r + (uint32_t)(rest * r) / (uint32_t)R; }
+    __device__ __forceinline__ long long begin(int r) const {
+        return rest == 0 ? each * r : each * r + (uint32_t)(rest * r) / (uint32_t)R;
+    }
     // The range that holds tile x: the last r with begin(r) <= x, so total r < (x + 1) R.
     __device__ __forceinline__ int of(long long x) const {
+        if (total == R) return (int)x;
         const long long y = (x + 1) * R - 1;
         return y >> 32 ? (int)(y / total) : (int)((uint32_t)y / (uint32_t)total);
     }
@@ -291,10 +295,20 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
         mine += r.t1 - r.t0;
     }
     long long upto = mine;
+    if (a.B <= 32) {                               // at most 2^31 tiles, in the first warp
+        uint32_t u = (uint32_t)mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, u, o);
+            if (lane >= o) u += v;
+        }
+        upto = u;
+    } else {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
     }
     if (lane == 31) scan[warp] = upto;
     __syncthreads();
@@ -350,7 +364,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     auto fetch_page = [&](bool new_row) {
         const int tok = in.t * T + lw * LT + lane;
         if (new_row) {
-            entry = tok / a.page_size;
+            entry = a.page_shift >= 0 ? tok >> a.page_shift : tok / a.page_size;
             offset = tok - entry * a.page_size;
         } else {
             entry += a.tile_entries;
@@ -755,10 +769,10 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. CTA (y, head) takes the y-th such range (there are at most as many
 // as sequences). Thread (row, 4 dims) takes every rows-th partial, its (m, l) and O loaded together and merged with a
 // running maximum; then the rows of threads are merged in order. The time is that of two dependent loads.
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedArgs a, PagedScratch ws, int ranges) {
-    constexpr int cols = D / 4, rows = kJoinThreads / cols, U = D == 256 ? 8 : 4;
-    __shared__ float4 acc[kJoinThreads];
+template <int D, int Threads>
+__global__ void __launch_bounds__(Threads) paged_join_kernel(PagedArgs a, PagedScratch ws, int ranges) {
+    constexpr int cols = D / 4, rows = Threads / cols, U = D == 256 ? 8 : 4;
+    __shared__ float4 acc[Threads];
     __shared__ float2 pair[rows];
     __shared__ int4 job_sh;                                                 // range, sequence, partials
     const int head = blockIdx.y, tid = threadIdx.x, col = tid % cols, row = tid / cols;
@@ -847,9 +861,14 @@ cudaError_t launch(const PagedArgs &a, cudaStream_t st) {
     PagedArgs b = a;
     b.tile_entries = C::tile / a.page_size;
     b.tile_rest = C::tile % a.page_size;
+    b.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     const cudaError_t e = launch_dependent(paged_tile_kernel<C>, dim3(ranges * a.Hkv), C::threads, C::smem, st, b, ws, ranges);
     if (e != cudaSuccess || ranges == 1) return e;      // one range cuts no sequence
-    return launch_dependent(paged_join_kernel<C::D>, dim3(std::min(ranges - 1, a.B), a.Hq), kJoinThreads, 0, st, a, ws, ranges);
+    // few sequences have many partials each: more threads for them (one of 4,096 tokens 6.9 against 7.3 us; but 30 of 512
+    // tokens 16.9 against 14.4)
+    const dim3 grid(std::min(ranges - 1, a.B), a.Hq);
+    return (int64_t)grid.x * grid.y <= kFewJoins ? launch_dependent(paged_join_kernel<C::D, 512>, grid, 512, 0, st, a, ws, ranges)
+                                                 : launch_dependent(paged_join_kernel<C::D, 256>, grid, 256, 0, st, a, ws, ranges);
 }
 
 template <int D, bool F8>
