@@ -18,6 +18,9 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 constexpr int kBatch = 4;          // heads whose loads are in flight together
+// K and V heads at a time. 4 took 95 registers a thread instead of 80: 4,096 tokens into FP8 rows 16.2 against 15.6 us;
+// 1: 16.1.
+constexpr int kKvBatch = 2;
 
 struct Slot {
     int a, b;       // first dims of the slot's two 8-element vectors
@@ -113,33 +116,23 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Thread (token n, slot s) for heads [h0, h0 + run), kBatch at a time: their loads are issued together, which
-// the compiler cannot do by itself since out may be x.
+// A token's slot in heads [h0, h1), kBatch at a time: their loads are issued together, which the compiler cannot do
+// by itself since dst may be src.
 template <bool Inter>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, RopeRows a, int run) {
-    let_next_begin();
-    wait_for_previous();
-    const int S = r.D >> 4;
-    const int64_t t = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
-    const int64_t n = t / S;
-    if (n >= a.N) return;
-    const Slot sl = slot_of(r, (int)(t - n * S));
-    if (sl.fa < 0 && a.x == a.out) return;         // in place: nothing to do
-    const int h0 = blockIdx.y * run, h1 = min(a.H, h0 + run);
-    const uint16_t *src = a.x + n * a.x_ld;
-    uint16_t *dst = a.out + n * a.out_ld;
+__device__ __forceinline__ void turn_heads(const RopeArgs &r, const uint16_t *src, uint16_t *dst, int D, const Slot &sl, int pos,
+                                           int h0, int h1) {
     uint4 va[kBatch], vb[kBatch];
     auto load = [&](int h) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
             if (h + i < h1) {
-                va[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)(h + i) * r.D + sl.a);
-                vb[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)(h + i) * r.D + sl.b);
+                va[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)(h + i) * D + sl.a);
+                vb[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)(h + i) * D + sl.b);
             }
     };
     load(h0);
     float co[8], si[8];
-    if (sl.fa >= 0) turns(r, sl, a.pos[n], co, si);
+    if (sl.fa >= 0) turns(r, sl, pos, co, si);
     for (int h = h0; h < h1; h += kBatch) {
         if (h > h0) load(h);
 #pragma unroll
@@ -152,10 +145,25 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, RopeRows
                 va[i] = pack8(x);
                 vb[i] = pack8(x + 8);
             }
-            *reinterpret_cast<uint4 *>(dst + (int64_t)(h + i) * r.D + sl.a) = va[i];
-            *reinterpret_cast<uint4 *>(dst + (int64_t)(h + i) * r.D + sl.b) = vb[i];
+            *reinterpret_cast<uint4 *>(dst + (int64_t)(h + i) * D + sl.a) = va[i];
+            *reinterpret_cast<uint4 *>(dst + (int64_t)(h + i) * D + sl.b) = vb[i];
         }
     }
+}
+
+// Thread (token n, slot s) for heads [h0, h0 + run).
+template <bool Inter>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, RopeRows a, int run) {
+    let_next_begin();
+    wait_for_previous();
+    const int S = r.D >> 4;
+    const int64_t t = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
+    const int64_t n = t / S;
+    if (n >= a.N) return;
+    const Slot sl = slot_of(r, (int)(t - n * S));
+    if (sl.fa < 0 && a.x == a.out) return;         // in place: nothing to do
+    const int h0 = blockIdx.y * run;
+    turn_heads<Inter>(r, a.x + n * a.x_ld, a.out + n * a.out_ld, r.D, sl, a.pos[n], h0, min(a.H, h0 + run));
 }
 
 // x / scale for inv = RN(1 / scale): one correction of the product by the reciprocal. For scale = RN(amax / 448) of any
@@ -212,10 +220,12 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], const Slot &sl,
     }
 }
 
-// Thread (token n, slot s) for a run of the token's 2 Hkv + Hq heads: k (turned into the cache), v (into the cache),
-// then q (turned into q_out): the runs with K and V, which take longer, begin first. S = D / 16 threads of one warp carry a head.
+// Thread (token n, slot s) for a run of a token's heads, all of K and V (blockIdx.y < kv_slices) or all of q: k is
+// turned into the cache, v copied into it, q turned into q_out. The K and V runs, which take longer, begin first. Runs of both
+// kinds cost every head the choice between them: 4,096 tokens into FP8 rows 16.8 against 16.1 us. S = D / 16 threads of one warp
+// carry a head.
 template <int S, bool F8, bool Inter>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, AppendArgs a, int run) {
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, AppendArgs a, int run, int kv_slices) {
     constexpr int D = S * 16;
     let_next_begin();
     wait_for_previous();
@@ -226,48 +236,47 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, A
     const int row = a.seq ? a.seq[n] : (int)n;
     if (row < 0) return;                                     // padding
     const int pos = a.pos[n];
-    const Slot sl = slot_of(r, s), straight = {8 * s, D / 2 + 8 * s, -1, -1};
-    const int kv_heads = 2 * a.Hkv;
-    const int h1 = min(kv_heads + (a.q ? a.Hq : 0), ((int)blockIdx.y + 1) * run);
-    const int h0 = blockIdx.y * run;
-    uint4 va[kBatch], vb[kBatch];
+    const Slot sl = slot_of(r, s);
+    if ((int)blockIdx.y >= kv_slices) {
+        const int h0 = ((int)blockIdx.y - kv_slices) * run, h1 = min(a.Hq, h0 + run);
+        turn_heads<Inter>(r, a.q + n * a.q_ld, a.q_out + n * a.q_out_ld, D, sl, pos, h0, h1);
+        return;
+    }
+    uint4 va[kKvBatch], vb[kKvBatch];
+    float co[8], si[8];
+    const Slot straight = {8 * s, D / 2 + 8 * s, -1, -1};
+    const int h0 = blockIdx.y * run, h1 = min(2 * a.Hkv, h0 + run);
     auto load = [&](int h) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
+        for (int i = 0; i < kKvBatch; ++i) {
             const int hi = h + i;
             if (hi >= h1) break;
-            const bool v = hi >= a.Hkv && hi < kv_heads;
-            const uint16_t *src = hi >= kv_heads ? a.q + n * a.q_ld + (hi - kv_heads) * D
-                                  : v            ? a.v + n * a.v_ld + (hi - a.Hkv) * D
-                                                 : a.k + n * a.k_ld + hi * D;
+            const bool v = hi >= a.Hkv;
+            const uint16_t *src = v ? a.v + n * a.v_ld + (hi - a.Hkv) * D : a.k + n * a.k_ld + hi * D;
             va[i] = *reinterpret_cast<const uint4 *>(src + (v ? straight.a : sl.a));
             vb[i] = *reinterpret_cast<const uint4 *>(src + (v ? straight.b : sl.b));
         }
     };
     load(h0);
-    int64_t slot = -1;
-    if (h0 < kv_heads) {
-        bool ok = row < a.n_rows && pos >= 0 && pos / a.page_size < a.ld;
-        if (ok) {
-            const int page = a.table[(int64_t)row * a.ld + pos / a.page_size];
-            ok = page >= 0 && page < a.n_pages;
-            slot = (int64_t)page * a.page_size + pos % a.page_size;
-        }
-        if (!ok) {
-            if (s == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereAppend, (int)n);
-            slot = -1;                                        // its K and V are left out
-        }
+    bool ok = row < a.n_rows && pos >= 0 && pos / a.page_size < a.ld;
+    int page = 0;
+    if (ok) {
+        page = a.table[(int64_t)row * a.ld + pos / a.page_size];
+        ok = page >= 0 && page < a.n_pages;
     }
-    float co[8], si[8];
-    if (sl.fa >= 0) turns(r, sl, pos, co, si);
-    for (int h = h0; h < h1; h += kBatch) {
+    if (!ok) {                                                // its K and V are left out
+        if (s == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereAppend, (int)n);
+        return;
+    }
+    const int64_t slot = (int64_t)page * a.page_size + pos % a.page_size;
+    if (sl.fa >= 0 && h0 < a.Hkv) turns(r, sl, pos, co, si);
+    for (int h = h0; h < h1; h += kKvBatch) {
         if (h > h0) load(h);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
+        for (int i = 0; i < kKvBatch; ++i) {
             const int hi = h + i;
             if (hi >= h1) break;
-            const bool is_q = hi >= kv_heads, is_v = hi >= a.Hkv && !is_q;
-            if (!is_q && slot < 0) continue;
+            const bool is_v = hi >= a.Hkv;
             const int g = hi - (is_v ? a.Hkv : 0);             // KV head
             const Slot at = is_v ? straight : sl;
             const bool turned = at.fa >= 0;
@@ -275,7 +284,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, A
             if (turned || F8) unpack16(va[i], vb[i], x);
             if (turned) turn16(x, co, si, Inter);
             const int64_t kv = (slot * a.Hkv + g) * D;
-            if (F8 && !is_q) {
+            if (F8) {
                 quantise16<S>(x, at, s, (is_v ? a.v_codes : a.k_codes) + kv,
                               (is_v ? a.v_scales : a.k_scales) + (slot * a.Hkv + g) * (D / 128), D / 128);
             } else {
@@ -283,7 +292,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, A
                     va[i] = pack8(x);
                     vb[i] = pack8(x + 8);
                 }
-                uint16_t *dst = is_q ? a.q_out + n * a.q_out_ld + (hi - kv_heads) * D : (is_v ? a.v_cache : a.k_cache) + kv;
+                uint16_t *dst = (is_v ? a.v_cache : a.k_cache) + kv;
                 *reinterpret_cast<uint4 *>(dst + at.a) = va[i];
                 *reinterpret_cast<uint4 *>(dst + at.b) = vb[i];
             }
@@ -299,12 +308,12 @@ int run_of(int64_t threads_per_head, int heads) {
 
 template <int S, bool F8>
 cudaError_t append(const RopeArgs &r, const AppendArgs &a, cudaStream_t st) {
-    const int heads = (a.q ? a.Hq : 0) + 2 * a.Hkv;
+    const int q_heads = a.q ? a.Hq : 0, kv_heads = 2 * a.Hkv;
     const int64_t threads = (int64_t)a.N * S;
-    const int run = run_of(threads, heads);
-    const dim3 grid((unsigned)((threads + kRopeThreads - 1) / kRopeThreads), (heads + run - 1) / run);
+    const int run = run_of(threads, q_heads + kv_heads), kv_slices = (kv_heads + run - 1) / run;
+    const dim3 grid((unsigned)((threads + kRopeThreads - 1) / kRopeThreads), kv_slices + (q_heads + run - 1) / run);
     return launch_dependent(r.interleaved ? rope_append_kernel<S, F8, true> : rope_append_kernel<S, F8, false>, grid, kRopeThreads,
-                            0, st, r, a, run);
+                            0, st, r, a, run, kv_slices);
 }
 
 }  // namespace
