@@ -19,10 +19,14 @@
 //   bf16 rows: P = P_hi + P_lo, two bf16 values (2^-17 of each weight): one bf16 would add as much error
 //     as the result's own rounding.
 //   FP8 rows: E4M3 codes are exact in f16. Q enters as f16 scaled by a power of two per head (values below 2^-24 of
-//     the head's largest are rounded there: beneath the fp32 sum's own rounding); the K scales multiply the fp32
-//     sums of each 128 dims. V's scales enter the weights, w = 2^(s + log2 v_scale - m) with m the running maximum of
-//     that exponent (so that the largest is 1), one set of weights for each 128 dims, rounded to f16: 2^-11 of each,
-//     well under the rows' own 2^-4. The softmax's sum is taken without v_scale, relative to the first set's m.
+//     the head's largest are rounded there: beneath the fp32 sum's own rounding); or, with 8 head rows of 256 dims, as
+//     the sum of two E4M3 values and K's codes as they are (m16n8k32): the second parts take the M rows that would be
+//     empty. Two E4M3 values hold bf16's 8 significant bits; the second, at most 2^-4 of the first, is scaled by
+//     another 2^5, so that its step is 2^-21 of the head's largest value (values below 2^-14 of that are rounded by up to
+//     2^-22 of it: a score by 2^-22 max |q| sum |k|). The K scales multiply the fp32 sums of each 128 dims. V's scales
+//     enter the weights, w = 2^(s + log2 v_scale - m) with m the running maximum of that exponent (so that the largest is
+//     1), one set of weights for each 128 dims, rounded to f16: 2^-11 of each, well under the rows' own 2^-4. The
+//     softmax's sum is taken without v_scale, relative to the first set's m.
 #include "paged.cuh"
 #include "qsa_ptx.cuh"
 
@@ -37,15 +41,24 @@ namespace {
 constexpr int kFewJoins = 152;           // CTAs of the join up to which they have 512 threads, one for each SM
 constexpr int kMaxRanges = 640;
 
-template <int D_, int GT_, bool F8_>
+// Loading: 16-byte cp.async keep the load/store unit busy for 1,100 of a 64 KB tile's 2,800 cycles, so warps of their own
+// issue them beside the products. They meet the others once a tile. Against loads by the multiplying warps, 32 sequences
+// of 20,000 tokens in FP8 rows of 256 dims: 114 against 135 us (8 head rows), 122 and 142 (16); bf16 rows of 256 dims: 192 and
+// 194.5, 512 sequences of 200 tokens 48 and 51; of 64 dims with 16 head rows 108 and 114. At 128 dims the registers of
+// more warps are not there. More threads also begin later: 1 token 5.4 against 5.2 us.
+constexpr int loaders_for(int D) { return D == 128 ? 0 : D == 256 ? 4 : 2; }
+constexpr int kFewRows = 8;
+
+template <int D_, int GT_, bool F8_, int Loaders = loaders_for(D_)>
 struct PagedCfg {
     static constexpr int D = D_, GT = GT_;          // GT: head rows kept (8 or 16)
     static constexpr bool F8 = F8_;
     static constexpr int warps = D / 32;            // that multiply
-    // that load; 0: those that multiply do. With 16 head rows these have enough to do: FP8 rows of 256 dims 125 us with
-    // loading warps, 142 without, 64 dims 108 and 114 (32 sequences of 20,000); with 8 rows 131 and 128, and a call of
-    // 4,096 tokens 7.5 and 7.3. At 128 dims the registers of more warps are not there.
-    static constexpr int loaders = GT == 8 || D == 128 ? 0 : D == 256 ? 4 : 2;
+    static constexpr int loaders = Loaders;         // that load; 0: those that multiply do
+    // Q as two E4M3 values, K's codes multiplied as they are: 114 against 121 us over FP8 rows of 256 dims. At 128 dims the
+    // products are not what the kernel waits for (217 against 213 us), and with 16 head rows, where no M rows are free
+    // for the second parts, there are not the registers.
+    static constexpr bool split = F8 && D == 256 && GT == 8;
     static constexpr int threads = (warps + loaders) * 32;
     static constexpr int tile = F8 ? 128 : 64;      // tokens
     static constexpr int row = D * (F8 ? 1 : 2);    // bytes of a K or V row
@@ -183,6 +196,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ void mma16832_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // Two E4M3 codes (the low or the high half of w) -> f16x2, exactly.
 __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t w, int half) {
     uint32_t r;
@@ -259,8 +279,70 @@ __device__ __forceinline__ void write_joined(const PagedArgs &a, int s, int head
     if (col == 0 && a.lse) a.lse[(int64_t)s * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// The block's barrier, from more than one place in the code.
+// The block's barrier, from more than one place in the code, and that of the multiplying warps.
 __device__ __forceinline__ void sync_all() { asm volatile("bar.sync 0;" ::: "memory"); }
+template <int Threads>
+__device__ __forceinline__ void sync_some() {
+    asm volatile("bar.sync 1, %0;" ::"n"(Threads) : "memory");
+}
+
+// FP8 rows: GT heads of D bf16 values in shared memory become, in place, D first parts and D second parts (bytes) of the
+// values divided by scale[h], a power of two. A warp takes every W-th head.
+template <int D, int GT, int W>
+__device__ __forceinline__ void split_queries(uint32_t queries, int warp, int lane, float *scale) {
+    for (int h = warp; h < GT; h += W) {
+        constexpr int PD = D / 32;     // dims of a lane
+        const uint32_t qrow = queries + h * D * 2, hx = h & 7;
+        uint32_t x[PD / 2];
+        if (PD == 8)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[PD / 2 - 2]), "=r"(x[PD / 2 - 1])
+                         : "r"(qrow + ((lane ^ hx) << 4))
+                         : "memory");
+        else
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                         : "=r"(x[0]), "=r"(x[1])
+                         : "r"(qrow + (((lane >> 1) ^ hx) << 4) + (lane & 1) * 8)
+                         : "memory");
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < PD / 2; ++k)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
+#pragma unroll
+        for (int n = 16; n >= 1; n >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, n));
+        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -119), 126);
+        // the largest becomes 2^7 .. 2^8; an infinite one makes the head NaN, not E4M3's largest value
+        const float down = top == INFINITY ? NAN : __uint_as_float((uint32_t)(134 - e) << 23);
+        uint32_t part[2][PD / 4];
+#pragma unroll
+        for (int k = 0; k < PD / 4; ++k) {
+            part[0][k] = part[1][k] = 0u;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const uint32_t y = x[2 * k + z];
+                const float u = __uint_as_float(y << 16) * down, v = __uint_as_float(y & 0xFFFF0000u) * down;
+                const uint32_t w = e4m3x2_of(u, v), back = e4m3_to_f16x2(w, 0);
+                const float2 near = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+                part[0][k] |= w << (16 * z);
+                part[1][k] |= e4m3x2_of((u - near.x) * 32.f, (v - near.y) * 32.f) << (16 * z);
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            if (PD == 8)
+                asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(qrow + (((z * D / 16 + (lane >> 1)) ^ hx) << 4) +
+                                                                     (lane & 1) * 8),
+                             "r"(part[z][0]), "r"(part[z][PD / 4 - 1])
+                             : "memory");
+            else
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(qrow + (((z * D / 16 + (lane >> 2)) ^ hx) << 4) + (lane & 3) * 4),
+                             "r"(part[z][0])
+                             : "memory");
+        }
+        if (lane == 0) scale[h] = __uint_as_float((uint32_t)(120 + e) << 23);
+    }
+}
 
 // dst + index x bytes, index >= 0
 __device__ __forceinline__ const char *row_ptr(const char *base, int index, uint32_t bytes) {
@@ -280,6 +362,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long scan[W + C::loaders];
     __shared__ int start[2];
+    __shared__ float head_scale[GT];               // split queries: Q is its parts' sum x head_scale
     __shared__ uint32_t real_tok[NS][C::load_warps];       // bit i: token i of the loading warp's share exists
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -362,16 +445,16 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     int entry, offset, page;
     bool wanted;
     auto fetch_page = [&](bool new_row) {
-        const int tok = in.t * T + lw * LT + lane;
+        const uint32_t tok = (uint32_t)in.t * T + lw * LT + lane;      // a tile may reach past 2^31
         if (new_row) {
-            entry = a.page_shift >= 0 ? tok >> a.page_shift : tok / a.page_size;
-            offset = tok - entry * a.page_size;
+            entry = a.page_shift >= 0 ? tok >> a.page_shift : tok / (uint32_t)a.page_size;
+            offset = tok - (uint32_t)entry * a.page_size;
         } else {
             entry += a.tile_entries;
             offset += a.tile_rest;
             if (offset >= a.page_size) offset -= a.page_size, ++entry;
         }
-        wanted = (LT == 32 || lane < LT) && tok >= in.r.lo && tok < in.r.len;
+        wanted = (LT == 32 || lane < LT) && tok >= (uint32_t)in.r.lo && tok < (uint32_t)in.r.len;
         page = wanted ? __ldg(a.table + in.s * a.ld + entry) : -1;
     };
     auto issue = [&](int stage, int q_slot, bool first) {      // tile `in`
@@ -430,19 +513,25 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
         for (int i = 0; i < NS - 1; ++i) advance();
     }
     if (C::loaders && warp >= W) {                 // the barriers of the loop below, and the loads between them
+        bool first = true;
         for (long long i = 0; i < n_tiles; ++i) {
             cp_async_wait<NS - 2>();
             sync_all();
-            sync_all();
+            if (first) sync_all();                 // tile i's queries, whose slot may be wanted now, are taken
             advance();
-            sync_all();
-            if (at.t + 1 == at.r.t1 || i + 1 == n_tiles) sync_all();
+            first = at.t + 1 == at.r.t1;
             if (i + 1 < n_tiles) at.next(a);
         }
         return;
     }
 
     // ---- products
+    auto sync_mul = []() {
+        if (C::loaders)
+            sync_some<W * 32>();
+        else
+            sync_all();
+    };
     constexpr int KS = D / 16;
     uint32_t qf[KS][2 * HR];                       // Q operand: rows g (and g + 8), two k halves
     float q_scale[HR];                             // logit = score x q_scale (x K scale)
@@ -482,6 +571,20 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                 }
 #pragma unroll
                 for (int h = 0; h < HR; ++h) q_scale[h] = a.scale_log2;
+            } else if constexpr (C::split) {
+                split_queries<D, GT, W>(qa, warp, lane, head_scale);
+                sync_mul();
+                // qf[k][0], [1]: first and second parts of dims 16k + 4c .. 4c + 3, as the codes of K lie
+                q_scale[0] = a.scale_log2 * head_scale[g];
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+#pragma unroll
+                    for (int k = 0; k < KS; k += 4) {
+                        uint32_t r[4];
+                        ldmatrix4(qa + (lane & 7) * D * 2 + (((z * D / 16 + k + (lane >> 3)) ^ (lane & 7)) << 4), r);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) qf[k + n][z] = r[n];
+                    }
             } else {
                 // k index (2c, 2c+1 | 2c+8, 2c+9) of a step stands for dims 16k + 4c .. 4c + 3, as the codes of K lie
 #pragma unroll
@@ -522,20 +625,49 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[n][k] = 0.f;
+            if (C::loaders) sync_all();
             first = false;
         }
         // S = Q K^T over this warp's tokens; s[nt]: tokens nt x 8 + 2c, + 1 for head rows g (and g + 8)
         float s[NQ][2 * HR];
         float lv[SG][NQ][2];                       // FP8: log2 of the tokens' V scales
         {
-            constexpr int CH = F8 ? (NQ <= 2 ? 2 : 1) : 4 / NQ > 0 ? 4 / NQ : 1;   // independent sums (FP8: of each 128 dims)
+            // independent sums (FP8: of each 128 dims)
+            constexpr int CH = C::split ? 1 : F8 ? (NQ <= 2 ? 2 : 1) : 4 / NQ > 0 ? 4 / NQ : 1;
             const uint32_t real = real_tok[stage][warp * TW / LT] >> (warp * TW % LT);
+            constexpr int NB = C::split ? NQ : 1;  // columns of tokens whose sums are formed together
+            float accs[NB][SG * CH][4];
 #pragma unroll
             for (int nt = 0; nt < NQ; ++nt) {
-                float acc[SG * CH][4];
+                auto &acc = accs[nt % NB];
+                if (nt == 0 || !C::split)
 #pragma unroll
-                for (int x = 0; x < SG * CH; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int x = 0; x < SG * CH; ++x) accs[n][x][0] = accs[n][x][1] = accs[n][x][2] = accs[n][x][3] = 0.f;
                 const uint32_t krow = st + (warp * TW + nt * 8 + (lane & 7)) * C::row;
+                if constexpr (C::split) {
+                    constexpr int KG = C::chunks / 4 / SG;     // loads of 64 bytes of a row in 128 dims
+#pragma unroll
+                    for (int k = 0; k < (nt == 0 ? KG : 0); ++k) {
+                        uint32_t b[NB][SG][4];
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+#pragma unroll
+                            for (int gr = 0; gr < SG; ++gr)
+                                ldmatrix4(krow + n * 8 * C::row + (((4 * (k + gr * KG) + (lane >> 3)) ^ (lane & 7)) << 4), b[n][gr]);
+#pragma unroll
+                        for (int z = 0; z < 4; z += 2)
+#pragma unroll
+                            for (int gr = 0; gr < SG; ++gr)
+#pragma unroll
+                                for (int n = 0; n < NB; ++n) {
+                                    const int step = 4 * (k + gr * KG) + z;
+                                    mma16832_e4m3(accs[n][gr], qf[step][0], qf[step][1], qf[step + 1][0], qf[step + 1][1],
+                                                  b[n][gr][z], b[n][gr][z + 1]);
+                                }
+                    }
+                } else
 #pragma unroll
                 for (int k = 0; k < C::chunks / 4; ++k) {
                     uint32_t b[4];
@@ -581,6 +713,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                         float sum = acc[gr * CH][x];
 #pragma unroll
                         for (int y = 1; y < CH; ++y) sum += acc[gr * CH + y][x];
+                        if (C::split) sum = fmaf(acc[gr * CH][(2 + x) & 3], 0.03125f, sum);     // the second parts' rows
                         v = F8 ? fmaf(sum, sc[x & 1][gr], v) : sum;
                     }
                     s[nt][x] = (real >> (t + (x & 1))) & 1 ? v * q_scale[x / 2] : -INFINITY;
@@ -600,7 +733,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                 top = quad_max(top);
                 if (c == 0) maxima[(gr * GT + g + 8 * h) * W + warp] = top;
             }
-        sync_all();
+        sync_mul();
         if (!C::loaders) advance();
         float alpha[HR];                           // of this warp's set
 #pragma unroll
@@ -648,7 +781,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
             o[n][0] *= alpha[0], o[n][1] *= alpha[0];
             if (HR == 2) o[n][2] *= alpha[HR - 1], o[n][3] *= alpha[HR - 1];
         }
-        sync_all();
+        sync_mul();
         // O += P V over this warp's 32 dims
         const uint32_t vt = st + C::k_bytes + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::row;
         const uint32_t pt = base + C::p_at + (F8 ? my_set * GT * C::p_pitch : 0) +
@@ -710,7 +843,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                 l[h] = quad_sum(l[h]);
                 if (c == 0) maxima[(g + 8 * h) * W + warp] = l[h];
             }
-            sync_all();
+            sync_mul();
 #pragma unroll
             for (int h = 0; h < HR; ++h) {
                 const int row = g + 8 * h;
@@ -873,7 +1006,11 @@ cudaError_t launch(const PagedArgs &a, cudaStream_t st) {
 
 template <int D, bool F8>
 cudaError_t launch_heads(const PagedArgs &a, cudaStream_t st) {
-    return a.G <= 8 ? launch<PagedCfg<D, 8, F8>>(a, st) : launch<PagedCfg<D, 16, F8>>(a, st);
+    if (a.G > 8) return launch<PagedCfg<D, 16, F8>>(a, st);
+    // few sequences over bf16 rows of 256 dims: one of 2,048 tokens 6.7 us without loading warps and 6.85 with them, of 4,096
+    // 6.9 and 7.1, of 16,384 13.5 and 13.2, a million 298.5 and 297.9; 8 of 2,048 12.6 and 12.3, 30 of 4,096 47.7 and 47.1
+    if (D == 256 && !F8 && a.B < kFewRows) return launch<PagedCfg<D, 8, F8, D == 256 && !F8 ? 0 : loaders_for(D)>>(a, st);
+    return launch<PagedCfg<D, 8, F8>>(a, st);
 }
 
 }  // namespace

@@ -271,7 +271,7 @@ def run_decode(cfg, q, planes, table, lens, ws, out=None, lse=None, stream=None)
     return out, lse
 
 
-def check_decode(out, lse, q, values, table, lens, page, window, scale, fp8=False):
+def check_decode(out, lse, q, values, table, lens, page, window, scale, fp8=False, q_step=0.0):
     out, lse, q = f64(out), f64(lse), f64(q)
     for r, n in enumerate(lens):
         slots = P.slots_of(table[r], n, page)
@@ -280,6 +280,8 @@ def check_decode(out, lse, q, values, table, lens, page, window, scale, fp8=Fals
         want, want_lse, mass, terms = P.decode(q[r], K, V, lo, scale)
         D = q.shape[-1]
         ds = D * 2.0 ** -24 * terms + 2.0 ** -21 * (terms + 1)
+        if q_step and n:                                  # q off by q_step of its head's largest
+            ds = ds + q_step * np.abs(q[r]).max(1) * np.abs(K[lo:]).sum(2).max() * scale
         if n == 0:
             assert np.all(out[r] == 0) and np.all(np.isneginf(lse[r]))
             continue
@@ -345,6 +347,41 @@ def test_decode_sharp_scores_and_wide_value_scales(cuda_lib, fp8):
     out, lse = run_decode(cfg, q, planes, tab, ints(lens), ws := qb.paged_workspace(cfg))
     check_decode(out, lse, q, values, table, lens, 16, 0, 1 / 16, fp8)
     assert status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 2, 256), (5, 1, 256), (12, 1, 256), (8, 2, 128)])
+def test_decode_queries_of_a_wide_range_over_fp8_rows(cuda_lib, Hq, Hkv, D):
+    """Values of one head from 2^-20 to 1 of its largest, heads from 2^-30 to 8 and zero: over FP8 rows a query value may be
+    rounded by 2^-22 of its head's largest (two E4M3 parts, the second with steps of 2^-21 of it)."""
+    lens = [300, 40]
+    q, planes, values, tab, table = paged_inputs(lens, Hq, Hkv, D, 16, True, seed=61)
+    g = torch.Generator().manual_seed(2)
+    q = (q * (2.0 ** torch.randint(-20, 1, q.shape, generator=g).to(DEV))).to(torch.bfloat16)
+    heads = 2.0 ** torch.randint(-30, 1, (2, Hq, 1), generator=g).to(DEV)
+    heads[0, 0], heads[1, Hq - 1] = 8.0, 0.0                  # few tokens matter; all count alike
+    q = (q * heads).to(torch.bfloat16).contiguous()
+    cfg = qb.make_paged_config(Hq, Hkv, D, 16)
+    ws = qb.paged_workspace(cfg)
+    out, lse = run_decode(cfg, q, planes, tab, ints(lens), ws)
+    check_decode(out, lse, q, values, table, lens, 16, 0, D ** -0.5, True, q_step=2.0 ** -22)
+    assert status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("Hq,D,fp8", [(8, 256, True), (16, 256, True), (8, 128, True), (8, 256, False)])
+def test_decode_query_that_is_not_finite_spoils_its_head_alone(cuda_lib, Hq, D, fp8, value):
+    lens = [70, 50]
+    q, planes, values, tab, table = paged_inputs(lens, Hq, 1, D, 16, fp8, seed=71)
+    cfg = qb.make_paged_config(Hq, 1, D, 16)
+    ws = qb.paged_workspace(cfg)
+    want, want_lse = run_decode(cfg, q, planes, tab, ints(lens), ws)
+    bad = q.clone()
+    bad[0, 3, 5] = value
+    out, lse = run_decode(cfg, bad, planes, tab, ints(lens), ws)
+    assert bool(torch.isnan(out[0, 3]).all())
+    keep = torch.ones(2, Hq, dtype=torch.bool, device=DEV)
+    keep[0, 3] = False
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
 
 
 def test_decode_strided_queries(cuda_lib):
