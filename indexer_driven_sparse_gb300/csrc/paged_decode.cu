@@ -44,12 +44,14 @@ constexpr int kMaxRanges = 640;
 // Loading: 16-byte cp.async keep the load/store unit busy for 1,100 of a 64 KB tile's 2,800 cycles, so warps of their own
 // issue them beside the products. They meet the others once a tile. Against loads by the multiplying warps, 32 sequences
 // of 20,000 tokens in FP8 rows of 256 dims: 114 against 135 us (8 head rows), 122 and 142 (16); bf16 rows of 256 dims: 192 and
-// 194.5, 512 sequences of 200 tokens 48 and 51; of 64 dims with 16 head rows 108 and 114. At 128 dims the registers of
-// more warps are not there. More threads also begin later: 1 token 5.4 against 5.2 us.
-constexpr int loaders_for(int D) { return D == 128 ? 0 : D == 256 ? 4 : 2; }
+// 194.5, 512 sequences of 200 tokens 48 and 51; of 64 dims with 16 head rows 108 and 114. At 128 dims bf16 rows come at the copy
+// rate without; FP8 rows take loading warps, two CTAs an SM and three stages with 16 head rows (32 x 20,000 tokens, 4 KV heads:
+// 112 against 115 us), three CTAs without them with 8 (8 KV heads: 213 against 222). More threads also begin later: 1 token 5.4
+// against 5.2 us.
+constexpr int loaders_for(int D, int GT, bool F8) { return D == 128 ? (F8 && GT == 16 ? 4 : 0) : D == 256 ? 4 : 2; }
 constexpr int kFewRows = 8;
 
-template <int D_, int GT_, bool F8_, int Loaders = loaders_for(D_)>
+template <int D_, int GT_, bool F8_, int Loaders = loaders_for(D_, GT_, F8_)>
 struct PagedCfg {
     static constexpr int D = D_, GT = GT_;          // GT: head rows kept (8 or 16)
     static constexpr bool F8 = F8_;
@@ -69,8 +71,8 @@ struct PagedCfg {
     static constexpr int groups = F8 ? D / 128 : 1; // scales of a row (FP8), sets of weights
     static constexpr int k_bytes = tile * row, s_bytes = F8 ? tile * groups * 4 : 0, q_bytes = GT * D * 2;
     static constexpr int stage = 2 * k_bytes + 2 * s_bytes;
-    static constexpr int stages = F8 && D == 128 ? 2 : 3;
-    static constexpr int ctas = D == 256 ? 1 : D == 128 ? (F8 ? 3 : 2) : (GT == 8 ? 4 : 3);   // per SM
+    static constexpr int stages = F8 && D == 128 && GT == 8 ? 2 : 3;
+    static constexpr int ctas = D == 256 ? 1 : D == 128 ? (F8 && GT == 8 ? 3 : 2) : (GT == 8 ? 4 : 3);   // per SM
     static constexpr int p_pitch = tile * 2 + 16;   // bytes between two heads' weights: an odd number of 16-byte chunks
     static constexpr int p_sets = F8 ? groups : 2;  // FP8: one per V scale; bf16: high and low parts
     static constexpr int q_at = stages * stage, p_at = q_at + (stages - 1) * q_bytes, x_at = p_at + p_sets * GT * p_pitch;
@@ -1009,7 +1011,7 @@ cudaError_t launch_heads(const PagedArgs &a, cudaStream_t st) {
     if (a.G > 8) return launch<PagedCfg<D, 16, F8>>(a, st);
     // few sequences over bf16 rows of 256 dims: one of 2,048 tokens 6.7 us without loading warps and 6.85 with them, of 4,096
     // 6.9 and 7.1, of 16,384 13.5 and 13.2, a million 298.5 and 297.9; 8 of 2,048 12.6 and 12.3, 30 of 4,096 47.7 and 47.1
-    if (D == 256 && !F8 && a.B < kFewRows) return launch<PagedCfg<D, 8, F8, D == 256 && !F8 ? 0 : loaders_for(D)>>(a, st);
+    if (D == 256 && !F8 && a.B < kFewRows) return launch<PagedCfg<D, 8, F8, D == 256 && !F8 ? 0 : loaders_for(D, 8, F8)>>(a, st);
     return launch<PagedCfg<D, 8, F8>>(a, st);
 }
 
