@@ -192,6 +192,12 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// fmaxf, but NaN if either is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -703,8 +709,8 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
 #pragma unroll
                         for (int gr = 0; gr < SG; ++gr) {
                             sc[x][gr] = ks[x * SG + gr];
-                            // a scale below 2^-100 counts as that: its row's values are beneath 2^-91
-                            lv[gr][nt][x] = fmaxf(lg2(vs[x * SG + gr]), -100.f);
+                            // a scale below 2^-100 counts as that: its row's values are beneath 2^-91; NaN stays NaN
+                            lv[gr][nt][x] = max_nan(lg2(vs[x * SG + gr]), -100.f);
                         }
                 }
 #pragma unroll

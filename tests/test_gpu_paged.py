@@ -384,6 +384,22 @@ def test_decode_query_that_is_not_finite_spoils_its_head_alone(cuda_lib, Hq, D, 
     assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
 
 
+@pytest.mark.parametrize("Hq,D", [(8, 256), (16, 256), (8, 128), (16, 128)])
+@pytest.mark.parametrize("plane", [1, 3])
+def test_decode_scale_that_is_not_a_number_spoils_its_row_alone(cuda_lib, Hq, D, plane):
+    lens = [70, 50]
+    q, planes, values, tab, table = paged_inputs(lens, Hq, 1, D, 16, True, seed=73)
+    cfg = qb.make_paged_config(Hq, 1, D, 16)
+    ws = qb.paged_workspace(cfg)
+    want, _ = run_decode(cfg, q, planes, tab, ints(lens), ws)
+    page = int(table[0][1])
+    planes[plane][page, 3, 0, 0] = float("nan")                # token 19 of row 0, its first 128 dims
+    out, lse = run_decode(cfg, q, planes, tab, ints(lens), ws)
+    assert bool(torch.isnan(out[0, :, :128]).all()) and torch.equal(out[1], want[1])
+    if plane == 1:
+        assert bool(torch.isnan(out[0]).all()) and bool(torch.isnan(lse[0]).all())
+
+
 def test_decode_strided_queries(cuda_lib):
     lens = [40, 300, 7]
     q, planes, values, tab, table = paged_inputs(lens, 8, 2, 128, 16, False, seed=31)
