@@ -378,70 +378,88 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     const int Hkv = a.Hkv, G = a.G;
     wait_for_previous();
 
-    // ---- this range's tiles: total over the batch, then the row and tile the range starts at
-    const int per = (a.B + C::threads - 1) / C::threads, s_lo = min(a.B, tid * per), s_hi = min(a.B, s_lo + per);
-    long long mine = 0;
-    for (int s = s_lo; s < s_hi; ++s) {
-        const Row r = row_of<T>(a, s);
-        mine += r.t1 - r.t0;
-    }
-    long long upto = mine;
-    if (a.B <= 32) {                               // at most 2^31 tiles, in the first warp
-        uint32_t u = (uint32_t)mine;
+    // ---- this range's tiles: total over the batch, then the row and tile the range starts at. Up to 32 rows every warp
+    // does that for itself, in 32 bits and without a barrier: 0.5 us of a call.
+    long long x0 = 0, x1 = 0;
+    Cursor<T> in, at;                              // the loads' place, and the products'
+    int skip = 0;                                  // tiles of its first row that come before the range
+    Ranges cut(1, 1);
+    if (a.B <= 32) {                               // at most 2^30 tiles
+        const Row r = row_of<T>(a, min(lane, a.B - 1));
+        const uint32_t mine = lane < a.B ? r.t1 - r.t0 : 0;
+        uint32_t upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, u, o);
-            if (lane >= o) u += v;
+            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
         }
-        upto = u;
+        const uint32_t total = __shfl_sync(0xffffffffu, upto, 31);
+        cut = Ranges(total, (int)min((uint32_t)ranges, max(total, 1u)));
+        if (range < cut.R) x0 = cut.begin(range), x1 = cut.begin(range + 1);
+        const int s = min(__popc(__ballot_sync(0xffffffffu, upto <= (uint32_t)x0)), 31);
+        skip = (int)((uint32_t)x0 - __shfl_sync(0xffffffffu, upto - mine, s));
+        in.s = s;
+        in.r = {__shfl_sync(0xffffffffu, r.len, s), __shfl_sync(0xffffffffu, r.lo, s), __shfl_sync(0xffffffffu, r.t0, s),
+                __shfl_sync(0xffffffffu, r.t1, s)};
+        in.t = in.r.t0 + skip;
     } else {
+        const int per = (a.B + C::threads - 1) / C::threads, s_lo = min(a.B, tid * per), s_hi = min(a.B, s_lo + per);
+        long long mine = 0;
+        for (int s = s_lo; s < s_hi; ++s) {
+            const Row r = row_of<T>(a, s);
+            mine += r.t1 - r.t0;
+        }
+        long long upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += v;
         }
-    }
-    if (lane == 31) scan[warp] = upto;
-    __syncthreads();
-    long long total = 0;
+        if (lane == 31) scan[warp] = upto;
+        __syncthreads();
+        long long total = 0;
 #pragma unroll
-    for (int w = 0; w < W + C::loaders; ++w) {
-        if (w < warp) upto += scan[w];
-        total += scan[w];
-    }
-    const int R = (int)min((long long)ranges, max(total, 1ll));
-    const Ranges cut(total, R);
-    const long long x0 = range < R ? cut.begin(range) : 0, x1 = range < R ? cut.begin(range + 1) : 0;
-    if (x0 < x1 && upto - mine <= x0 && x0 < upto) {
-        long long at = upto - mine;
-        int s = s_lo;
-        for (;; ++s) {
-            const Row r = row_of<T>(a, s);
-            if (x0 < at + r.t1 - r.t0) break;
-            at += r.t1 - r.t0;
+        for (int w = 0; w < W + C::loaders; ++w) {
+            if (w < warp) upto += scan[w];
+            total += scan[w];
         }
-        start[0] = s;
-        start[1] = (int)(x0 - at);
+        cut = Ranges(total, (int)min((long long)ranges, max(total, 1ll)));
+        if (range < cut.R) x0 = cut.begin(range), x1 = cut.begin(range + 1);
+        if (x0 < x1 && upto - mine <= x0 && x0 < upto) {
+            long long before = upto - mine;
+            int s = s_lo;
+            for (;; ++s) {
+                const Row r = row_of<T>(a, s);
+                if (x0 < before + r.t1 - r.t0) break;
+                before += r.t1 - r.t0;
+            }
+            start[0] = s;
+            start[1] = (int)(x0 - before);
+        }
+        __syncthreads();
+        if (x0 < x1) {
+            skip = start[1];
+            in.at(a, start[0], skip);
+        }
     }
-    // rows without a token: zeros
-    for (int s = range; s < a.B; s += ranges) {
-        const Row r = row_of<T>(a, s);
-        if (r.t1 > r.t0) continue;
-        const int len = a.seq_len[s];
-        if (len != 0 && kvh == 0 && tid == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, s);
-        uint16_t *o = a.out + ((int64_t)s * a.Hq + kvh * G) * D;
-        for (int i = tid; i < G * D / 8; i += C::threads) reinterpret_cast<uint4 *>(o)[i] = make_uint4(0, 0, 0, 0);
-        if (a.lse && tid < G) a.lse[(int64_t)s * a.Hq + kvh * G + tid] = -INFINITY;
-    }
-    __syncthreads();
+    at = in;
     const long long n_tiles = x1 - x0;
     if (kvh == 0 && tid == 0) ws.meta[range] = make_int2(-1, 0);
-    if (n_tiles == 0) return;
 
+    auto empty_rows = [&](int threads) {           // rows without a token: zeros, by the first `threads`
+        for (int s = range; s < a.B; s += ranges) {
+            const Row r = row_of<T>(a, s);
+            if (r.t1 > r.t0) continue;
+            const int len = a.seq_len[s];
+            if (len != 0 && kvh == 0 && tid == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, s);
+            uint16_t *o = a.out + ((int64_t)s * a.Hq + kvh * G) * D;
+            for (int i = tid; i < G * D / 8; i += threads) reinterpret_cast<uint4 *>(o)[i] = make_uint4(0, 0, 0, 0);
+            if (a.lse && tid < G) a.lse[(int64_t)s * a.Hq + kvh * G + tid] = -INFINITY;
+        }
+    };
+    empty_rows(C::threads);
+    if (n_tiles == 0) return;
     const uint32_t base = smem_u32(smem);
-    Cursor<T> in, at;                              // the loads' place, and the products'
-    in.at(a, start[0], start[1]);
-    at = in;
 
     // ---- loads. Lane i < LT keeps token i of the loading warp's share: its page's place in the table and offset in the
     // page, stepped by a tile at a time, and the page id, fetched one tile ahead of the copies.
@@ -547,7 +565,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     float o[4][4];
     const int my_set = SG == 2 ? warp / 4 : 0;     // the weights this warp's dims use
     float *const maxima = reinterpret_cast<float *>(smem + C::x_at);    // [SG][GT][W]
-    bool begins = start[1] == 0;                   // the segment starts its sequence
+    bool begins = skip == 0;                   // the segment starts its sequence
     bool first = true;
     int stage = 0, q_slot = 0;
     for (long long i = 0; i < n_tiles; ++i, stage = stage + 1 == NS ? 0 : stage + 1) {
