@@ -41,22 +41,19 @@ namespace {
 constexpr int kFewJoins = 152;           // CTAs of the join up to which they have 512 threads, one for each SM
 constexpr int kMaxRanges = 640;
 
-// Loading: 16-byte cp.async keep the load/store unit busy for 1,100 of a 64 KB tile's 2,800 cycles, so warps of their own
-// issue them beside the products. They meet the others once a tile. Against loads by the multiplying warps, 32 sequences
-// of 20,000 tokens in FP8 rows of 256 dims: 114 against 135 us (8 head rows), 122 and 142 (16); bf16 rows of 256 dims: 192 and
-// 194.5, 512 sequences of 200 tokens 48 and 51; of 64 dims with 16 head rows 108 and 114. At 128 dims bf16 rows come at the copy
-// rate without; FP8 rows take loading warps, two CTAs an SM and three stages with 16 head rows (32 x 20,000 tokens, 4 KV heads:
-// 112 against 115 us), three CTAs without them with 8 (8 KV heads: 213 against 222). More threads also begin later: 1 token 5.4
-// against 5.2 us.
-constexpr int loaders_for(int D, int GT, bool F8) { return D == 128 ? (F8 && GT == 16 ? 4 : 0) : D == 256 ? 4 : 2; }
-constexpr int kFewRows = 8;
-
-template <int D_, int GT_, bool F8_, int Loaders = loaders_for(D_, GT_, F8_)>
+template <int D_, int GT_, bool F8_>
 struct PagedCfg {
     static constexpr int D = D_, GT = GT_;          // GT: head rows kept (8 or 16)
     static constexpr bool F8 = F8_;
     static constexpr int warps = D / 32;            // that multiply
-    static constexpr int loaders = Loaders;         // that load; 0: those that multiply do
+    // that load; 0: those that multiply do. 16-byte cp.async keep the load/store unit busy for 1,100 of a 64 KB tile's 2,800
+    // cycles, so warps of their own issue them beside the products; they meet the others once a tile. Against loads by
+    // the multiplying warps, 32 sequences of 20,000 tokens in FP8 rows of 256 dims: 114 against 135 us (8 head rows), 122 and
+    // 142 (16); bf16 rows of 256 dims: 192 and 194.5, 512 sequences of 200 tokens 48 and 51, one of 16,384 tokens 12.7 and 13.1,
+    // but of 4,096 6.6 and 6.5; of 64 dims with 16 head rows 108 and 114. At 128 dims bf16 rows come at the copy rate
+    // without; FP8 rows take them, with two CTAs an SM and three stages, for 16 head rows (32 x 20,000 tokens, 4 KV heads:
+    // 112 against 115 us) and three CTAs without them for 8 (8 KV heads: 213 against 222).
+    static constexpr int loaders = D == 128 ? (F8 && GT == 16 ? 4 : 0) : D == 256 ? 4 : 2;
     // Q as two E4M3 values, K's codes multiplied as they are: 114 against 121 us over FP8 rows of 256 dims. At 128 dims the
     // products are not what the kernel waits for (217 against 213 us), and with 16 head rows, where no M rows are free
     // for the second parts, there are not the registers.
@@ -1032,11 +1029,7 @@ cudaError_t launch(const PagedArgs &a, cudaStream_t st) {
 
 template <int D, bool F8>
 cudaError_t launch_heads(const PagedArgs &a, cudaStream_t st) {
-    if (a.G > 8) return launch<PagedCfg<D, 16, F8>>(a, st);
-    // few sequences over bf16 rows of 256 dims: one of 2,048 tokens 6.7 us without loading warps and 6.85 with them, of 4,096
-    // 6.9 and 7.1, of 16,384 13.5 and 13.2, a million 298.5 and 297.9; 8 of 2,048 12.6 and 12.3, 30 of 4,096 47.7 and 47.1
-    if (D == 256 && !F8 && a.B < kFewRows) return launch<PagedCfg<D, 8, F8, D == 256 && !F8 ? 0 : loaders_for(D, 8, F8)>>(a, st);
-    return launch<PagedCfg<D, 8, F8>>(a, st);
+    return a.G <= 8 ? launch<PagedCfg<D, 8, F8>>(a, st) : launch<PagedCfg<D, 16, F8>>(a, st);
 }
 
 }  // namespace
