@@ -50,10 +50,9 @@ struct PagedCfg {
     // cycles, so warps of their own issue them beside the products; they meet the others once a tile. Against loads by
     // the multiplying warps, 32 sequences of 20,000 tokens in FP8 rows of 256 dims: 114 against 135 us (8 head rows), 122 and
     // 142 (16); bf16 rows of 256 dims: 192 and 194.5, 512 sequences of 200 tokens 48 and 51, one of 16,384 tokens 12.7 and 13.1,
-    // but of 4,096 6.6 and 6.5; of 64 dims with 16 head rows 108 and 114. At 128 dims bf16 rows come at the copy rate
-    // without; FP8 rows take them, with two CTAs an SM and three stages, for 16 head rows (32 x 20,000 tokens, 4 KV heads:
-    // 112 against 115 us) and three CTAs without them for 8 (8 KV heads: 213 against 222).
-    static constexpr int loaders = D == 128 ? (F8 && GT == 16 ? 4 : 0) : D == 256 ? 4 : 2;
+    // but of 4,096 6.6 and 6.5; of 64 dims with 16 head rows 108 and 114. At 128 dims two or three CTAs on an SM do that for
+    // each other: FP8 rows take 211 us without loading warps and 222 with (8 KV heads, 8 head rows), 114 either way with 16.
+    static constexpr int loaders = D == 128 ? 0 : D == 256 ? 4 : 2;
     // Q as two E4M3 values, K's codes multiplied as they are: 114 against 121 us over FP8 rows of 256 dims. At 128 dims the
     // products are not what the kernel waits for (217 against 213 us), and with 16 head rows, where no M rows are free
     // for the second parts, there are not the registers.
@@ -68,8 +67,8 @@ struct PagedCfg {
     static constexpr int groups = F8 ? D / 128 : 1; // scales of a row (FP8), sets of weights
     static constexpr int k_bytes = tile * row, s_bytes = F8 ? tile * groups * 4 : 0, q_bytes = GT * D * 2;
     static constexpr int stage = 2 * k_bytes + 2 * s_bytes;
-    static constexpr int stages = F8 && D == 128 && GT == 8 ? 2 : 3;
-    static constexpr int ctas = D == 256 ? 1 : D == 128 ? (F8 && GT == 8 ? 3 : 2) : (GT == 8 ? 4 : 3);   // per SM
+    static constexpr int stages = F8 && D == 128 ? 2 : 3;
+    static constexpr int ctas = D == 256 ? 1 : D == 128 ? (F8 ? 3 : 2) : (GT == 8 ? 4 : 3);   // per SM
     static constexpr int p_pitch = tile * 2 + 16;   // bytes between two heads' weights: an odd number of 16-byte chunks
     static constexpr int p_sets = F8 ? groups : 2;  // FP8: one per V scale; bf16: high and low parts
     static constexpr int q_at = stages * stage, p_at = q_at + (stages - 1) * q_bytes, x_at = p_at + p_sets * GT * p_pitch;
