@@ -284,8 +284,20 @@ __device__ __forceinline__ void move_pages(const PlaneGroups &pg, int n, int pag
         for (int64_t w = warp; w < items; w += warps) {
             // the part is turned by the page: a warp that met the same part of every page would copy all of the partly
             // filled ones (low parts) or none
-            const int64_t rest = w / parts, part = (w - rest * parts + rest % 13) % parts;
-            const int plane = (int)(rest % g.n_planes), k = (int)(rest / g.n_planes);
+            int64_t rest, part;
+            int plane, k;
+            if ((items + 13) >> 32 == 0) {         // in 32 bits: a 64-bit division takes some 100 instructions
+                const uint32_t p = (uint32_t)parts, r = (uint32_t)w / p;
+                rest = r;
+                part = ((uint32_t)w - r * p + r % 13u) % p;
+                k = r / (uint32_t)g.n_planes;
+                plane = r - k * g.n_planes;
+            } else {
+                rest = w / parts;
+                part = (w - rest * parts + rest % 13) % parts;
+                k = (int)(rest / g.n_planes);
+                plane = (int)(rest % g.n_planes);
+            }
             int src, dst;
             const int used = pair(k, src, dst);
             if (used == 0) continue;
