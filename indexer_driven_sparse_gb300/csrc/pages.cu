@@ -476,14 +476,14 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
 // Shared memory of a CTA's plan.
 struct SmallFork {
     int *len, *full;                       // [n_in] tokens, full pages (-1: an impossible length)
-    int *last;                             // [n_in] the last, partly filled page (kAlone: nothing else names it; -1: none)
+    int *last;                             // [n_in] the last, partly filled page (-1: none)
     int *first, *children;                 // [n_in] lowest row that continues it (later: whether one keeps the last page), how many do
     int *parent, *pages, *off;             // [n_out] parent -1: starts empty; pages in all; off kKeeps: keeps the parent's last page; -1: failed
-    int *delta;                            // [n_pages] CTA 0: references that come and go
+    int *delta;                            // [n_pages] ref; later, in CTA 0, with the references that come and go
     uint16_t *pairs;                       // [n_out] rows that copy a page
     uint16_t *fresh;                       // [n_pages] free pages in order
 };
-constexpr int kAlone = 1 << 30, kKeeps = 1 << 30;
+constexpr int kKeeps = 1 << 30;
 constexpr int kSmallChunks = kSmallPages / kSmallThreads, kSmallWarps = kSmallThreads / 32;
 static_assert(kSmallChunks <= 32 && kSmallChunks * kSmallWarps <= kSmallThreads, "a thread's pages fit a word, the counts a scan");
 
@@ -495,10 +495,10 @@ constexpr int kSmallSmem = kSmallRows * 32 + kSmallPages * 6 + 1024;    // above
 
 // test(ref[p]) for the pages p = tid, tid + kSmallThreads, ... as a word; counts[t] becomes the number of pages that
 // pass before chunk t / kSmallWarps of kSmallThreads pages and warp t % kSmallWarps in it, *total all that pass.
-// `also(p, r)` sees every page. Ends with a barrier.
-template <typename Test, typename Also>
-__device__ __forceinline__ uint32_t small_ranks(const int32_t *ref, int n_pages, int *counts, int *sh, int *total, Test test,
-                                                Also also) {
+// `also(p, r)` sees every page. Ahead: the thread's first ref is `ahead`. Ends with a barrier.
+template <bool Ahead, typename Test, typename Also>
+__device__ __forceinline__ uint32_t small_ranks(const int32_t *ref, int n_pages, int ahead, int *counts, int *sh, int *total,
+                                                Test test, Also also) {
     const int tid = threadIdx.x, warp = tid >> 5, chunks = (n_pages + kSmallThreads - 1) / kSmallThreads;
     uint32_t mine = 0;
     for (int i0 = 0; i0 < chunks; i0 += 16) {
@@ -506,7 +506,10 @@ __device__ __forceinline__ uint32_t small_ranks(const int32_t *ref, int n_pages,
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int p = (i0 + i) * kSmallThreads + tid;
-            if (p < n_pages) r[i] = ref[p];
+            if (Ahead && i0 == 0 && i == 0)
+                r[i] = ahead;
+            else if (p < n_pages)
+                r[i] = ref[p];
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -563,6 +566,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) fork_small_kernel(ForkArgs a
     s.delta = s.off + a.n_out;
     s.pairs = reinterpret_cast<uint16_t *>(s.delta + a.n_pages);
     s.fresh = s.pairs + a.n_out;
+    const int ahead = tid < a.n_pages ? a.ref[tid] : 0;    // before the rows' dependent loads
     // CTA 0's table entries come along with the first loads
     const int ld = (int)a.ld, entries = a.n_in * ld;
     int entry[kEntriesAhead];
@@ -583,10 +587,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) fork_small_kernel(ForkArgs a
         if (full >= 0 && full + (len != full * ps) > ld) full = -1;
         if (full >= 0 && len != full * ps) {
             last = a.table[p * ld + full];
-            if (last >= 0 && last < a.n_pages)
-                last |= a.ref[last] == 1 ? kAlone : 0;
-            else
-                last = -1;
+            if (last < 0 || last >= a.n_pages) last = -1;
         }
         s.len[p] = len;
         s.full[p] = full;
@@ -595,7 +596,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) fork_small_kernel(ForkArgs a
         s.children[p] = 0;
     }
     int n_free;
-    const uint32_t is_free = small_ranks(a.ref, a.n_pages, counts, sh, &n_free, [](int r) { return r == 0; },
+    const uint32_t is_free = small_ranks<true>(a.ref, a.n_pages, ahead, counts, sh, &n_free, [](int r) { return r == 0; },
                                          [&](int p, int r) { s.delta[p] = r; });
     for_ranks(is_free, a.n_pages, counts, [&](int p, bool free, int rank) {
         if (free) s.fresh[rank] = (uint16_t)p;
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) fork_small_kernel(ForkArgs a
             if (parent >= 0 && s.len[parent] != full * ps) {
                 const int last = s.last[parent];
                 if (last < 0 && blockIdx.x == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePages, i);
-                keep = last >= 0 && (last & kAlone) != 0 && s.first[parent] == i;
+                keep = last >= 0 && s.delta[last] == 1 && s.first[parent] == i;
                 copies = last >= 0 && !keep;
             }
             mine = s.pages[i] - full - keep + (copies << 48);
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) fork_small_kernel(ForkArgs a
     move_pages<kSmallThreads>(pg, n_pairs, a.page_size, [&](int k, int &src, int &dst) {
         const int i = s.pairs[k], parent = s.parent[i], off = s.off[i];
         if (off < 0) return 0;                     // failed
-        src = s.last[parent] & ~kAlone;
+        src = s.last[parent];
         dst = s.fresh[off];                        // a row that copies keeps nothing: no flag
         return s.len[parent] - s.full[parent] * ps;
     });
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) compact_small_kernel(Compact
                    *const holes = movers + (a.n_pages + 1) / 2;
     constexpr uint16_t kFree = 0xFFFF;
     int n_live;
-    const uint32_t is_live = small_ranks(a.ref, a.n_pages, counts, sh, &n_live, [](int r) { return r > 0; }, [](int, int) {});
+    const uint32_t is_live = small_ranks<false>(a.ref, a.n_pages, 0, counts, sh, &n_live, [](int r) { return r > 0; }, [](int, int) {});
     if (tid == 0 && n_live == a.n_pages) moving_sh = 0;
     for_ranks(is_live, a.n_pages, counts, [&](int p, bool live, int below) {
         if (p == n_live) moving_sh = n_live - below;
