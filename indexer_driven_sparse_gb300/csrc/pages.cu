@@ -9,7 +9,7 @@
 //
 // Pools and tables that one CTA can plan in its shared memory (kSmallPages, kSmallRows, kSmallEntries) take a single
 // kernel instead: every CTA makes the whole plan for itself from L2, so none waits for another, and goes on to its
-// share of the tables and copies. Two kernels against one, a call: 9.0 against 6.1 us for a fork of 8 rows, 6.5 against 4.3 us for a
+// share of the tables and copies. Two kernels against one, a call: 9.0 against 5.1 us for a fork of 8 rows, 6.5 against 3.9 us for a
 // small compaction; above the limits the repeated plan would cost more than the second launch.
 #include "paged.cuh"
 
