@@ -794,6 +794,30 @@ def test_calls_take_a_stream(cuda_lib):
     check_decode(out, lse, q, values, table, [70, 3], 16, 0, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("Hq,D,fp8", [(8, 64, False), (8, 256, False), (8, 128, True), (16, 256, True)])
+def test_decode_of_the_longest_sequence(cuda_lib, Hq, D, fp8):
+    """2^31 - 1 tokens, all pages the same one, and a window over the last 100: the last tile reaches past 2^31."""
+    page, n, window = 1 << 20, (1 << 31) - 1, 100
+    groups = D // 128
+    if fp8:
+        planes = [torch.full((1, page, 1, D), 0x7F, dtype=torch.uint8, device=DEV),
+                  torch.full((1, page, 1, groups), float("nan"), device=DEV)]
+        planes += [p.clone() for p in planes]
+    else:
+        planes = [torch.full((1, page, 1, D), float("nan"), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    q, small, values, _, _ = paged_inputs([window], Hq, 1, D, 128, fp8, seed=91, spare=0)
+    at = slice(page - 1 - window, page - 1)               # token n - 1 lies in slot page - 2 of page 2047
+    order = slice(0, window)
+    for p, x in zip(planes, small):
+        p[0, at] = x[0, order]
+    cfg = qb.make_paged_config(Hq, 1, D, page, 0.0, window)
+    ws = qb.paged_workspace(cfg)
+    table = torch.zeros(1, 2048, dtype=torch.int32, device=DEV)
+    out, lse = run_decode(cfg, q, tuple(planes), table, ints([n]), ws)
+    assert status(ws) == (0, 0)
+    check_decode(out, lse, q, values, np.zeros((1, 1), dtype=np.int64), [window], 128, 0, D ** -0.5, fp8)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_far_slots_of_a_large_cache(cuda_lib, fp8):
     """Rows whose byte offsets pass 2^32 (and 2^33 with bf16 rows): appended, attended, copied and compacted."""
