@@ -487,11 +487,14 @@ constexpr int kKeeps = 1 << 30;
 constexpr int kSmallChunks = kSmallPages / kSmallThreads, kSmallWarps = kSmallThreads / 32;
 static_assert(kSmallChunks <= 32 && kSmallChunks * kSmallWarps <= kSmallThreads, "a thread's pages fit a word, the counts a scan");
 
-size_t small_fork_bytes(int n_in, int n_out, int n_pages) {
+// Shared memory of the arrays above, in their order (and 16 bytes), and of compact_small_kernel's.
+constexpr size_t small_fork_bytes(int n_in, int n_out, int n_pages) {
     return (size_t)n_in * 20 + (size_t)n_out * 12 + (size_t)n_pages * 4 + ((size_t)n_out + n_pages + 8) * 2;
 }
-size_t small_compact_bytes(int n_pages) { return ((size_t)n_pages * 2 + 8) * 2; }
-constexpr int kSmallSmem = kSmallRows * 32 + kSmallPages * 6 + 1024;    // above both sums at their limits
+constexpr size_t small_compact_bytes(int n_pages) { return ((size_t)n_pages * 2 + 8) * 2; }
+constexpr size_t kSmallSmem = small_fork_bytes(kSmallRows, kSmallRows, kSmallPages);    // the most that a launch asks for
+static_assert(small_compact_bytes(kSmallPages) <= kSmallSmem, "one limit serves both kernels");
+static_assert(kSmallSmem + kSmallThreads * 4 + 33 * 12 <= 227 * 1024, "with the static arrays: what a CTA may have");
 
 // test(ref[p]) for the pages p = tid, tid + kSmallThreads, ... as a word; counts[t] becomes the number of pages that
 // pass before chunk t / kSmallWarps of kSmallThreads pages and warp t % kSmallWarps in it, *total all that pass.
@@ -780,7 +783,7 @@ cudaError_t launch_small(K kern, const A &a, const PlaneGroups &p, size_t bytes,
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!ready[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }

@@ -952,3 +952,34 @@ def test_workspace_shared_by_other_geometries(cuda_lib):
                           ints(ref.tolist()), t2, l2, r2, [], pws)
         assert np.array_equal(t2.cpu().numpy(), want[0]) and np.array_equal(r2.cpu().numpy(), want[2])
     assert status(big) == (0, 0) and status(pws) == (0, 0)
+
+
+# ------------------------------------------------------------------------------------------ limits of the small plan
+@pytest.mark.parametrize("n_in,n_out,n_pages,ld", [
+    (1024, 1024, 16384, 64), (1025, 1024, 16384, 63), (1024, 1025, 16384, 64), (1024, 1024, 16385, 64),
+    (1024, 1024, 16384, 65), (994, 994, 16384, 64), (1024, 1024, 16211, 64), (1, 1024, 16384, 65536), (1024, 1, 16384, 64)])
+def test_fork_at_the_limits_of_the_single_kernel(cuda_lib, n_in, n_out, n_pages, ld):
+    """The largest tables and pools that one kernel plans, and one row, page or entry more."""
+    page, rng = 4, np.random.default_rng(n_in + n_pages)
+    most = min(ld, n_pages // (2 * max(n_in, n_out))) * page          # half the pool at most, so that every row finds pages
+    lens = rng.integers(0, most + 1, n_in).astype(np.int32)
+    count, order = -(-lens // page), rng.permutation(n_pages)
+    table, ref, at = np.full((n_in, ld), -1, np.int32), np.zeros(n_pages, np.int32), 0
+    for r, c in enumerate(count):
+        table[r, :c] = order[at:at + c]
+        ref[order[at:at + c]] = 1
+        at += c
+    parent, add = rng.integers(-1, n_in, n_out), rng.integers(0, 3, n_out)
+    planes = planes_of(n_pages, page, 3)
+    want = P.fork(table, lens, ref, parent.tolist(), add.tolist(), page)
+    assert want[4] == []
+    want_planes = [copied(p, want[3], page) for p in planes]
+    ws = qb.pages_workspace(max(n_in, n_out), n_pages)
+    t_out = torch.full((n_out, ld), 77, dtype=torch.int32, device=DEV)
+    l_out, r_out = torch.full((n_out,), 77, dtype=torch.int32, device=DEV), torch.full((n_pages,), 77, dtype=torch.int32,
+                                                                                      device=DEV)
+    qb.qsa_fork_pages(page, ints(parent), ints(add), ints(table), ints(lens), ints(ref), t_out, l_out, r_out, planes, ws)
+    assert np.array_equal(t_out.cpu().numpy(), want[0]) and np.array_equal(l_out.cpu().numpy(), want[1])
+    assert np.array_equal(r_out.cpu().numpy(), want[2])
+    assert all(torch.equal(a, b) for a, b in zip(planes, want_planes))
+    assert status(ws) == (0, 0)
