@@ -24,9 +24,10 @@
 //     empty. Two E4M3 values hold bf16's 8 significant bits; the second, at most 2^-4 of the first, is scaled by
 //     another 2^5, so that its step is 2^-21 of the head's largest value (values below 2^-14 of that are rounded by up to
 //     2^-22 of it: a score by 2^-22 max |q| sum |k|). The K scales multiply the fp32 sums of each 128 dims. V's scales
-//     enter the weights, w = 2^(s + log2 v_scale - m) with m the running maximum of that exponent (so that the largest is
-//     1), one set of weights for each 128 dims, rounded to f16: 2^-11 of each, well under the rows' own 2^-4. The
-//     softmax's sum is taken without v_scale, relative to the first set's m.
+//     enter the weights, w = 2^(s + log2 v_scale - m + 15) with m the running maximum of s + log2 v_scale (so that the
+//     largest is 2^15), one set of weights for each 128 dims, rounded to f16: 2^-11 of each down to 2^-29 of the largest,
+//     well under the rows' own 2^-4, and 2^-40 of the largest below that, so that a million tokens that are light
+//     beside one still count. The softmax's sum is taken without v_scale, relative to the first set's m.
 #include "paged.cuh"
 #include "qsa_ptx.cuh"
 
@@ -71,6 +72,9 @@ struct PagedCfg {
     static constexpr int ctas = D == 256 ? 1 : D == 128 ? (F8 ? 3 : 2) : (GT == 8 ? 4 : 3);   // per SM
     static constexpr int p_pitch = tile * 2 + 16;   // bytes between two heads' weights: an odd number of 16-byte chunks
     static constexpr int p_sets = F8 ? groups : 2;  // FP8: one per V scale; bf16: high and low parts
+    // log2 of what the largest weight x V scale of FP8 rows becomes: f16 reaches 2^16, so the weights below its normal range
+    // (2^-14) lie under 2^-29 of the largest, and only those under 2^-40 are lost
+    static constexpr float raise = F8 ? 15.f : 0.f, lower = F8 ? 0x1p-15f : 1.f;
     static constexpr int q_at = stages * stage, p_at = q_at + (stages - 1) * q_bytes, x_at = p_at + p_sets * GT * p_pitch;
     static constexpr int smem = x_at + groups * GT * warps * 4;
 };
@@ -652,7 +656,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
         }
         // S = Q K^T over this warp's tokens; s[nt]: tokens nt x 8 + 2c, + 1 for head rows g (and g + 8)
         float s[NQ][2 * HR];
-        float lv[SG][NQ][2];                       // FP8: log2 of the tokens' V scales
+        float lv[SG][NQ][2];                       // FP8: log2 of the tokens' V scales, raised
         {
             // independent sums (FP8: of each 128 dims)
             constexpr int CH = C::split ? 1 : F8 ? (NQ <= 2 ? 2 : 1) : 4 / NQ > 0 ? 4 / NQ : 1;
@@ -724,7 +728,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                         for (int gr = 0; gr < SG; ++gr) {
                             sc[x][gr] = ks[x * SG + gr];
                             // a scale below 2^-100 counts as that: its row's values are beneath 2^-91; NaN stays NaN
-                            lv[gr][nt][x] = max_nan(lg2(vs[x * SG + gr]), -100.f);
+                            lv[gr][nt][x] = max_nan(lg2(vs[x * SG + gr]), -100.f) + C::raise;
                         }
                 }
 #pragma unroll
@@ -752,7 +756,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                 for (int nt = 0; nt < NQ; ++nt)
                     top = fmaxf(top, F8 ? fmaxf(s[nt][2 * h] + lv[gr][nt][0], s[nt][2 * h + 1] + lv[gr][nt][1])
                                         : fmaxf(s[nt][2 * h], s[nt][2 * h + 1]));
-                top = quad_max(top);
+                top = quad_max(top) - C::raise;
                 if (c == 0) maxima[(gr * GT + g + 8 * h) * W + warp] = top;
             }
         sync_mul();
@@ -874,15 +878,15 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
 #pragma unroll
                 for (int w = 0; w < W; ++w) sum += maxima[row * W + w];
                 const int head = kvh * G + row;
-                // bf16: O / sum, or (m, sum, O) as a partial. FP8: O 2^(m_set - log2 of the softmax's denominator), with
+                // bf16: O / sum, or (m, sum, O) as a partial. FP8: O 2^(m_set - 15 - log2 of the softmax's denominator), with
                 // (that logarithm, 1) as the partial's pair: the sets' maxima may lie far apart
                 const float lse2 = sum == 0.f ? -INFINITY : m[0][h] + log2f(sum);
                 float f;
                 if (F8)
-                    f = sum == 0.f ? 0.f : ex2(m[SG == 2 ? 1 : 0][h] - lse2);
+                    f = sum == 0.f ? 0.f : ex2(m[SG == 2 ? 1 : 0][h] - C::raise - lse2);
                 else
                     f = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-                if (SG == 2 && my_set == 0) f = sum == 0.f ? 0.f : 1.f / sum;
+                if (SG == 2 && my_set == 0) f = sum == 0.f ? 0.f : C::lower / sum;
                 float *po = ws.o + ((int64_t)slot * a.Hq + head) * D + warp * 32;
                 uint16_t *out = a.out + ((int64_t)at.s * a.Hq + head) * D + warp * 32;
 #pragma unroll

@@ -983,3 +983,45 @@ def test_fork_at_the_limits_of_the_single_kernel(cuda_lib, n_in, n_out, n_pages,
     assert np.array_equal(r_out.cpu().numpy(), want[2])
     assert all(torch.equal(a, b) for a, b in zip(planes, want_planes))
     assert status(ws) == (0, 0)
+
+
+# ------------------------------------------------------------------------------------------ light tokens
+@pytest.mark.parametrize("Hq,D", [(8, 256), (16, 256), (8, 128), (16, 128)])
+@pytest.mark.parametrize("nats", [12.0, 15.0, 18.0, 22.0])
+@pytest.mark.parametrize("n", [100, 20000])
+def test_light_tokens_beside_a_heavy_one_over_fp8_rows(cuda_lib, Hq, D, nats, n):
+    """One token `nats` above the others, whose V is zero in a quarter of the dims: there the others alone make the output.
+    A weight x V scale is rounded to f16 relative to the largest, which is 2^15: half a step is 2^-11 of it, and below f16's
+    normal range 2^-25, which is 2^-40 of the largest. The largest times 448 is at most the largest of `mass` in its 128
+    dims, since every row has a code of 448 there, so n tokens add at most n 2^-40 of that."""
+    q, planes, values, tab, table = paged_inputs([n], Hq, 1, D, 16, True, seed=81)
+    g = torch.Generator().manual_seed(4)
+    base = torch.randn(D, generator=g)
+    q.copy_((base + 0.05 * torch.randn(1, Hq, D, generator=g)).to(torch.bfloat16))
+    slot = P.slots_of(table[0], n, 16)[n // 2]
+    heavy = base * (nats / (D ** -0.5 * float(base @ base)))
+    scale = heavy.view(-1, 128).abs().amax(-1) / 448.0
+    codes = (heavy.view(-1, 128) / scale[:, None]).to(torch.float8_e4m3fn)
+    planes[0].flatten(0, 1)[slot, 0] = codes.view(torch.uint8).flatten().to(DEV)
+    planes[1].flatten(0, 1)[slot, 0] = scale.to(DEV)
+    values[0].reshape(-1, D)[slot] = (codes.float().double() * scale.double()[:, None]).flatten().numpy()
+    planes[2].bitwise_and_(0x7F)                          # V is not negative: nothing cancels
+    np.abs(values[1], out=values[1])
+    planes[2].flatten(0, 1)[slot, 0].view(-1, 128)[:, :33] = torch.tensor([0] * 32 + [0x7E], dtype=torch.uint8, device=DEV)
+    values[1].reshape(-1, D // 128, 128)[slot, :, :32] = 0
+    values[1].reshape(-1, D // 128, 128)[slot, :, 32] = 448 * f64(planes[3].flatten(0, 1)[slot, 0])
+    cfg = qb.make_paged_config(Hq, 1, D, 16)
+    ws = qb.paged_workspace(cfg)
+    out, lse = run_decode(cfg, q, planes, tab, ints([n]), ws)
+    at = P.slots_of(table[0], n, 16)
+    K, V = (x.reshape(-1, 1, D)[at] for x in values)
+    want, want_lse, mass, terms = P.decode(f64(q[0]), K, V, 0, D ** -0.5)
+    ds = D * 2.0 ** -24 * terms + 2.0 ** -21 * (terms + 1)
+    if D == 256 and Hq <= 8:                              # queries as two E4M3 values: 2^-22 of the head's largest
+        ds = ds + 2.0 ** -22 * np.abs(f64(q[0])).max(1) * np.abs(K).sum(2).max() * D ** -0.5
+    sums = n / 8 * 2.0 ** -24 + 2.0 ** -15
+    most = np.repeat(mass.reshape(Hq, -1, 128).max(-1), 128, -1)
+    tol = 2.0 ** -8 * np.abs(want) + (2 * ds[:, None] + sums + 2.0 ** -11) * mass + n * 2.0 ** -40 * most
+    assert np.all(np.abs(f64(out[0]) - want) <= tol), np.abs((f64(out[0]) - want) / tol).max()
+    assert np.all(np.abs(f64(lse[0]) - want_lse) <= ds + sums + 2.0 ** -22 * np.abs(want_lse))
+    assert status(ws) == (0, 0)
