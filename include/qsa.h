@@ -525,10 +525,13 @@ typedef struct {
  * one by `scaling`:
  *   LINEAR    f_i / factor;
  *   NTK       the base becomes base x factor^(rot_dim / (rot_dim - 2));
- *   BY_PARTS  f_i (1 - g) + g f_i / factor with g = clamp((i - lo) / (hi - lo), 0, 1), lo = max(floor(c(beta_fast)), 0),
- *             hi = min(ceil(c(beta_slow)), rot_dim / 2 - 1) (hi - lo at least 0.001), c(b) = (rot_dim / 2)
- *             ln(original_len / (2 pi b)) / ln(base): pairs that turn more than beta_fast times over the
- *             trained length stay, those that turn less than beta_slow times are slowed;
+ *   BY_PARTS  the interpolation by parts of YaRN (Peng et al. 2023, "YaRN: Efficient Context Window Extension of Large
+ *             Language Models"): f_i (1 - g) + g f_i / factor with g = clamp((i - lo) / (hi - lo), 0, 1),
+ *             lo = max(floor(c(beta_fast)), 0), hi = min(ceil(c(beta_slow)), rot_dim - 1) (hi - lo at least 0.001),
+ *             c(b) = (rot_dim / 2) ln(original_len / (2 pi b)) / ln(base): pairs that turn more than beta_fast
+ *             times over the trained length stay, those that turn less than beta_slow times are slowed. Where even the
+ *             last pair turns more often than that (small bases, long trained lengths), hi lies past it and the
+ *             ramp is cut off by the head's end;
  *             amplitude = 0.1 ln(factor) + 1 (factor > 1; else 1). The other scalings have amplitude 1. */
 typedef enum {
     QSA_ROPE_NONE = 0,

@@ -131,7 +131,7 @@ QSA_API qsa_status qsa_rope_table(const qsa_rope_config *rope, uint64_t *phase, 
                  "beta_fast must be above beta_slow, and both positive");
         auto at = [&](double beta) { return half * log(rope->original_len / (beta * 2.0 * M_PI)) / log(base); };
         lo = std::max(floor(at(rope->beta_fast)), 0.0);
-        hi = std::min(ceil(at(rope->beta_slow)), half - 1.0);
+        hi = std::min(ceil(at(rope->beta_slow)), rope->rot_dim - 1.0);    // in dims, not pairs: the ramp may end past the last pair
         if (rope->factor > 1.0) *amplitude = (float)(0.1 * log(rope->factor) + 1.0);
     }
     for (int i = 0; i < half; ++i) {

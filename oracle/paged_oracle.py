@@ -26,7 +26,7 @@ def rope_frequencies(rot, base, scaling="none", factor=1.0, original_len=0, beta
     def pair_turning(times):   # index of the pair that turns `times` times over the trained length
         return half * math.log(original_len / (2 * math.pi * times)) / math.log(base)
 
-    lo, hi = max(math.floor(pair_turning(beta_fast)), 0), min(math.ceil(pair_turning(beta_slow)), half - 1)
+    lo, hi = max(math.floor(pair_turning(beta_fast)), 0), min(math.ceil(pair_turning(beta_slow)), rot - 1)
     out = []
     for i in range(half):
         g = min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0)

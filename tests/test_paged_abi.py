@@ -235,3 +235,24 @@ def test_binding_refuses_wrong_tensors(lib):
         qb.rope_table(120, device="cpu")
     t = qb.rope_table(128, 64, device="cpu")
     assert t.phase.shape == (32,) and t.amplitude == 1.0
+
+
+@pytest.mark.parametrize("rot,base,trained,lo,hi", [
+    # by hand: c(b) = rot / 2 x ln(trained / (2 pi b)) / ln(base)
+    (128, 1e4, 131072, 45, 70),    # c(32) = 64 x 6.4798 / 9.2103 = 45.03, c(1) = 64 x 9.9456 / 9.2103 = 69.11: past pair 63
+    (64, 1e4, 262144, 24, 37),     # c(32) = 32 x 7.1730 / 9.2103 = 24.92, c(1) = 32 x 10.6387 / 9.2103 = 36.96: past pair 31
+    (16, 100.0, 65536, 10, 15),    # c(32) = 8 x 5.7867 / 4.6052 = 10.05, c(1) = 8 x 9.2525 / 4.6052 = 16.07: 17, but at most 15
+    (128, 1e6, 32768, 23, 40)])    # c(32) = 64 x 5.0936 / 13.8155 = 23.60, c(1) = 64 x 8.5593 / 13.8155 = 39.65: inside
+def test_rope_by_parts_ramp_may_end_past_the_last_pair(lib, rot, base, trained, lo, hi):
+    """Frequencies of scaling by parts against the ramp's ends worked out by hand."""
+    cfg = rope_cfg(head_dim=256, rot_dim=rot, base=base, scaling=qb.ROPE_SCALINGS.index("by_parts"), factor=4.0,
+                   original_len=trained)
+    st, phase, amp = table_of(lib, cfg)
+    assert st == qb.QSA_OK and abs(amp - (0.1 * np.log(4.0) + 1.0)) < 1e-6
+    i = np.arange(rot // 2)
+    g = np.clip((i - lo) / (hi - lo), 0.0, 1.0)
+    want = base ** (-2.0 * i / rot) * (1.0 - 0.75 * g)
+    turns = phase.astype(np.float64) * 2.0 ** -64
+    assert np.all(np.abs(turns - want / (2 * np.pi)) <= 1e-14 * want + 2.0 ** -64)
+    if rot == 128 and base == 1e4:                        # pair 63: g = 18 / 25, 1e4^(-126/128) x 0.46
+        assert abs(turns[63] * 2 * np.pi - 5.3119e-5) < 1e-8
