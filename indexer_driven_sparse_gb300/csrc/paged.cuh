@@ -9,7 +9,9 @@ constexpr int kWhereAppend = 9, kWherePaged = 10, kWherePages = 11;
 
 // Programmatic dependent launch: a kernel launched by launch_dependent may begin while the kernel before it on the
 // stream ends; it waits for that one's memory before its first access. Every kernel here does that at its start, so
-// each still follows all that came before it; the short streaming ones also let the next one begin at once.
+// each still follows all that came before it; the short streaming ones also let the next one begin at once. What such a
+// kernel reads may thus be written while it already exists: ordinary loads only, since the read-only path (__ldg) is
+// for memory that stays the same from the kernel's beginning. The rotary phases do.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -119,7 +119,7 @@ struct Row {
 template <int T>
 __device__ __forceinline__ Row row_of(const PagedArgs &a, int s) {
     Row r;
-    r.len = __ldg(a.seq_len + s);
+    r.len = a.seq_len[s];
     if (r.len < 0 || r.len > a.ld * a.page_size) r.len = 0;
     r.lo = a.window > 0 ? max(0, r.len - a.window) : 0;
     r.t0 = r.lo / T;
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
             if (offset >= a.page_size) offset -= a.page_size, ++entry;
         }
         wanted = (LT == 32 || lane < LT) && tok >= (uint32_t)in.r.lo && tok < (uint32_t)in.r.len;
-        page = wanted ? __ldg(a.table + in.s * a.ld + entry) : -1;
+        page = wanted ? a.table[in.s * a.ld + entry] : -1;
     };
     auto issue = [&](int stage, int q_slot, bool first) {      // tile `in`
         const uint32_t st = base + stage * C::stage;

@@ -1025,3 +1025,34 @@ def test_light_tokens_beside_a_heavy_one_over_fp8_rows(cuda_lib, Hq, D, nats, n)
     assert np.all(np.abs(f64(out[0]) - want) <= tol), np.abs((f64(out[0]) - want) / tol).max()
     assert np.all(np.abs(f64(lse[0]) - want_lse) <= ds + sums + 2.0 ** -22 * np.abs(want_lse))
     assert status(ws) == (0, 0)
+
+
+# ------------------------------------------------------------------------------------------ attention right behind the page calls
+@pytest.mark.parametrize("rows,fp8", [(3, False), (40, False), (3, True)])
+def test_attention_reads_what_a_fork_right_before_it_wrote(cuda_lib, rows, fp8):
+    """Fork, then attention, many times without a wait in between: each call sees the lengths and pages of its own fork,
+    which swaps rows of different lengths, and of the compaction behind it."""
+    D, page = 128, 8
+    cache = PagedCache(1, 40 * rows, page, rows, 30, 4, 1, D, fp8=fp8)
+    lens = [5 + (37 * r) % 150 for r in range(rows)]
+    cache.fork(ints([-1] * rows), ints(lens))
+    rope = qb.rope_table(D)
+    for r, n in enumerate(lens):
+        x = randn((n, 2, D), seed=200 + r)
+        cache.append(0, rope, None, x[:, :1], x[:, 1:], torch.arange(n, dtype=torch.int32, device=DEV),
+                     torch.full((n,), r, dtype=torch.int32, device=DEV))
+    q = randn((1, 4, D), seed=5).expand(rows, 4, D).contiguous()
+    first = torch.empty_like(q)
+    cache.attend(0, q, first)
+    turn, none = ints([(r + 1) % rows for r in range(rows)]), ints([0] * rows)
+    outs = [torch.empty_like(q) for _ in range(24)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        cache.fork(turn, none)
+        if i % 5 == 4:
+            cache.compact()
+        cache.attend(0, q, out)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(out, first.roll(-(i + 1), 0)), i
+    assert cache.status() == ((0, 0), (0, 0))

@@ -1,6 +1,7 @@
 """Host-side checks of the paged-cache calls (nothing is launched, no GPU is needed) and the rotary table."""
 
 import ctypes as C
+import os
 
 import numpy as np
 import pytest
@@ -256,3 +257,13 @@ def test_rope_by_parts_ramp_may_end_past_the_last_pair(lib, rot, base, trained, 
     assert np.all(np.abs(turns - want / (2 * np.pi)) <= 1e-14 * want + 2.0 ** -64)
     if rot == 128 and base == 1e4:                        # pair 63: g = 18 / 25, 1e4^(-126/128) x 0.46
         assert abs(turns[63] * 2 * np.pi - 5.3119e-5) < 1e-8
+
+
+def test_kernels_that_begin_early_use_no_read_only_loads():
+    """The paged kernels start while the one before them still writes lengths, tables and rows: of all they read only the
+    rotary phases may come through the read-only path."""
+    for name in ("paged.cuh", "paged_decode.cu", "pages.cu", "rope.cu"):
+        with open(os.path.join(qbuild.CSRC, name)) as f:
+            code = [line.split("//")[0] for line in f]
+        assert not any("ld.global.nc" in line or "ldg_nc" in line for line in code), name
+        assert all("r.phase" in line for line in code if "__ldg(" in line), name
