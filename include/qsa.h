@@ -604,7 +604,8 @@ QSA_API qsa_status qsa_rope_append_fp8kv(const qsa_paged_config *cfg, const qsa_
  * one among them, and attends j in [max(0, n - window), n) (all n without a window):
  *   out[s][h] = sum_j softmax_j(scale q[s][h] . K[j]) V[j],   lse[s][h] = ln sum_j e^(scale q.K[j]).
  * A sequence with n = 0 gets out = 0 and lse = -inf. fp32 scores, softmax and sums; the weights enter the
- * second product as the sum of two bf16 values. Pages that no attended token lies in are not read.
+ * second product as the sum of two bf16 values (2^-16 of each; an infinite V value of an attended token gives that
+ * infinity). Pages that no attended token lies in are not read.
  *   q rows of n_q_heads x head_dim, q_ld elements apart (a multiple of 8), 16-byte aligned; k_cache, v_cache
  *   16-byte aligned, device memory or mapped pinned host memory; n_pages page_size < 2^31; seq_len [B];
  *   out [B][n_q_heads][head_dim] bf16, 16-byte aligned; lse [B][n_q_heads] fp32 or NULL.

@@ -16,8 +16,10 @@
 // maxima, each turns its own scores into weights P (in shared memory), and for O += P V each takes 32 dims of V and
 // all tokens. Every warp keeps the same running maximum; the sum of the weights stays with the warp that formed
 // them until a segment ends.
-//   bf16 rows: P = P_hi + P_lo, two bf16 values (2^-17 of each weight): one bf16 would add as much error
-//     as the result's own rounding.
+//   bf16 rows: P = P_hi + P_lo, two bf16 values (2^-16 of each weight): one bf16 would add as much error
+//     as the result's own rounding. P_hi is rounded toward zero and P_lo is at least 2^-126: neither is then zero, or of
+//     another sign than the weight, and an infinite V value stays that infinity instead of becoming inf - inf or 0 x inf
+//     (it is NaN only where its weight underflows, 2^-126 of the largest).
 //   FP8 rows: E4M3 codes are exact in f16. Q enters as f16 scaled by a power of two per head (values below 2^-24 of
 //     the head's largest are rounded there: beneath the fp32 sum's own rounding); or, with 8 head rows of 256 dims, as
 //     the sum of two E4M3 values and K's codes as they are (m16n8k32): the second parts take the M rows that would be
@@ -224,6 +226,11 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint32_t bf16x2_toward_zero(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -286,6 +293,9 @@ __device__ __forceinline__ void write_joined(const PagedArgs &a, int s, int head
         make_uint2(bf16x2(x.x * f, x.y * f), bf16x2(x.z * f, x.w * f));
     if (col == 0 && a.lse) a.lse[(int64_t)s * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
+
+// What is left of a weight w >= 0 beside its high part: above zero unless w is zero.
+__device__ __forceinline__ float low_part(float w, float high) { return fminf(fmaxf(w - high, 0x1p-126f), w); }
 
 // The block's barrier, from more than one place in the code, and that of the multiplying warps.
 __device__ __forceinline__ void sync_all() { asm volatile("bar.sync 0;" ::: "memory"); }
@@ -795,10 +805,10 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                     } else {
                         const float e = ex2(u), f = ex2(v);
                         l[h] += e + f;
-                        const uint32_t w = bf16x2(e, f);
+                        const uint32_t w = bf16x2_toward_zero(e, f);
                         *reinterpret_cast<uint32_t *>(p + nt * 16) = w;
                         *reinterpret_cast<uint32_t *>(p + GT * C::p_pitch + nt * 16) =
-                            bf16x2(e - __uint_as_float(w << 16), f - __uint_as_float(w & 0xFFFF0000u));
+                            bf16x2(low_part(e, __uint_as_float(w << 16)), low_part(f, __uint_as_float(w & 0xFFFF0000u)));
                     }
                 }
             }

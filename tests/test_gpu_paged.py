@@ -1056,3 +1056,30 @@ def test_attention_reads_what_a_fork_right_before_it_wrote(cuda_lib, rows, fp8):
     for i, out in enumerate(outs):
         assert torch.equal(out, first.roll(-(i + 1), 0)), i
     assert cache.status() == ((0, 0), (0, 0))
+
+
+# ------------------------------------------------------------------------------------------ infinite V
+@pytest.mark.parametrize("Hq,D", [(8, 256), (16, 256), (7, 128), (16, 64), (8, 64)])
+@pytest.mark.parametrize("n", [1, 70, 5000])
+def test_decode_infinite_values_stay_infinite(cuda_lib, Hq, D, n):
+    """V infinite in a dim: the output is that infinity there, and the same bits as before elsewhere; infinities of both
+    signs, or a NaN, give NaN."""
+    q, planes, values, tab, table = paged_inputs([n, 60], Hq, 1, D, 16, False, seed=83)
+    cfg = qb.make_paged_config(Hq, 1, D, 16)
+    ws = qb.paged_workspace(cfg)
+    want, want_lse = run_decode(cfg, q, planes, tab, ints([n, 60]), ws)
+    logit = torch.from_numpy(values[0].reshape(-1, D)[P.slots_of(table[0], n, 16)]).float() @ q[0].float().cpu().T
+    slots = P.slots_of(table[0], n, 16)
+    heaviest, lightest = int(slots[int(logit[:, 0].argmax())]), int(slots[int(logit[:, 0].argmin())])
+    flat = planes[1].flatten(0, 1)
+    flat[heaviest, 0, 3], flat[lightest, 0, D - 2] = float("inf"), float("-inf")
+    flat[int(slots[n // 2]), 0, 9] = float("nan")
+    if n > 1:
+        flat[int(slots[0]), 0, 20], flat[int(slots[n - 1]), 0, 20] = float("inf"), float("-inf")
+    out, lse = run_decode(cfg, q, planes, tab, ints([n, 60]), ws)
+    assert bool((out[0, :, 3] == float("inf")).all()) and bool((out[0, :, D - 2] == float("-inf")).all())
+    assert bool(torch.isnan(out[0, :, 9]).all()) and (n == 1 or bool(torch.isnan(out[0, :, 20]).all()))
+    keep = torch.ones(D, dtype=torch.bool, device=DEV)
+    keep[[3, D - 2, 9, 20]] = False
+    assert torch.equal(out[0][:, keep], want[0][:, keep]) and torch.equal(out[1], want[1]) and torch.equal(lse, want_lse)
+    assert status(ws) == (0, 0)
