@@ -588,7 +588,8 @@ QSA_API qsa_status qsa_rope_append(const qsa_paged_config *cfg, const qsa_rope_c
 
 /* qsa_rope_append into FP8 rows: the turned K row (in fp32, not rounded to bf16 first) and the V row are
  * quantised per 128 dims as qsa_quantize_kv_fp8 does (scale = max |x| / 448, E4M3(x / scale), scale 0 and
- * zero codes for zeros).
+ * zero codes for zeros). A NaN gets a NaN code and counts as nothing in max |x|; a group with an infinite value has an
+ * infinite scale, which makes NaN of it.
  *   codes [n_pages][page_size][n_kv_heads][head_dim] uint8, 16-byte aligned; scales [..][head_dim / 128] fp32,
  *   8-byte aligned. */
 QSA_API qsa_status qsa_rope_append_fp8kv(const qsa_paged_config *cfg, const qsa_rope_config *rope,

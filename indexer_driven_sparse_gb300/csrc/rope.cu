@@ -175,8 +175,8 @@ __device__ __forceinline__ float quotient(float x, float scale, float inv) {
     return fmaf(fmaf(-q, scale, x), inv, q);
 }
 
-// Eight values of one 128-dim group (or of two groups, g0 != g1) quantised as quantize_kv_fp8_kernel does: the
-// group's |max| over the row's S threads (a power of two <= 16 that starts at a multiple of S in the warp).
+// Eight values of one 128-dim group (or of two groups, g0 != g1) quantised as quantize_kv_fp8_kernel does, but that a NaN
+// keeps a NaN code in a group without other values too: the group's |max| over the row's S threads (a power of two <= 16 that starts at a multiple of S in the warp).
 template <int S>
 __device__ __forceinline__ void quantise16(const float (&x)[16], const Slot &sl, int s, uint8_t *codes, float *scales,
                                            int groups) {
@@ -198,20 +198,20 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], const Slot &sl,
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
         const float scale = (v ? gb : ga) ? s1 : s0;
-        uint32_t w0 = 0u, w1 = 0u;
-        if (scale > 0.f) {
-            float y[8];
-            if (scale > 0x1p-60f && scale < 0x1p60f) {         // no remainder below the normal range
-                const float inv = __frcp_rn(scale);
+        float y[8];
+        if (scale > 0x1p-60f && scale < 0x1p60f) {             // no remainder below the normal range
+            const float inv = __frcp_rn(scale);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = quotient(x[8 * v + i], scale, inv);
-            } else {
+            for (int i = 0; i < 8; ++i) y[i] = quotient(x[8 * v + i], scale, inv);
+        } else if (scale > 0.f) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[8 * v + i], scale);
-            }
-            w0 = e4m3x2_of(y[0], y[1]) | (e4m3x2_of(y[2], y[3]) << 16);
-            w1 = e4m3x2_of(y[4], y[5]) | (e4m3x2_of(y[6], y[7]) << 16);
+            for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[8 * v + i], scale);
+        } else {                                               // zeros, or NaN, which the maximum leaves out
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = isnan(x[8 * v + i]) ? x[8 * v + i] : 0.f;
         }
+        const uint32_t w0 = e4m3x2_of(y[0], y[1]) | (e4m3x2_of(y[2], y[3]) << 16);
+        const uint32_t w1 = e4m3x2_of(y[4], y[5]) | (e4m3x2_of(y[6], y[7]) << 16);
         *reinterpret_cast<uint2 *>(codes + (v ? sl.b : sl.a)) = make_uint2(w0, w1);
     }
     if (s == 0) {

@@ -1083,3 +1083,33 @@ def test_decode_infinite_values_stay_infinite(cuda_lib, Hq, D, n):
     keep[[3, D - 2, 9, 20]] = False
     assert torch.equal(out[0][:, keep], want[0][:, keep]) and torch.equal(out[1], want[1]) and torch.equal(lse, want_lse)
     assert status(ws) == (0, 0)
+
+
+# ------------------------------------------------------------------------------------------ NaN in an FP8 append
+@pytest.mark.parametrize("D,rot", [(256, 0), (128, 0), (256, 256), (128, 64)])
+def test_append_keeps_what_is_not_a_number(cuda_lib, D, rot):
+    """A group of 128 dims that is NaN throughout, or NaN and zeros, is stored with NaN codes, not as zeros; beside other
+    values a NaN spoils its own code alone (and its pair's, where K turns); attention over it is NaN."""
+    cfg = qb.make_paged_config(2, 1, D, 4)
+    ws, rope = qb.paged_workspace(cfg), qb.rope_table(D, rot)
+    x = randn((4, 2, D), seed=85)
+    x[0, :, :128] = float("nan")                          # a group
+    x[1, :, :128], x[1, :, 5] = 0.0, float("nan")         # NaN among zeros
+    x[2, :, 7] = float("nan")                             # NaN among others
+    x[3, :, :128] = 0.0
+    x[3, :, 1] = -0.0
+    shape = (1, 4, 1, D)
+    kv8 = [torch.full(shape, 17, dtype=torch.uint8, device=DEV), torch.full(shape[:3] + (D // 128,), 2.0, device=DEV),
+           torch.full(shape, 18, dtype=torch.uint8, device=DEV), torch.full(shape[:3] + (D // 128,), 3.0, device=DEV)]
+    qb.qsa_rope_append_fp8kv(cfg, rope, None, x[:, :1], x[:, 1:], ints([0, 1, 2, 3]), ints([0] * 4), None, kv8, ints([[0]]), ws)
+    k, v = (torch.isnan(c[0, :, 0].view(torch.float8_e4m3fn).float()) for c in (kv8[0], kv8[2]))
+    assert bool(v[0, :128].all()) and not v[0, 128:].any()
+    assert v[1].nonzero().flatten().tolist() == [5] and v[2].nonzero().flatten().tolist() == [7] and not v[3].any()
+    assert bool(k[0, :128].all())
+    pair = lambda d: sorted({d, (d + rot // 2) % rot}) if rot and d < rot else [d]  # noqa: E731
+    assert k[1].nonzero().flatten().tolist() == pair(5) and k[2].nonzero().flatten().tolist() == pair(7)
+    assert not kv8[2][0, 3, 0, :128].any() and float(kv8[3][0, 3, 0, 0]) == 0.0        # zeros: zero codes, scale 0
+    q = randn((1, 2, D), seed=86)
+    out, _ = run_decode(cfg, q, kv8, ints([[0]]), ints([1]), ws)
+    assert bool(torch.isnan(out).all())
+    assert status(ws) == (0, 0)
