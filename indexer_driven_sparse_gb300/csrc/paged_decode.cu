@@ -737,8 +737,10 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
 #pragma unroll
                         for (int gr = 0; gr < SG; ++gr) {
                             sc[x][gr] = ks[x * SG + gr];
-                            // a scale below 2^-100 counts as that: its row's values are beneath 2^-91; NaN stays NaN
-                            lv[gr][nt][x] = max_nan(lg2(vs[x * SG + gr]), -100.f) + C::raise;
+                            // a scale below 2^-100 counts as that: its row's values are beneath 2^-91; NaN stays NaN, and
+                            // infinity becomes it: as a maximum it would take every other token's weight to zero
+                            const float v_scale = vs[x * SG + gr];
+                            lv[gr][nt][x] = max_nan(fmaf(v_scale, 0.f, lg2(v_scale)), -100.f) + C::raise;
                         }
                 }
 #pragma unroll

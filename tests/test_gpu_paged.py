@@ -1113,3 +1113,27 @@ def test_append_keeps_what_is_not_a_number(cuda_lib, D, rot):
     out, _ = run_decode(cfg, q, kv8, ints([[0]]), ints([1]), ws)
     assert bool(torch.isnan(out).all())
     assert status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("Hq,D", [(8, 256), (16, 256), (8, 128), (16, 128)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("n", [70, 3000])
+def test_decode_value_scale_that_is_not_finite_spoils_its_dims_alone(cuda_lib, Hq, D, value, n):
+    lens = [n, 50]
+    q, planes, values, tab, table = paged_inputs(lens, Hq, 1, D, 16, True, seed=75)
+    cfg = qb.make_paged_config(Hq, 1, D, 16)
+    ws = qb.paged_workspace(cfg)
+    want, want_lse = run_decode(cfg, q, planes, tab, ints(lens), ws)
+    for group in range(D // 128):
+        keep = planes[3].clone()
+        planes[3][int(table[0][1]), 3, 0, group] = value   # token 19 of row 0
+        out, lse = run_decode(cfg, q, planes, tab, ints(lens), ws)
+        planes[3].copy_(keep)
+        dims = torch.arange(D, device=DEV) // 128 == group
+        assert bool(torch.isnan(out[0][:, dims]).all()) and torch.equal(out[1], want[1])
+        # weights are relative to the largest, which this token's may have been: each side rounds them to f16 (2^-11 of a
+        # sum of at most max |V|) and its result to bf16 (2^-8); the sums' fp32 rounding is far below
+        a, b = f64(out[0][:, ~dims]), f64(want[0][:, ~dims])
+        assert np.all(np.abs(a - b) <= 2.0 ** -7 * np.abs(b) + 2.0 ** -10 * np.nanmax(np.abs(values[1])))
+        assert np.abs(f64(lse) - f64(want_lse)).max() <= 2.0 ** -20 * (1 + np.abs(f64(want_lse)).max())
+    assert status(ws) == (0, 0)
