@@ -234,14 +234,22 @@ def _workspace(nbytes: int, device):
     return ws
 
 
+def _on_stream(stream):
+    """The stream of a call (None, a torch stream or a cudaStream_t) as torch's current one."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream())
+
+
 class PagedCache:
     """K/V of every layer in one pool of pages, and the sequences that share it: row r of `table` lists the
     pages of sequence r, `seq_len[r]` its tokens and `ref[p]` the rows that name page p.
 
-    A decode step is ``extend`` (room for the new tokens), then per layer ``append`` and ``attend``; ``fork``
-    lets rows continue other rows (beams, shared prompts) or gives their pages back, and ``compact`` moves
-    the live pages to the front of the pool. Nothing here synchronises; ``status`` does. ``fork`` and ``compact``
-    write beside what they read and then change over: a captured CUDA graph holds an even number of each."""
+    A decode step is ``extend`` (room for the new tokens of the rows in use), then per layer ``append`` and
+    ``attend``; ``fork`` starts rows, lets them continue other rows (beams, shared prompts) or gives their pages
+    back, and ``compact`` moves the live pages to the front of the pool. A row that finds no page left becomes empty,
+    which ``status`` tells. Nothing else here synchronises. ``fork`` (``extend`` with it) and ``compact`` write
+    beside what they read and then change over: a captured CUDA graph holds an even number of each."""
 
     def __init__(self, n_layers: int, n_pages: int, page_size: int, n_rows: int, max_pages: int, n_q_heads: int,
                  n_kv_heads: int, head_dim: int = 256, fp8: bool = False, softmax_scale: float = 0.0, window: int = 0,
@@ -263,7 +271,7 @@ class PagedCache:
         self._refs = [torch.zeros(n_pages, **i32) for _ in range(2)]
         self._now, self._ref_now = 0, 0
         self._rows = torch.arange(n_rows, **i32)
-        self._one = torch.ones(n_rows, **i32)
+        self._one = torch.zeros(n_rows, **i32)        # extend's: 1 for each row that holds tokens
         self.ws = qb.paged_workspace(self.cfg, device)
         self.pages_ws = qb.pages_workspace(n_rows, n_pages, device)
 
@@ -287,8 +295,11 @@ class PagedCache:
         self._now, self._ref_now = new, new_ref
 
     def extend(self, add=None, stream=None):
-        """Room for add[i] more tokens in row i (None: one each)."""
-        self.fork(self._rows, self._one if add is None else add, stream)
+        """Room for add[i] more tokens in row i (None: one in each row that holds tokens, none in the empty ones)."""
+        if add is None:
+            with _on_stream(stream):
+                add = torch.clamp(self.seq_len, 0, 1, out=self._one)
+        self.fork(self._rows, add, stream)
 
     def compact(self, stream=None):
         new_ref = 1 - self._ref_now

@@ -1137,3 +1137,39 @@ def test_decode_value_scale_that_is_not_finite_spoils_its_dims_alone(cuda_lib, H
         assert np.all(np.abs(a - b) <= 2.0 ** -7 * np.abs(b) + 2.0 ** -10 * np.nanmax(np.abs(values[1])))
         assert np.abs(f64(lse) - f64(want_lse)).max() <= 2.0 ** -20 * (1 + np.abs(f64(want_lse)).max())
     assert status(ws) == (0, 0)
+
+
+# ------------------------------------------------------------------------------------------ rows that nobody uses
+@pytest.mark.parametrize("kind", ["none", "stream", "pointer", "zero"])
+def test_extend_leaves_empty_rows_empty(cuda_lib, kind):
+    own = torch.cuda.Stream()
+    side = {"none": None, "stream": own, "pointer": own.cuda_stream, "zero": 0}[kind]
+    cache = PagedCache(1, 12, 4, 5, 6, 4, 2, 64)
+    cache.fork(ints([-1] * 5), ints([3, 0, 8, 1, 0]))
+    cache.fork(ints([0, 1, 2, -1, 4]), ints([0] * 5))     # row 3 is given back
+    torch.cuda.synchronize()
+    for step in range(1, 10):
+        cache.extend(stream=side)
+        torch.cuda.synchronize()
+        assert cache.seq_len.tolist() == [3 + step, 0, 8 + step, 0, 0]
+    assert int((cache.ref > 0).sum()) == 3 + 5 and cache.status() == ((0, 0), (0, 0))
+    assert cache.table[[1, 3, 4]].eq(-1).all()
+    cache.extend(ints([0, 2, 0, 0, 1]))                   # by name: any row
+    assert cache.seq_len.tolist() == [12, 2, 17, 0, 1]
+
+
+def test_captured_extends_grow_the_rows_in_use(cuda_lib):
+    cache = PagedCache(1, 20, 4, 3, 6, 4, 2, 64)
+    cache.fork(ints([-1] * 3), ints([3, 0, 8]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        cache.extend()
+        cache.extend()
+    for i in range(3):
+        with torch.cuda.stream(side):
+            g.replay()
+        side.synchronize()
+        assert cache.seq_len.tolist() == [5 + 2 * i, 0, 10 + 2 * i]
+    assert cache.status() == ((0, 0), (0, 0))
