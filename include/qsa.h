@@ -553,7 +553,8 @@ typedef struct {
 
 /* Host only: the table the rotary kernels read. phase[i] (rot_dim / 2 entries, HOST memory) is f_i / (2 pi)
  * modulo 1 as a 64-bit binary fraction of a turn, so position x phase modulo 2^64 is the angle exactly:
- * positions of millions lose nothing. *amplitude as above. Copy phase to the device once and keep it. */
+ * positions of millions lose nothing. *amplitude as above. Copy phase to the device once and keep it. A factor
+ * that makes a frequency or the NTK base infinite or zero is QSA_ERR_INVALID_ARGUMENT. */
 QSA_API qsa_status qsa_rope_table(const qsa_rope_config *rope, uint64_t *phase, float *amplitude);
 
 /* Turn rows: out[n][h] = rotary(x[n][h], pos[n]) for n < N, h < n_heads, in fp32 with one rounding to bf16.

@@ -125,6 +125,7 @@ QSA_API qsa_status qsa_rope_table(const qsa_rope_config *rope, uint64_t *phase, 
     *amplitude = 1.f;
     if (scaling == QSA_ROPE_NTK && rope->rot_dim > 2)
         base *= pow(rope->factor, rope->rot_dim / (rope->rot_dim - 2.0));
+    QSA_NEED(call, isfinite(base) && base > 0.0, "factor %g takes the base out of range", rope->factor);
     if (scaling == QSA_ROPE_BY_PARTS) {
         QSA_NEED(call, rope->original_len > 0, "original_len must be positive");
         QSA_NEED(call, isfinite(rope->beta_fast) && rope->beta_slow > 0.0 && rope->beta_fast > rope->beta_slow,
@@ -141,6 +142,7 @@ QSA_API qsa_status qsa_rope_table(const qsa_rope_config *rope, uint64_t *phase, 
             const double g = std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
             f = f * (1.0 - g) + f / rope->factor * g;
         }
+        QSA_NEED(call, isfinite(f), "factor %g makes pair %d's frequency infinite", rope->factor, i);
         const double turn = f / (2.0 * M_PI);
         phase[i] = (uint64_t)ldexp(turn - floor(turn), 64);   // below 2^64: the fraction is at most 1 - 2^-53
     }

@@ -267,3 +267,11 @@ def test_kernels_that_begin_early_use_no_read_only_loads():
             code = [line.split("//")[0] for line in f]
         assert not any("ld.global.nc" in line or "ldg_nc" in line for line in code), name
         assert all("r.phase" in line for line in code if "__ldg(" in line), name
+
+
+@pytest.mark.parametrize("bad", [dict(scaling=1, factor=1e-320), dict(scaling=2, factor=1e-300, rot_dim=16),
+                                 dict(scaling=2, factor=1e300, rot_dim=16), dict(scaling=3, factor=5e-324)])
+def test_rope_table_refuses_factors_out_of_range(lib, bad):
+    """A frequency that is no number has no fraction of a turn."""
+    assert table_of(lib, rope_cfg(**bad))[0] == BAD
+    assert b"factor" in lib.qsa_last_error()
