@@ -166,10 +166,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, RopeRows
     turn_heads<Inter>(r, a.x + n * a.x_ld, a.out + n * a.out_ld, r.D, sl, a.pos[n], h0, min(a.H, h0 + run));
 }
 
-// x / scale for inv = RN(1 / scale): one correction of the product by the reciprocal. For scale = RN(amax / 448) of any
-// bf16 amax and any bf16 x this is the correctly rounded quotient (all 128 x 128 pairs of significands compared in
-// exact arithmetic; powers of two do not matter in the range quantise16 uses it in); for a turned fp32 x it is
-// at most one unit in the last place off.
+// x / scale for inv = RN(1 / scale): the product by the reciprocal, corrected once by its remainder (Markstein 1990,
+// "Computation of elementary functions on the IBM RISC System/6000 processor"). For scale = RN(amax / 448) of any bf16 amax
+// and any bf16 x this is the correctly rounded quotient (tests/test_paged_abi.py goes through all 128 x 128 pairs of
+// significands in exact arithmetic; powers of two do not matter in the range quantise16 uses it in); for a turned
+// fp32 x it is at most one unit in the last place off.
 __device__ __forceinline__ float quotient(float x, float scale, float inv) {
     const float q = x * inv;
     return fmaf(fmaf(-q, scale, x), inv, q);

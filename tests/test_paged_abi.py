@@ -275,3 +275,28 @@ def test_rope_table_refuses_factors_out_of_range(lib, bad):
     """A frequency that is no number has no fraction of a turn."""
     assert table_of(lib, rope_cfg(**bad))[0] == BAD
     assert b"factor" in lib.qsa_last_error()
+
+
+def test_corrected_quotient_of_bf16_values_is_correctly_rounded():
+    """The FP8 append divides x by scale = RN(amax / 448) as q = RN(x RN(1 / scale)), then RN(q + RN(x - q scale) RN(1 / scale))
+    with fused multiply-adds: the correctly rounded quotient for all pairs of bf16 significands, and one unit in the last
+    place off at most for 24-bit x. fp32 operations round once; the products below have 48 bits and the remainder
+    cancels, so both are exact in fp64; the last sum is checked not to lie where rounding it twice could matter."""
+    f32, f64 = np.float32, np.float64
+    rng = np.random.default_rng(0)
+    short = np.arange(128, 256, dtype=f32) / f32(128)
+    wide = rng.integers(1 << 23, 1 << 24, 512).astype(f32) / f32(1 << 23)
+    for a in short:
+        scale = f32(a / f32(448))
+        inv = f32(f32(1) / scale)
+        for xs in (short, wide):
+            q = xs * inv
+            rest = (xs.astype(f64) - q.astype(f64) * f64(scale)).astype(f32)
+            total = q.astype(f64) + rest.astype(f64) * f64(inv)
+            got = total.astype(f32)
+            want = xs / scale
+            ulp = np.spacing(want)
+            assert got.dtype == want.dtype == f32 and q.dtype == f32
+            # fp64 rounds `total` by 2^-53 of it, far less than its distance to the middle between two fp32 values
+            assert np.all(np.abs(np.abs(total - got.astype(f64)) - ulp / f64(2)) > f64(2) ** -48 * total)
+            assert np.array_equal(got, want) if xs is short else np.all(np.abs(got - want) <= ulp)
