@@ -20,8 +20,8 @@
 //     as the result's own rounding. P_hi is rounded toward zero and P_lo is at least 2^-126: neither is then zero, or of
 //     another sign than the weight, and an infinite V value stays that infinity instead of becoming inf - inf or 0 x inf
 //     (it is NaN only where its weight underflows, 2^-126 of the largest).
-//   FP8 rows: E4M3 codes are exact in f16. Q enters as f16 scaled by a power of two per head (values below 2^-24 of
-//     the head's largest are rounded there: beneath the fp32 sum's own rounding); or, with 8 head rows of 256 dims, as
+//   FP8 rows: E4M3 codes are exact in f16. Q enters as f16 scaled by a power of two per head (exact down to 2^-17 of the head's
+//     largest, below that off by at most 2^-25 of it: beneath the fp32 sum's own rounding); or, with 8 head rows of 256 dims, as
 //     the sum of two E4M3 values and K's codes as they are (m16n8k32): the second parts take the M rows that would be
 //     empty. Two E4M3 values hold bf16's 8 significant bits; the second, at most 2^-4 of the first, is scaled by
 //     another 2^5, so that its step is 2^-21 of the head's largest value (values below 2^-14 of that are rounded by up to
@@ -308,32 +308,26 @@ __device__ __forceinline__ void sync_some() {
 // values divided by scale[h], a power of two. A warp takes every W-th head.
 template <int D, int GT, int W>
 __device__ __forceinline__ void split_queries(uint32_t queries, int warp, int lane, float *scale) {
+    static_assert(D == 256, "a lane has 8 dims");
     for (int h = warp; h < GT; h += W) {
-        constexpr int PD = D / 32;     // dims of a lane
         const uint32_t qrow = queries + h * D * 2, hx = h & 7;
-        uint32_t x[PD / 2];
-        if (PD == 8)
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[PD / 2 - 2]), "=r"(x[PD / 2 - 1])
-                         : "r"(qrow + ((lane ^ hx) << 4))
-                         : "memory");
-        else
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                         : "=r"(x[0]), "=r"(x[1])
-                         : "r"(qrow + (((lane >> 1) ^ hx) << 4) + (lane & 1) * 8)
-                         : "memory");
+        uint32_t x[4];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(qrow + ((lane ^ hx) << 4))
+                     : "memory");
         float top = 0.f;
 #pragma unroll
-        for (int k = 0; k < PD / 2; ++k)
+        for (int k = 0; k < 4; ++k)
             top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
 #pragma unroll
         for (int n = 16; n >= 1; n >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, n));
         const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -119), 126);
         // the largest becomes 2^7 .. 2^8; an infinite one makes the head NaN, not E4M3's largest value
         const float down = top == INFINITY ? NAN : __uint_as_float((uint32_t)(134 - e) << 23);
-        uint32_t part[2][PD / 4];
+        uint32_t part[2][2];
 #pragma unroll
-        for (int k = 0; k < PD / 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
             part[0][k] = part[1][k] = 0u;
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
@@ -347,17 +341,10 @@ __device__ __forceinline__ void split_queries(uint32_t queries, int warp, int la
         }
         __syncwarp();
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            if (PD == 8)
-                asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(qrow + (((z * D / 16 + (lane >> 1)) ^ hx) << 4) +
-                                                                     (lane & 1) * 8),
-                             "r"(part[z][0]), "r"(part[z][PD / 4 - 1])
-                             : "memory");
-            else
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(qrow + (((z * D / 16 + (lane >> 2)) ^ hx) << 4) + (lane & 3) * 4),
-                             "r"(part[z][0])
-                             : "memory");
-        }
+        for (int z = 0; z < 2; ++z)
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(qrow + (((z * D / 16 + (lane >> 1)) ^ hx) << 4) + (lane & 1) * 8),
+                         "r"(part[z][0]), "r"(part[z][1])
+                         : "memory");
         if (lane == 0) scale[h] = __uint_as_float((uint32_t)(120 + e) << 23);
     }
 }
@@ -456,18 +443,15 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
     const long long n_tiles = x1 - x0;
     if (kvh == 0 && tid == 0) ws.meta[range] = make_int2(-1, 0);
 
-    auto empty_rows = [&](int threads) {           // rows without a token: zeros, by the first `threads`
-        for (int s = range; s < a.B; s += ranges) {
-            const Row r = row_of<T>(a, s);
-            if (r.t1 > r.t0) continue;
-            const int len = a.seq_len[s];
-            if (len != 0 && kvh == 0 && tid == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, s);
-            uint16_t *o = a.out + ((int64_t)s * a.Hq + kvh * G) * D;
-            for (int i = tid; i < G * D / 8; i += threads) reinterpret_cast<uint4 *>(o)[i] = make_uint4(0, 0, 0, 0);
-            if (a.lse && tid < G) a.lse[(int64_t)s * a.Hq + kvh * G + tid] = -INFINITY;
-        }
-    };
-    empty_rows(C::threads);
+    for (int s = range; s < a.B; s += ranges) {    // rows without a token: zeros
+        const Row r = row_of<T>(a, s);
+        if (r.t1 > r.t0) continue;
+        const int len = a.seq_len[s];
+        if (len != 0 && kvh == 0 && tid == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWherePaged, s);
+        uint16_t *o = a.out + ((int64_t)s * a.Hq + kvh * G) * D;
+        for (int i = tid; i < G * D / 8; i += C::threads) reinterpret_cast<uint4 *>(o)[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse && tid < G) a.lse[(int64_t)s * a.Hq + kvh * G + tid] = -INFINITY;
+    }
     if (n_tiles == 0) return;
     const uint32_t base = smem_u32(smem);
 
@@ -586,14 +570,14 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
             const uint32_t qa = base + C::q_at + q_slot * C::q_bytes;
             q_slot = q_slot + 1 == NS - 1 ? 0 : q_slot + 1;
             if (!F8) {
-                if (GT == 16) {
+                if constexpr (GT == 16) {
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         const int h = (lane & 7) + ((lane >> 3) & 1) * 8, ch = 2 * k + (lane >> 4);
                         uint32_t r[4];
                         ldmatrix4(qa + h * D * 2 + ((ch ^ (h & 7)) << 4), r);
                         qf[k][0] = r[0], qf[k][1] = r[2];
-                        qf[k][2 * HR - 2] = GT == 16 ? r[1] : r[0], qf[k][2 * HR - 1] = GT == 16 ? r[3] : r[2];
+                        qf[k][2] = r[1], qf[k][3] = r[3];
                     }
                 } else {
 #pragma unroll

@@ -181,7 +181,7 @@ __device__ __forceinline__ float quotient(float x, float scale, float inv) {
 template <int S>
 __device__ __forceinline__ void quantise16(const float (&x)[16], const Slot &sl, int s, uint8_t *codes, float *scales,
                                            int groups) {
-    const unsigned mask = (S == 32 ? 0xffffffffu : ((1u << S) - 1u)) << ((threadIdx.x & 31) & ~(S - 1));
+    const unsigned mask = ((1u << S) - 1u) << ((threadIdx.x & 31) & ~(S - 1));
     const int ga = sl.a >> 7, gb = sl.b >> 7;
     float ma = 0.f, mb = 0.f;
 #pragma unroll
