@@ -9,8 +9,11 @@
 //
 // Pools and tables that one CTA can plan in its shared memory (kSmallPages, kSmallRows, kSmallEntries) take a single
 // kernel instead: every CTA makes the whole plan for itself from L2, so none waits for another, and goes on to its
-// share of the tables and copies. Two kernels against one, a call: 9.0 against 5.1 us for a fork of 8 rows, 6.5 against 3.9 us for a
-// small compaction; above the limits the repeated plan would cost more than the second launch.
+// share of the tables and copies. The plan's time grows with the pages and the table's entries, that of two kernels hardly; the
+// limits are where they meet. One kernel against two, extending every row by a token (captured, 20 in a row):
+//   pages 1,024: 5.4 and 8.1 us with 1,024 entries, 8.0 and 8.2 with 8,192, 10.8 and 8.1 with 16,384 (64 or 256 rows);
+//   4,096: 6.2 and 8.2, 9.0 and 8.4, 13.4 and 8.5; 8,192: 7.3 and 8.6, 10.0 and 8.8, 14.5 and 9.0; 12,288 with 1,024: 8.8 and 8.4;
+//   1,024 rows of 4 entries over 4,096 pages: 9.2 and 9.3. Compaction: 600 pages 2.9 and 4.5, 8,192 5.4 either way, 16,384 9.2 and 5.5.
 #include "paged.cuh"
 
 #include <algorithm>
@@ -25,10 +28,10 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveBytes = 4096;       // one warp's share of a page copy at a time: eight 16-byte words a lane, in two goes
 constexpr int kSharedRows = 4096;      // per-parent words kept in shared memory up to this many rows
 constexpr int kSmallThreads = 512;
-constexpr int kSmallPages = 16384;     // page ids in 16 bits, at most 96 KB of shared memory for the pages
+constexpr int kSmallPages = 8192;      // page ids in 16 bits
 constexpr int kSmallRows = 1024;
-constexpr int64_t kSmallEntries = 65536;   // table entries whose references one CTA counts
-constexpr int kEntriesAhead = 12;      // ... this many of each thread's loaded before the plan
+constexpr int64_t kSmallEntries = 8192;    // table entries whose references one CTA counts
+constexpr int kEntriesAhead = 12;      // ... this many of each thread's loaded before the plan, as many as there are registers for
 
 struct RowCopy {                       // new page fresh[off] becomes page src's first `used` tokens
     int32_t src, off, used;
@@ -494,7 +497,7 @@ constexpr size_t small_fork_bytes(int n_in, int n_out, int n_pages) {
 constexpr size_t small_compact_bytes(int n_pages) { return ((size_t)n_pages * 2 + 8) * 2; }
 constexpr size_t kSmallSmem = small_fork_bytes(kSmallRows, kSmallRows, kSmallPages);    // the most that a launch asks for
 static_assert(small_compact_bytes(kSmallPages) <= kSmallSmem, "one limit serves both kernels");
-static_assert(kSmallSmem + kSmallThreads * 4 + 33 * 12 <= 227 * 1024, "with the static arrays: what a CTA may have");
+static_assert(2 * (kSmallSmem + kSmallThreads * 4 + 33 * 12 + 1024) <= 228 * 1024, "two CTAs, with their static arrays, on an SM");
 
 // test(ref[p]) for the pages p = tid, tid + kSmallThreads, ... as a word; counts[t] becomes the number of pages that
 // pass before chunk t / kSmallWarps of kSmallThreads pages and warp t % kSmallWarps in it, *total all that pass.
@@ -775,7 +778,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) compact_small_kernel(Compact
     });
 }
 
-// CTAs of the small kernels: two for each of 152 SMs where their shared memory allows it. The first call on a device raises the shared-memory limit.
+// CTAs of the small kernels: two for each of 152 SMs. The first call on a device raises the shared-memory limit.
 template <typename K, typename A>
 cudaError_t launch_small(K kern, const A &a, const PlaneGroups &p, size_t bytes, bool (&ready)[64], cudaStream_t st) {
     int dev = 0;
@@ -787,7 +790,7 @@ cudaError_t launch_small(K kern, const A &a, const PlaneGroups &p, size_t bytes,
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    return launch_dependent(kern, dim3(bytes <= 100 * 1024 ? 152 * 2 : 152), kSmallThreads, bytes, st, a, p);
+    return launch_dependent(kern, dim3(152 * 2), kSmallThreads, bytes, st, a, p);
 }
 
 // CTAs of the copying kernels: four for each of 152 SMs.

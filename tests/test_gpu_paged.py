@@ -957,7 +957,9 @@ def test_workspace_shared_by_other_geometries(cuda_lib):
 # ------------------------------------------------------------------------------------------ limits of the small plan
 @pytest.mark.parametrize("n_in,n_out,n_pages,ld", [
     (1024, 1024, 16384, 64), (1025, 1024, 16384, 63), (1024, 1025, 16384, 64), (1024, 1024, 16385, 64),
-    (1024, 1024, 16384, 65), (994, 994, 16384, 64), (1024, 1024, 16211, 64), (1, 1024, 16384, 65536), (1024, 1, 16384, 64)])
+    (1024, 1024, 16384, 65), (994, 994, 16384, 64), (1024, 1024, 16211, 64), (1, 1024, 16384, 65536), (1024, 1, 16384, 64),
+    (1024, 1024, 8192, 8), (1025, 1024, 8192, 7), (1024, 1025, 8192, 8), (1024, 1024, 8193, 8), (1024, 1024, 8192, 9),
+    (1, 1024, 8192, 8192), (1, 1, 8192, 8193), (1024, 1, 8192, 8)])
 def test_fork_at_the_limits_of_the_single_kernel(cuda_lib, n_in, n_out, n_pages, ld):
     """The largest tables and pools that one kernel plans, and one row, page or entry more."""
     page, rng = 4, np.random.default_rng(n_in + n_pages)
