@@ -487,6 +487,7 @@ struct SmallFork {
     uint16_t *fresh;                       // [n_pages] free pages in order
 };
 constexpr int kKeeps = 1 << 30;
+constexpr int kFewPages = 8;
 constexpr int kSmallChunks = kSmallPages / kSmallThreads, kSmallWarps = kSmallThreads / 32;
 static_assert(kSmallChunks <= 32 && kSmallChunks * kSmallWarps <= kSmallThreads, "a thread's pages fit a word, the counts a scan");
 
@@ -688,14 +689,25 @@ __global__ void __launch_bounds__(kSmallThreads, 2) fork_small_kernel(ForkArgs a
             if (tid + i * kSmallThreads < entries) count(entry[i]);
 #pragma unroll 4
         for (int x = tid + kEntriesAhead * kSmallThreads; x < entries; x += kSmallThreads) count(a.table[x]);
-        // new pages were free: each is named once
-        for (int i = tid; i < a.n_out; i += kSmallThreads) {
+        // new pages were free: each is named once. A thread takes a row's first few, warps the rest of a row that starts
+        // with many, as a prompt does: 1,000 pages 8.5 us, by one thread 29.8
+        auto new_pages = [&](int i) {
             const int off = s.off[i], parent = s.parent[i];
-            if (off < 0) continue;
-            const int mine = s.pages[i] - (parent >= 0 ? s.full[parent] : 0) - (off & kKeeps ? 1 : 0);
-            for (int k = 0; k < mine; ++k) atomicAdd(s.delta + s.fresh[(off & ~kKeeps) + k], 1);
+            return off < 0 ? 0 : s.pages[i] - (parent >= 0 ? s.full[parent] : 0) - (off & kKeeps ? 1 : 0);
+        };
+        bool many = false;
+        for (int i = tid; i < a.n_out; i += kSmallThreads) {
+            const int mine = new_pages(i), off = s.off[i] & ~kKeeps;
+            for (int k = 0; k < min(mine, kFewPages); ++k) atomicAdd(s.delta + s.fresh[off + k], 1);
+            many |= mine > kFewPages;
         }
-        __syncthreads();
+        if (__syncthreads_or(many)) {
+            for (int i = tid >> 5; i < a.n_out; i += kSmallWarps) {
+                const int mine = new_pages(i), off = s.off[i] & ~kKeeps;
+                for (int k = kFewPages + lane; k < mine; k += 32) atomicAdd(s.delta + s.fresh[off + k], 1);
+            }
+            __syncthreads();
+        }
         for (int x = tid; x < a.n_pages; x += kSmallThreads) a.ref_out[x] = s.delta[x];
     }
     for (int i = warp; i < a.n_out; i += warps) {

@@ -1175,3 +1175,34 @@ def test_captured_extends_grow_the_rows_in_use(cuda_lib):
         side.synchronize()
         assert cache.seq_len.tolist() == [5 + 2 * i, 0, 10 + 2 * i]
     assert cache.status() == ((0, 0), (0, 0))
+
+
+@pytest.mark.parametrize("n_pages,ld", [(3000, 900), (8192, 1024), (8193, 1024)])
+def test_fork_starts_long_rows_beside_short_ones(cuda_lib, n_pages, ld):
+    """Prompts of hundreds of pages start in some rows while others go on, end, find no page or share a last page."""
+    page, rng = 4, np.random.default_rng(n_pages)
+    lens = np.array([9, 0, 31, 4, 700, 2, 12], np.int32)
+    table, ref, at = np.full((7, ld), -1, np.int32), np.zeros(n_pages, np.int32), 0
+    order = rng.permutation(n_pages)
+    for r, n in enumerate(lens):
+        c = -(-int(n) // page)
+        table[r, :c] = order[at:at + c]
+        ref[order[at:at + c]] = 1
+        at += c
+    parent = [-1, 0, 0, -1, 2, -1, 4, 5, 4, -1]
+    add = [4 * 800 - 3, 1, 2500, 4 * 8, 0, 4 * 9 + 1, 300, 1, 0, 4 * (ld if n_pages == 3000 else 9)]
+    if n_pages == 3000:
+        parent, add = parent + [-1] * 3, add + [4 * 700] * 3     # the last finds too few pages
+    want = P.fork(table, lens, ref, parent, add, page)
+    assert (want[4] == []) == (n_pages != 3000)
+    planes = planes_of(n_pages, page, 6)
+    want_planes = [copied(p, want[3], page) for p in planes]
+    ws = qb.pages_workspace(len(parent), n_pages)
+    t_out = torch.full((len(parent), ld), 77, dtype=torch.int32, device=DEV)
+    l_out, r_out = ints([77] * len(parent)), ints([77] * n_pages)
+    qb.qsa_fork_pages(page, ints(parent), ints(add), ints(table), ints(lens), ints(ref), t_out, l_out, r_out, planes, ws)
+    assert np.array_equal(t_out.cpu().numpy(), want[0]) and np.array_equal(l_out.cpu().numpy(), want[1])
+    assert np.array_equal(r_out.cpu().numpy(), want[2])
+    assert all(torch.equal(a, b) for a, b in zip(planes, want_planes))
+    st, row = status(ws)
+    assert (st, row) == (0, 0) if not want[4] else st == qb.QSA_ERR_DEVICE_BOUNDS and row in want[4]
