@@ -661,7 +661,8 @@ QSA_API size_t qsa_pages_workspace_size(int32_t n_rows, int64_t n_pages);
  *   ref, ref_out [n_pages] (another array); n_in, n_out <= 65536. planes: n_groups <= 8 groups (HOST
  *   array; 0 groups: bookkeeping alone).
  * A row that runs out of pages or of the table's ld, or names a parent outside [0, n_in), becomes empty
- * and QSA_ERR_DEVICE_BOUNDS is recorded with its index. */
+ * and QSA_ERR_DEVICE_BOUNDS is recorded with its index; what a row short of pages would have taken is not handed to
+ * later rows. */
 QSA_API qsa_status qsa_fork_pages(int32_t page_size, const int32_t *parent, const int32_t *add, int32_t n_out,
                                   const int32_t *table, const int32_t *seq_len, int32_t n_in, int64_t ld,
                                   const int32_t *ref, int64_t n_pages, int32_t *table_out, int32_t *seq_len_out,
