@@ -626,7 +626,7 @@ QSA_API qsa_status qsa_paged_decode(const qsa_paged_config *cfg, const qsa_bf16 
  * the sum of two scaled E4M3 values, which hold all of a bf16 value down to 2^-14 of the head's largest; smaller ones are
  * rounded by up to 2^-22 of that. Each weight x V scale is rounded once, by at most 2^-11 of it or 2^-40 of the largest of
  * its sequence (so what lies below 2^-40 of that is zero). Scales must not be negative; a V scale that is infinite or NaN
- * makes its 128 dims of its sequence's heads NaN, and nothing else. */
+ * makes its 128 dims of its sequence's heads NaN, and nothing else; one below 2^-126 counts as zero. */
 QSA_API qsa_status qsa_paged_decode_fp8kv(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
                                           const uint8_t *k_codes, const float *k_scales, const uint8_t *v_codes,
                                           const float *v_scales, int64_t n_pages, const int32_t *table,

@@ -194,12 +194,6 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// fmaxf, but NaN if either is.
-__device__ __forceinline__ float max_nan(float x, float y) {
-    float z;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
-    return z;
-}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -732,11 +726,10 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
 #pragma unroll
                         for (int gr = 0; gr < SG; ++gr) {
                             sc[x][gr] = ks[x * SG + gr];
-                            // a scale below 2^-100 counts as that: its row's values are beneath 2^-91; NaN stays NaN, and
-                            // infinity becomes it (the loading warps see to that, or the product): as a maximum it would
-                            // take every other token's weight to zero
+                            // NaN stays NaN, and infinity becomes it (the loading warps see to that, or the product): as a
+                            // maximum it would take every other token's weight to zero
                             const float v_scale = vs[x * SG + gr], e = lg2(v_scale);
-                            lv[gr][nt][x] = max_nan(C::loaders ? e : fmaf(v_scale, 0.f, e), -100.f);
+                            lv[gr][nt][x] = C::loaders ? e : fmaf(v_scale, 0.f, e);
                         }
                 }
 #pragma unroll
@@ -762,7 +755,10 @@ __global__ void __launch_bounds__(C::threads, C::ctas) paged_tile_kernel(PagedAr
                 float top = -INFINITY;
 #pragma unroll
                 for (int nt = 0; nt < NQ; ++nt)
-                    top = fmaxf(top, F8 ? fmaxf(s[nt][2 * h] + lv[gr][nt][0], s[nt][2 * h + 1] + lv[gr][nt][1])
+                    // a V scale below 2^-100, or that is not a number, counts as 2^-100 here: the maximum is finite
+                    // whenever a score is
+                    top = fmaxf(top, F8 ? fmaxf(s[nt][2 * h] + fmaxf(lv[gr][nt][0], -100.f),
+                                                s[nt][2 * h + 1] + fmaxf(lv[gr][nt][1], -100.f))
                                         : fmaxf(s[nt][2 * h], s[nt][2 * h + 1]));
                 top = quad_max(top);
                 if (c == 0) maxima[(gr * GT + g + 8 * h) * W + warp] = top;

@@ -1206,3 +1206,34 @@ def test_fork_starts_long_rows_beside_short_ones(cuda_lib, n_pages, ld):
     assert all(torch.equal(a, b) for a, b in zip(planes, want_planes))
     st, row = status(ws)
     assert (st, row) == (0, 0) if not want[4] else st == qb.QSA_ERR_DEVICE_BOUNDS and row in want[4]
+
+
+@pytest.mark.parametrize("Hq,D", [(8, 256), (16, 256), (8, 128), (16, 128)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 0.0, 2.0 ** -110])
+@pytest.mark.parametrize("n,bad", [(1, 1), (70, 70), (400, 128), (400, 300), (3000, 2900)])
+def test_decode_value_scales_of_whole_tiles_leave_the_rest(cuda_lib, Hq, D, value, n, bad):
+    """The first `bad` tokens' V scales of a group are infinite, NaN, zero or tiny: the group's dims are NaN, or what the
+    other tokens give; other dims and the log-sum-exp are as they would be."""
+    q, planes, values, tab, table = paged_inputs([n], Hq, 1, D, 16, True, seed=76)
+    cfg = qb.make_paged_config(Hq, 1, D, 16)
+    ws = qb.paged_workspace(cfg)
+    slots = P.slots_of(table[0], n, 16)
+    keep = planes[3].clone()
+    for group in range(D // 128):
+        planes[3].copy_(keep).flatten(0, 1)[slots[:bad], 0, group] = value
+        out, lse = run_decode(cfg, q, planes, tab, ints([n]), ws)
+        small = value == value and value < 1
+        dims = torch.arange(D, device=DEV) // 128 == group
+        if small:
+            V, of_group = values[1].copy(), slice(group * 128, group * 128 + 128)
+            V.reshape(-1, 1, D)[slots[:bad], :, of_group] = value * e4m3(planes[2]).reshape(-1, 1, D)[slots[:bad], :, of_group]
+            check_decode(out, lse, q, (values[0], V), table, [n], 16, 0, D ** -0.5, True,
+                         q_step=2.0 ** -22 if D == 256 and Hq <= 8 else 0.0)
+            continue
+        assert bool(torch.isnan(out[0][:, dims]).all()) and not torch.isnan(out[0][:, ~dims]).any()
+        got = torch.where(dims, 0.0, out.float()).to(torch.bfloat16)              # the NaN dims compared as zeros
+        zeroed = values[1].copy()
+        zeroed.reshape(-1, 1, D)[slots, :, group * 128:group * 128 + 128] = 0.0
+        check_decode(got, lse, q, (values[0], zeroed), table, [n], 16, 0, D ** -0.5, True,
+                     q_step=2.0 ** -22 if D == 256 and Hq <= 8 else 0.0)
+    assert status(ws) == (0, 0)
