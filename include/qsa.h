@@ -686,6 +686,137 @@ QSA_API qsa_status qsa_copy_pages(const int32_t *src, const int32_t *dst, int32_
                                   int64_t n_pages, const qsa_page_planes *dst_planes, int64_t n_dst_pages,
                                   int32_t n_groups, void *ws, size_t ws_bytes, qsa_stream stream);
 
+/* ------------------------------------------------- drafted tokens and eviction over a paged cache
+ * Speculative decoding: qsa_rope_append_at stores a sequence's drafted tokens behind its cached ones,
+ * qsa_tree_decode attends for all of them, qsa_accept_drafts keeps the accepted ones. A cache with a budget:
+ * qsa_paged_decode_weights accumulates each token's attention weight and qsa_evict_tokens drops the lightest tokens.
+ * There a token's place in its row (which fixes its page and slot) is no longer its position (which fixes its rotary
+ * angle): a drafted token's position is its depth in the tree, and an evicted token's place is taken by a later one. */
+
+/* qsa_rope_append for tokens whose place is not their position: token n turns to position pos[n] and is stored as token
+ * place[n] of row seq[n]. positions (NULL: not wanted) [n_rows][positions_ld] int32: positions[r][place[n]] = pos[n], for
+ * places below positions_ld. Everything else as qsa_rope_append, with place in pos's part in the device checks. */
+QSA_API qsa_status qsa_rope_append_at(const qsa_paged_config *cfg, const qsa_rope_config *rope, const uint64_t *phase,
+                                      float amplitude, const qsa_bf16 *q, int64_t q_ld, const qsa_bf16 *k, int64_t k_ld,
+                                      const qsa_bf16 *v, int64_t v_ld, const int32_t *seq, const int32_t *pos,
+                                      const int32_t *place, int32_t N, qsa_bf16 *q_out, int64_t q_out_ld,
+                                      qsa_bf16 *k_cache, qsa_bf16 *v_cache, int64_t n_pages, const int32_t *table,
+                                      int64_t table_ld, int32_t n_rows, int32_t *positions, int64_t positions_ld,
+                                      void *ws, size_t ws_bytes, qsa_stream stream);
+QSA_API qsa_status qsa_rope_append_at_fp8kv(const qsa_paged_config *cfg, const qsa_rope_config *rope,
+                                            const uint64_t *phase, float amplitude, const qsa_bf16 *q, int64_t q_ld,
+                                            const qsa_bf16 *k, int64_t k_ld, const qsa_bf16 *v, int64_t v_ld,
+                                            const int32_t *seq, const int32_t *pos, const int32_t *place, int32_t N,
+                                            qsa_bf16 *q_out, int64_t q_out_ld, uint8_t *k_codes, float *k_scales,
+                                            uint8_t *v_codes, float *v_scales, int64_t n_pages, const int32_t *table,
+                                            int64_t table_ld, int32_t n_rows, int32_t *positions, int64_t positions_ld,
+                                            void *ws, size_t ws_bytes, qsa_stream stream);
+
+#define QSA_MAX_DRAFT 128
+
+/* Workspace of qsa_tree_decode for at most max_draft drafted tokens a sequence (the same for every batch, length and
+ * page count; 0 on unsupported geometry). Zero it once with qsa_workspace_init. */
+QSA_API size_t qsa_tree_workspace_size(const qsa_paged_config *cfg, int32_t max_draft);
+
+/* Attention of every sequence's drafted tokens over its paged cache. Sequence s has the drafted tokens
+ * i = draft_off[s] .. draft_off[s + 1] - 1 of the batch's list, T of them: the last T of its n = seq_len[s] cached
+ * tokens, in the list's order. parent[i] is the place of token i's parent among the sequence's own T (below i's own
+ * place), or -1 for a child of the cached tokens. Token i attends the n - T cached tokens before the drafts, its
+ * ancestors and itself:
+ *   out[i][h] = sum_j softmax_j(scale q[i][h] . K[j]) V[j],   lse[i][h] = ln sum_j e^(scale q.K[j]).
+ * A chain (parent = place - 1) is the causal attention of several new tokens. With a window a token at depth d (1: no
+ * drafted ancestor) has position n - T + d - 1 and attends positions above that - window; the cached tokens' positions
+ * are their places.
+ *   q [N] rows of n_q_heads x head_dim, q_ld elements apart (a multiple of 8), 16-byte aligned; draft_off [B + 1],
+ *   ascending, within [0, N]; parent [N]; max_draft: the most drafted tokens of a sequence, 1 .. QSA_MAX_DRAFT;
+ *   out [N][n_q_heads][head_dim] bf16, 16-byte aligned; lse [N][n_q_heads] fp32 or NULL; k_cache, v_cache 16-byte
+ *   aligned device memory. Rows of out and lse that no sequence names stay as they were.
+ * fp32 scores, softmax and sums; the weights enter the second product as bf16 (each rounded by at most 2^-8 of it, as out itself is).
+ * Device checks (QSA_ERR_DEVICE_BOUNDS is recorded): a sequence whose offsets do not ascend within [0, N], or begin below an
+ * earlier one's, attends nothing and its rows are not written; one with T > max_draft, T > n or n > table_ld page_size
+ * attends nothing (out = 0, lse = -inf); a parent outside [-1, own place) counts as -1; a page outside [0, n_pages) has
+ * its tokens left out. A token that attends nothing gets out = 0 and
+ * lse = -inf. Results do not depend on timing: the split depends on the lengths, max_draft and the device alone. The first
+ * call on a device queries its occupancy and should precede stream capture. */
+QSA_API qsa_status qsa_tree_decode(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
+                                   const int32_t *draft_off, const int32_t *parent, int32_t N, int32_t max_draft,
+                                   const qsa_bf16 *k_cache, const qsa_bf16 *v_cache, int64_t n_pages,
+                                   const int32_t *table, int64_t table_ld, const int32_t *seq_len, int32_t B,
+                                   qsa_bf16 *out, float *lse, void *ws, size_t ws_bytes, qsa_stream stream);
+
+/* qsa_tree_decode over the FP8 rows qsa_rope_append_fp8kv writes (head_dim 128 or 256). */
+QSA_API qsa_status qsa_tree_decode_fp8kv(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
+                                         const int32_t *draft_off, const int32_t *parent, int32_t N,
+                                         int32_t max_draft, const uint8_t *k_codes, const float *k_scales,
+                                         const uint8_t *v_codes, const float *v_scales, int64_t n_pages,
+                                         const int32_t *table, int64_t table_ld, const int32_t *seq_len, int32_t B,
+                                         qsa_bf16 *out, float *lse, void *ws, size_t ws_bytes, qsa_stream stream);
+
+/* Workspace of qsa_paged_decode_weights for a batch of at most B sequences with at most n_tokens attended tokens
+ * together (0 on unsupported geometry). Zero it once with qsa_workspace_init. */
+QSA_API size_t qsa_paged_weights_workspace_size(const qsa_paged_config *cfg, int32_t B, int64_t n_tokens);
+
+/* qsa_paged_decode that also accumulates what each cached token received:
+ *   weights[s][j] += sum_h softmax_j(scale q[s][h] . K[j])   for the attended tokens j of sequence s,
+ * in fp32, each head's weight from its final log-sum-exp and the heads summed in order. weights [B][weights_ld] fp32,
+ * 4-byte aligned; entries of tokens that are not attended stay as they were. out and lse are qsa_paged_decode's, bit
+ * for bit. Device checks beside those: tokens at or behind weights_ld, and those behind the workspace's n_tokens, add
+ * nothing (QSA_ERR_DEVICE_BOUNDS). */
+QSA_API qsa_status qsa_paged_decode_weights(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
+                                            const qsa_bf16 *k_cache, const qsa_bf16 *v_cache, int64_t n_pages,
+                                            const int32_t *table, int64_t table_ld, const int32_t *seq_len, int32_t B,
+                                            qsa_bf16 *out, float *lse, float *weights, int64_t weights_ld, void *ws,
+                                            size_t ws_bytes, qsa_stream stream);
+QSA_API qsa_status qsa_paged_decode_weights_fp8kv(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
+                                                  const uint8_t *k_codes, const float *k_scales,
+                                                  const uint8_t *v_codes, const float *v_scales, int64_t n_pages,
+                                                  const int32_t *table, int64_t table_ld, const int32_t *seq_len,
+                                                  int32_t B, qsa_bf16 *out, float *lse, float *weights,
+                                                  int64_t weights_ld, void *ws, size_t ws_bytes, qsa_stream stream);
+
+/* Workspace of qsa_accept_drafts (max_tokens 0) and qsa_evict_tokens (max_tokens: its weights_ld) for at most n_rows
+ * rows. Zero it once with qsa_workspace_init. */
+QSA_API size_t qsa_keep_workspace_size(int32_t n_rows, int64_t max_tokens);
+
+/* Keep the accepted drafted tokens. Row r's drafted tokens are the last T = draft_off[r + 1] - draft_off[r] of its
+ * seq_len[r] tokens, with parents as in qsa_tree_decode. accepted[r] is the place of the last accepted one among them
+ * (-1: none): it and its ancestors stay, oldest first, directly behind the cached tokens, in every plane; the rest is
+ * dropped and pages that hold no token any more are given back:
+ *   seq_len_out[r] = seq_len[r] - T + depth of accepted[r];  ref_out[p] = ref[p] - entries that named p and are dropped;
+ *   table_out: the table with -1 behind each row's last page.
+ * The pages of kept drafted tokens must be the row's own (qsa_fork_pages sees to that for tokens appended behind it).
+ *   draft_off [n_rows + 1]; parent [N]; accepted, seq_len, seq_len_out [n_rows]; table, table_out [n_rows][ld]; ref, ref_out
+ *   [n_pages] (each _out another array); n_rows <= 65536, n_pages page_size < 2^31; positions (NULL: none) [n_rows][positions_ld] int32, moved along in
+ *   place; planes as in qsa_fork_pages, page_bytes a multiple of page_size x 4.
+ * A row whose seq_len, draft_off, parents or accepted are out of range (QSA_ERR_DEVICE_BOUNDS, the row) keeps all its
+ * tokens; a page out of range is left out. */
+QSA_API qsa_status qsa_accept_drafts(int32_t page_size, const int32_t *draft_off, const int32_t *parent, int32_t N,
+                                     const int32_t *accepted, const int32_t *table, const int32_t *seq_len,
+                                     int32_t n_rows, int64_t ld, const int32_t *ref, int64_t n_pages, int32_t *table_out,
+                                     int32_t *seq_len_out, int32_t *ref_out, int32_t *positions, int64_t positions_ld,
+                                     const qsa_page_planes *planes, int32_t n_groups, void *ws, size_t ws_bytes,
+                                     qsa_stream stream);
+
+/* Cut rows down to their budget by accumulated weight. Row r of n = seq_len[r] tokens keeps all of them if n <=
+ * budget[r] or budget[r] < 0. Otherwise it always keeps the tokens at positions below `first`, those at the last `recent`
+ * positions (above the row's highest position - recent) and those in pages that other references share (ref > 1:
+ * dropping them would free nothing), P tokens; of the others it keeps the heaviest, equal weights by lower place, until
+ * K = max(budget[r], P) stay. Only kept tokens at places >= K move: in ascending order into the places below K that
+ * dropped tokens held, ascending, in every plane, with their weights and positions. Pages that hold no token any more
+ * are given back (ref_out, table_out as in qsa_accept_drafts).
+ *   weights [n_rows][tokens_ld] fp32 (a NaN counts as the lightest, -0 as 0), positions [n_rows][tokens_ld] int32;
+ *   weights_out, positions_out: other arrays of their shape, 0 and -1 behind a row's new length; budget [n_rows];
+ *   first, recent >= 0; the rest as in qsa_accept_drafts.
+ * A row with seq_len outside [0, ld page_size] or above tokens_ld keeps its table and length (QSA_ERR_DEVICE_BOUNDS, the
+ * row); its weights_out and positions_out are copies. A page out of range is left out and recorded. */
+QSA_API qsa_status qsa_evict_tokens(int32_t page_size, const int32_t *budget, int32_t first, int32_t recent,
+                                    const float *weights, const int32_t *positions, int64_t tokens_ld,
+                                    const int32_t *table, const int32_t *seq_len, int32_t n_rows, int64_t ld,
+                                    const int32_t *ref, int64_t n_pages, float *weights_out, int32_t *positions_out,
+                                    int32_t *table_out, int32_t *seq_len_out, int32_t *ref_out,
+                                    const qsa_page_planes *planes, int32_t n_groups, void *ws, size_t ws_bytes,
+                                    qsa_stream stream);
+
 /* Static description of a status code. */
 QSA_API const char *qsa_status_string(qsa_status s);
 

@@ -126,6 +126,23 @@ _SIGNATURES = {
     "qsa_fork_pages": (_I32, [_I32, _P, _P, _I32, _P, _P, _I32, _I64, _P, _I64, _P, _P, _P, _PLANES, _I32, _P, _SZ,
                               _P]),
     "qsa_compact_pages": (_I32, [_I32, _P, _P, _I32, _I64, _P, _I64, _P, _P, _PLANES, _I32, _P, _SZ, _P]),
+    "qsa_rope_append_at": (_I32, [_PCFG, _RCFG, _P, _F32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I32, _P, _I64, _P, _P,
+                                  _I64, _P, _I64, _I32, _P, _I64, _P, _SZ, _P]),
+    "qsa_rope_append_at_fp8kv": (_I32, [_PCFG, _RCFG, _P, _F32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I32, _P, _I64,
+                                        _P, _P, _P, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _SZ, _P]),
+    "qsa_tree_workspace_size": (_SZ, [_PCFG, _I32]),
+    "qsa_tree_decode": (_I32, [_PCFG, _P, _I64, _P, _P, _I32, _I32, _P, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _SZ, _P]),
+    "qsa_tree_decode_fp8kv": (_I32, [_PCFG, _P, _I64, _P, _P, _I32, _I32, _P, _P, _P, _P, _I64, _P, _I64, _P, _I32, _P, _P,
+                                     _P, _SZ, _P]),
+    "qsa_paged_weights_workspace_size": (_SZ, [_PCFG, _I32, _I64]),
+    "qsa_paged_decode_weights": (_I32, [_PCFG, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _I64, _P, _SZ, _P]),
+    "qsa_paged_decode_weights_fp8kv": (_I32, [_PCFG, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _I64,
+                                              _P, _SZ, _P]),
+    "qsa_keep_workspace_size": (_SZ, [_I32, _I64]),
+    "qsa_accept_drafts": (_I32, [_I32, _P, _P, _I32, _P, _P, _P, _I32, _I64, _P, _I64, _P, _P, _P, _P, _I64, _PLANES, _I32,
+                                 _P, _SZ, _P]),
+    "qsa_evict_tokens": (_I32, [_I32, _P, _I32, _I32, _P, _P, _I64, _P, _P, _I32, _I64, _P, _I64, _P, _P, _P, _P, _P,
+                                _PLANES, _I32, _P, _SZ, _P]),
     "qsa_copy_pages": (_I32, [_P, _P, _I32, _PLANES, _I64, _PLANES, _I64, _I32, _P, _SZ, _P]),
     "qsa_status_string": (C.c_char_p, [_I32]),
     "qsa_last_error": (C.c_char_p, []),
@@ -600,6 +617,108 @@ def qsa_copy_pages(src, dst, planes, ws, dst_planes=None, stream=None):
                                            None if stream is None else _stream(stream))
     if st:
         _check(st, "qsa_copy_pages")
+
+
+# ------------------------------------------------- drafted tokens and eviction over a paged cache
+def tree_workspace(cfg: qsa_paged_config, max_draft: int, device="cuda", stream=None):
+    """A zero-initialised workspace for qsa_tree_decode with at most max_draft drafted tokens a sequence."""
+    n = int(load().qsa_tree_workspace_size(C.byref(cfg), max_draft))
+    if n == 0:
+        raise QsaError(QSA_ERR_UNSUPPORTED, "unsupported tree geometry: " + load().qsa_last_error().decode())
+    return _zeroed(n, device, stream)
+
+
+def weights_workspace(cfg: qsa_paged_config, batch: int, n_tokens: int, device="cuda", stream=None):
+    """A zero-initialised workspace for qsa_paged_decode_weights: batch sequences of n_tokens attended tokens together."""
+    n = int(load().qsa_paged_weights_workspace_size(C.byref(cfg), batch, n_tokens))
+    if n == 0:
+        raise QsaError(QSA_ERR_UNSUPPORTED, "unsupported paged geometry: " + load().qsa_last_error().decode())
+    return _zeroed(n, device, stream)
+
+
+def keep_workspace(n_rows: int, max_tokens: int = 0, device="cuda", stream=None):
+    """A zero-initialised workspace for qsa_accept_drafts, and for qsa_evict_tokens on rows of max_tokens places."""
+    n = int(load().qsa_keep_workspace_size(n_rows, max_tokens))
+    if n == 0:
+        raise QsaError(QSA_ERR_UNSUPPORTED, "too many rows or tokens")
+    return _zeroed(n, device, stream)
+
+
+def qsa_rope_append_at(cfg, rope: RopeTable, q, k, v, pos, place, seq, q_out, k_cache, v_cache, table, ws, positions=None,
+                       stream=None):
+    """qsa_rope_append with token n stored at place[n] of its row and turned to position pos[n]; positions
+    [rows, places] int32 (or None) receives each stored token's position."""
+    st = (_NATIVE or _native()).rope_append_at(cfg, rope.cfg, rope.phase, rope.amplitude, q, k, v, pos, seq, q_out,
+                                               (k_cache, v_cache), table, ws, None if stream is None else _stream(stream),
+                                               place, positions)
+    if st:
+        _check(st, "qsa_rope_append_at")
+
+
+def qsa_rope_append_at_fp8kv(cfg, rope: RopeTable, q, k, v, pos, place, seq, q_out, kv8, table, ws, positions=None,
+                             stream=None):
+    """qsa_rope_append_at into FP8 rows kv8 = (k_codes, k_scales, v_codes, v_scales)."""
+    st = (_NATIVE or _native()).rope_append_at_fp8kv(cfg, rope.cfg, rope.phase, rope.amplitude, q, k, v, pos, seq, q_out, kv8,
+                                                     table, ws, None if stream is None else _stream(stream), place, positions)
+    if st:
+        _check(st, "qsa_rope_append_at_fp8kv")
+
+
+def qsa_tree_decode(cfg, q, draft_off, parent, max_draft, k_cache, v_cache, table, seq_len, out, lse, ws, stream=None):
+    """Attention of every sequence's drafted tokens, the last draft_off[s + 1] - draft_off[s] of its seq_len[s] cached
+    ones: each sees the cached tokens before the drafts, its ancestors (parent [N], -1: none) and itself. q [N, Hq, D]
+    (rows may be strided), draft_off [B + 1], table [B, max_pages], out [N, Hq, D], lse [N, Hq] or None."""
+    st = (_NATIVE or _native()).tree_decode(cfg, q, draft_off, parent, max_draft, (k_cache, v_cache), table, seq_len, out, lse,
+                                            ws, None if stream is None else _stream(stream))
+    if st:
+        _check(st, "qsa_tree_decode")
+
+
+def qsa_tree_decode_fp8kv(cfg, q, draft_off, parent, max_draft, kv8, table, seq_len, out, lse, ws, stream=None):
+    """qsa_tree_decode over FP8 rows kv8 = (k_codes, k_scales, v_codes, v_scales)."""
+    st = (_NATIVE or _native()).tree_decode_fp8kv(cfg, q, draft_off, parent, max_draft, kv8, table, seq_len, out, lse, ws,
+                                                  None if stream is None else _stream(stream))
+    if st:
+        _check(st, "qsa_tree_decode_fp8kv")
+
+
+def qsa_paged_decode_weights(cfg, q, k_cache, v_cache, table, seq_len, out, lse, weights, ws, stream=None):
+    """qsa_paged_decode that also adds to weights [B, places] fp32 what each attended token received from all heads."""
+    st = (_NATIVE or _native()).paged_decode_weights(cfg, q, (k_cache, v_cache), table, seq_len, out, lse, weights, ws,
+                                                     None if stream is None else _stream(stream))
+    if st:
+        _check(st, "qsa_paged_decode_weights")
+
+
+def qsa_paged_decode_weights_fp8kv(cfg, q, kv8, table, seq_len, out, lse, weights, ws, stream=None):
+    """qsa_paged_decode_weights over FP8 rows kv8 = (k_codes, k_scales, v_codes, v_scales)."""
+    st = (_NATIVE or _native()).paged_decode_weights_fp8kv(cfg, q, kv8, table, seq_len, out, lse, weights, ws,
+                                                           None if stream is None else _stream(stream))
+    if st:
+        _check(st, "qsa_paged_decode_weights_fp8kv")
+
+
+def qsa_accept_drafts(page_size, draft_off, parent, accepted, table, seq_len, ref, table_out, seq_len_out, ref_out, planes,
+                      ws, positions=None, stream=None):
+    """Of each row's drafted tokens keep accepted[r] (-1: none) and its ancestors, directly behind the cached tokens, and
+    give back the pages that empty. planes: a list of pool tensors [n_planes, n_pages, ...]; positions [rows, places]
+    int32 (or None) moves along."""
+    st = (_NATIVE or _native()).accept_drafts(page_size, draft_off, parent, accepted, table, seq_len, ref, table_out,
+                                              seq_len_out, ref_out, planes, ws, positions,
+                                              None if stream is None else _stream(stream))
+    if st:
+        _check(st, "qsa_accept_drafts")
+
+
+def qsa_evict_tokens(page_size, budget, first, recent, weights, positions, table, seq_len, ref, weights_out, positions_out,
+                     table_out, seq_len_out, ref_out, planes, ws, stream=None):
+    """Cut the rows that hold more than budget[r] tokens (negative: any number) down to it: tokens at positions below
+    `first`, at the last `recent` positions and in shared pages stay, and of the others the heaviest."""
+    st = (_NATIVE or _native()).evict_tokens(page_size, budget, first, recent, weights, positions, table, seq_len, ref,
+                                             weights_out, positions_out, table_out, seq_len_out, ref_out, planes, ws,
+                                             None if stream is None else _stream(stream))
+    if st:
+        _check(st, "qsa_evict_tokens")
 
 
 def version() -> str:

@@ -5,7 +5,7 @@
 
 namespace qsa {
 
-constexpr int kWhereAppend = 9, kWherePaged = 10, kWherePages = 11;
+constexpr int kWhereAppend = 9, kWherePaged = 10, kWherePages = 11, kWhereTree = 12, kWhereKeep = 13, kWhereWeights = 14;
 
 // Programmatic dependent launch: a kernel launched by launch_dependent may begin while the kernel before it on the
 // stream ends; it waits for that one's memory before its first access. Every kernel here does that at its start, so
@@ -49,6 +49,9 @@ struct AppendArgs {
     const uint16_t *q, *k, *v;   // q may be nullptr
     int64_t q_ld, k_ld, v_ld;
     const int32_t *seq, *pos;    // seq may be nullptr: token n is row n
+    const int32_t *place;        // where a token is stored; nullptr: at its position
+    int32_t *positions;          // [n_rows][positions_ld] or nullptr: what is stored at each place
+    int64_t positions_ld;
     int32_t N, Hq, Hkv;
     uint16_t *q_out;
     int64_t q_out_ld;
@@ -84,6 +87,40 @@ struct PagedArgs {
 size_t paged_scratch_bytes(int D, int Hq, int Hkv);
 cudaError_t launch_paged_decode(const PagedArgs &a, int D, bool fp8, cudaStream_t st);
 
+// Attention that accumulates weights: the scores of each tile and what the second kernel needs to turn them into weights.
+struct WeightArgs {
+    float *scores;                      // [tiles][Hq][tile tokens], base 2
+    int2 *tiles;                        // [tiles] (row, tile of the row)
+    int32_t *n_tiles;                   // tiles of the batch
+    float *lse2;                        // [B][Hq], base 2
+    int64_t cap;                        // tiles that scores has room for
+    float *weights;
+    int64_t weights_ld;
+};
+int paged_tile_tokens(bool fp8);
+cudaError_t launch_paged_decode_weights(const PagedArgs &a, const WeightArgs &w, int D, bool fp8, cudaStream_t st);
+
+struct TreeArgs {
+    const uint16_t *q;
+    int64_t q_ld;
+    const int32_t *draft_off, *parent;
+    int32_t N, max_draft;
+    const void *k, *v;                  // bf16 rows, or E4M3 codes
+    const float *k_scales, *v_scales;   // nullptr with bf16 rows
+    int64_t n_pages;
+    const int32_t *table;
+    int64_t ld;
+    const int32_t *seq_len;
+    int32_t B, Hq, Hkv, G, page_size, window;
+    float scale_log2;
+    uint16_t *out;
+    float *lse;
+    WsHeader *hdr;
+    char *scratch;
+};
+size_t tree_scratch_bytes(int D, int Hq, int Hkv, int max_draft);
+cudaError_t launch_tree_decode(const TreeArgs &a, int D, bool fp8, cudaStream_t st);
+
 struct PlaneGroup {
     char *src, *dst;
     int64_t src_stride, dst_stride, page_bytes;
@@ -113,6 +150,33 @@ struct CompactArgs {
 size_t pages_scratch_bytes(int n_rows, int64_t n_pages);
 cudaError_t launch_fork_pages(const ForkArgs &a, const PlaneGroups &p, cudaStream_t st);
 cudaError_t launch_compact_pages(const CompactArgs &a, const PlaneGroups &p, cudaStream_t st);
+struct KeepArgs {
+    const int32_t *table, *seq_len, *ref;
+    int32_t *table_out, *seq_len_out, *ref_out;
+    int32_t n_rows, page_size, n_pages;
+    int32_t page_shift;                 // log2 of page_size, -1: no power of two
+    int64_t ld;
+    WsHeader *hdr;
+    char *scratch;
+};
+struct AcceptArgs {
+    const int32_t *draft_off, *parent, *accepted;
+    int32_t N;
+    int32_t *positions;                 // or nullptr
+    int64_t positions_ld;
+};
+struct EvictArgs {
+    const int32_t *budget;
+    int32_t first, recent;
+    const float *weights;
+    const int32_t *positions;
+    float *weights_out;
+    int32_t *positions_out;
+    int64_t tokens_ld;
+};
+size_t keep_scratch_bytes(int n_rows, int64_t tokens);
+cudaError_t launch_accept_drafts(const KeepArgs &a, const AcceptArgs &d, const PlaneGroups &p, cudaStream_t st);
+cudaError_t launch_evict_tokens(const KeepArgs &a, const EvictArgs &e, const PlaneGroups &p, cudaStream_t st);
 cudaError_t launch_copy_pages(const int32_t *src, const int32_t *dst, int n, const PlaneGroups &p, int64_t n_src,
                               int64_t n_dst, WsHeader *hdr, cudaStream_t st);
 

@@ -200,6 +200,8 @@ qsa_status rope_append(const char *call, const qsa_paged_config *cfg, const qsa_
     QSA_NEED(call, a.pos && a.table && (phase != nullptr || rope->rot_dim == 0), "NULL tensor pointer");
     QSA_NEED(call, aligned(phase, 16), "phase must be 16-byte aligned");
     QSA_NEED(call, aligned(a.pos, 4) && aligned(a.seq, 4) && aligned(a.table, 4), "pos, seq and table must be 4-byte aligned");
+    QSA_NEED(call, aligned(a.place, 4) && aligned(a.positions, 4), "place and positions must be 4-byte aligned");
+    QSA_NEED(call, a.positions == nullptr || a.positions_ld >= 0, "positions_ld must not be negative");
     if (fp8) {
         QSA_NEED(call, a.k_codes && a.v_codes && a.k_scales && a.v_scales, "NULL tensor pointer");
         QSA_NEED(call, aligned(a.k_codes, 16) && aligned(a.v_codes, 16) && aligned(a.k_scales, 8) && aligned(a.v_scales, 8),
@@ -215,13 +217,28 @@ qsa_status rope_append(const char *call, const qsa_paged_config *cfg, const qsa_
     return launched(launch_rope_append(rope_args(rope, phase, amplitude), a, static_cast<cudaStream_t>(stream)), call);
 }
 
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// What qsa_paged_decode_weights keeps behind qsa_paged_decode's workspace: the batch's log-sum-exps and tile count, then for
+// each tile its row and the scores of its tokens.
+size_t weights_fixed(const qsa_paged_config *c, int32_t B) {
+    return up256(paged_ws(c)) + 256 + up256((size_t)B * c->n_q_heads * sizeof(float));
+}
+size_t weights_per_tile(const qsa_paged_config *c, bool fp8) {
+    return sizeof(int2) + (size_t)paged_tile_tokens(fp8) * c->n_q_heads * sizeof(float);
+}
+
+// weights: w.weights is set (the rest of w is filled in here).
 qsa_status paged_decode(const char *call, const qsa_paged_config *cfg, PagedArgs a, void *ws, size_t ws_bytes,
-                        qsa_stream stream, bool fp8) {
+                        qsa_stream stream, bool fp8, WeightArgs w = WeightArgs{}, bool weights = false) {
     QSA_TRY(check_paged(call, cfg, fp8));
     QSA_NEED(call, a.B >= 0 && a.B <= 65535, "B = %d out of range [0, 65535]", a.B);
     QSA_TRY(check_table(call, cfg, a.n_pages, a.ld));
-    QSA_TRY(check_workspace(call, ws, ws_bytes, paged_ws(cfg)));
+    QSA_TRY(check_workspace(call, ws, ws_bytes, weights ? weights_fixed(cfg, a.B) : paged_ws(cfg)));
+    QSA_NEED(call, !weights || w.weights_ld >= 0, "weights_ld must not be negative");
     if (a.B == 0) return host_ok();
+    QSA_NEED(call, !weights || w.weights != nullptr, "weights is NULL");
+    QSA_NEED(call, aligned(w.weights, 4), "weights must be 4-byte aligned");
     QSA_TRY(check_rows(call, "q", a.q, a.q_ld, (int64_t)cfg->n_q_heads * cfg->head_dim));
     QSA_NEED(call, a.k && a.v && a.table && a.seq_len && a.out && (!fp8 || (a.k_scales && a.v_scales)),
              "NULL tensor pointer");
@@ -241,7 +258,61 @@ qsa_status paged_decode(const char *call, const qsa_paged_config *cfg, PagedArgs
     a.scale_log2 = (cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.0f / sqrtf((float)cfg->head_dim)) * kLog2e;
     a.hdr = static_cast<WsHeader *>(ws);
     a.scratch = static_cast<char *>(ws) + kWsHeaderBytes;
+    if (weights) {
+        char *at = static_cast<char *>(ws) + up256(paged_ws(cfg));
+        w.n_tiles = reinterpret_cast<int32_t *>(at);
+        w.lse2 = reinterpret_cast<float *>(at + 256);
+        at = static_cast<char *>(ws) + weights_fixed(cfg, a.B);
+        // the scores first: 16-byte vectors
+        w.cap = (int64_t)((ws_bytes - weights_fixed(cfg, a.B)) / weights_per_tile(cfg, fp8));
+        w.scores = reinterpret_cast<float *>(at);
+        w.tiles = reinterpret_cast<int2 *>(at + (size_t)w.cap * (weights_per_tile(cfg, fp8) - sizeof(int2)));
+        return launched(launch_paged_decode_weights(a, w, cfg->head_dim, fp8, static_cast<cudaStream_t>(stream)), call);
+    }
     return launched(launch_paged_decode(a, cfg->head_dim, fp8, static_cast<cudaStream_t>(stream)), call);
+}
+
+qsa_status check_drafts(const char *call, int32_t max_draft) {
+    if (max_draft < 1 || max_draft > QSA_MAX_DRAFT)
+        return fail(QSA_ERR_UNSUPPORTED, call, "max_draft %d (1 to %d)", max_draft, QSA_MAX_DRAFT);
+    return QSA_OK;
+}
+
+size_t tree_ws(const qsa_paged_config *c, int32_t max_draft) {
+    return kWsHeaderBytes + tree_scratch_bytes(c->head_dim, c->n_q_heads, c->n_kv_heads, max_draft);
+}
+
+qsa_status tree_decode(const char *call, const qsa_paged_config *cfg, TreeArgs a, void *ws, size_t ws_bytes,
+                       qsa_stream stream, bool fp8) {
+    QSA_TRY(check_paged(call, cfg, fp8));
+    QSA_TRY(check_drafts(call, a.max_draft));
+    QSA_NEED(call, a.B >= 0 && a.B <= 65535, "B = %d out of range [0, 65535]", a.B);
+    QSA_NEED(call, a.N >= 0, "N must not be negative");
+    QSA_TRY(check_table(call, cfg, a.n_pages, a.ld));
+    QSA_TRY(check_workspace(call, ws, ws_bytes, tree_ws(cfg, a.max_draft)));
+    if (a.B == 0 || a.N == 0) return host_ok();
+    QSA_TRY(check_rows(call, "q", a.q, a.q_ld, (int64_t)cfg->n_q_heads * cfg->head_dim));
+    QSA_NEED(call, a.draft_off && a.parent && a.k && a.v && a.table && a.seq_len && a.out &&
+                       (!fp8 || (a.k_scales && a.v_scales)),
+             "NULL tensor pointer");
+    QSA_NEED(call, aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.out, 16),
+             "the K/V rows and out must be 16-byte aligned");
+    QSA_NEED(call, !fp8 || (aligned(a.k_scales, 8) && aligned(a.v_scales, 8)), "scales must be 8-byte aligned");
+    QSA_NEED(call, aligned(a.table, 4) && aligned(a.seq_len, 4) && aligned(a.lse, 4) && aligned(a.draft_off, 4) &&
+                 aligned(a.parent, 4),
+             "table, seq_len, draft_off, parent and lse must be 4-byte aligned");
+    QSA_NEED(call, device_accessible(a.k) && device_accessible(a.v) &&
+                 (!fp8 || (device_accessible(a.k_scales) && device_accessible(a.v_scales))),
+             "the K/V rows (and their scales) must be device memory");
+    a.Hq = cfg->n_q_heads;
+    a.Hkv = cfg->n_kv_heads;
+    a.G = a.Hq / a.Hkv;
+    a.page_size = cfg->page_size;
+    a.window = cfg->window;
+    a.scale_log2 = (cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.0f / sqrtf((float)cfg->head_dim)) * kLog2e;
+    a.hdr = static_cast<WsHeader *>(ws);
+    a.scratch = static_cast<char *>(ws) + kWsHeaderBytes;
+    return launched(launch_tree_decode(a, cfg->head_dim, fp8, static_cast<cudaStream_t>(stream)), call);
 }
 
 constexpr int kMaxPageRows = 65536;
@@ -291,6 +362,39 @@ qsa_status check_pool(const char *call, int32_t page_size, int64_t n_pages, int6
     return QSA_OK;
 }
 
+// The arguments that qsa_accept_drafts and qsa_evict_tokens share; the caller has set a's arrays.
+qsa_status keep_args(const char *call, int32_t page_size, int32_t n_rows, int64_t ld, int64_t n_pages, int64_t max_tokens,
+                     const qsa_page_planes *planes, int32_t n_groups, void *ws, size_t ws_bytes, KeepArgs *a,
+                     PlaneGroups *groups) {
+    QSA_TRY(check_pool(call, page_size, n_pages, ld));
+    if (n_pages > INT32_MAX / page_size)
+        return fail(QSA_ERR_UNSUPPORTED, call, "n_pages %lld x page_size %d exceed 2^31 - 1 tokens", (long long)n_pages, page_size);
+    QSA_NEED(call, n_rows >= 0 && n_rows <= kMaxPageRows, "n_rows = %d out of range [0, %d]", n_rows, kMaxPageRows);
+    QSA_TRY(plane_groups(call, planes, nullptr, n_groups, groups));
+    for (int i = 0; i < groups->n; ++i) {
+        PlaneGroup &g = groups->g[i];
+        QSA_NEED(call, g.page_bytes % (4 * (int64_t)page_size) == 0,
+                 "planes[%d]: page_bytes %lld must be a multiple of 4 bytes for each of %d tokens", i, (long long)g.page_bytes,
+                 page_size);
+        g.wide = g.wide && g.page_bytes / page_size % 16 == 0;      // a token's words
+    }
+    QSA_TRY(check_workspace(call, ws, ws_bytes, kWsHeaderBytes + keep_scratch_bytes(n_rows, max_tokens)));
+    QSA_NEED(call, n_rows == 0 || (a->seq_len && a->seq_len_out && (ld == 0 || (a->table && a->table_out))), "NULL tensor pointer");
+    QSA_NEED(call, n_pages == 0 || (a->ref && a->ref_out), "NULL tensor pointer");
+    QSA_NEED(call, a->table == nullptr || a->table_out != a->table, "table_out must be another array than table");
+    QSA_NEED(call, a->seq_len == nullptr || a->seq_len_out != a->seq_len, "seq_len_out must be another array than seq_len");
+    QSA_NEED(call, a->ref == nullptr || a->ref_out != a->ref, "ref_out must be another array than ref");
+    for (const void *p : {static_cast<const void *>(a->table), static_cast<const void *>(a->seq_len),
+                          static_cast<const void *>(a->ref), static_cast<const void *>(a->table_out),
+                          static_cast<const void *>(a->seq_len_out), static_cast<const void *>(a->ref_out)})
+        QSA_NEED(call, aligned(p, 4), "the int32 arrays must be 4-byte aligned");
+    a->n_rows = n_rows, a->page_size = page_size, a->n_pages = (int32_t)n_pages, a->ld = ld;
+    a->page_shift = (page_size & (page_size - 1)) == 0 ? __builtin_ctz((unsigned)page_size) : -1;
+    a->hdr = static_cast<WsHeader *>(ws);
+    a->scratch = static_cast<char *>(ws) + kWsHeaderBytes;
+    return QSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -324,6 +428,43 @@ QSA_API qsa_status qsa_rope_append_fp8kv(const qsa_paged_config *cfg, const qsa_
     return rope_append("qsa_rope_append_fp8kv", cfg, rope, phase, amplitude, a, ws, ws_bytes, stream, true);
 }
 
+QSA_API qsa_status qsa_rope_append_at(const qsa_paged_config *cfg, const qsa_rope_config *rope, const uint64_t *phase,
+                                      float amplitude, const qsa_bf16 *q, int64_t q_ld, const qsa_bf16 *k, int64_t k_ld,
+                                      const qsa_bf16 *v, int64_t v_ld, const int32_t *seq, const int32_t *pos,
+                                      const int32_t *place, int32_t N, qsa_bf16 *q_out, int64_t q_out_ld,
+                                      qsa_bf16 *k_cache, qsa_bf16 *v_cache, int64_t n_pages, const int32_t *table,
+                                      int64_t table_ld, int32_t n_rows, int32_t *positions, int64_t positions_ld,
+                                      void *ws, size_t ws_bytes, qsa_stream stream) {
+    const char *call = "qsa_rope_append_at";
+    QSA_NEED(call, place != nullptr || N <= 0, "place is NULL");
+    AppendArgs a{};
+    a.q = q, a.q_ld = q_ld, a.k = k, a.k_ld = k_ld, a.v = v, a.v_ld = v_ld;
+    a.seq = seq, a.pos = pos, a.place = place, a.N = N, a.q_out = q_out, a.q_out_ld = q_out_ld;
+    a.k_cache = k_cache, a.v_cache = v_cache;
+    a.n_pages = n_pages, a.table = table, a.ld = table_ld, a.n_rows = n_rows;
+    a.positions = positions, a.positions_ld = positions_ld;
+    return rope_append(call, cfg, rope, phase, amplitude, a, ws, ws_bytes, stream, false);
+}
+
+QSA_API qsa_status qsa_rope_append_at_fp8kv(const qsa_paged_config *cfg, const qsa_rope_config *rope,
+                                            const uint64_t *phase, float amplitude, const qsa_bf16 *q, int64_t q_ld,
+                                            const qsa_bf16 *k, int64_t k_ld, const qsa_bf16 *v, int64_t v_ld,
+                                            const int32_t *seq, const int32_t *pos, const int32_t *place, int32_t N,
+                                            qsa_bf16 *q_out, int64_t q_out_ld, uint8_t *k_codes, float *k_scales,
+                                            uint8_t *v_codes, float *v_scales, int64_t n_pages, const int32_t *table,
+                                            int64_t table_ld, int32_t n_rows, int32_t *positions, int64_t positions_ld,
+                                            void *ws, size_t ws_bytes, qsa_stream stream) {
+    const char *call = "qsa_rope_append_at_fp8kv";
+    QSA_NEED(call, place != nullptr || N <= 0, "place is NULL");
+    AppendArgs a{};
+    a.q = q, a.q_ld = q_ld, a.k = k, a.k_ld = k_ld, a.v = v, a.v_ld = v_ld;
+    a.seq = seq, a.pos = pos, a.place = place, a.N = N, a.q_out = q_out, a.q_out_ld = q_out_ld;
+    a.k_codes = k_codes, a.k_scales = k_scales, a.v_codes = v_codes, a.v_scales = v_scales;
+    a.n_pages = n_pages, a.table = table, a.ld = table_ld, a.n_rows = n_rows;
+    a.positions = positions, a.positions_ld = positions_ld;
+    return rope_append(call, cfg, rope, phase, amplitude, a, ws, ws_bytes, stream, true);
+}
+
 QSA_API qsa_status qsa_paged_decode(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
                                     const qsa_bf16 *k_cache, const qsa_bf16 *v_cache, int64_t n_pages,
                                     const int32_t *table, int64_t table_ld, const int32_t *seq_len, int32_t B,
@@ -345,6 +486,77 @@ QSA_API qsa_status qsa_paged_decode_fp8kv(const qsa_paged_config *cfg, const qsa
     a.n_pages = n_pages, a.table = table, a.ld = table_ld, a.seq_len = seq_len, a.B = B;
     a.out = out, a.lse = lse;
     return paged_decode("qsa_paged_decode_fp8kv", cfg, a, ws, ws_bytes, stream, true);
+}
+
+QSA_API size_t qsa_paged_weights_workspace_size(const qsa_paged_config *cfg, int32_t B, int64_t n_tokens) {
+    const char *call = "qsa_paged_weights_workspace_size";
+    if (check_paged(call, cfg, false) != QSA_OK || B < 0 || B > 65535 || n_tokens < 0) return 0;
+    // a sequence's first and last tile may each hold tokens that are not attended
+    const auto bytes = [&](bool fp8) {
+        const int64_t T = paged_tile_tokens(fp8);
+        return weights_fixed(cfg, B) + (size_t)(n_tokens / T + 2 * (int64_t)B) * weights_per_tile(cfg, fp8);
+    };
+    return std::max(bytes(false), bytes(true));
+}
+
+QSA_API qsa_status qsa_paged_decode_weights(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
+                                            const qsa_bf16 *k_cache, const qsa_bf16 *v_cache, int64_t n_pages,
+                                            const int32_t *table, int64_t table_ld, const int32_t *seq_len, int32_t B,
+                                            qsa_bf16 *out, float *lse, float *weights, int64_t weights_ld, void *ws,
+                                            size_t ws_bytes, qsa_stream stream) {
+    PagedArgs a{};
+    a.q = q, a.q_ld = q_ld, a.k = k_cache, a.v = v_cache;
+    a.n_pages = n_pages, a.table = table, a.ld = table_ld, a.seq_len = seq_len, a.B = B;
+    a.out = out, a.lse = lse;
+    WeightArgs w{};
+    w.weights = weights, w.weights_ld = weights_ld;
+    return paged_decode("qsa_paged_decode_weights", cfg, a, ws, ws_bytes, stream, false, w, true);
+}
+
+QSA_API qsa_status qsa_paged_decode_weights_fp8kv(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
+                                                  const uint8_t *k_codes, const float *k_scales,
+                                                  const uint8_t *v_codes, const float *v_scales, int64_t n_pages,
+                                                  const int32_t *table, int64_t table_ld, const int32_t *seq_len,
+                                                  int32_t B, qsa_bf16 *out, float *lse, float *weights,
+                                                  int64_t weights_ld, void *ws, size_t ws_bytes, qsa_stream stream) {
+    PagedArgs a{};
+    a.q = q, a.q_ld = q_ld, a.k = k_codes, a.v = v_codes, a.k_scales = k_scales, a.v_scales = v_scales;
+    a.n_pages = n_pages, a.table = table, a.ld = table_ld, a.seq_len = seq_len, a.B = B;
+    a.out = out, a.lse = lse;
+    WeightArgs w{};
+    w.weights = weights, w.weights_ld = weights_ld;
+    return paged_decode("qsa_paged_decode_weights_fp8kv", cfg, a, ws, ws_bytes, stream, true, w, true);
+}
+
+QSA_API size_t qsa_tree_workspace_size(const qsa_paged_config *cfg, int32_t max_draft) {
+    const char *call = "qsa_tree_workspace_size";
+    return check_paged(call, cfg, false) == QSA_OK && check_drafts(call, max_draft) == QSA_OK ? tree_ws(cfg, max_draft) : 0;
+}
+
+QSA_API qsa_status qsa_tree_decode(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
+                                   const int32_t *draft_off, const int32_t *parent, int32_t N, int32_t max_draft,
+                                   const qsa_bf16 *k_cache, const qsa_bf16 *v_cache, int64_t n_pages,
+                                   const int32_t *table, int64_t table_ld, const int32_t *seq_len, int32_t B,
+                                   qsa_bf16 *out, float *lse, void *ws, size_t ws_bytes, qsa_stream stream) {
+    TreeArgs a{};
+    a.q = q, a.q_ld = q_ld, a.draft_off = draft_off, a.parent = parent, a.N = N, a.max_draft = max_draft;
+    a.k = k_cache, a.v = v_cache, a.n_pages = n_pages, a.table = table, a.ld = table_ld, a.seq_len = seq_len, a.B = B;
+    a.out = out, a.lse = lse;
+    return tree_decode("qsa_tree_decode", cfg, a, ws, ws_bytes, stream, false);
+}
+
+QSA_API qsa_status qsa_tree_decode_fp8kv(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
+                                         const int32_t *draft_off, const int32_t *parent, int32_t N,
+                                         int32_t max_draft, const uint8_t *k_codes, const float *k_scales,
+                                         const uint8_t *v_codes, const float *v_scales, int64_t n_pages,
+                                         const int32_t *table, int64_t table_ld, const int32_t *seq_len, int32_t B,
+                                         qsa_bf16 *out, float *lse, void *ws, size_t ws_bytes, qsa_stream stream) {
+    TreeArgs a{};
+    a.q = q, a.q_ld = q_ld, a.draft_off = draft_off, a.parent = parent, a.N = N, a.max_draft = max_draft;
+    a.k = k_codes, a.v = v_codes, a.k_scales = k_scales, a.v_scales = v_scales;
+    a.n_pages = n_pages, a.table = table, a.ld = table_ld, a.seq_len = seq_len, a.B = B;
+    a.out = out, a.lse = lse;
+    return tree_decode("qsa_tree_decode_fp8kv", cfg, a, ws, ws_bytes, stream, true);
 }
 
 QSA_API size_t qsa_pages_workspace_size(int32_t n_rows, int64_t n_pages) {
@@ -411,6 +623,65 @@ QSA_API qsa_status qsa_compact_pages(int32_t page_size, const int32_t *table, co
     a.hdr = static_cast<WsHeader *>(ws);
     a.scratch = static_cast<char *>(ws) + kWsHeaderBytes;
     return launched(launch_compact_pages(a, groups, static_cast<cudaStream_t>(stream)), call);
+}
+
+QSA_API size_t qsa_keep_workspace_size(int32_t n_rows, int64_t max_tokens) {
+    if (n_rows < 0 || n_rows > kMaxPageRows || max_tokens < 0 || max_tokens > INT32_MAX) return 0;
+    return kWsHeaderBytes + keep_scratch_bytes(n_rows, max_tokens);
+}
+
+QSA_API qsa_status qsa_accept_drafts(int32_t page_size, const int32_t *draft_off, const int32_t *parent, int32_t N,
+                                     const int32_t *accepted, const int32_t *table, const int32_t *seq_len,
+                                     int32_t n_rows, int64_t ld, const int32_t *ref, int64_t n_pages, int32_t *table_out,
+                                     int32_t *seq_len_out, int32_t *ref_out, int32_t *positions, int64_t positions_ld,
+                                     const qsa_page_planes *planes, int32_t n_groups, void *ws, size_t ws_bytes,
+                                     qsa_stream stream) {
+    const char *call = "qsa_accept_drafts";
+    KeepArgs a{};
+    PlaneGroups groups;
+    a.table = table, a.seq_len = seq_len, a.ref = ref;
+    a.table_out = table_out, a.seq_len_out = seq_len_out, a.ref_out = ref_out;
+    QSA_TRY(keep_args(call, page_size, n_rows, ld, n_pages, 0, planes, n_groups, ws, ws_bytes, &a, &groups));
+    QSA_NEED(call, N >= 0 && positions_ld >= 0, "negative size");
+    QSA_NEED(call, n_rows == 0 || (draft_off && accepted && (parent || N == 0)), "NULL tensor pointer");
+    QSA_NEED(call, aligned(draft_off, 4) && aligned(parent, 4) && aligned(accepted, 4) && aligned(positions, 4),
+             "the int32 arrays must be 4-byte aligned");
+    if (n_rows == 0 && n_pages == 0) return host_ok();
+    QSA_TRY(check_planes_memory(call, groups));
+    AcceptArgs d{};
+    d.draft_off = draft_off, d.parent = parent, d.accepted = accepted, d.N = N;
+    d.positions = positions, d.positions_ld = positions_ld;
+    return launched(launch_accept_drafts(a, d, groups, static_cast<cudaStream_t>(stream)), call);
+}
+
+QSA_API qsa_status qsa_evict_tokens(int32_t page_size, const int32_t *budget, int32_t first, int32_t recent,
+                                    const float *weights, const int32_t *positions, int64_t tokens_ld,
+                                    const int32_t *table, const int32_t *seq_len, int32_t n_rows, int64_t ld,
+                                    const int32_t *ref, int64_t n_pages, float *weights_out, int32_t *positions_out,
+                                    int32_t *table_out, int32_t *seq_len_out, int32_t *ref_out,
+                                    const qsa_page_planes *planes, int32_t n_groups, void *ws, size_t ws_bytes,
+                                    qsa_stream stream) {
+    const char *call = "qsa_evict_tokens";
+    KeepArgs a{};
+    PlaneGroups groups;
+    a.table = table, a.seq_len = seq_len, a.ref = ref;
+    a.table_out = table_out, a.seq_len_out = seq_len_out, a.ref_out = ref_out;
+    QSA_NEED(call, first >= 0 && recent >= 0, "first %d and recent %d must not be negative", first, recent);
+    QSA_NEED(call, tokens_ld >= 0 && tokens_ld <= INT32_MAX, "tokens_ld %lld out of range [0, 2^31 - 1]", (long long)tokens_ld);
+    QSA_TRY(keep_args(call, page_size, n_rows, ld, n_pages, tokens_ld, planes, n_groups, ws, ws_bytes, &a, &groups));
+    QSA_NEED(call, n_rows == 0 || (budget && (tokens_ld == 0 || (weights && positions && weights_out && positions_out))),
+             "NULL tensor pointer");
+    QSA_NEED(call, tokens_ld == 0 || n_rows == 0 || (weights != weights_out && positions != positions_out),
+             "weights_out and positions_out must be other arrays than weights and positions");
+    QSA_NEED(call, aligned(budget, 4) && aligned(weights, 4) && aligned(positions, 4) && aligned(weights_out, 4) &&
+                 aligned(positions_out, 4),
+             "the arrays must be 4-byte aligned");
+    if (n_rows == 0 && n_pages == 0) return host_ok();
+    QSA_TRY(check_planes_memory(call, groups));
+    EvictArgs e{};
+    e.budget = budget, e.first = first, e.recent = recent, e.weights = weights, e.positions = positions;
+    e.weights_out = weights_out, e.positions_out = positions_out, e.tokens_ld = tokens_ld;
+    return launched(launch_evict_tokens(a, e, groups, static_cast<cudaStream_t>(stream)), call);
 }
 
 QSA_API qsa_status qsa_copy_pages(const int32_t *src, const int32_t *dst, int32_t n, const qsa_page_planes *planes,

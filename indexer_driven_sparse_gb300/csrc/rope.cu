@@ -259,17 +259,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs r, A
         }
     };
     load(h0);
-    bool ok = row < a.n_rows && pos >= 0 && pos / a.page_size < a.ld;
+    const int place = a.place ? a.place[n] : pos;
+    bool ok = row < a.n_rows && place >= 0 && place / a.page_size < a.ld;
     int page = 0;
     if (ok) {
-        page = a.table[(int64_t)row * a.ld + pos / a.page_size];
+        page = a.table[(int64_t)row * a.ld + place / a.page_size];
         ok = page >= 0 && page < a.n_pages;
     }
     if (!ok) {                                                // its K and V are left out
         if (s == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereAppend, (int)n);
         return;
     }
-    const int64_t slot = (int64_t)page * a.page_size + pos % a.page_size;
+    if (a.positions && s == 0 && h0 == 0 && place < a.positions_ld) a.positions[row * a.positions_ld + place] = pos;
+    const int64_t slot = (int64_t)page * a.page_size + place % a.page_size;
     if (sl.fa >= 0 && h0 < a.Hkv) turns(r, sl, pos, co, si);
     for (int h = h0; h < h1; h += kKvBatch) {
         if (h > h0) load(h);

@@ -161,7 +161,7 @@ struct Planes {
 };
 
 // kv: (k_cache, v_cache), or (k_codes, k_scales, v_codes, v_scales)
-Planes planes(Call &c, const qsa_paged_config &cfg, PyObject *kv, bool fp8) {
+Planes planes(Call &c, const qsa_paged_config &cfg, PyObject *kv, bool fp8, bool or_host = true) {
     Planes p{};
     PyObject *fast = PySequence_Fast(kv, "the cache must be a sequence of tensors");
     if (fast == nullptr) throw Raised();
@@ -175,19 +175,19 @@ Planes planes(Call &c, const qsa_paged_config &cfg, PyObject *kv, bool fp8) {
     const int64_t rows[4] = {p.n_pages, cfg.page_size, cfg.n_kv_heads, cfg.head_dim};
     const int64_t groups[4] = {p.n_pages, cfg.page_size, cfg.n_kv_heads, cfg.head_dim / 128};
     if (fp8) {
-        p.k_codes = c.at<uint8_t>(o[0], "k_codes", at::kByte, rows, true);
-        p.k_scales = c.at<float>(o[1], "k_scales", at::kFloat, groups, true);
-        p.v_codes = c.at<uint8_t>(o[2], "v_codes", at::kByte, rows, true);
-        p.v_scales = c.at<float>(o[3], "v_scales", at::kFloat, groups, true);
+        p.k_codes = c.at<uint8_t>(o[0], "k_codes", at::kByte, rows, or_host);
+        p.k_scales = c.at<float>(o[1], "k_scales", at::kFloat, groups, or_host);
+        p.v_codes = c.at<uint8_t>(o[2], "v_codes", at::kByte, rows, or_host);
+        p.v_scales = c.at<float>(o[3], "v_scales", at::kFloat, groups, or_host);
     } else {
-        p.k = c.at<qsa_bf16>(o[0], "k_cache", at::kBFloat16, rows, true);
-        p.v = c.at<qsa_bf16>(o[1], "v_cache", at::kBFloat16, rows, true);
+        p.k = c.at<qsa_bf16>(o[0], "k_cache", at::kBFloat16, rows, or_host);
+        p.v = c.at<qsa_bf16>(o[1], "v_cache", at::kBFloat16, rows, or_host);
     }
     return p;
 }
 
-// rope_append[_fp8kv](cfg, rope_cfg, phase, amplitude, q, k, v, pos, seq, q_out, kv, table, ws, stream)
-template <bool F8>
+// rope_append[_at][_fp8kv](cfg, rope_cfg, phase, amplitude, q, k, v, pos, seq, q_out, kv, table, ws, stream[, place, positions])
+template <bool F8, bool At>
 qsa_status rope_append(PyObject *const *a) {
     Call c;
     const auto cfg = config<qsa_paged_config>(a[0], "qsa_paged_config");
@@ -212,6 +212,21 @@ qsa_status rope_append(PyObject *const *a) {
     const float amplitude = static_cast<float>(number(a[3]));
     const auto N = static_cast<int32_t>(n), rows = length(table, "table");
     void *st = c.stream(a[13]);
+    if (At) {
+        const auto *place = c.at<int32_t>(a[14], "place", at::kInt, {n});
+        int32_t *positions = nullptr;
+        int64_t positions_ld = 0;
+        if (a[15] != Py_None) {
+            positions_ld = matrix(a[15], "positions").size(1);
+            positions = c.at<int32_t>(a[15], "positions", at::kInt, {rows, positions_ld});
+        }
+        if (F8)
+            return qsa_rope_append_at_fp8kv(&cfg, &rope, phase, amplitude, q, q_ld, k, k_ld, v, v_ld, seq, pos, place, N, q_out,
+                                            q_out_ld, p.k_codes, p.k_scales, p.v_codes, p.v_scales, p.n_pages, entries,
+                                            table.size(1), rows, positions, positions_ld, ws.p, ws.bytes, st);
+        return qsa_rope_append_at(&cfg, &rope, phase, amplitude, q, q_ld, k, k_ld, v, v_ld, seq, pos, place, N, q_out, q_out_ld,
+                                  p.k, p.v, p.n_pages, entries, table.size(1), rows, positions, positions_ld, ws.p, ws.bytes, st);
+    }
     if (F8)
         return qsa_rope_append_fp8kv(&cfg, &rope, phase, amplitude, q, q_ld, k, k_ld, v, v_ld, seq, pos, N, q_out, q_out_ld,
                                      p.k_codes, p.k_scales, p.v_codes, p.v_scales, p.n_pages, entries, table.size(1), rows,
@@ -241,6 +256,59 @@ qsa_status paged_decode(PyObject *const *a) {
                                       table.size(1), seq_len, B, out, lse, ws.p, ws.bytes, st);
     return qsa_paged_decode(&cfg, q, q_ld, p.k, p.v, p.n_pages, entries, table.size(1), seq_len, B, out, lse, ws.p, ws.bytes,
                             st);
+}
+
+// paged_decode_weights[_fp8kv](cfg, q, kv, table, seq_len, out, lse, weights, ws, stream)
+template <bool F8>
+qsa_status paged_decode_weights(PyObject *const *a) {
+    Call c;
+    const auto cfg = config<qsa_paged_config>(a[0], "qsa_paged_config");
+    const Tensor &table = matrix(a[3], "table");
+    const int32_t B = length(table, "table");
+    int64_t q_ld;
+    const auto *q = c.rows(a[1], "q", B, cfg.n_q_heads, cfg.head_dim, q_ld);
+    const auto *seq_len = c.at<int32_t>(a[4], "seq_len", at::kInt, {B});
+    auto *out = c.at<qsa_bf16>(a[5], "out", at::kBFloat16, {B, cfg.n_q_heads, cfg.head_dim});
+    auto *lse = a[6] == Py_None ? nullptr : c.at<float>(a[6], "lse", at::kFloat, {B, cfg.n_q_heads});
+    const Tensor &w = of_type(a[7], "weights", at::kFloat);
+    if (w.dim() != 2) raise(PyExc_ValueError, "weights must have two dimensions");
+    auto *weights = c.at<float>(a[7], "weights", at::kFloat, {B, w.size(1)});
+    const auto *entries = c.address<int32_t>(table, "table");
+    const Planes p = planes(c, cfg, a[2], F8);
+    const Workspace ws = workspace(c, a[8]);
+    void *st = c.stream(a[9]);
+    if (F8)
+        return qsa_paged_decode_weights_fp8kv(&cfg, q, q_ld, p.k_codes, p.k_scales, p.v_codes, p.v_scales, p.n_pages, entries,
+                                              table.size(1), seq_len, B, out, lse, weights, w.size(1), ws.p, ws.bytes, st);
+    return qsa_paged_decode_weights(&cfg, q, q_ld, p.k, p.v, p.n_pages, entries, table.size(1), seq_len, B, out, lse, weights,
+                                    w.size(1), ws.p, ws.bytes, st);
+}
+
+// tree_decode[_fp8kv](cfg, q, draft_off, parent, max_draft, kv, table, seq_len, out, lse, ws, stream)
+template <bool F8>
+qsa_status tree_decode(PyObject *const *a) {
+    Call c;
+    const auto cfg = config<qsa_paged_config>(a[0], "qsa_paged_config");
+    const int32_t n = length(tensor(a[1], "q"), "q");
+    const Tensor &table = matrix(a[6], "table");
+    const int32_t B = length(table, "table");
+    int64_t q_ld;
+    const auto *q = c.rows(a[1], "q", n, cfg.n_q_heads, cfg.head_dim, q_ld);
+    const auto *off = c.at<int32_t>(a[2], "draft_off", at::kInt, {static_cast<int64_t>(B) + 1});
+    const auto *parent = c.at<int32_t>(a[3], "parent", at::kInt, {n});
+    const int32_t max_draft = whole(a[4]);
+    const auto *seq_len = c.at<int32_t>(a[7], "seq_len", at::kInt, {B});
+    auto *out = c.at<qsa_bf16>(a[8], "out", at::kBFloat16, {n, cfg.n_q_heads, cfg.head_dim});
+    auto *lse = a[9] == Py_None ? nullptr : c.at<float>(a[9], "lse", at::kFloat, {n, cfg.n_q_heads});
+    const auto *entries = c.address<int32_t>(table, "table");
+    const Planes p = planes(c, cfg, a[5], F8, false);
+    const Workspace ws = workspace(c, a[10]);
+    void *st = c.stream(a[11]);
+    if (F8)
+        return qsa_tree_decode_fp8kv(&cfg, q, q_ld, off, parent, n, max_draft, p.k_codes, p.k_scales, p.v_codes, p.v_scales,
+                                     p.n_pages, entries, table.size(1), seq_len, B, out, lse, ws.p, ws.bytes, st);
+    return qsa_tree_decode(&cfg, q, q_ld, off, parent, n, max_draft, p.k, p.v, p.n_pages, entries, table.size(1), seq_len, B, out,
+                           lse, ws.p, ws.bytes, st);
 }
 
 // A list of pool tensors [n_planes, n_pages, ...] with contiguous planes.
@@ -344,6 +412,68 @@ qsa_status copy_pages(PyObject *const *a) {
                           c.stream(a[5]));
 }
 
+// What accept_drafts and evict_tokens share: a table and its rows' lengths, the pool's references, and what they become.
+struct Kept {
+    const int32_t *table, *seq_len, *ref;
+    int32_t *table_out, *len_out, *ref_out;
+    int32_t rows;
+    int64_t ld, n_pages;
+};
+Kept kept(Call &c, PyObject *table, PyObject *seq_len, PyObject *ref, PyObject *table_out, PyObject *len_out, PyObject *ref_out) {
+    Kept k{};
+    const Tensor &t = matrix(table, "table");
+    k.rows = length(t, "table");
+    k.ld = t.size(1);
+    k.n_pages = length(tensor(ref, "ref"), "ref");
+    k.table = c.address<int32_t>(t, "table");
+    k.seq_len = c.at<int32_t>(seq_len, "seq_len", at::kInt, {k.rows});
+    k.ref = c.at<int32_t>(ref, "ref", at::kInt, {k.n_pages});
+    k.table_out = c.at<int32_t>(table_out, "table_out", at::kInt, {k.rows, k.ld});
+    k.len_out = c.at<int32_t>(len_out, "seq_len_out", at::kInt, {k.rows});
+    k.ref_out = c.at<int32_t>(ref_out, "ref_out", at::kInt, {k.n_pages});
+    return k;
+}
+
+// accept_drafts(page_size, draft_off, parent, accepted, table, seq_len, ref, table_out, seq_len_out, ref_out, planes, ws,
+// positions, stream)
+qsa_status accept_drafts(PyObject *const *a) {
+    Call c;
+    const Kept k = kept(c, a[4], a[5], a[6], a[7], a[8], a[9]);
+    const int32_t n = length(tensor(a[2], "parent"), "parent");
+    const auto *off = c.at<int32_t>(a[1], "draft_off", at::kInt, {static_cast<int64_t>(k.rows) + 1});
+    const auto *parent = c.at<int32_t>(a[2], "parent", at::kInt, {n});
+    const auto *accepted = c.at<int32_t>(a[3], "accepted", at::kInt, {k.rows});
+    const Groups g = groups(c, a[10], k.n_pages);
+    const Workspace ws = workspace(c, a[11]);
+    int32_t *positions = nullptr;
+    int64_t positions_ld = 0;
+    if (a[12] != Py_None) {
+        positions_ld = matrix(a[12], "positions").size(1);
+        positions = c.at<int32_t>(a[12], "positions", at::kInt, {k.rows, positions_ld});
+    }
+    return qsa_accept_drafts(whole(a[0]), off, parent, n, accepted, k.table, k.seq_len, k.rows, k.ld, k.ref, k.n_pages,
+                             k.table_out, k.len_out, k.ref_out, positions, positions_ld, g.g, g.n, ws.p, ws.bytes,
+                             c.stream(a[13]));
+}
+
+// evict_tokens(page_size, budget, first, recent, weights, positions, table, seq_len, ref, weights_out, positions_out,
+// table_out, seq_len_out, ref_out, planes, ws, stream)
+qsa_status evict_tokens(PyObject *const *a) {
+    Call c;
+    const Kept k = kept(c, a[6], a[7], a[8], a[11], a[12], a[13]);
+    const auto *budget = c.at<int32_t>(a[1], "budget", at::kInt, {k.rows});
+    const int64_t tokens = matrix(a[5], "positions").size(1);
+    const auto *positions = c.at<int32_t>(a[5], "positions", at::kInt, {k.rows, tokens});
+    const auto *weights = c.at<float>(a[4], "weights", at::kFloat, {k.rows, tokens});
+    auto *weights_out = c.at<float>(a[9], "weights_out", at::kFloat, {k.rows, tokens});
+    auto *positions_out = c.at<int32_t>(a[10], "positions_out", at::kInt, {k.rows, tokens});
+    const Groups g = groups(c, a[14], k.n_pages);
+    const Workspace ws = workspace(c, a[15]);
+    return qsa_evict_tokens(whole(a[0]), budget, whole(a[2]), whole(a[3]), weights, positions, tokens, k.table, k.seq_len, k.rows,
+                            k.ld, k.ref, k.n_pages, weights_out, positions_out, k.table_out, k.len_out, k.ref_out, g.g, g.n,
+                            ws.p, ws.bytes, c.stream(a[16]));
+}
+
 template <qsa_status (*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != N) {
@@ -360,18 +490,26 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     }
 }
 
-#define QSA_METHOD(name, f, n) \
-    {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
+#define QSA_METHOD(name, n, ...) \
+    {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<__VA_ARGS__, n>)), METH_FASTCALL, nullptr}
 
 PyMethodDef methods[] = {
-    QSA_METHOD("rope", rope, 7),
-    QSA_METHOD("rope_append", rope_append<false>, 14),
-    QSA_METHOD("rope_append_fp8kv", rope_append<true>, 14),
-    QSA_METHOD("paged_decode", paged_decode<false>, 9),
-    QSA_METHOD("paged_decode_fp8kv", paged_decode<true>, 9),
-    QSA_METHOD("fork_pages", fork_pages, 12),
-    QSA_METHOD("compact_pages", compact_pages, 9),
-    QSA_METHOD("copy_pages", copy_pages, 6),
+    QSA_METHOD("rope", 7, rope),
+    QSA_METHOD("rope_append", 14, rope_append<false, false>),
+    QSA_METHOD("rope_append_fp8kv", 14, rope_append<true, false>),
+    QSA_METHOD("rope_append_at", 16, rope_append<false, true>),
+    QSA_METHOD("rope_append_at_fp8kv", 16, rope_append<true, true>),
+    QSA_METHOD("paged_decode", 9, paged_decode<false>),
+    QSA_METHOD("paged_decode_fp8kv", 9, paged_decode<true>),
+    QSA_METHOD("paged_decode_weights", 10, paged_decode_weights<false>),
+    QSA_METHOD("paged_decode_weights_fp8kv", 10, paged_decode_weights<true>),
+    QSA_METHOD("tree_decode", 12, tree_decode<false>),
+    QSA_METHOD("tree_decode_fp8kv", 12, tree_decode<true>),
+    QSA_METHOD("fork_pages", 12, fork_pages),
+    QSA_METHOD("compact_pages", 9, compact_pages),
+    QSA_METHOD("copy_pages", 6, copy_pages),
+    QSA_METHOD("accept_drafts", 14, accept_drafts),
+    QSA_METHOD("evict_tokens", 17, evict_tokens),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -248,12 +248,19 @@ class PagedCache:
     A decode step is ``extend`` (room for the new tokens of the rows in use), then per layer ``append`` and
     ``attend``; ``fork`` starts rows, lets them continue other rows (beams, shared prompts) or gives their pages
     back, and ``compact`` moves the live pages to the front of the pool. A row that finds no page left becomes empty,
-    which ``status`` tells. Nothing else here synchronises. ``fork`` (``extend`` with it) and ``compact`` write
-    beside what they read and then change over: a captured CUDA graph holds an even number of each."""
+    which ``status`` tells. Nothing else here synchronises. ``fork`` (``extend`` with it), ``compact``, ``accept`` and
+    ``evict`` write beside what they read and then change over: a captured CUDA graph holds an even number of those that
+    change the table (``fork``, ``accept``, ``evict``), of those that change ``ref`` (all) and of those that change the
+    weights (``fork`` and ``evict`` of an evictable cache).
+
+    Drafted tokens (max_draft > 0, the most in a row): room by ``extend(count)``, then per layer ``append`` with their places
+    and positions and ``attend_tree``; ``accept`` keeps the accepted path. An evictable cache accumulates in ``weights[r, j]``
+    what token j of row r receives (``attend`` with weigh=True) and holds its position in ``positions[r, j]`` (``append`` of
+    layer 0 with a place); ``evict`` cuts rows to a budget. Its window must be 0: places are no positions any more."""
 
     def __init__(self, n_layers: int, n_pages: int, page_size: int, n_rows: int, max_pages: int, n_q_heads: int,
                  n_kv_heads: int, head_dim: int = 256, fp8: bool = False, softmax_scale: float = 0.0, window: int = 0,
-                 device="cuda"):
+                 device="cuda", max_draft: int = 0, evictable: bool = False, weighed_tokens: int | None = None):
         self.cfg = qb.make_paged_config(n_q_heads, n_kv_heads, head_dim, page_size, softmax_scale, window)
         self.fp8, self.device, self.n_rows = fp8, device, n_rows
         shape = (n_layers, n_pages, page_size, n_kv_heads)
@@ -274,6 +281,20 @@ class PagedCache:
         self._one = torch.zeros(n_rows, **i32)        # extend's: 1 for each row that holds tokens
         self.ws = qb.paged_workspace(self.cfg, device)
         self.pages_ws = qb.pages_workspace(n_rows, n_pages, device)
+        self.max_draft, self.evictable = max_draft, evictable
+        places = max_pages * page_size
+        if evictable and window:
+            raise ValueError("an evictable cache has no window")
+        if max_draft:
+            self.tree_ws = qb.tree_workspace(self.cfg, max_draft, device)
+        if max_draft or evictable:
+            self.keep_ws = qb.keep_workspace(n_rows, places if evictable else 0, device)
+        if evictable:
+            # weighed_tokens: the most tokens that one attend weighs (None: the pool's, each by one row)
+            self.weights_ws = qb.weights_workspace(self.cfg, n_rows, weighed_tokens or n_pages * page_size, device)
+            self._weights = [torch.zeros(n_rows, places, dtype=torch.float32, device=device) for _ in range(2)]
+            self._positions = [torch.full((n_rows, places), -1, **i32) for _ in range(2)]
+            self._weights_now = 0
 
     @property
     def table(self):
@@ -287,8 +308,26 @@ class PagedCache:
     def ref(self):
         return self._refs[self._ref_now]
 
+    @property
+    def weights(self):
+        return self._weights[self._weights_now]
+
+    @property
+    def positions(self):
+        return self._positions[self._weights_now]
+
     def fork(self, parent, add, stream=None):
         """Row i continues row parent[i] (-1: starts empty) with room for add[i] more tokens (qsa_fork_pages)."""
+        self._fork(parent, add, stream)
+        if self.evictable:                            # what is kept per row goes with it
+            new = 1 - self._weights_now
+            with _on_stream(stream):
+                row, empty = parent.clamp(min=0, max=self.n_rows - 1), (parent < 0)[:, None]
+                torch.index_select(self.weights, 0, row, out=self._weights[new]).masked_fill_(empty, 0.0)
+                torch.index_select(self.positions, 0, row, out=self._positions[new]).masked_fill_(empty, -1)
+            self._weights_now = new
+
+    def _fork(self, parent, add, stream):
         new, new_ref = 1 - self._now, 1 - self._ref_now
         qb.qsa_fork_pages(self.cfg.page_size, parent, add, self.table, self.seq_len, self.ref, self._tables[new],
                           self._lens[new], self._refs[new_ref], self.planes, self.pages_ws, stream)
@@ -299,7 +338,7 @@ class PagedCache:
         if add is None:
             with _on_stream(stream):
                 add = torch.clamp(self.seq_len, 0, 1, out=self._one)
-        self.fork(self._rows, add, stream)
+        self._fork(self._rows, add, stream)
 
     def compact(self, stream=None):
         new_ref = 1 - self._ref_now
@@ -307,22 +346,73 @@ class PagedCache:
                              self.planes, self.pages_ws, stream)
         self._ref_now = new_ref
 
-    def append(self, layer: int, rope, q, k, v, pos, seq=None, q_out=None, stream=None):
-        """Store k (turned) and v at position pos[n] of row seq[n] (None: row n) of a layer; q turned into q_out."""
+    def append(self, layer: int, rope, q, k, v, pos, seq=None, q_out=None, stream=None, place=None):
+        """Store k (turned) and v at position pos[n] of row seq[n] (None: row n) of a layer; q turned into q_out. place[n]:
+        the token's place in its row, where that is not its position."""
         planes = [p[layer] for p in self.planes]
+        if place is not None:
+            positions = self.positions if self.evictable and layer == 0 else None
+            if self.fp8:
+                qb.qsa_rope_append_at_fp8kv(self.cfg, rope, q, k, v, pos, place, seq, q_out, planes, self.table, self.ws,
+                                            positions, stream)
+            else:
+                qb.qsa_rope_append_at(self.cfg, rope, q, k, v, pos, place, seq, q_out, *planes, self.table, self.ws, positions,
+                                      stream)
+            return
         if self.fp8:
             qb.qsa_rope_append_fp8kv(self.cfg, rope, q, k, v, pos, seq, q_out, planes, self.table, self.ws, stream)
         else:
             qb.qsa_rope_append(self.cfg, rope, q, k, v, pos, seq, q_out, *planes, self.table, self.ws, stream)
 
-    def attend(self, layer: int, q, out, lse=None, stream=None):
-        """Attention of each row's newest token over the row's tokens of a layer."""
+    def attend(self, layer: int, q, out, lse=None, stream=None, weigh=False):
+        """Attention of each row's newest token over the row's tokens of a layer; weigh: what each token receives is added
+        to ``weights``."""
         planes = [p[layer] for p in self.planes]
+        if weigh:
+            if self.fp8:
+                qb.qsa_paged_decode_weights_fp8kv(self.cfg, q, planes, self.table, self.seq_len, out, lse, self.weights,
+                                                  self.weights_ws, stream)
+            else:
+                qb.qsa_paged_decode_weights(self.cfg, q, *planes, self.table, self.seq_len, out, lse, self.weights,
+                                            self.weights_ws, stream)
+            return
         if self.fp8:
             qb.qsa_paged_decode_fp8kv(self.cfg, q, planes, self.table, self.seq_len, out, lse, self.ws, stream)
         else:
             qb.qsa_paged_decode(self.cfg, q, *planes, self.table, self.seq_len, out, lse, self.ws, stream)
 
+    def attend_tree(self, layer: int, q, draft_off, parent, out, lse=None, stream=None):
+        """Attention of every row's drafted tokens, its newest, each over the cached tokens, its ancestors and itself."""
+        planes = [p[layer] for p in self.planes]
+        if self.fp8:
+            qb.qsa_tree_decode_fp8kv(self.cfg, q, draft_off, parent, self.max_draft, planes, self.table, self.seq_len, out,
+                                     lse, self.tree_ws, stream)
+        else:
+            qb.qsa_tree_decode(self.cfg, q, draft_off, parent, self.max_draft, *planes, self.table, self.seq_len, out, lse,
+                               self.tree_ws, stream)
+
+    def accept(self, draft_off, parent, accepted, stream=None):
+        """Of each row's drafted tokens keep accepted[r] (-1: none) and its ancestors (qsa_accept_drafts)."""
+        new, new_ref = 1 - self._now, 1 - self._ref_now
+        qb.qsa_accept_drafts(self.cfg.page_size, draft_off, parent, accepted, self.table, self.seq_len, self.ref,
+                             self._tables[new], self._lens[new], self._refs[new_ref], self.planes, self.keep_ws,
+                             self.positions if self.evictable else None, stream)
+        self._now, self._ref_now = new, new_ref
+
+    def evict(self, budget, first: int, recent: int, stream=None):
+        """Cut row r to budget[r] tokens (negative: as it is): positions below `first`, the last `recent` ones and shared
+        pages stay, and the heaviest of the others (qsa_evict_tokens)."""
+        new, new_ref, new_w = 1 - self._now, 1 - self._ref_now, 1 - self._weights_now
+        qb.qsa_evict_tokens(self.cfg.page_size, budget, first, recent, self.weights, self.positions, self.table, self.seq_len,
+                            self.ref, self._weights[new_w], self._positions[new_w], self._tables[new], self._lens[new],
+                            self._refs[new_ref], self.planes, self.keep_ws, stream)
+        self._now, self._ref_now, self._weights_now = new, new_ref, new_w
+
     def status(self, stream=None):
         """(status, detail) of the attention and append calls, then of the page calls."""
         return qb.qsa_read_device_status(self.ws, stream), qb.qsa_read_device_status(self.pages_ws, stream)
+
+    def more_status(self, stream=None):
+        """(status, detail) of attend_tree, of attend with weigh, and of accept and evict, for those the cache is made for."""
+        return tuple(qb.qsa_read_device_status(ws, stream)
+                     for ws in (getattr(self, name, None) for name in ("tree_ws", "weights_ws", "keep_ws")) if ws is not None)

@@ -1,0 +1,786 @@
+"""The paged cache's operators for drafted tokens and eviction on the GPU against a plain 64-bit implementation: tokens
+stored at a place that is not their position, attention of a tree of drafted tokens, accepting its path, attention that
+accumulates each token's weight, evicting the lightest tokens, and runs of them together.
+
+Tolerances. Those of the paged attention's tests (scores: D 2^-24 of the terms and 2^-21; a weight twice that, 2^-15 and the
+fp32 sums over n tokens; the result's own rounding to bf16, 2^-8), and:
+- a tree's weights enter the second product as bf16, half a step of its 8 bits, 2^-8 of each (over FP8 rows with V's scale
+  as f16: 2^-11 of each, and 2^-31 of the largest below f16's normal range);
+- an accumulated weight sums Hq weights, each off by twice its score's error and 2^-21 for the exponential, and adds them
+  in fp32: (Hq + 1) 2^-24 of the sum."""
+
+import numpy as np
+import pytest
+import torch
+
+from indexer_driven_sparse_gb300 import binding as qb
+from indexer_driven_sparse_gb300.pipeline import PagedCache
+from oracle import drafts_oracle as T
+from oracle import paged_oracle as P
+from tests.test_gpu_paged import DECODE_GEOMETRY, DEV, check_decode, f64, ints, paged_inputs, randn, run_decode, status
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------------ places and positions
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_at_a_place(cuda_lib, fp8, inter):
+    """The bits that qsa_rope_append writes at position p are those that qsa_rope_append_at writes at place x for position p."""
+    n, Hq, Hkv, D, page, rows, ld = 37, 8, 2, 128, 5, 3, 9
+    rng = np.random.default_rng(3)
+    room = ld * page
+    flat = rng.permutation(rows * room)[:n]
+    seq, place = flat // room, flat % room
+    seq[5], pos = -1, rng.integers(0, room, n)
+    used = {}
+    for i in range(n):                                    # positions distinct within a row, to compare by
+        while (seq[i], pos[i]) in used:
+            pos[i] = (pos[i] + 1) % room
+        used[(seq[i], pos[i])] = i
+    table = ints(rng.permutation(rows * ld).reshape(rows, ld).tolist())
+    x = randn((n, Hq + 2 * Hkv, D), 1)
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    cfg = qb.make_paged_config(Hq, Hkv, D, page)
+    ws = qb.paged_workspace(cfg)
+    rope = qb.rope_table(D, 64, interleaved=inter, base=1e5)
+
+    def planes():
+        shape = (rows * ld, page, Hkv, D)
+        if fp8:
+            return [torch.full(shape[:3] + (w,), 9, dtype=t, device=DEV)
+                    for w, t in ((D, torch.uint8), (1, torch.float32)) * 2]
+        return [torch.full(shape, 9.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+
+    a, b = planes(), planes()
+    qa, qb_ = torch.full((2, n, Hq, D), 9.0, dtype=torch.bfloat16, device=DEV)
+    positions = torch.full((rows, room - 2), -7, dtype=torch.int32, device=DEV)
+    s, p, at = ints(seq.tolist()), ints(pos.tolist()), ints(place.tolist())
+    if fp8:
+        qb.qsa_rope_append_fp8kv(cfg, rope, q, k, v, p, s, qa, a, table, ws)
+        qb.qsa_rope_append_at_fp8kv(cfg, rope, q, k, v, p, at, s, qb_, b, table, ws, positions)
+    else:
+        qb.qsa_rope_append(cfg, rope, q, k, v, p, s, qa, *a, table, ws)
+        qb.qsa_rope_append_at(cfg, rope, q, k, v, p, at, s, qb_, *b, table, ws, positions)
+    assert torch.equal(qa, qb_) and status(ws) == (0, 0)
+    tab, want = table.cpu().numpy(), np.full((rows, room - 2), -7)
+    for i in range(n):
+        if seq[i] < 0:
+            continue
+        if place[i] < room - 2:
+            want[seq[i], place[i]] = pos[i]
+        for u, w in zip(a, b):
+            assert torch.equal(u[tab[seq[i], pos[i] // page], pos[i] % page], w[tab[seq[i], place[i] // page], place[i] % page])
+    assert np.array_equal(positions.cpu().numpy(), want)
+    places = {(tab[s_, x_ // page], x_ % page) for s_, x_ in zip(seq, place) if s_ >= 0}
+    for w in b:                                           # nothing else is written
+        rest = [(g, o) for g in range(rows * ld) for o in range(page) if (g, o) not in places]
+        assert bool((w[[g for g, _ in rest], [o for _, o in rest]] == 9).all())
+
+
+@pytest.mark.parametrize("seq,place,page", [(3, 0, 0), (0, -1, 0), (0, 16, 0), (0, 3, -1), (0, 3, 4)])
+def test_append_at_skips_and_records_bad_places(cuda_lib, seq, place, page):
+    cfg = qb.make_paged_config(4, 1, 64, 4)
+    ws = qb.paged_workspace(cfg)
+    kc, vc = torch.full((2, 4, 4, 1, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    table = ints([[page, page, page, page]] * 3)
+    positions = torch.full((3, 16), -7, dtype=torch.int32, device=DEV)
+    q = randn((1, 4, 64), 1)
+    out = torch.zeros_like(q)
+    qb.qsa_rope_append_at(cfg, qb.rope_table(64), q, q[:, :1], q[:, 1:2], ints([2]), ints([place]), ints([seq]), out, kc, vc,
+                          table, ws, positions)
+    assert status(ws) == (qb.QSA_ERR_DEVICE_BOUNDS, 0)
+    assert bool((vc == 5).all()) and bool((kc == 5).all()) and bool((positions == -7).all()) and bool(out.any())
+
+
+# ------------------------------------------------------------------------------------------ trees
+def random_parents(rng, count, chain=0.6):
+    """Parents of `count` tokens: mostly chains."""
+    return [i - 1 if rng.random() < chain else int(rng.integers(-1, i)) if i else -1 for i in range(count)]
+
+
+def tree_inputs(lens, counts, Hq, Hkv, D, page, fp8, seed, spare_rows=3, scale=1.0, chain=0.6):
+    rng = np.random.default_rng(seed)
+    q0, planes, values, tab, table = paged_inputs(lens, Hq, Hkv, D, page, fp8, seed, scale=scale)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    parents = [random_parents(rng, c, chain) for c in counts]
+    n = int(off[-1]) + spare_rows
+    q = randn((n, Hq, D), seed + 7)
+    return q, planes, values, tab, table, off.tolist(), parents
+
+
+def run_tree(cfg, q, planes, tab, lens, off, parents, max_draft, ws, out=None, lse=None, stream=None):
+    n = q.shape[0]
+    out = torch.full((n, cfg.n_q_heads, cfg.head_dim), 8.0, dtype=torch.bfloat16, device=DEV) if out is None else out
+    lse = torch.full((n, cfg.n_q_heads), 8.0, device=DEV) if lse is None else lse
+    flat = [p for row in parents for p in row]
+    parent = ints(flat + [-5] * (n - len(flat)))
+    if len(planes) == 2:
+        qb.qsa_tree_decode(cfg, q, ints(off), parent, max_draft, *planes, tab, ints(lens), out, lse, ws, stream)
+    else:
+        qb.qsa_tree_decode_fp8kv(cfg, q, ints(off), parent, max_draft, planes, tab, ints(lens), out, lse, ws, stream)
+    return out, lse
+
+
+def check_tree(out, lse, q, values, table, lens, off, parents, page, scale, window=0, fp8=False, leave_out={}):
+    out, lse, q = f64(out), f64(lse), f64(q)
+    D = q.shape[-1]
+    for r, n in enumerate(lens):
+        slots = P.slots_of(np.maximum(table[r], 0), n, page)
+        K, V = (x.reshape(-1, *x.shape[2:])[slots] for x in values)
+        for i, (want, want_lse, mass, terms, seen) in enumerate(
+                T.tree(q[off[r]:off[r + 1]], K, V, parents[r], scale, window, leave_out.get(r, ()))):
+            got, got_lse = out[off[r] + i], lse[off[r] + i]
+            if seen == 0:
+                assert np.all(got == 0) and np.all(np.isneginf(got_lse))
+                continue
+            ds = D * 2.0 ** -24 * terms + 2.0 ** -21 * (terms + 1)
+            sums = seen / 8 * 2.0 ** -24 + 2.0 ** -15
+            tol = 2.0 ** -8 * np.abs(want) + (2 * ds[:, None] + sums + (2.0 ** -11 if fp8 else 2.0 ** -8)) * mass
+            if fp8:
+                tol += seen * 2.0 ** -31 * mass.max(1, keepdims=True)
+            assert np.all(np.abs(got - want) <= tol), (r, i, np.abs(got - want).max(), tol.min())
+            assert np.all(np.abs(got_lse - want_lse) <= ds + sums + 2.0 ** -22 * np.abs(want_lse)), (r, i)
+    assert np.all(out[off[-1]:] == 8) and np.all(lse[off[-1]:] == 8)      # rows that no sequence names
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,fp8", DECODE_GEOMETRY)
+@pytest.mark.parametrize("lens,counts", [
+    ([1], [1]), ([5, 0, 3, 64, 65, 66, 1], [5, 0, 2, 1, 0, 66, 0]), ([127, 128, 129, 130, 200, 257], [1, 2, 7, 33, 16, 128]),
+    ([3000, 700], [12, 31]), ([17, 1500, 64, 700], [16, 20, 64, 100])])
+@pytest.mark.parametrize("window", [0, 50])
+def test_tree(cuda_lib, Hq, Hkv, D, page, fp8, lens, counts, window):
+    if max(counts) * Hq > 600:                            # keeps the oracle quick
+        counts = [min(c, 600 // Hq) for c in counts]
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, Hq, Hkv, D, page, fp8, seed=Hq + D + len(lens))
+    cfg = qb.make_paged_config(Hq, Hkv, D, page, window=window)
+    ws = qb.tree_workspace(cfg, max(counts))
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, parents, max(counts), ws)
+    assert status(ws) == (0, 0)
+    check_tree(out, lse, q, values, table, lens, off, parents, page, D ** -0.5, window, fp8)
+    again, lse2 = run_tree(cfg, q, planes, tab, lens, off, parents, max(counts), ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    third = torch.full_like(out, 8.0)                     # without lse
+    parent = ints([p for row in parents for p in row] + [-1] * 3)
+    if fp8:
+        qb.qsa_tree_decode_fp8kv(cfg, q, ints(off), parent, max(counts), planes, tab, ints(lens), third, None, ws)
+    else:
+        qb.qsa_tree_decode(cfg, q, ints(off), parent, max(counts), *planes, tab, ints(lens), third, None, ws)
+    assert torch.equal(out, third)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,fp8", [(16, 2, 256, 64, False), (8, 2, 128, 16, False), (4, 4, 64, 100, False),
+                                               (16, 1, 256, 48, True), (32, 8, 128, 24, True)])
+@pytest.mark.parametrize("max_draft", [8, 64])
+def test_tree_long_and_many(cuda_lib, Hq, Hkv, D, page, fp8, max_draft):
+    """Rows of very different lengths and trees, more of them than fit in one wave; a scale of its own."""
+    rng = np.random.default_rng(max_draft)
+    lens = [9000] + rng.integers(0, 200, 150).tolist() + [4000, 1]
+    counts = [min(n, int(c)) for n, c in zip(lens, rng.integers(0, 4, len(lens)))]
+    counts[0], counts[7] = min(max_draft, 12), min(lens[7], max_draft)
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, Hq, Hkv, D, page, fp8, seed=9)
+    cfg = qb.make_paged_config(Hq, Hkv, D, page, softmax_scale=0.11)
+    ws = qb.tree_workspace(cfg, max_draft)
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, parents, max_draft, ws)
+    assert status(ws) == (0, 0)
+    check_tree(out, lse, q, values, table, lens, off, parents, page, float(np.float32(0.11)), 0, fp8)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,fp8", [(16, 2, 256, False), (6, 1, 128, False), (8, 1, 64, False), (16, 2, 256, True),
+                                          (9, 1, 128, True)])
+def test_a_tree_of_one_token_is_the_decode(cuda_lib, Hq, Hkv, D, fp8):
+    """One drafted token a row: the attention of qsa_paged_decode, within both operators' roundings."""
+    lens = [1, 64, 130, 1000, 4097]
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, [1] * 5, Hq, Hkv, D, 16, fp8, seed=4, spare_rows=0)
+    cfg = qb.make_paged_config(Hq, Hkv, D, 16)
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, parents, 1, qb.tree_workspace(cfg, 1))
+    want, want_lse = run_decode(cfg, q, planes, tab, ints(lens), qb.paged_workspace(cfg))
+    # both are 2^-8 of a value off by their own rounding, and 2^-8 of the mean |V| by the weights'; |V| is below 5 here
+    assert bool(((out - want).abs().float() <= 2.0 ** -7 * want.abs().float() + 2.0 ** -8 * 5).all())
+    assert bool(((lse - want_lse).abs() <= 1e-4).all())
+    check_tree(out, lse, q, values, table, lens, off, parents, 16, D ** -0.5, 0, fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_chain_is_causal_attention(cuda_lib, fp8):
+    lens, counts = [40, 300], [40, 37]
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, 8, 2, 128, 16, fp8, seed=2, chain=2.0)
+    assert parents[1] == list(range(-1, 36))
+    cfg = qb.make_paged_config(8, 2, 128, 16)
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, parents, 40, qb.tree_workspace(cfg, 40))
+    for r, n in enumerate(lens):
+        for i in (0, 1, counts[r] - 1):                   # token i sees what a row cut behind it holds
+            cut = n - counts[r] + i + 1
+            w = run_tree(cfg, q[off[r] + i:off[r] + i + 1], planes, tab[r:r + 1], [cut], [0, 1], [[-1]], 1,
+                         qb.tree_workspace(cfg, 1))
+            diff = (w[0][0] - out[off[r] + i]).abs().float()
+            assert bool((diff <= 2.0 ** -7 * w[0][0].abs().float() + 2.0 ** -8 * 5).all())
+            assert bool(((w[1][0] - lse[off[r] + i]).abs() <= 1e-4).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_sharp_scores(cuda_lib, fp8):
+    """Scores of hundreds: the weights of almost all tokens vanish, and the running maximum moves often."""
+    lens, counts = [1500, 260], [9, 16]
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, 16, 2, 256, 32, fp8, seed=8, scale=12.0)
+    cfg = qb.make_paged_config(16, 2, 256, 32, softmax_scale=1.0)
+    ws = qb.tree_workspace(cfg, 16)
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, parents, 16, ws)
+    check_tree(out, lse, q, values, table, lens, off, parents, 32, 1.0, 0, fp8)
+
+
+def test_tree_strided_queries_and_another_stream(cuda_lib):
+    lens, counts = [400, 20], [6, 3]
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, 16, 2, 256, 16, False, seed=3)
+    wide = torch.full((q.shape[0], 20, 256), float("nan"), dtype=torch.bfloat16, device=DEV)
+    wide[:, 2:18] = q
+    cfg = qb.make_paged_config(16, 2, 256, 16)
+    ws = qb.tree_workspace(cfg, 6)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = run_tree(cfg, wide[:, 2:18], planes, tab, lens, off, parents, 6, ws, stream=side)
+    side.synchronize()
+    check_tree(out, lse, q, values, table, lens, off, parents, 16, 1 / 16, 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_leaves_out_and_records_bad_pages(cuda_lib, fp8):
+    lens, counts = [100, 50, 70], [4, 2, 3]
+    Hq, Hkv, D, page = 8, 2, 128, 8
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, Hq, Hkv, D, page, fp8, seed=5)
+    bad = tab.clone()
+    bad[0, 3], bad[1, 0], bad[1, 6] = -1, planes[0].shape[0], 2 ** 31 - 1
+    cfg = qb.make_paged_config(Hq, Hkv, D, page)
+    ws = qb.tree_workspace(cfg, 4)
+    out, lse = run_tree(cfg, q, planes, bad, lens, off, parents, 4, ws)
+    st, detail = status(ws)
+    assert st == qb.QSA_ERR_DEVICE_BOUNDS and detail in (0, 1)
+    gone = {0: range(24, 32), 1: list(range(8)) + [48, 49]}
+    check_tree(out, lse, q, values, table, lens, off, parents, page, D ** -0.5, 0, fp8, gone)
+
+
+@pytest.mark.parametrize("lens,off,max_draft,bad", [
+    ([30, 40, 20], [0, 5, 9, 12], 4, 0),                  # more drafted tokens than max_draft
+    ([30, 2, 20], [0, 4, 8, 12], 4, 1),                   # more drafted tokens than cached ones
+    ([30, 40, 10 ** 6], [0, 4, 8, 12], 4, 2),             # longer than its table row
+    ([30, -3, 20], [0, 4, 8, 12], 4, 1)])
+def test_tree_rows_out_of_range_attend_nothing(cuda_lib, lens, off, max_draft, bad):
+    fine = [30, 40, 20]
+    counts = np.diff(off).tolist()
+    q, planes, values, tab, table, _, parents = tree_inputs(fine, counts, 8, 2, 128, 8, False, seed=6)
+    cfg = qb.make_paged_config(8, 2, 128, 8)
+    ws = qb.tree_workspace(cfg, max_draft)
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, parents, max_draft, ws)
+    assert status(ws) == (qb.QSA_ERR_DEVICE_BOUNDS, bad)
+    assert not out[off[bad]:off[bad + 1]].any() and bool(torch.isneginf(lse[off[bad]:off[bad + 1]]).all())
+    want, _ = run_tree(cfg, q, planes, tab, fine, off, parents, 5, qb.tree_workspace(cfg, 5))
+    for r in range(3):
+        if r != bad:
+            diff = (out[off[r]:off[r + 1]] - want[off[r]:off[r + 1]]).abs().float()
+            assert bool((diff <= 0.05).all()) and bool((lse[off[r]:off[r + 1]] < 8).all())
+
+
+def test_tree_offsets_out_of_range(cuda_lib):
+    """Descending offsets and offsets behind N: those rows attend nothing, and nothing outside the arrays is touched."""
+    lens, counts = [30, 40, 20], [4, 4, 4]
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, 8, 2, 128, 8, False, seed=6, spare_rows=0)
+    cfg = qb.make_paged_config(8, 2, 128, 8)
+    ws = qb.tree_workspace(cfg, 8)
+    good, _ = run_tree(cfg, q, planes, tab, lens, off, parents, 8, ws)
+    assert status(ws) == (0, 0)
+    for bad in ([0, 4, 2, 12], [0, 4, 8, 15], [-2, 4, 8, 12], [0, 4, 2 ** 31 - 1, 12], [5, 4, -2 ** 31, 2 ** 31 - 1]):
+        ws = qb.tree_workspace(cfg, 8)
+        out, lse = run_tree(cfg, q, planes, tab, lens, bad, parents, 8, ws)
+        assert status(ws)[0] == qb.QSA_ERR_DEVICE_BOUNDS
+        if bad[:2] == [0, 4]:
+            assert bool(((out[:4] - good[:4]).abs() <= 0.05).all())
+
+
+@pytest.mark.parametrize("parent,as_if", [([-1, 5, 1, 2], [-1, -1, 1, 2]), ([-1, 0, 2, 2], [-1, 0, -1, 2]), ([-2, 0, 1, 9], [-1, 0, 1, -1])])
+def test_tree_parents_out_of_range_count_as_none(cuda_lib, parent, as_if):
+    lens = [60]
+    q, planes, values, tab, table, off, _ = tree_inputs(lens, [4], 8, 2, 128, 8, False, seed=6)
+    cfg = qb.make_paged_config(8, 2, 128, 8)
+    ws = qb.tree_workspace(cfg, 4)
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, [parent], 4, ws)
+    assert status(ws) == (qb.QSA_ERR_DEVICE_BOUNDS, 0)
+    check_tree(out, lse, q, values, table, lens, off, [as_if], 8, 128 ** -0.5, 0)
+
+
+def test_tree_captured_replays_with_new_lengths(cuda_lib):
+    lens, counts = [500, 90], [6, 5]
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, 16, 2, 256, 16, False, seed=12)
+    cfg = qb.make_paged_config(16, 2, 256, 16)
+    ws = qb.tree_workspace(cfg, 9)
+    first = run_tree(cfg, q, planes, tab, lens, off, parents, 9, ws)       # before the capture
+    out, lse = (torch.full_like(t, 8.0) for t in first)
+    lens_d, off_d = ints(lens), ints(off)
+    parent = ints([p for row in parents for p in row] + [-1] * 3)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        qb.qsa_tree_decode(cfg, q, off_d, parent, 9, *planes, tab, lens_d, out, lse, ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    lens_d.copy_(ints([333, 47]))
+    off_d.copy_(ints([0, 2, 11]))
+    out.fill_(8.0), lse.fill_(8.0)
+    parents = [[-1, 0], random_parents(np.random.default_rng(1), 9)]
+    parent.copy_(ints(parents[0] + parents[1] + [-1] * 3))
+    graph.replay()
+    torch.cuda.synchronize()
+    check_tree(out, lse, q, values, table, [333, 47], [0, 2, 11], parents, 16, 1 / 16, 0)
+    assert status(ws) == (0, 0)
+
+
+# ------------------------------------------------------------------------------------------ accumulated weights
+def run_weights(cfg, q, planes, tab, lens, weights, ws, stream=None, lse=True):
+    out = torch.full((q.shape[0], cfg.n_q_heads, cfg.head_dim), 8.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((q.shape[0], cfg.n_q_heads), 8.0, device=DEV) if lse else None
+    if len(planes) == 2:
+        qb.qsa_paged_decode_weights(cfg, q, *planes, tab, lens, out, lse, weights, ws, stream)
+    else:
+        qb.qsa_paged_decode_weights_fp8kv(cfg, q, planes, tab, lens, out, lse, weights, ws, stream)
+    return out, lse
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,fp8", DECODE_GEOMETRY)
+@pytest.mark.parametrize("lens", [[1], [0, 1, 2, 15, 16, 17, 31, 63, 64, 65, 0, 127, 129], [5, 0, 1500, 700, 64, 0] + [3] * 40])
+@pytest.mark.parametrize("window", [0, 50])
+def test_weights(cuda_lib, Hq, Hkv, D, page, fp8, lens, window):
+    q, planes, values, tab, table = paged_inputs(lens, Hq, Hkv, D, page, fp8, seed=Hq + D + len(lens))
+    cfg = qb.make_paged_config(Hq, Hkv, D, page, window=window)
+    want = run_decode(cfg, q, planes, tab, ints(lens), qb.paged_workspace(cfg))
+    ws = qb.weights_workspace(cfg, len(lens), sum(lens))
+    before = torch.rand(len(lens), max(lens) + 3, generator=torch.Generator().manual_seed(1)).to(DEV)
+    weights = before.clone()
+    out, lse = run_weights(cfg, q, planes, tab, ints(lens), weights, ws)
+    assert status(ws) == (0, 0)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])        # bit for bit
+    got, old, q64 = f64(weights), f64(before), f64(q)
+    for r, n in enumerate(lens):
+        lo = max(0, n - window) if window else 0
+        assert np.array_equal(got[r, n:], old[r, n:]) and np.array_equal(got[r, :lo], old[r, :lo])
+        if n == 0:
+            continue
+        slots = P.slots_of(table[r], n, page)
+        K, V = (x.reshape(-1, *x.shape[2:])[slots] for x in values)
+        add = T.token_weights(q64[r], K, lo, D ** -0.5)
+        terms = P.decode(q64[r], K, V, lo, D ** -0.5)[3].max()
+        ds = D * 2.0 ** -24 * terms + 2.0 ** -21 * (terms + 1)
+        tol = (4 * ds + 2.0 ** -20 + n / 8 * 2.0 ** -24 + (Hq + 1) * 2.0 ** -24) * add + 2.0 ** -24 * (old[r, :n] + add)
+        assert np.all(np.abs(got[r, :n] - old[r, :n] - add) <= tol + 1e-37), r
+    twice = before.clone()                                # the same bits again, and without lse
+    run_weights(cfg, q, planes, tab, ints(lens), twice, ws, lse=False)
+    assert torch.equal(twice, weights)
+
+
+def test_weights_behind_the_array_or_the_workspace_add_nothing(cuda_lib):
+    lens = [300, 200]
+    q, planes, values, tab, table = paged_inputs(lens, 8, 2, 128, 16, False, seed=1)
+    cfg = qb.make_paged_config(8, 2, 128, 16)
+    full = torch.zeros(2, 300, device=DEV)
+    run_weights(cfg, q, planes, tab, ints(lens), full, qb.weights_workspace(cfg, 2, 500))
+    ws = qb.weights_workspace(cfg, 2, 500)
+    short = torch.zeros(2, 250, device=DEV)
+    out, _ = run_weights(cfg, q, planes, tab, ints(lens), short, ws)
+    assert status(ws) == (qb.QSA_ERR_DEVICE_BOUNDS, 0) and torch.equal(short, full[:, :250])
+    ws = qb.weights_workspace(cfg, 2, 0)                  # room for four tiles of the nine
+    some = torch.zeros(2, 300, device=DEV)
+    again, _ = run_weights(cfg, q, planes, tab, ints(lens), some, ws)
+    assert status(ws) == (qb.QSA_ERR_DEVICE_BOUNDS, -1) and torch.equal(again, out)
+    held = some != 0
+    assert bool(held.any()) and not bool(held.all()) and torch.equal(some[held], full[held])
+
+
+def test_weights_sum_to_the_heads_over_many_steps(cuda_lib):
+    """Every step adds a total of Hq to a row: each weight is within 2^-18 relative (scores' and exponential's errors are
+    below that here), each of the 50 additions rounds a total below 2^10 in fp32."""
+    lens = [777, 64, 1]
+    q, planes, values, tab, table = paged_inputs(lens, 16, 2, 256, 16, False, seed=1)
+    cfg = qb.make_paged_config(16, 2, 256, 16)
+    ws = qb.weights_workspace(cfg, 3, sum(lens))
+    weights = torch.zeros(3, 800, device=DEV)
+    for _ in range(50):
+        run_weights(cfg, q, planes, tab, ints(lens), weights, ws)
+    assert np.allclose(f64(weights).sum(1), 800.0, rtol=2.0 ** -18 + 50 * 2.0 ** -24, atol=0)
+
+
+# ------------------------------------------------------------------------------------------ accepting
+def token_planes(n_pages, page, seed):
+    """Plane groups of tokens of 48 bytes (16-byte words), of 4 bytes and of 20 bytes."""
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randint(-2 ** 15, 2 ** 15, (3, n_pages, page, 24), dtype=torch.int16, generator=g).to(DEV),
+            torch.randn((2, n_pages, page, 1), generator=g).to(DEV), torch.randn((1, n_pages, page, 5), generator=g).to(DEV)]
+
+
+def moved(plane, table, moves, page):
+    """The plane after moves {row: [(to, from)]}, all read before any is written."""
+    want = plane.clone()
+    for r, some in moves.items():
+        for to, at in some:
+            want[:, table[r][to // page], to % page] = plane[:, table[r][at // page], at % page]
+    return want
+
+
+def private_pool(lens, page, seed, spare=3, shared=0):
+    """Page table, references and lengths; the last row shares row 0's first `shared` pages."""
+    rng = np.random.default_rng(seed)
+    count = [-(-n // page) for n in lens]
+    ld, n_pages = max(count + [1]) + 1, sum(count) + spare
+    order, at = rng.permutation(n_pages), 0
+    table, ref = np.full((len(lens), ld), -1, np.int32), np.zeros(n_pages, np.int32)
+    for r, c in enumerate(count):
+        table[r, :c] = order[at:at + c]
+        at += c
+    if shared:
+        k = min(shared, lens[0] // page, lens[-1] // page)
+        table[-1, :k] = table[0, :k]
+    for r, c in enumerate(count):
+        np.add.at(ref, table[r, :c], 1)
+    return table, ref
+
+
+def filled(*shape):
+    return torch.full(shape, 77, dtype=torch.int32, device=DEV)
+
+
+ACCEPT_ROWS = [([9], [4]), ([40, 0, 7, 1, 200, 128], [8, 0, 7, 1, 128, 128]), ([300] * 70, [33] * 70),
+               ([20, 21, 22] * 500, [3, 0, 1] * 500)]
+
+
+@pytest.mark.parametrize("lens,counts", ACCEPT_ROWS)
+@pytest.mark.parametrize("page", [1, 4, 24])
+def test_accept(cuda_lib, lens, counts, page):
+    rng = np.random.default_rng(len(lens) + page)
+    table, ref = private_pool(lens, page, 1)
+    off = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    parents = [random_parents(rng, c, 0.5) for c in counts]
+    last = [int(rng.integers(-1, c)) if c else -1 for c in counts]
+    cut = [T.accept(n, p, a) for n, p, a in zip(lens, parents, last)]
+    new_len = np.array([c[0] for c in cut])
+    moves = {r: c[1] for r, c in enumerate(cut)}
+    planes = token_planes(len(ref), page, 1)
+    want = [moved(p, table, moves, page) for p in planes]
+    ld = table.shape[1]
+    t_out, l_out, r_out = filled(len(lens), ld), filled(len(lens)), filled(len(ref))
+    positions = ints(rng.integers(0, 1000, (len(lens), ld * page - 1)).tolist())
+    want_pos = positions.cpu().numpy().copy()
+    for r, some in moves.items():
+        old = want_pos[r].copy()
+        for to, at in some:
+            want_pos[r, to] = old[at]
+    ws = qb.keep_workspace(len(lens))
+    flat = ints([p for row in parents for p in row] + [0, 0])
+    args = (page, ints(off), flat, ints(last), ints(table.tolist()), ints(lens), ints(ref.tolist()))
+    qb.qsa_accept_drafts(*args, t_out, l_out, r_out, planes, ws, positions)
+    assert status(ws) == (0, 0)
+    want_t, want_r = T.release(table, ref, lens, new_len, page)
+    assert np.array_equal(l_out.cpu().numpy(), new_len) and np.array_equal(t_out.cpu().numpy(), want_t)
+    assert np.array_equal(r_out.cpu().numpy(), want_r) and np.array_equal(positions.cpu().numpy(), want_pos)
+    for got, w in zip(planes, want):
+        assert torch.equal(got, w)
+    r_out.fill_(77)
+    qb.qsa_accept_drafts(*args, t_out, l_out, r_out, [], ws)               # no planes, no positions
+    assert np.array_equal(r_out.cpu().numpy(), want_r)
+
+
+@pytest.mark.parametrize("what", ["length", "long", "drafts", "offset", "parent", "accepted"])
+def test_accept_leaves_rows_out_of_range_as_they_are(cuda_lib, what):
+    page, lens, off, parents, last = 4, [10, 12, 9], [0, 4, 8, 12], [[-1, 0, 1, 2]] * 3, [1, 3, 2]
+    table, ref = private_pool(lens, page, 1)
+    held = [10, 12, 9]
+    parents = [list(p) for p in parents]
+    if what == "length":
+        held[1] = -1
+    elif what == "long":
+        held[1] = 10 ** 6
+    elif what == "drafts":
+        held[1] = 3
+    elif what == "offset":
+        off = [0, 4, 8, 99]
+    elif what == "parent":
+        parents[1][2] = 2
+    else:
+        last[1] = 4
+    bad = 2 if what == "offset" else 1
+    planes = token_planes(len(ref), page, 1)
+    cut = [T.accept(n, [-1, 0, 1, 2], a) if r != bad else (held[r], []) for r, (n, a) in enumerate(zip(lens, last))]
+    want = [moved(p, table, {r: c[1] for r, c in enumerate(cut)}, page) for p in planes]
+    t_out, l_out, r_out = filled(3, table.shape[1]), filled(3), filled(len(ref))
+    ws = qb.keep_workspace(3)
+    qb.qsa_accept_drafts(page, ints(off), ints(sum(parents, [])), ints(last), ints(table.tolist()), ints(held),
+                         ints(ref.tolist()), t_out, l_out, r_out, planes, ws)
+    assert status(ws) == (qb.QSA_ERR_DEVICE_BOUNDS, bad)
+    fine = [r for r in range(3) if r != bad]
+    new_len = [c[0] for c in cut]
+    assert l_out.tolist() == new_len
+    want_t, want_r = T.release(table[fine], ref, [lens[r] for r in fine], [new_len[r] for r in fine], page)
+    assert np.array_equal(t_out.cpu().numpy()[fine], want_t) and np.array_equal(t_out[bad].cpu().numpy(), table[bad])
+    assert np.array_equal(r_out.cpu().numpy(), want_r)
+    for got, w in zip(planes, want):
+        assert torch.equal(got, w)
+
+
+# ------------------------------------------------------------------------------------------ evicting
+def run_evict(page, budget, first, recent, weights, positions, table, lens, ref, planes, ws=None):
+    S, places = weights.shape
+    w_out, p_out = torch.full_like(weights, 77.0), torch.full_like(positions, 77)
+    t_out, l_out, r_out = filled(*table.shape), filled(S), filled(len(ref))
+    ws = qb.keep_workspace(S, places) if ws is None else ws
+    qb.qsa_evict_tokens(page, ints(budget), first, recent, weights, positions, ints(table.tolist()), ints(list(lens)),
+                        ints(ref.tolist()), w_out, p_out, t_out, l_out, r_out, planes, ws)
+    return w_out, p_out, t_out, l_out, r_out, ws
+
+
+def check_evict(page, budget, first, recent, weights, positions, table, lens, ref, planes, result, before):
+    w_out, p_out, t_out, l_out, r_out, ws = result
+    w, p = weights.cpu().numpy(), positions.cpu().numpy()
+    new_len, moves = [], {}
+    want_w, want_p = np.zeros_like(w), np.full_like(p, -1)
+    for r, n in enumerate(lens):
+        shared = [ref[table[r, j // page]] > 1 for j in range(n)]
+        keep, moves[r] = T.evict(w[r, :n], p[r, :n], shared, budget[r], first, recent)
+        new_len.append(keep)
+        want_w[r, :keep], want_p[r, :keep] = w[r, :keep], p[r, :keep]
+        for to, at in moves[r]:
+            want_w[r, to], want_p[r, to] = w[r, at], p[r, at]
+    want_t, want_r = T.release(table, ref, lens, new_len, page)
+    assert l_out.tolist() == new_len
+    assert np.array_equal(t_out.cpu().numpy(), want_t) and np.array_equal(r_out.cpu().numpy(), want_r)
+    assert np.array_equal(p_out.cpu().numpy(), want_p)
+    assert np.array_equal(w_out.cpu().numpy().view(np.int32), want_w.view(np.int32))      # NaN and all
+    for got, old in zip(planes, before):
+        assert torch.equal(got, moved(old, table, moves, page))
+    assert status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("lens,budget,first,recent,page,shared", [
+    ([10], 4, 0, 0, 4, 0), ([10], 0, 0, 0, 4, 0), ([1, 0, 2, 30, 31, 33], 16, 2, 5, 4, 2), ([500, 20, 700], 100, 4, 32, 16, 0),
+    ([500, 20, 700], 100, 4, 200, 16, 0), ([9000, 5000, 100], 1000, 16, 100, 64, 3), ([64] * 300, 60, 1, 8, 8, 0),
+    ([3000], 2999, 0, 1, 1, 0), ([40000], 20000, 64, 512, 24, 0)])
+@pytest.mark.parametrize("kind", ["spread", "ties", "zeros", "odd"])
+def test_evict(cuda_lib, lens, budget, first, recent, page, shared, kind):
+    rng = np.random.default_rng(len(lens) + page)
+    table, ref = private_pool(lens, page, 2, shared=shared)
+    places = table.shape[1] * page
+    S = len(lens)
+    w = {"spread": np.exp(2 * rng.standard_normal((S, places))), "ties": rng.integers(0, 3, (S, places)) * 0.5,
+         "zeros": np.zeros((S, places)), "odd": rng.standard_normal((S, places))}[kind].astype(np.float32)
+    if kind == "odd":                                     # NaN, infinities, both zeros, subnormals
+        w.flat[::7], w.flat[1::11], w.flat[2::13] = np.nan, np.inf, -0.0
+        w.flat[3::17], w.flat[4::19], w.flat[5::23] = 0.0, -np.inf, 1e-41
+    pos = np.stack([rng.permutation(3 * places)[:places] for _ in range(S)])
+    weights, positions = torch.from_numpy(w).to(DEV), ints(pos.tolist())
+    planes = token_planes(len(ref), page, 3)
+    before = [p.clone() for p in planes]
+    budgets = [budget] * S
+    if S > 2:
+        budgets[1] = -1                                   # any number of tokens
+    result = run_evict(page, budgets, first, recent, weights, positions, table, lens, ref, planes)
+    check_evict(page, budgets, first, recent, weights, positions, table, lens, ref, planes, result, before)
+
+
+def test_evict_rows_out_of_range_are_left(cuda_lib):
+    page, lens = 4, [30, 20, 25]
+    table, ref = private_pool(lens, page, 2)
+    places = table.shape[1] * page
+    g = torch.Generator().manual_seed(1)
+    weights, positions = torch.rand(3, places, generator=g).to(DEV), ints(np.arange(3 * places).reshape(3, -1).tolist())
+    for bad in (-1, places + 1, 2 ** 31 - 1):
+        planes = token_planes(len(ref), page, 3)
+        before = [p.clone() for p in planes]
+        w_out, p_out, t_out, l_out, r_out, ws = run_evict(page, [8] * 3, 1, 2, weights, positions, table, [30, bad, 25], ref, planes)
+        assert status(ws) == (qb.QSA_ERR_DEVICE_BOUNDS, 1) and l_out.tolist() == [8, bad, 8]
+        assert torch.equal(w_out[1], weights[1]) and torch.equal(p_out[1], positions[1])
+        assert np.array_equal(t_out[1].cpu().numpy(), table[1])
+        mine = table[1][table[1] >= 0].tolist()
+        assert all(torch.equal(a[:, mine], b[:, mine]) for a, b in zip(planes, before))
+        assert bool((r_out[mine] == 1).all())
+
+
+def test_evict_leaves_out_and_records_bad_pages(cuda_lib):
+    """A page out of range: its tokens' contents do not move, and nothing outside the pool is touched."""
+    page, lens = 4, [30]
+    table, ref = private_pool(lens, page, 2)
+    places = table.shape[1] * page
+    weights = torch.arange(places, device=DEV, dtype=torch.float32)[None].contiguous()
+    positions = ints([list(range(places))])
+    broken = table.copy()
+    broken[0, 1], broken[0, 6] = -1, 2 ** 30
+    planes = token_planes(len(ref), page, 3)
+    w_out, p_out, t_out, l_out, r_out, ws = run_evict(page, [10], 0, 0, weights, positions, broken, lens, ref, planes)
+    assert status(ws)[0] == qb.QSA_ERR_DEVICE_BOUNDS and l_out.tolist() == [10]
+    assert sorted(p_out[0, :10].tolist()) == list(range(20, 30))
+
+
+# ------------------------------------------------------------------------------------------ together
+@pytest.mark.parametrize("fp8", [False, True])
+def test_speculative_steps_equal_plain_decoding(cuda_lib, fp8):
+    """Rows that draft trees and accept a path hold, after every step, the K and V bytes of rows that appended the accepted
+    tokens one by one; their attention agrees, as does the freed pages' bookkeeping."""
+    Hq, Hkv, D, page, S, layers = 8, 2, 128, 8, 3, 2
+    rope = qb.rope_table(D, base=1e5)
+    make = dict(n_layers=layers, n_pages=60, page_size=page, n_rows=S, max_pages=12, n_q_heads=Hq, n_kv_heads=Hkv, head_dim=D,
+                fp8=fp8)
+    spec, plain = PagedCache(**make, max_draft=16), PagedCache(**make)
+    prompt = [13, 1, 30]
+    x = randn((layers, sum(prompt), Hq + 2 * Hkv, D), 1)
+    seq, pos = ints(sum(([r] * n for r, n in enumerate(prompt)), [])), ints(sum((list(range(n)) for n in prompt), []))
+    for cache in (spec, plain):
+        cache.fork(ints([-1] * S), ints(prompt))
+        for layer in range(layers):
+            cache.append(layer, rope, None, x[layer, :, Hq:Hq + Hkv], x[layer, :, Hq + Hkv:], pos, seq)
+    rng = np.random.default_rng(0)
+    lens = list(prompt)
+    for step in range(6):
+        counts = [int(c) for c in rng.integers(1, 12, S)]
+        if step == 3:
+            counts[1] = 0
+        parents = [random_parents(rng, c) for c in counts]
+        last = [int(rng.integers(-1, c)) if c else -1 for c in counts]
+        off = np.concatenate([[0], np.cumsum(counts)]).tolist()
+        n = off[-1]
+        depth = [len(line) for p in parents for line in T.lines(p)]
+        seq = sum(([r] * c for r, c in enumerate(counts)), [])
+        place = [lens[r] + i for r, c in enumerate(counts) for i in range(c)]
+        where = [lens[r] + d - 1 for r, d in zip(seq, depth)]
+        x = randn((layers, n, Hq + 2 * Hkv, D), 10 + step)
+        parent = ints(sum(parents, []))
+        spec.extend(ints(counts))
+        outs = []
+        for layer in range(layers):
+            q = torch.empty(n, Hq, D, dtype=torch.bfloat16, device=DEV)
+            spec.append(layer, rope, x[layer, :, :Hq], x[layer, :, Hq:Hq + Hkv], x[layer, :, Hq + Hkv:], ints(where), ints(seq), q,
+                        place=ints(place))
+            out, lse = torch.empty_like(q), torch.empty(n, Hq, device=DEV)
+            spec.attend_tree(layer, q, ints(off), parent, out, lse)
+            outs.append((q, out, lse))
+        spec.accept(ints(off), parent, ints(last))
+        # the accepted tokens one by one
+        paths = [[off[r] + i for i in T.lines(p)[a]] if a >= 0 else [] for r, (p, a) in enumerate(zip(parents, last))]
+        for k in range(max(map(len, paths))):
+            rows = [r for r in range(S) if k < len(paths[r])]
+            plain.extend(ints([int(k < len(p)) for p in paths]))
+            pick = [paths[r][k] for r in rows]
+            for layer in range(layers):
+                y = x[layer, pick]
+                q = torch.zeros(S, Hq, D, dtype=torch.bfloat16, device=DEV)
+                turned = torch.empty(len(rows), Hq, D, dtype=torch.bfloat16, device=DEV)
+                plain.append(layer, rope, y[:, :Hq].contiguous(), y[:, Hq:Hq + Hkv].contiguous(), y[:, Hq + Hkv:].contiguous(),
+                             ints([lens[r] + k for r in rows]), ints(rows), turned)
+                q[rows] = turned
+                out, lse = torch.empty(S, Hq, D, dtype=torch.bfloat16, device=DEV), torch.empty(S, Hq, device=DEV)
+                plain.attend(layer, q, out, lse)
+                tq, tout, tlse = outs[layer]
+                assert torch.equal(turned, tq[pick])
+                # |V| is below 5: both operators' roundings
+                assert bool(((out[rows] - tout[pick]).abs().float() <= 2.0 ** -7 * out[rows].abs().float() + 2.0 ** -8 * 5).all())
+                assert bool(((lse[rows] - tlse[pick]).abs() <= 1e-4).all())
+        lens = [n_ + len(p) for n_, p in zip(lens, paths)]
+        assert spec.seq_len.tolist() == lens == plain.seq_len.tolist()
+        assert int((spec.ref > 0).sum()) == sum(-(-n_ // page) for n_ in lens) == int((plain.ref > 0).sum())
+        for r in range(S):
+            for a, b in zip(spec.planes, plain.planes):
+                u, w = (c.table[r].cpu().numpy() for c in (spec, plain))
+                s1, s2 = P.slots_of(u, lens[r], page), P.slots_of(w, lens[r], page)
+                assert torch.equal(a.flatten(1, 2)[:, s1], b.flatten(1, 2)[:, s2])
+    assert spec.status() == ((0, 0), (0, 0)) and spec.more_status() == ((0, 0), (0, 0))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_decode_loop_under_a_budget(cuda_lib, fp8):
+    """Decoding with eviction every few steps, beams forked in between: rows hold the bytes and positions that a host model
+    of the policy says, and the attention is that over exactly those tokens."""
+    Hq, Hkv, D, page, S = 8, 2, 128, 4, 4
+    rope = qb.rope_table(D, base=1e5)
+    cache = PagedCache(1, 80, page, S, 20, Hq, Hkv, D, fp8=fp8, evictable=True, max_draft=4)
+    n0 = 30
+    x = randn((S, n0, Hq + 2 * Hkv, D), 1)
+    cache.fork(ints([-1] * S), ints([n0] * S))
+    flat = x.flatten(0, 1)
+    cache.append(0, rope, None, flat[:, Hq:Hq + Hkv], flat[:, Hq + Hkv:], ints(list(range(n0)) * S),
+                 ints(sum(([r] * n0 for r in range(S)), [])), place=ints(list(range(n0)) * S))
+    where = [n0] * S                                      # the next position of each row
+    rows = [list(range(n0)) for _ in range(S)]            # positions at each place
+    weights = [np.zeros(n0) for _ in range(S)]
+    rng = np.random.default_rng(1)
+    for step in range(12):
+        cache.extend()
+        y = randn((S, Hq + 2 * Hkv, D), 50 + step)
+        q = torch.empty(S, Hq, D, dtype=torch.bfloat16, device=DEV)
+        cache.append(0, rope, y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], ints(where), None, q, place=ints([len(r) for r in rows]))
+        out, lse = torch.empty(S, Hq, D, dtype=torch.bfloat16, device=DEV), torch.empty(S, Hq, device=DEV)
+        cache.attend(0, q, out, lse, weigh=True)
+        table = cache.table.cpu().numpy()
+        for r in range(S):
+            rows[r].append(where[r])
+            weights[r] = np.append(weights[r], 0.0)
+            where[r] += 1
+        if fp8:
+            values = [f64(c.view(torch.float8_e4m3fn).float())[0] * np.repeat(f64(s)[0], 128, -1)
+                      for c, s in (cache.planes[:2], cache.planes[2:])]
+        else:
+            values = [f64(p)[0] for p in cache.planes]
+        check_decode(out, lse, q, values, table, [len(r) for r in rows], page, 0, D ** -0.5, fp8)
+        got = cache.weights.cpu().numpy()
+        for r in range(S):
+            K = values[0].reshape(-1, Hkv, D)[P.slots_of(table[r], len(rows[r]), page)]
+            weights[r] += T.token_weights(f64(q[r]), K, 0, D ** -0.5)
+            assert np.allclose(got[r, :len(rows[r])], weights[r], rtol=1e-4, atol=0) and not got[r, len(rows[r]):].any()
+            assert cache.positions[r, :len(rows[r])].tolist() == rows[r]
+        if step % 3 == 2:
+            shared = [[bool(v) for v in (cache.ref[cache.table[r].long().clamp(min=0)] > 1).repeat_interleave(page)[:len(rows[r])]]
+                      for r in range(S)]
+            held = cache.weights.cpu().numpy()
+            cache.evict(ints([24] * S), 2, 6)
+            for r in range(S):
+                keep, moves = T.evict(held[r, :len(rows[r])], rows[r], shared[r], 24, 2, 6)
+                for to, at in moves:
+                    rows[r][to], weights[r][to] = rows[r][at], weights[r][at]
+                rows[r], weights[r] = rows[r][:keep], weights[r][:keep]
+            assert cache.seq_len.tolist() == [len(r) for r in rows]
+            assert [cache.positions[r, :len(rows[r])].tolist() for r in range(S)] == rows
+        if step in (4, 7):                                # a beam step: two rows continue row 1
+            parent = [1, 1, 2, 3] if step == 4 else [0, 3, 2, 3]
+            cache.fork(ints(parent), ints([0] * S))
+            rows, weights = [list(rows[p]) for p in parent], [weights[p].copy() for p in parent]
+            where = [where[p] for p in parent]
+            cache.compact()
+    assert cache.status() == ((0, 0), (0, 0)) and cache.more_status() == ((0, 0),) * 3
+
+
+def test_captured_speculative_steps_replay(cuda_lib):
+    """Two steps (drafts, attention, acceptance) in one graph, replayed: the lengths grow by the accepted tokens each time."""
+    Hq, Hkv, D, page, S = 8, 2, 128, 8, 2
+    rope = qb.rope_table(D)
+    cache = PagedCache(1, 64, page, S, 24, Hq, Hkv, D, max_draft=4)
+    cache.fork(ints([-1] * S), ints([5, 9]))
+    x = randn((8, Hq + 2 * Hkv, D), 3)
+    off, parent, last, count = ints([0, 4, 8]), ints([-1, 0, 0, 2, -1, 0, 1, -1]), ints([3, 2]), ints([4, 4])
+    step, depth, seq = ints([0, 1, 2, 3] * 2), ints([0, 1, 1, 2, 0, 1, 2, 0]), ints([0] * 4 + [1] * 4)
+    q = torch.empty(8, Hq, D, dtype=torch.bfloat16, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(8, Hq, device=DEV)
+
+    def steps():
+        for _ in range(2):
+            base = cache.seq_len[seq.long()]
+            cache.extend(count)
+            cache.append(0, rope, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], base + depth, seq, q, place=base + step)
+            cache.attend_tree(0, q, off, parent, out, lse)
+            cache.accept(off, parent, last)
+
+    steps()                                               # before the capture
+    cache.extend(ints([0, 0]))                            # and an even number of changes again
+    cache.extend(ints([0, 0]))
+    assert cache.seq_len.tolist() == [11, 15]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        steps()
+    for i in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert cache.seq_len.tolist() == [17 + 6 * i, 21 + 6 * i]
+    assert int((cache.ref > 0).sum()) == 4 + 5 and cache.status() == ((0, 0), (0, 0)) and cache.more_status() == ((0, 0),) * 2
