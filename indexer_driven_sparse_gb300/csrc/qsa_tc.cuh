@@ -25,6 +25,11 @@ bool encode_tmap_bf16_2d(CUtensorMap *m, const void *base, uint64_t inner, uint6
 bool encode_tmap_f32_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows, uint64_t row_bytes,
                         uint32_t box_inner, uint32_t box_rows);
 
+// Rows of `blocks` blocks of 128 bytes (64 bf16 values, or 128 bytes of codes), row_bytes apart, as a 3-D map (byte in the
+// block, row, block) with 128B swizzle; boxes of box_rows rows of box_blocks blocks land block by block.
+bool encode_tmap_rows(CUtensorMap *m, const void *base, bool bytes, uint64_t rows, uint64_t blocks, uint64_t row_bytes,
+                      uint32_t box_rows, uint32_t box_blocks);
+
 __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
            ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);

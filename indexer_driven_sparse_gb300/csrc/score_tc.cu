@@ -333,12 +333,11 @@ __global__ void __launch_bounds__(kStThreads, 1)
 // ----------------------------------------------------------------------------- host side
 
 // 2-D tensor maps (rows of `inner` elements, `row_bytes` apart), 128B swizzle
-static bool encode_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
-                           uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows) {
-    using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                       const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                       CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                       CUtensorMapFloatOOBfill);
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiledFn encode_tiled() {
     static const EncodeTiledFn fn = []() -> EncodeTiledFn {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q{};
@@ -348,6 +347,12 @@ static bool encode_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *b
             return nullptr;
         return reinterpret_cast<EncodeTiledFn>(p);
     }();
+    return fn;
+}
+
+static bool encode_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
+                           uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows) {
+    const EncodeTiledFn fn = encode_tiled();
     if (fn == nullptr || rows == 0) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
@@ -355,6 +360,20 @@ static bool encode_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *b
     const cuuint32_t estr[2] = {1, 1};
     return fn(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tmap_rows(CUtensorMap *m, const void *base, bool bytes, uint64_t rows, uint64_t blocks, uint64_t row_bytes,
+                      uint32_t box_rows, uint32_t box_blocks) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr || rows == 0) return false;
+    const cuuint32_t inner = bytes ? 128 : 64;
+    const cuuint64_t dims[3] = {inner, (cuuint64_t)rows, (cuuint64_t)blocks};
+    const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, 128};
+    const cuuint32_t box[3] = {inner, box_rows, box_blocks};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

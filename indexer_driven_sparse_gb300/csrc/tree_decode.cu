@@ -1,5 +1,39 @@
-// Attention of a tree of drafted tokens over a paged K/V cache (qsa_tree_decode, qsa_tree_decode_fp8kv).
-#include "paged.cuh"
+// Attention of a tree of drafted tokens over a paged K/V cache (qsa_tree_decode, qsa_tree_decode_fp8kv):
+//   out[i] = sum_j softmax_j(scale q[i] . K[j]) V[j] over the cached tokens before the drafts, i's ancestors and i.
+//
+// A sequence's T drafted tokens times the G query heads of a KV head are T G rows that share every K and V row: 4 T G flops
+// per value read, 16 tokens with 8 heads each are the 128 rows of one tcgen05 tile. One such tile needs 2,050 cycles of the tensor
+// core for 128 tokens of 256 dims (two products of 128 x 128 x 256) and their 128 KB take an SM's share of HBM 5,600: up to two
+// tiles the rows' stream bounds the call, from three on the products.
+//
+// Split: as in the decode of one token (paged_decode.cuh), the batch's tokens, cut into tiles of one sequence each, form one list,
+// dealt to R ranges of equal length; CTA (range, KV head, M tile) walks its part. The M tiles of a range are neighbouring
+// CTAs that read the same rows at the same time: from L2, all but one of them. A sequence that a range boundary cuts
+// leaves partials (m, l, O), joined by tree_join_kernel; all others are written at once.
+//
+// Roles of a CTA (one per SM), which meet at mbarriers only:
+//   4 softmax warps   a row each thread: running maximum and sum in base 2, O rescaled only when the maximum has grown by
+//                     more than 2^8; weights go back to tensor memory over the scores they came from;
+//   1 MMA warp        S = Q K^T (M 128, N the tile's tokens) into one of two buffers, O += P V with P from tensor memory; the next
+//                     tile's S is issued before this tile's O;
+//   1 index warp      page table -> slots, a tile ahead; with pages of whole runs of 16 tokens it also issues the tiled TMA loads
+//                     (a box is a run of a page), whose cost per 16 KB is nothing beside 1,024 copies of 16 bytes;
+//   2 query warps     the rows' queries, the ancestors' bits, and the clean-up of V rows that not every row attends;
+//   8 worker warps    other page sizes: cp.async of 16 bytes, row by row. FP8 rows: codes -> f16 operands.
+// K and V lie in shared memory as slots of 16 KB in 128-byte swizzle (K: 64 dims of the tile's tokens; V: 16 KB of whole rows),
+// a ring in the order in which the products take them: K0 K1 V0 K2 V1 ...
+//
+// A masked token's weight is zero, but zero times an infinite or undefined V value is not: V rows that no row attends (behind the
+// sequence's end, before its window) become zeros, and values that are not finite in rows that only some attend (drafts, the
+// window's edge) are taken out of the product and added at the end to the rows that attend them.
+//
+// bf16 rows: weights enter the second product as bf16 (2^-8 of each; the decode of one token adds a second bf16 value, which
+// here would make half as many products again). FP8 rows: codes are exact in f16, q enters as f16 scaled by a power of two
+// per row, K's scales multiply the fp32 sums of each 128 dims, V's enter the weights: w = 2^(s + log2 v_scale - m + 8) with m the
+// lazy maximum of s + log2 v_scale, below 2^15, one set for each 128 dims, rounded to f16 (2^-11 of each, 2^-33 of the largest below
+// the normal range).
+#include "paged_decode.cuh"
+#include "qsa_tc.cuh"
 
 #include <algorithm>
 
@@ -7,117 +41,1245 @@ namespace qsa {
 
 namespace {
 
-constexpr int kTreeThreads = 128;
+constexpr int kRows = 128;                       // MMA M: rows of a CTA
+constexpr int kSlot = 16384;                     // bytes of a ring slot
+constexpr int kMetas = 4;                        // tiles whose slots and scales are known
+constexpr uint32_t kTmemS = 0, kTmemO = 256;     // two S buffers of 128 columns, then O
+constexpr float kLazy = 8.f;                     // O is rescaled when a maximum has grown by more than 2^8
 
-// A warp for each (drafted token, query head).
-template <int D, bool F8>
-__global__ void __launch_bounds__(kTreeThreads) tree_kernel(TreeArgs a) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * (kTreeThreads / 32) + (threadIdx.x >> 5);
+template <int D_, bool F8_>
+struct TreeCfg {
+    static constexpr int D = D_;
+    static constexpr bool F8 = F8_;
+    static constexpr int T = F8 ? 64 : 128;                  // tokens of a tile
+    static constexpr int SL = F8 ? D / 128 : D / 64;         // slots of a tile's K, and of its V
+    static constexpr int VT = F8 ? 64 : 128 * 64 / D;        // tokens of a V slot
+    static constexpr int SG = F8 ? D / 128 : 1;              // scales of a row, sets of weights
+    static constexpr int q_bytes = kRows * D * 2;
+    static constexpr int ring = F8 ? 4 : D == 256 ? 9 : D == 128 ? 11 : 12;
+    static constexpr int codes = F8 ? (D == 256 ? 10 : 12) : 0;      // slots of codes, 8 KB each
+    static constexpr int softmax = 128, q_threads = 64, workers = 256;
+    static constexpr int mma_warp = 4, index_warp = 5, q_warp = 6, work_warp = 8;
+    static constexpr int threads = softmax + 64 + q_threads + workers;
+    static constexpr int ring_at = q_bytes, codes_at = ring_at + ring * kSlot, smem = codes_at + codes * kSlot / 2 + 1024;
+    static_assert(smem + 8192 <= 227 * 1024, "shared memory of a CTA");
+    static constexpr float raise = F8 ? 8.f : 0.f;
+};
+
+struct TreeMaps {
+    CUtensorMap k, v;
+};
+
+// How rows get into shared memory: runs of `k_run` (K) and `v_run` (V) tokens by tiled TMA, or (k_run 0) by the worker warps.
+struct TreePlan {
+    int32_t ranges, m_tiles, k_run, v_run;
+    int32_t page_shift;
+    int32_t min_tiles;       // of a range
+};
+
+struct TreeScratch {
+    int2 *meta;              // [ranges] (row, parts)
+    float2 *ml;              // [2 ranges][Hkv m_tiles][128]
+    float *o;                // [..][D]
+};
+
+struct TreeRow {
+    int len, off, T, base, lo, t0, t1;    // tokens; drafts [off, off + T) in places [base, len); first attended place; tiles
+    bool named;                           // its offsets are fine
+};
+
+// high: the largest offset of an earlier sequence (0 at first).
+template <int Tt>
+__device__ __forceinline__ TreeRow tree_row(const TreeArgs &a, int s, int &high) {
+    TreeRow r;
+    r.off = a.draft_off[s];
+    const int end = a.draft_off[s + 1];
+    r.named = r.off >= high && end >= r.off && end <= a.N;
+    high = max(high, r.off);
+    r.T = r.named ? end - r.off : 0;
+    r.len = a.seq_len[s];
+    r.t0 = r.t1 = 0;
+    if (r.T > 0 && r.T <= a.max_draft && r.len >= r.T && r.len <= a.ld * a.page_size) {
+        r.base = r.len - r.T;
+        r.lo = a.window > 0 ? max(0, r.base + 1 - a.window) : 0;
+        r.t0 = r.lo / Tt;
+        r.t1 = r.len / Tt + (r.len % Tt != 0);
+    }
+    return r;
+}
+
+struct Seg {
+    TreeRow r;
+    int s, ta, tb;           // tiles [ta, tb) of sequence s
+    int i0;                  // tiles of this CTA before them
+    bool begins, ends;       // with the sequence
+};
+
+// The tiles [x, x1) of the list as segments of one sequence each; sequences without a row in this M tile are passed over.
+template <int Tt>
+struct Walk {
+    long long x, x1;
+    int s, skip, high, i = 0;
+    __device__ __forceinline__ bool next(const TreeArgs &a, int m_tile, Seg &g) {
+        while (x < x1) {
+            g.r = tree_row<Tt>(a, s, high);
+            const int n = g.r.t1 - g.r.t0;
+            if (n == 0) {
+                ++s;
+                continue;
+            }
+            g.s = s++;
+            g.ta = g.r.t0 + skip;
+            g.tb = (int)min((long long)g.r.t1, g.ta + (x1 - x));
+            g.begins = skip == 0;
+            g.ends = g.tb == g.r.t1;
+            x += g.tb - g.ta;
+            skip = 0;
+            if (m_tile * kRows >= g.r.T * a.G) continue;
+            g.i0 = i;
+            i += g.tb - g.ta;
+            return true;
+        }
+        return false;
+    }
+};
+
+// The order of a segment's n tiles in the ring, in slots of one tile's K or V: K0 K1 V0 K2 V1 ... V(n-1).
+__device__ __forceinline__ int k_turn(int c) { return c == 0 ? 0 : 2 * c - 1; }
+__device__ __forceinline__ int v_turn(int c, int n) { return c == n - 1 ? 2 * n - 1 : 2 * c + 2; }
+
+// Whether some row may not attend some token of tile t.
+template <int Tt>
+__device__ __forceinline__ bool masked(const TreeArgs &a, const TreeRow &r, int t) {
+    const int j0 = t * Tt;
+    return j0 > r.base - Tt || (a.window > 0 && j0 < r.base + r.T - a.window);
+}
+
+template <typename C>
+struct TreeShared {
+    uint64_t full[C::ring], empty[C::ring];
+    uint64_t c_full[C::F8 ? C::codes : 1], c_empty[C::F8 ? C::codes : 1];
+    uint64_t s_full[2], p_full[2], pv_done[2], meta_full[kMetas], meta_empty[kMetas];
+    uint64_t to_clean, clean, q_full, q_free, nodes_full, nodes_free, flags_full, o_free;
+    uint32_t kin[QSA_MAX_DRAFT][QSA_MAX_DRAFT / 32];      // of each drafted token: itself and its ancestors inside the window
+    int lo[QSA_MAX_DRAFT];                                // its first attended place
+    uint32_t odd[2][QSA_MAX_DRAFT / 32];                  // tokens with values that are not finite: drafts, places from r.lo
+    float q_scale[2][C::F8 ? kRows : 1];               // of every other segment
+    int slots[kMetas][C::T];
+    uint32_t real[kMetas][C::T / 32];                     // bit: the token's page exists
+    float4 scales[kMetas][C::F8 ? C::T : 1];              // K scales of 128 dims each, log2 of V scales
+    uint32_t tmem;
+    volatile int abort;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// kind::f16 with f16 operands (tc_idesc is bf16's)
+__host__ __device__ constexpr uint32_t f16_idesc(int N, int b_mn) {
+    return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+
+// Which of the eight bf16 values of v are not finite: all of them as zeros, and whether there was one.
+__device__ __forceinline__ bool drop_odd(uint4 &v) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+    bool some = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u, some = true;
+        if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu, some = true;
+    }
+    return some;
+}
+
+// Codes 0x7F and 0xFF of four E4M3 codes as zeros, and whether there was one.
+__device__ __forceinline__ bool drop_nan_codes(uint32_t &w) {
+    const uint32_t nan = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    w &= ~nan;
+    return nan != 0;
+}
+
+template <typename C>
+__global__ void __launch_bounds__(C::threads, 1)
+    tree_tile_kernel(TreeArgs a, TreePlan plan, TreeScratch ws, const __grid_constant__ TreeMaps maps) {
+    constexpr int D = C::D, T = C::T, SL = C::SL, RING = C::ring, SG = C::SG;
+    constexpr bool F8 = C::F8;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ TreeShared<C> sh;
+    __shared__ long long scan[C::threads / 32];
+    __shared__ int start[3];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t q_at = smem_u32(sm), ring_at = q_at + C::ring_at, codes_at = q_at + C::codes_at;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int m_tile = blockIdx.x % plan.m_tiles, kvh = blockIdx.x / plan.m_tiles % a.Hkv, range = blockIdx.x / plan.m_tiles / a.Hkv;
+    const bool speaks = kvh == 0 && m_tile == 0;          // records errors that all CTAs of a range see
+    const bool tiled = plan.k_run > 0;
+
+    if (warp == C::mma_warp) tmem_alloc(&sh.tmem, 512);
+    if (tid == 0) {
+        // the loads' arrivals: one with the bytes it expects, or every worker's
+        const int load = tiled ? 1 : C::workers;
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), F8 ? C::workers : load);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        if (F8)
+            for (int i = 0; i < C::codes; ++i) {
+                mbar_init(smem_u32(&sh.c_full[i]), load);
+                mbar_init(smem_u32(&sh.c_empty[i]), C::workers / 32);
+            }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.s_full[i]), 1);
+            mbar_init(smem_u32(&sh.p_full[i]), C::softmax);
+            mbar_init(smem_u32(&sh.pv_done[i]), 1);
+        }
+        for (int i = 0; i < kMetas; ++i) {
+            mbar_init(smem_u32(&sh.meta_full[i]), 1);
+            mbar_init(smem_u32(&sh.meta_empty[i]), C::softmax / 32 + (tiled ? 0 : C::workers / 32));
+        }
+        mbar_init(smem_u32(&sh.to_clean), 1);
+        mbar_init(smem_u32(&sh.clean), C::q_threads);
+        mbar_init(smem_u32(&sh.q_full), C::q_threads);
+        mbar_init(smem_u32(&sh.q_free), 1);
+        mbar_init(smem_u32(&sh.nodes_full), C::q_threads);
+        mbar_init(smem_u32(&sh.nodes_free), C::softmax);
+        mbar_init(smem_u32(&sh.flags_full), C::q_threads);
+        mbar_init(smem_u32(&sh.o_free), C::softmax);
+        fence_mbar_init();
+        sh.abort = 0;
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
+    }
     wait_for_previous();
-    const int i = (int)(item / a.Hq), h = (int)(item % a.Hq);
-    if (i >= a.N) return;
-    int s = -1, off = 0, T = 0, high = 0;            // high: the largest offset so far
-    for (int b0 = 0; b0 < a.B && (s < 0 || item == 0); b0 += 32) {
-        const int b = b0 + lane;
-        const int lo = b < a.B ? a.draft_off[b] : 0, hi = b < a.B ? a.draft_off[b + 1] : 0;
-        int top = max(high, lo);
-        for (int o = 1; o < 32; o <<= 1) top = max(top, __shfl_up_sync(0xffffffffu, top, o));
-        const bool fine = b < a.B && lo == top && hi >= lo && hi <= a.N;
-        if (b < a.B && !fine && item == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereTree, b);
-        const uint32_t in = __ballot_sync(0xffffffffu, fine && lo <= i && i < hi);
-        if (in) {
-            const int l = __ffs(in) - 1;
-            s = b0 + l;
-            off = __shfl_sync(0xffffffffu, lo, l);
-            T = __shfl_sync(0xffffffffu, hi, l) - off;
+
+    // ---- this range's part of the list: tiles before each thread's run of sequences, then the place of the first tile.
+    // Sequences that cannot be attended get their zeros here.
+    Walk<T> walk;
+    {
+        const int per = (a.B + C::threads - 1) / C::threads, s_lo = min(a.B, tid * per), s_hi = min(a.B, s_lo + per);
+        int top = 0;                                      // the largest offset of the run
+        for (int s = s_lo; s < s_hi; ++s) top = max(top, a.draft_off[s]);
+        int upto_top = top;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto_top, o);
+            if (lane >= o) upto_top = max(upto_top, v);
         }
-        high = __shfl_sync(0xffffffffu, top, 31);
-    }
-    if (s < 0) return;
-    uint16_t *out = a.out + ((int64_t)i * a.Hq + h) * D;
-    const int n = a.seq_len[s];
-    const bool ok = T <= a.max_draft && n >= T && n <= a.ld * a.page_size;
-    if (!ok && lane == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereTree, s);
-    const int base = ok ? n - T : 0;
-    uint32_t kin[4] = {0u, 0u, 0u, 0u};
-    int depth = 0;
-    if (ok)
-        for (int j = i - off; j >= 0;) {
-            ++depth;
-            for (int w = 0; w < 4; ++w)
-                if (j / 32 == w) kin[w] |= 1u << (j % 32);
-            const int p = a.parent[off + j];
-            if (p < -1 || p >= j) {
-                if (lane == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereTree, s);
-                break;
+        if (lane == 31) scan[warp] = upto_top;
+        int high = __shfl_up_sync(0xffffffffu, upto_top, 1);
+        if (lane == 0) high = 0;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) high = max(high, (int)scan[w]);
+        const int high0 = high;
+        long long mine = 0;
+        for (int s = s_lo; s < s_hi; ++s) {
+            const TreeRow r = tree_row<T>(a, s, high);
+            mine += r.t1 - r.t0;
+            if (r.t1 > r.t0 || (r.named && r.T == 0)) continue;
+            if (!speaks || s % plan.ranges != range) continue;
+            record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereTree, s);
+            for (int64_t i = (int64_t)r.off * a.Hq; r.named && i < (int64_t)(r.off + r.T) * a.Hq; ++i) {
+                for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(a.out + i * D + d) = make_uint4(0, 0, 0, 0);
+                if (a.lse) a.lse[i] = -INFINITY;
             }
-            j = p;
         }
-    const int own = base + depth - 1, lo = a.window > 0 ? max(0, own - a.window + 1) : 0;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
-    const int kvh = h / a.G;
-    for (int e = 0; e < E; ++e) {
-        q[e] = bf16_bits_to_float(a.q[i * a.q_ld + h * D + lane * E + e]) * a.scale_log2;
-        o[e] = 0.f;
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = upto;
+        __syncthreads();
+        long long total = 0;
+#pragma unroll 1
+        for (int w = 0; w < C::threads / 32; ++w) {
+            if (w < warp) upto += scan[w];
+            total += scan[w];
+        }
+        const Ranges cut(total, (int)max(1ll, min((long long)plan.ranges, total / plan.min_tiles)));
+        walk.x = walk.x1 = 0;
+        if (range < cut.R) walk.x = cut.begin(range), walk.x1 = cut.begin(range + 1);
+        if (walk.x < walk.x1 && upto - mine <= walk.x && walk.x < upto) {
+            long long before = upto - mine;
+            int at = high0;
+            for (int s = s_lo;; ++s) {
+                const int was = at;
+                const TreeRow r = tree_row<T>(a, s, at);
+                if (walk.x < before + r.t1 - r.t0) {
+                    start[0] = s, start[1] = (int)(walk.x - before), start[2] = was;
+                    break;
+                }
+                before += r.t1 - r.t0;
+            }
+        }
+        if (speaks && tid == 0) ws.meta[range] = make_int2(-1, 0);
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        walk.s = start[0], walk.skip = start[1], walk.high = start[2];
+        if (walk.x >= walk.x1) walk.s = walk.skip = walk.high = 0;
+
+        // the sequence that this range starts and leaves unfinished: how many ranges it spans
+        if (speaks && tid == 0 && walk.x < walk.x1) {
+            Walk<T> w = walk;
+            Seg g;
+            while (w.next(a, 0, g))
+                if (g.begins && !g.ends) {
+                    const long long last = w.x - 1 + (g.r.t1 - g.tb);      // the list's number of its last tile
+                    ws.meta[range] = make_int2(g.s, cut.of(last) - range + 1);
+                }
+        }
     }
-    int passed = 0;                                  // ancestors met
-    for (int j = min(lo, base); j < (ok ? n : 0); ++j) {
-        if (j >= base) {
-            const int t = j - base;
-            if (!(kin[t / 32] >> (t % 32) & 1u)) continue;
-            ++passed;
-            if (a.window > 0 && base + passed - 1 <= own - a.window) continue;
-        } else if (j < lo) {
-            continue;
+    const uint32_t tmem = sh.tmem;
+
+    auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+        if (mbar_wait_bounded(smem_u32(bar), phase & 1u, kWaitLimitNs)) return true;
+        record_error(a.hdr, QSA_ERR_DEVICE_TIMEOUT, kWhereTree, blockIdx.x);
+        sh.abort = 1;
+        return false;
+    };
+    // a warp's wait: it goes on only if all its lanes saw the phase and no role has given up
+    auto wait_warp = [&](uint64_t *bar, uint32_t phase) -> bool {
+        const bool w = wait(bar, phase);
+        return __all_sync(0xffffffffu, w) && !__any_sync(0xffffffffu, sh.abort != 0);
+    };
+
+    Seg g{};
+    if (warp == C::index_warp) {
+        // ================================================================ slots of each tile; TMA loads
+        constexpr int E = T / 32;                         // tokens of a lane, neighbours
+        const int rows_end = (int)min((int64_t)INT32_MAX, a.n_pages * a.page_size);       // a row that does not exist: zeros
+        int page[E], offset[E];
+        bool ok = true;
+        auto fetch = [&](int t) {                         // the page table's entries for tile t of g
+            const int pages_end = (g.r.len - 1) / a.page_size, pages_begin = g.r.lo / a.page_size;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const uint32_t j = (uint32_t)t * T + lane * E + e;      // may pass 2^31
+                const uint32_t entry = plan.page_shift >= 0 ? j >> plan.page_shift : j / (uint32_t)a.page_size;
+                offset[e] = (int)(j - entry * a.page_size);
+                const bool some = entry >= (uint32_t)pages_begin && entry <= (uint32_t)pages_end;
+                page[e] = some ? a.table[g.s * a.ld + entry] : -2;
+            }
+        };
+        int asked = 0;                                    // ring slots asked for
+        int slot_k[E], slot_v[E];                         // slots of the tile whose K, and whose V, comes next
+        auto load_k = [&](int q0) -> bool {               // ring slots q0 ... of one tile's K
+            for (int k = 0; k < SL; ++k) {
+                const int q = q0 + k, at = q % (F8 ? C::codes : RING), turn = q / (F8 ? C::codes : RING);
+                uint64_t *full = F8 ? &sh.c_full[at] : &sh.full[at], *empty = F8 ? &sh.c_empty[at] : &sh.empty[at];
+                if (turn > 0 && !wait_warp(empty, turn - 1)) return false;
+                asked = q + 1;
+                const uint32_t dst = F8 ? codes_at + at * (kSlot / 2) : ring_at + at * kSlot;
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(full), F8 ? kSlot / 2 : kSlot);
+                __syncwarp();
+                const int first = lane * plan.k_run;      // token of this lane's box
+                int y = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int v = __shfl_sync(0xffffffffu, slot_k[e], first / E & 31);
+                    if (first % E == e) y = v;
+                }
+                if (first < T)
+                    tma_load_3d(dst + first * 128, &maps.k, 0, y < 0 ? rows_end : y, kvh * (F8 ? D / 128 : D / 64) + k, smem_u32(full));
+            }
+            return true;
+        };
+        auto load_v = [&](int q0) -> bool {
+            for (int k = 0; k < SL; ++k) {
+                const int q = q0 + k, at = q % (F8 ? C::codes : RING), turn = q / (F8 ? C::codes : RING);
+                uint64_t *full = F8 ? &sh.c_full[at] : &sh.full[at], *empty = F8 ? &sh.c_empty[at] : &sh.empty[at];
+                if (turn > 0 && !wait_warp(empty, turn - 1)) return false;
+                asked = q + 1;
+                const uint32_t dst = F8 ? codes_at + at * (kSlot / 2) : ring_at + at * kSlot;
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(full), F8 ? kSlot / 2 : kSlot);
+                __syncwarp();
+                const int boxes = C::VT / plan.v_run;     // of whole rows: one, or (64 dims each) several
+                const int run = lane % boxes, block = lane / boxes;
+                const int first = (F8 ? 0 : k * C::VT) + run * plan.v_run;
+                int y = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int v = __shfl_sync(0xffffffffu, slot_v[e], first / E & 31);
+                    if (first % E == e) y = v;
+                }
+                y = y < 0 ? rows_end : y;
+                if (F8) {
+                    if (block == 0) tma_load_3d(dst + run * plan.v_run * 128, &maps.v, 0, y, kvh * (D / 128) + k, smem_u32(full));
+                } else if (boxes == 1) {
+                    if (lane == 0) tma_load_3d(dst, &maps.v, 0, y, kvh * (D / 64), smem_u32(full));
+                } else if (block < D / 64) {
+                    tma_load_3d(dst + block * (C::VT * 128) + run * plan.v_run * 128, &maps.v, 0, y, kvh * (D / 64) + block, smem_u32(full));
+                }
+            }
+            return true;
+        };
+        Walk<T> w = walk;
+        int done = 0;
+        bool more = w.next(a, m_tile, g);
+        if (more) fetch(g.ta);
+        while (more && ok) {
+            const Seg now = g;
+            const int n = now.tb - now.ta, turn0 = 2 * now.i0;
+            for (int c = 0; c < n && ok; ++c, ++done) {
+                int slot[E];
+                float4 scale[F8 ? E : 1];
+                bool exists[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int j = (now.ta + c) * T + lane * E + e;
+                    const bool in = (uint32_t)j >= (uint32_t)now.r.lo && (uint32_t)j < (uint32_t)now.r.len;
+                    const bool fine = (uint32_t)page[e] < (uint32_t)a.n_pages;
+                    if (in && !fine && speaks) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereTree, now.s);
+                    slot[e] = fine ? page[e] * a.page_size + offset[e] : -1;
+                    exists[e] = in && fine;
+                    if (F8) {
+                        scale[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (exists[e]) {
+                            const int64_t at = ((int64_t)slot[e] * a.Hkv + kvh) * SG;
+                            if (SG == 2) {
+                                const float2 x = *reinterpret_cast<const float2 *>(a.k_scales + at);
+                                const float2 y = *reinterpret_cast<const float2 *>(a.v_scales + at);
+                                scale[e] = make_float4(x.x, x.y, y.x, y.y);
+                            } else {
+                                scale[e] = make_float4(a.k_scales[at], 0.f, a.v_scales[at], 0.f);
+                            }
+                        }
+                    }
+                }
+                // the next tile's entries, on their way meanwhile
+                const int t = now.ta + c;
+                if (c + 1 < n) {
+                    fetch(t + 1);
+                } else {
+                    more = w.next(a, m_tile, g);
+                    if (more) fetch(g.ta);
+                }
+                const int m = done % kMetas;
+                if (done >= kMetas && !wait_warp(&sh.meta_empty[m], done / kMetas - 1)) {
+                    ok = false;
+                    break;
+                }
+                uint32_t bits = 0;                        // tokens lane E + e as bit (lane E + e) % 32 of word (lane E) / 32
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    bits |= (exists[e] ? 1u : 0u) << ((lane * E + e) & 31);
+                    if (!tiled) sh.slots[m][lane * E + e] = exists[e] ? slot[e] : -1;
+                    if (F8) {
+                        // infinite V scales become NaN: as a maximum they would take every other token's weight to zero
+                        const float4 x = scale[e];
+                        sh.scales[m][lane * E + e] = make_float4(x.x, x.y, fmaf(x.z, 0.f, lg2(x.z)), fmaf(x.w, 0.f, lg2(x.w)));
+                    }
+                }
+#pragma unroll
+                for (int o = 1; o < 32 / E; o <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+                if (lane % (32 / E) == 0) sh.real[m][lane * E / 32] = bits;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.meta_full[m]));
+                if (tiled) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) slot_k[e] = slot[e];
+                    ok = load_k((turn0 + k_turn(c)) * SL);
+                    if (ok && c > 0) ok = load_v((turn0 + v_turn(c - 1, n)) * SL);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) slot_v[e] = slot[e];
+                    if (ok && c + 1 == n) ok = load_v((turn0 + v_turn(c, n)) * SL);
+                }
+            }
         }
-        const int page = a.table[s * a.ld + j / a.page_size];
-        if ((uint32_t)page >= (uint32_t)a.n_pages) {
-            if (lane == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereTree, s);
-            continue;
+        // no load may still be writing shared memory when the CTA ends (bounded waits; they are over unless a role gave up)
+        constexpr int R = F8 ? C::codes : RING;
+        for (int q = max(0, asked - R); q < asked; ++q)
+            mbar_wait_bounded(smem_u32(F8 ? &sh.c_full[F8 ? q % R : 0] : &sh.full[q % RING]), (uint32_t)(q / R) & 1u, kWaitLimitNs);
+    } else if (warp >= C::work_warp) {
+        // ================================================================ workers: cp.async loads; codes -> f16
+        const int wt = tid - C::work_warp * 32;
+        Walk<T> w = walk;
+        bool ok = true;
+        if (!F8) {
+            const uint16_t *rows[2] = {static_cast<const uint16_t *>(a.k) + kvh * D, static_cast<const uint16_t *>(a.v) + kvh * D};
+            const int64_t pitch = (int64_t)a.Hkv * D;
+            auto copy = [&](int is_v, int tile, int q0) -> bool {      // a tile's K or V into ring slots q0 ...
+                const int m = tile % kMetas;
+                if (!is_v && !wait_warp(&sh.meta_full[m], tile / kMetas)) return false;
+                for (int k = 0; k < SL; ++k) {
+                    const int q = q0 + k, at = q % RING, turn = q / RING;
+                    if (turn > 0 && !wait_warp(&sh.empty[at], turn - 1)) return false;
+                    const uint32_t dst = ring_at + at * kSlot;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int id = i * C::workers + wt;
+                        const int tok = is_v ? id / (D / 8) : id / 8, gr = is_v ? id % (D / 8) : id % 8;
+                        const int sl = sh.slots[m][is_v ? k * C::VT + tok : tok];
+                        const uint32_t to = dst + (is_v ? gr / 8 * (C::VT * 128) : 0) + swz(tok, gr & 7);
+                        cp_async16_zfill(to, rows[is_v] + max(sl, 0) * pitch + (is_v ? 0 : k * 64) + gr * 8, sl >= 0);
+                    }
+                    cp_async_arrive(smem_u32(&sh.full[at]));
+                }
+                if (is_v) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.meta_empty[m]));
+                }
+                return true;
+            };
+            while (!tiled && ok && w.next(a, m_tile, g)) {
+                const int n = g.tb - g.ta, turn0 = 2 * g.i0;
+                for (int c = 0; c < n && ok; ++c) {
+                    ok = copy(0, g.i0 + c, (turn0 + k_turn(c)) * SL);
+                    if (ok && c > 0) ok = copy(1, g.i0 + c - 1, (turn0 + v_turn(c - 1, n)) * SL);
+                    if (ok && c + 1 == n) ok = copy(1, g.i0 + c, (turn0 + v_turn(c, n)) * SL);
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if constexpr (F8) {
+            // slots in turn: q = 0, 1, ...; codes of slot q + codes - 1 are asked for before slot q is converted
+            constexpr int NC = C::codes;
+            const uint8_t *rows[2] = {static_cast<const uint8_t *>(a.k) + kvh * D, static_cast<const uint8_t *>(a.v) + kvh * D};
+            const int64_t pitch = (int64_t)a.Hkv * D;
+            auto copy = [&](int is_v, int tile, int q0) -> bool {
+                const int m = tile % kMetas;
+                if (!is_v && !wait_warp(&sh.meta_full[m], tile / kMetas)) return false;
+                for (int k = 0; k < SL; ++k) {
+                    const int q = q0 + k, at = q % NC, turn = q / NC;
+                    if (turn > 0 && !wait_warp(&sh.c_empty[at], turn - 1)) return false;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int id = i * C::workers + wt, tok = id / 8, gr = id % 8;
+                        const int sl = sh.slots[m][tok];
+                        cp_async16_zfill(codes_at + at * (kSlot / 2) + swz(tok, gr), rows[is_v] + max(sl, 0) * pitch + k * 128 + gr * 16,
+                                         sl >= 0);
+                    }
+                    cp_async_arrive(smem_u32(&sh.c_full[at]));
+                }
+                if (is_v) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.meta_empty[m]));
+                }
+                return true;
+            };
+            // lo, len, base, edge: of the tile's sequence (V only); tokens at or behind len and before lo become zeros, NaN codes of those
+            // that not every row attends too
+            auto convert = [&](int q0, bool is_v, int j0, const TreeRow &r, bool some) -> bool {
+                const int edge = a.window > 0 ? r.base + r.T - a.window : 0;
+                for (int k = 0; k < SL; ++k) {
+                    const int q = q0 + k, from = q % NC, to = q % RING;
+                    if (!wait_warp(&sh.c_full[from], q / NC)) return false;
+                    if (q >= RING && !wait_warp(&sh.empty[to], q / RING - 1)) return false;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int id = i * C::workers + wt, tok = id / 8, gr = id % 8;
+                        uint4 v = *reinterpret_cast<const uint4 *>(sm + C::codes_at + from * (kSlot / 2) + swz(tok, gr));
+                        if (is_v && some) {
+                            const int j = j0 + tok;
+                            if ((uint32_t)j >= (uint32_t)r.len || j < r.lo)
+                                v = make_uint4(0, 0, 0, 0);
+                            else if (j >= r.base || j < edge)
+                                drop_nan_codes(v.x), drop_nan_codes(v.y), drop_nan_codes(v.z), drop_nan_codes(v.w);
+                        }
+                        uint8_t *dst = sm + C::ring_at + to * kSlot + (gr >> 2) * (T * 128);
+                        const int at = (gr & 3) * 2;
+                        *reinterpret_cast<uint4 *>(dst + swz(tok, at)) =
+                            make_uint4(e4m3_to_f16x2(v.x, 0), e4m3_to_f16x2(v.x, 1), e4m3_to_f16x2(v.y, 0), e4m3_to_f16x2(v.y, 1));
+                        *reinterpret_cast<uint4 *>(dst + swz(tok, at + 1)) =
+                            make_uint4(e4m3_to_f16x2(v.z, 0), e4m3_to_f16x2(v.z, 1), e4m3_to_f16x2(v.w, 0), e4m3_to_f16x2(v.w, 1));
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(smem_u32(&sh.full[to]));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.c_empty[from]));
+                }
+                return true;
+            };
+            // without TMA the copies run `ahead` turns (of a tile's K or V) before the conversion, on a walk of their own
+            // (at most 6: a tile's K is asked for when the softmax has left the tile four before it, which needs the V turns up to
+            // seven before this one converted)
+            constexpr int ahead = NC / SL - 1 < 6 ? NC / SL - 1 : 6;
+            Walk<T> wc = walk;
+            Seg gc;
+            int cc = 0, nc = 0, asked = 0;                // copies: turn within the segment's 2 n, and turns in all
+            bool more = !tiled && wc.next(a, m_tile, gc);
+            if (more) nc = 2 * (gc.tb - gc.ta);
+            auto ask = [&]() -> bool {                    // the copies' next turn
+                if (!more) return true;
+                const int n = nc / 2, c = cc;
+                // turn -> (K or V, tile): 0: K0; 2i - 1: Ki; 2i + 2: Vi; 2n - 1: V(n-1)
+                const bool is_v = c == nc - 1 || (c > 0 && (c & 1) == 0);
+                const int tile = c == 0 ? 0 : c == nc - 1 ? n - 1 : is_v ? c / 2 - 1 : (c + 1) / 2;
+                if (!copy(is_v, gc.i0 + tile, (2 * gc.i0 + c) * SL)) return false;
+                ++asked;
+                if (++cc == nc) {
+                    more = wc.next(a, m_tile, gc);
+                    cc = 0;
+                    nc = more ? 2 * (gc.tb - gc.ta) : 0;
+                }
+                return true;
+            };
+            for (int i = 0; i < ahead && ok; ++i) ok = ask();
+            while (ok && w.next(a, m_tile, g)) {
+                const int n = g.tb - g.ta;
+                for (int c = 0; c < 2 * n && ok; ++c) {
+                    const bool is_v = c == 2 * n - 1 || (c > 0 && (c & 1) == 0);
+                    const int tile = c == 0 ? 0 : c == 2 * n - 1 ? n - 1 : is_v ? c / 2 - 1 : (c + 1) / 2;
+                    ok = ask();
+                    if (ok) ok = convert((2 * g.i0 + c) * SL, is_v, (g.ta + tile) * T, g.r, masked<T>(a, g.r, g.ta + tile));
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
-        const int64_t row = ((int64_t)page * a.page_size + j % a.page_size) * a.Hkv + kvh;
-        float k[E], v[E];
-        for (int e = 0; e < E; ++e) {
-            const int64_t at = row * D + lane * E + e;
-            if (F8) {
-                const int g = (lane * E + e) / 128;
-                const uint32_t c = static_cast<const uint8_t *>(a.k)[at] | static_cast<const uint8_t *>(a.v)[at] << 8;
-                uint32_t f;
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"((uint16_t)c));
-                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&f));
-                k[e] = x.x * a.k_scales[row * (D / 128) + g];
-                v[e] = x.y * a.v_scales[row * (D / 128) + g];
+    } else if (warp >= C::q_warp && warp < C::work_warp) {
+        // ================================================================ queries, ancestors, clean V rows
+        const int qt = tid - C::q_warp * 32;
+        Walk<T> w = walk;
+        bool ok = true;
+        int seg = 0, cleaned = 0;
+        while (ok && w.next(a, m_tile, g)) {
+            const int n = g.tb - g.ta, rows = g.r.T * a.G - m_tile * kRows;     // this CTA's rows (maybe more than 128)
+            if (seg > 0 && !wait_warp(&sh.q_free, seg - 1)) break;
+            auto row_at = [&](int r) -> const uint16_t * {
+                const int node = (m_tile * kRows + r) / a.G, h = (m_tile * kRows + r) % a.G;
+                return a.q + (int64_t)(g.r.off + node) * a.q_ld + (kvh * a.G + h) * D;
+            };
+            if (!F8) {
+                for (int i = qt; i < kRows * (D / 8); i += C::q_threads) {
+                    const int r = i / (D / 8), gr = i % (D / 8);
+                    const uint32_t dst = q_at + gr / 8 * (kRows * 128) + swz(r, gr & 7);
+                    cp_async16_zfill(dst, r < rows ? row_at(r) + gr * 8 : a.q, r < rows);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
             } else {
-                k[e] = bf16_bits_to_float(static_cast<const uint16_t *>(a.k)[at]);
-                v[e] = bf16_bits_to_float(static_cast<const uint16_t *>(a.v)[at]);
+                // D / 8 lanes have a row, 8 values each
+                constexpr int each = C::q_threads / (D / 8);
+#pragma unroll 4
+                for (int i = 0; i < kRows / each; ++i) {
+                    const int r = i * each + qt / (D / 8), gr = qt % (D / 8);
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (r < rows) v = *reinterpret_cast<const uint4 *>(row_at(r) + gr * 8);
+                    float f[8], top = 0.f;
+                    unpack8(v, f);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
+#pragma unroll
+                    for (int o = D / 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                    const uint32_t dst = q_at + gr / 8 * (kRows * 128) + swz(r, gr & 7);
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(f16x2(f[0] * down, f[1] * down)),
+                                 "r"(f16x2(f[2] * down, f[3] * down)), "r"(f16x2(f[4] * down, f[5] * down)),
+                                 "r"(f16x2(f[6] * down, f[7] * down))
+                                 : "memory");
+                    if (gr == 0) sh.q_scale[seg & 1][r] = __uint_as_float((uint32_t)(127 + e) << 23);
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(&sh.q_full));
+            // ---- the drafted tokens' ancestors, once the last segment's are no longer needed
+            if (seg > 0 && !wait_warp(&sh.nodes_free, seg - 1)) break;
+            for (int i = qt; i < g.r.T; i += C::q_threads) {
+                uint32_t kin[4] = {0u, 0u, 0u, 0u};
+                int depth = 0;
+                for (int j = i; j >= 0;) {                // parents lie below their children, so this ends
+                    if (a.window == 0 || depth < a.window)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (j >> 5 == x) kin[x] |= 1u << (j & 31);
+                    ++depth;
+                    int p = a.parent[g.r.off + j];
+                    if (p < -1 || p >= j) {
+                        if (speaks) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereTree, g.s);
+                        p = -1;
+                    }
+                    j = p;
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sh.kin[i][x] = kin[x];
+                sh.lo[i] = a.window > 0 ? max(0, g.r.base + depth - a.window) : 0;
+            }
+            if (qt < 8) sh.odd[qt >> 2][qt & 3] = 0u;
+            mbar_arrive(smem_u32(&sh.nodes_full));
+            asm volatile("bar.sync 2, %0;" ::"n"(C::q_threads) : "memory");        // the flags are cleared
+            // ---- V rows that not every row attends
+            const int edge = a.window > 0 ? g.r.base + g.r.T - a.window : 0;       // places below it: not for all
+            auto flag = [&](int j) {
+                const int x = j >= g.r.base ? j - g.r.base : j - g.r.lo, set = j >= g.r.base ? 0 : 1;
+                if (x < QSA_MAX_DRAFT) atomicOr(&sh.odd[set][x >> 5], 1u << (x & 31));
+            };
+            for (int c = 0; c < n && ok; ++c) {
+                const int t = g.ta + c;
+                if (!masked<T>(a, g.r, t)) continue;
+                if (!F8) {
+                    // the MMA warp says when the rows are in: it meets every turn of the ring, and a wait tells only two from each other
+                    if (!wait_warp(&sh.to_clean, cleaned)) {
+                        ok = false;
+                        break;
+                    }
+                    for (int k = 0; k < SL; ++k) {
+                        const int at = ((2 * g.i0 + v_turn(c, n)) * SL + k) % RING;
+                        for (int i = qt; i < C::VT * (D / 8); i += C::q_threads) {
+                            const int tok = i / (D / 8), gr = i % (D / 8), j = t * T + k * C::VT + tok;
+                            const bool out = (uint32_t)j >= (uint32_t)g.r.len || j < g.r.lo;
+                            if (!out && j < g.r.base && j >= edge) continue;
+                            uint4 *p = reinterpret_cast<uint4 *>(sm + C::ring_at + at * kSlot + gr / 8 * (C::VT * 128) + swz(tok, gr & 7));
+                            if (out) {
+                                *p = make_uint4(0, 0, 0, 0);
+                            } else {
+                                uint4 v = *p;
+                                if (drop_odd(v)) {
+                                    *p = v;
+                                    flag(j);
+                                }
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(smem_u32(&sh.clean));
+                    ++cleaned;
+                } else {
+                    // the workers clean; the tokens to add at the end are found in the cache
+                    for (int i = qt; i < T * (D / 16); i += C::q_threads) {
+                        const int tok = i / (D / 16), gr = i % (D / 16), j = t * T + tok;
+                        if ((uint32_t)j >= (uint32_t)g.r.len || j < g.r.lo || (j < g.r.base && j >= edge)) continue;
+                        const int pg = a.table[g.s * a.ld + j / a.page_size];
+                        if ((uint32_t)pg >= (uint32_t)a.n_pages) continue;
+                        const int64_t row = ((int64_t)pg * a.page_size + j % a.page_size) * a.Hkv + kvh;
+                        uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.v) + row * D + gr * 16);
+                        if (drop_nan_codes(v.x) | drop_nan_codes(v.y) | drop_nan_codes(v.z) | drop_nan_codes(v.w)) flag(j);
+                    }
+                }
+            }
+            if (!ok) break;
+            mbar_arrive(smem_u32(&sh.flags_full));
+            ++seg;
+        }
+    } else if (warp == C::mma_warp) {
+        // ================================================================ products
+        if (lane == 0) {
+            Walk<T> w = walk;
+            uint64_t *last_bar = nullptr;                 // the barrier of the last commit, and its phase
+            uint32_t last_phase = 0;
+            int seg = 0, cleaned = 0;
+            bool ok = true;
+            auto scores = [&](int i, int q0, bool first, bool last) -> bool {
+                const uint32_t s_at = tmem + kTmemS + (i & 1) * 128;
+                if (first && !wait(&sh.q_full, seg)) return false;
+                for (int k = 0; k < SL; ++k) {
+                    const int q = q0 + k, at = q % RING;
+                    if (!wait(&sh.full[at], q / RING)) return false;
+                    fence_proxy_async_smem();
+                    tc_fence_after();
+                    const uint32_t b = ring_at + at * kSlot;
+                    if (!F8) {
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            tc_mma(s_at, tc_desc(q_at + k * (kRows * 128) + z * 32, 16, 1024), tc_desc(b + z * 32, 16, 1024),
+                                   tc_idesc(kRows, T, 0), k > 0 || z > 0);
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < 8; ++z)
+                            tc_mma(s_at + k * T, tc_desc(q_at + (2 * k + z / 4) * (kRows * 128) + (z & 3) * 32, 16, 1024),
+                                   tc_desc(b + z / 4 * (T * 128) + (z & 3) * 32, 16, 1024), f16_idesc(T, 0), z > 0);
+                    }
+                    tc_commit(smem_u32(&sh.empty[at]));
+                }
+                tc_commit(smem_u32(&sh.s_full[i & 1]));
+                last_bar = &sh.s_full[i & 1], last_phase = i >> 1;
+                if (last) tc_commit(smem_u32(&sh.q_free));
+                return true;
+            };
+            while (ok && w.next(a, m_tile, g)) {
+                const int n = g.tb - g.ta, turn0 = 2 * g.i0;
+                ok = scores(g.i0, turn0 * SL, true, n == 1);
+                for (int c = 0; c < n && ok; ++c) {
+                    const int i = g.i0 + c;
+                    if (c + 1 < n && !scores(i + 1, (turn0 + k_turn(c + 1)) * SL, false, c + 2 == n)) {
+                        ok = false;
+                        break;
+                    }
+                    // ---- O (+)= P V
+                    const int q0 = (turn0 + v_turn(c, n)) * SL;
+                    const bool part = !F8 && masked<T>(a, g.r, g.ta + c);
+                    if (part) {
+                        for (int k = 0; k < SL && ok; ++k) ok = wait(&sh.full[(q0 + k) % RING], (q0 + k) / RING);
+                        mbar_arrive(smem_u32(&sh.to_clean));
+                    }
+                    if (!ok || !wait(&sh.p_full[i & 1], i >> 1) || (c == 0 && seg > 0 && !wait(&sh.o_free, seg - 1))) {
+                        ok = false;
+                        break;
+                    }
+                    if (part && !wait(&sh.clean, cleaned++)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t p_at = tmem + kTmemS + (i & 1) * 128;
+                    for (int k = 0; k < SL; ++k) {
+                        const int q = q0 + k, at = q % RING;
+                        if (!wait(&sh.full[at], q / RING)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_proxy_async_smem();
+                        tc_fence_after();
+                        const uint32_t b = ring_at + at * kSlot;
+                        if (!F8) {
+#pragma unroll
+                            for (int z = 0; z < C::VT / 16; ++z)
+                                tc_mma_ta(tmem + kTmemO, p_at + (k * C::VT / 16 + z) * 8, tc_desc(b + z * 2048, C::VT * 128, 1024),
+                                          tc_idesc(kRows, D, 1), c > 0 || k > 0 || z > 0);
+                        } else {
+#pragma unroll
+                            for (int z = 0; z < T / 16; ++z)
+                                tc_mma_ta(tmem + kTmemO + k * 128, p_at + k * (T / 2) + z * 8, tc_desc(b + z * 2048, T * 128, 1024),
+                                          f16_idesc(128, 1), c > 0 || z > 0);
+                        }
+                        tc_commit(smem_u32(&sh.empty[at]));
+                    }
+                    if (!ok) break;
+                    tc_commit(smem_u32(&sh.pv_done[i & 1]));
+                    last_bar = &sh.pv_done[i & 1], last_phase = i >> 1;
+                }
+                ++seg;
+            }
+            // the last commit covers every product issued: wait for it before tensor memory is freed
+            if (last_bar != nullptr) mbar_wait_bounded(smem_u32(last_bar), last_phase & 1u, kWaitLimitNs);
+        }
+    } else {
+        // ================================================================ softmax
+        const uint32_t t_row = tmem + ((uint32_t)(32 * warp) << 16), t_o = t_row + kTmemO;
+        const int row = tid;
+        Walk<T> w = walk;
+        int seg = 0;
+        bool ok = true;
+        for (; ok && w.next(a, m_tile, g); ++seg) {
+            const int n = g.tb - g.ta;
+            const int node = (m_tile * kRows + row) / a.G, head = kvh * a.G + (m_tile * kRows + row) % a.G;
+            const bool valid = node < g.r.T, some = __any_sync(0xffffffffu, valid);
+            if (!wait_warp(&sh.nodes_full, seg)) break;
+            const int lo = sh.lo[min(node, g.r.T - 1)];
+            const float scale = F8 ? a.scale_log2 * sh.q_scale[seg & 1][F8 ? row : 0] : a.scale_log2;
+            float ref[SG], l = 0.f;                       // the lazy maxima, and the weights' sum relative to the first
+#pragma unroll
+            for (int x = 0; x < SG; ++x) ref[x] = -INFINITY;
+            for (int c = 0; c < n; ++c) {
+                const int i = g.i0 + c, t = g.ta + c, m = i % kMetas;
+                if (!wait_warp(&sh.meta_full[m], i / kMetas)) {
+                    ok = false;
+                    break;
+                }
+                // which of the tile's tokens this row attends
+                constexpr int W = T / 32;
+                uint32_t see[W];
+                const bool part = masked<T>(a, g.r, t);
+#pragma unroll
+                for (int x = 0; x < W; ++x) {
+                    see[x] = sh.real[m][x];
+                    if (part) {
+                        const int j = t * T + 32 * x, from = lo - j, to = g.r.base - j;
+                        uint32_t v = to >= 32 ? ~0u : to > 0 ? (1u << to) - 1u : 0u;
+                        if (from >= 32)
+                            v = 0u;
+                        else if (from > 0)
+                            v &= ~0u << from;
+                        const int o = -to;                // place of bit 0 among the drafts
+                        if (o > -32 && o < QSA_MAX_DRAFT && valid) {
+                            if (o < 0) {
+                                v |= sh.kin[node][0] << -o;
+                            } else {
+                                v |= sh.kin[node][o >> 5] >> (o & 31);
+                                if ((o & 31) && (o >> 5) < QSA_MAX_DRAFT / 32 - 1) v |= sh.kin[node][(o >> 5) + 1] << (32 - (o & 31));
+                            }
+                        }
+                        see[x] &= v;
+                    }
+                }
+                uint32_t both = ~0u;
+#pragma unroll
+                for (int x = 0; x < W; ++x) both &= see[x];
+                const bool all = __all_sync(0xffffffffu, both == ~0u || !valid);       // no token to mask in this warp
+                if (!wait_warp(&sh.s_full[i & 1], i >> 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t_s = t_row + kTmemS + (i & 1) * 128;
+                float f[SG];
+#pragma unroll
+                for (int x = 0; x < SG; ++x) f[x] = 1.f;
+                if (!F8) {
+                    if (some) {
+                        float mx[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            float v[32];
+                            tmem_ld32(t_s + h * 32, v);
+                            if (all) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) mx[k & 7] = fmaxf(mx[k & 7], v[k]);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) mx[k & 7] = fmaxf(mx[k & 7], (see[F8 ? 0 : h] >> k) & 1u ? v[k] : -INFINITY);
+                            }
+                        }
+                        const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                                fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * scale;
+                        if (top > ref[0] + kLazy) {
+                            if (ref[0] != -INFINITY) f[0] = ex2(ref[0] - top);
+                            ref[0] = top;
+                        }
+                        const float at = ref[0] == -INFINITY ? 0.f : ref[0];
+                        l *= f[0];
+                        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t pk[32];
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                float v[32];
+                                tmem_ld32(t_s + (2 * h + y) * 32, v);
+                                const uint32_t sw = see[F8 ? 0 : 2 * h + y];
+#pragma unroll
+                                for (int k = 0; k < 32; k += 2) {
+                                    float e0 = ex2(fmaf(v[k], scale, -at)), e1 = ex2(fmaf(v[k + 1], scale, -at));
+                                    if (!all) {
+                                        e0 = (sw >> k) & 1u ? e0 : 0.f;
+                                        e1 = (sw >> (k + 1)) & 1u ? e1 : 0.f;
+                                    }
+                                    ps[(k >> 1) & 3] += e0 + e1;
+                                    pk[y * 16 + k / 2] = bf16x2(e0, e1);
+                                }
+                            }
+                            tmem_st32(t_s + h * 32, pk);          // over scores that have been read
+                        }
+                        l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                    }
+                } else if (some) {
+                    float v[64];
+                    const float4 *sc = sh.scales[m];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float u[32];
+                        tmem_ld32(t_s + h * 32, u);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[h * 32 + k] = u[k] * sc[F8 ? h * 32 + k : 0].x;
+                    }
+                    if (SG == 2)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float u[32];
+                            tmem_ld32(t_s + 64 + h * 32, u);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[h * 32 + k] = fmaf(u[k], sc[F8 ? h * 32 + k : 0].y, v[h * 32 + k]);
+                        }
+                    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) {
+                        v[k] *= scale;
+                        if (!all) v[k] = (see[k >> 5] >> (k & 31)) & 1u ? v[k] : -INFINITY;
+                        // a V scale below 2^-100, or that is not a number, counts as 2^-100 here: the maximum is finite whenever a score is
+                        top[0] = fmaxf(top[0], v[k] + fmaxf(sc[F8 ? k : 0].z, -100.f));
+                        if (SG == 2) top[1] = fmaxf(top[1], v[k] + fmaxf(sc[F8 ? k : 0].w, -100.f));
+                    }
+                    float at[2];
+#pragma unroll
+                    for (int x = 0; x < SG; ++x) {
+                        if (top[x] > ref[x] + (15.f - C::raise)) {
+                            if (ref[x] != -INFINITY) f[x] = ex2(ref[x] - top[x]);
+                            ref[x] = top[x];
+                        }
+                        at[x] = (ref[x] == -INFINITY ? 0.f : ref[x]) - C::raise;
+                    }
+                    l *= f[0];
+                    float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int x = 0; x < SG; ++x) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int k = 0; k < 64; k += 2) {
+                            float e[2];
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const float u = v[k + y] - at[x], lv = x == 0 ? sc[F8 ? k + y : 0].z : sc[F8 ? k + y : 0].w;
+                                if (x == 0) ps[(k >> 1) & 3] += ex2(u);
+                                e[y] = ex2(u + lv);
+                                if (!all) e[y] = v[k + y] == -INFINITY ? 0.f : e[y];       // whatever its scale is
+                            }
+                            pk[k / 2] = f16x2(e[0], e[1]);
+                        }
+                        tmem_st32(t_s + x * 32, pk);
+                    }
+                    l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) * 0x1p-8f;
+                    static_assert(!F8 || C::raise == 8.f, "the sum is relative to the maximum");
+                }
+                bool grew = false;
+#pragma unroll
+                for (int x = 0; x < SG; ++x) grew |= f[x] != 1.f;
+                if (c > 0 && __any_sync(0xffffffffu, grew)) {          // O follows, once the product before it is done
+                    if (!wait_warp(&sh.pv_done[(i - 1) & 1], (i - 1) >> 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        float v[32];
+                        const float by = f[SG == 2 ? c0 / 128 : 0];
+                        tmem_ld32(t_o + c0, v);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] *= by;
+                        tmem_st32(t_o + c0, v);
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.p_full[i & 1]));
+                if (lane == 0) mbar_arrive(smem_u32(&sh.meta_empty[m]));
+            }
+            if (!ok) break;
+            // ---- the segment's end: out, or a partial
+            const int i = g.i0 + n - 1;
+            if (!wait_warp(&sh.pv_done[i & 1], i >> 1) || !wait_warp(&sh.flags_full, seg)) break;
+            tc_fence_after();
+            const bool whole = g.begins && g.ends;
+            const float lse2 = l == 0.f ? -INFINITY : ref[0] + log2f(l);
+            float by[SG];
+#pragma unroll
+            for (int x = 0; x < SG; ++x)
+                by[x] = l == 0.f ? 0.f : F8 ? ex2(ref[x] - C::raise - lse2) : whole ? 1.f / l : 1.f;
+            // values that are not finite, of attended tokens that not every row attends
+            uint32_t odd[2][4];
+            bool strange = false;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                odd[0][x] = valid ? sh.odd[0][x] & sh.kin[min(node, QSA_MAX_DRAFT - 1)][x] : 0u;
+                odd[1][x] = valid ? sh.odd[1][x] : 0u;
+                strange |= (odd[0][x] | odd[1][x]) != 0u;
+            }
+            const int64_t at = (int64_t)(2 * range + (g.begins ? 1 : 0)) * a.Hkv * plan.m_tiles + kvh * plan.m_tiles + m_tile;
+            float *po = ws.o + (at * kRows + row) * D;
+            uint16_t *dst = a.out + ((int64_t)(g.r.off + min(node, g.r.T - 1)) * a.Hq + head) * D;
+            if (some) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    float v[32];
+                    __syncwarp();
+                    tmem_ld32(t_o + c0, v);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : v[k] * by[SG == 2 ? c0 / 128 : 0];
+                    if (strange) {
+#pragma unroll 1
+                        for (int x = 0; x < 2 * QSA_MAX_DRAFT; ++x) {
+                            const int y = x & (QSA_MAX_DRAFT - 1), j = (x == y ? g.r.base : g.r.lo) + y;
+                            if (!((x == y ? sh.odd[0] : sh.odd[1])[y >> 5] >> (y & 31) & 1u)) continue;
+                            if (x == y ? !(sh.kin[node][y >> 5] >> (y & 31) & 1u) : j < lo || j >= g.r.base) continue;
+                            const int page = a.table[g.s * a.ld + j / a.page_size];
+                            if ((uint32_t)page >= (uint32_t)a.n_pages) continue;
+                            const int64_t vr = (((int64_t)page * a.page_size + j % a.page_size) * a.Hkv + kvh) * D + c0;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                if (F8) {
+                                    if ((static_cast<const uint8_t *>(a.v)[vr + k] & 0x7Fu) == 0x7Fu) v[k] = NAN;
+                                } else {
+                                    const float z = bf16_bits_to_float(static_cast<const uint16_t *>(a.v)[vr + k]);
+                                    if (!isfinite(z)) v[k] += z;
+                                }
+                            }
+                        }
+                    }
+                    if (valid && whole) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4 *>(dst + c0 + 8 * k) =
+                                make_uint4(bf16x2(v[8 * k], v[8 * k + 1]), bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                                           bf16x2(v[8 * k + 4], v[8 * k + 5]), bf16x2(v[8 * k + 6], v[8 * k + 7]));
+                    } else if (valid) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<float4 *>(po + c0 + 4 * k) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    }
+                }
+                if (valid) {
+                    if (!whole)
+                        ws.ml[at * kRows + row] = F8 ? make_float2(lse2, l == 0.f ? 0.f : 1.f) : make_float2(ref[0], l);
+                    else if (a.lse)
+                        a.lse[(int64_t)(g.r.off + node) * a.Hq + head] = lse2 * kLn2;
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sh.o_free));
+            mbar_arrive(smem_u32(&sh.nodes_free));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::mma_warp) tmem_dealloc(tmem, 512);
+}
+
+// The partials of the sequences that a range starts and leaves unfinished, joined. A CTA takes Rows rows of the y-th such range;
+// D / 4 threads a row, Groups of them on every Groups-th partial, merged in order at the end.
+template <int D, int Groups>
+__global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, TreePlan plan, TreeScratch ws) {
+    constexpr int cols = D / 4, Rows = 256 / cols / Groups, U = 8;
+    static_assert(Rows >= 1, "a row");
+    __shared__ float4 acc[Groups > 1 ? 256 : 1];
+    __shared__ float2 pair[256 / cols];
+    __shared__ int4 job_sh;
+    const int tid = threadIdx.x, col = tid % cols, group = tid / cols % Groups, sub = tid / cols / Groups;
+    wait_for_previous();
+    if (tid < 32) {
+        if (tid == 0) job_sh.x = -1;
+        __syncwarp();
+        int n = 0;
+        for (int r0 = 0; r0 < plan.ranges - 1; r0 += 32) {
+            const int r = r0 + tid;
+            const int2 meta = r < plan.ranges - 1 ? __ldcg(ws.meta + r) : make_int2(-1, 0);
+            const uint32_t some = __ballot_sync(0xffffffffu, meta.x >= 0);
+            if (meta.x >= 0 && n + __popc(some & ((1u << tid) - 1u)) == (int)blockIdx.x) job_sh = make_int4(r, meta.x, meta.y, 0);
+            n += __popc(some);
+        }
+    }
+    __syncthreads();
+    const int4 job = job_sh;
+    if (job.x < 0) return;
+    const int off = a.draft_off[job.y], T = a.draft_off[job.y + 1] - off;
+    // rows: (drafted token, query head), the heads of a KV head together
+    const int64_t id = (int64_t)blockIdx.y * Rows + sub;
+    const int per = T * a.G, kvh = (int)(id / per), r = (int)(id % per);
+    const bool valid = kvh < a.Hkv;
+    const int64_t C = (int64_t)a.Hkv * plan.m_tiles, at = (int64_t)(valid ? kvh : 0) * plan.m_tiles + r / kRows;
+    float m = -INFINITY, l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = group; i0 < job.z; i0 += U * Groups) {
+        float2 ml[U];
+        float4 o[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * Groups;
+            ml[u] = make_float2(-INFINITY, 0.f);
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < job.z) {
+                const int64_t p = (part_slot(job.x, i) * C + at) * kRows + r % kRows;
+                ml[u] = __ldcg(ws.ml + p);
+                o[u] = __ldcg(reinterpret_cast<const float4 *>(ws.o + p * D + 4 * col));
             }
         }
-        float dot = 0.f;
-        for (int e = 0; e < E; ++e) dot = fmaf(q[e], k[e], dot);
-        for (int x = 16; x >= 1; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
-        const float top = fmaxf(m, dot), ref = top == -INFINITY ? 0.f : top;
-        const float old = exp2f(m - ref), w = exp2f(dot - ref);
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+        const float ref = top == -INFINITY ? 0.f : top, old = ex2(m - ref);
         m = top;
-        l = l * old + w;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * old + w * v[e];
+        l *= old;
+        x.x *= old, x.y *= old, x.z *= old, x.w *= old;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float w = ex2(ml[u].x - ref);
+            l = fmaf(w, ml[u].y, l);
+            x.x = fmaf(w, o[u].x, x.x), x.y = fmaf(w, o[u].y, x.y);
+            x.z = fmaf(w, o[u].z, x.z), x.w = fmaf(w, o[u].w, x.w);
+        }
     }
+    if (Groups > 1) {
+        acc[tid] = x;
+        if (col == 0) pair[tid / cols] = make_float2(m, l);
+        __syncthreads();
+        if (group > 0) return;
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < Groups; ++i) top = fmaxf(top, pair[sub * Groups + i].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        l = 0.f, m = top;
+        x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < Groups; ++i) {
+            const float w = ex2(pair[sub * Groups + i].x - ref);
+            const float4 v = acc[tid + i * cols];
+            l = fmaf(w, pair[sub * Groups + i].y, l);
+            x.x = fmaf(w, v.x, x.x), x.y = fmaf(w, v.y, x.y), x.z = fmaf(w, v.z, x.z), x.w = fmaf(w, v.w, x.w);
+        }
+    }
+    if (!valid) return;
+    const int64_t to = (int64_t)(off + r / a.G) * a.Hq + kvh * a.G + r % a.G;
     const float f = l == 0.f ? 0.f : 1.f / l;
-    for (int e = 0; e < E; ++e) out[lane * E + e] = float_to_bf16_bits(o[e] * f);
-    if (lane == 0 && a.lse) a.lse[(int64_t)i * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    *reinterpret_cast<uint2 *>(a.out + to * D + 4 * col) = make_uint2(bf16x2(x.x * f, x.y * f), bf16x2(x.z * f, x.w * f));
+    if (col == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+constexpr int kMaxCtas = 160;
+
+int m_tiles_of(int G, int max_draft) { return (max_draft * G + kRows - 1) / kRows; }
+
+TreeScratch tree_scratch(char *w, int D, int Hkv, int m_tiles) {
+    const size_t parts = 2 * (size_t)std::max(1, kMaxCtas / (Hkv * m_tiles)) * Hkv * m_tiles * kRows;
+    TreeScratch s;
+    s.meta = reinterpret_cast<int2 *>(w);
+    s.ml = reinterpret_cast<float2 *>(w + kMaxCtas * sizeof(int2));
+    s.o = reinterpret_cast<float *>(w + kMaxCtas * sizeof(int2) + parts * sizeof(float2));
+    return s;
+}
+
+// SMs of the current device (cached per device; 0 on an error).
+template <typename C>
+int sms() {
+    static int cached[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (cached[dev] == 0) {
+        int n = 0;
+        if (cudaFuncSetAttribute(tree_tile_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem) != cudaSuccess ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return 0;
+        cached[dev] = std::min(n, kMaxCtas);
+    }
+    return cached[dev];
 }
 
 template <int D, bool F8>
 cudaError_t launch(const TreeArgs &a, cudaStream_t st) {
-    const int64_t items = (int64_t)a.N * a.Hq;
-    const unsigned ctas = (unsigned)((items + kTreeThreads / 32 - 1) / (kTreeThreads / 32));
-    return launch_dependent(tree_kernel<D, F8>, dim3(ctas), kTreeThreads, 0, st, a);
+    using C = TreeCfg<D, F8>;
+    const int ctas = sms<C>();
+    if (ctas == 0) {
+        const cudaError_t e = cudaGetLastError();
+        return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    }
+    TreePlan plan{};
+    plan.m_tiles = m_tiles_of(a.G, a.max_draft);
+    plan.ranges = std::max(1, ctas / (a.Hkv * plan.m_tiles));
+    plan.min_tiles = 2;
+    plan.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
+    // tiled loads of runs of a page; below 16 tokens the engine's cost for each box outweighs the copies of the worker warps
+    const int run = std::min(a.page_size & -a.page_size, C::T);
+    TreeMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    const int64_t rows = a.n_pages * a.page_size;
+    if (run >= 16 && rows > 0) {
+        plan.k_run = run;
+        plan.v_run = std::min(run, C::VT);
+        const uint64_t row = (uint64_t)a.Hkv * D * (F8 ? 1 : 2), blocks = row / 128;
+        const uint32_t whole = !F8 && plan.v_run == C::VT ? D / 64 : 1;
+        if (!encode_tmap_rows(&maps.k, a.k, F8, rows, blocks, row, plan.k_run, 1) ||
+            !encode_tmap_rows(&maps.v, a.v, F8, rows, blocks, row, plan.v_run, whole))
+            return cudaErrorInvalidValue;
+    }
+    const TreeScratch ws = tree_scratch(a.scratch, D, a.Hkv, plan.m_tiles);
+    const dim3 grid((unsigned)(plan.ranges * a.Hkv * plan.m_tiles));
+    const cudaError_t e = launch_dependent(tree_tile_kernel<C>, grid, C::threads, C::smem, st, a, plan, ws, maps);
+    if (e != cudaSuccess || plan.ranges == 1) return e;               // one range cuts no sequence
+    constexpr int groups = 256 / (D / 4);
+    const unsigned jobs = (unsigned)std::min(plan.ranges - 1, a.B), most = (unsigned)(a.max_draft * a.Hq);
+    return launch_dependent(tree_join_kernel<D, groups>, dim3(jobs, most), 256, 0, st, a, plan, ws);
 }
 
 }  // namespace
 
-size_t tree_scratch_bytes(int, int, int, int) { return 0; }
+size_t tree_scratch_bytes(int D, int Hq, int Hkv, int max_draft) {
+    const int m_tiles = m_tiles_of(Hq / Hkv, max_draft);
+    const size_t parts = 2 * (size_t)std::max(1, kMaxCtas / (Hkv * m_tiles)) * Hkv * m_tiles * kRows;
+    return kMaxCtas * sizeof(int2) + (kMaxCtas / (Hkv * m_tiles) > 1 ? parts * (sizeof(float2) + D * sizeof(float)) : 0);
+}
 
 cudaError_t launch_tree_decode(const TreeArgs &a, int D, bool fp8, cudaStream_t st) {
     switch (D) {
