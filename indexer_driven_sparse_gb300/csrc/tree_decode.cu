@@ -42,37 +42,38 @@ namespace qsa {
 namespace {
 
 constexpr int kRows = 128;                       // MMA M: rows of a CTA
-constexpr int kSlot = 16384;                     // bytes of a ring slot
+constexpr int kTile = 64;                        // tokens of a tile
 constexpr int kMetas = 4;                        // tiles whose slots and scales are known
-constexpr uint32_t kTmemS = 0, kTmemO = 256;     // two S buffers of 128 columns, then O
 constexpr float kLazy = 8.f;                     // O is rescaled when a maximum has grown by more than 2^8
+constexpr float kRaise = 6.f;                    // FP8 rows: weights up to 2^8, scales below 2, so below 2^15 in f16
 
 template <int D_, bool F8_>
 struct TreeCfg {
     static constexpr int D = D_;
     static constexpr bool F8 = F8_;
-    static constexpr int T = F8 ? 64 : 128;                  // tokens of a tile
-    static constexpr int SL = F8 ? D / 128 : D / 64;         // slots of a tile's K, and of its V
-    static constexpr int VT = F8 ? 64 : 128 * 64 / D;        // tokens of a V slot
-    static constexpr int SG = F8 ? D / 128 : 1;              // scales of a row, sets of weights
-    static constexpr int q_bytes = kRows * D * 2;
-    static constexpr int ring = F8 ? 4 : D == 256 ? 9 : D == 128 ? 11 : 12;
-    static constexpr int codes = F8 ? (D == 256 ? 10 : 12) : 0;      // slots of codes, 8 KB each
-    static constexpr int softmax = 128, q_threads = 64, workers = 256;
-    static constexpr int mma_warp = 4, index_warp = 5, q_warp = 6, work_warp = 8;
+    static constexpr int SD = D < 128 ? D : 128, SL = D / SD;   // dims of a slot; slots of a tile's K, and of its V
+    static constexpr int SG = F8 ? D / 128 : 1;                 // scales of a row, sets of weights
+    static constexpr int slot = kTile * SD * 2, code_slot = F8 ? kTile * SD : 0;    // bytes
+    static constexpr int ring = F8 ? 4 : 212992 / slot;
+    static constexpr int codes = F8 ? (D == 256 ? 10 : 12) : 0;
+    static constexpr int from = F8 ? codes : ring;              // slots that global memory is read into
+    static constexpr int ring_at = F8 ? kRows * D * 2 : 0, codes_at = ring_at + ring * slot;
+    static constexpr int smem = codes_at + codes * code_slot + 1024;
+    static_assert(smem + 12288 <= 227 * 1024, "shared memory of a CTA");
+    // tensor memory columns: O, the queries (bf16 rows; with FP8 rows they are in shared memory), two buffers of scores
+    static constexpr uint32_t t_o = 0, t_q = D, t_s = F8 ? 256 : 384, s_cols = F8 ? 128 : 64;
+    static constexpr int softmax = 128, q_threads = F8 ? 64 : 128, workers = F8 ? 256 : 192;
+    static constexpr int mma_warp = 4, index_warp = 5, q_warp = 6, work_warp = q_warp + q_threads / 32;
     static constexpr int threads = softmax + 64 + q_threads + workers;
-    static constexpr int ring_at = q_bytes, codes_at = ring_at + ring * kSlot, smem = codes_at + codes * kSlot / 2 + 1024;
-    static_assert(smem + 8192 <= 227 * 1024, "shared memory of a CTA");
-    static constexpr float raise = F8 ? 8.f : 0.f;
 };
 
 struct TreeMaps {
     CUtensorMap k, v;
 };
 
-// How rows get into shared memory: runs of `k_run` (K) and `v_run` (V) tokens by tiled TMA, or (k_run 0) by the worker warps.
+// How rows get into shared memory: runs of `run` tokens by tiled TMA, or (0) by the worker warps.
 struct TreePlan {
-    int32_t ranges, m_tiles, k_run, v_run;
+    int32_t ranges, m_tiles, run;
     int32_t page_shift;
     int32_t min_tiles;       // of a range
 };
@@ -89,7 +90,6 @@ struct TreeRow {
 };
 
 // high: the largest offset of an earlier sequence (0 at first).
-template <int Tt>
 __device__ __forceinline__ TreeRow tree_row(const TreeArgs &a, int s, int &high) {
     TreeRow r;
     r.off = a.draft_off[s];
@@ -102,8 +102,8 @@ __device__ __forceinline__ TreeRow tree_row(const TreeArgs &a, int s, int &high)
     if (r.T > 0 && r.T <= a.max_draft && r.len >= r.T && r.len <= a.ld * a.page_size) {
         r.base = r.len - r.T;
         r.lo = a.window > 0 ? max(0, r.base + 1 - a.window) : 0;
-        r.t0 = r.lo / Tt;
-        r.t1 = r.len / Tt + (r.len % Tt != 0);
+        r.t0 = r.lo / kTile;
+        r.t1 = r.len / kTile + (r.len % kTile != 0);
     }
     return r;
 }
@@ -116,13 +116,12 @@ struct Seg {
 };
 
 // The tiles [x, x1) of the list as segments of one sequence each; sequences without a row in this M tile are passed over.
-template <int Tt>
 struct Walk {
     long long x, x1;
     int s, skip, high, i = 0;
     __device__ __forceinline__ bool next(const TreeArgs &a, int m_tile, Seg &g) {
         while (x < x1) {
-            g.r = tree_row<Tt>(a, s, high);
+            g.r = tree_row(a, s, high);
             const int n = g.r.t1 - g.r.t0;
             if (n == 0) {
                 ++s;
@@ -149,10 +148,9 @@ __device__ __forceinline__ int k_turn(int c) { return c == 0 ? 0 : 2 * c - 1; }
 __device__ __forceinline__ int v_turn(int c, int n) { return c == n - 1 ? 2 * n - 1 : 2 * c + 2; }
 
 // Whether some row may not attend some token of tile t.
-template <int Tt>
 __device__ __forceinline__ bool masked(const TreeArgs &a, const TreeRow &r, int t) {
-    const int j0 = t * Tt;
-    return j0 > r.base - Tt || (a.window > 0 && j0 < r.base + r.T - a.window);
+    const int j0 = t * kTile;
+    return j0 > r.base - kTile || (a.window > 0 && j0 < r.base + r.T - a.window);
 }
 
 template <typename C>
@@ -165,9 +163,10 @@ struct TreeShared {
     int lo[QSA_MAX_DRAFT];                                // its first attended place
     uint32_t odd[2][QSA_MAX_DRAFT / 32];                  // tokens with values that are not finite: drafts, places from r.lo
     float q_scale[2][C::F8 ? kRows : 1];               // of every other segment
-    int slots[kMetas][C::T];
-    uint32_t real[kMetas][C::T / 32];                     // bit: the token's page exists
-    float4 scales[kMetas][C::F8 ? C::T : 1];              // K scales of 128 dims each, log2 of V scales
+    int slots[kMetas][kTile];
+    uint32_t real[kMetas][kTile / 32];                     // bit: the token's page exists
+    float4 scales[kMetas][C::F8 ? kTile : 1];             // K scales of 128 dims each, V scales
+    float2 top[kMetas];                                   // powers of two at most 2 below the tile's largest V scales
     uint32_t tmem;
     volatile int abort;
 };
@@ -206,7 +205,7 @@ __device__ __forceinline__ bool drop_nan_codes(uint32_t &w) {
 template <typename C>
 __global__ void __launch_bounds__(C::threads, 1)
     tree_tile_kernel(TreeArgs a, TreePlan plan, TreeScratch ws, const __grid_constant__ TreeMaps maps) {
-    constexpr int D = C::D, T = C::T, SL = C::SL, RING = C::ring, SG = C::SG;
+    constexpr int D = C::D, T = kTile, SD = C::SD, SL = C::SL, RING = C::ring, SG = C::SG;
     constexpr bool F8 = C::F8;
     extern __shared__ uint8_t smem_raw[];
     __shared__ TreeShared<C> sh;
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(C::threads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int m_tile = blockIdx.x % plan.m_tiles, kvh = blockIdx.x / plan.m_tiles % a.Hkv, range = blockIdx.x / plan.m_tiles / a.Hkv;
     const bool speaks = kvh == 0 && m_tile == 0;          // records errors that all CTAs of a range see
-    const bool tiled = plan.k_run > 0;
+    const bool tiled = plan.run > 0;
 
     if (warp == C::mma_warp) tmem_alloc(&sh.tmem, 512);
     if (tid == 0) {
@@ -258,7 +257,7 @@ __global__ void __launch_bounds__(C::threads, 1)
 
     // ---- this range's part of the list: tiles before each thread's run of sequences, then the place of the first tile.
     // Sequences that cannot be attended get their zeros here.
-    Walk<T> walk;
+    Walk walk;
     {
         const int per = (a.B + C::threads - 1) / C::threads, s_lo = min(a.B, tid * per), s_hi = min(a.B, s_lo + per);
         int top = 0;                                      // the largest offset of the run
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(C::threads, 1)
         const int high0 = high;
         long long mine = 0;
         for (int s = s_lo; s < s_hi; ++s) {
-            const TreeRow r = tree_row<T>(a, s, high);
+            const TreeRow r = tree_row(a, s, high);
             mine += r.t1 - r.t0;
             if (r.t1 > r.t0 || (r.named && r.T == 0)) continue;
             if (!speaks || s % plan.ranges != range) continue;
@@ -310,7 +309,7 @@ __global__ void __launch_bounds__(C::threads, 1)
             int at = high0;
             for (int s = s_lo;; ++s) {
                 const int was = at;
-                const TreeRow r = tree_row<T>(a, s, at);
+                const TreeRow r = tree_row(a, s, at);
                 if (walk.x < before + r.t1 - r.t0) {
                     start[0] = s, start[1] = (int)(walk.x - before), start[2] = was;
                     break;
@@ -327,7 +326,7 @@ __global__ void __launch_bounds__(C::threads, 1)
 
         // the sequence that this range starts and leaves unfinished: how many ranges it spans
         if (speaks && tid == 0 && walk.x < walk.x1) {
-            Walk<T> w = walk;
+            Walk w = walk;
             Seg g;
             while (w.next(a, 0, g))
                 if (g.begins && !g.ends) {
@@ -354,6 +353,7 @@ __global__ void __launch_bounds__(C::threads, 1)
     if (warp == C::index_warp) {
         // ================================================================ slots of each tile; TMA loads
         constexpr int E = T / 32;                         // tokens of a lane, neighbours
+        constexpr int blocks = F8 ? 1 : SD / 64;          // 128-byte blocks of a slot's rows
         const int rows_end = (int)min((int64_t)INT32_MAX, a.n_pages * a.page_size);       // a row that does not exist: zeros
         int page[E], offset[E];
         bool ok = true;
@@ -369,64 +369,32 @@ __global__ void __launch_bounds__(C::threads, 1)
             }
         };
         int asked = 0;                                    // ring slots asked for
-        int slot_k[E], slot_v[E];                         // slots of the tile whose K, and whose V, comes next
-        auto load_k = [&](int q0) -> bool {               // ring slots q0 ... of one tile's K
+        int slot_v[E];                                    // slots of the tile whose V comes next
+        const int boxes = tiled ? T / plan.run : 1, whole = boxes == 1 ? 1 : blocks;
+        auto load = [&](const void *map, const int (&slot)[E], int q0) -> bool {      // one tile's K or V into ring slots q0 ...
+            const int run = lane % boxes, block = lane / boxes;
+            const int y = __shfl_sync(0xffffffffu, slot[0], run * (T / E / boxes));
             for (int k = 0; k < SL; ++k) {
-                const int q = q0 + k, at = q % (F8 ? C::codes : RING), turn = q / (F8 ? C::codes : RING);
-                uint64_t *full = F8 ? &sh.c_full[at] : &sh.full[at], *empty = F8 ? &sh.c_empty[at] : &sh.empty[at];
-                if (turn > 0 && !wait_warp(empty, turn - 1)) return false;
+                const int q = q0 + k, at = q % C::from, turn = q / C::from;
+                uint64_t *full = F8 ? &sh.c_full[F8 ? at : 0] : &sh.full[F8 ? 0 : at];
+                if (turn > 0 && !wait_warp(F8 ? &sh.c_empty[F8 ? at : 0] : &sh.empty[F8 ? 0 : at], turn - 1)) return false;
                 asked = q + 1;
-                const uint32_t dst = F8 ? codes_at + at * (kSlot / 2) : ring_at + at * kSlot;
-                if (lane == 0) mbar_arrive_expect_tx(smem_u32(full), F8 ? kSlot / 2 : kSlot);
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(full), F8 ? C::code_slot : C::slot);
                 __syncwarp();
-                const int first = lane * plan.k_run;      // token of this lane's box
-                int y = 0;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int v = __shfl_sync(0xffffffffu, slot_k[e], first / E & 31);
-                    if (first % E == e) y = v;
-                }
-                if (first < T)
-                    tma_load_3d(dst + first * 128, &maps.k, 0, y < 0 ? rows_end : y, kvh * (F8 ? D / 128 : D / 64) + k, smem_u32(full));
+                if (block < whole)
+                    tma_load_3d((F8 ? codes_at + at * C::code_slot : ring_at + at * C::slot) + block * (T * 128) + run * plan.run * 128,
+                                map, 0, y < 0 ? rows_end : y, (kvh * SL + k) * blocks + block, smem_u32(full));
             }
             return true;
         };
-        auto load_v = [&](int q0) -> bool {
-            for (int k = 0; k < SL; ++k) {
-                const int q = q0 + k, at = q % (F8 ? C::codes : RING), turn = q / (F8 ? C::codes : RING);
-                uint64_t *full = F8 ? &sh.c_full[at] : &sh.full[at], *empty = F8 ? &sh.c_empty[at] : &sh.empty[at];
-                if (turn > 0 && !wait_warp(empty, turn - 1)) return false;
-                asked = q + 1;
-                const uint32_t dst = F8 ? codes_at + at * (kSlot / 2) : ring_at + at * kSlot;
-                if (lane == 0) mbar_arrive_expect_tx(smem_u32(full), F8 ? kSlot / 2 : kSlot);
-                __syncwarp();
-                const int boxes = C::VT / plan.v_run;     // of whole rows: one, or (64 dims each) several
-                const int run = lane % boxes, block = lane / boxes;
-                const int first = (F8 ? 0 : k * C::VT) + run * plan.v_run;
-                int y = 0;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int v = __shfl_sync(0xffffffffu, slot_v[e], first / E & 31);
-                    if (first % E == e) y = v;
-                }
-                y = y < 0 ? rows_end : y;
-                if (F8) {
-                    if (block == 0) tma_load_3d(dst + run * plan.v_run * 128, &maps.v, 0, y, kvh * (D / 128) + k, smem_u32(full));
-                } else if (boxes == 1) {
-                    if (lane == 0) tma_load_3d(dst, &maps.v, 0, y, kvh * (D / 64), smem_u32(full));
-                } else if (block < D / 64) {
-                    tma_load_3d(dst + block * (C::VT * 128) + run * plan.v_run * 128, &maps.v, 0, y, kvh * (D / 64) + block, smem_u32(full));
-                }
-            }
-            return true;
-        };
-        Walk<T> w = walk;
+        Walk w = walk;
         int done = 0;
         bool more = w.next(a, m_tile, g);
         if (more) fetch(g.ta);
         while (more && ok) {
             const Seg now = g;
             const int n = now.tb - now.ta, turn0 = 2 * now.i0;
+            float2 top = make_float2(0.f, 0.f);           // FP8: powers of two next to the largest V scales of the segment so far
             for (int c = 0; c < n && ok; ++c, ++done) {
                 int slot[E];
                 float4 scale[F8 ? E : 1];
@@ -466,115 +434,120 @@ __global__ void __launch_bounds__(C::threads, 1)
                     ok = false;
                     break;
                 }
-                uint32_t bits = 0;                        // tokens lane E + e as bit (lane E + e) % 32 of word (lane E) / 32
+                uint32_t bits = 0;                        // token lane E + e as bit (lane E + e) % 32 of word lane E / 32
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     bits |= (exists[e] ? 1u : 0u) << ((lane * E + e) & 31);
                     if (!tiled) sh.slots[m][lane * E + e] = exists[e] ? slot[e] : -1;
-                    if (F8) {
-                        // infinite V scales become NaN: as a maximum they would take every other token's weight to zero
-                        const float4 x = scale[e];
-                        sh.scales[m][lane * E + e] = make_float4(x.x, x.y, fmaf(x.z, 0.f, lg2(x.z)), fmaf(x.w, 0.f, lg2(x.w)));
-                    }
                 }
 #pragma unroll
                 for (int o = 1; o < 32 / E; o <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
                 if (lane % (32 / E) == 0) sh.real[m][lane * E / 32] = bits;
+                if (F8) {
+                    float z = 0.f, u = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        z = fmaxf(z, scale[e].z < INFINITY ? scale[e].z : 0.f);
+                        u = fmaxf(u, scale[e].w < INFINITY ? scale[e].w : 0.f);
+                    }
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) {
+                        z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
+                        if (SG == 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
+                    }
+                    auto power = [](float x) { return __uint_as_float(min(max(__float_as_uint(x) & 0x7F800000u, 7u << 23), 247u << 23)); };
+                    top = make_float2(fmaxf(top.x, power(z)), fmaxf(top.y, power(u)));
+                    auto inverse = [](float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); };
+                    const float cx = inverse(top.x) * (float)(1 << (int)kRaise), cy = inverse(top.y) * (float)(1 << (int)kRaise);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float4 x = scale[e];        // infinite V scales become NaN
+                        sh.scales[m][F8 ? lane * E + e : 0] = make_float4(x.x, x.y, fmaf(x.z, 0.f, x.z) * cx, fmaf(x.w, 0.f, x.w) * cy);
+                    }
+                    if (lane == 0) sh.top[m] = top;
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.meta_full[m]));
                 if (tiled) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) slot_k[e] = slot[e];
-                    ok = load_k((turn0 + k_turn(c)) * SL);
-                    if (ok && c > 0) ok = load_v((turn0 + v_turn(c - 1, n)) * SL);
+                    ok = load(&maps.k, slot, (turn0 + k_turn(c)) * SL);
+                    if (ok && c > 0) ok = load(&maps.v, slot_v, (turn0 + v_turn(c - 1, n)) * SL);
 #pragma unroll
                     for (int e = 0; e < E; ++e) slot_v[e] = slot[e];
-                    if (ok && c + 1 == n) ok = load_v((turn0 + v_turn(c, n)) * SL);
+                    if (ok && c + 1 == n) ok = load(&maps.v, slot_v, (turn0 + v_turn(c, n)) * SL);
                 }
             }
         }
         // no load may still be writing shared memory when the CTA ends (bounded waits; they are over unless a role gave up)
-        constexpr int R = F8 ? C::codes : RING;
-        for (int q = max(0, asked - R); q < asked; ++q)
-            mbar_wait_bounded(smem_u32(F8 ? &sh.c_full[F8 ? q % R : 0] : &sh.full[q % RING]), (uint32_t)(q / R) & 1u, kWaitLimitNs);
+        for (int q = max(0, asked - C::from); q < asked; ++q)
+            mbar_wait_bounded(smem_u32(F8 ? &sh.c_full[F8 ? q % C::from : 0] : &sh.full[F8 ? 0 : q % C::from]),
+                              (uint32_t)(q / C::from) & 1u, kWaitLimitNs);
     } else if (warp >= C::work_warp) {
         // ================================================================ workers: cp.async loads; codes -> f16
         const int wt = tid - C::work_warp * 32;
-        Walk<T> w = walk;
-        bool ok = true;
-        if (!F8) {
-            const uint16_t *rows[2] = {static_cast<const uint16_t *>(a.k) + kvh * D, static_cast<const uint16_t *>(a.v) + kvh * D};
-            const int64_t pitch = (int64_t)a.Hkv * D;
-            auto copy = [&](int is_v, int tile, int q0) -> bool {      // a tile's K or V into ring slots q0 ...
-                const int m = tile % kMetas;
-                if (!is_v && !wait_warp(&sh.meta_full[m], tile / kMetas)) return false;
-                for (int k = 0; k < SL; ++k) {
-                    const int q = q0 + k, at = q % RING, turn = q / RING;
-                    if (turn > 0 && !wait_warp(&sh.empty[at], turn - 1)) return false;
-                    const uint32_t dst = ring_at + at * kSlot;
+        constexpr int row_chunks = F8 ? SD / 16 : SD / 8;     // 16-byte chunks of a token's row in a slot
+        const char *rows[2] = {static_cast<const char *>(a.k) + (int64_t)kvh * SL * row_chunks * 16,
+                               static_cast<const char *>(a.v) + (int64_t)kvh * SL * row_chunks * 16};
+        const int64_t pitch = (int64_t)a.Hkv * SL * row_chunks * 16;
+        // a tile's K or V into the slots of turn q0 ...
+        auto copy = [&](int is_v, int tile, int q0) -> bool {
+            const int m = tile % kMetas;
+            if (!is_v && !wait_warp(&sh.meta_full[m], tile / kMetas)) return false;
+            for (int k = 0; k < SL; ++k) {
+                const int q = q0 + k, at = q % C::from, turn = q / C::from;
+                if (turn > 0 && !wait_warp(F8 ? &sh.c_empty[F8 ? at : 0] : &sh.empty[F8 ? 0 : at], turn - 1)) return false;
+                const uint32_t dst = F8 ? codes_at + at * C::code_slot : ring_at + at * C::slot;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int id = i * C::workers + wt;
-                        const int tok = is_v ? id / (D / 8) : id / 8, gr = is_v ? id % (D / 8) : id % 8;
-                        const int sl = sh.slots[m][is_v ? k * C::VT + tok : tok];
-                        const uint32_t to = dst + (is_v ? gr / 8 * (C::VT * 128) : 0) + swz(tok, gr & 7);
-                        cp_async16_zfill(to, rows[is_v] + max(sl, 0) * pitch + (is_v ? 0 : k * 64) + gr * 8, sl >= 0);
-                    }
-                    cp_async_arrive(smem_u32(&sh.full[at]));
+                for (int i = 0; i < (T * row_chunks + C::workers - 1) / C::workers; ++i) {
+                    const int id = i * C::workers + wt, tok = id / row_chunks, gr = id % row_chunks;
+                    if (tok >= T) break;
+                    const int sl = sh.slots[m][tok];
+                    cp_async16_zfill(dst + gr / 8 * (T * 128) + swz(tok, gr & 7), rows[is_v] + max(sl, 0) * pitch + (k * row_chunks + gr) * 16,
+                                     sl >= 0);
                 }
-                if (is_v) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.meta_empty[m]));
-                }
-                return true;
-            };
-            while (!tiled && ok && w.next(a, m_tile, g)) {
-                const int n = g.tb - g.ta, turn0 = 2 * g.i0;
-                for (int c = 0; c < n && ok; ++c) {
-                    ok = copy(0, g.i0 + c, (turn0 + k_turn(c)) * SL);
-                    if (ok && c > 0) ok = copy(1, g.i0 + c - 1, (turn0 + v_turn(c - 1, n)) * SL);
-                    if (ok && c + 1 == n) ok = copy(1, g.i0 + c, (turn0 + v_turn(c, n)) * SL);
-                }
+                cp_async_arrive(smem_u32(F8 ? &sh.c_full[F8 ? at : 0] : &sh.full[F8 ? 0 : at]));
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-        } else if constexpr (F8) {
-            // slots in turn: q = 0, 1, ...; codes of slot q + codes - 1 are asked for before slot q is converted
-            constexpr int NC = C::codes;
-            const uint8_t *rows[2] = {static_cast<const uint8_t *>(a.k) + kvh * D, static_cast<const uint8_t *>(a.v) + kvh * D};
-            const int64_t pitch = (int64_t)a.Hkv * D;
-            auto copy = [&](int is_v, int tile, int q0) -> bool {
-                const int m = tile % kMetas;
-                if (!is_v && !wait_warp(&sh.meta_full[m], tile / kMetas)) return false;
-                for (int k = 0; k < SL; ++k) {
-                    const int q = q0 + k, at = q % NC, turn = q / NC;
-                    if (turn > 0 && !wait_warp(&sh.c_empty[at], turn - 1)) return false;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int id = i * C::workers + wt, tok = id / 8, gr = id % 8;
-                        const int sl = sh.slots[m][tok];
-                        cp_async16_zfill(codes_at + at * (kSlot / 2) + swz(tok, gr), rows[is_v] + max(sl, 0) * pitch + k * 128 + gr * 16,
-                                         sl >= 0);
-                    }
-                    cp_async_arrive(smem_u32(&sh.c_full[at]));
-                }
-                if (is_v) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.meta_empty[m]));
-                }
-                return true;
-            };
-            // lo, len, base, edge: of the tile's sequence (V only); tokens at or behind len and before lo become zeros, NaN codes of those
-            // that not every row attends too
+            if (is_v) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.meta_empty[m]));
+            }
+            return true;
+        };
+        // The copies' walk: turn cc of the segment's 2 n. 0: K0; 2i - 1: K of tile i; 2i + 2: V of tile i; 2n - 1: the last V.
+        Walk wc = walk;
+        Seg gc{};
+        int cc = 0, nc = 0;
+        bool more = !tiled && wc.next(a, m_tile, gc);
+        if (more) nc = 2 * (gc.tb - gc.ta);
+        auto turn_is_v = [](int c, int turns) { return c == turns - 1 || (c > 0 && (c & 1) == 0); };
+        auto turn_tile = [&](int c, int turns) { return c == 0 ? 0 : c == turns - 1 ? turns / 2 - 1 : turn_is_v(c, turns) ? c / 2 - 1 : (c + 1) / 2; };
+        auto ask = [&]() -> bool {
+            if (!more) return true;
+            if (!copy(turn_is_v(cc, nc), gc.i0 + turn_tile(cc, nc), (2 * gc.i0 + cc) * SL)) return false;
+            if (++cc == nc) {
+                more = wc.next(a, m_tile, gc);
+                cc = 0;
+                nc = more ? 2 * (gc.tb - gc.ta) : 0;
+            }
+            return true;
+        };
+        bool ok = true;
+        if constexpr (!F8) {
+            while (ok && more) ok = ask();
+        } else {
+            // codes of a turn are asked for `ahead` turns before it is converted. At most 6: a tile's K is asked for when the
+            // softmax has left the tile four before it, which needs the V turns up to seven before this one converted.
+            constexpr int ahead = C::codes / SL - 1 < 6 ? C::codes / SL - 1 : 6;
             auto convert = [&](int q0, bool is_v, int j0, const TreeRow &r, bool some) -> bool {
+                // V: rows that nothing attends become zeros, and NaN codes of rows that not every row attends
                 const int edge = a.window > 0 ? r.base + r.T - a.window : 0;
                 for (int k = 0; k < SL; ++k) {
-                    const int q = q0 + k, from = q % NC, to = q % RING;
-                    if (!wait_warp(&sh.c_full[from], q / NC)) return false;
+                    const int q = q0 + k, from = q % C::codes, to = q % RING;
+                    if (!wait_warp(&sh.c_full[from], q / C::codes)) return false;
                     if (q >= RING && !wait_warp(&sh.empty[to], q / RING - 1)) return false;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int id = i * C::workers + wt, tok = id / 8, gr = id % 8;
-                        uint4 v = *reinterpret_cast<const uint4 *>(sm + C::codes_at + from * (kSlot / 2) + swz(tok, gr));
+                    for (int i = 0; i < T * row_chunks / C::workers; ++i) {
+                        const int id = i * C::workers + wt, tok = id / row_chunks, gr = id % row_chunks;
+                        uint4 v = *reinterpret_cast<const uint4 *>(sm + C::codes_at + from * C::code_slot + swz(tok, gr));
                         if (is_v && some) {
                             const int j = j0 + tok;
                             if ((uint32_t)j >= (uint32_t)r.len || j < r.lo)
@@ -582,7 +555,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                             else if (j >= r.base || j < edge)
                                 drop_nan_codes(v.x), drop_nan_codes(v.y), drop_nan_codes(v.z), drop_nan_codes(v.w);
                         }
-                        uint8_t *dst = sm + C::ring_at + to * kSlot + (gr >> 2) * (T * 128);
+                        uint8_t *dst = sm + C::ring_at + to * C::slot + (gr >> 2) * (T * 128);
                         const int at = (gr & 3) * 2;
                         *reinterpret_cast<uint4 *>(dst + swz(tok, at)) =
                             make_uint4(e4m3_to_f16x2(v.x, 0), e4m3_to_f16x2(v.x, 1), e4m3_to_f16x2(v.y, 0), e4m3_to_f16x2(v.y, 1));
@@ -596,46 +569,22 @@ __global__ void __launch_bounds__(C::threads, 1)
                 }
                 return true;
             };
-            // without TMA the copies run `ahead` turns (of a tile's K or V) before the conversion, on a walk of their own
-            // (at most 6: a tile's K is asked for when the softmax has left the tile four before it, which needs the V turns up to
-            // seven before this one converted)
-            constexpr int ahead = NC / SL - 1 < 6 ? NC / SL - 1 : 6;
-            Walk<T> wc = walk;
-            Seg gc;
-            int cc = 0, nc = 0, asked = 0;                // copies: turn within the segment's 2 n, and turns in all
-            bool more = !tiled && wc.next(a, m_tile, gc);
-            if (more) nc = 2 * (gc.tb - gc.ta);
-            auto ask = [&]() -> bool {                    // the copies' next turn
-                if (!more) return true;
-                const int n = nc / 2, c = cc;
-                // turn -> (K or V, tile): 0: K0; 2i - 1: Ki; 2i + 2: Vi; 2n - 1: V(n-1)
-                const bool is_v = c == nc - 1 || (c > 0 && (c & 1) == 0);
-                const int tile = c == 0 ? 0 : c == nc - 1 ? n - 1 : is_v ? c / 2 - 1 : (c + 1) / 2;
-                if (!copy(is_v, gc.i0 + tile, (2 * gc.i0 + c) * SL)) return false;
-                ++asked;
-                if (++cc == nc) {
-                    more = wc.next(a, m_tile, gc);
-                    cc = 0;
-                    nc = more ? 2 * (gc.tb - gc.ta) : 0;
-                }
-                return true;
-            };
+            Walk w = walk;
             for (int i = 0; i < ahead && ok; ++i) ok = ask();
             while (ok && w.next(a, m_tile, g)) {
-                const int n = g.tb - g.ta;
-                for (int c = 0; c < 2 * n && ok; ++c) {
-                    const bool is_v = c == 2 * n - 1 || (c > 0 && (c & 1) == 0);
-                    const int tile = c == 0 ? 0 : c == 2 * n - 1 ? n - 1 : is_v ? c / 2 - 1 : (c + 1) / 2;
+                const int turns = 2 * (g.tb - g.ta);
+                for (int c = 0; c < turns && ok; ++c) {
+                    const int t = g.ta + turn_tile(c, turns);
                     ok = ask();
-                    if (ok) ok = convert((2 * g.i0 + c) * SL, is_v, (g.ta + tile) * T, g.r, masked<T>(a, g.r, g.ta + tile));
+                    if (ok) ok = convert((2 * g.i0 + c) * SL, turn_is_v(c, turns), t * T, g.r, masked(a, g.r, t));
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp >= C::q_warp && warp < C::work_warp) {
         // ================================================================ queries, ancestors, clean V rows
         const int qt = tid - C::q_warp * 32;
-        Walk<T> w = walk;
+        Walk w = walk;
         bool ok = true;
         int seg = 0, cleaned = 0;
         while (ok && w.next(a, m_tile, g)) {
@@ -645,13 +594,24 @@ __global__ void __launch_bounds__(C::threads, 1)
                 const int node = (m_tile * kRows + r) / a.G, h = (m_tile * kRows + r) % a.G;
                 return a.q + (int64_t)(g.r.off + node) * a.q_ld + (kvh * a.G + h) * D;
             };
-            if (!F8) {
-                for (int i = qt; i < kRows * (D / 8); i += C::q_threads) {
-                    const int r = i / (D / 8), gr = i % (D / 8);
-                    const uint32_t dst = q_at + gr / 8 * (kRows * 128) + swz(r, gr & 7);
-                    cp_async16_zfill(dst, r < rows ? row_at(r) + gr * 8 : a.q, r < rows);
+            if constexpr (!F8) {
+                // a row each thread, into its lane of tensor memory (a warp reaches the lanes of its number modulo 4)
+                const int r = 32 * (warp & 3) + lane;
+                const uint32_t dst = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C::t_q;
+                const uint16_t *src = r < rows ? row_at(r) : nullptr;
+#pragma unroll
+                for (int c0 = 0; c0 < D / 2; c0 += 32) {          // 32 columns are 64 dims
+                    uint32_t x[32];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (src) v = *reinterpret_cast<const uint4 *>(src + 2 * c0 + 8 * k);
+                        x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
+                    }
+                    __syncwarp();
+                    tmem_st32(dst + c0, x);
                 }
-                asm volatile("cp.async.wait_all;" ::: "memory");
+                tc_fence_before();
             } else {
                 // D / 8 lanes have a row, 8 values each
                 constexpr int each = C::q_threads / (D / 8);
@@ -675,8 +635,8 @@ __global__ void __launch_bounds__(C::threads, 1)
                                  : "memory");
                     if (gr == 0) sh.q_scale[seg & 1][r] = __uint_as_float((uint32_t)(127 + e) << 23);
                 }
+                fence_proxy_async_smem();
             }
-            fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sh.q_full));
             // ---- the drafted tokens' ancestors, once the last segment's are no longer needed
             if (seg > 0 && !wait_warp(&sh.nodes_free, seg - 1)) break;
@@ -711,7 +671,7 @@ __global__ void __launch_bounds__(C::threads, 1)
             };
             for (int c = 0; c < n && ok; ++c) {
                 const int t = g.ta + c;
-                if (!masked<T>(a, g.r, t)) continue;
+                if (!masked(a, g.r, t)) continue;
                 if (!F8) {
                     // the MMA warp says when the rows are in: it meets every turn of the ring, and a wait tells only two from each other
                     if (!wait_warp(&sh.to_clean, cleaned)) {
@@ -720,11 +680,11 @@ __global__ void __launch_bounds__(C::threads, 1)
                     }
                     for (int k = 0; k < SL; ++k) {
                         const int at = ((2 * g.i0 + v_turn(c, n)) * SL + k) % RING;
-                        for (int i = qt; i < C::VT * (D / 8); i += C::q_threads) {
-                            const int tok = i / (D / 8), gr = i % (D / 8), j = t * T + k * C::VT + tok;
+                        for (int i = qt; i < T * (SD / 8); i += C::q_threads) {
+                            const int tok = i / (SD / 8), gr = i % (SD / 8), j = t * T + tok;
                             const bool out = (uint32_t)j >= (uint32_t)g.r.len || j < g.r.lo;
                             if (!out && j < g.r.base && j >= edge) continue;
-                            uint4 *p = reinterpret_cast<uint4 *>(sm + C::ring_at + at * kSlot + gr / 8 * (C::VT * 128) + swz(tok, gr & 7));
+                            uint4 *p = reinterpret_cast<uint4 *>(sm + C::ring_at + at * C::slot + gr / 8 * (T * 128) + swz(tok, gr & 7));
                             if (out) {
                                 *p = make_uint4(0, 0, 0, 0);
                             } else {
@@ -759,30 +719,28 @@ __global__ void __launch_bounds__(C::threads, 1)
     } else if (warp == C::mma_warp) {
         // ================================================================ products
         if (lane == 0) {
-            Walk<T> w = walk;
+            Walk w = walk;
             uint64_t *last_bar = nullptr;                 // the barrier of the last commit, and its phase
             uint32_t last_phase = 0;
             int seg = 0, cleaned = 0;
             bool ok = true;
             auto scores = [&](int i, int q0, bool first, bool last) -> bool {
-                const uint32_t s_at = tmem + kTmemS + (i & 1) * 128;
+                const uint32_t s_at = tmem + C::t_s + (i & 1) * C::s_cols;
                 if (first && !wait(&sh.q_full, seg)) return false;
                 for (int k = 0; k < SL; ++k) {
                     const int q = q0 + k, at = q % RING;
                     if (!wait(&sh.full[at], q / RING)) return false;
                     fence_proxy_async_smem();
                     tc_fence_after();
-                    const uint32_t b = ring_at + at * kSlot;
-                    if (!F8) {
+                    const uint32_t b = ring_at + at * C::slot;
 #pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            tc_mma(s_at, tc_desc(q_at + k * (kRows * 128) + z * 32, 16, 1024), tc_desc(b + z * 32, 16, 1024),
-                                   tc_idesc(kRows, T, 0), k > 0 || z > 0);
-                    } else {
-#pragma unroll
-                        for (int z = 0; z < 8; ++z)
-                            tc_mma(s_at + k * T, tc_desc(q_at + (2 * k + z / 4) * (kRows * 128) + (z & 3) * 32, 16, 1024),
-                                   tc_desc(b + z / 4 * (T * 128) + (z & 3) * 32, 16, 1024), f16_idesc(T, 0), z > 0);
+                    for (int z = 0; z < SD / 16; ++z) {
+                        const uint64_t bd = tc_desc(b + z / 4 * (T * 128) + (z & 3) * 32, 16, 1024);
+                        if (!F8)
+                            tc_mma_ta(s_at, tmem + C::t_q + (k * (SD / 16) + z) * 8, bd, tc_idesc(kRows, T, 0), k > 0 || z > 0);
+                        else
+                            tc_mma(s_at + k * T, tc_desc(q_at + (2 * k + z / 4) * (kRows * 128) + (z & 3) * 32, 16, 1024), bd,
+                                   f16_idesc(T, 0), z > 0);
                     }
                     tc_commit(smem_u32(&sh.empty[at]));
                 }
@@ -802,20 +760,17 @@ __global__ void __launch_bounds__(C::threads, 1)
                     }
                     // ---- O (+)= P V
                     const int q0 = (turn0 + v_turn(c, n)) * SL;
-                    const bool part = !F8 && masked<T>(a, g.r, g.ta + c);
+                    const bool part = !F8 && masked(a, g.r, g.ta + c);
                     if (part) {
                         for (int k = 0; k < SL && ok; ++k) ok = wait(&sh.full[(q0 + k) % RING], (q0 + k) / RING);
                         mbar_arrive(smem_u32(&sh.to_clean));
                     }
-                    if (!ok || !wait(&sh.p_full[i & 1], i >> 1) || (c == 0 && seg > 0 && !wait(&sh.o_free, seg - 1))) {
+                    if (!ok || !wait(&sh.p_full[i & 1], i >> 1) || (c == 0 && seg > 0 && !wait(&sh.o_free, seg - 1)) ||
+                        (part && !wait(&sh.clean, cleaned++))) {
                         ok = false;
                         break;
                     }
-                    if (part && !wait(&sh.clean, cleaned++)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t p_at = tmem + kTmemS + (i & 1) * 128;
+                    const uint32_t p_at = tmem + C::t_s + (i & 1) * C::s_cols;
                     for (int k = 0; k < SL; ++k) {
                         const int q = q0 + k, at = q % RING;
                         if (!wait(&sh.full[at], q / RING)) {
@@ -824,18 +779,11 @@ __global__ void __launch_bounds__(C::threads, 1)
                         }
                         fence_proxy_async_smem();
                         tc_fence_after();
-                        const uint32_t b = ring_at + at * kSlot;
-                        if (!F8) {
+                        const uint32_t b = ring_at + at * C::slot;
 #pragma unroll
-                            for (int z = 0; z < C::VT / 16; ++z)
-                                tc_mma_ta(tmem + kTmemO, p_at + (k * C::VT / 16 + z) * 8, tc_desc(b + z * 2048, C::VT * 128, 1024),
-                                          tc_idesc(kRows, D, 1), c > 0 || k > 0 || z > 0);
-                        } else {
-#pragma unroll
-                            for (int z = 0; z < T / 16; ++z)
-                                tc_mma_ta(tmem + kTmemO + k * 128, p_at + k * (T / 2) + z * 8, tc_desc(b + z * 2048, T * 128, 1024),
-                                          f16_idesc(128, 1), c > 0 || z > 0);
-                        }
+                        for (int z = 0; z < T / 16; ++z)
+                            tc_mma_ta(tmem + C::t_o + k * SD, p_at + (F8 ? k * (T / 2) : 0) + z * 8, tc_desc(b + z * 2048, T * 128, 1024),
+                                      F8 ? f16_idesc(SD, 1) : tc_idesc(kRows, SD, 1), c > 0 || z > 0);
                         tc_commit(smem_u32(&sh.empty[at]));
                     }
                     if (!ok) break;
@@ -849,9 +797,9 @@ __global__ void __launch_bounds__(C::threads, 1)
         }
     } else {
         // ================================================================ softmax
-        const uint32_t t_row = tmem + ((uint32_t)(32 * warp) << 16), t_o = t_row + kTmemO;
+        const uint32_t t_row = tmem + ((uint32_t)(32 * warp) << 16), t_o = t_row + C::t_o;
         const int row = tid;
-        Walk<T> w = walk;
+        Walk w = walk;
         int seg = 0;
         bool ok = true;
         for (; ok && w.next(a, m_tile, g); ++seg) {
@@ -861,9 +809,8 @@ __global__ void __launch_bounds__(C::threads, 1)
             if (!wait_warp(&sh.nodes_full, seg)) break;
             const int lo = sh.lo[min(node, g.r.T - 1)];
             const float scale = F8 ? a.scale_log2 * sh.q_scale[seg & 1][F8 ? row : 0] : a.scale_log2;
-            float ref[SG], l = 0.f;                       // the lazy maxima, and the weights' sum relative to the first
-#pragma unroll
-            for (int x = 0; x < SG; ++x) ref[x] = -INFINITY;
+            float ref = -INFINITY, l = 0.f;               // the lazy maximum, and the weights' sum relative to it
+            float2 unit = make_float2(0.f, 0.f);          // FP8: O is in units of these over 2^kRaise
             for (int c = 0; c < n; ++c) {
                 const int i = g.i0 + c, t = g.ta + c, m = i % kMetas;
                 if (!wait_warp(&sh.meta_full[m], i / kMetas)) {
@@ -872,8 +819,8 @@ __global__ void __launch_bounds__(C::threads, 1)
                 }
                 // which of the tile's tokens this row attends
                 constexpr int W = T / 32;
-                uint32_t see[W];
-                const bool part = masked<T>(a, g.r, t);
+                uint32_t see[W], both = ~0u;
+                const bool part = masked(a, g.r, t);
 #pragma unroll
                 for (int x = 0; x < W; ++x) {
                     see[x] = sh.real[m][x];
@@ -895,131 +842,88 @@ __global__ void __launch_bounds__(C::threads, 1)
                         }
                         see[x] &= v;
                     }
+                    both &= see[x];
                 }
-                uint32_t both = ~0u;
-#pragma unroll
-                for (int x = 0; x < W; ++x) both &= see[x];
                 const bool all = __all_sync(0xffffffffu, both == ~0u || !valid);       // no token to mask in this warp
                 if (!wait_warp(&sh.s_full[i & 1], i >> 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t t_s = t_row + kTmemS + (i & 1) * 128;
-                float f[SG];
+                const uint32_t t_s = t_row + C::t_s + (i & 1) * C::s_cols;
+                float f = 1.f;
+                float2 was = unit;
+                if (some) {
+                    float v[2][32];
+                    tmem_ld32_async(t_s, v[0]);
+                    tmem_ld32_async(t_s + 32, v[1]);
+                    tmem_wait_ld(v[0]);
+                    tmem_wait_ld(v[1]);
+                    const float4 *sc = sh.scales[m];
+                    if (F8) {
 #pragma unroll
-                for (int x = 0; x < SG; ++x) f[x] = 1.f;
-                if (!F8) {
-                    if (some) {
-                        float mx[8];
+                        for (int h = 0; h < 2; ++h) {
+                            if (SG == 2) {
+                                float u[32];
+                                tmem_ld32(t_s + 64 + h * 32, u);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            float v[32];
-                            tmem_ld32(t_s + h * 32, v);
-                            if (all) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) mx[k & 7] = fmaxf(mx[k & 7], v[k]);
+                                for (int k = 0; k < 32; ++k) {
+                                    const float2 s2 = *reinterpret_cast<const float2 *>(sc + (F8 ? h * 32 + k : 0));
+                                    v[h][k] = fmaf(u[k], s2.y, v[h][k] * s2.x);
+                                }
                             } else {
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) mx[k & 7] = fmaxf(mx[k & 7], (see[F8 ? 0 : h] >> k) & 1u ? v[k] : -INFINITY);
+                                for (int k = 0; k < 32; ++k) v[h][k] *= sc[F8 ? h * 32 + k : 0].x;
                             }
                         }
-                        const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                                fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * scale;
-                        if (top > ref[0] + kLazy) {
-                            if (ref[0] != -INFINITY) f[0] = ex2(ref[0] - top);
-                            ref[0] = top;
-                        }
-                        const float at = ref[0] == -INFINITY ? 0.f : ref[0];
-                        l *= f[0];
-                        float ps[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t pk[32];
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                float v[32];
-                                tmem_ld32(t_s + (2 * h + y) * 32, v);
-                                const uint32_t sw = see[F8 ? 0 : 2 * h + y];
-#pragma unroll
-                                for (int k = 0; k < 32; k += 2) {
-                                    float e0 = ex2(fmaf(v[k], scale, -at)), e1 = ex2(fmaf(v[k + 1], scale, -at));
-                                    if (!all) {
-                                        e0 = (sw >> k) & 1u ? e0 : 0.f;
-                                        e1 = (sw >> (k + 1)) & 1u ? e1 : 0.f;
-                                    }
-                                    ps[(k >> 1) & 3] += e0 + e1;
-                                    pk[y * 16 + k / 2] = bf16x2(e0, e1);
-                                }
-                            }
-                            tmem_st32(t_s + h * 32, pk);          // over scores that have been read
-                        }
-                        l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                        unit = sh.top[m];
                     }
-                } else if (some) {
-                    float v[64];
-                    const float4 *sc = sh.scales[m];
+                    if (!all)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float u[32];
-                        tmem_ld32(t_s + h * 32, u);
+                        for (int k = 0; k < 64; ++k) v[k >> 5][k & 31] = (see[k >> 5] >> (k & 31)) & 1u ? v[k >> 5][k & 31] : -INFINITY;
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[h * 32 + k] = u[k] * sc[F8 ? h * 32 + k : 0].x;
+                    for (int k = 0; k < 64; ++k) mx[k & 3] = fmaxf(mx[k & 3], v[k >> 5][k & 31]);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                    if (top > ref + kLazy) {
+                        if (ref != -INFINITY) f = ex2(ref - top);
+                        ref = top;
                     }
-                    if (SG == 2)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float u[32];
-                            tmem_ld32(t_s + 64 + h * 32, u);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) v[h * 32 + k] = fmaf(u[k], sc[F8 ? h * 32 + k : 0].y, v[h * 32 + k]);
-                        }
-                    float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < 64; ++k) {
-                        v[k] *= scale;
-                        if (!all) v[k] = (see[k >> 5] >> (k & 31)) & 1u ? v[k] : -INFINITY;
-                        // a V scale below 2^-100, or that is not a number, counts as 2^-100 here: the maximum is finite whenever a score is
-                        top[0] = fmaxf(top[0], v[k] + fmaxf(sc[F8 ? k : 0].z, -100.f));
-                        if (SG == 2) top[1] = fmaxf(top[1], v[k] + fmaxf(sc[F8 ? k : 0].w, -100.f));
-                    }
-                    float at[2];
-#pragma unroll
-                    for (int x = 0; x < SG; ++x) {
-                        if (top[x] > ref[x] + (15.f - C::raise)) {
-                            if (ref[x] != -INFINITY) f[x] = ex2(ref[x] - top[x]);
-                            ref[x] = top[x];
-                        }
-                        at[x] = (ref[x] == -INFINITY ? 0.f : ref[x]) - C::raise;
-                    }
-                    l *= f[0];
+                    const float at = ref == -INFINITY ? 0.f : ref;
+                    l *= f;
                     float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int x = 0; x < SG; ++x) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int k = 0; k < 64; k += 2) {
-                            float e[2];
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const float u = v[k + y] - at[x], lv = x == 0 ? sc[F8 ? k + y : 0].z : sc[F8 ? k + y : 0].w;
-                                if (x == 0) ps[(k >> 1) & 3] += ex2(u);
-                                e[y] = ex2(u + lv);
-                                if (!all) e[y] = v[k + y] == -INFINITY ? 0.f : e[y];       // whatever its scale is
-                            }
-                            pk[k / 2] = f16x2(e[0], e[1]);
-                        }
-                        tmem_st32(t_s + x * 32, pk);
+                    for (int k = 0; k < 64; ++k) {
+                        float &x = v[k >> 5][k & 31];
+                        x = ex2(fmaf(x, scale, -at));
+                        ps[k & 3] += x;
                     }
-                    l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) * 0x1p-8f;
-                    static_assert(!F8 || C::raise == 8.f, "the sum is relative to the maximum");
-                }
-                bool grew = false;
+                    l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                    uint32_t pk[32];
+                    if (!F8) {
 #pragma unroll
-                for (int x = 0; x < SG; ++x) grew |= f[x] != 1.f;
-                if (c > 0 && __any_sync(0xffffffffu, grew)) {          // O follows, once the product before it is done
+                        for (int k = 0; k < 32; ++k) pk[k] = bf16x2(v[k >> 4][2 * k & 31], v[k >> 4][(2 * k & 31) + 1]);
+                        tmem_st32(t_s, pk);               // over scores that have been read
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < SG; ++x) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const int z = F8 ? 2 * k : 0;
+                                const float e0 = v[k >> 4][2 * k & 31], e1 = v[k >> 4][(2 * k & 31) + 1];
+                                float w0 = e0 * (x ? sc[z].w : sc[z].z), w1 = e1 * (x ? sc[F8 ? z + 1 : 0].w : sc[F8 ? z + 1 : 0].z);
+                                if (!all) {               // whatever a masked token's scale is
+                                    w0 = (see[k >> 4] >> (2 * k & 31)) & 1u ? w0 : 0.f;
+                                    w1 = (see[k >> 4] >> ((2 * k & 31) + 1)) & 1u ? w1 : 0.f;
+                                }
+                                pk[k] = f16x2(w0, w1);
+                            }
+                            tmem_st32(t_s + x * 32, pk);
+                        }
+                    }
+                }
+                const bool turned = F8 && (was.x != unit.x || was.y != unit.y);
+                if (c > 0 && __any_sync(0xffffffffu, f != 1.f || turned)) {       // O follows, once the product before it is done
                     if (!wait_warp(&sh.pv_done[(i - 1) & 1], (i - 1) >> 1)) {
                         ok = false;
                         break;
@@ -1028,7 +932,7 @@ __global__ void __launch_bounds__(C::threads, 1)
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         float v[32];
-                        const float by = f[SG == 2 ? c0 / 128 : 0];
+                        const float by = !F8 ? f : c0 < 128 ? f * (was.x / unit.x) : f * (was.y / unit.y);
                         tmem_ld32(t_o + c0, v);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] *= by;
@@ -1037,6 +941,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                 }
                 tc_fence_before();
                 mbar_arrive(smem_u32(&sh.p_full[i & 1]));
+                __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.meta_empty[m]));
             }
             if (!ok) break;
@@ -1045,20 +950,12 @@ __global__ void __launch_bounds__(C::threads, 1)
             if (!wait_warp(&sh.pv_done[i & 1], i >> 1) || !wait_warp(&sh.flags_full, seg)) break;
             tc_fence_after();
             const bool whole = g.begins && g.ends;
-            const float lse2 = l == 0.f ? -INFINITY : ref[0] + log2f(l);
-            float by[SG];
-#pragma unroll
-            for (int x = 0; x < SG; ++x)
-                by[x] = l == 0.f ? 0.f : F8 ? ex2(ref[x] - C::raise - lse2) : whole ? 1.f / l : 1.f;
+            const float by = l == 0.f ? 0.f : (whole ? 1.f / l : 1.f) * (F8 ? 1.f / (1 << (int)kRaise) : 1.f);
             // values that are not finite, of attended tokens that not every row attends
-            uint32_t odd[2][4];
             bool strange = false;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                odd[0][x] = valid ? sh.odd[0][x] & sh.kin[min(node, QSA_MAX_DRAFT - 1)][x] : 0u;
-                odd[1][x] = valid ? sh.odd[1][x] : 0u;
-                strange |= (odd[0][x] | odd[1][x]) != 0u;
-            }
+            for (int x = 0; x < 4; ++x)
+                strange |= valid && ((sh.odd[0][x] & sh.kin[min(node, QSA_MAX_DRAFT - 1)][x]) | sh.odd[1][x]) != 0u;
             const int64_t at = (int64_t)(2 * range + (g.begins ? 1 : 0)) * a.Hkv * plan.m_tiles + kvh * plan.m_tiles + m_tile;
             float *po = ws.o + (at * kRows + row) * D;
             uint16_t *dst = a.out + ((int64_t)(g.r.off + min(node, g.r.T - 1)) * a.Hq + head) * D;
@@ -1066,10 +963,11 @@ __global__ void __launch_bounds__(C::threads, 1)
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     float v[32];
+                    const float times = !F8 ? by : by * (c0 < 128 ? unit.x : unit.y);
                     __syncwarp();
                     tmem_ld32(t_o + c0, v);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : v[k] * by[SG == 2 ? c0 / 128 : 0];
+                    for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : v[k] * times;
                     if (strange) {
 #pragma unroll 1
                         for (int x = 0; x < 2 * QSA_MAX_DRAFT; ++x) {
@@ -1104,9 +1002,9 @@ __global__ void __launch_bounds__(C::threads, 1)
                 }
                 if (valid) {
                     if (!whole)
-                        ws.ml[at * kRows + row] = F8 ? make_float2(lse2, l == 0.f ? 0.f : 1.f) : make_float2(ref[0], l);
+                        ws.ml[at * kRows + row] = make_float2(ref, l);
                     else if (a.lse)
-                        a.lse[(int64_t)(g.r.off + node) * a.Hq + head] = lse2 * kLn2;
+                        a.lse[(int64_t)(g.r.off + node) * a.Hq + head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
                 }
             }
             tc_fence_before();
@@ -1251,17 +1149,16 @@ cudaError_t launch(const TreeArgs &a, cudaStream_t st) {
     plan.min_tiles = 2;
     plan.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     // tiled loads of runs of a page; below 16 tokens the engine's cost for each box outweighs the copies of the worker warps
-    const int run = std::min(a.page_size & -a.page_size, C::T);
+    const int run = std::min(a.page_size & -a.page_size, kTile);
     TreeMaps maps;
     memset(&maps, 0, sizeof(maps));
     const int64_t rows = a.n_pages * a.page_size;
     if (run >= 16 && rows > 0) {
-        plan.k_run = run;
-        plan.v_run = std::min(run, C::VT);
-        const uint64_t row = (uint64_t)a.Hkv * D * (F8 ? 1 : 2), blocks = row / 128;
-        const uint32_t whole = !F8 && plan.v_run == C::VT ? D / 64 : 1;
-        if (!encode_tmap_rows(&maps.k, a.k, F8, rows, blocks, row, plan.k_run, 1) ||
-            !encode_tmap_rows(&maps.v, a.v, F8, rows, blocks, row, plan.v_run, whole))
+        plan.run = run;
+        const uint64_t row = (uint64_t)a.Hkv * D * (F8 ? 1 : 2);
+        const uint32_t blocks = !F8 && run == kTile ? C::SD / 64 : 1;
+        if (!encode_tmap_rows(&maps.k, a.k, F8, rows, row / 128, row, run, blocks) ||
+            !encode_tmap_rows(&maps.v, a.v, F8, rows, row / 128, row, run, blocks))
             return cudaErrorInvalidValue;
     }
     const TreeScratch ws = tree_scratch(a.scratch, D, a.Hkv, plan.m_tiles);
