@@ -51,20 +51,24 @@ template <int D_, bool F8_>
 struct TreeCfg {
     static constexpr int D = D_;
     static constexpr bool F8 = F8_;
-    static constexpr int SD = D < 128 ? D : 128, SL = D / SD;   // dims of a slot; slots of a tile's K, and of its V
+    static constexpr int SD = F8 ? 128 : D, SL = D / SD;   // dims of a slot; slots of a tile's K, and of its V
     static constexpr int SG = F8 ? D / 128 : 1;                 // scales of a row, sets of weights
     static constexpr int slot = kTile * SD * 2, code_slot = F8 ? kTile * SD : 0;    // bytes
-    static constexpr int ring = F8 ? 4 : 212992 / slot;
+    static constexpr int ring = F8 ? 4 : D == 64 ? 24 : 212992 / slot;
     static constexpr int codes = F8 ? (D == 256 ? 10 : 12) : 0;
     static constexpr int from = F8 ? codes : ring;              // slots that global memory is read into
     static constexpr int ring_at = F8 ? kRows * D * 2 : 0, codes_at = ring_at + ring * slot;
     static constexpr int smem = codes_at + codes * code_slot + 1024;
     static_assert(smem + 12288 <= 227 * 1024, "shared memory of a CTA");
-    // tensor memory columns: O, the queries (bf16 rows; with FP8 rows they are in shared memory), two buffers of scores
-    static constexpr uint32_t t_o = 0, t_q = D, t_s = F8 ? 256 : 384, s_cols = F8 ? 128 : 64;
-    static constexpr int softmax = 128, q_threads = F8 ? 64 : 128, workers = F8 ? 256 : 192;
-    static constexpr int mma_warp = 4, index_warp = 5, q_warp = 6, work_warp = q_warp + q_threads / 32;
-    static constexpr int threads = softmax + 64 + q_threads + workers;
+    // tensor memory columns: O, the queries (bf16 rows; with FP8 rows they are in shared memory), buffers of scores
+    static constexpr uint32_t t_o = 0, t_q = D, t_s = D == 256 && !F8 ? 384 : 256, s_cols = SG * kTile;
+    static constexpr int buffers = (512 - t_s) / s_cols;
+    // 16 warps of 128 registers; the query warps' numbers modulo 4 are the four quarters of tensor memory's lanes
+    static constexpr int softmax = 128, q_threads = F8 ? 64 : 128, workers = F8 ? 192 : 160;
+    static constexpr int s_warp = 4, o_warp = 5, index_warp = 6, q_warp = 7, load_warp = q_warp + q_threads / 32;
+    static constexpr int work_warp = F8 ? load_warp + 1 : load_warp;
+    static constexpr int threads = 512;
+    static_assert(work_warp * 32 + workers == threads, "roles");
 };
 
 struct TreeMaps {
@@ -119,7 +123,7 @@ struct Seg {
 struct Walk {
     long long x, x1;
     int s, skip, high, i = 0;
-    __device__ __forceinline__ bool next(const TreeArgs &a, int m_tile, Seg &g) {
+    __device__ __noinline__ bool next(const TreeArgs &a, int m_tile, Seg &g) {
         while (x < x1) {
             g.r = tree_row(a, s, high);
             const int n = g.r.t1 - g.r.t0;
@@ -157,7 +161,7 @@ template <typename C>
 struct TreeShared {
     uint64_t full[C::ring], empty[C::ring];
     uint64_t c_full[C::F8 ? C::codes : 1], c_empty[C::F8 ? C::codes : 1];
-    uint64_t s_full[2], p_full[2], pv_done[2], meta_full[kMetas], meta_empty[kMetas];
+    uint64_t s_full[C::buffers], p_full[C::buffers], pv_done[C::buffers], meta_full[kMetas], meta_empty[kMetas];
     uint64_t to_clean, clean, q_full, q_free, nodes_full, nodes_free, flags_full, o_free;
     uint32_t kin[QSA_MAX_DRAFT][QSA_MAX_DRAFT / 32];      // of each drafted token: itself and its ancestors inside the window
     int lo[QSA_MAX_DRAFT];                                // its first attended place
@@ -165,10 +169,9 @@ struct TreeShared {
     float q_scale[2][C::F8 ? kRows : 1];               // of every other segment
     int slots[kMetas][kTile];
     uint32_t real[kMetas][kTile / 32];                     // bit: the token's page exists
-    float4 scales[kMetas][C::F8 ? kTile : 1];             // K scales of 128 dims each, V scales
+    float4 k_scales[kMetas][C::SG][C::F8 ? kTile / 4 : 1], v_scales[kMetas][C::SG][C::F8 ? kTile / 4 : 1];   // four tokens each
     float2 top[kMetas];                                   // powers of two at most 2 below the tile's largest V scales
     uint32_t tmem;
-    volatile int abort;
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
@@ -202,10 +205,62 @@ __device__ __forceinline__ bool drop_nan_codes(uint32_t &w) {
     return nan != 0;
 }
 
+// Wait for phase `parity` of an mbarrier, a bounded number of times: false, and recorded, if in vain. Each try may suspend
+// the thread for kHintNs. Out of line: with the waits and the walks inlined the kernel had 256 KB of instructions, and its
+// roles, each on a part of its own, waited for them more than for anything else.
+constexpr uint32_t kHintNs = 1000000;
+constexpr int kTries = 1 << 20;
+__device__ __forceinline__ bool try_turn(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(kHintNs)
+        : "memory");
+    return done != 0;
+}
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, WsHeader *hdr) {
+#pragma unroll 1
+    for (int i = 0; i < kTries; ++i)
+        if (try_turn(bar, parity)) return true;
+    record_error(hdr, QSA_ERR_DEVICE_TIMEOUT, kWhereTree, blockIdx.x);
+    return false;
+}
+__device__ __forceinline__ bool wait_turn(uint32_t bar, uint32_t parity, WsHeader *hdr) {
+    return try_turn(bar, parity) || wait_long(bar, parity, hdr);
+}
+
+// Values that are not finite, of tokens that this row attends but not every row: added to its result (whole) or its partial.
+template <int D, bool F8>
+__device__ __noinline__ void add_odd(const TreeArgs &a, const Seg &g, const uint32_t (*odd)[QSA_MAX_DRAFT / 32], const uint32_t *kin,
+                                     int lo, int kvh, bool whole, uint16_t *dst, float *po) {
+#pragma unroll 1
+    for (int x = 0; x < 2 * QSA_MAX_DRAFT; ++x) {
+        const int y = x % QSA_MAX_DRAFT, j = (x == y ? g.r.base : g.r.lo) + y;
+        if (!(odd[x / QSA_MAX_DRAFT][y >> 5] >> (y & 31) & 1u)) continue;
+        if (x == y ? !(kin[y >> 5] >> (y & 31) & 1u) : j < lo || j >= g.r.base) continue;
+        const int page = a.table[g.s * a.ld + j / a.page_size];
+        if ((uint32_t)page >= (uint32_t)a.n_pages) continue;
+        const int64_t row = (((int64_t)page * a.page_size + j % a.page_size) * a.Hkv + kvh) * D;
+#pragma unroll 1
+        for (int d = 0; d < D; ++d) {
+            const float z = F8 ? ((static_cast<const uint8_t *>(a.v)[row + d] & 0x7Fu) == 0x7Fu ? NAN : 0.f)
+                               : bf16_bits_to_float(static_cast<const uint16_t *>(a.v)[row + d]);
+            if (isfinite(z)) continue;
+            if (whole)
+                dst[d] = float_to_bf16_bits(bf16_bits_to_float(dst[d]) + z);
+            else
+                po[d] += z;
+        }
+    }
+}
+
 template <typename C>
 __global__ void __launch_bounds__(C::threads, 1)
     tree_tile_kernel(TreeArgs a, TreePlan plan, TreeScratch ws, const __grid_constant__ TreeMaps maps) {
-    constexpr int D = C::D, T = kTile, SD = C::SD, SL = C::SL, RING = C::ring, SG = C::SG;
+    constexpr int D = C::D, T = kTile, SD = C::SD, SL = C::SL, RING = C::ring, SG = C::SG, NB = C::buffers;
     constexpr bool F8 = C::F8;
     extern __shared__ uint8_t smem_raw[];
     __shared__ TreeShared<C> sh;
@@ -218,7 +273,7 @@ __global__ void __launch_bounds__(C::threads, 1)
     const bool speaks = kvh == 0 && m_tile == 0;          // records errors that all CTAs of a range see
     const bool tiled = plan.run > 0;
 
-    if (warp == C::mma_warp) tmem_alloc(&sh.tmem, 512);
+    if (warp == C::s_warp) tmem_alloc(&sh.tmem, 512);
     if (tid == 0) {
         // the loads' arrivals: one with the bytes it expects, or every worker's
         const int load = tiled ? 1 : C::workers;
@@ -231,14 +286,14 @@ __global__ void __launch_bounds__(C::threads, 1)
                 mbar_init(smem_u32(&sh.c_full[i]), load);
                 mbar_init(smem_u32(&sh.c_empty[i]), C::workers / 32);
             }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::buffers; ++i) {
             mbar_init(smem_u32(&sh.s_full[i]), 1);
             mbar_init(smem_u32(&sh.p_full[i]), C::softmax);
             mbar_init(smem_u32(&sh.pv_done[i]), 1);
         }
         for (int i = 0; i < kMetas; ++i) {
             mbar_init(smem_u32(&sh.meta_full[i]), 1);
-            mbar_init(smem_u32(&sh.meta_empty[i]), C::softmax / 32 + (tiled ? 0 : C::workers / 32));
+            mbar_init(smem_u32(&sh.meta_empty[i]), C::softmax / 32 + (tiled ? 1 : C::workers / 32));
         }
         mbar_init(smem_u32(&sh.to_clean), 1);
         mbar_init(smem_u32(&sh.clean), C::q_threads);
@@ -249,7 +304,6 @@ __global__ void __launch_bounds__(C::threads, 1)
         mbar_init(smem_u32(&sh.flags_full), C::q_threads);
         mbar_init(smem_u32(&sh.o_free), C::softmax);
         fence_mbar_init();
-        sh.abort = 0;
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
     }
@@ -337,28 +391,19 @@ __global__ void __launch_bounds__(C::threads, 1)
     }
     const uint32_t tmem = sh.tmem;
 
-    auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
-        if (mbar_wait_bounded(smem_u32(bar), phase & 1u, kWaitLimitNs)) return true;
-        record_error(a.hdr, QSA_ERR_DEVICE_TIMEOUT, kWhereTree, blockIdx.x);
-        sh.abort = 1;
-        return false;
-    };
-    // a warp's wait: it goes on only if all its lanes saw the phase and no role has given up
-    auto wait_warp = [&](uint64_t *bar, uint32_t phase) -> bool {
-        const bool w = wait(bar, phase);
-        return __all_sync(0xffffffffu, w) && !__any_sync(0xffffffffu, sh.abort != 0);
-    };
+    // A role that waits in vain ends; the roles that depend on it then do the same.
+    auto wait = [&](uint64_t *bar, uint32_t phase) -> bool { return wait_turn(smem_u32(bar), phase & 1u, a.hdr); };
+    auto wait_warp = [&](uint64_t *bar, uint32_t phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
 
     Seg g{};
     if (warp == C::index_warp) {
         // ================================================================ slots of each tile; TMA loads
         constexpr int E = T / 32;                         // tokens of a lane, neighbours
-        constexpr int blocks = F8 ? 1 : SD / 64;          // 128-byte blocks of a slot's rows
-        const int rows_end = (int)min((int64_t)INT32_MAX, a.n_pages * a.page_size);       // a row that does not exist: zeros
         int page[E], offset[E];
         bool ok = true;
+        int pages_begin = 0, pages_end = 0;               // entries that g needs
+        auto enter = [&]() { pages_end = (g.r.len - 1) / a.page_size, pages_begin = g.r.lo / a.page_size; };
         auto fetch = [&](int t) {                         // the page table's entries for tile t of g
-            const int pages_end = (g.r.len - 1) / a.page_size, pages_begin = g.r.lo / a.page_size;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const uint32_t j = (uint32_t)t * T + lane * E + e;      // may pass 2^31
@@ -368,32 +413,13 @@ __global__ void __launch_bounds__(C::threads, 1)
                 page[e] = some ? a.table[g.s * a.ld + entry] : -2;
             }
         };
-        int asked = 0;                                    // ring slots asked for
-        int slot_v[E];                                    // slots of the tile whose V comes next
-        const int boxes = tiled ? T / plan.run : 1, whole = boxes == 1 ? 1 : blocks;
-        auto load = [&](const void *map, const int (&slot)[E], int q0) -> bool {      // one tile's K or V into ring slots q0 ...
-            const int run = lane % boxes, block = lane / boxes;
-            const int y = __shfl_sync(0xffffffffu, slot[0], run * (T / E / boxes));
-            for (int k = 0; k < SL; ++k) {
-                const int q = q0 + k, at = q % C::from, turn = q / C::from;
-                uint64_t *full = F8 ? &sh.c_full[F8 ? at : 0] : &sh.full[F8 ? 0 : at];
-                if (turn > 0 && !wait_warp(F8 ? &sh.c_empty[F8 ? at : 0] : &sh.empty[F8 ? 0 : at], turn - 1)) return false;
-                asked = q + 1;
-                if (lane == 0) mbar_arrive_expect_tx(smem_u32(full), F8 ? C::code_slot : C::slot);
-                __syncwarp();
-                if (block < whole)
-                    tma_load_3d((F8 ? codes_at + at * C::code_slot : ring_at + at * C::slot) + block * (T * 128) + run * plan.run * 128,
-                                map, 0, y < 0 ? rows_end : y, (kvh * SL + k) * blocks + block, smem_u32(full));
-            }
-            return true;
-        };
         Walk w = walk;
         int done = 0;
         bool more = w.next(a, m_tile, g);
-        if (more) fetch(g.ta);
+        if (more) enter(), fetch(g.ta);
         while (more && ok) {
             const Seg now = g;
-            const int n = now.tb - now.ta, turn0 = 2 * now.i0;
+            const int n = now.tb - now.ta;
             float2 top = make_float2(0.f, 0.f);           // FP8: powers of two next to the largest V scales of the segment so far
             for (int c = 0; c < n && ok; ++c, ++done) {
                 int slot[E];
@@ -427,7 +453,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                     fetch(t + 1);
                 } else {
                     more = w.next(a, m_tile, g);
-                    if (more) fetch(g.ta);
+                    if (more) enter(), fetch(g.ta);
                 }
                 const int m = done % kMetas;
                 if (done >= kMetas && !wait_warp(&sh.meta_empty[m], done / kMetas - 1)) {
@@ -438,7 +464,7 @@ __global__ void __launch_bounds__(C::threads, 1)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     bits |= (exists[e] ? 1u : 0u) << ((lane * E + e) & 31);
-                    if (!tiled) sh.slots[m][lane * E + e] = exists[e] ? slot[e] : -1;
+                    sh.slots[m][lane * E + e] = exists[e] || tiled ? slot[e] : -1;        // a box may begin before the first token
                 }
 #pragma unroll
                 for (int o = 1; o < 32 / E; o <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
@@ -462,40 +488,49 @@ __global__ void __launch_bounds__(C::threads, 1)
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
                         const float4 x = scale[e];        // infinite V scales become NaN
-                        sh.scales[m][F8 ? lane * E + e : 0] = make_float4(x.x, x.y, fmaf(x.z, 0.f, x.z) * cx, fmaf(x.w, 0.f, x.w) * cy);
+                        float *ks = reinterpret_cast<float *>(sh.k_scales[m]), *vs = reinterpret_cast<float *>(sh.v_scales[m]);
+                        const int tok = F8 ? lane * E + e : 0;
+                        ks[tok] = x.x, vs[tok] = fmaf(x.z, 0.f, x.z) * cx;
+                        if (SG == 2) ks[T + tok] = x.y, vs[T + tok] = fmaf(x.w, 0.f, x.w) * cy;
                     }
                     if (lane == 0) sh.top[m] = top;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.meta_full[m]));
-                if (tiled) {
-                    ok = load(&maps.k, slot, (turn0 + k_turn(c)) * SL);
-                    if (ok && c > 0) ok = load(&maps.v, slot_v, (turn0 + v_turn(c - 1, n)) * SL);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) slot_v[e] = slot[e];
-                    if (ok && c + 1 == n) ok = load(&maps.v, slot_v, (turn0 + v_turn(c, n)) * SL);
-                }
             }
         }
-        // no load may still be writing shared memory when the CTA ends (bounded waits; they are over unless a role gave up)
-        for (int q = max(0, asked - C::from); q < asked; ++q)
-            mbar_wait_bounded(smem_u32(F8 ? &sh.c_full[F8 ? q % C::from : 0] : &sh.full[F8 ? 0 : q % C::from]),
-                              (uint32_t)(q / C::from) & 1u, kWaitLimitNs);
-    } else if (warp >= C::work_warp) {
-        // ================================================================ workers: cp.async loads; codes -> f16
+    } else if (warp >= C::load_warp) {
+        // ================================================================ loads; codes -> f16
         const int wt = tid - C::work_warp * 32;
         constexpr int row_chunks = F8 ? SD / 16 : SD / 8;     // 16-byte chunks of a token's row in a slot
         const char *rows[2] = {static_cast<const char *>(a.k) + (int64_t)kvh * SL * row_chunks * 16,
                                static_cast<const char *>(a.v) + (int64_t)kvh * SL * row_chunks * 16};
         const int64_t pitch = (int64_t)a.Hkv * SL * row_chunks * 16;
+        // TMA: a box is a run of a page; a row that does not exist reads as zeros
+        constexpr int blocks = F8 ? 1 : SD / 64;              // 128-byte blocks of a slot's rows
+        const int rows_end = (int)min((int64_t)INT32_MAX, a.n_pages * a.page_size);
+        const int boxes = tiled ? T / plan.run : 1, whole = boxes == 1 ? 1 : blocks, run = lane % boxes, block = lane / boxes;
+        int asked = 0;                                        // slots asked for
         // a tile's K or V into the slots of turn q0 ...
         auto copy = [&](int is_v, int tile, int q0) -> bool {
             const int m = tile % kMetas;
             if (!is_v && !wait_warp(&sh.meta_full[m], tile / kMetas)) return false;
+            const int box = sh.slots[m][tiled ? run * plan.run : 0], y = box < 0 ? rows_end : box;
+#pragma unroll 1
             for (int k = 0; k < SL; ++k) {
                 const int q = q0 + k, at = q % C::from, turn = q / C::from;
                 if (turn > 0 && !wait_warp(F8 ? &sh.c_empty[F8 ? at : 0] : &sh.empty[F8 ? 0 : at], turn - 1)) return false;
                 const uint32_t dst = F8 ? codes_at + at * C::code_slot : ring_at + at * C::slot;
+                if (tiled) {
+                    const uint32_t full = smem_u32(F8 ? &sh.c_full[F8 ? at : 0] : &sh.full[F8 ? 0 : at]);
+                    asked = q + 1;
+                    if (lane == 0) mbar_arrive_expect_tx(full, F8 ? C::code_slot : C::slot);
+                    __syncwarp();
+                    if (block < whole)
+                        tma_load_3d(dst + block * (T * 128) + run * plan.run * 128, is_v ? &maps.v : &maps.k, 0, y,
+                                    (kvh * SL + k) * blocks + block, full);
+                    continue;
+                }
 #pragma unroll
                 for (int i = 0; i < (T * row_chunks + C::workers - 1) / C::workers; ++i) {
                     const int id = i * C::workers + wt, tok = id / row_chunks, gr = id % row_chunks;
@@ -516,7 +551,8 @@ __global__ void __launch_bounds__(C::threads, 1)
         Walk wc = walk;
         Seg gc{};
         int cc = 0, nc = 0;
-        bool more = !tiled && wc.next(a, m_tile, gc);
+        const bool loads = tiled ? warp == C::load_warp : warp >= C::work_warp;
+        bool more = loads && wc.next(a, m_tile, gc);
         if (more) nc = 2 * (gc.tb - gc.ta);
         auto turn_is_v = [](int c, int turns) { return c == turns - 1 || (c > 0 && (c & 1) == 0); };
         auto turn_tile = [&](int c, int turns) { return c == 0 ? 0 : c == turns - 1 ? turns / 2 - 1 : turn_is_v(c, turns) ? c / 2 - 1 : (c + 1) / 2; };
@@ -531,9 +567,13 @@ __global__ void __launch_bounds__(C::threads, 1)
             return true;
         };
         bool ok = true;
-        if constexpr (!F8) {
+        if (!F8 || warp == C::load_warp) {
+#pragma unroll 1
             while (ok && more) ok = ask();
-        } else {
+            // no load may still be writing shared memory when the CTA ends (bounded waits; they are over unless a role gave up)
+            for (int q = max(0, asked - C::from); q < asked; ++q)
+                wait_turn(smem_u32(F8 ? &sh.c_full[F8 ? q % C::from : 0] : &sh.full[F8 ? 0 : q % C::from]), (uint32_t)(q / C::from) & 1u, a.hdr);
+        } else if constexpr (F8) {
             // codes of a turn are asked for `ahead` turns before it is converted. At most 6: a tile's K is asked for when the
             // softmax has left the tile four before it, which needs the V turns up to seven before this one converted.
             constexpr int ahead = C::codes / SL - 1 < 6 ? C::codes / SL - 1 : 6;
@@ -545,8 +585,9 @@ __global__ void __launch_bounds__(C::threads, 1)
                     if (!wait_warp(&sh.c_full[from], q / C::codes)) return false;
                     if (q >= RING && !wait_warp(&sh.empty[to], q / RING - 1)) return false;
 #pragma unroll
-                    for (int i = 0; i < T * row_chunks / C::workers; ++i) {
+                    for (int i = 0; i < (T * row_chunks + C::workers - 1) / C::workers; ++i) {
                         const int id = i * C::workers + wt, tok = id / row_chunks, gr = id % row_chunks;
+                        if (tok >= T) break;
                         uint4 v = *reinterpret_cast<const uint4 *>(sm + C::codes_at + from * C::code_slot + swz(tok, gr));
                         if (is_v && some) {
                             const int j = j0 + tok;
@@ -581,7 +622,7 @@ __global__ void __launch_bounds__(C::threads, 1)
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp >= C::q_warp && warp < C::work_warp) {
+    } else if (warp >= C::q_warp) {
         // ================================================================ queries, ancestors, clean V rows
         const int qt = tid - C::q_warp * 32;
         Walk w = walk;
@@ -673,7 +714,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                 const int t = g.ta + c;
                 if (!masked(a, g.r, t)) continue;
                 if (!F8) {
-                    // the MMA warp says when the rows are in: it meets every turn of the ring, and a wait tells only two from each other
+                    // the output warp says when the rows are in: it meets every turn of its slots, and a wait tells only two from each other
                     if (!wait_warp(&sh.to_clean, cleaned)) {
                         ok = false;
                         break;
@@ -716,84 +757,95 @@ __global__ void __launch_bounds__(C::threads, 1)
             mbar_arrive(smem_u32(&sh.flags_full));
             ++seg;
         }
-    } else if (warp == C::mma_warp) {
-        // ================================================================ products
+    } else if (warp == C::s_warp) {
+        // ================================================================ scores
         if (lane == 0) {
             Walk w = walk;
-            uint64_t *last_bar = nullptr;                 // the barrier of the last commit, and its phase
-            uint32_t last_phase = 0;
-            int seg = 0, cleaned = 0;
+            int seg = 0, i = 0;
             bool ok = true;
-            auto scores = [&](int i, int q0, bool first, bool last) -> bool {
-                const uint32_t s_at = tmem + C::t_s + (i & 1) * C::s_cols;
-                if (first && !wait(&sh.q_full, seg)) return false;
-                for (int k = 0; k < SL; ++k) {
-                    const int q = q0 + k, at = q % RING;
-                    if (!wait(&sh.full[at], q / RING)) return false;
-                    fence_proxy_async_smem();
-                    tc_fence_after();
-                    const uint32_t b = ring_at + at * C::slot;
-#pragma unroll
-                    for (int z = 0; z < SD / 16; ++z) {
-                        const uint64_t bd = tc_desc(b + z / 4 * (T * 128) + (z & 3) * 32, 16, 1024);
-                        if (!F8)
-                            tc_mma_ta(s_at, tmem + C::t_q + (k * (SD / 16) + z) * 8, bd, tc_idesc(kRows, T, 0), k > 0 || z > 0);
-                        else
-                            tc_mma(s_at + k * T, tc_desc(q_at + (2 * k + z / 4) * (kRows * 128) + (z & 3) * 32, 16, 1024), bd,
-                                   f16_idesc(T, 0), z > 0);
-                    }
-                    tc_commit(smem_u32(&sh.empty[at]));
-                }
-                tc_commit(smem_u32(&sh.s_full[i & 1]));
-                last_bar = &sh.s_full[i & 1], last_phase = i >> 1;
-                if (last) tc_commit(smem_u32(&sh.q_free));
-                return true;
-            };
-            while (ok && w.next(a, m_tile, g)) {
-                const int n = g.tb - g.ta, turn0 = 2 * g.i0;
-                ok = scores(g.i0, turn0 * SL, true, n == 1);
-                for (int c = 0; c < n && ok; ++c) {
-                    const int i = g.i0 + c;
-                    if (c + 1 < n && !scores(i + 1, (turn0 + k_turn(c + 1)) * SL, false, c + 2 == n)) {
+            for (; ok && w.next(a, m_tile, g); ++seg) {
+                const int n = g.tb - g.ta;
+                if (!wait(&sh.q_full, seg)) break;
+                for (int c = 0; c < n && ok; ++c, ++i) {
+                    // the buffer's last weights are used up
+                    if (i >= NB && !wait(&sh.pv_done[i % NB], i / NB - 1)) {
                         ok = false;
                         break;
                     }
-                    // ---- O (+)= P V
-                    const int q0 = (turn0 + v_turn(c, n)) * SL;
+                    const uint32_t s_at = tmem + C::t_s + (i % NB) * C::s_cols;
+                    for (int k = 0; k < SL; ++k) {
+                        const int q = (2 * g.i0 + k_turn(c)) * SL + k, at = q % RING;
+                        if (!wait(&sh.full[at], q / RING)) {
+                            ok = false;
+                            break;
+                        }
+                        if (!F8 && !tiled) fence_proxy_async_smem();      // rows by cp.async; TMA needs none, the conversion has its own
+                        tc_fence_after();
+                        const uint32_t b = ring_at + at * C::slot;
+                        const uint64_t bd = tc_desc(b, 16, 1024);
+                        const uint32_t q_row = q_at + 2 * k * (kRows * 128);
+#pragma unroll
+                        for (int z = 0; z < SD / 16; ++z) {       // 16 dims: 32 bytes on, or in the next block of 64
+                            const uint64_t zd = bd + (z >> 2) * (T * 128 / 16) + (z & 3) * 2;
+                            if (!F8)
+                                tc_mma_ta(s_at, tmem + C::t_q + z * 8, zd, tc_idesc(kRows, T, 0), z > 0);
+                            else
+                                tc_mma(s_at + k * T, tc_desc(q_row + (z >> 2) * (kRows * 128) + (z & 3) * 32, 16, 1024), zd, f16_idesc(T, 0),
+                                       z > 0);
+                        }
+                        tc_commit(smem_u32(&sh.empty[at]));
+                    }
+                    if (!ok) break;
+                    tc_commit(smem_u32(&sh.s_full[i % NB]));
+                    if (c + 1 == n) tc_commit(smem_u32(&sh.q_free));
+                }
+            }
+            // the last commit covers every product issued: wait for it before tensor memory is freed
+            if (i > 0) wait_turn(smem_u32(&sh.s_full[(i - 1) % NB]), (uint32_t)((i - 1) / NB) & 1u, a.hdr);
+        }
+    } else if (warp == C::o_warp) {
+        // ================================================================ O (+)= P V
+        if (lane == 0) {
+            Walk w = walk;
+            int seg = 0, cleaned = 0, i = 0;
+            bool ok = true;
+            for (; ok && w.next(a, m_tile, g); ++seg) {
+                const int n = g.tb - g.ta;
+                for (int c = 0; c < n && ok; ++c, ++i) {
+                    const int q0 = (2 * g.i0 + v_turn(c, n)) * SL;
                     const bool part = !F8 && masked(a, g.r, g.ta + c);
                     if (part) {
                         for (int k = 0; k < SL && ok; ++k) ok = wait(&sh.full[(q0 + k) % RING], (q0 + k) / RING);
                         mbar_arrive(smem_u32(&sh.to_clean));
                     }
-                    if (!ok || !wait(&sh.p_full[i & 1], i >> 1) || (c == 0 && seg > 0 && !wait(&sh.o_free, seg - 1)) ||
+                    if (!ok || !wait(&sh.p_full[i % NB], i / NB) || (c == 0 && seg > 0 && !wait(&sh.o_free, seg - 1)) ||
                         (part && !wait(&sh.clean, cleaned++))) {
                         ok = false;
                         break;
                     }
-                    const uint32_t p_at = tmem + C::t_s + (i & 1) * C::s_cols;
+                    const uint32_t p_at = tmem + C::t_s + (i % NB) * C::s_cols;
                     for (int k = 0; k < SL; ++k) {
                         const int q = q0 + k, at = q % RING;
                         if (!wait(&sh.full[at], q / RING)) {
                             ok = false;
                             break;
                         }
-                        fence_proxy_async_smem();
+                        if (!F8 && !tiled) fence_proxy_async_smem();
                         tc_fence_after();
                         const uint32_t b = ring_at + at * C::slot;
+                        const uint64_t bd = tc_desc(b, T * 128, 1024);
+                        const uint32_t p_set = p_at + (F8 ? k * (T / 2) : 0);
 #pragma unroll
-                        for (int z = 0; z < T / 16; ++z)
-                            tc_mma_ta(tmem + C::t_o + k * SD, p_at + (F8 ? k * (T / 2) : 0) + z * 8, tc_desc(b + z * 2048, T * 128, 1024),
-                                      F8 ? f16_idesc(SD, 1) : tc_idesc(kRows, SD, 1), c > 0 || z > 0);
+                        for (int z = 0; z < T / 16; ++z)          // 16 tokens are 2,048 bytes
+                            tc_mma_ta(tmem + C::t_o + k * SD, p_set + z * 8, bd + z * 128, F8 ? f16_idesc(SD, 1) : tc_idesc(kRows, SD, 1),
+                                      c > 0 || z > 0);
                         tc_commit(smem_u32(&sh.empty[at]));
                     }
                     if (!ok) break;
-                    tc_commit(smem_u32(&sh.pv_done[i & 1]));
-                    last_bar = &sh.pv_done[i & 1], last_phase = i >> 1;
+                    tc_commit(smem_u32(&sh.pv_done[i % NB]));
                 }
-                ++seg;
             }
-            // the last commit covers every product issued: wait for it before tensor memory is freed
-            if (last_bar != nullptr) mbar_wait_bounded(smem_u32(last_bar), last_phase & 1u, kWaitLimitNs);
+            if (i > 0) wait_turn(smem_u32(&sh.pv_done[(i - 1) % NB]), (uint32_t)((i - 1) / NB) & 1u, a.hdr);
         }
     } else {
         // ================================================================ softmax
@@ -845,12 +897,12 @@ __global__ void __launch_bounds__(C::threads, 1)
                     both &= see[x];
                 }
                 const bool all = __all_sync(0xffffffffu, both == ~0u || !valid);       // no token to mask in this warp
-                if (!wait_warp(&sh.s_full[i & 1], i >> 1)) {
+                if (!wait_warp(&sh.s_full[i % NB], i / NB)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t t_s = t_row + C::t_s + (i & 1) * C::s_cols;
+                const uint32_t t_s = t_row + C::t_s + (i % NB) * C::s_cols;
                 float f = 1.f;
                 float2 was = unit;
                 if (some) {
@@ -859,21 +911,30 @@ __global__ void __launch_bounds__(C::threads, 1)
                     tmem_ld32_async(t_s + 32, v[1]);
                     tmem_wait_ld(v[0]);
                     tmem_wait_ld(v[1]);
-                    const float4 *sc = sh.scales[m];
                     if (F8) {
+                        auto times = [&](float (&x)[32], int h, int set, const float (*plus)[32]) {       // x scale (+ plus)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (SG == 2) {
-                                float u[32];
-                                tmem_ld32(t_s + 64 + h * 32, u);
+                            for (int k = 0; k < 8; ++k) {
+                                const float4 s4 = sh.k_scales[m][set][F8 ? h * 8 + k : 0];
+                                x[4 * k] = plus ? fmaf(x[4 * k], s4.x, (*plus)[4 * k]) : x[4 * k] * s4.x;
+                                x[4 * k + 1] = plus ? fmaf(x[4 * k + 1], s4.y, (*plus)[4 * k + 1]) : x[4 * k + 1] * s4.y;
+                                x[4 * k + 2] = plus ? fmaf(x[4 * k + 2], s4.z, (*plus)[4 * k + 2]) : x[4 * k + 2] * s4.z;
+                                x[4 * k + 3] = plus ? fmaf(x[4 * k + 3], s4.w, (*plus)[4 * k + 3]) : x[4 * k + 3] * s4.w;
+                            }
+                        };
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) {
-                                    const float2 s2 = *reinterpret_cast<const float2 *>(sc + (F8 ? h * 32 + k : 0));
-                                    v[h][k] = fmaf(u[k], s2.y, v[h][k] * s2.x);
-                                }
-                            } else {
+                        for (int h = 0; h < 2; ++h) times(v[h], h, 0, nullptr);
+                        if constexpr (SG == 2) {
+                            float u[2][32];
+                            tmem_ld32_async(t_s + 64, u[0]);
+                            tmem_ld32_async(t_s + 96, u[1]);
+                            tmem_wait_ld(u[0]);
+                            tmem_wait_ld(u[1]);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) v[h][k] *= sc[F8 ? h * 32 + k : 0].x;
+                            for (int h = 0; h < 2; ++h) {
+                                times(u[h], h, SG - 1, &v[h]);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[h][k] = u[h][k];
                             }
                         }
                         unit = sh.top[m];
@@ -908,15 +969,14 @@ __global__ void __launch_bounds__(C::threads, 1)
 #pragma unroll
                         for (int x = 0; x < SG; ++x) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const int z = F8 ? 2 * k : 0;
-                                const float e0 = v[k >> 4][2 * k & 31], e1 = v[k >> 4][(2 * k & 31) + 1];
-                                float w0 = e0 * (x ? sc[z].w : sc[z].z), w1 = e1 * (x ? sc[F8 ? z + 1 : 0].w : sc[F8 ? z + 1 : 0].z);
-                                if (!all) {               // whatever a masked token's scale is
-                                    w0 = (see[k >> 4] >> (2 * k & 31)) & 1u ? w0 : 0.f;
-                                    w1 = (see[k >> 4] >> ((2 * k & 31) + 1)) & 1u ? w1 : 0.f;
-                                }
-                                pk[k] = f16x2(w0, w1);
+                            for (int k = 0; k < 16; ++k) {
+                                const float4 s4 = sh.v_scales[m][x][F8 ? k : 0];
+                                float w4[4] = {v[k >> 3][4 * k & 31] * s4.x, v[k >> 3][(4 * k & 31) + 1] * s4.y,
+                                               v[k >> 3][(4 * k & 31) + 2] * s4.z, v[k >> 3][(4 * k & 31) + 3] * s4.w};
+                                if (!all)                 // whatever a masked token's scale is
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y) w4[y] = (see[k >> 3] >> ((4 * k & 31) + y)) & 1u ? w4[y] : 0.f;
+                                pk[2 * k] = f16x2(w4[0], w4[1]), pk[2 * k + 1] = f16x2(w4[2], w4[3]);
                             }
                             tmem_st32(t_s + x * 32, pk);
                         }
@@ -924,7 +984,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                 }
                 const bool turned = F8 && (was.x != unit.x || was.y != unit.y);
                 if (c > 0 && __any_sync(0xffffffffu, f != 1.f || turned)) {       // O follows, once the product before it is done
-                    if (!wait_warp(&sh.pv_done[(i - 1) & 1], (i - 1) >> 1)) {
+                    if (!wait_warp(&sh.pv_done[(i - 1) % NB], (i - 1) / NB)) {
                         ok = false;
                         break;
                     }
@@ -940,14 +1000,14 @@ __global__ void __launch_bounds__(C::threads, 1)
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(smem_u32(&sh.p_full[i & 1]));
+                mbar_arrive(smem_u32(&sh.p_full[i % NB]));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.meta_empty[m]));
             }
             if (!ok) break;
             // ---- the segment's end: out, or a partial
             const int i = g.i0 + n - 1;
-            if (!wait_warp(&sh.pv_done[i & 1], i >> 1) || !wait_warp(&sh.flags_full, seg)) break;
+            if (!wait_warp(&sh.pv_done[i % NB], i / NB) || !wait_warp(&sh.flags_full, seg)) break;
             tc_fence_after();
             const bool whole = g.begins && g.ends;
             const float by = l == 0.f ? 0.f : (whole ? 1.f / l : 1.f) * (F8 ? 1.f / (1 << (int)kRaise) : 1.f);
@@ -968,26 +1028,6 @@ __global__ void __launch_bounds__(C::threads, 1)
                     tmem_ld32(t_o + c0, v);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : v[k] * times;
-                    if (strange) {
-#pragma unroll 1
-                        for (int x = 0; x < 2 * QSA_MAX_DRAFT; ++x) {
-                            const int y = x & (QSA_MAX_DRAFT - 1), j = (x == y ? g.r.base : g.r.lo) + y;
-                            if (!((x == y ? sh.odd[0] : sh.odd[1])[y >> 5] >> (y & 31) & 1u)) continue;
-                            if (x == y ? !(sh.kin[node][y >> 5] >> (y & 31) & 1u) : j < lo || j >= g.r.base) continue;
-                            const int page = a.table[g.s * a.ld + j / a.page_size];
-                            if ((uint32_t)page >= (uint32_t)a.n_pages) continue;
-                            const int64_t vr = (((int64_t)page * a.page_size + j % a.page_size) * a.Hkv + kvh) * D + c0;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                if (F8) {
-                                    if ((static_cast<const uint8_t *>(a.v)[vr + k] & 0x7Fu) == 0x7Fu) v[k] = NAN;
-                                } else {
-                                    const float z = bf16_bits_to_float(static_cast<const uint16_t *>(a.v)[vr + k]);
-                                    if (!isfinite(z)) v[k] += z;
-                                }
-                            }
-                        }
-                    }
                     if (valid && whole) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -1000,6 +1040,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                             *reinterpret_cast<float4 *>(po + c0 + 4 * k) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                     }
                 }
+                if (strange) add_odd<D, F8>(a, g, sh.odd, sh.kin[node], lo, kvh, whole, dst, po);
                 if (valid) {
                     if (!whole)
                         ws.ml[at * kRows + row] = make_float2(ref, l);
@@ -1014,17 +1055,19 @@ __global__ void __launch_bounds__(C::threads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == C::mma_warp) tmem_dealloc(tmem, 512);
+    if (warp == C::s_warp) tmem_dealloc(tmem, 512);
 }
 
-// The partials of the sequences that a range starts and leaves unfinished, joined. A CTA takes Rows rows of the y-th such range;
-// D / 4 threads a row, Groups of them on every Groups-th partial, merged in order at the end.
+// The partials of the sequences that a range starts and leaves unfinished, joined. A CTA takes every gridDim.y-th pair of rows
+// of the y-th such range; D / 4 threads have a row, `Groups` of them every Groups-th partial, merged in order at the end. CTAs for
+// single rows, 8,000 of them for 32 sequences of 16 drafted tokens, took longer to begin than to read their partials.
+constexpr int kJoinThreads = 256;
 template <int D, int Groups>
-__global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, TreePlan plan, TreeScratch ws) {
-    constexpr int cols = D / 4, Rows = 256 / cols / Groups, U = 8;
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeArgs a, TreePlan plan, TreeScratch ws) {
+    constexpr int cols = D / 4, Rows = kJoinThreads / cols / Groups, U = 4;
     static_assert(Rows >= 1, "a row");
-    __shared__ float4 acc[Groups > 1 ? 256 : 1];
-    __shared__ float2 pair[256 / cols];
+    __shared__ float4 acc[Groups > 1 ? kJoinThreads : 1];
+    __shared__ float2 pair[kJoinThreads / cols];
     __shared__ int4 job_sh;
     const int tid = threadIdx.x, col = tid % cols, group = tid / cols % Groups, sub = tid / cols / Groups;
     wait_for_previous();
@@ -1044,66 +1087,69 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, TreePlan pla
     const int4 job = job_sh;
     if (job.x < 0) return;
     const int off = a.draft_off[job.y], T = a.draft_off[job.y + 1] - off;
-    // rows: (drafted token, query head), the heads of a KV head together
-    const int64_t id = (int64_t)blockIdx.y * Rows + sub;
-    const int per = T * a.G, kvh = (int)(id / per), r = (int)(id % per);
-    const bool valid = kvh < a.Hkv;
-    const int64_t C = (int64_t)a.Hkv * plan.m_tiles, at = (int64_t)(valid ? kvh : 0) * plan.m_tiles + r / kRows;
-    float m = -INFINITY, l = 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = group; i0 < job.z; i0 += U * Groups) {
-        float2 ml[U];
-        float4 o[U];
+    // rows: (KV head, drafted token, query head of the KV head)
+    const int per = T * a.G, rows = per * a.Hkv;
+    const int64_t C = (int64_t)a.Hkv * plan.m_tiles;
+    for (int id0 = blockIdx.y * Rows; id0 < rows; id0 += gridDim.y * Rows) {
+        const int id = min(id0 + sub, rows - 1), kvh = id / per, r = id % per;
+        const int64_t at = (int64_t)kvh * plan.m_tiles + r / kRows;
+        float m = -INFINITY, l = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = group; i0 < job.z; i0 += U * Groups) {
+            float2 ml[U];
+            float4 o[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * Groups;
-            ml[u] = make_float2(-INFINITY, 0.f);
-            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < job.z) {
-                const int64_t p = (part_slot(job.x, i) * C + at) * kRows + r % kRows;
-                ml[u] = __ldcg(ws.ml + p);
-                o[u] = __ldcg(reinterpret_cast<const float4 *>(ws.o + p * D + 4 * col));
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * Groups;
+                ml[u] = make_float2(-INFINITY, 0.f);
+                o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < job.z) {
+                    const int64_t p = (part_slot(job.x, i) * C + at) * kRows + r % kRows;
+                    ml[u] = __ldcg(ws.ml + p);
+                    o[u] = __ldcg(reinterpret_cast<const float4 *>(ws.o + p * D + 4 * col));
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+            const float ref = top == -INFINITY ? 0.f : top, old = ex2(m - ref);
+            m = top;
+            l *= old;
+            x.x *= old, x.y *= old, x.z *= old, x.w *= old;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float w = ex2(ml[u].x - ref);
+                l = fmaf(w, ml[u].y, l);
+                x.x = fmaf(w, o[u].x, x.x), x.y = fmaf(w, o[u].y, x.y);
+                x.z = fmaf(w, o[u].z, x.z), x.w = fmaf(w, o[u].w, x.w);
             }
         }
-        float top = m;
+        if (Groups > 1) {
+            __syncthreads();                              // the row before has been merged
+            acc[tid] = x;
+            if (col == 0) pair[tid / cols] = make_float2(m, l);
+            __syncthreads();
+            if (group > 0) continue;
+            float top = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
-        const float ref = top == -INFINITY ? 0.f : top, old = ex2(m - ref);
-        m = top;
-        l *= old;
-        x.x *= old, x.y *= old, x.z *= old, x.w *= old;
+            for (int i = 0; i < Groups; ++i) top = fmaxf(top, pair[sub * Groups + i].x);
+            const float ref = top == -INFINITY ? 0.f : top;
+            l = 0.f, m = top;
+            x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const float w = ex2(ml[u].x - ref);
-            l = fmaf(w, ml[u].y, l);
-            x.x = fmaf(w, o[u].x, x.x), x.y = fmaf(w, o[u].y, x.y);
-            x.z = fmaf(w, o[u].z, x.z), x.w = fmaf(w, o[u].w, x.w);
+            for (int i = 0; i < Groups; ++i) {
+                const float w = ex2(pair[sub * Groups + i].x - ref);
+                const float4 v = acc[tid + i * cols];
+                l = fmaf(w, pair[sub * Groups + i].y, l);
+                x.x = fmaf(w, v.x, x.x), x.y = fmaf(w, v.y, x.y), x.z = fmaf(w, v.z, x.z), x.w = fmaf(w, v.w, x.w);
+            }
         }
+        if (id0 + sub >= rows) continue;
+        const int64_t to = (int64_t)(off + r / a.G) * a.Hq + kvh * a.G + r % a.G;
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<uint2 *>(a.out + to * D + 4 * col) = make_uint2(bf16x2(x.x * f, x.y * f), bf16x2(x.z * f, x.w * f));
+        if (col == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
-    if (Groups > 1) {
-        acc[tid] = x;
-        if (col == 0) pair[tid / cols] = make_float2(m, l);
-        __syncthreads();
-        if (group > 0) return;
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < Groups; ++i) top = fmaxf(top, pair[sub * Groups + i].x);
-        const float ref = top == -INFINITY ? 0.f : top;
-        l = 0.f, m = top;
-        x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < Groups; ++i) {
-            const float w = ex2(pair[sub * Groups + i].x - ref);
-            const float4 v = acc[tid + i * cols];
-            l = fmaf(w, pair[sub * Groups + i].y, l);
-            x.x = fmaf(w, v.x, x.x), x.y = fmaf(w, v.y, x.y), x.z = fmaf(w, v.z, x.z), x.w = fmaf(w, v.w, x.w);
-        }
-    }
-    if (!valid) return;
-    const int64_t to = (int64_t)(off + r / a.G) * a.Hq + kvh * a.G + r % a.G;
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2 *>(a.out + to * D + 4 * col) = make_uint2(bf16x2(x.x * f, x.y * f), bf16x2(x.z * f, x.w * f));
-    if (col == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 constexpr int kMaxCtas = 160;
@@ -1165,9 +1211,14 @@ cudaError_t launch(const TreeArgs &a, cudaStream_t st) {
     const dim3 grid((unsigned)(plan.ranges * a.Hkv * plan.m_tiles));
     const cudaError_t e = launch_dependent(tree_tile_kernel<C>, grid, C::threads, C::smem, st, a, plan, ws, maps);
     if (e != cudaSuccess || plan.ranges == 1) return e;               // one range cuts no sequence
-    constexpr int groups = 256 / (D / 4);
-    const unsigned jobs = (unsigned)std::min(plan.ranges - 1, a.B), most = (unsigned)(a.max_draft * a.Hq);
-    return launch_dependent(tree_join_kernel<D, groups>, dim3(jobs, most), 256, 0, st, a, plan, ws);
+    // as many CTAs as fit at once; few rows have many partials each, and more threads for a row
+    const int64_t jobs = std::min(plan.ranges - 1, a.B), most = (int64_t)a.max_draft * a.Hq;
+    const int groups = kJoinThreads / (D / 4);
+    const bool few = jobs * most <= 152 * 8;
+    const int64_t each = few ? 1 : groups / 2;
+    const dim3 join((unsigned)jobs, (unsigned)std::max<int64_t>(1, std::min((most + each - 1) / each, 152 * 8 / jobs)));
+    return few ? launch_dependent(tree_join_kernel<D, kJoinThreads / (D / 4)>, join, kJoinThreads, 0, st, a, plan, ws)
+               : launch_dependent(tree_join_kernel<D, 2>, join, kJoinThreads, 0, st, a, plan, ws);
 }
 
 }  // namespace
