@@ -186,6 +186,12 @@ __host__ __device__ constexpr uint32_t f16_idesc(int N, int b_mn) {
     return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
 // Which of the eight bf16 values of v are not finite: all of them as zeros, and whether there was one.
 __device__ __forceinline__ bool drop_odd(uint4 &v) {
     uint32_t *w = reinterpret_cast<uint32_t *>(&v);
@@ -759,94 +765,98 @@ __global__ void __launch_bounds__(C::threads, 1)
         }
     } else if (warp == C::s_warp) {
         // ================================================================ scores
-        if (lane == 0) {
-            Walk w = walk;
-            int seg = 0, i = 0;
-            bool ok = true;
-            for (; ok && w.next(a, m_tile, g); ++seg) {
-                const int n = g.tb - g.ta;
-                if (!wait(&sh.q_full, seg)) break;
-                for (int c = 0; c < n && ok; ++c, ++i) {
-                    // the buffer's last weights are used up
-                    if (i >= NB && !wait(&sh.pv_done[i % NB], i / NB - 1)) {
+        // The warp stays together and one elected lane issues: addresses and descriptors are then the warp's, not a lane's, which
+        // the instruction wants them to be.
+        Walk w = walk;
+        int seg = 0, i = 0;
+        bool ok = true;
+        for (; ok && w.next(a, m_tile, g); ++seg) {
+            const int n = g.tb - g.ta;
+            if (!wait_warp(&sh.q_full, seg)) break;
+#pragma unroll 1
+            for (int c = 0; c < n && ok; ++c, ++i) {
+                // the buffer's last weights are used up
+                if (i >= NB && !wait_warp(&sh.pv_done[i % NB], i / NB - 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t s_at = tmem + C::t_s + (i % NB) * C::s_cols;
+#pragma unroll 1
+                for (int k = 0; k < SL; ++k) {
+                    const int q = (2 * g.i0 + k_turn(c)) * SL + k, at = q % RING;
+                    if (!wait_warp(&sh.full[at], q / RING)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t s_at = tmem + C::t_s + (i % NB) * C::s_cols;
-                    for (int k = 0; k < SL; ++k) {
-                        const int q = (2 * g.i0 + k_turn(c)) * SL + k, at = q % RING;
-                        if (!wait(&sh.full[at], q / RING)) {
-                            ok = false;
-                            break;
-                        }
-                        if (!F8 && !tiled) fence_proxy_async_smem();      // rows by cp.async; TMA needs none, the conversion has its own
-                        tc_fence_after();
-                        const uint32_t b = ring_at + at * C::slot;
-                        const uint64_t bd = tc_desc(b, 16, 1024);
-                        const uint32_t q_row = q_at + 2 * k * (kRows * 128);
+                    if (!F8 && !tiled) fence_proxy_async_smem();      // rows by cp.async; TMA needs none, the conversion has its own
+                    tc_fence_after();
+                    const uint64_t bd = tc_desc(ring_at + at * C::slot, 16, 1024), ad = tc_desc(q_at + 2 * k * (kRows * 128), 16, 1024);
+                    if (elect_one()) {
 #pragma unroll
-                        for (int z = 0; z < SD / 16; ++z) {       // 16 dims: 32 bytes on, or in the next block of 64
+                        for (int z = 0; z < SD / 16; ++z) {           // 16 dims: 32 bytes on, or in the next block of 64
                             const uint64_t zd = bd + (z >> 2) * (T * 128 / 16) + (z & 3) * 2;
                             if (!F8)
                                 tc_mma_ta(s_at, tmem + C::t_q + z * 8, zd, tc_idesc(kRows, T, 0), z > 0);
                             else
-                                tc_mma(s_at + k * T, tc_desc(q_row + (z >> 2) * (kRows * 128) + (z & 3) * 32, 16, 1024), zd, f16_idesc(T, 0),
-                                       z > 0);
+                                tc_mma(s_at + k * T, ad + (z >> 2) * (kRows * 128 / 16) + (z & 3) * 2, zd, f16_idesc(T, 0), z > 0);
                         }
                         tc_commit(smem_u32(&sh.empty[at]));
+                        if (k + 1 == SL) {
+                            tc_commit(smem_u32(&sh.s_full[i % NB]));
+                            if (c + 1 == n) tc_commit(smem_u32(&sh.q_free));
+                        }
                     }
-                    if (!ok) break;
-                    tc_commit(smem_u32(&sh.s_full[i % NB]));
-                    if (c + 1 == n) tc_commit(smem_u32(&sh.q_free));
+                    __syncwarp();
                 }
             }
-            // the last commit covers every product issued: wait for it before tensor memory is freed
-            if (i > 0) wait_turn(smem_u32(&sh.s_full[(i - 1) % NB]), (uint32_t)((i - 1) / NB) & 1u, a.hdr);
         }
+        // the last commit covers every product issued: wait for it before tensor memory is freed
+        if (i > 0 && lane == 0) wait_turn(smem_u32(&sh.s_full[(i - 1) % NB]), (uint32_t)((i - 1) / NB) & 1u, a.hdr);
     } else if (warp == C::o_warp) {
         // ================================================================ O (+)= P V
-        if (lane == 0) {
-            Walk w = walk;
-            int seg = 0, cleaned = 0, i = 0;
-            bool ok = true;
-            for (; ok && w.next(a, m_tile, g); ++seg) {
-                const int n = g.tb - g.ta;
-                for (int c = 0; c < n && ok; ++c, ++i) {
-                    const int q0 = (2 * g.i0 + v_turn(c, n)) * SL;
-                    const bool part = !F8 && masked(a, g.r, g.ta + c);
-                    if (part) {
-                        for (int k = 0; k < SL && ok; ++k) ok = wait(&sh.full[(q0 + k) % RING], (q0 + k) / RING);
-                        mbar_arrive(smem_u32(&sh.to_clean));
-                    }
-                    if (!ok || !wait(&sh.p_full[i % NB], i / NB) || (c == 0 && seg > 0 && !wait(&sh.o_free, seg - 1)) ||
-                        (part && !wait(&sh.clean, cleaned++))) {
+        Walk w = walk;
+        int seg = 0, cleaned = 0, i = 0;
+        bool ok = true;
+        for (; ok && w.next(a, m_tile, g); ++seg) {
+            const int n = g.tb - g.ta;
+#pragma unroll 1
+            for (int c = 0; c < n && ok; ++c, ++i) {
+                const int q0 = (2 * g.i0 + v_turn(c, n)) * SL;
+                const bool part = !F8 && masked(a, g.r, g.ta + c);
+                if (part) {
+                    for (int k = 0; k < SL && ok; ++k) ok = wait_warp(&sh.full[(q0 + k) % RING], (q0 + k) / RING);
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.to_clean));
+                }
+                if (!ok || !wait_warp(&sh.p_full[i % NB], i / NB) || (c == 0 && seg > 0 && !wait_warp(&sh.o_free, seg - 1)) ||
+                    (part && !wait_warp(&sh.clean, cleaned++))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t p_at = tmem + C::t_s + (i % NB) * C::s_cols;
+#pragma unroll 1
+                for (int k = 0; k < SL; ++k) {
+                    const int q = q0 + k, at = q % RING;
+                    if (!wait_warp(&sh.full[at], q / RING)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t p_at = tmem + C::t_s + (i % NB) * C::s_cols;
-                    for (int k = 0; k < SL; ++k) {
-                        const int q = q0 + k, at = q % RING;
-                        if (!wait(&sh.full[at], q / RING)) {
-                            ok = false;
-                            break;
-                        }
-                        if (!F8 && !tiled) fence_proxy_async_smem();
-                        tc_fence_after();
-                        const uint32_t b = ring_at + at * C::slot;
-                        const uint64_t bd = tc_desc(b, T * 128, 1024);
-                        const uint32_t p_set = p_at + (F8 ? k * (T / 2) : 0);
+                    if (!F8 && !tiled) fence_proxy_async_smem();
+                    tc_fence_after();
+                    const uint64_t bd = tc_desc(ring_at + at * C::slot, T * 128, 1024);
+                    const uint32_t p_set = p_at + (F8 ? k * (T / 2) : 0);
+                    if (elect_one()) {
 #pragma unroll
-                        for (int z = 0; z < T / 16; ++z)          // 16 tokens are 2,048 bytes
+                        for (int z = 0; z < T / 16; ++z)              // 16 tokens are 2,048 bytes
                             tc_mma_ta(tmem + C::t_o + k * SD, p_set + z * 8, bd + z * 128, F8 ? f16_idesc(SD, 1) : tc_idesc(kRows, SD, 1),
                                       c > 0 || z > 0);
                         tc_commit(smem_u32(&sh.empty[at]));
+                        if (k + 1 == SL) tc_commit(smem_u32(&sh.pv_done[i % NB]));
                     }
-                    if (!ok) break;
-                    tc_commit(smem_u32(&sh.pv_done[i % NB]));
+                    __syncwarp();
                 }
             }
-            if (i > 0) wait_turn(smem_u32(&sh.pv_done[(i - 1) % NB]), (uint32_t)((i - 1) / NB) & 1u, a.hdr);
         }
+        if (i > 0 && lane == 0) wait_turn(smem_u32(&sh.pv_done[(i - 1) % NB]), (uint32_t)((i - 1) / NB) & 1u, a.hdr);
     } else {
         // ================================================================ softmax
         const uint32_t t_row = tmem + ((uint32_t)(32 * warp) << 16), t_o = t_row + C::t_o;
