@@ -54,8 +54,8 @@ struct TreeCfg {
     static constexpr int SD = F8 ? 128 : D, SL = D / SD;   // dims of a slot; slots of a tile's K, and of its V
     static constexpr int SG = F8 ? D / 128 : 1;                 // scales of a row, sets of weights
     static constexpr int slot = kTile * SD * 2, code_slot = F8 ? kTile * SD : 0;    // bytes
-    static constexpr int ring = F8 ? 4 : D == 64 ? 24 : 212992 / slot;
-    static constexpr int codes = F8 ? (D == 256 ? 10 : 12) : 0;
+    static constexpr int ring = F8 ? 6 : D == 64 ? 24 : 212992 / slot;
+    static constexpr int codes = F8 ? (D == 256 ? 6 : 10) : 0;
     static constexpr int from = F8 ? codes : ring;              // slots that global memory is read into
     static constexpr int ring_at = F8 ? kRows * D * 2 : 0, codes_at = ring_at + ring * slot;
     static constexpr int smem = codes_at + codes * code_slot + 1024;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(C::threads, 1)
         // the loads' arrivals: one with the bytes it expects, or every worker's
         const int load = tiled ? 1 : C::workers;
         for (int i = 0; i < RING; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), F8 ? C::workers : load);
+            mbar_init(smem_u32(&sh.full[i]), F8 ? C::workers / 32 : load);
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
         if (F8)
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(C::threads, 1)
             }
         for (int i = 0; i < C::buffers; ++i) {
             mbar_init(smem_u32(&sh.s_full[i]), 1);
-            mbar_init(smem_u32(&sh.p_full[i]), C::softmax);
+            mbar_init(smem_u32(&sh.p_full[i]), C::softmax / 32);
             mbar_init(smem_u32(&sh.pv_done[i]), 1);
         }
         for (int i = 0; i < kMetas; ++i) {
@@ -590,29 +590,36 @@ __global__ void __launch_bounds__(C::threads, 1)
                     const int q = q0 + k, from = q % C::codes, to = q % RING;
                     if (!wait_warp(&sh.c_full[from], q / C::codes)) return false;
                     if (q >= RING && !wait_warp(&sh.empty[to], q / RING - 1)) return false;
+                    constexpr int N = (T * row_chunks + C::workers - 1) / C::workers;
+                    uint4 v[N];
 #pragma unroll
-                    for (int i = 0; i < (T * row_chunks + C::workers - 1) / C::workers; ++i) {
+                    for (int i = 0; i < N; ++i) {
+                        const int id = i * C::workers + wt, tok = id / row_chunks, gr = id % row_chunks;
+                        if (tok < T) v[i] = *reinterpret_cast<const uint4 *>(sm + C::codes_at + from * C::code_slot + swz(tok, gr));
+                    }
+                    if (is_v && some)
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            const int j = j0 + (i * C::workers + wt) / row_chunks;
+                            if ((uint32_t)j >= (uint32_t)r.len || j < r.lo)
+                                v[i] = make_uint4(0, 0, 0, 0);
+                            else if (j >= r.base || j < edge)
+                                drop_nan_codes(v[i].x), drop_nan_codes(v[i].y), drop_nan_codes(v[i].z), drop_nan_codes(v[i].w);
+                        }
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
                         const int id = i * C::workers + wt, tok = id / row_chunks, gr = id % row_chunks;
                         if (tok >= T) break;
-                        uint4 v = *reinterpret_cast<const uint4 *>(sm + C::codes_at + from * C::code_slot + swz(tok, gr));
-                        if (is_v && some) {
-                            const int j = j0 + tok;
-                            if ((uint32_t)j >= (uint32_t)r.len || j < r.lo)
-                                v = make_uint4(0, 0, 0, 0);
-                            else if (j >= r.base || j < edge)
-                                drop_nan_codes(v.x), drop_nan_codes(v.y), drop_nan_codes(v.z), drop_nan_codes(v.w);
-                        }
                         uint8_t *dst = sm + C::ring_at + to * C::slot + (gr >> 2) * (T * 128);
                         const int at = (gr & 3) * 2;
                         *reinterpret_cast<uint4 *>(dst + swz(tok, at)) =
-                            make_uint4(e4m3_to_f16x2(v.x, 0), e4m3_to_f16x2(v.x, 1), e4m3_to_f16x2(v.y, 0), e4m3_to_f16x2(v.y, 1));
+                            make_uint4(e4m3_to_f16x2(v[i].x, 0), e4m3_to_f16x2(v[i].x, 1), e4m3_to_f16x2(v[i].y, 0), e4m3_to_f16x2(v[i].y, 1));
                         *reinterpret_cast<uint4 *>(dst + swz(tok, at + 1)) =
-                            make_uint4(e4m3_to_f16x2(v.z, 0), e4m3_to_f16x2(v.z, 1), e4m3_to_f16x2(v.w, 0), e4m3_to_f16x2(v.w, 1));
+                            make_uint4(e4m3_to_f16x2(v[i].z, 0), e4m3_to_f16x2(v[i].z, 1), e4m3_to_f16x2(v[i].w, 0), e4m3_to_f16x2(v[i].w, 1));
                     }
                     fence_proxy_async_smem();
-                    mbar_arrive(smem_u32(&sh.full[to]));
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.c_empty[from]));
+                    __syncwarp();                         // an arrival for each warp: 192 of them on one word take hundreds of cycles
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.full[to])), mbar_arrive(smem_u32(&sh.c_empty[from]));
                 }
                 return true;
             };
@@ -935,16 +942,13 @@ __global__ void __launch_bounds__(C::threads, 1)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) times(v[h], h, 0, nullptr);
                         if constexpr (SG == 2) {
-                            float u[2][32];
-                            tmem_ld32_async(t_s + 64, u[0]);
-                            tmem_ld32_async(t_s + 96, u[1]);
-                            tmem_wait_ld(u[0]);
-                            tmem_wait_ld(u[1]);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                times(u[h], h, SG - 1, &v[h]);
+                                float u[32];
+                                tmem_ld32(t_s + 64 + 32 * h, u);
+                                times(u, h, SG - 1, &v[h]);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) v[h][k] = u[h][k];
+                                for (int k = 0; k < 32; ++k) v[h][k] = u[k];
                             }
                         }
                         unit = sh.top[m];
@@ -1010,9 +1014,8 @@ __global__ void __launch_bounds__(C::threads, 1)
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(smem_u32(&sh.p_full[i % NB]));
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.meta_empty[m]));
+                if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[i % NB])), mbar_arrive(smem_u32(&sh.meta_empty[m]));
             }
             if (!ok) break;
             // ---- the segment's end: out, or a partial
