@@ -51,11 +51,10 @@ template <int D_, bool F8_>
 struct TreeCfg {
     static constexpr int D = D_;
     static constexpr bool F8 = F8_;
-    static constexpr int SD = F8 ? 128 : D, SL = D / SD;   // dims of a slot; slots of a tile's K, and of its V
     static constexpr int SG = F8 ? D / 128 : 1;                 // scales of a row, sets of weights
-    static constexpr int slot = kTile * SD * 2, code_slot = F8 ? kTile * SD : 0;    // bytes
-    static constexpr int ring = F8 ? 6 : D == 64 ? 24 : 212992 / slot;
-    static constexpr int codes = F8 ? (D == 256 ? 6 : 10) : 0;
+    static constexpr int slot = kTile * D * 2, code_slot = F8 ? kTile * D : 0;      // bytes: a tile's K or V
+    static constexpr int ring = F8 ? (D == 256 ? 3 : 6) : D == 64 ? 24 : 212992 / slot;
+    static constexpr int codes = F8 ? (D == 256 ? 3 : 10) : 0;
     static constexpr int from = F8 ? codes : ring;              // slots that global memory is read into
     static constexpr int ring_at = F8 ? kRows * D * 2 : 0, codes_at = ring_at + ring * slot;
     static constexpr int smem = codes_at + codes * code_slot + 1024;
@@ -63,11 +62,11 @@ struct TreeCfg {
     // tensor memory columns: O, the queries (bf16 rows; with FP8 rows they are in shared memory), buffers of scores
     static constexpr uint32_t t_o = 0, t_q = D, t_s = D == 256 && !F8 ? 384 : 256, s_cols = SG * kTile;
     static constexpr int buffers = (512 - t_s) / s_cols;
-    // 16 warps of 128 registers; the query warps' numbers modulo 4 are the four quarters of tensor memory's lanes
-    static constexpr int softmax = 128, q_threads = F8 ? 64 : 128, workers = F8 ? 192 : 160;
-    static constexpr int s_warp = 4, o_warp = 5, index_warp = 6, q_warp = 7, load_warp = q_warp + q_threads / 32;
+    // 20 warps of 96 registers; the query warps' numbers modulo 4 are the four quarters of tensor memory's lanes
+    static constexpr int softmax = 256, q_threads = F8 ? 64 : 128, workers = F8 ? 192 : 160;
+    static constexpr int s_warp = 8, o_warp = 9, index_warp = 10, q_warp = 11, load_warp = q_warp + q_threads / 32;
     static constexpr int work_warp = F8 ? load_warp + 1 : load_warp;
-    static constexpr int threads = 512;
+    static constexpr int threads = 640;
     static_assert(work_warp * 32 + workers == threads, "roles");
 };
 
@@ -171,6 +170,7 @@ struct TreeShared {
     uint32_t real[kMetas][kTile / 32];                     // bit: the token's page exists
     float4 k_scales[kMetas][C::SG][C::F8 ? kTile / 4 : 1], v_scales[kMetas][C::SG][C::F8 ? kTile / 4 : 1];   // four tokens each
     float2 top[kMetas];                                   // powers of two at most 2 below the tile's largest V scales
+    float tops[2][2][kRows];                              // of every other tile: the halves' maxima
     uint32_t tmem;
 };
 
@@ -184,6 +184,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int x
 // kind::f16 with f16 operands (tc_idesc is bf16's)
 __host__ __device__ constexpr uint32_t f16_idesc(int N, int b_mn) {
     return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+                 "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -241,7 +249,7 @@ __device__ __forceinline__ bool wait_turn(uint32_t bar, uint32_t parity, WsHeade
 // Values that are not finite, of tokens that this row attends but not every row: added to its result (whole) or its partial.
 template <int D, bool F8>
 __device__ __noinline__ void add_odd(const TreeArgs &a, const Seg &g, const uint32_t (*odd)[QSA_MAX_DRAFT / 32], const uint32_t *kin,
-                                     int lo, int kvh, bool whole, uint16_t *dst, float *po) {
+                                     int lo, int kvh, int first, bool whole, uint16_t *dst, float *po) {
 #pragma unroll 1
     for (int x = 0; x < 2 * QSA_MAX_DRAFT; ++x) {
         const int y = x % QSA_MAX_DRAFT, j = (x == y ? g.r.base : g.r.lo) + y;
@@ -251,8 +259,8 @@ __device__ __noinline__ void add_odd(const TreeArgs &a, const Seg &g, const uint
         if ((uint32_t)page >= (uint32_t)a.n_pages) continue;
         const int64_t row = (((int64_t)page * a.page_size + j % a.page_size) * a.Hkv + kvh) * D;
 #pragma unroll 1
-        for (int d = 0; d < D; ++d) {
-            const float z = F8 ? ((static_cast<const uint8_t *>(a.v)[row + d] & 0x7Fu) == 0x7Fu ? NAN : 0.f)
+        for (int d = first; d < first + D / 2; ++d) {
+            const float z = F8 ? ((static_cast<const uint8_t *>(a.v)[row + d] & 0x7Fu) == 0x7Fu || !isfinite(a.v_scales[(row + d) / 128]) ? NAN : 0.f)
                                : bf16_bits_to_float(static_cast<const uint16_t *>(a.v)[row + d]);
             if (isfinite(z)) continue;
             if (whole)
@@ -266,7 +274,7 @@ __device__ __noinline__ void add_odd(const TreeArgs &a, const Seg &g, const uint
 template <typename C>
 __global__ void __launch_bounds__(C::threads, 1)
     tree_tile_kernel(TreeArgs a, TreePlan plan, TreeScratch ws, const __grid_constant__ TreeMaps maps) {
-    constexpr int D = C::D, T = kTile, SD = C::SD, SL = C::SL, RING = C::ring, SG = C::SG, NB = C::buffers;
+    constexpr int D = C::D, T = kTile, RING = C::ring, SG = C::SG, NB = C::buffers;
     constexpr bool F8 = C::F8;
     extern __shared__ uint8_t smem_raw[];
     __shared__ TreeShared<C> sh;
@@ -306,9 +314,9 @@ __global__ void __launch_bounds__(C::threads, 1)
         mbar_init(smem_u32(&sh.q_full), C::q_threads);
         mbar_init(smem_u32(&sh.q_free), 1);
         mbar_init(smem_u32(&sh.nodes_full), C::q_threads);
-        mbar_init(smem_u32(&sh.nodes_free), C::softmax);
+        mbar_init(smem_u32(&sh.nodes_free), C::softmax / 32);
         mbar_init(smem_u32(&sh.flags_full), C::q_threads);
-        mbar_init(smem_u32(&sh.o_free), C::softmax);
+        mbar_init(smem_u32(&sh.o_free), C::softmax / 32);
         fence_mbar_init();
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
@@ -493,7 +501,8 @@ __global__ void __launch_bounds__(C::threads, 1)
                     const float cx = inverse(top.x) * (float)(1 << (int)kRaise), cy = inverse(top.y) * (float)(1 << (int)kRaise);
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
-                        const float4 x = scale[e];        // infinite V scales become NaN
+                        float4 x = scale[e];              // infinite V scales become NaN; where not every row attends, it is added at the end
+                        if (masked(a, now.r, t)) x.z = x.z < INFINITY ? x.z : 0.f, x.w = x.w < INFINITY ? x.w : 0.f;
                         float *ks = reinterpret_cast<float *>(sh.k_scales[m]), *vs = reinterpret_cast<float *>(sh.v_scales[m]);
                         const int tok = F8 ? lane * E + e : 0;
                         ks[tok] = x.x, vs[tok] = fmaf(x.z, 0.f, x.z) * cx;
@@ -508,44 +517,40 @@ __global__ void __launch_bounds__(C::threads, 1)
     } else if (warp >= C::load_warp) {
         // ================================================================ loads; codes -> f16
         const int wt = tid - C::work_warp * 32;
-        constexpr int row_chunks = F8 ? SD / 16 : SD / 8;     // 16-byte chunks of a token's row in a slot
-        const char *rows[2] = {static_cast<const char *>(a.k) + (int64_t)kvh * SL * row_chunks * 16,
-                               static_cast<const char *>(a.v) + (int64_t)kvh * SL * row_chunks * 16};
-        const int64_t pitch = (int64_t)a.Hkv * SL * row_chunks * 16;
+        constexpr int row_chunks = F8 ? D / 16 : D / 8;       // 16-byte chunks of a token's row
+        const char *rows[2] = {static_cast<const char *>(a.k) + (int64_t)kvh * row_chunks * 16,
+                               static_cast<const char *>(a.v) + (int64_t)kvh * row_chunks * 16};
+        const int64_t pitch = (int64_t)a.Hkv * row_chunks * 16;
         // TMA: a box is a run of a page; a row that does not exist reads as zeros
-        constexpr int blocks = F8 ? 1 : SD / 64;              // 128-byte blocks of a slot's rows
+        constexpr int blocks = row_chunks / 8;                // 128-byte blocks of a row
         const int rows_end = (int)min((int64_t)INT32_MAX, a.n_pages * a.page_size);
         const int boxes = tiled ? T / plan.run : 1, whole = boxes == 1 ? 1 : blocks, run = lane % boxes, block = lane / boxes;
         int asked = 0;                                        // slots asked for
-        // a tile's K or V into the slots of turn q0 ...
-        auto copy = [&](int is_v, int tile, int q0) -> bool {
+        // a tile's K or V into the slot of turn q
+        auto copy = [&](int is_v, int tile, int q) -> bool {
             const int m = tile % kMetas;
             if (!is_v && !wait_warp(&sh.meta_full[m], tile / kMetas)) return false;
             const int box = sh.slots[m][tiled ? run * plan.run : 0], y = box < 0 ? rows_end : box;
-#pragma unroll 1
-            for (int k = 0; k < SL; ++k) {
-                const int q = q0 + k, at = q % C::from, turn = q / C::from;
-                if (turn > 0 && !wait_warp(F8 ? &sh.c_empty[F8 ? at : 0] : &sh.empty[F8 ? 0 : at], turn - 1)) return false;
-                const uint32_t dst = F8 ? codes_at + at * C::code_slot : ring_at + at * C::slot;
-                if (tiled) {
-                    const uint32_t full = smem_u32(F8 ? &sh.c_full[F8 ? at : 0] : &sh.full[F8 ? 0 : at]);
-                    asked = q + 1;
-                    if (lane == 0) mbar_arrive_expect_tx(full, F8 ? C::code_slot : C::slot);
-                    __syncwarp();
-                    if (block < whole)
-                        tma_load_3d(dst + block * (T * 128) + run * plan.run * 128, is_v ? &maps.v : &maps.k, 0, y,
-                                    (kvh * SL + k) * blocks + block, full);
-                    continue;
-                }
+            const int at = q % C::from, turn = q / C::from;
+            uint64_t *full = F8 ? &sh.c_full[F8 ? at : 0] : &sh.full[F8 ? 0 : at];
+            if (turn > 0 && !wait_warp(F8 ? &sh.c_empty[F8 ? at : 0] : &sh.empty[F8 ? 0 : at], turn - 1)) return false;
+            const uint32_t dst = F8 ? codes_at + at * C::code_slot : ring_at + at * C::slot;
+            if (tiled) {
+                asked = q + 1;
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(full), F8 ? C::code_slot : C::slot);
+                __syncwarp();
+                if (block < whole)
+                    tma_load_3d(dst + block * (T * 128) + run * plan.run * 128, is_v ? &maps.v : &maps.k, 0, y, kvh * blocks + block,
+                                smem_u32(full));
+            } else {
 #pragma unroll
                 for (int i = 0; i < (T * row_chunks + C::workers - 1) / C::workers; ++i) {
                     const int id = i * C::workers + wt, tok = id / row_chunks, gr = id % row_chunks;
                     if (tok >= T) break;
                     const int sl = sh.slots[m][tok];
-                    cp_async16_zfill(dst + gr / 8 * (T * 128) + swz(tok, gr & 7), rows[is_v] + max(sl, 0) * pitch + (k * row_chunks + gr) * 16,
-                                     sl >= 0);
+                    cp_async16_zfill(dst + gr / 8 * (T * 128) + swz(tok, gr & 7), rows[is_v] + max(sl, 0) * pitch + gr * 16, sl >= 0);
                 }
-                cp_async_arrive(smem_u32(F8 ? &sh.c_full[F8 ? at : 0] : &sh.full[F8 ? 0 : at]));
+                cp_async_arrive(smem_u32(full));
             }
             if (is_v) {
                 __syncwarp();
@@ -564,7 +569,7 @@ __global__ void __launch_bounds__(C::threads, 1)
         auto turn_tile = [&](int c, int turns) { return c == 0 ? 0 : c == turns - 1 ? turns / 2 - 1 : turn_is_v(c, turns) ? c / 2 - 1 : (c + 1) / 2; };
         auto ask = [&]() -> bool {
             if (!more) return true;
-            if (!copy(turn_is_v(cc, nc), gc.i0 + turn_tile(cc, nc), (2 * gc.i0 + cc) * SL)) return false;
+            if (!copy(turn_is_v(cc, nc), gc.i0 + turn_tile(cc, nc), 2 * gc.i0 + cc)) return false;
             if (++cc == nc) {
                 more = wc.next(a, m_tile, gc);
                 cc = 0;
@@ -582,45 +587,59 @@ __global__ void __launch_bounds__(C::threads, 1)
         } else if constexpr (F8) {
             // codes of a turn are asked for `ahead` turns before it is converted. At most 6: a tile's K is asked for when the
             // softmax has left the tile four before it, which needs the V turns up to seven before this one converted.
-            constexpr int ahead = C::codes / SL - 1 < 6 ? C::codes / SL - 1 : 6;
-            auto convert = [&](int q0, bool is_v, int j0, const TreeRow &r, bool some) -> bool {
+            constexpr int ahead = C::codes - 1 < 6 ? C::codes - 1 : 6;
+            // a thread's chunks of 16 codes, the same in every slot: chunk `gr` of token `tok`, and where its two granules go. The
+            // second half of a token's chunks goes in the other order, to other banks than the first half's.
+            constexpr int N = (T * row_chunks + C::workers - 1) / C::workers;
+            uint32_t src[N], dst[N][2];
+            int toks[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int id = i * C::workers + wt, tok = id / row_chunks, gr = id % row_chunks, at = (gr & 3) * 2, swap = gr >> 2 & 1;
+                toks[i] = tok < T ? tok : -1;
+                src[i] = gr / 8 * (T * 128) + swz(tok & (T - 1), gr & 7);
+                dst[i][0] = gr / 4 * (T * 128) + swz(tok & (T - 1), at + swap);
+                dst[i][1] = gr / 4 * (T * 128) + swz(tok & (T - 1), at + 1 - swap);
+            }
+            const bool swap = wt % row_chunks >> 2 & 1;   // the same for every chunk: C::workers is a multiple of row_chunks
+            static_assert(C::workers % row_chunks == 0, "a thread keeps its chunk");
+            auto convert = [&](int q, bool is_v, int j0, const TreeRow &r, bool some) -> bool {
                 // V: rows that nothing attends become zeros, and NaN codes of rows that not every row attends
                 const int edge = a.window > 0 ? r.base + r.T - a.window : 0;
-                for (int k = 0; k < SL; ++k) {
-                    const int q = q0 + k, from = q % C::codes, to = q % RING;
-                    if (!wait_warp(&sh.c_full[from], q / C::codes)) return false;
-                    if (q >= RING && !wait_warp(&sh.empty[to], q / RING - 1)) return false;
-                    constexpr int N = (T * row_chunks + C::workers - 1) / C::workers;
-                    uint4 v[N];
+                if (!wait_warp(&sh.c_full[q % C::codes], q / C::codes)) return false;
+                if (q >= RING && !wait_warp(&sh.empty[q % RING], q / RING - 1)) return false;
+                const uint8_t *from = sm + C::codes_at + q % C::codes * C::code_slot;
+                uint8_t *to = sm + C::ring_at + q % RING * C::slot;
+                constexpr int H = 3;                      // chunks at a time
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const int id = i * C::workers + wt, tok = id / row_chunks, gr = id % row_chunks;
-                        if (tok < T) v[i] = *reinterpret_cast<const uint4 *>(sm + C::codes_at + from * C::code_slot + swz(tok, gr));
-                    }
+                for (int i0 = 0; i0 < N; i0 += H) {
+                    uint4 v[H];
+#pragma unroll
+                    for (int i = 0; i < H; ++i)
+                        if (i0 + i < N) v[i] = *reinterpret_cast<const uint4 *>(from + src[i0 + i]);
                     if (is_v && some)
 #pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const int j = j0 + (i * C::workers + wt) / row_chunks;
+                        for (int i = 0; i < H; ++i) {
+                            if (i0 + i >= N) break;
+                            const int j = j0 + toks[i0 + i];
                             if ((uint32_t)j >= (uint32_t)r.len || j < r.lo)
                                 v[i] = make_uint4(0, 0, 0, 0);
                             else if (j >= r.base || j < edge)
                                 drop_nan_codes(v[i].x), drop_nan_codes(v[i].y), drop_nan_codes(v[i].z), drop_nan_codes(v[i].w);
                         }
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const int id = i * C::workers + wt, tok = id / row_chunks, gr = id % row_chunks;
-                        if (tok >= T) break;
-                        uint8_t *dst = sm + C::ring_at + to * C::slot + (gr >> 2) * (T * 128);
-                        const int at = (gr & 3) * 2;
-                        *reinterpret_cast<uint4 *>(dst + swz(tok, at)) =
-                            make_uint4(e4m3_to_f16x2(v[i].x, 0), e4m3_to_f16x2(v[i].x, 1), e4m3_to_f16x2(v[i].y, 0), e4m3_to_f16x2(v[i].y, 1));
-                        *reinterpret_cast<uint4 *>(dst + swz(tok, at + 1)) =
-                            make_uint4(e4m3_to_f16x2(v[i].z, 0), e4m3_to_f16x2(v[i].z, 1), e4m3_to_f16x2(v[i].w, 0), e4m3_to_f16x2(v[i].w, 1));
+                    for (int i = 0; i < H; ++i) {
+                        if (i0 + i >= N || toks[i0 + i] < 0) break;
+                        const uint4 x = swap ? make_uint4(v[i].z, v[i].w, v[i].x, v[i].y) : v[i];
+                        *reinterpret_cast<uint4 *>(to + dst[i0 + i][0]) =
+                            make_uint4(e4m3_to_f16x2(x.x, 0), e4m3_to_f16x2(x.x, 1), e4m3_to_f16x2(x.y, 0), e4m3_to_f16x2(x.y, 1));
+                        *reinterpret_cast<uint4 *>(to + dst[i0 + i][1]) =
+                            make_uint4(e4m3_to_f16x2(x.z, 0), e4m3_to_f16x2(x.z, 1), e4m3_to_f16x2(x.w, 0), e4m3_to_f16x2(x.w, 1));
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();                         // an arrival for each warp: 192 of them on one word take hundreds of cycles
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.full[to])), mbar_arrive(smem_u32(&sh.c_empty[from]));
                 }
+                fence_proxy_async_smem();
+                __syncwarp();                             // an arrival for each warp: 192 of them on one word take hundreds of cycles
+                if (lane == 0) mbar_arrive(smem_u32(&sh.full[q % RING])), mbar_arrive(smem_u32(&sh.c_empty[q % C::codes]));
                 return true;
             };
             Walk w = walk;
@@ -630,7 +649,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                 for (int c = 0; c < turns && ok; ++c) {
                     const int t = g.ta + turn_tile(c, turns);
                     ok = ask();
-                    if (ok) ok = convert((2 * g.i0 + c) * SL, turn_is_v(c, turns), t * T, g.r, masked(a, g.r, t));
+                    if (ok) ok = convert(2 * g.i0 + c, turn_is_v(c, turns), t * T, g.r, masked(a, g.r, t));
                 }
             }
         }
@@ -732,21 +751,19 @@ __global__ void __launch_bounds__(C::threads, 1)
                         ok = false;
                         break;
                     }
-                    for (int k = 0; k < SL; ++k) {
-                        const int at = ((2 * g.i0 + v_turn(c, n)) * SL + k) % RING;
-                        for (int i = qt; i < T * (SD / 8); i += C::q_threads) {
-                            const int tok = i / (SD / 8), gr = i % (SD / 8), j = t * T + tok;
-                            const bool out = (uint32_t)j >= (uint32_t)g.r.len || j < g.r.lo;
-                            if (!out && j < g.r.base && j >= edge) continue;
-                            uint4 *p = reinterpret_cast<uint4 *>(sm + C::ring_at + at * C::slot + gr / 8 * (T * 128) + swz(tok, gr & 7));
-                            if (out) {
-                                *p = make_uint4(0, 0, 0, 0);
-                            } else {
-                                uint4 v = *p;
-                                if (drop_odd(v)) {
-                                    *p = v;
-                                    flag(j);
-                                }
+                    const int at = (2 * g.i0 + v_turn(c, n)) % RING;
+                    for (int i = qt; i < T * (D / 8); i += C::q_threads) {
+                        const int tok = i / (D / 8), gr = i % (D / 8), j = t * T + tok;
+                        const bool out = (uint32_t)j >= (uint32_t)g.r.len || j < g.r.lo;
+                        if (!out && j < g.r.base && j >= edge) continue;
+                        uint4 *p = reinterpret_cast<uint4 *>(sm + C::ring_at + at * C::slot + gr / 8 * (T * 128) + swz(tok, gr & 7));
+                        if (out) {
+                            *p = make_uint4(0, 0, 0, 0);
+                        } else {
+                            uint4 v = *p;
+                            if (drop_odd(v)) {
+                                *p = v;
+                                flag(j);
                             }
                         }
                     }
@@ -762,7 +779,8 @@ __global__ void __launch_bounds__(C::threads, 1)
                         if ((uint32_t)pg >= (uint32_t)a.n_pages) continue;
                         const int64_t row = ((int64_t)pg * a.page_size + j % a.page_size) * a.Hkv + kvh;
                         uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.v) + row * D + gr * 16);
-                        if (drop_nan_codes(v.x) | drop_nan_codes(v.y) | drop_nan_codes(v.z) | drop_nan_codes(v.w)) flag(j);
+                        if (drop_nan_codes(v.x) | drop_nan_codes(v.y) | drop_nan_codes(v.z) | drop_nan_codes(v.w) | !isfinite(a.v_scales[row * SG + gr / 8]))
+                            flag(j);
                     }
                 }
             }
@@ -788,33 +806,28 @@ __global__ void __launch_bounds__(C::threads, 1)
                     break;
                 }
                 const uint32_t s_at = tmem + C::t_s + (i % NB) * C::s_cols;
-#pragma unroll 1
-                for (int k = 0; k < SL; ++k) {
-                    const int q = (2 * g.i0 + k_turn(c)) * SL + k, at = q % RING;
-                    if (!wait_warp(&sh.full[at], q / RING)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!F8 && !tiled) fence_proxy_async_smem();      // rows by cp.async; TMA needs none, the conversion has its own
-                    tc_fence_after();
-                    const uint64_t bd = tc_desc(ring_at + at * C::slot, 16, 1024), ad = tc_desc(q_at + 2 * k * (kRows * 128), 16, 1024);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int z = 0; z < SD / 16; ++z) {           // 16 dims: 32 bytes on, or in the next block of 64
-                            const uint64_t zd = bd + (z >> 2) * (T * 128 / 16) + (z & 3) * 2;
-                            if (!F8)
-                                tc_mma_ta(s_at, tmem + C::t_q + z * 8, zd, tc_idesc(kRows, T, 0), z > 0);
-                            else
-                                tc_mma(s_at + k * T, ad + (z >> 2) * (kRows * 128 / 16) + (z & 3) * 2, zd, f16_idesc(T, 0), z > 0);
-                        }
-                        tc_commit(smem_u32(&sh.empty[at]));
-                        if (k + 1 == SL) {
-                            tc_commit(smem_u32(&sh.s_full[i % NB]));
-                            if (c + 1 == n) tc_commit(smem_u32(&sh.q_free));
-                        }
-                    }
-                    __syncwarp();
+                const int q = 2 * g.i0 + k_turn(c), at = q % RING;
+                if (!wait_warp(&sh.full[at], q / RING)) {
+                    ok = false;
+                    break;
                 }
+                if (!F8 && !tiled) fence_proxy_async_smem();          // rows by cp.async; TMA needs none, the conversion has its own
+                tc_fence_after();
+                const uint64_t bd = tc_desc(ring_at + at * C::slot, 16, 1024), ad = tc_desc(q_at, 16, 1024);
+                if (elect_one()) {
+#pragma unroll
+                    for (int z = 0; z < D / 16; ++z) {                // 16 dims: 32 bytes on, or in the next block of 64
+                        const uint64_t zd = bd + (z >> 2) * (T * 128 / 16) + (z & 3) * 2;
+                        if (!F8)
+                            tc_mma_ta(s_at, tmem + C::t_q + z * 8, zd, tc_idesc(kRows, T, 0), z > 0);
+                        else
+                            tc_mma(s_at + z / 8 * T, ad + (z >> 2) * (kRows * 128 / 16) + (z & 3) * 2, zd, f16_idesc(T, 0), z % 8 > 0);
+                    }
+                    tc_commit(smem_u32(&sh.empty[at]));
+                    tc_commit(smem_u32(&sh.s_full[i % NB]));
+                    if (c + 1 == n) tc_commit(smem_u32(&sh.q_free));
+                }
+                __syncwarp();
             }
         }
         // the last commit covers every product issued: wait for it before tensor memory is freed
@@ -828,46 +841,42 @@ __global__ void __launch_bounds__(C::threads, 1)
             const int n = g.tb - g.ta;
 #pragma unroll 1
             for (int c = 0; c < n && ok; ++c, ++i) {
-                const int q0 = (2 * g.i0 + v_turn(c, n)) * SL;
+                const int q = 2 * g.i0 + v_turn(c, n), at = q % RING;
                 const bool part = !F8 && masked(a, g.r, g.ta + c);
                 if (part) {
-                    for (int k = 0; k < SL && ok; ++k) ok = wait_warp(&sh.full[(q0 + k) % RING], (q0 + k) / RING);
+                    ok = wait_warp(&sh.full[at], q / RING);
                     if (lane == 0) mbar_arrive(smem_u32(&sh.to_clean));
                 }
                 if (!ok || !wait_warp(&sh.p_full[i % NB], i / NB) || (c == 0 && seg > 0 && !wait_warp(&sh.o_free, seg - 1)) ||
-                    (part && !wait_warp(&sh.clean, cleaned++))) {
+                    !wait_warp(part ? &sh.clean : &sh.full[at], part ? cleaned++ : q / RING)) {
                     ok = false;
                     break;
                 }
+                if (!F8 && !tiled) fence_proxy_async_smem();
+                tc_fence_after();
                 const uint32_t p_at = tmem + C::t_s + (i % NB) * C::s_cols;
-#pragma unroll 1
-                for (int k = 0; k < SL; ++k) {
-                    const int q = q0 + k, at = q % RING;
-                    if (!wait_warp(&sh.full[at], q / RING)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!F8 && !tiled) fence_proxy_async_smem();
-                    tc_fence_after();
-                    const uint64_t bd = tc_desc(ring_at + at * C::slot, T * 128, 1024);
-                    const uint32_t p_set = p_at + (F8 ? k * (T / 2) : 0);
-                    if (elect_one()) {
+                const uint64_t bd = tc_desc(ring_at + at * C::slot, T * 128, 1024);
+                if (elect_one()) {
 #pragma unroll
-                        for (int z = 0; z < T / 16; ++z)              // 16 tokens are 2,048 bytes
-                            tc_mma_ta(tmem + C::t_o + k * SD, p_set + z * 8, bd + z * 128, F8 ? f16_idesc(SD, 1) : tc_idesc(kRows, SD, 1),
-                                      c > 0 || z > 0);
-                        tc_commit(smem_u32(&sh.empty[at]));
-                        if (k + 1 == SL) tc_commit(smem_u32(&sh.pv_done[i % NB]));
-                    }
-                    __syncwarp();
+                    for (int z = 0; z < T / 16; ++z)                  // 16 tokens are 2,048 bytes; each set of weights has its 128 dims
+#pragma unroll
+                        for (int x = 0; x < SG; ++x)
+                            tc_mma_ta(tmem + C::t_o + x * 128, p_at + x * (T / 2) + z * 8, bd + z * 128 + x * (2 * T * 128 / 16),
+                                      F8 ? f16_idesc(128, 1) : tc_idesc(kRows, D, 1), c > 0 || z > 0);
+                    tc_commit(smem_u32(&sh.empty[at]));
+                    tc_commit(smem_u32(&sh.pv_done[i % NB]));
                 }
+                __syncwarp();
             }
         }
         if (i > 0 && lane == 0) wait_turn(smem_u32(&sh.pv_done[(i - 1) % NB]), (uint32_t)((i - 1) / NB) & 1u, a.hdr);
     } else {
         // ================================================================ softmax
-        const uint32_t t_row = tmem + ((uint32_t)(32 * warp) << 16), t_o = t_row + C::t_o;
-        const int row = tid;
+        // A row has two threads, each for half of a tile's tokens and half of O's columns, in warps that reach the same quarter of
+        // the lanes; they exchange the maxima of a tile, and their sums at the end.
+        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+        const uint32_t t_row = tmem + ((uint32_t)(32 * quarter) << 16), t_o = t_row + C::t_o;
+        auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(4 + quarter) : "memory"); };
         Walk w = walk;
         int seg = 0;
         bool ok = true;
@@ -878,42 +887,36 @@ __global__ void __launch_bounds__(C::threads, 1)
             if (!wait_warp(&sh.nodes_full, seg)) break;
             const int lo = sh.lo[min(node, g.r.T - 1)];
             const float scale = F8 ? a.scale_log2 * sh.q_scale[seg & 1][F8 ? row : 0] : a.scale_log2;
-            float ref = -INFINITY, l = 0.f;               // the lazy maximum, and the weights' sum relative to it
+            float ref = -INFINITY, l = 0.f;               // the lazy maximum, and this thread's weights' sum relative to it
             float2 unit = make_float2(0.f, 0.f);          // FP8: O is in units of these over 2^kRaise
+#pragma unroll 1
             for (int c = 0; c < n; ++c) {
                 const int i = g.i0 + c, t = g.ta + c, m = i % kMetas;
                 if (!wait_warp(&sh.meta_full[m], i / kMetas)) {
                     ok = false;
                     break;
                 }
-                // which of the tile's tokens this row attends
-                constexpr int W = T / 32;
-                uint32_t see[W], both = ~0u;
-                const bool part = masked(a, g.r, t);
-#pragma unroll
-                for (int x = 0; x < W; ++x) {
-                    see[x] = sh.real[m][x];
-                    if (part) {
-                        const int j = t * T + 32 * x, from = lo - j, to = g.r.base - j;
-                        uint32_t v = to >= 32 ? ~0u : to > 0 ? (1u << to) - 1u : 0u;
-                        if (from >= 32)
-                            v = 0u;
-                        else if (from > 0)
-                            v &= ~0u << from;
-                        const int o = -to;                // place of bit 0 among the drafts
-                        if (o > -32 && o < QSA_MAX_DRAFT && valid) {
-                            if (o < 0) {
-                                v |= sh.kin[node][0] << -o;
-                            } else {
-                                v |= sh.kin[node][o >> 5] >> (o & 31);
-                                if ((o & 31) && (o >> 5) < QSA_MAX_DRAFT / 32 - 1) v |= sh.kin[node][(o >> 5) + 1] << (32 - (o & 31));
-                            }
+                // which of this half's tokens the row attends
+                uint32_t see = sh.real[m][half];
+                if (masked(a, g.r, t)) {
+                    const int j = t * T + 32 * half, from = lo - j, to = g.r.base - j;
+                    uint32_t v = to >= 32 ? ~0u : to > 0 ? (1u << to) - 1u : 0u;
+                    if (from >= 32)
+                        v = 0u;
+                    else if (from > 0)
+                        v &= ~0u << from;
+                    const int o = -to;                    // place of bit 0 among the drafts
+                    if (o > -32 && o < QSA_MAX_DRAFT && valid) {
+                        if (o < 0) {
+                            v |= sh.kin[node][0] << -o;
+                        } else {
+                            v |= sh.kin[node][o >> 5] >> (o & 31);
+                            if ((o & 31) && (o >> 5) < QSA_MAX_DRAFT / 32 - 1) v |= sh.kin[node][(o >> 5) + 1] << (32 - (o & 31));
                         }
-                        see[x] &= v;
                     }
-                    both &= see[x];
+                    see &= v;
                 }
-                const bool all = __all_sync(0xffffffffu, both == ~0u || !valid);       // no token to mask in this warp
+                const bool all = __all_sync(0xffffffffu, see == ~0u || !valid);        // no token to mask in this warp
                 if (!wait_warp(&sh.s_full[i % NB], i / NB)) {
                     ok = false;
                     break;
@@ -921,78 +924,66 @@ __global__ void __launch_bounds__(C::threads, 1)
                 tc_fence_after();
                 const uint32_t t_s = t_row + C::t_s + (i % NB) * C::s_cols;
                 float f = 1.f;
-                float2 was = unit;
+                const float2 was = unit;
+                if (F8) unit = sh.top[m];
                 if (some) {
-                    float v[2][32];
-                    tmem_ld32_async(t_s, v[0]);
-                    tmem_ld32_async(t_s + 32, v[1]);
-                    tmem_wait_ld(v[0]);
-                    tmem_wait_ld(v[1]);
-                    if (F8) {
-                        auto times = [&](float (&x)[32], int h, int set, const float (*plus)[32]) {       // x scale (+ plus)
+                    float v[32];
+                    tmem_ld32(t_s + 32 * half, v);
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 s4 = sh.k_scales[m][0][half * 8 + k];
+                            v[4 * k] *= s4.x, v[4 * k + 1] *= s4.y, v[4 * k + 2] *= s4.z, v[4 * k + 3] *= s4.w;
+                        }
+                        if constexpr (SG == 2) {
+                            float u[32];
+                            tmem_ld32(t_s + 64 + 32 * half, u);
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
-                                const float4 s4 = sh.k_scales[m][set][F8 ? h * 8 + k : 0];
-                                x[4 * k] = plus ? fmaf(x[4 * k], s4.x, (*plus)[4 * k]) : x[4 * k] * s4.x;
-                                x[4 * k + 1] = plus ? fmaf(x[4 * k + 1], s4.y, (*plus)[4 * k + 1]) : x[4 * k + 1] * s4.y;
-                                x[4 * k + 2] = plus ? fmaf(x[4 * k + 2], s4.z, (*plus)[4 * k + 2]) : x[4 * k + 2] * s4.z;
-                                x[4 * k + 3] = plus ? fmaf(x[4 * k + 3], s4.w, (*plus)[4 * k + 3]) : x[4 * k + 3] * s4.w;
-                            }
-                        };
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) times(v[h], h, 0, nullptr);
-                        if constexpr (SG == 2) {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float u[32];
-                                tmem_ld32(t_s + 64 + 32 * h, u);
-                                times(u, h, SG - 1, &v[h]);
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) v[h][k] = u[k];
+                                const float4 s4 = sh.k_scales[m][1][half * 8 + k];
+                                v[4 * k] = fmaf(u[4 * k], s4.x, v[4 * k]), v[4 * k + 1] = fmaf(u[4 * k + 1], s4.y, v[4 * k + 1]);
+                                v[4 * k + 2] = fmaf(u[4 * k + 2], s4.z, v[4 * k + 2]), v[4 * k + 3] = fmaf(u[4 * k + 3], s4.w, v[4 * k + 3]);
                             }
                         }
-                        unit = sh.top[m];
                     }
                     if (!all)
 #pragma unroll
-                        for (int k = 0; k < 64; ++k) v[k >> 5][k & 31] = (see[k >> 5] >> (k & 31)) & 1u ? v[k >> 5][k & 31] : -INFINITY;
+                        for (int k = 0; k < 32; ++k) v[k] = (see >> k) & 1u ? v[k] : -INFINITY;
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) mx[k & 3] = fmaxf(mx[k & 3], v[k >> 5][k & 31]);
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                    for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], v[k]);
+                    const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                    sh.tops[i & 1][half][row] = mine;
+                    meet();                               // both halves have read their scores, too
+                    const float top = fmaxf(mine, sh.tops[i & 1][half ^ 1][row]);
                     if (top > ref + kLazy) {
                         if (ref != -INFINITY) f = ex2(ref - top);
                         ref = top;
                     }
                     const float at = ref == -INFINITY ? 0.f : ref;
-                    l *= f;
                     float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) {
-                        float &x = v[k >> 5][k & 31];
-                        x = ex2(fmaf(x, scale, -at));
-                        ps[k & 3] += x;
+                    for (int k = 0; k < 32; ++k) {
+                        v[k] = ex2(fmaf(v[k], scale, -at));
+                        ps[k & 3] += v[k];
                     }
-                    l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-                    uint32_t pk[32];
-                    if (!F8) {
+                    l = fmaf(l, f, (ps[0] + ps[1]) + (ps[2] + ps[3]));
+                    if constexpr (!F8) {
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) pk[k] = bf16x2(v[k >> 4][2 * k & 31], v[k >> 4][(2 * k & 31) + 1]);
-                        tmem_st32(t_s, pk);               // over scores that have been read
+                        for (int k = 0; k < 16; ++k) pk[k] = bf16x2(v[2 * k], v[2 * k + 1]);
+                        tmem_st16(t_s + 16 * half, pk);   // over scores that have been read
                     } else {
 #pragma unroll
                         for (int x = 0; x < SG; ++x) {
+                            uint32_t pk[16];
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float4 s4 = sh.v_scales[m][x][F8 ? k : 0];
-                                float w4[4] = {v[k >> 3][4 * k & 31] * s4.x, v[k >> 3][(4 * k & 31) + 1] * s4.y,
-                                               v[k >> 3][(4 * k & 31) + 2] * s4.z, v[k >> 3][(4 * k & 31) + 3] * s4.w};
-                                if (!all)                 // whatever a masked token's scale is
-#pragma unroll
-                                    for (int y = 0; y < 4; ++y) w4[y] = (see[k >> 3] >> ((4 * k & 31) + y)) & 1u ? w4[y] : 0.f;
-                                pk[2 * k] = f16x2(w4[0], w4[1]), pk[2 * k + 1] = f16x2(w4[2], w4[3]);
+                            for (int k = 0; k < 8; ++k) {
+                                const float4 s4 = sh.v_scales[m][x][half * 8 + k];
+                                pk[2 * k] = f16x2(v[4 * k] * s4.x, v[4 * k + 1] * s4.y);
+                                pk[2 * k + 1] = f16x2(v[4 * k + 2] * s4.z, v[4 * k + 3] * s4.w);
                             }
-                            tmem_st32(t_s + x * 32, pk);
+                            tmem_st16(t_s + 32 * x + 16 * half, pk);
                         }
                     }
                 }
@@ -1004,7 +995,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                     }
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
+                    for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
                         float v[32];
                         const float by = !F8 ? f : c0 < 128 ? f * (was.x / unit.x) : f * (was.y / unit.y);
                         tmem_ld32(t_o + c0, v);
@@ -1022,19 +1013,23 @@ __global__ void __launch_bounds__(C::threads, 1)
             const int i = g.i0 + n - 1;
             if (!wait_warp(&sh.pv_done[i % NB], i / NB) || !wait_warp(&sh.flags_full, seg)) break;
             tc_fence_after();
-            const bool whole = g.begins && g.ends;
-            const float by = l == 0.f ? 0.f : (whole ? 1.f / l : 1.f) * (F8 ? 1.f / (1 << (int)kRaise) : 1.f);
-            // values that are not finite, of attended tokens that not every row attends
-            bool strange = false;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                strange |= valid && ((sh.odd[0][x] & sh.kin[min(node, QSA_MAX_DRAFT - 1)][x]) | sh.odd[1][x]) != 0u;
-            const int64_t at = (int64_t)(2 * range + (g.begins ? 1 : 0)) * a.Hkv * plan.m_tiles + kvh * plan.m_tiles + m_tile;
-            float *po = ws.o + (at * kRows + row) * D;
-            uint16_t *dst = a.out + ((int64_t)(g.r.off + min(node, g.r.T - 1)) * a.Hq + head) * D;
             if (some) {
+                sh.tops[(i & 1) ^ 1][half][row] = l;      // the sums, where the maxima two tiles back were
+                meet();
+                l = half == 0 ? l + sh.tops[(i & 1) ^ 1][1][row] : sh.tops[(i & 1) ^ 1][0][row] + l;
+                meet();
+                const bool whole = g.begins && g.ends;
+                const float by = l == 0.f ? 0.f : (whole ? 1.f / l : 1.f) * (F8 ? 1.f / (1 << (int)kRaise) : 1.f);
+                // values that are not finite, of attended tokens that not every row attends
+                bool strange = false;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    strange |= valid && ((sh.odd[0][x] & sh.kin[min(node, QSA_MAX_DRAFT - 1)][x]) | sh.odd[1][x]) != 0u;
+                const int64_t at = (int64_t)(2 * range + (g.begins ? 1 : 0)) * a.Hkv * plan.m_tiles + kvh * plan.m_tiles + m_tile;
+                float *po = ws.o + (at * kRows + row) * D;
+                uint16_t *dst = a.out + ((int64_t)(g.r.off + min(node, g.r.T - 1)) * a.Hq + head) * D;
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
                     float v[32];
                     const float times = !F8 ? by : by * (c0 < 128 ? unit.x : unit.y);
                     __syncwarp();
@@ -1053,8 +1048,8 @@ __global__ void __launch_bounds__(C::threads, 1)
                             *reinterpret_cast<float4 *>(po + c0 + 4 * k) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                     }
                 }
-                if (strange) add_odd<D, F8>(a, g, sh.odd, sh.kin[node], lo, kvh, whole, dst, po);
-                if (valid) {
+                if (strange) add_odd<D, F8>(a, g, sh.odd, sh.kin[node], lo, kvh, half * (D / 2), whole, dst, po);
+                if (valid && half == 0) {
                     if (!whole)
                         ws.ml[at * kRows + row] = make_float2(ref, l);
                     else if (a.lse)
@@ -1062,8 +1057,8 @@ __global__ void __launch_bounds__(C::threads, 1)
                 }
             }
             tc_fence_before();
-            mbar_arrive(smem_u32(&sh.o_free));
-            mbar_arrive(smem_u32(&sh.nodes_free));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.o_free)), mbar_arrive(smem_u32(&sh.nodes_free));
         }
     }
     tc_fence_before();
@@ -1215,7 +1210,7 @@ cudaError_t launch(const TreeArgs &a, cudaStream_t st) {
     if (run >= 16 && rows > 0) {
         plan.run = run;
         const uint64_t row = (uint64_t)a.Hkv * D * (F8 ? 1 : 2);
-        const uint32_t blocks = !F8 && run == kTile ? C::SD / 64 : 1;
+        const uint32_t blocks = run == kTile ? D * (F8 ? 1 : 2) / 128 : 1;
         if (!encode_tmap_rows(&maps.k, a.k, F8, rows, row / 128, row, run, blocks) ||
             !encode_tmap_rows(&maps.v, a.v, F8, rows, row / 128, row, run, blocks))
             return cudaErrorInvalidValue;
