@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kKeepThreads = 256;
 constexpr int kSelectThreads = 512, kSelectCluster = 8;
+constexpr int kSmallThreads = 1024, kSmallKeys = 16;  // rows of up to 16,384 places: one CTA, 16 keys in registers a thread
 constexpr int kDigit = 11, kBins = 1 << kDigit;      // of the radix selection: 11, 11 and 10 bits of a key
 constexpr uint32_t kAlways = 0xFFFFFFFFu;            // key of a token that is always kept
 
@@ -401,6 +402,159 @@ __global__ void __cluster_dims__(kSelectCluster, 1, 1) __launch_bounds__(kSelect
     cluster_sync();                                  // no CTA's shared memory goes while another reads it
 }
 
+// Rows of at most kSmallThreads kSmallKeys places: one CTA for a row, its keys in registers, so that each pass of the selection
+// costs two barriers and no memory. Key i of thread x is that of place 1,024 i + x. 32 rows of 4,080 tokens: 20 us a call, the
+// moves among them, with the cluster's kernel 86; 16 rows of 14,000: 81 and 132.
+__global__ void __launch_bounds__(kSmallThreads) evict_small_kernel(KeepArgs a, EvictArgs e, KeepScratch s) {
+    constexpr int W = kSmallThreads / 32;
+    __shared__ uint32_t hist[kBins];
+    __shared__ uint2 counts[kSmallKeys * W];         // keys above and equal of each warp's 32 places, then those before them
+    __shared__ uint2 sums[W];
+    __shared__ int tops[W];
+    __shared__ uint32_t pick[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x;
+    wait_for_previous();
+    for (int64_t p = (int64_t)r * kSmallThreads + tid; p < a.n_pages; p += (int64_t)gridDim.x * kSmallThreads) a.ref_out[p] = a.ref[p];
+    const int len = a.seq_len[r];
+    const bool ok = len >= 0 && len <= a.ld * a.page_size && len <= e.tokens_ld;
+    const int64_t row_at = r * e.tokens_ld;
+    const float *w = e.weights + row_at;
+    const int32_t *pos = e.positions + row_at;
+    float *w_out = e.weights_out + row_at;
+    int32_t *pos_out = e.positions_out + row_at;
+    if (!ok || e.budget[r] < 0 || e.budget[r] >= len) {      // nothing to drop
+        for (int64_t j = tid; j < e.tokens_ld; j += kSmallThreads) {
+            const bool in = !ok || j < len;
+            w_out[j] = in ? w[j] : 0.f;
+            pos_out[j] = in ? pos[j] : -1;
+        }
+        if (tid == 0) {
+            if (!ok) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereKeep, r);
+            s.cut[r] = {ok ? len : -1, 0};
+            a.seq_len_out[r] = len;
+        }
+        return;
+    }
+    const int32_t *row = a.table + r * a.ld;
+    int p[kSmallKeys], top = INT32_MIN;
+#pragma unroll
+    for (int i = 0; i < kSmallKeys; ++i) {
+        const int j = i * kSmallThreads + tid;
+        p[i] = j < len ? pos[j] : INT32_MIN;
+        top = max(top, p[i]);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) tops[warp] = top;
+    uint32_t keys[kSmallKeys], shared = 0, bad = 0;  // shared: a bit for each key
+#pragma unroll
+    for (int i = 0; i < kSmallKeys; ++i) {
+        const int j = i * kSmallThreads + tid;
+        keys[i] = 0;
+        if (j < len) {
+            const int page = row[a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size];
+            const bool real = (uint32_t)page < (uint32_t)a.n_pages;
+            bad |= !real;
+            if (real && a.ref[page] > 1) shared |= 1u << i;
+            keys[i] = key_of(w[j]);
+        }
+    }
+    if (bad) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereKeep, r);
+    for (int i = tid; i < kBins; i += kSmallThreads) hist[i] = 0;
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, tops[lane]);
+    uint32_t always = 0;
+#pragma unroll
+    for (int i = 0; i < kSmallKeys; ++i)
+        if (i * kSmallThreads + tid < len && (p[i] < e.first || (int64_t)p[i] > (int64_t)top - e.recent || (shared >> i & 1u)))
+            keys[i] = kAlways, ++always;
+    always = __reduce_add_sync(0xffffffffu, always);
+    if (lane == 0) sums[warp].x = always;
+    __syncthreads();
+    const uint32_t P = __reduce_add_sync(0xffffffffu, sums[lane].x);
+    const int K = max(e.budget[r], (int)P);          // P <= len, budget < len
+    uint32_t need = K - P, key = kAlways;            // tokens to keep among the others, the last one's key
+    if (need > 0) {
+        uint32_t prefix = 0, known = 0;              // the key's upper bits
+#pragma unroll 1
+        for (int step = 0; step < 3; ++step) {
+            const int bits = step == 2 ? 10 : kDigit, shift = step == 0 ? 21 : step == 1 ? 10 : 0;
+#pragma unroll
+            for (int i = 0; i < kSmallKeys; ++i)
+                if (i * kSmallThreads + tid < len && keys[i] != kAlways && (keys[i] & known) == prefix)
+                    atomicAdd(&hist[(keys[i] >> shift) & ((1u << bits) - 1u)], 1u);
+            __syncthreads();
+            // bins from the highest down, two each thread
+            const uint32_t n0 = hist[kBins - 1 - 2 * tid], n1 = hist[kBins - 2 - 2 * tid];
+            uint32_t upto = n0 + n1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            if (lane == 31) sums[warp].y = upto;
+            hist[kBins - 1 - 2 * tid] = hist[kBins - 2 - 2 * tid] = 0;      // its own, for the next pass
+            __syncthreads();
+            uint32_t before = upto - n0 - n1 + __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane].y : 0u);
+            if (before < need && need <= before + n0) pick[0] = kBins - 1 - 2 * tid, pick[1] = need - before;
+            before += n0;
+            if (before < need && need <= before + n1) pick[0] = kBins - 2 - 2 * tid, pick[1] = need - before;
+            __syncthreads();
+            prefix |= pick[0] << shift;
+            known |= ((1u << bits) - 1u) << shift;
+            need = pick[1];
+        }
+        key = prefix;
+    }
+    // ---- keys above and equal before each warp's 32 places of each round
+    uint32_t overs[kSmallKeys], sames[kSmallKeys];
+#pragma unroll
+    for (int i = 0; i < kSmallKeys; ++i) {
+        const bool in = i * kSmallThreads + tid < len;
+        overs[i] = __ballot_sync(0xffffffffu, in && (keys[i] > key || keys[i] == kAlways));
+        sames[i] = __ballot_sync(0xffffffffu, in && keys[i] == key && keys[i] != kAlways);
+        if (lane == 0) counts[i * W + warp] = make_uint2(__popc(overs[i]), __popc(sames[i]));
+    }
+    __syncthreads();
+    uint2 mine = make_uint2(0, 0), run;
+    if (tid < kSmallKeys * W) mine = counts[tid];
+    run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, run.x, o), y = __shfl_up_sync(0xffffffffu, run.y, o);
+        if (lane >= o) run.x += x, run.y += y;
+    }
+    if (lane == 31) sums[warp] = run;
+    __syncthreads();
+    const uint2 part = lane < warp ? sums[lane] : make_uint2(0, 0);
+    run.x += __reduce_add_sync(0xffffffffu, part.x) - mine.x;
+    run.y += __reduce_add_sync(0xffffffffu, part.y) - mine.y;
+    if (tid < kSmallKeys * W) counts[tid] = run;
+    __syncthreads();
+    const int64_t list = r * s.half;
+#pragma unroll
+    for (int i = 0; i < kSmallKeys; ++i) {
+        const int j = i * kSmallThreads + tid;
+        if (j >= len) break;
+        const uint2 at = counts[i * W + warp];
+        const uint32_t below = (1u << lane) - 1u;
+        const uint32_t equal = at.y + __popc(sames[i] & below);
+        const int before = (int)(at.x + __popc(overs[i] & below) + min(equal, need));
+        const bool kept = (overs[i] >> lane & 1u) || ((sames[i] >> lane & 1u) && equal < need);
+        if (j < K && kept) w_out[j] = w[j], pos_out[j] = p[i];
+        if (j < K && !kept) s.holes[list + j - before] = make_int2(j, slot_of(a, row, j));
+        if (j >= K) {
+            w_out[j] = 0.f, pos_out[j] = -1;
+            if (kept) s.fillers[list + K - 1 - before] = make_int2(j, slot_of(a, row, j));
+        }
+        if (j == K - 1) s.cut[r] = {K, K - before - (int)kept};
+    }
+    for (int64_t j = len + tid; j < e.tokens_ld; j += kSmallThreads) w_out[j] = 0.f, pos_out[j] = -1;
+    if (tid == 0) {
+        a.seq_len_out[r] = K;
+        if (K == 0) s.cut[r] = {0, 0};
+    }
+}
+
 template <typename W>
 __device__ __forceinline__ void move_tokens(const PlaneGroup &g, int page_size, const int2 *holes, const int2 *fillers, int n,
                                             int warp, int warps) {
@@ -409,13 +563,15 @@ __device__ __forceinline__ void move_tokens(const PlaneGroup &g, int page_size, 
     int group = 32;                                  // lanes for a token
     while (group > 1 && group / 2 >= words) group /= 2;
     const int each = 32 / group, mine = lane / group, first = lane % group;
-    for (int plane = 0; plane < g.n_planes; ++plane)
-        for (int k = warp * each + mine; k < n; k += warps * each) {
-            const int to = holes[k].y, from = fillers[n - 1 - k].y;
-            if (to < 0 || from < 0) continue;
-            for (int w = first; w < words; w += group)
-                *token_word<W>(g.src, g.src_stride, plane, to, bytes, w) = *token_word<W>(g.src, g.src_stride, plane, from, bytes, w);
-        }
+    // (plane, move) pairs, so that few moves in many planes are copied at once too
+    const int64_t units = (int64_t)g.n_planes * n;
+    for (int64_t u = (int64_t)warp * each + mine; u < units; u += (int64_t)warps * each) {
+        const int plane = units >> 31 ? (int)(u / n) : (int)((uint32_t)u / (uint32_t)n), k = (int)(u - (int64_t)plane * n);
+        const int to = holes[k].y, from = fillers[n - 1 - k].y;
+        if (to < 0 || from < 0) continue;
+        for (int w = first; w < words; w += group)
+            *token_word<W>(g.src, g.src_stride, plane, to, bytes, w) = *token_word<W>(g.src, g.src_stride, plane, from, bytes, w);
+    }
 }
 
 // CTA (row, part): the row's moves, which are independent of each other (tokens behind the new length into places before it).
@@ -478,8 +634,10 @@ cudaError_t launch_evict_tokens(const KeepArgs &a, const EvictArgs &e, const Pla
                         : cudaSuccess;
     }
     const KeepScratch s = keep_scratch(a.scratch, a.n_rows, e.tokens_ld);
-    const cudaError_t err = launch_dependent(evict_select_kernel, dim3((unsigned)a.n_rows * kSelectCluster), kSelectThreads, 0, st,
-                                             a, e, s);
+    const cudaError_t err =
+        e.tokens_ld <= kSmallThreads * kSmallKeys
+            ? launch_dependent(evict_small_kernel, dim3((unsigned)a.n_rows), kSmallThreads, 0, st, a, e, s)
+            : launch_dependent(evict_select_kernel, dim3((unsigned)a.n_rows * kSelectCluster), kSelectThreads, 0, st, a, e, s);
     if (err != cudaSuccess) return err;
     const int parts = parts_of(a.n_rows);
     return launch_dependent(evict_move_kernel, dim3((unsigned)a.n_rows * parts), kKeepThreads, 0, st, a, e, s, p, parts);

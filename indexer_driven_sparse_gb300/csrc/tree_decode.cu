@@ -1207,7 +1207,7 @@ cudaError_t launch(const TreeArgs &a, cudaStream_t st) {
     TreeMaps maps;
     memset(&maps, 0, sizeof(maps));
     const int64_t rows = a.n_pages * a.page_size;
-    if (run >= 16 && rows > 0) {
+    if (run >= (F8 ? 4 : 16) && rows > 0) {
         plan.run = run;
         const uint64_t row = (uint64_t)a.Hkv * D * (F8 ? 1 : 2);
         const uint32_t blocks = run == kTile ? D * (F8 ? 1 : 2) / 128 : 1;
