@@ -53,14 +53,14 @@ struct TreeCfg {
     static constexpr bool F8 = F8_;
     static constexpr int SG = F8 ? D / 128 : 1;                 // scales of a row, sets of weights
     static constexpr int slot = kTile * D * 2, code_slot = F8 ? kTile * D : 0;      // bytes: a tile's K or V
-    static constexpr int ring = F8 ? (D == 256 ? 3 : 6) : D == 64 ? 24 : 212992 / slot;
-    static constexpr int codes = F8 ? (D == 256 ? 3 : 10) : 0;
-    static constexpr int from = F8 ? codes : ring;              // slots that global memory is read into
-    static constexpr int ring_at = F8 ? kRows * D * 2 : 0, codes_at = ring_at + ring * slot;
-    static constexpr int smem = codes_at + codes * code_slot + 1024;
+    // bf16 rows: one ring for K and V. FP8 rows: K's codes, V's codes, and V as f16 operands, each in a ring of its own.
+    static constexpr int ring = F8 ? 2 : D == 64 ? 24 : 212992 / slot;
+    static constexpr int k_ring = F8 ? (D == 256 ? 3 : 6) : 0, v_ring = F8 ? (D == 256 ? 2 : 6) : 0;
+    static constexpr int ring_at = F8 ? kRows * D * 2 : 0, k_at = ring_at + ring * slot, v_at = k_at + k_ring * code_slot;
+    static constexpr int smem = v_at + v_ring * code_slot + 1024;
     static_assert(smem + 12288 <= 227 * 1024, "shared memory of a CTA");
     // tensor memory columns: O, the queries (bf16 rows; with FP8 rows they are in shared memory), buffers of scores
-    static constexpr uint32_t t_o = 0, t_q = D, t_s = D == 256 && !F8 ? 384 : 256, s_cols = SG * kTile;
+    static constexpr uint32_t t_o = 0, t_q = F8 ? 0 : D, t_s = D == 256 && !F8 ? 384 : 256, s_cols = SG * kTile;
     static constexpr int buffers = (512 - t_s) / s_cols;
     // 20 warps of 96 registers; the query warps' numbers modulo 4 are the four quarters of tensor memory's lanes
     static constexpr int softmax = 256, q_threads = F8 ? 64 : 128, workers = F8 ? 192 : 160;
@@ -159,7 +159,7 @@ __device__ __forceinline__ bool masked(const TreeArgs &a, const TreeRow &r, int 
 template <typename C>
 struct TreeShared {
     uint64_t full[C::ring], empty[C::ring];
-    uint64_t c_full[C::F8 ? C::codes : 1], c_empty[C::F8 ? C::codes : 1];
+    uint64_t k_full[C::F8 ? C::k_ring : 1], k_empty[C::F8 ? C::k_ring : 1], v_full[C::F8 ? C::v_ring : 1], v_empty[C::F8 ? C::v_ring : 1];
     uint64_t s_full[C::buffers], p_full[C::buffers], pv_done[C::buffers], meta_full[kMetas], meta_empty[kMetas];
     uint64_t to_clean, clean, q_full, q_free, nodes_full, nodes_free, flags_full, o_free;
     uint32_t kin[QSA_MAX_DRAFT][QSA_MAX_DRAFT / 32];      // of each drafted token: itself and its ancestors inside the window
@@ -178,6 +178,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int x
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Operands in shared memory, both E4M3 (the descriptor's format bits are zero, as f16's are for kind::f16); 32 bytes of K.
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0)
         : "memory");
 }
 
@@ -281,7 +290,7 @@ __global__ void __launch_bounds__(C::threads, 1)
     __shared__ long long scan[C::threads / 32];
     __shared__ int start[3];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    const uint32_t q_at = smem_u32(sm), ring_at = q_at + C::ring_at, codes_at = q_at + C::codes_at;
+    const uint32_t q_at = smem_u32(sm), ring_at = q_at + C::ring_at;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int m_tile = blockIdx.x % plan.m_tiles, kvh = blockIdx.x / plan.m_tiles % a.Hkv, range = blockIdx.x / plan.m_tiles / a.Hkv;
     const bool speaks = kvh == 0 && m_tile == 0;          // records errors that all CTAs of a range see
@@ -295,10 +304,11 @@ __global__ void __launch_bounds__(C::threads, 1)
             mbar_init(smem_u32(&sh.full[i]), F8 ? C::workers / 32 : load);
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
-        if (F8)
-            for (int i = 0; i < C::codes; ++i) {
-                mbar_init(smem_u32(&sh.c_full[i]), load);
-                mbar_init(smem_u32(&sh.c_empty[i]), C::workers / 32);
+        if constexpr (F8)
+            for (int i = 0; i < C::k_ring + C::v_ring; ++i) {
+                const bool k = i < C::k_ring;
+                mbar_init(smem_u32(k ? &sh.k_full[i] : &sh.v_full[i - C::k_ring]), load);
+                mbar_init(smem_u32(k ? &sh.k_empty[i] : &sh.v_empty[i - C::k_ring]), k ? 1 : C::workers / 32);
             }
         for (int i = 0; i < C::buffers; ++i) {
             mbar_init(smem_u32(&sh.s_full[i]), 1);
@@ -525,18 +535,20 @@ __global__ void __launch_bounds__(C::threads, 1)
         constexpr int blocks = row_chunks / 8;                // 128-byte blocks of a row
         const int rows_end = (int)min((int64_t)INT32_MAX, a.n_pages * a.page_size);
         const int boxes = tiled ? T / plan.run : 1, whole = boxes == 1 ? 1 : blocks, run = lane % boxes, block = lane / boxes;
-        int asked = 0;                                        // slots asked for
+        int asked[2] = {0, 0};                                // slots asked for, of each ring
         // a tile's K or V into the slot of turn q
         auto copy = [&](int is_v, int tile, int q) -> bool {
             const int m = tile % kMetas;
             if (!is_v && !wait_warp(&sh.meta_full[m], tile / kMetas)) return false;
             const int box = sh.slots[m][tiled ? run * plan.run : 0], y = box < 0 ? rows_end : box;
-            const int at = q % C::from, turn = q / C::from;
-            uint64_t *full = F8 ? &sh.c_full[F8 ? at : 0] : &sh.full[F8 ? 0 : at];
-            if (turn > 0 && !wait_warp(F8 ? &sh.c_empty[F8 ? at : 0] : &sh.empty[F8 ? 0 : at], turn - 1)) return false;
-            const uint32_t dst = F8 ? codes_at + at * C::code_slot : ring_at + at * C::slot;
+            // FP8 rows: rings of their own, by tiles; bf16 rows: one, by turns
+            const int slots = F8 ? (is_v ? C::v_ring : C::k_ring) : RING, x = F8 ? tile : q, at = x % slots, turn = x / slots;
+            uint64_t *full = F8 ? (is_v ? &sh.v_full[F8 ? at : 0] : &sh.k_full[F8 ? at : 0]) : &sh.full[F8 ? 0 : at];
+            if (turn > 0 && !wait_warp(F8 ? (is_v ? &sh.v_empty[F8 ? at : 0] : &sh.k_empty[F8 ? at : 0]) : &sh.empty[F8 ? 0 : at], turn - 1))
+                return false;
+            const uint32_t dst = F8 ? q_at + (is_v ? C::v_at : C::k_at) + at * C::code_slot : ring_at + at * C::slot;
             if (tiled) {
-                asked = q + 1;
+                asked[F8 ? is_v : 0] = x + 1;
                 if (lane == 0) mbar_arrive_expect_tx(smem_u32(full), F8 ? C::code_slot : C::slot);
                 __syncwarp();
                 if (block < whole)
@@ -582,12 +594,17 @@ __global__ void __launch_bounds__(C::threads, 1)
 #pragma unroll 1
             while (ok && more) ok = ask();
             // no load may still be writing shared memory when the CTA ends (bounded waits; they are over unless a role gave up)
-            for (int q = max(0, asked - C::from); q < asked; ++q)
-                wait_turn(smem_u32(F8 ? &sh.c_full[F8 ? q % C::from : 0] : &sh.full[F8 ? 0 : q % C::from]), (uint32_t)(q / C::from) & 1u, a.hdr);
+            for (int x = 0; x < (F8 ? 2 : 1); ++x) {
+                const int slots = F8 ? (x ? C::v_ring : C::k_ring) : RING;
+                for (int q = max(0, asked[x] - slots); q < asked[x]; ++q)
+                    wait_turn(smem_u32(F8 ? (x ? &sh.v_full[F8 ? q % slots : 0] : &sh.k_full[F8 ? q % slots : 0]) : &sh.full[F8 ? 0 : q % slots]),
+                              (uint32_t)(q / slots) & 1u, a.hdr);
+            }
         } else if constexpr (F8) {
-            // codes of a turn are asked for `ahead` turns before it is converted. At most 6: a tile's K is asked for when the
-            // softmax has left the tile four before it, which needs the V turns up to seven before this one converted.
-            constexpr int ahead = C::codes - 1 < 6 ? C::codes - 1 : 6;
+            // Without TMA the codes of a turn are asked for `ahead` turns before its V, if it is one, is converted. At most 6: a tile's
+            // K is asked for when the softmax has left the tile four before it, which needs the V turns up to seven before this one
+            // converted; and as many turns as the rings hold, which a turn that is asked for may have to wait for.
+            constexpr int ahead = D == 256 ? 2 : 6;
             // a thread's chunks of 16 codes, the same in every slot: chunk `gr` of token `tok`, and where its two granules go. The
             // second half of a token's chunks goes in the other order, to other banks than the first half's.
             constexpr int N = (T * row_chunks + C::workers - 1) / C::workers;
@@ -603,43 +620,43 @@ __global__ void __launch_bounds__(C::threads, 1)
             }
             const bool swap = wt % row_chunks >> 2 & 1;   // the same for every chunk: C::workers is a multiple of row_chunks
             static_assert(C::workers % row_chunks == 0, "a thread keeps its chunk");
-            auto convert = [&](int q, bool is_v, int j0, const TreeRow &r, bool some) -> bool {
-                // V: rows that nothing attends become zeros, and NaN codes of rows that not every row attends
+            auto convert = [&](int i, int j0, const TreeRow &r, bool some) -> bool {       // tile i's V
+                // rows that nothing attends become zeros, and NaN codes of rows that not every row attends
                 const int edge = a.window > 0 ? r.base + r.T - a.window : 0;
-                if (!wait_warp(&sh.c_full[q % C::codes], q / C::codes)) return false;
-                if (q >= RING && !wait_warp(&sh.empty[q % RING], q / RING - 1)) return false;
-                const uint8_t *from = sm + C::codes_at + q % C::codes * C::code_slot;
-                uint8_t *to = sm + C::ring_at + q % RING * C::slot;
+                if (!wait_warp(&sh.v_full[i % C::v_ring], i / C::v_ring)) return false;
+                if (i >= RING && !wait_warp(&sh.empty[i % RING], i / RING - 1)) return false;
+                const uint8_t *from = sm + C::v_at + i % C::v_ring * C::code_slot;
+                uint8_t *to = sm + C::ring_at + i % RING * C::slot;
                 constexpr int H = 3;                      // chunks at a time
 #pragma unroll
-                for (int i0 = 0; i0 < N; i0 += H) {
+                for (int n0 = 0; n0 < N; n0 += H) {
                     uint4 v[H];
 #pragma unroll
-                    for (int i = 0; i < H; ++i)
-                        if (i0 + i < N) v[i] = *reinterpret_cast<const uint4 *>(from + src[i0 + i]);
-                    if (is_v && some)
+                    for (int n = 0; n < H; ++n)
+                        if (n0 + n < N) v[n] = *reinterpret_cast<const uint4 *>(from + src[n0 + n]);
+                    if (some)
 #pragma unroll
-                        for (int i = 0; i < H; ++i) {
-                            if (i0 + i >= N) break;
-                            const int j = j0 + toks[i0 + i];
+                        for (int n = 0; n < H; ++n) {
+                            if (n0 + n >= N) break;
+                            const int j = j0 + toks[n0 + n];
                             if ((uint32_t)j >= (uint32_t)r.len || j < r.lo)
-                                v[i] = make_uint4(0, 0, 0, 0);
+                                v[n] = make_uint4(0, 0, 0, 0);
                             else if (j >= r.base || j < edge)
-                                drop_nan_codes(v[i].x), drop_nan_codes(v[i].y), drop_nan_codes(v[i].z), drop_nan_codes(v[i].w);
+                                drop_nan_codes(v[n].x), drop_nan_codes(v[n].y), drop_nan_codes(v[n].z), drop_nan_codes(v[n].w);
                         }
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        if (i0 + i >= N || toks[i0 + i] < 0) break;
-                        const uint4 x = swap ? make_uint4(v[i].z, v[i].w, v[i].x, v[i].y) : v[i];
-                        *reinterpret_cast<uint4 *>(to + dst[i0 + i][0]) =
+                    for (int n = 0; n < H; ++n) {
+                        if (n0 + n >= N || toks[n0 + n] < 0) break;
+                        const uint4 x = swap ? make_uint4(v[n].z, v[n].w, v[n].x, v[n].y) : v[n];
+                        *reinterpret_cast<uint4 *>(to + dst[n0 + n][0]) =
                             make_uint4(e4m3_to_f16x2(x.x, 0), e4m3_to_f16x2(x.x, 1), e4m3_to_f16x2(x.y, 0), e4m3_to_f16x2(x.y, 1));
-                        *reinterpret_cast<uint4 *>(to + dst[i0 + i][1]) =
+                        *reinterpret_cast<uint4 *>(to + dst[n0 + n][1]) =
                             make_uint4(e4m3_to_f16x2(x.z, 0), e4m3_to_f16x2(x.z, 1), e4m3_to_f16x2(x.w, 0), e4m3_to_f16x2(x.w, 1));
                     }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();                             // an arrival for each warp: 192 of them on one word take hundreds of cycles
-                if (lane == 0) mbar_arrive(smem_u32(&sh.full[q % RING])), mbar_arrive(smem_u32(&sh.c_empty[q % C::codes]));
+                if (lane == 0) mbar_arrive(smem_u32(&sh.full[i % RING])), mbar_arrive(smem_u32(&sh.v_empty[i % C::v_ring]));
                 return true;
             };
             Walk w = walk;
@@ -649,7 +666,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                 for (int c = 0; c < turns && ok; ++c) {
                     const int t = g.ta + turn_tile(c, turns);
                     ok = ask();
-                    if (ok) ok = convert(2 * g.i0 + c, turn_is_v(c, turns), t * T, g.r, masked(a, g.r, t));
+                    if (ok && turn_is_v(c, turns)) ok = convert(g.i0 + turn_tile(c, turns), t * T, g.r, masked(a, g.r, t));
                 }
             }
         }
@@ -699,14 +716,25 @@ __global__ void __launch_bounds__(C::threads, 1)
                     for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
 #pragma unroll
                     for (int o = D / 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);
-                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                    const uint32_t dst = q_at + gr / 8 * (kRows * 128) + swz(r, gr & 7);
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(f16x2(f[0] * down, f[1] * down)),
-                                 "r"(f16x2(f[2] * down, f[3] * down)), "r"(f16x2(f[4] * down, f[5] * down)),
-                                 "r"(f16x2(f[6] * down, f[7] * down))
-                                 : "memory");
-                    if (gr == 0) sh.q_scale[seg & 1][r] = __uint_as_float((uint32_t)(127 + e) << 23);
+                    // the largest becomes 2^7 .. 2^8; an infinite one makes the row NaN, not E4M3's largest value
+                    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -119), 126);
+                    const float down = top == INFINITY ? NAN : __uint_as_float((uint32_t)(134 - e) << 23);
+                    uint32_t part[2][2] = {};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float x = f[2 * k] * down, y = f[2 * k + 1] * down;
+                        const uint32_t c = e4m3x2_of(x, y), back = e4m3_to_f16x2(c, 0);
+                        const float2 near = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+                        part[0][k >> 1] |= c << (16 * (k & 1));
+                        part[1][k >> 1] |= e4m3x2_of(x - near.x, y - near.y) << (16 * (k & 1));
+                    }
+                    // first parts, then second ones; 128 dims are a block of 128 bytes
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+                        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(q_at + (z * SG + gr / 16) * (kRows * 128) + swz(r, gr / 2 & 7) + (gr & 1) * 8),
+                                     "r"(part[z][0]), "r"(part[z][1])
+                                     : "memory");
+                    if (gr == 0) sh.q_scale[seg & 1][r] = __uint_as_float((uint32_t)(120 + e) << 23);
                 }
                 fence_proxy_async_smem();
             }
@@ -806,24 +834,31 @@ __global__ void __launch_bounds__(C::threads, 1)
                     break;
                 }
                 const uint32_t s_at = tmem + C::t_s + (i % NB) * C::s_cols;
-                const int q = 2 * g.i0 + k_turn(c), at = q % RING;
-                if (!wait_warp(&sh.full[at], q / RING)) {
+                const int q = F8 ? i : 2 * g.i0 + k_turn(c), slots = F8 ? C::k_ring : RING, at = q % slots;
+                uint64_t *full = F8 ? &sh.k_full[F8 ? at : 0] : &sh.full[F8 ? 0 : at];
+                if (!wait_warp(full, q / slots)) {
                     ok = false;
                     break;
                 }
-                if (!F8 && !tiled) fence_proxy_async_smem();          // rows by cp.async; TMA needs none, the conversion has its own
+                if (!tiled) fence_proxy_async_smem();                 // rows by cp.async; TMA needs none
                 tc_fence_after();
-                const uint64_t bd = tc_desc(ring_at + at * C::slot, 16, 1024), ad = tc_desc(q_at, 16, 1024);
+                const uint64_t bd = tc_desc(F8 ? q_at + C::k_at + at * C::code_slot : ring_at + at * C::slot, 16, 1024), ad = tc_desc(q_at, 16, 1024);
                 if (elect_one()) {
+                    if constexpr (!F8) {
 #pragma unroll
-                    for (int z = 0; z < D / 16; ++z) {                // 16 dims: 32 bytes on, or in the next block of 64
-                        const uint64_t zd = bd + (z >> 2) * (T * 128 / 16) + (z & 3) * 2;
-                        if (!F8)
-                            tc_mma_ta(s_at, tmem + C::t_q + z * 8, zd, tc_idesc(kRows, T, 0), z > 0);
-                        else
-                            tc_mma(s_at + z / 8 * T, ad + (z >> 2) * (kRows * 128 / 16) + (z & 3) * 2, zd, f16_idesc(T, 0), z % 8 > 0);
+                        for (int z = 0; z < D / 16; ++z)              // 16 dims: 32 bytes on, or in the next block of 64
+                            tc_mma_ta(s_at, tmem + C::t_q + z * 8, bd + (z >> 2) * (T * 128 / 16) + (z & 3) * 2, tc_idesc(kRows, T, 0), z > 0);
+                        tc_commit(smem_u32(&sh.empty[at]));
+                    } else {
+                        // codes as they are; 32 dims: 32 bytes on; first and second parts of q into the same sums, for each 128 dims
+#pragma unroll
+                        for (int x = 0; x < SG; ++x)
+#pragma unroll
+                            for (int z = 0; z < 8; ++z)
+                                mma_e4m3(s_at + x * T, ad + ((z >> 2) * SG + x) * (kRows * 128 / 16) + (z & 3) * 2,
+                                         bd + x * (T * 128 / 16) + (z & 3) * 2, f16_idesc(T, 0), z > 0);
+                        tc_commit(smem_u32(&sh.k_empty[at]));
                     }
-                    tc_commit(smem_u32(&sh.empty[at]));
                     tc_commit(smem_u32(&sh.s_full[i % NB]));
                     if (c + 1 == n) tc_commit(smem_u32(&sh.q_free));
                 }
@@ -841,7 +876,7 @@ __global__ void __launch_bounds__(C::threads, 1)
             const int n = g.tb - g.ta;
 #pragma unroll 1
             for (int c = 0; c < n && ok; ++c, ++i) {
-                const int q = 2 * g.i0 + v_turn(c, n), at = q % RING;
+                const int q = F8 ? i : 2 * g.i0 + v_turn(c, n), at = q % RING;
                 const bool part = !F8 && masked(a, g.r, g.ta + c);
                 if (part) {
                     ok = wait_warp(&sh.full[at], q / RING);
