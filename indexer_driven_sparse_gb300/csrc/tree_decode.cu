@@ -47,9 +47,11 @@ constexpr int kMetas = 4;                        // tiles whose slots and scales
 constexpr float kLazy = 8.f;                     // O is rescaled when a maximum has grown by more than 2^8
 constexpr float kRaise = 6.f;                    // FP8 rows: weights up to 2^8, scales below 2, so below 2^15 in f16
 
-template <int D_, bool F8_>
+// Tiled: rows come by TMA (pages of whole runs of tokens), else by cp.async.
+template <int D_, bool F8_, bool Tiled_>
 struct TreeCfg {
     static constexpr int D = D_;
+    static constexpr bool tiled = Tiled_;
     static constexpr bool F8 = F8_;
     static constexpr int SG = F8 ? D / 128 : 1;                 // scales of a row, sets of weights
     static constexpr int slot = kTile * D * 2, code_slot = F8 ? kTile * D : 0;      // bytes: a tile's K or V
@@ -64,8 +66,10 @@ struct TreeCfg {
     static constexpr int buffers = (512 - t_s) / s_cols;
     // 20 warps of 96 registers; the query warps' numbers modulo 4 are the four quarters of tensor memory's lanes
     static constexpr int softmax = 256, q_threads = F8 ? 64 : 128, workers = F8 ? 192 : 160;
-    static constexpr int s_warp = 8, o_warp = 9, index_warp = 10, q_warp = 11, load_warp = q_warp + q_threads / 32;
-    static constexpr int work_warp = F8 ? load_warp + 1 : load_warp;
+    // FP8 rows: the converting warps 14 to 19 are two on schedulers 2 and 3; the index warp beside two of them slowed their softmax
+    // warps by half
+    static constexpr int s_warp = 8, o_warp = 9, index_warp = F8 ? 12 : 10, q_warp = F8 ? 10 : 11, load_warp = F8 ? 13 : 15;
+    static constexpr int work_warp = F8 ? 14 : 15;
     static constexpr int threads = 640;
     static_assert(work_warp * 32 + workers == threads, "roles");
 };
@@ -294,7 +298,7 @@ __global__ void __launch_bounds__(C::threads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int m_tile = blockIdx.x % plan.m_tiles, kvh = blockIdx.x / plan.m_tiles % a.Hkv, range = blockIdx.x / plan.m_tiles / a.Hkv;
     const bool speaks = kvh == 0 && m_tile == 0;          // records errors that all CTAs of a range see
-    const bool tiled = plan.run > 0;
+    constexpr bool tiled = C::tiled;
 
     if (warp == C::s_warp) tmem_alloc(&sh.tmem, 512);
     if (tid == 0) {
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(C::threads, 1)
     Seg g{};
     if (warp == C::index_warp) {
         // ================================================================ slots of each tile; TMA loads
-        constexpr int E = T / 32;                         // tokens of a lane, neighbours
+        constexpr int E = T / 32;                         // tokens of a lane: lane, 32 + lane
         int page[E], offset[E];
         bool ok = true;
         int pages_begin = 0, pages_end = 0;               // entries that g needs
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(C::threads, 1)
         auto fetch = [&](int t) {                         // the page table's entries for tile t of g
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const uint32_t j = (uint32_t)t * T + lane * E + e;      // may pass 2^31
+                const uint32_t j = (uint32_t)t * T + e * 32 + lane;     // may pass 2^31
                 const uint32_t entry = plan.page_shift >= 0 ? j >> plan.page_shift : j / (uint32_t)a.page_size;
                 offset[e] = (int)(j - entry * a.page_size);
                 const bool some = entry >= (uint32_t)pages_begin && entry <= (uint32_t)pages_end;
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                 bool exists[E];
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    const int j = (now.ta + c) * T + lane * E + e;
+                    const int j = (now.ta + c) * T + e * 32 + lane;
                     const bool in = (uint32_t)j >= (uint32_t)now.r.lo && (uint32_t)j < (uint32_t)now.r.len;
                     const bool fine = (uint32_t)page[e] < (uint32_t)a.n_pages;
                     if (in && !fine && speaks) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereTree, now.s);
@@ -484,15 +488,12 @@ __global__ void __launch_bounds__(C::threads, 1)
                     ok = false;
                     break;
                 }
-                uint32_t bits = 0;                        // token lane E + e as bit (lane E + e) % 32 of word lane E / 32
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    bits |= (exists[e] ? 1u : 0u) << ((lane * E + e) & 31);
-                    sh.slots[m][lane * E + e] = exists[e] || tiled ? slot[e] : -1;        // a box may begin before the first token
+                    sh.slots[m][e * 32 + lane] = exists[e] || tiled ? slot[e] : -1;       // a box may begin before the first token
+                    const uint32_t bits = __ballot_sync(0xffffffffu, exists[e]);
+                    if (lane == 0) sh.real[m][e] = bits;
                 }
-#pragma unroll
-                for (int o = 1; o < 32 / E; o <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
-                if (lane % (32 / E) == 0) sh.real[m][lane * E / 32] = bits;
                 if (F8) {
                     float z = 0.f, u = 0.f;
 #pragma unroll
@@ -500,11 +501,9 @@ __global__ void __launch_bounds__(C::threads, 1)
                         z = fmaxf(z, scale[e].z < INFINITY ? scale[e].z : 0.f);
                         u = fmaxf(u, scale[e].w < INFINITY ? scale[e].w : 0.f);
                     }
-#pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1) {
-                        z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
-                        if (SG == 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
-                    }
+                    // scales are not negative: their order is that of their bits
+                    z = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(z)));
+                    if (SG == 2) u = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(u)));
                     auto power = [](float x) { return __uint_as_float(min(max(__float_as_uint(x) & 0x7F800000u, 7u << 23), 247u << 23)); };
                     top = make_float2(fmaxf(top.x, power(z)), fmaxf(top.y, power(u)));
                     auto inverse = [](float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); };
@@ -514,7 +513,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                         float4 x = scale[e];              // infinite V scales become NaN; where not every row attends, it is added at the end
                         if (masked(a, now.r, t)) x.z = x.z < INFINITY ? x.z : 0.f, x.w = x.w < INFINITY ? x.w : 0.f;
                         float *ks = reinterpret_cast<float *>(sh.k_scales[m]), *vs = reinterpret_cast<float *>(sh.v_scales[m]);
-                        const int tok = F8 ? lane * E + e : 0;
+                        const int tok = F8 ? e * 32 + lane : 0;
                         ks[tok] = x.x, vs[tok] = fmaf(x.z, 0.f, x.z) * cx;
                         if (SG == 2) ks[T + tok] = x.y, vs[T + tok] = fmaf(x.w, 0.f, x.w) * cy;
                     }
@@ -1224,9 +1223,9 @@ int sms() {
     return cached[dev];
 }
 
-template <int D, bool F8>
-cudaError_t launch(const TreeArgs &a, cudaStream_t st) {
-    using C = TreeCfg<D, F8>;
+template <int D, bool F8, bool Tiled>
+cudaError_t launch_as(const TreeArgs &a, int run, cudaStream_t st) {
+    using C = TreeCfg<D, F8, Tiled>;
     const int ctas = sms<C>();
     if (ctas == 0) {
         const cudaError_t e = cudaGetLastError();
@@ -1237,12 +1236,10 @@ cudaError_t launch(const TreeArgs &a, cudaStream_t st) {
     plan.ranges = std::max(1, ctas / (a.Hkv * plan.m_tiles));
     plan.min_tiles = 2;
     plan.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
-    // tiled loads of runs of a page; below 16 tokens the engine's cost for each box outweighs the copies of the worker warps
-    const int run = std::min(a.page_size & -a.page_size, kTile);
     TreeMaps maps;
     memset(&maps, 0, sizeof(maps));
     const int64_t rows = a.n_pages * a.page_size;
-    if (run >= (F8 ? 4 : 16) && rows > 0) {
+    if (Tiled) {
         plan.run = run;
         const uint64_t row = (uint64_t)a.Hkv * D * (F8 ? 1 : 2);
         const uint32_t blocks = run == kTile ? D * (F8 ? 1 : 2) / 128 : 1;
@@ -1262,6 +1259,15 @@ cudaError_t launch(const TreeArgs &a, cudaStream_t st) {
     const dim3 join((unsigned)jobs, (unsigned)std::max<int64_t>(1, std::min((most + each - 1) / each, 152 * 8 / jobs)));
     return few ? launch_dependent(tree_join_kernel<D, kJoinThreads / (D / 4)>, join, kJoinThreads, 0, st, a, plan, ws)
                : launch_dependent(tree_join_kernel<D, 2>, join, kJoinThreads, 0, st, a, plan, ws);
+}
+
+template <int D, bool F8>
+cudaError_t launch(const TreeArgs &a, cudaStream_t st) {
+    // Tiled loads of runs of a page. bf16 rows of 256 dims, 32 sequences of 4,096 to 32,768 tokens, runs of 32, 16 and 8 tokens: 232, 268
+    // and 371 us, by cp.async 264; FP8 rows, whose workers convert as well: runs of 16, 8 and 4 tokens 372, 393 and 498, by cp.async 515
+    // to 524.
+    const int run = std::min(a.page_size & -a.page_size, kTile);
+    return run >= (F8 ? 4 : 16) && a.n_pages > 0 ? launch_as<D, F8, true>(a, run, st) : launch_as<D, F8, false>(a, 0, st);
 }
 
 }  // namespace
