@@ -784,3 +784,168 @@ def test_captured_speculative_steps_replay(cuda_lib):
         torch.cuda.synchronize()
         assert cache.seq_len.tolist() == [17 + 6 * i, 21 + 6 * i]
     assert int((cache.ref > 0).sum()) == 4 + 5 and cache.status() == ((0, 0), (0, 0)) and cache.more_status() == ((0, 0),) * 2
+
+
+# ------------------------------------------------------------------------------------------ values that are not finite
+@pytest.mark.parametrize("Hq,Hkv,D,fp8", [(16, 2, 256, False), (8, 2, 128, False), (4, 1, 64, False), (16, 2, 256, True), (8, 2, 128, True)])
+@pytest.mark.parametrize("page", [16, 3])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_tree_odd_values_of_a_draft_reach_its_family_alone(cuda_lib, Hq, Hkv, D, fp8, page, value):
+    """K and V of one drafted token that are not finite: the tokens that attend it get what their sums give (the value in its
+    dim, or NaN), its other relatives and siblings stay as they were."""
+    lens, counts = [150, 40, 9], [12, 7, 9]
+    q, planes, values, tab, table, off, _ = tree_inputs(lens, counts, Hq, Hkv, D, page, fp8, seed=4, spare_rows=0)
+    parents = [[-1, 0, 0, 1, 1, 2, 2, -1, 7, 8, 3, 3], [-1, 0, 1, -1, 3, 4, 5], [-1, 0, 0, 0, 1, 2, 3, -1, -1]]
+    cfg = qb.make_paged_config(Hq, Hkv, D, page)
+    ws = qb.tree_workspace(cfg, 12)
+    good, good_lse = run_tree(cfg, q, planes, tab, lens, off, parents, 12, ws)
+    odd = 2                                               # the third draft of each row, dim 5 of KV head 0
+    for r, n in enumerate(lens):
+        slot = int(P.slots_of(table[r], n, page)[n - counts[r] + odd])
+        if fp8:
+            planes[2].flatten(0, 1)[slot, 0, 5] = 0x7F    # E4M3 has no infinity
+        else:
+            planes[1].flatten(0, 1)[slot, 0, 5] = value
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, parents, 12, ws)
+    assert status(ws) == (0, 0) and torch.equal(lse, good_lse)
+    G = Hq // Hkv
+    want = good.clone()
+    for r in range(3):
+        for i, line in enumerate(T.lines(parents[r])):
+            if odd in line:
+                want[off[r] + i, :G, 5] = float("nan") if fp8 else value
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(out, 0.0), torch.nan_to_num(want, 0.0))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page", [32, 3])
+def test_tree_odd_values_at_the_windows_edge(cuda_lib, fp8, page):
+    """Tokens that some drafts see and others, deeper ones, do not: what is not finite in them reaches those that do."""
+    Hq, Hkv, D, n, window = 8, 2, 128, 300, 90
+    parents = [[-1, 0, 1, 2, 3, -1]]
+    q, planes, values, tab, table, off, _ = tree_inputs([n], [6], Hq, Hkv, D, page, fp8, seed=4, spare_rows=0)
+    cfg = qb.make_paged_config(Hq, Hkv, D, page, window=window)
+    ws = qb.tree_workspace(cfg, 6)
+    good, _ = run_tree(cfg, q, planes, tab, [n], off, parents, 6, ws)
+    place = n - 6 + 1 - window + 2                        # positions above own - window: seen at depths 1, 2 and 3
+    slot = int(P.slots_of(table[0], n, page)[place])
+    gone = int(P.slots_of(table[0], n, page)[place - 4])  # seen by none
+    if fp8:
+        planes[2].flatten(0, 1)[slot, 1, 3] = 0xFF
+        planes[3].flatten(0, 1)[gone] = float("nan")
+    else:
+        planes[1].flatten(0, 1)[slot, 1, 3] = float("nan")
+        planes[1].flatten(0, 1)[gone] = float("inf")
+    out, _ = run_tree(cfg, q, planes, tab, [n], off, parents, 6, ws)
+    seen = [place in places for places in T.attended(n, parents[0], window)]
+    assert seen == [True, True, True, False, False, True]
+    for i in range(6):
+        spoiled = torch.isnan(out[i])
+        assert bool(spoiled[4:, 3].all()) == seen[i] and int(spoiled.sum()) == (4 if seen[i] else 0)
+        assert torch.equal(out[i][~spoiled], good[i][~spoiled])
+
+
+@pytest.mark.parametrize("Hq,D", [(8, 256), (8, 128)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("where", ["history", "draft"])
+def test_tree_value_scale_that_is_not_finite(cuda_lib, Hq, D, value, where):
+    """An infinite or undefined V scale makes NaN of its 128 dims for the tokens that attend it, and of nothing else."""
+    page, n, counts = 16, 500, [8]
+    q, planes, values, tab, table, off, parents = tree_inputs([n], counts, Hq, 1, D, page, True, seed=4, spare_rows=0, chain=0.3)
+    cfg = qb.make_paged_config(Hq, 1, D, page)
+    ws = qb.tree_workspace(cfg, 8)
+    good, good_lse = run_tree(cfg, q, planes, tab, [n], off, parents, 8, ws)
+    at = 100 if where == "history" else n - 8 + 1
+    planes[3].flatten(0, 1)[int(P.slots_of(table[0], n, page)[at]), 0, -1] = value
+    out, lse = run_tree(cfg, q, planes, tab, [n], off, parents, 8, ws)
+    assert torch.equal(lse, good_lse)
+    for i, places in enumerate(T.attended(n, parents[0])):
+        if at in places:
+            assert bool(torch.isnan(out[i, :, -128:]).all())
+            assert torch.equal(out[i, :, :-128], good[i, :, :-128])
+        else:
+            assert torch.equal(out[i], good[i])
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("Hq,D,fp8", [(8, 256, True), (8, 128, True), (8, 256, False), (4, 64, False)])
+def test_tree_query_that_is_not_finite_spoils_its_head_alone(cuda_lib, Hq, D, fp8, value):
+    lens, counts = [300, 70], [5, 3]
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, Hq, 1, D, 16, fp8, seed=4, spare_rows=0)
+    cfg = qb.make_paged_config(Hq, 1, D, 16)
+    ws = qb.tree_workspace(cfg, 5)
+    good, good_lse = run_tree(cfg, q, planes, tab, lens, off, parents, 5, ws)
+    q[6, 1, 7] = value
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, parents, 5, ws)
+    assert bool(torch.isnan(out[6, 1]).all())
+    out[6, 1], lse[6, 1] = good[6, 1], good_lse[6, 1]
+    assert torch.equal(out, good) and torch.equal(lse, good_lse)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_tree_odd_keys_of_masked_tokens_change_nothing(cuda_lib, value):
+    lens, counts = [90], [6]
+    q, planes, values, tab, table, off, _ = tree_inputs(lens, counts, 8, 2, 128, 8, False, seed=4, spare_rows=0)
+    parents = [[-1, 0, 1, -1, 3, 4]]
+    cfg = qb.make_paged_config(8, 2, 128, 8)
+    ws = qb.tree_workspace(cfg, 6)
+    good, _ = run_tree(cfg, q, planes, tab, lens, off, parents, 6, ws)
+    planes[0].flatten(0, 1)[int(P.slots_of(table[0], 90, 8)[84 + 1])] = value         # draft 1: seen by 1 and 2
+    out, _ = run_tree(cfg, q, planes, tab, lens, off, parents, 6, ws)
+    assert torch.equal(out[[0, 3, 4, 5]], good[[0, 3, 4, 5]])
+
+
+# ------------------------------------------------------------------------------------------ limits
+@pytest.mark.parametrize("Hq,Hkv,D,drafts", [(160, 160, 64, 3), (16, 1, 256, 128), (64, 4, 128, 100), (620, 310, 64, 2)])
+def test_tree_of_many_heads_and_drafts(cuda_lib, Hq, Hkv, D, drafts):
+    """More CTAs than one wave, and sixteen tiles of query rows."""
+    lens = [drafts + 300, drafts + 1, 64]
+    counts = [drafts, drafts, min(drafts, 64)]
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, Hq, Hkv, D, 16, False, seed=3)
+    cfg = qb.make_paged_config(Hq, Hkv, D, 16)
+    ws = qb.tree_workspace(cfg, drafts)
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, parents, drafts, ws)
+    assert status(ws) == (0, 0)
+    pick = [0, drafts // 2, drafts - 1]                   # a few tokens of each row against the oracle
+    for r in range(3):
+        keep = [i for i in pick if i < counts[r]]
+        slots = P.slots_of(table[r], lens[r], 16)
+        K, V = (x.reshape(-1, *x.shape[2:])[slots] for x in values)
+        for i in keep:
+            at = T.attended(lens[r], parents[r])[i]
+            want, want_lse, mass, terms = P.decode(f64(q[off[r] + i]), K[at], V[at], 0, D ** -0.5)
+            ds = D * 2.0 ** -24 * terms + 2.0 ** -21 * (terms + 1)
+            sums = len(at) / 8 * 2.0 ** -24 + 2.0 ** -15
+            tol = 2.0 ** -8 * np.abs(want) + (2 * ds[:, None] + sums + 2.0 ** -8) * mass
+            assert np.all(np.abs(f64(out[off[r] + i]) - want) <= tol)
+            assert np.all(np.abs(f64(lse[off[r] + i]) - want_lse) <= ds + sums + 2.0 ** -22 * np.abs(want_lse))
+    assert bool((out[off[-1]:] == 8).all())
+
+
+@pytest.mark.parametrize("Hq,D", [(8, 256), (8, 128)])
+@pytest.mark.parametrize("spread", [4, 16])
+def test_tree_queries_and_scales_of_a_wide_range_over_fp8_rows(cuda_lib, Hq, D, spread):
+    """Queries whose values span 2^spread within a head: what lies below 2^-10 of a head's largest value is off by at most 2^-17
+    of that. V scales that span 2^spread over the tokens: each weight times its scale is off by 2^-11 of it and 2^-31 of
+    the largest weight (2^8 of the lazy maximum's) times the largest scale."""
+    n, count, page = 700, 9, 16
+    q, planes, values, tab, table, off, parents = tree_inputs([n], [count], Hq, 1, D, page, True, seed=2, spare_rows=0)
+    g = torch.Generator().manual_seed(5)
+    q *= torch.exp2(-spread * torch.rand(q.shape, generator=g)).to(DEV)
+    factor = torch.exp2(-spread * torch.rand(planes[3].shape, generator=g)).to(DEV)
+    planes[3].mul_(factor)
+    values = (values[0], values[1] * np.repeat(f64(factor), 128, -1))
+    cfg = qb.make_paged_config(Hq, 1, D, page)
+    ws = qb.tree_workspace(cfg, count)
+    out, lse = run_tree(cfg, q, planes, tab, [n], off, parents, count, ws)
+    slots = P.slots_of(table[0], n, page)
+    K, V = (x.reshape(-1, *x.shape[2:])[slots] for x in values)
+    for i, at in enumerate(T.attended(n, parents[0])):
+        qi = f64(q[i])
+        want, want_lse, mass, terms = P.decode(qi, K[at], V[at], 0, D ** -0.5)
+        ds = D * 2.0 ** -24 * terms + 2.0 ** -21 * (terms + 1) + 2.0 ** -17 * np.abs(qi).max(1) * np.abs(K[at]).sum(2).max() * D ** -0.5
+        sums = len(at) / 8 * 2.0 ** -24 + 2.0 ** -15
+        tol = 2.0 ** -8 * np.abs(want) + (2 * ds[:, None] + sums + 2.0 ** -11) * mass + len(at) * 2.0 ** -31 * 2.0 ** 8 * np.abs(V[at]).max()
+        assert np.all(np.abs(f64(out[i]) - want) <= tol)
+        assert np.all(np.abs(f64(lse[i]) - want_lse) <= ds + sums + 2.0 ** -22 * np.abs(want_lse))
