@@ -731,7 +731,8 @@ QSA_API size_t qsa_tree_workspace_size(const qsa_paged_config *cfg, int32_t max_
  *   ascending, within [0, N]; parent [N]; max_draft: the most drafted tokens of a sequence, 1 .. QSA_MAX_DRAFT;
  *   out [N][n_q_heads][head_dim] bf16, 16-byte aligned; lse [N][n_q_heads] fp32 or NULL; k_cache, v_cache 16-byte
  *   aligned device memory. Rows of out and lse that no sequence names stay as they were.
- * fp32 scores, softmax and sums; the weights enter the second product as bf16 (each rounded by at most 2^-8 of it, as out itself is).
+ * fp32 scores, softmax and sums; the weights enter the second product as bf16 (each rounded by at most 2^-8 of it, as out
+ * itself is). V values that are not finite reach the tokens that attend them, and no others.
  * Device checks (QSA_ERR_DEVICE_BOUNDS is recorded): a sequence whose offsets do not ascend within [0, N], or begin below an
  * earlier one's, attends nothing and its rows are not written; one with T > max_draft, T > n or n > table_ld page_size
  * attends nothing (out = 0, lse = -inf); a parent outside [-1, own place) counts as -1; a page outside [0, n_pages) has
@@ -744,7 +745,12 @@ QSA_API qsa_status qsa_tree_decode(const qsa_paged_config *cfg, const qsa_bf16 *
                                    const int32_t *table, int64_t table_ld, const int32_t *seq_len, int32_t B,
                                    qsa_bf16 *out, float *lse, void *ws, size_t ws_bytes, qsa_stream stream);
 
-/* qsa_tree_decode over the FP8 rows qsa_rope_append_fp8kv writes (head_dim 128 or 256). */
+/* qsa_tree_decode over the FP8 rows qsa_rope_append_fp8kv writes (head_dim 128 or 256). The codes enter both products
+ * exactly. q enters as the sum of two scaled E4M3 values, which hold all of a bf16 value down to 2^-10 of its head's largest;
+ * smaller ones are rounded by up to 2^-17 of that. Each weight x V scale is rounded once, by at most 2^-11 of it or 2^-31 of
+ * the largest weight times the largest V scale of the sequence. Scales must not be negative; a V scale that is infinite or
+ * NaN makes its 128 dims NaN for the tokens that attend it, and nothing else; V scales outside 2^-120 .. 2^120 are not
+ * told from those bounds. */
 QSA_API qsa_status qsa_tree_decode_fp8kv(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
                                          const int32_t *draft_off, const int32_t *parent, int32_t N,
                                          int32_t max_draft, const uint8_t *k_codes, const float *k_scales,

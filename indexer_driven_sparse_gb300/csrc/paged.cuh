@@ -181,7 +181,8 @@ cudaError_t launch_copy_pages(const int32_t *src, const int32_t *dst, int n, con
                               int64_t n_dst, WsHeader *hdr, cudaStream_t st);
 
 // Host checks shared with qsa_api.cu.
-bool device_accessible(const void *p);
+bool device_accessible(const void *p);      // or mapped pinned host memory
+bool device_resident(const void *p);
 qsa_status host_ok();
 
 }  // namespace qsa

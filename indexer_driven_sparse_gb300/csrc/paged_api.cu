@@ -301,8 +301,8 @@ qsa_status tree_decode(const char *call, const qsa_paged_config *cfg, TreeArgs a
     QSA_NEED(call, aligned(a.table, 4) && aligned(a.seq_len, 4) && aligned(a.lse, 4) && aligned(a.draft_off, 4) &&
                  aligned(a.parent, 4),
              "table, seq_len, draft_off, parent and lse must be 4-byte aligned");
-    QSA_NEED(call, device_accessible(a.k) && device_accessible(a.v) &&
-                 (!fp8 || (device_accessible(a.k_scales) && device_accessible(a.v_scales))),
+    QSA_NEED(call, device_resident(a.k) && device_resident(a.v) &&
+                 (!fp8 || (device_resident(a.k_scales) && device_resident(a.v_scales))),
              "the K/V rows (and their scales) must be device memory");
     a.Hq = cfg->n_q_heads;
     a.Hkv = cfg->n_kv_heads;

@@ -2,36 +2,39 @@
 //   out[i] = sum_j softmax_j(scale q[i] . K[j]) V[j] over the cached tokens before the drafts, i's ancestors and i.
 //
 // A sequence's T drafted tokens times the G query heads of a KV head are T G rows that share every K and V row: 4 T G flops
-// per value read, 16 tokens with 8 heads each are the 128 rows of one tcgen05 tile. One such tile needs 2,050 cycles of the tensor
-// core for 128 tokens of 256 dims (two products of 128 x 128 x 256) and their 128 KB take an SM's share of HBM 5,600: up to two
-// tiles the rows' stream bounds the call, from three on the products.
+// per value read. 16 tokens with 8 heads each are the 128 rows of one tcgen05 tile; their 64 KB of K and V for 64 tokens of 256
+// dims take an SM's share of HBM 2,900 cycles, the products 1,500: with one such M tile the rows' stream bounds the call, with
+// two or more the products.
 //
-// Split: as in the decode of one token (paged_decode.cuh), the batch's tokens, cut into tiles of one sequence each, form one list,
-// dealt to R ranges of equal length; CTA (range, KV head, M tile) walks its part. The M tiles of a range are neighbouring
+// Split: as in the decode of one token (paged_decode.cuh), the batch's tokens, cut into tiles of 64 of one sequence each, form one
+// list, dealt to R ranges of equal length; CTA (range, KV head, M tile) walks its part. The M tiles of a range are neighbouring
 // CTAs that read the same rows at the same time: from L2, all but one of them. A sequence that a range boundary cuts
 // leaves partials (m, l, O), joined by tree_join_kernel; all others are written at once.
 //
-// Roles of a CTA (one per SM), which meet at mbarriers only:
-//   4 softmax warps   a row each thread: running maximum and sum in base 2, O rescaled only when the maximum has grown by
-//                     more than 2^8; weights go back to tensor memory over the scores they came from;
-//   1 MMA warp        S = Q K^T (M 128, N the tile's tokens) into one of two buffers, O += P V with P from tensor memory; the next
-//                     tile's S is issued before this tile's O;
-//   1 index warp      page table -> slots, a tile ahead; with pages of whole runs of 16 tokens it also issues the tiled TMA loads
-//                     (a box is a run of a page), whose cost per 16 KB is nothing beside 1,024 copies of 16 bytes;
-//   2 query warps     the rows' queries, the ancestors' bits, and the clean-up of V rows that not every row attends;
-//   8 worker warps    other page sizes: cp.async of 16 bytes, row by row. FP8 rows: codes -> f16 operands.
-// K and V lie in shared memory as slots of 16 KB in 128-byte swizzle (K: 64 dims of the tile's tokens; V: 16 KB of whole rows),
-// a ring in the order in which the products take them: K0 K1 V0 K2 V1 ...
+// Roles of a CTA's 20 warps (one CTA per SM), which meet at mbarriers only:
+//   8 softmax warps  two threads a row, 32 of a tile's tokens each: running maximum and sum in base 2, O rescaled only when the
+//                    maximum has grown by more than 2^8; weights go back to tensor memory over the scores they came from;
+//   1 score warp     S = Q K^T (M 128, N 64) into the next of its buffers, queries (bf16 rows) from tensor memory;
+//   1 output warp    O += P V (N 256), P from tensor memory. An instruction of N 64 takes as long as one of N 128 (61 cycles), so Q K^T
+//                    runs at half the rate; 512 columns hold O, the queries and two buffers of 64 scores at 256 dims, not of 128;
+//   1 index warp     page table -> slots, scales, a tile ahead;
+//   1 load warp      tiled TMA loads, a box for each run of a page; or all workers: cp.async of 16 bytes, row by row;
+//   2 or 4 query warps  the rows' queries, the ancestors' bits, and the clean-up of V rows that not every row attends;
+//   5 or 6 workers   cp.async loads; FP8 rows: V's codes -> f16 operands.
+// K and V of a tile lie in shared memory as slots of 128-byte-swizzled blocks, a ring in the order in which the products take
+// them: K0 K1 V0 K2 V1 ... The kernel is as short as it is for the instruction caches' sake: every role runs code of its own, and
+// with the waits and walks inlined (256 KB of it) they waited for instructions three times as long as they issued them.
 //
 // A masked token's weight is zero, but zero times an infinite or undefined V value is not: V rows that no row attends (behind the
 // sequence's end, before its window) become zeros, and values that are not finite in rows that only some attend (drafts, the
 // window's edge) are taken out of the product and added at the end to the rows that attend them.
 //
 // bf16 rows: weights enter the second product as bf16 (2^-8 of each; the decode of one token adds a second bf16 value, which
-// here would make half as many products again). FP8 rows: codes are exact in f16, q enters as f16 scaled by a power of two
-// per row, K's scales multiply the fp32 sums of each 128 dims, V's enter the weights: w = 2^(s + log2 v_scale - m + 8) with m the
-// lazy maximum of s + log2 v_scale, below 2^15, one set for each 128 dims, rounded to f16 (2^-11 of each, 2^-33 of the largest below
-// the normal range).
+// here would make half as many products again). FP8 rows: K's codes are multiplied as they are, q enters as the sum of two E4M3
+// values scaled by a power of two per row (all of a bf16 value down to 2^-10 of the row's largest, smaller ones off by at most
+// 2^-17 of that), K's scales multiply the fp32 sums of each 128 dims; V's codes become f16, exactly, and V's scales enter the weights:
+// w = 2^(s - m) v_scale / u 2^6 with m the lazy maximum and u the power of two next to the largest V scale so far, one set for
+// each 128 dims, below 2^15 and rounded to f16 (2^-11 of each, 2^-31 of the largest weight times the largest scale).
 #include "paged_decode.cuh"
 #include "qsa_tc.cuh"
 
@@ -62,7 +65,7 @@ struct TreeCfg {
     static constexpr int smem = v_at + v_ring * code_slot + 1024;
     static_assert(smem + 12288 <= 227 * 1024, "shared memory of a CTA");
     // tensor memory columns: O, the queries (bf16 rows; with FP8 rows they are in shared memory), buffers of scores
-    static constexpr uint32_t t_o = 0, t_q = F8 ? 0 : D, t_s = D == 256 && !F8 ? 384 : 256, s_cols = SG * kTile;
+    static constexpr uint32_t t_o = 0, t_q = F8 ? 0u : (uint32_t)D, t_s = D == 256 && !F8 ? 384 : 256, s_cols = SG * kTile;
     static constexpr int buffers = (512 - t_s) / s_cols;
     // 20 warps of 96 registers; the query warps' numbers modulo 4 are the four quarters of tensor memory's lanes
     static constexpr int softmax = 256, q_threads = F8 ? 64 : 128, workers = F8 ? 192 : 160;
@@ -71,7 +74,7 @@ struct TreeCfg {
     static constexpr int s_warp = 8, o_warp = 9, index_warp = F8 ? 12 : 10, q_warp = F8 ? 10 : 11, load_warp = F8 ? 13 : 15;
     static constexpr int work_warp = F8 ? 14 : 15;
     static constexpr int threads = 640;
-    static_assert(work_warp * 32 + workers == threads, "roles");
+    static_assert(work_warp * 32 + workers == threads && t_o + D <= t_s && t_q + (F8 ? 0 : D / 2) <= t_s, "roles, columns");
 };
 
 struct TreeMaps {
@@ -301,39 +304,43 @@ __global__ void __launch_bounds__(C::threads, 1)
     constexpr bool tiled = C::tiled;
 
     if (warp == C::s_warp) tmem_alloc(&sh.tmem, 512);
-    if (tid == 0) {
+    {
         // the loads' arrivals: one with the bytes it expects, or every worker's
         const int load = tiled ? 1 : C::workers;
-        for (int i = 0; i < RING; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), F8 ? C::workers / 32 : load);
-            mbar_init(smem_u32(&sh.empty[i]), 1);
+        if (warp == 0 && lane < RING) {
+            mbar_init(smem_u32(&sh.full[lane]), F8 ? C::workers / 32 : load);
+            mbar_init(smem_u32(&sh.empty[lane]), 1);
         }
         if constexpr (F8)
-            for (int i = 0; i < C::k_ring + C::v_ring; ++i) {
-                const bool k = i < C::k_ring;
-                mbar_init(smem_u32(k ? &sh.k_full[i] : &sh.v_full[i - C::k_ring]), load);
-                mbar_init(smem_u32(k ? &sh.k_empty[i] : &sh.v_empty[i - C::k_ring]), k ? 1 : C::workers / 32);
+            if (warp == 1 && lane < C::k_ring + C::v_ring) {
+                const bool k = lane < C::k_ring;
+                mbar_init(smem_u32(k ? &sh.k_full[lane] : &sh.v_full[lane - C::k_ring]), load);
+                mbar_init(smem_u32(k ? &sh.k_empty[lane] : &sh.v_empty[lane - C::k_ring]), k ? 1 : C::workers / 32);
             }
-        for (int i = 0; i < C::buffers; ++i) {
-            mbar_init(smem_u32(&sh.s_full[i]), 1);
-            mbar_init(smem_u32(&sh.p_full[i]), C::softmax / 32);
-            mbar_init(smem_u32(&sh.pv_done[i]), 1);
+        if (warp == 2 && lane < NB) {
+            mbar_init(smem_u32(&sh.s_full[lane]), 1);
+            mbar_init(smem_u32(&sh.p_full[lane]), C::softmax / 32);
+            mbar_init(smem_u32(&sh.pv_done[lane]), 1);
         }
-        for (int i = 0; i < kMetas; ++i) {
-            mbar_init(smem_u32(&sh.meta_full[i]), 1);
-            mbar_init(smem_u32(&sh.meta_empty[i]), C::softmax / 32 + (tiled ? 1 : C::workers / 32));
+        if (warp == 3 && lane < kMetas) {
+            mbar_init(smem_u32(&sh.meta_full[lane]), 1);
+            mbar_init(smem_u32(&sh.meta_empty[lane]), C::softmax / 32 + (tiled ? 1 : C::workers / 32));
         }
-        mbar_init(smem_u32(&sh.to_clean), 1);
-        mbar_init(smem_u32(&sh.clean), C::q_threads);
-        mbar_init(smem_u32(&sh.q_full), C::q_threads);
-        mbar_init(smem_u32(&sh.q_free), 1);
-        mbar_init(smem_u32(&sh.nodes_full), C::q_threads);
-        mbar_init(smem_u32(&sh.nodes_free), C::softmax / 32);
-        mbar_init(smem_u32(&sh.flags_full), C::q_threads);
-        mbar_init(smem_u32(&sh.o_free), C::softmax / 32);
+        if (tid == 128) {
+            mbar_init(smem_u32(&sh.to_clean), 1);
+            mbar_init(smem_u32(&sh.clean), C::q_threads);
+            mbar_init(smem_u32(&sh.q_full), C::q_threads);
+            mbar_init(smem_u32(&sh.q_free), 1);
+            mbar_init(smem_u32(&sh.nodes_full), C::q_threads);
+            mbar_init(smem_u32(&sh.nodes_free), C::softmax / 32);
+            mbar_init(smem_u32(&sh.flags_full), C::q_threads);
+            mbar_init(smem_u32(&sh.o_free), C::softmax / 32);
+        }
         fence_mbar_init();
-        tma_prefetch_desc(&maps.k);
-        tma_prefetch_desc(&maps.v);
+        if (tiled && tid == 160) {
+            tma_prefetch_desc(&maps.k);
+            tma_prefetch_desc(&maps.v);
+        }
     }
     wait_for_previous();
 
@@ -1234,6 +1241,7 @@ cudaError_t launch_as(const TreeArgs &a, int run, cudaStream_t st) {
     TreePlan plan{};
     plan.m_tiles = m_tiles_of(a.G, a.max_draft);
     plan.ranges = std::max(1, ctas / (a.Hkv * plan.m_tiles));
+    // the least length of a part: one sequence of 4,096 tokens took 19.9, 19.2, 20.6 and 24.0 us with 1, 2, 4 and 8 tiles
     plan.min_tiles = 2;
     plan.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     TreeMaps maps;
