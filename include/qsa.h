@@ -794,8 +794,8 @@ QSA_API size_t qsa_keep_workspace_size(int32_t n_rows, int64_t max_tokens);
  *   draft_off [n_rows + 1]; parent [N]; accepted, seq_len, seq_len_out [n_rows]; table, table_out [n_rows][ld]; ref, ref_out
  *   [n_pages] (each _out another array); n_rows <= 65536, n_pages page_size < 2^31; positions (NULL: none) [n_rows][positions_ld] int32, moved along in
  *   place; planes as in qsa_fork_pages, page_bytes a multiple of page_size x 4.
- * A row whose seq_len, draft_off, parents or accepted are out of range (QSA_ERR_DEVICE_BOUNDS, the row) keeps all its
- * tokens; a page out of range is left out. */
+ * A row whose seq_len, draft_off, parents or accepted are out of range, or whose tokens would move into a page that other
+ * references share (ref > 1), keeps all its tokens (QSA_ERR_DEVICE_BOUNDS, the row); a page out of range is left out. */
 QSA_API qsa_status qsa_accept_drafts(int32_t page_size, const int32_t *draft_off, const int32_t *parent, int32_t N,
                                      const int32_t *accepted, const int32_t *table, const int32_t *seq_len,
                                      int32_t n_rows, int64_t ld, const int32_t *ref, int64_t n_pages, int32_t *table_out,

@@ -146,10 +146,34 @@ __global__ void __launch_bounds__(kKeepThreads) accept_kernel(KeepArgs a, Accept
             }
         found[0] = n;
         found[1] = 0;
-        if (n < 0 && part == 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereKeep, r);
     }
     __syncthreads();
-    const int n = found[0], base = len - T, new_len = n < 0 ? len : base + n;
+    const int base = len - T;
+    if (tid < 32) {                                  // the moves, in order; a token already in place stays
+        const int n = found[0];
+        bool shared = false;                         // a move into a page that others read too
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            const int k = k0 + tid, i = k < n ? node[n - 1 - k] : 0;
+            const bool moves = k < n && i != k;
+            const uint32_t all = __ballot_sync(0xffffffffu, moves);
+            const int at = found[1] + __popc(all & ((1u << tid) - 1u));
+            __syncwarp();
+            if (moves) {
+                const int s = slot_of(a, row, base + i), t = slot_of(a, row, base + k);
+                if (part == 0 && (s < 0 || t < 0)) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereKeep, r);
+                shared |= t >= 0 && a.ref[a.page_shift >= 0 ? t >> a.page_shift : t / a.page_size] > 1;
+                from[at] = t < 0 ? -1 : s;
+                to[at] = t;
+            }
+            if (tid == 0) found[1] += __popc(all);
+            __syncwarp();
+        }
+        shared = __any_sync(0xffffffffu, shared);
+        if (tid == 0 && shared) found[0] = -1;
+        if (tid == 0 && part == 0 && found[0] < 0) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereKeep, r);
+    }
+    __syncthreads();
+    const int n = found[0], new_len = n < 0 ? len : base + n;
     if (part == 0) {
         if (tid == 0) a.seq_len_out[r] = new_len;
         if (n < 0) {
@@ -166,23 +190,6 @@ __global__ void __launch_bounds__(kKeepThreads) accept_kernel(KeepArgs a, Accept
         }
     }
     if (n < 0) return;
-    if (tid < 32)                                    // the moves, in order; a token already in place stays
-        for (int k0 = 0; k0 < n; k0 += 32) {
-            const int k = k0 + tid, i = k < n ? node[n - 1 - k] : 0;
-            const bool moves = k < n && i != k;
-            const uint32_t all = __ballot_sync(0xffffffffu, moves);
-            const int at = found[1] + __popc(all & ((1u << tid) - 1u));
-            __syncwarp();
-            if (moves) {
-                const int s = slot_of(a, row, base + i), t = slot_of(a, row, base + k);
-                if (part == 0 && (s < 0 || t < 0)) record_error(a.hdr, QSA_ERR_DEVICE_BOUNDS, kWhereKeep, r);
-                from[at] = t < 0 ? -1 : s;
-                to[at] = t;
-            }
-            if (tid == 0) found[1] += __popc(all);
-            __syncwarp();
-        }
-    __syncthreads();
     const int moves = found[1];
     if (moves > 0)
         for (int gi = 0; gi < pg.n; ++gi) {

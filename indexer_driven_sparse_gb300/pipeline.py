@@ -256,7 +256,8 @@ class PagedCache:
     Drafted tokens (max_draft > 0, the most in a row): room by ``extend(count)``, then per layer ``append`` with their places
     and positions and ``attend_tree``; ``accept`` keeps the accepted path. An evictable cache accumulates in ``weights[r, j]``
     what token j of row r receives (``attend`` with weigh=True) and holds its position in ``positions[r, j]`` (``append`` of
-    layer 0 with a place); ``evict`` cuts rows to a budget. Its window must be 0: places are no positions any more."""
+    layer 0); ``evict`` cuts rows to a budget. Its window must be 0: places are no positions any more. A row of it that ran
+    out of pages is started again by ``fork``, which clears what it had received."""
 
     def __init__(self, n_layers: int, n_pages: int, page_size: int, n_rows: int, max_pages: int, n_q_heads: int,
                  n_kv_heads: int, head_dim: int = 256, fp8: bool = False, softmax_scale: float = 0.0, window: int = 0,
@@ -316,13 +317,17 @@ class PagedCache:
     def positions(self):
         return self._positions[self._weights_now]
 
+    def _made_for(self, made, what):
+        if not made:
+            raise ValueError(f"the cache was made without {what}")
+
     def fork(self, parent, add, stream=None):
         """Row i continues row parent[i] (-1: starts empty) with room for add[i] more tokens (qsa_fork_pages)."""
         self._fork(parent, add, stream)
         if self.evictable:                            # what is kept per row goes with it
             new = 1 - self._weights_now
             with _on_stream(stream):
-                row, empty = parent.clamp(min=0, max=self.n_rows - 1), (parent < 0)[:, None]
+                row, empty = parent.clamp(min=0, max=self.n_rows - 1), ((parent < 0) | (self.seq_len == 0))[:, None]
                 torch.index_select(self.weights, 0, row, out=self._weights[new]).masked_fill_(empty, 0.0)
                 torch.index_select(self.positions, 0, row, out=self._positions[new]).masked_fill_(empty, -1)
             self._weights_now = new
@@ -350,8 +355,10 @@ class PagedCache:
         """Store k (turned) and v at position pos[n] of row seq[n] (None: row n) of a layer; q turned into q_out. place[n]:
         the token's place in its row, where that is not its position."""
         planes = [p[layer] for p in self.planes]
+        positions = self.positions if self.evictable and layer == 0 else None
+        if positions is not None and place is None:   # recorded all the same
+            place = pos
         if place is not None:
-            positions = self.positions if self.evictable and layer == 0 else None
             if self.fp8:
                 qb.qsa_rope_append_at_fp8kv(self.cfg, rope, q, k, v, pos, place, seq, q_out, planes, self.table, self.ws,
                                             positions, stream)
@@ -369,6 +376,7 @@ class PagedCache:
         to ``weights``."""
         planes = [p[layer] for p in self.planes]
         if weigh:
+            self._made_for(self.evictable, "evictable")
             if self.fp8:
                 qb.qsa_paged_decode_weights_fp8kv(self.cfg, q, planes, self.table, self.seq_len, out, lse, self.weights,
                                                   self.weights_ws, stream)
@@ -383,6 +391,7 @@ class PagedCache:
 
     def attend_tree(self, layer: int, q, draft_off, parent, out, lse=None, stream=None):
         """Attention of every row's drafted tokens, its newest, each over the cached tokens, its ancestors and itself."""
+        self._made_for(self.max_draft, "max_draft")
         planes = [p[layer] for p in self.planes]
         if self.fp8:
             qb.qsa_tree_decode_fp8kv(self.cfg, q, draft_off, parent, self.max_draft, planes, self.table, self.seq_len, out,
@@ -393,6 +402,7 @@ class PagedCache:
 
     def accept(self, draft_off, parent, accepted, stream=None):
         """Of each row's drafted tokens keep accepted[r] (-1: none) and its ancestors (qsa_accept_drafts)."""
+        self._made_for(self.max_draft, "max_draft")
         new, new_ref = 1 - self._now, 1 - self._ref_now
         qb.qsa_accept_drafts(self.cfg.page_size, draft_off, parent, accepted, self.table, self.seq_len, self.ref,
                              self._tables[new], self._lens[new], self._refs[new_ref], self.planes, self.keep_ws,
@@ -402,6 +412,7 @@ class PagedCache:
     def evict(self, budget, first: int, recent: int, stream=None):
         """Cut row r to budget[r] tokens (negative: as it is): positions below `first`, the last `recent` ones and shared
         pages stay, and the heaviest of the others (qsa_evict_tokens)."""
+        self._made_for(self.evictable, "evictable")
         new, new_ref, new_w = 1 - self._now, 1 - self._ref_now, 1 - self._weights_now
         qb.qsa_evict_tokens(self.cfg.page_size, budget, first, recent, self.weights, self.positions, self.table, self.seq_len,
                             self.ref, self._weights[new_w], self._positions[new_w], self._tables[new], self._lens[new],

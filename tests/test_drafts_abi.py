@@ -8,6 +8,7 @@ import pytest
 
 from indexer_driven_sparse_gb300 import binding as qb
 from indexer_driven_sparse_gb300 import build as qbuild
+from indexer_driven_sparse_gb300.pipeline import PagedCache
 from oracle import drafts_oracle as T
 from tests.test_paged_abi import BAD, FAKE, SMALL, UNSUPPORTED, rope_cfg
 
@@ -202,3 +203,14 @@ def test_oracle_of_trees_and_eviction_by_hand():
     assert T.evict(w, pos, [True] * 4 + [False] * 2, 2, 0, 0) == (4, [])    # four in shared pages
     table, ref = T.release([[4, 2, -1], [1, 0, 3]], [1, 1, 1, 1, 1], [5, 9], [3, 4], 4)
     assert table.tolist() == [[4, -1, -1], [1, -1, -1]] and ref.tolist() == [0, 1, 0, 0, 1]
+
+
+def test_a_cache_refuses_what_it_was_not_made_for():
+    cache = object.__new__(PagedCache)                    # no GPU here: only what the checks read
+    cache.max_draft, cache.evictable, cache.planes = 0, False, []
+    for call in (lambda: cache.attend_tree(0, None, None, None, None), lambda: cache.accept(None, None, None)):
+        with pytest.raises(ValueError, match="max_draft"):
+            call()
+    for call in (lambda: cache.evict(None, 0, 0), lambda: cache.attend(0, None, None, weigh=True)):
+        with pytest.raises(ValueError, match="evictable"):
+            call()

@@ -600,6 +600,31 @@ def test_evict_rows_out_of_range_are_left(cuda_lib):
         assert bool((r_out[mine] == 1).all())
 
 
+def test_accept_moves_nothing_into_shared_pages(cuda_lib):
+    """A row forked with its drafts in full pages that both rows name: what would move into them stays, in this row alone;
+    a path that is in place already may be kept."""
+    page, lens, off, parents = 4, [12, 12, 12], [0, 6, 12, 18], [-1, 0, 1, 0, -1, 4]
+    table, ref = private_pool(lens, page, 1)
+    ref[table[0, 1]] += 1
+    ref[table[1, 1]] += 1
+    last = [5, 1, 5]                                      # rows 0 and 2 move two tokens, row 1's first two are in place
+    planes = token_planes(len(ref), page, 1)
+    cut = [(12, []), T.accept(12, parents, 1), T.accept(12, parents, 5)]
+    want = [moved(p, table, {r: c[1] for r, c in enumerate(cut)}, page) for p in planes]
+    t_out, l_out, r_out = filled(3, table.shape[1]), filled(3), filled(len(ref))
+    positions = ints(np.arange(3 * 12).reshape(3, 12).tolist())
+    ws = qb.keep_workspace(3)
+    qb.qsa_accept_drafts(page, ints(off), ints(parents * 3), ints(last), ints(table.tolist()), ints(lens), ints(ref.tolist()),
+                         t_out, l_out, r_out, planes, ws, positions)
+    assert status(ws) == (qb.QSA_ERR_DEVICE_BOUNDS, 0)
+    want_t, want_r = T.release(table, ref, lens, [c[0] for c in cut], page)
+    assert l_out.tolist() == [12, 8, 8]
+    assert np.array_equal(t_out.cpu().numpy(), want_t) and np.array_equal(r_out.cpu().numpy(), want_r)
+    assert positions[:2].tolist() == np.arange(24).reshape(2, 12).tolist() and positions[2, 6:8].tolist() == [34, 35]
+    for got, w in zip(planes, want):
+        assert torch.equal(got, w)
+
+
 def test_evict_leaves_out_and_records_bad_pages(cuda_lib):
     """A page out of range: its tokens' contents do not move, and nothing outside the pool is touched."""
     page, lens = 4, [30]
@@ -749,6 +774,28 @@ def test_a_decode_loop_under_a_budget(cuda_lib, fp8):
             where = [where[p] for p in parent]
             cache.compact()
     assert cache.status() == ((0, 0), (0, 0)) and cache.more_status() == ((0, 0),) * 3
+
+
+def test_an_evictable_cache_keeps_its_own_records(cuda_lib):
+    """Tokens appended by position alone have their positions recorded; rows that a fork empties have received nothing."""
+    Hq, Hkv, D, page, S = 4, 1, 64, 4, 2
+    rope = qb.rope_table(D)
+    cache = PagedCache(2, 6, page, S, 6, Hq, Hkv, D, evictable=True)
+    cache.fork(ints([-1] * S), ints([6, 5]))
+    x = randn((11, 2 * Hkv, D), 1)
+    seq, pos = ints([0] * 6 + [1] * 5), ints(list(range(6)) + list(range(5)))
+    for layer in range(2):
+        cache.append(layer, rope, None, x[:, :Hkv], x[:, Hkv:], pos, seq)
+    assert cache.positions[0, :6].tolist() == list(range(6)) and cache.positions[1, :5].tolist() == list(range(5))
+    q = randn((S, Hq, D), 2)
+    cache.attend(0, q, torch.empty_like(q), weigh=True)
+    assert bool((cache.weights[0, :6] > 0).all()) and bool((cache.weights[1, :5] > 0).all())
+    cache.evict(ints([3, -1]), 0, 1)
+    assert cache.seq_len.tolist() == [3, 5] and cache.positions[0, :3].max() == 5
+    assert cache.status() == ((0, 0), (0, 0)) and cache.more_status() == ((0, 0), (0, 0))
+    cache.fork(ints([0, 1]), ints([0, 100]))              # row 1 is out of pages, and empty
+    assert cache.status()[1] == (qb.QSA_ERR_DEVICE_BOUNDS, 1) and cache.seq_len.tolist() == [3, 0]
+    assert not cache.weights[1].any() and bool((cache.positions[1] == -1).all()) and bool((cache.weights[0, :3] > 0).all())
 
 
 def test_captured_speculative_steps_replay(cuda_lib):
