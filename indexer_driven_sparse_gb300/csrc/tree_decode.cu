@@ -46,7 +46,6 @@ namespace {
 
 constexpr int kRows = 128;                       // MMA M: rows of a CTA
 constexpr int kTile = 64;                        // tokens of a tile
-constexpr int kMetas = 4;                        // tiles whose slots and scales are known
 constexpr float kLazy = 8.f;                     // O is rescaled when a maximum has grown by more than 2^8
 constexpr float kRaise = 6.f;                    // FP8 rows: weights up to 2^8, scales below 2, so below 2^15 in f16
 
@@ -63,10 +62,11 @@ struct TreeCfg {
     static constexpr int k_ring = F8 ? (D == 256 ? 3 : 6) : 0, v_ring = F8 ? (D == 256 ? 2 : 6) : 0;
     static constexpr int ring_at = F8 ? kRows * D * 2 : 0, k_at = ring_at + ring * slot, v_at = k_at + k_ring * code_slot;
     static constexpr int smem = v_at + v_ring * code_slot + 1024;
-    static_assert(smem + 12288 <= 227 * 1024, "shared memory of a CTA");
+    static_assert(smem + 17920 <= 227 * 1024, "shared memory of a CTA");
     // tensor memory columns: O, the queries (bf16 rows; with FP8 rows they are in shared memory), buffers of scores
     static constexpr uint32_t t_o = 0, t_q = F8 ? 0u : (uint32_t)D, t_s = D == 256 && !F8 ? 384 : 256, s_cols = SG * kTile;
     static constexpr int buffers = (512 - t_s) / s_cols;
+    static constexpr int metas = D == 128 ? 16 : 8;              // tiles whose slots and scales are known
     // 20 warps of 96 registers; the query warps' numbers modulo 4 are the four quarters of tensor memory's lanes
     static constexpr int softmax = 256, q_threads = F8 ? 64 : 128, workers = F8 ? 192 : 160;
     // FP8 rows: the converting warps 14 to 19 are two on schedulers 2 and 3; the index warp beside two of them slowed their softmax
@@ -76,6 +76,43 @@ struct TreeCfg {
     static constexpr int threads = 640;
     static_assert(work_warp * 32 + workers == threads && t_o + D <= t_s && t_q + (F8 ? 0 : D / 2) <= t_s, "roles, columns");
 };
+
+// Two fp32 values an instruction, each rounded as alone.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 get2(const float *v, int k) { return make_float2(v[2 * k], v[2 * k + 1]); }
+__device__ __forceinline__ void set2(float *v, int k, float2 x) { v[2 * k] = x.x, v[2 * k + 1] = x.y; }
+
+// 16 consecutive fp32 columns of tensor memory.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 
 struct TreeMaps {
     CUtensorMap k, v;
@@ -167,16 +204,16 @@ template <typename C>
 struct TreeShared {
     uint64_t full[C::ring], empty[C::ring];
     uint64_t k_full[C::F8 ? C::k_ring : 1], k_empty[C::F8 ? C::k_ring : 1], v_full[C::F8 ? C::v_ring : 1], v_empty[C::F8 ? C::v_ring : 1];
-    uint64_t s_full[C::buffers], p_full[C::buffers], pv_done[C::buffers], meta_full[kMetas], meta_empty[kMetas];
+    uint64_t s_full[C::buffers], p_full[C::buffers], pv_done[C::buffers], meta_full[C::metas], meta_empty[C::metas];
     uint64_t to_clean, clean, q_full, q_free, nodes_full, nodes_free, flags_full, o_free;
     uint32_t kin[QSA_MAX_DRAFT][QSA_MAX_DRAFT / 32];      // of each drafted token: itself and its ancestors inside the window
     int lo[QSA_MAX_DRAFT];                                // its first attended place
     uint32_t odd[2][QSA_MAX_DRAFT / 32];                  // tokens with values that are not finite: drafts, places from r.lo
     float q_scale[2][C::F8 ? kRows : 1];               // of every other segment
-    int slots[kMetas][kTile];
-    uint32_t real[kMetas][kTile / 32];                     // bit: the token's page exists
-    float4 k_scales[kMetas][C::SG][C::F8 ? kTile / 4 : 1], v_scales[kMetas][C::SG][C::F8 ? kTile / 4 : 1];   // four tokens each
-    float2 top[kMetas];                                   // powers of two at most 2 below the tile's largest V scales
+    int slots[C::metas][kTile];
+    uint32_t real[C::metas][kTile / 32];                     // bit: the token's page exists
+    float4 k_scales[C::metas][C::SG][C::F8 ? kTile / 4 : 1], v_scales[C::metas][C::SG][C::F8 ? kTile / 4 : 1];   // four tokens each
+    float2 top[C::metas];                                   // powers of two at most 2 below the tile's largest V scales
     float tops[2][2][kRows];                              // of every other tile: the halves' maxima
     uint32_t tmem;
 };
@@ -322,7 +359,7 @@ __global__ void __launch_bounds__(C::threads, 1)
             mbar_init(smem_u32(&sh.p_full[lane]), C::softmax / 32);
             mbar_init(smem_u32(&sh.pv_done[lane]), 1);
         }
-        if (warp == 3 && lane < kMetas) {
+        if (warp == 3 && lane < C::metas) {
             mbar_init(smem_u32(&sh.meta_full[lane]), 1);
             mbar_init(smem_u32(&sh.meta_empty[lane]), C::softmax / 32 + (tiled ? 1 : C::workers / 32));
         }
@@ -490,8 +527,8 @@ __global__ void __launch_bounds__(C::threads, 1)
                     more = w.next(a, m_tile, g);
                     if (more) enter(), fetch(g.ta);
                 }
-                const int m = done % kMetas;
-                if (done >= kMetas && !wait_warp(&sh.meta_empty[m], done / kMetas - 1)) {
+                const int m = done % C::metas;
+                if (done >= C::metas && !wait_warp(&sh.meta_empty[m], done / C::metas - 1)) {
                     ok = false;
                     break;
                 }
@@ -544,8 +581,8 @@ __global__ void __launch_bounds__(C::threads, 1)
         int asked[2] = {0, 0};                                // slots asked for, of each ring
         // a tile's K or V into the slot of turn q
         auto copy = [&](int is_v, int tile, int q) -> bool {
-            const int m = tile % kMetas;
-            if (!is_v && !wait_warp(&sh.meta_full[m], tile / kMetas)) return false;
+            const int m = tile % C::metas;
+            if (!is_v && !wait_warp(&sh.meta_full[m], tile / C::metas)) return false;
             const int box = sh.slots[m][tiled ? run * plan.run : 0], y = box < 0 ? rows_end : box;
             // FP8 rows: rings of their own, by tiles; bf16 rows: one, by turns
             const int slots = F8 ? (is_v ? C::v_ring : C::k_ring) : RING, x = F8 ? tile : q, at = x % slots, turn = x / slots;
@@ -709,38 +746,52 @@ __global__ void __launch_bounds__(C::threads, 1)
                 }
                 tc_fence_before();
             } else {
-                // D / 8 lanes have a row, 8 values each
-                constexpr int each = C::q_threads / (D / 8);
-#pragma unroll 4
-                for (int i = 0; i < kRows / each; ++i) {
-                    const int r = i * each + qt / (D / 8), gr = qt % (D / 8);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (r < rows) v = *reinterpret_cast<const uint4 *>(row_at(r) + gr * 8);
-                    float f[8], top = 0.f;
-                    unpack8(v, f);
+                // D / 16 lanes have a row, 16 values each, four rows on their way. Rows without a token keep the codes that are there,
+                // which reach no other row.
+                constexpr int each = C::q_threads / (D / 16), U = 4;
+                static_assert(kRows % (U * each) == 0, "rows");
+                const int gr = qt % (D / 16);
+                for (int r = qt; r < kRows; r += C::q_threads)
+                    if (r >= rows) sh.q_scale[seg & 1][r] = 0.f;
+#pragma unroll 1
+                for (int i = qt / (D / 16); i - qt / (D / 16) < min(rows, kRows); i += U * each) {
+                    uint4 v[U][2];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
-#pragma unroll
-                    for (int o = D / 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // the largest becomes 2^7 .. 2^8; an infinite one makes the row NaN, not E4M3's largest value
-                    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -119), 126);
-                    const float down = top == INFINITY ? NAN : __uint_as_float((uint32_t)(134 - e) << 23);
-                    uint32_t part[2][2] = {};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float x = f[2 * k] * down, y = f[2 * k + 1] * down;
-                        const uint32_t c = e4m3x2_of(x, y), back = e4m3_to_f16x2(c, 0);
-                        const float2 near = __half22float2(*reinterpret_cast<const __half2 *>(&back));
-                        part[0][k >> 1] |= c << (16 * (k & 1));
-                        part[1][k >> 1] |= e4m3x2_of(x - near.x, y - near.y) << (16 * (k & 1));
+                    for (int u = 0; u < U; ++u) {
+                        const bool in = i + u * each < rows;
+                        const uint4 *from = reinterpret_cast<const uint4 *>(row_at(in ? i + u * each : 0) + gr * 16);
+                        v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+                        if (in) v[u][0] = from[0], v[u][1] = from[1];
                     }
-                    // first parts, then second ones; 128 dims are a block of 128 bytes
 #pragma unroll
-                    for (int z = 0; z < 2; ++z)
-                        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(q_at + (z * SG + gr / 16) * (kRows * 128) + swz(r, gr / 2 & 7) + (gr & 1) * 8),
-                                     "r"(part[z][0]), "r"(part[z][1])
-                                     : "memory");
-                    if (gr == 0) sh.q_scale[seg & 1][r] = __uint_as_float((uint32_t)(120 + e) << 23);
+                    for (int u = 0; u < U; ++u) {
+                        const int r = i + u * each;
+                        float f[2][8], top = 0.f;
+                        unpack8(v[u][0], f[0]), unpack8(v[u][1], f[1]);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(f[k >> 3][k & 7]));
+#pragma unroll
+                        for (int o = D / 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        // the largest becomes 2^7 .. 2^8; an infinite one makes the row NaN, not E4M3's largest value
+                        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -119), 126);
+                        const float down = top == INFINITY ? NAN : __uint_as_float((uint32_t)(134 - e) << 23);
+                        uint32_t part[2][4] = {};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float x = f[k >> 2][2 * k & 7] * down, y = f[k >> 2][(2 * k & 7) + 1] * down;
+                            const uint32_t c = e4m3x2_of(x, y), back = e4m3_to_f16x2(c, 0);
+                            const float2 near = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+                            part[0][k >> 1] |= c << (16 * (k & 1));
+                            part[1][k >> 1] |= e4m3x2_of(x - near.x, y - near.y) << (16 * (k & 1));
+                        }
+                        // first parts, then second ones; 128 dims are a block of 128 bytes
+#pragma unroll
+                        for (int z = 0; z < 2; ++z)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(q_at + (z * SG + gr / 8) * (kRows * 128) + swz(r, gr & 7)),
+                                         "r"(part[z][0]), "r"(part[z][1]), "r"(part[z][2]), "r"(part[z][3])
+                                         : "memory");
+                        if (gr == 0 && r < rows) sh.q_scale[seg & 1][r] = __uint_as_float((uint32_t)(120 + e) << 23);
+                    }
                 }
                 fence_proxy_async_smem();
             }
@@ -932,8 +983,8 @@ __global__ void __launch_bounds__(C::threads, 1)
             float2 unit = make_float2(0.f, 0.f);          // FP8: O is in units of these over 2^kRaise
 #pragma unroll 1
             for (int c = 0; c < n; ++c) {
-                const int i = g.i0 + c, t = g.ta + c, m = i % kMetas;
-                if (!wait_warp(&sh.meta_full[m], i / kMetas)) {
+                const int i = g.i0 + c, t = g.ta + c, m = i % C::metas;
+                if (!wait_warp(&sh.meta_full[m], i / C::metas)) {
                     ok = false;
                     break;
                 }
@@ -974,16 +1025,21 @@ __global__ void __launch_bounds__(C::threads, 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const float4 s4 = sh.k_scales[m][0][half * 8 + k];
-                            v[4 * k] *= s4.x, v[4 * k + 1] *= s4.y, v[4 * k + 2] *= s4.z, v[4 * k + 3] *= s4.w;
+                            set2(v, 2 * k, mul2(get2(v, 2 * k), make_float2(s4.x, s4.y)));
+                            set2(v, 2 * k + 1, mul2(get2(v, 2 * k + 1), make_float2(s4.z, s4.w)));
                         }
                         if constexpr (SG == 2) {
-                            float u[32];
-                            tmem_ld32(t_s + 64 + 32 * half, u);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float4 s4 = sh.k_scales[m][1][half * 8 + k];
-                                v[4 * k] = fmaf(u[4 * k], s4.x, v[4 * k]), v[4 * k + 1] = fmaf(u[4 * k + 1], s4.y, v[4 * k + 1]);
-                                v[4 * k + 2] = fmaf(u[4 * k + 2], s4.z, v[4 * k + 2]), v[4 * k + 3] = fmaf(u[4 * k + 3], s4.w, v[4 * k + 3]);
+                            for (int k0 = 0; k0 < 8; k0 += 4) {       // 16 at a time, for the registers' sake
+                                float u[16];
+                                tmem_ld16(t_s + 64 + 32 * half + 4 * k0, u);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float4 s4 = sh.k_scales[m][1][half * 8 + k0 + k];
+                                    const int at = 2 * (k0 + k);
+                                    set2(v, at, fma2(get2(u, 2 * k), make_float2(s4.x, s4.y), get2(v, at)));
+                                    set2(v, at + 1, fma2(get2(u, 2 * k + 1), make_float2(s4.z, s4.w), get2(v, at + 1)));
+                                }
                             }
                         }
                     }
@@ -1002,13 +1058,14 @@ __global__ void __launch_bounds__(C::threads, 1)
                         ref = top;
                     }
                     const float at = ref == -INFINITY ? 0.f : ref;
-                    float ps[4] = {0.f, 0.f, 0.f, 0.f};
+                    float2 ps[2] = {};
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        v[k] = ex2(fmaf(v[k], scale, -at));
-                        ps[k & 3] += v[k];
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 e = fma2(get2(v, k), make_float2(scale, scale), make_float2(-at, -at));
+                        set2(v, k, make_float2(ex2(e.x), ex2(e.y)));
+                        ps[k & 1] = add2(ps[k & 1], get2(v, k));
                     }
-                    l = fmaf(l, f, (ps[0] + ps[1]) + (ps[2] + ps[3]));
+                    l = fmaf(l, f, (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y));
                     if constexpr (!F8) {
                         uint32_t pk[16];
 #pragma unroll
@@ -1021,8 +1078,9 @@ __global__ void __launch_bounds__(C::threads, 1)
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
                                 const float4 s4 = sh.v_scales[m][x][half * 8 + k];
-                                pk[2 * k] = f16x2(v[4 * k] * s4.x, v[4 * k + 1] * s4.y);
-                                pk[2 * k + 1] = f16x2(v[4 * k + 2] * s4.z, v[4 * k + 3] * s4.w);
+                                const float2 w0 = mul2(get2(v, 2 * k), make_float2(s4.x, s4.y));
+                                const float2 w1 = mul2(get2(v, 2 * k + 1), make_float2(s4.z, s4.w));
+                                pk[2 * k] = f16x2(w0.x, w0.y), pk[2 * k + 1] = f16x2(w1.x, w1.y);
                             }
                             tmem_st16(t_s + 32 * x + 16 * half, pk);
                         }
@@ -1041,7 +1099,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                         const float by = !F8 ? f : c0 < 128 ? f * (was.x / unit.x) : f * (was.y / unit.y);
                         tmem_ld32(t_o + c0, v);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] *= by;
+                        for (int k = 0; k < 16; ++k) set2(v, k, mul2(get2(v, k), make_float2(by, by)));
                         tmem_st32(t_o + c0, v);
                     }
                 }
