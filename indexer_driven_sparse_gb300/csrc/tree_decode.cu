@@ -17,7 +17,7 @@
 //   1 score warp     S = Q K^T (M 128, N 64) into the next of its buffers, queries (bf16 rows) from tensor memory;
 //   1 output warp    O += P V (N 256), P from tensor memory. An instruction of N 64 takes as long as one of N 128 (61 cycles), so Q K^T
 //                    runs at half the rate; 512 columns hold O, the queries and two buffers of 64 scores at 256 dims, not of 128;
-//   1 index warp     page table -> slots, scales, a tile ahead;
+//   1 index warp     page table -> slots, scales, up to 8 or 16 tiles ahead;
 //   1 load warp      tiled TMA loads, a box for each run of a page; or all workers: cp.async of 16 bytes, row by row;
 //   2 or 4 query warps  the rows' queries, the ancestors' bits, and the clean-up of V rows that not every row attends;
 //   5 or 6 workers   cp.async loads; FP8 rows: V's codes -> f16 operands.
@@ -66,7 +66,8 @@ struct TreeCfg {
     // tensor memory columns: O, the queries (bf16 rows; with FP8 rows they are in shared memory), buffers of scores
     static constexpr uint32_t t_o = 0, t_q = F8 ? 0u : (uint32_t)D, t_s = D == 256 && !F8 ? 384 : 256, s_cols = SG * kTile;
     static constexpr int buffers = (512 - t_s) / s_cols;
-    static constexpr int metas = D == 128 ? 16 : 8;              // tiles whose slots and scales are known
+    // tiles whose slots and scales are known: 4, 6, 8 and 16 of them took 270, 264, 254 and 251 us over 128 ragged sequences of FP8 rows
+    static constexpr int metas = D == 128 ? 16 : 8;
     // 20 warps of 96 registers; the query warps' numbers modulo 4 are the four quarters of tensor memory's lanes
     static constexpr int softmax = 256, q_threads = F8 ? 64 : 128, workers = F8 ? 192 : 160;
     // FP8 rows: the converting warps 14 to 19 are two on schedulers 2 and 3; the index warp beside two of them slowed their softmax
@@ -211,9 +212,9 @@ struct TreeShared {
     uint32_t odd[2][QSA_MAX_DRAFT / 32];                  // tokens with values that are not finite: drafts, places from r.lo
     float q_scale[2][C::F8 ? kRows : 1];               // of every other segment
     int slots[C::metas][kTile];
-    uint32_t real[C::metas][kTile / 32];                     // bit: the token's page exists
+    uint32_t real[C::metas][kTile / 32];                   // bit: the token's page exists
     float4 k_scales[C::metas][C::SG][C::F8 ? kTile / 4 : 1], v_scales[C::metas][C::SG][C::F8 ? kTile / 4 : 1];   // four tokens each
-    float2 top[C::metas];                                   // powers of two at most 2 below the tile's largest V scales
+    float2 top[C::metas];                                 // powers of two at most 2 below the tile's largest V scales
     float tops[2][2][kRows];                              // of every other tile: the halves' maxima
     uint32_t tmem;
 };
@@ -644,10 +645,11 @@ __global__ void __launch_bounds__(C::threads, 1)
                               (uint32_t)(q / slots) & 1u, a.hdr);
             }
         } else if constexpr (F8) {
-            // Without TMA the codes of a turn are asked for `ahead` turns before its V, if it is one, is converted. At most 6: a tile's
-            // K is asked for when the softmax has left the tile four before it, which needs the V turns up to seven before this one
-            // converted; and as many turns as the rings hold, which a turn that is asked for may have to wait for.
+            // Without TMA the codes of a turn are asked for `ahead` turns before its V, if it is one, is converted: at most as many as
+            // the rings hold, which a turn that is asked for may have to wait for, and fewer than 2 metas - 1, since a tile's K is
+            // asked for when the softmax has left the tile `metas` before it, and with it when that tile's V has been converted.
             constexpr int ahead = D == 256 ? 2 : 6;
+            static_assert(ahead < 2 * C::metas - 1, "turns");
             // a thread's chunks of 16 codes, the same in every slot: chunk `gr` of token `tok`, and where its two granules go. The
             // second half of a token's chunks goes in the other order, to other banks than the first half's.
             constexpr int N = (T * row_chunks + C::workers - 1) / C::workers;
@@ -1030,7 +1032,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                         }
                         if constexpr (SG == 2) {
 #pragma unroll
-                            for (int k0 = 0; k0 < 8; k0 += 4) {       // 16 at a time, for the registers' sake
+                            for (int k0 = 0; k0 < 8; k0 += 4) {       // all at once, registers spilled: 351 us, 307 so
                                 float u[16];
                                 tmem_ld16(t_s + 64 + 32 * half + 4 * k0, u);
 #pragma unroll
@@ -1329,11 +1331,10 @@ cudaError_t launch_as(const TreeArgs &a, int run, cudaStream_t st) {
 
 template <int D, bool F8>
 cudaError_t launch(const TreeArgs &a, cudaStream_t st) {
-    // Tiled loads of runs of a page. bf16 rows of 256 dims, 32 sequences of 4,096 to 32,768 tokens, runs of 32, 16 and 8 tokens: 232, 268
-    // and 371 us, by cp.async 264; FP8 rows, whose workers convert as well: runs of 16, 8 and 4 tokens 372, 393 and 498, by cp.async 515
-    // to 524.
+    // Tiled loads of runs of a page. 32 sequences of 4,096 to 32,768 tokens, 256 dims: bf16 rows in runs of 32 and 16 tokens 247 and 273 us,
+    // by cp.async 273; FP8 rows, whose workers convert as well, in runs of 16, 8 and 4 tokens 279, 337 and 451, by cp.async 384 to 401.
     const int run = std::min(a.page_size & -a.page_size, kTile);
-    return run >= (F8 ? 4 : 16) && a.n_pages > 0 ? launch_as<D, F8, true>(a, run, st) : launch_as<D, F8, false>(a, 0, st);
+    return run >= (F8 ? 8 : 16) && a.n_pages > 0 ? launch_as<D, F8, true>(a, run, st) : launch_as<D, F8, false>(a, 0, st);
 }
 
 }  // namespace
