@@ -201,6 +201,11 @@ __device__ __forceinline__ bool masked(const TreeArgs &a, const TreeRow &r, int 
     return j0 > r.base - kTile || (a.window > 0 && j0 < r.base + r.T - a.window);
 }
 
+// Whether every row attends token j of [r.lo, r.len). In a tile that is masked some tokens are for all rows nevertheless.
+__device__ __forceinline__ bool for_all(const TreeArgs &a, const TreeRow &r, int j) {
+    return j < r.base && (a.window == 0 || j >= r.base + r.T - a.window);
+}
+
 template <typename C>
 struct TreeShared {
     uint64_t full[C::ring], empty[C::ring];
@@ -555,8 +560,8 @@ __global__ void __launch_bounds__(C::threads, 1)
                     const float cx = inverse(top.x) * (float)(1 << (int)kRaise), cy = inverse(top.y) * (float)(1 << (int)kRaise);
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
-                        float4 x = scale[e];              // infinite V scales become NaN; where not every row attends, it is added at the end
-                        if (masked(a, now.r, t)) x.z = x.z < INFINITY ? x.z : 0.f, x.w = x.w < INFINITY ? x.w : 0.f;
+                        float4 x = scale[e];              // infinite V scales become NaN; of tokens that not every row attends, at the end
+                        if (!for_all(a, now.r, t * T + e * 32 + lane)) x.z = x.z < INFINITY ? x.z : 0.f, x.w = x.w < INFINITY ? x.w : 0.f;
                         float *ks = reinterpret_cast<float *>(sh.k_scales[m]), *vs = reinterpret_cast<float *>(sh.v_scales[m]);
                         const int tok = F8 ? e * 32 + lane : 0;
                         ks[tok] = x.x, vs[tok] = fmaf(x.z, 0.f, x.z) * cx;

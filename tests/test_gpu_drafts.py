@@ -915,6 +915,42 @@ def test_tree_value_scale_that_is_not_finite(cuda_lib, Hq, D, value, where):
             assert torch.equal(out[i], good[i])
 
 
+@pytest.mark.parametrize("D", [256, 128])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("n,window,place", [
+    (20, 0, 3), (20, 0, 11), (500, 0, 491), (500, 0, 448), (500, 0, 447), (500, 0, 492), (500, 0, 499),
+    # the drafts' positions reach 8 deep: places below 492 + 8 - 90 = 410 are not for all of them, those below 403 for none
+    (500, 90, 402), (500, 90, 403), (500, 90, 409), (500, 90, 410), (500, 90, 447), (500, 90, 448)])
+def test_tree_value_scale_that_is_not_finite_in_a_masked_tile(cuda_lib, D, value, n, window, place):
+    """Such a scale in a tile that holds drafts, or the window's edge: of a token that all, some or none of the drafts attend."""
+    Hq, page, T_ = 8, 16, 8
+    q, planes, values, tab, table, off, _ = tree_inputs([n], [T_], Hq, 1, D, page, True, seed=4, spare_rows=0)
+    for parents in ([list(range(-1, 7))], [[-1, 0, 0, 1, 2, 2, -1, 6]]):
+        cfg = qb.make_paged_config(Hq, 1, D, page, window=window)
+        ws = qb.tree_workspace(cfg, T_)
+        good, good_lse = run_tree(cfg, q, planes, tab, [n], off, parents, T_, ws)
+        spoiled = [p.clone() for p in planes]
+        spoiled[3].flatten(0, 1)[int(P.slots_of(table[0], n, page)[place]), 0, -1] = value
+        out, lse = run_tree(cfg, q, spoiled, tab, [n], off, parents, T_, ws)
+        assert torch.equal(lse, good_lse) and status(ws) == (0, 0)
+        for i, places in enumerate(T.attended(n, parents[0], window)):
+            odd = torch.isnan(out[i])
+            assert bool(odd[:, -128:].all()) if place in places else not bool(odd.any()), i
+            assert torch.equal(out[i][~odd], good[i][~odd])
+
+
+@pytest.mark.parametrize("D", [256, 128])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("n,place", [(20, 0), (20, 18), (20, 19), (300, 256), (300, 298), (300, 255)])
+def test_one_token_meets_value_scales_as_the_decode_does(cuda_lib, D, value, n, place):
+    q, planes, values, tab, table, off, parents = tree_inputs([n], [1], 8, 1, D, 16, True, seed=4, spare_rows=0)
+    planes[3].flatten(0, 1)[int(P.slots_of(table[0], n, 16)[place]), 0, 0] = value
+    cfg = qb.make_paged_config(8, 1, D, 16)
+    out, _ = run_tree(cfg, q, planes, tab, [n], off, parents, 1, qb.tree_workspace(cfg, 1))
+    want, _ = run_decode(cfg, q, planes, tab, ints([n]), qb.paged_workspace(cfg))
+    assert torch.equal(torch.isnan(out), torch.isnan(want)) and bool(torch.isnan(out[..., :128]).all())
+
+
 @pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
 @pytest.mark.parametrize("Hq,D,fp8", [(8, 256, True), (8, 128, True), (8, 256, False), (4, 64, False)])
 def test_tree_query_that_is_not_finite_spoils_its_head_alone(cuda_lib, Hq, D, fp8, value):
