@@ -780,7 +780,7 @@ QSA_API qsa_status qsa_paged_decode_weights_fp8kv(const qsa_paged_config *cfg, c
                                                   int32_t B, qsa_bf16 *out, float *lse, float *weights,
                                                   int64_t weights_ld, void *ws, size_t ws_bytes, qsa_stream stream);
 
-/* Workspace of qsa_accept_drafts (max_tokens 0) and qsa_evict_tokens (max_tokens: its weights_ld) for at most n_rows
+/* Workspace of qsa_accept_drafts, qsa_accept_drafts_weights (max_tokens 0) and qsa_evict_tokens (max_tokens: its weights_ld) for at most n_rows
  * rows. Zero it once with qsa_workspace_init. */
 QSA_API size_t qsa_keep_workspace_size(int32_t n_rows, int64_t max_tokens);
 
@@ -802,6 +802,17 @@ QSA_API qsa_status qsa_accept_drafts(int32_t page_size, const int32_t *draft_off
                                      int32_t *seq_len_out, int32_t *ref_out, int32_t *positions, int64_t positions_ld,
                                      const qsa_page_planes *planes, int32_t n_groups, void *ws, size_t ws_bytes,
                                      qsa_stream stream);
+
+/* qsa_accept_drafts for rows that accumulate weights, with drafted tokens among those that were weighed: weights and
+ * positions [n_rows][tokens_ld] move along with the accepted path in place, and become 0 and -1 from each row's new length to
+ * its old one, so that a later token at a dropped one's place starts with nothing. A row that keeps all its tokens keeps
+ * these too. weights fp32, both 4-byte aligned; everything else as in qsa_accept_drafts. */
+QSA_API qsa_status qsa_accept_drafts_weights(int32_t page_size, const int32_t *draft_off, const int32_t *parent, int32_t N,
+                                             const int32_t *accepted, float *weights, int32_t *positions, int64_t tokens_ld,
+                                             const int32_t *table, const int32_t *seq_len, int32_t n_rows, int64_t ld,
+                                             const int32_t *ref, int64_t n_pages, int32_t *table_out, int32_t *seq_len_out,
+                                             int32_t *ref_out, const qsa_page_planes *planes, int32_t n_groups, void *ws,
+                                             size_t ws_bytes, qsa_stream stream);
 
 /* Cut rows down to their budget by accumulated weight. Row r of n = seq_len[r] tokens keeps all of them if n <=
  * budget[r] or budget[r] < 0. Otherwise it always keeps the tokens at positions below `first`, those at the last `recent`

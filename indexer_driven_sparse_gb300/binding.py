@@ -141,6 +141,8 @@ _SIGNATURES = {
     "qsa_keep_workspace_size": (_SZ, [_I32, _I64]),
     "qsa_accept_drafts": (_I32, [_I32, _P, _P, _I32, _P, _P, _P, _I32, _I64, _P, _I64, _P, _P, _P, _P, _I64, _PLANES, _I32,
                                  _P, _SZ, _P]),
+    "qsa_accept_drafts_weights": (_I32, [_I32, _P, _P, _I32, _P, _P, _P, _I64, _P, _P, _I32, _I64, _P, _I64, _P, _P, _P, _PLANES,
+                                         _I32, _P, _SZ, _P]),
     "qsa_evict_tokens": (_I32, [_I32, _P, _I32, _I32, _P, _P, _I64, _P, _P, _I32, _I64, _P, _I64, _P, _P, _P, _P, _P,
                                 _PLANES, _I32, _P, _SZ, _P]),
     "qsa_copy_pages": (_I32, [_P, _P, _I32, _PLANES, _I64, _PLANES, _I64, _I32, _P, _SZ, _P]),
@@ -708,6 +710,17 @@ def qsa_accept_drafts(page_size, draft_off, parent, accepted, table, seq_len, re
                                               None if stream is None else _stream(stream))
     if st:
         _check(st, "qsa_accept_drafts")
+
+
+def qsa_accept_drafts_weights(page_size, draft_off, parent, accepted, weights, positions, table, seq_len, ref, table_out,
+                              seq_len_out, ref_out, planes, ws, stream=None):
+    """qsa_accept_drafts for rows that accumulate weights: weights and positions [rows, places] move along, and are cleared
+    where tokens are dropped."""
+    st = (_NATIVE or _native()).accept_drafts_weights(page_size, draft_off, parent, accepted, weights, positions, table, seq_len,
+                                                      ref, table_out, seq_len_out, ref_out, planes, ws,
+                                                      None if stream is None else _stream(stream))
+    if st:
+        _check(st, "qsa_accept_drafts_weights")
 
 
 def qsa_evict_tokens(page_size, budget, first, recent, weights, positions, table, seq_len, ref, weights_out, positions_out,

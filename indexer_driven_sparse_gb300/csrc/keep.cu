@@ -1,5 +1,5 @@
-// Which cached tokens stay: qsa_accept_drafts (the accepted path of a tree of drafted tokens) and qsa_evict_tokens (the
-// heaviest tokens by accumulated weight). Both cut rows to a new length, move some of the kept tokens into earlier places in
+// Which cached tokens stay: qsa_accept_drafts[_weights] (the accepted path of a tree of drafted tokens) and qsa_evict_tokens
+// (the heaviest tokens by accumulated weight). Both cut rows to a new length, move some of the kept tokens into earlier places in
 // every plane, and give back the pages that empty.
 #include "paged.cuh"
 
@@ -179,14 +179,22 @@ __global__ void __launch_bounds__(kKeepThreads) accept_kernel(KeepArgs a, Accept
         if (n < 0) {
             for (int64_t j = tid; j < a.ld; j += kKeepThreads) a.table_out[r * a.ld + j] = row[j];
         } else if (d.positions && tid < 32) {        // in batches of a warp, read before they are written
+            int32_t *pos = d.positions + r * d.positions_ld;
+            float *w = d.weights ? d.weights + r * d.positions_ld : nullptr;
             for (int k0 = 0; k0 < n; k0 += 32) {
                 const int k = k0 + tid, src = k < n ? base + node[n - 1 - k] : 0;
                 const bool some = k < n && src < d.positions_ld;
-                const int v = some ? d.positions[r * d.positions_ld + src] : 0;
+                const int v = some ? pos[src] : 0;
+                const float x = some && w ? w[src] : 0.f;
                 __syncwarp();
-                if (some) d.positions[r * d.positions_ld + base + k] = v;
+                if (some) {
+                    pos[base + k] = v;
+                    if (w) w[base + k] = x;
+                }
                 __syncwarp();
             }
+            if (w)                                   // a later token at a dropped one's place starts with nothing
+                for (int64_t j = new_len + tid; j < min((int64_t)len, d.positions_ld); j += 32) pos[j] = -1, w[j] = 0.f;
         }
     }
     if (n < 0) return;

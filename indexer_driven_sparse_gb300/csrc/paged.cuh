@@ -163,6 +163,7 @@ struct AcceptArgs {
     const int32_t *draft_off, *parent, *accepted;
     int32_t N;
     int32_t *positions;                 // or nullptr
+    float *weights;                     // or nullptr; beside positions, of the same shape: both are cleared behind a row's new length
     int64_t positions_ld;
 };
 struct EvictArgs {

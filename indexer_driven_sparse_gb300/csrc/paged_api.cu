@@ -395,6 +395,22 @@ qsa_status keep_args(const char *call, int32_t page_size, int32_t n_rows, int64_
     return QSA_OK;
 }
 
+// qsa_accept_drafts[_weights]; the caller has set a's and d's arrays.
+qsa_status accept_drafts(const char *call, int32_t page_size, KeepArgs a, const AcceptArgs &d, int32_t n_rows, int64_t ld,
+                         int64_t n_pages, const qsa_page_planes *planes, int32_t n_groups, void *ws, size_t ws_bytes,
+                         qsa_stream stream) {
+    PlaneGroups groups;
+    QSA_TRY(keep_args(call, page_size, n_rows, ld, n_pages, 0, planes, n_groups, ws, ws_bytes, &a, &groups));
+    QSA_NEED(call, d.N >= 0 && d.positions_ld >= 0, "negative size");
+    QSA_NEED(call, n_rows == 0 || (d.draft_off && d.accepted && (d.parent || d.N == 0)), "NULL tensor pointer");
+    QSA_NEED(call, aligned(d.draft_off, 4) && aligned(d.parent, 4) && aligned(d.accepted, 4) && aligned(d.positions, 4) &&
+                 aligned(d.weights, 4),
+             "the arrays must be 4-byte aligned");
+    if (n_rows == 0 && n_pages == 0) return host_ok();
+    QSA_TRY(check_planes_memory(call, groups));
+    return launched(launch_accept_drafts(a, d, groups, static_cast<cudaStream_t>(stream)), call);
+}
+
 }  // namespace
 
 extern "C" {
@@ -636,22 +652,30 @@ QSA_API qsa_status qsa_accept_drafts(int32_t page_size, const int32_t *draft_off
                                      int32_t *seq_len_out, int32_t *ref_out, int32_t *positions, int64_t positions_ld,
                                      const qsa_page_planes *planes, int32_t n_groups, void *ws, size_t ws_bytes,
                                      qsa_stream stream) {
-    const char *call = "qsa_accept_drafts";
-    KeepArgs a{};
-    PlaneGroups groups;
-    a.table = table, a.seq_len = seq_len, a.ref = ref;
-    a.table_out = table_out, a.seq_len_out = seq_len_out, a.ref_out = ref_out;
-    QSA_TRY(keep_args(call, page_size, n_rows, ld, n_pages, 0, planes, n_groups, ws, ws_bytes, &a, &groups));
-    QSA_NEED(call, N >= 0 && positions_ld >= 0, "negative size");
-    QSA_NEED(call, n_rows == 0 || (draft_off && accepted && (parent || N == 0)), "NULL tensor pointer");
-    QSA_NEED(call, aligned(draft_off, 4) && aligned(parent, 4) && aligned(accepted, 4) && aligned(positions, 4),
-             "the int32 arrays must be 4-byte aligned");
-    if (n_rows == 0 && n_pages == 0) return host_ok();
-    QSA_TRY(check_planes_memory(call, groups));
     AcceptArgs d{};
     d.draft_off = draft_off, d.parent = parent, d.accepted = accepted, d.N = N;
     d.positions = positions, d.positions_ld = positions_ld;
-    return launched(launch_accept_drafts(a, d, groups, static_cast<cudaStream_t>(stream)), call);
+    KeepArgs a{};
+    a.table = table, a.seq_len = seq_len, a.ref = ref;
+    a.table_out = table_out, a.seq_len_out = seq_len_out, a.ref_out = ref_out;
+    return accept_drafts("qsa_accept_drafts", page_size, a, d, n_rows, ld, n_pages, planes, n_groups, ws, ws_bytes, stream);
+}
+
+QSA_API qsa_status qsa_accept_drafts_weights(int32_t page_size, const int32_t *draft_off, const int32_t *parent, int32_t N,
+                                             const int32_t *accepted, float *weights, int32_t *positions, int64_t tokens_ld,
+                                             const int32_t *table, const int32_t *seq_len, int32_t n_rows, int64_t ld,
+                                             const int32_t *ref, int64_t n_pages, int32_t *table_out, int32_t *seq_len_out,
+                                             int32_t *ref_out, const qsa_page_planes *planes, int32_t n_groups, void *ws,
+                                             size_t ws_bytes, qsa_stream stream) {
+    const char *call = "qsa_accept_drafts_weights";
+    QSA_NEED(call, n_rows <= 0 || tokens_ld == 0 || (weights && positions), "weights and positions must be non-NULL");
+    AcceptArgs d{};
+    d.draft_off = draft_off, d.parent = parent, d.accepted = accepted, d.N = N;
+    d.positions = positions, d.positions_ld = tokens_ld, d.weights = weights;
+    KeepArgs a{};
+    a.table = table, a.seq_len = seq_len, a.ref = ref;
+    a.table_out = table_out, a.seq_len_out = seq_len_out, a.ref_out = ref_out;
+    return accept_drafts(call, page_size, a, d, n_rows, ld, n_pages, planes, n_groups, ws, ws_bytes, stream);
 }
 
 QSA_API qsa_status qsa_evict_tokens(int32_t page_size, const int32_t *budget, int32_t first, int32_t recent,

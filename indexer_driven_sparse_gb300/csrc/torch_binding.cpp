@@ -456,6 +456,25 @@ qsa_status accept_drafts(PyObject *const *a) {
                              c.stream(a[13]));
 }
 
+// accept_drafts_weights(page_size, draft_off, parent, accepted, weights, positions, table, seq_len, ref, table_out,
+// seq_len_out, ref_out, planes, ws, stream)
+qsa_status accept_drafts_weights(PyObject *const *a) {
+    Call c;
+    const Kept k = kept(c, a[6], a[7], a[8], a[9], a[10], a[11]);
+    const int32_t n = length(tensor(a[2], "parent"), "parent");
+    const auto *off = c.at<int32_t>(a[1], "draft_off", at::kInt, {static_cast<int64_t>(k.rows) + 1});
+    const auto *parent = c.at<int32_t>(a[2], "parent", at::kInt, {n});
+    const auto *accepted = c.at<int32_t>(a[3], "accepted", at::kInt, {k.rows});
+    const int64_t tokens = matrix(a[5], "positions").size(1);
+    auto *weights = c.at<float>(a[4], "weights", at::kFloat, {k.rows, tokens});
+    auto *positions = c.at<int32_t>(a[5], "positions", at::kInt, {k.rows, tokens});
+    const Groups g = groups(c, a[12], k.n_pages);
+    const Workspace ws = workspace(c, a[13]);
+    return qsa_accept_drafts_weights(whole(a[0]), off, parent, n, accepted, weights, positions, tokens, k.table, k.seq_len, k.rows,
+                                     k.ld, k.ref, k.n_pages, k.table_out, k.len_out, k.ref_out, g.g, g.n, ws.p, ws.bytes,
+                                     c.stream(a[14]));
+}
+
 // evict_tokens(page_size, budget, first, recent, weights, positions, table, seq_len, ref, weights_out, positions_out,
 // table_out, seq_len_out, ref_out, planes, ws, stream)
 qsa_status evict_tokens(PyObject *const *a) {
@@ -509,6 +528,7 @@ PyMethodDef methods[] = {
     QSA_METHOD("compact_pages", 9, compact_pages),
     QSA_METHOD("copy_pages", 6, copy_pages),
     QSA_METHOD("accept_drafts", 14, accept_drafts),
+    QSA_METHOD("accept_drafts_weights", 15, accept_drafts_weights),
     QSA_METHOD("evict_tokens", 17, evict_tokens),
     {nullptr, nullptr, 0, nullptr},
 };

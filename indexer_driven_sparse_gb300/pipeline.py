@@ -401,12 +401,16 @@ class PagedCache:
                                self.tree_ws, stream)
 
     def accept(self, draft_off, parent, accepted, stream=None):
-        """Of each row's drafted tokens keep accepted[r] (-1: none) and its ancestors (qsa_accept_drafts)."""
+        """Of each row's drafted tokens keep accepted[r] (-1: none) and its ancestors (qsa_accept_drafts); in an evictable
+        cache their weights and positions with them."""
         self._made_for(self.max_draft, "max_draft")
         new, new_ref = 1 - self._now, 1 - self._ref_now
-        qb.qsa_accept_drafts(self.cfg.page_size, draft_off, parent, accepted, self.table, self.seq_len, self.ref,
-                             self._tables[new], self._lens[new], self._refs[new_ref], self.planes, self.keep_ws,
-                             self.positions if self.evictable else None, stream)
+        pool = (self.table, self.seq_len, self.ref, self._tables[new], self._lens[new], self._refs[new_ref], self.planes, self.keep_ws)
+        if self.evictable:
+            qb.qsa_accept_drafts_weights(self.cfg.page_size, draft_off, parent, accepted, self.weights, self.positions, *pool,
+                                         stream)
+        else:
+            qb.qsa_accept_drafts(self.cfg.page_size, draft_off, parent, accepted, *pool, None, stream)
         self._now, self._ref_now = new, new_ref
 
     def evict(self, budget, first: int, recent: int, stream=None):

@@ -149,6 +149,19 @@ def test_keep_refusals(lib):
                                 FAKE, lib.qsa_keep_workspace_size(3, 999), None) == SMALL
 
 
+def test_accept_weights_refusals(lib):
+    def call(off=FAKE, parent=FAKE, n=5, accepted=FAKE, weights=FAKE, positions=FAKE, t_ld=16, table=FAKE, rows=3, t_out=FAKE + 256,
+             ws=FAKE, bytes=1 << 30):
+        return lib.qsa_accept_drafts_weights(4, off, parent, n, accepted, weights, positions, t_ld, table, FAKE, rows, 4, FAKE,
+                                             9 if rows else 0, t_out, FAKE + 256, FAKE + 256, None, 0, ws, bytes, None)
+
+    assert call(rows=0) == call(rows=0, weights=0, positions=0) == qb.QSA_OK
+    for kw in (dict(weights=0), dict(positions=0), dict(weights=FAKE + 2), dict(positions=FAKE + 1), dict(t_ld=-1), dict(off=0),
+               dict(accepted=0), dict(parent=0), dict(n=-1), dict(rows=-1), dict(table=0), dict(t_out=FAKE), dict(ws=0)):
+        assert call(**kw) == BAD, kw
+    assert call(bytes=256) == SMALL
+
+
 def test_binding_refuses_wrong_tensors(lib):
     import torch
     bf16, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)

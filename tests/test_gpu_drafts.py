@@ -486,6 +486,50 @@ def test_accept(cuda_lib, lens, counts, page):
     assert np.array_equal(r_out.cpu().numpy(), want_r)
 
 
+@pytest.mark.parametrize("lens,counts", ACCEPT_ROWS)
+@pytest.mark.parametrize("cut", [0, 5])
+def test_accept_moves_weights_along(cuda_lib, lens, counts, cut):
+    """Weights and positions follow the accepted path and are cleared where tokens are dropped, in arrays of all places and in
+    shorter ones; the rest of the call is qsa_accept_drafts."""
+    page, rng = 4, np.random.default_rng(len(lens) + cut)
+    table, ref = private_pool(lens, page, 1)
+    off = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    parents = [random_parents(rng, c, 0.5) for c in counts]
+    last = [int(rng.integers(-1, c)) if c else -1 for c in counts]
+    held = list(lens)
+    if len(lens) > 3:                                     # a row out of range keeps what it has
+        last[4] = counts[4]
+    places = max(1, max(lens) - cut)
+    positions = rng.integers(0, 1000, (len(lens), places)).astype(np.int32)
+    weights = rng.random((len(lens), places)).astype(np.float32)
+    want_p, want_w, moves, new_len = positions.copy(), weights.copy(), {}, []
+    for r, (n, p, a) in enumerate(zip(lens, parents, last)):
+        new, moves[r] = T.accept(n, p, a) if a < len(p) else (n, [])
+        new_len.append(new)
+        for to, at in moves[r]:
+            if at < places:
+                want_p[r, to], want_w[r, to] = positions[r, at], weights[r, at]
+        want_p[r, new:n], want_w[r, new:n] = -1, 0
+    planes = token_planes(len(ref), page, 1)
+    want = [moved(p, table, moves, page) for p in planes]
+    t_out, l_out, r_out = filled(*table.shape), filled(len(lens)), filled(len(ref))
+    ws = qb.keep_workspace(len(lens))
+    pos, w = ints(positions.tolist()), torch.from_numpy(weights).to(DEV)
+    qb.qsa_accept_drafts_weights(page, ints(off), ints([p for row in parents for p in row] + [0]), ints(last), w, pos,
+                                 ints(table.tolist()), ints(held), ints(ref.tolist()), t_out, l_out, r_out, planes, ws)
+    assert status(ws) == ((qb.QSA_ERR_DEVICE_BOUNDS, 4) if len(lens) > 3 else (0, 0))
+    fine = np.array([r for r in range(len(lens)) if last[r] < counts[r] or last[r] < 0])
+    want_t, want_r = T.release(table[fine], ref, np.array(lens)[fine], np.array(new_len)[fine], page)
+    assert l_out.tolist() == new_len and np.array_equal(t_out.cpu().numpy()[fine], want_t)
+    assert np.array_equal(r_out.cpu().numpy(), want_r)
+    for r in range(len(lens)):                            # what of a moved token lies behind the arrays is nothing to compare
+        sure = [j for j in range(places) if not any(to == j and at >= places for to, at in moves[r])]
+        assert np.array_equal(pos[r].cpu().numpy()[sure], want_p[r, sure]), r
+        assert np.array_equal(w[r].cpu().numpy()[sure], want_w[r, sure]), r
+    for got, x in zip(planes, want):
+        assert torch.equal(got, x)
+
+
 @pytest.mark.parametrize("what", ["length", "long", "drafts", "offset", "parent", "accepted"])
 def test_accept_leaves_rows_out_of_range_as_they_are(cuda_lib, what):
     page, lens, off, parents, last = 4, [10, 12, 9], [0, 4, 8, 12], [[-1, 0, 1, 2]] * 3, [1, 3, 2]
@@ -773,6 +817,63 @@ def test_a_decode_loop_under_a_budget(cuda_lib, fp8):
             rows, weights = [list(rows[p]) for p in parent], [weights[p].copy() for p in parent]
             where = [where[p] for p in parent]
             cache.compact()
+    assert cache.status() == ((0, 0), (0, 0)) and cache.more_status() == ((0, 0),) * 3
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_drafting_under_a_budget(cuda_lib, fp8):
+    """Drafts that are weighed while they are in their rows, then accepted or not, then cut by weight: what each token has
+    received stays with it, and a token at a dropped one's place starts with nothing."""
+    Hq, Hkv, D, page, S = 8, 2, 128, 4, 3
+    rope = qb.rope_table(D, base=1e5)
+    cache = PagedCache(1, 60, page, S, 20, Hq, Hkv, D, fp8=fp8, evictable=True, max_draft=8)
+    n0 = 26
+    x = randn((S * n0, 2 * Hkv, D), 1)
+    cache.fork(ints([-1] * S), ints([n0] * S))
+    cache.append(0, rope, None, x[:, :Hkv], x[:, Hkv:], ints(list(range(n0)) * S), ints(sum(([r] * n0 for r in range(S)), [])))
+    rows, weights, newest = [list(range(n0)) for _ in range(S)], [np.zeros(n0) for _ in range(S)], [n0] * S
+    parents, lasts = [-1, 0, 0, 2, 1, 3], [5, -1, 3]
+    off, depth = [0, 6, 12, 18], [len(line) - 1 for line in T.lines(parents)]
+    for step in range(6):
+        cache.extend(ints([6] * S))
+        y = randn((S * 6, Hq + 2 * Hkv, D), 20 + step)
+        where = [newest[r] + d for r in range(S) for d in depth]
+        place = [len(rows[r]) + i for r in range(S) for i in range(6)]
+        q = torch.empty(S * 6, Hq, D, dtype=torch.bfloat16, device=DEV)
+        cache.append(0, rope, y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], ints(where), ints(sum(([r] * 6 for r in range(S)), [])),
+                     q, place=ints(place))
+        before = cache.weights.cpu().numpy()
+        for r in range(S):
+            rows[r] += where[6 * r:6 * r + 6]
+            assert not before[r, len(weights[r]):].any()
+            weights[r] = np.append(weights[r], np.zeros(6))
+        out = torch.empty(S, Hq, D, dtype=torch.bfloat16, device=DEV)
+        cache.attend(0, q[5::6], out, weigh=True)         # the newest token's queries, over drafts and all
+        held = cache.weights.cpu().numpy()
+        for r in range(S):
+            weights[r] = held[r, :len(rows[r])].copy()
+            assert (weights[r][-6:] > 0).all()
+        cache.accept(ints(off), ints(parents * S), ints(lasts))
+        for r in range(S):
+            n, moves = T.accept(len(rows[r]), parents, lasts[r])
+            newest[r] += n - (len(rows[r]) - 6)
+            old_p, old_w = list(rows[r]), weights[r].copy()
+            for to, at in moves:
+                rows[r][to], weights[r][to] = old_p[at], old_w[at]
+            rows[r], weights[r] = rows[r][:n], weights[r][:n]
+        check = cache.weights.cpu().numpy(), cache.positions.cpu().numpy()
+        for r in range(S):
+            n = len(rows[r])
+            assert np.array_equal(check[0][r, :n], weights[r].astype(np.float32)) and not check[0][r, n:].any()
+            assert check[1][r, :n].tolist() == rows[r] and (check[1][r, n:] == -1).all()
+        if step % 2:
+            cache.evict(ints([24] * S), 2, 4)
+            for r in range(S):
+                keep, moves = T.evict(weights[r], rows[r], [False] * len(rows[r]), 24, 2, 4)
+                for to, at in moves:
+                    rows[r][to], weights[r][to] = rows[r][at], weights[r][at]
+                rows[r], weights[r] = rows[r][:keep], weights[r][:keep]
+            assert [cache.positions[r, :len(rows[r])].tolist() for r in range(S)] == rows
     assert cache.status() == ((0, 0), (0, 0)) and cache.more_status() == ((0, 0),) * 3
 
 
