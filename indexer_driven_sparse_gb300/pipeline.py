@@ -257,7 +257,9 @@ class PagedCache:
     and positions and ``attend_tree``; ``accept`` keeps the accepted path. An evictable cache accumulates in ``weights[r, j]``
     what token j of row r receives (``attend`` with weigh=True) and holds its position in ``positions[r, j]`` (``append`` of
     layer 0); ``evict`` cuts rows to a budget. Its window must be 0: places are no positions any more. A row of it that ran
-    out of pages is started again by ``fork``, which clears what it had received."""
+    out of pages is started again by ``fork``, which clears what it had received. Weighing takes 4 n_q_heads bytes of
+    workspace for each token that the rows attend together: of every row's room, unless weighed_tokens says how many that is
+    at most (what lies behind it in a call receives nothing, which ``more_status`` tells)."""
 
     def __init__(self, n_layers: int, n_pages: int, page_size: int, n_rows: int, max_pages: int, n_q_heads: int,
                  n_kv_heads: int, head_dim: int = 256, fp8: bool = False, softmax_scale: float = 0.0, window: int = 0,
@@ -291,8 +293,9 @@ class PagedCache:
         if max_draft or evictable:
             self.keep_ws = qb.keep_workspace(n_rows, places if evictable else 0, device)
         if evictable:
-            # weighed_tokens: the most tokens that one attend weighs (None: the pool's, each by one row)
-            self.weights_ws = qb.weights_workspace(self.cfg, n_rows, weighed_tokens or n_pages * page_size, device)
+            if weighed_tokens is None:                # rows may share pages: each may name as many as it has room for
+                weighed_tokens = n_rows * min(max_pages, n_pages) * page_size
+            self.weights_ws = qb.weights_workspace(self.cfg, n_rows, weighed_tokens, device)
             self._weights = [torch.zeros(n_rows, places, dtype=torch.float32, device=device) for _ in range(2)]
             self._positions = [torch.full((n_rows, places), -1, **i32) for _ in range(2)]
             self._weights_now = 0

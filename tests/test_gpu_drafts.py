@@ -877,6 +877,28 @@ def test_drafting_under_a_budget(cuda_lib, fp8):
     assert cache.status() == ((0, 0), (0, 0)) and cache.more_status() == ((0, 0),) * 3
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_beams_over_a_shared_prompt_are_all_weighed(cuda_lib, fp8):
+    """Rows that share a prompt attend more tokens together than the pool holds: each step adds Hq to every row's weights (each
+    weight off by less than 2^-17, n sums of it in fp32)."""
+    Hq, Hkv, D, page, S, n = 8, 2, 128, 16, 12, 800
+    cache = PagedCache(1, n // page + S, page, S, n // page + 2, Hq, Hkv, D, fp8=fp8, evictable=True)
+    rope = qb.rope_table(D)
+    x = randn((n, 2 * Hkv, D), 1)
+    cache.fork(ints([-1] * S), ints([n] + [0] * (S - 1)))
+    cache.append(0, rope, None, x[:, :Hkv], x[:, Hkv:], ints(list(range(n))), ints([0] * n))
+    cache.fork(ints([0] * S), ints([0] * S))
+    for step in range(2):
+        cache.extend()
+        y = randn((S, Hq + 2 * Hkv, D), 5 + step)
+        q = torch.empty(S, Hq, D, dtype=torch.bfloat16, device=DEV)
+        cache.append(0, rope, y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], ints([n + step] * S), None, q)
+        cache.attend(0, q, torch.empty_like(q), weigh=True)
+        assert cache.status() == ((0, 0), (0, 0)) and cache.more_status() == ((0, 0), (0, 0))
+        assert np.allclose(f64(cache.weights).sum(1), Hq * (step + 1), rtol=2.0 ** -17 + 2 * 2.0 ** -24, atol=0)
+        assert bool((cache.weights[:, :n + step + 1] > 0).all()) and not bool(cache.weights[:, n + step + 1:].any())
+
+
 def test_an_evictable_cache_keeps_its_own_records(cuda_lib):
     """Tokens appended by position alone have their positions recorded; rows that a fork empties have received nothing."""
     Hq, Hkv, D, page, S = 4, 1, 64, 4, 2
