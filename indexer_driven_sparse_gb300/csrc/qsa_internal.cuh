@@ -24,12 +24,12 @@ struct WsHeader {
     int32_t status;      // first device-side error (qsa_status), 0 = none
     int32_t detail;      // kernel-specific detail (row, index)
     int32_t where;       // which kernel recorded it
-    int32_t debug;       // test knob: kDebugStallBarrier makes the first row barrier never complete
+    int32_t debug;       // test knob: kDebugStallBarrier makes the first row barrier (qsa_tree_decode: the fourth tile) never come
     uint32_t sem[60];    // self-resetting counters (last-CTA-done, grid barriers)
 };
 static_assert(sizeof(WsHeader) == 256, "status block must be 256 bytes");
 constexpr size_t kWsHeaderBytes = 256;
-constexpr int32_t kDebugStallBarrier = 0x5741171;   // written only by the device-timeout test
+constexpr int32_t kDebugStallBarrier = 0x5741171;   // written only by the device-timeout tests
 constexpr int32_t kDebugTrace = 0x7ACE;             // record per-CTA phase timestamps (qsa_decode_step)
 constexpr int kTraceSlots = 16;
 constexpr uint64_t kWaitLimitNs = 250ull * 1000 * 1000;   // every device-side wait gives up after 250 ms

@@ -278,11 +278,20 @@ __device__ __forceinline__ bool drop_nan_codes(uint32_t &w) {
     return nan != 0;
 }
 
-// Wait for phase `parity` of an mbarrier, a bounded number of times: false, and recorded, if in vain. Each try may suspend
-// the thread for kHintNs. Out of line: with the waits and the walks inlined the kernel had 256 KB of instructions, and its
-// roles, each on a part of its own, waited for them more than for anything else.
+// What a CTA's waits share: whether one of them has given up, how many tiles the index warp has named, and where to record. Not
+// handed to each wait: two more arguments cost registers.
+struct TreeWaits {
+    uint32_t gave_up, tiles;
+    WsHeader *hdr;
+};
+__shared__ volatile TreeWaits tree_waits;
+
+// Wait for phase `parity` of an mbarrier: false if the CTA has given up, or if kWaitLimitNs pass without a further tile; that is
+// recorded, and ends the CTA's other waits. (A wait for a segment's end may last longer while its tiles go by.) Each try may
+// suspend the thread for kHintNs. Out of line: with the waits and the walks inlined the kernel had 256 KB of
+// instructions, and its roles, each on a part of its own, waited for them more than for anything else.
 constexpr uint32_t kHintNs = 1000000;
-constexpr int kTries = 1 << 20;
+constexpr int kTries = 8;                        // between looks at the clock, which takes as long as many a wait
 __device__ __forceinline__ bool try_turn(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
@@ -294,15 +303,43 @@ __device__ __forceinline__ bool try_turn(uint32_t bar, uint32_t parity) {
         : "memory");
     return done != 0;
 }
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, WsHeader *hdr) {
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
+    uint64_t since = 0;
+    uint32_t seen = 0;
 #pragma unroll 1
-    for (int i = 0; i < kTries; ++i)
-        if (try_turn(bar, parity)) return true;
-    record_error(hdr, QSA_ERR_DEVICE_TIMEOUT, kWhereTree, blockIdx.x);
-    return false;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < kTries; ++i)
+            if (try_turn(bar, parity)) return true;
+        if (tree_waits.gave_up) return false;
+        const uint32_t now = tree_waits.tiles;
+        if (since == 0 || now != seen) {
+            seen = now, since = globaltimer_ns();
+        } else if (globaltimer_ns() - since > kWaitLimitNs) {
+            tree_waits.gave_up = 1;
+            record_error(tree_waits.hdr, QSA_ERR_DEVICE_TIMEOUT, kWhereTree, blockIdx.x);
+            return false;
+        }
+    }
 }
-__device__ __forceinline__ bool wait_turn(uint32_t bar, uint32_t parity, WsHeader *hdr) {
-    return try_turn(bar, parity) || wait_long(bar, parity, hdr);
+__device__ __forceinline__ bool wait_turn(uint32_t bar, uint32_t parity) {
+    return try_turn(bar, parity) || wait_long(bar, parity);
+}
+// Wait for what is on its way already, a copy or a product, before shared or tensor memory is given up: whether or not the CTA has
+// given up, and for kWaitLimitNs at most.
+__device__ __noinline__ void wait_landed(uint32_t bar, uint32_t parity) {
+    if (!mbar_wait_bounded(bar, parity, kWaitLimitNs)) record_error(tree_waits.hdr, QSA_ERR_DEVICE_TIMEOUT, kWhereTree, blockIdx.x);
+}
+// A barrier of `threads` threads that also tells whether any of them came with `bad`. Warps that share a barrier leave together:
+// one that left alone after a wait in vain would keep the others there for good.
+__device__ __forceinline__ bool meet_any(int barrier, int threads, bool bad) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.aligned.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(bad ? 1u : 0u), "r"(barrier), "r"(threads)
+        : "memory");
+    return any != 0;
 }
 
 // Values that are not finite, of tokens that this row attends but not every row: added to its result (whole) or its partial.
@@ -378,6 +415,7 @@ __global__ void __launch_bounds__(C::threads, 1)
             mbar_init(smem_u32(&sh.nodes_free), C::softmax / 32);
             mbar_init(smem_u32(&sh.flags_full), C::q_threads);
             mbar_init(smem_u32(&sh.o_free), C::softmax / 32);
+            tree_waits.gave_up = 0, tree_waits.tiles = 0, tree_waits.hdr = a.hdr;
         }
         fence_mbar_init();
         if (tiled && tid == 160) {
@@ -469,8 +507,8 @@ __global__ void __launch_bounds__(C::threads, 1)
     }
     const uint32_t tmem = sh.tmem;
 
-    // A role that waits in vain ends; the roles that depend on it then do the same.
-    auto wait = [&](uint64_t *bar, uint32_t phase) -> bool { return wait_turn(smem_u32(bar), phase & 1u, a.hdr); };
+    // A role that waits in vain ends, and so do all others at their next wait.
+    auto wait = [&](uint64_t *bar, uint32_t phase) -> bool { return wait_turn(smem_u32(bar), phase & 1u); };
     auto wait_warp = [&](uint64_t *bar, uint32_t phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
 
     Seg g{};
@@ -534,7 +572,9 @@ __global__ void __launch_bounds__(C::threads, 1)
                     if (more) enter(), fetch(g.ta);
                 }
                 const int m = done % C::metas;
-                if (done >= C::metas && !wait_warp(&sh.meta_empty[m], done / C::metas - 1)) {
+                // the header's test knob: nothing comes after the third tile, and what waits for it waits in vain
+                if ((done == 3 && a.hdr->debug == kDebugStallBarrier) ||
+                    (done >= C::metas && !wait_warp(&sh.meta_empty[m], done / C::metas - 1))) {
                     ok = false;
                     break;
                 }
@@ -570,7 +610,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                     if (lane == 0) sh.top[m] = top;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.meta_full[m]));
+                if (lane == 0) mbar_arrive(smem_u32(&sh.meta_full[m])), tree_waits.tiles = done + 1;
             }
         }
     } else if (warp >= C::load_warp) {
@@ -642,12 +682,12 @@ __global__ void __launch_bounds__(C::threads, 1)
         if (!F8 || warp == C::load_warp) {
 #pragma unroll 1
             while (ok && more) ok = ask();
-            // no load may still be writing shared memory when the CTA ends (bounded waits; they are over unless a role gave up)
+            // no load may still be writing shared memory when the CTA ends
             for (int x = 0; x < (F8 ? 2 : 1); ++x) {
                 const int slots = F8 ? (x ? C::v_ring : C::k_ring) : RING;
                 for (int q = max(0, asked[x] - slots); q < asked[x]; ++q)
-                    wait_turn(smem_u32(F8 ? (x ? &sh.v_full[F8 ? q % slots : 0] : &sh.k_full[F8 ? q % slots : 0]) : &sh.full[F8 ? 0 : q % slots]),
-                              (uint32_t)(q / slots) & 1u, a.hdr);
+                    wait_landed(smem_u32(F8 ? (x ? &sh.v_full[F8 ? q % slots : 0] : &sh.k_full[F8 ? q % slots : 0]) : &sh.full[F8 ? 0 : q % slots]),
+                                (uint32_t)(q / slots) & 1u);
             }
         } else if constexpr (F8) {
             // Without TMA the codes of a turn are asked for `ahead` turns before its V, if it is one, is converted: at most as many as
@@ -725,11 +765,12 @@ __global__ void __launch_bounds__(C::threads, 1)
         // ================================================================ queries, ancestors, clean V rows
         const int qt = tid - C::q_warp * 32;
         Walk w = walk;
-        bool ok = true;
+        bool bad = false;                                 // a wait in vain: up to the next barrier, where all of these warps leave
         int seg = 0, cleaned = 0;
-        while (ok && w.next(a, m_tile, g)) {
+        while (w.next(a, m_tile, g)) {
             const int n = g.tb - g.ta, rows = g.r.T * a.G - m_tile * kRows;     // this CTA's rows (maybe more than 128)
-            if (seg > 0 && !wait_warp(&sh.q_free, seg - 1)) break;
+            bad = bad || (seg > 0 && !wait_warp(&sh.q_free, seg - 1));
+            if (meet_any(2, C::q_threads, bad)) break;
             auto row_at = [&](int r) -> const uint16_t * {
                 const int node = (m_tile * kRows + r) / a.G, h = (m_tile * kRows + r) % a.G;
                 return a.q + (int64_t)(g.r.off + node) * a.q_ld + (kvh * a.G + h) * D;
@@ -804,7 +845,7 @@ __global__ void __launch_bounds__(C::threads, 1)
             }
             mbar_arrive(smem_u32(&sh.q_full));
             // ---- the drafted tokens' ancestors, once the last segment's are no longer needed
-            if (seg > 0 && !wait_warp(&sh.nodes_free, seg - 1)) break;
+            if (meet_any(2, C::q_threads, seg > 0 && !wait_warp(&sh.nodes_free, seg - 1))) break;
             for (int i = qt; i < g.r.T; i += C::q_threads) {
                 uint32_t kin[4] = {0u, 0u, 0u, 0u};
                 int depth = 0;
@@ -834,15 +875,13 @@ __global__ void __launch_bounds__(C::threads, 1)
                 const int x = j >= g.r.base ? j - g.r.base : j - g.r.lo, set = j >= g.r.base ? 0 : 1;
                 if (x < QSA_MAX_DRAFT) atomicOr(&sh.odd[set][x >> 5], 1u << (x & 31));
             };
-            for (int c = 0; c < n && ok; ++c) {
+            for (int c = 0; c < n; ++c) {
                 const int t = g.ta + c;
                 if (!masked(a, g.r, t)) continue;
                 if (!F8) {
                     // the output warp says when the rows are in: it meets every turn of its slots, and a wait tells only two from each other
-                    if (!wait_warp(&sh.to_clean, cleaned)) {
-                        ok = false;
-                        break;
-                    }
+                    bad = !wait_warp(&sh.to_clean, cleaned);
+                    if (bad) break;
                     const int at = (2 * g.i0 + v_turn(c, n)) % RING;
                     for (int i = qt; i < T * (D / 8); i += C::q_threads) {
                         const int tok = i / (D / 8), gr = i % (D / 8), j = t * T + tok;
@@ -876,8 +915,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                     }
                 }
             }
-            if (!ok) break;
-            mbar_arrive(smem_u32(&sh.flags_full));
+            if (!bad) mbar_arrive(smem_u32(&sh.flags_full));
             ++seg;
         }
     } else if (warp == C::s_warp) {
@@ -930,7 +968,7 @@ __global__ void __launch_bounds__(C::threads, 1)
             }
         }
         // the last commit covers every product issued: wait for it before tensor memory is freed
-        if (i > 0 && lane == 0) wait_turn(smem_u32(&sh.s_full[(i - 1) % NB]), (uint32_t)((i - 1) / NB) & 1u, a.hdr);
+        if (i > 0 && lane == 0) wait_landed(smem_u32(&sh.s_full[(i - 1) % NB]), (uint32_t)((i - 1) / NB) & 1u);
     } else if (warp == C::o_warp) {
         // ================================================================ O (+)= P V
         Walk w = walk;
@@ -968,7 +1006,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                 __syncwarp();
             }
         }
-        if (i > 0 && lane == 0) wait_turn(smem_u32(&sh.pv_done[(i - 1) % NB]), (uint32_t)((i - 1) / NB) & 1u, a.hdr);
+        if (i > 0 && lane == 0) wait_landed(smem_u32(&sh.pv_done[(i - 1) % NB]), (uint32_t)((i - 1) / NB) & 1u);
     } else {
         // ================================================================ softmax
         // A row has two threads, each for half of a tile's tokens and half of O's columns, in warps that reach the same quarter of
@@ -976,14 +1014,20 @@ __global__ void __launch_bounds__(C::threads, 1)
         const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
         const uint32_t t_row = tmem + ((uint32_t)(32 * quarter) << 16), t_o = t_row + C::t_o;
         auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(4 + quarter) : "memory"); };
+        // They leave together: one that waits in vain comes to their next exchange all the same, and gives a NaN there that no
+        // arithmetic gives. (A wait in vain carried in a register up to a barrier.red: FP8 rows of 256 dims 307 us, 292 so.)
+        constexpr uint32_t gone = 0xFFC00001u;
         Walk w = walk;
         int seg = 0;
-        bool ok = true;
-        for (; ok && w.next(a, m_tile, g); ++seg) {
+        int out = -1;                                     // the tile whose exchange it is; -2: the other has told
+        for (; w.next(a, m_tile, g); ++seg) {
             const int n = g.tb - g.ta;
             const int node = (m_tile * kRows + row) / a.G, head = kvh * a.G + (m_tile * kRows + row) % a.G;
             const bool valid = node < g.r.T, some = __any_sync(0xffffffffu, valid);
-            if (!wait_warp(&sh.nodes_full, seg)) break;
+            if (!wait_warp(&sh.nodes_full, seg)) {
+                out = g.i0;
+                break;
+            }
             const int lo = sh.lo[min(node, g.r.T - 1)];
             const float scale = F8 ? a.scale_log2 * sh.q_scale[seg & 1][F8 ? row : 0] : a.scale_log2;
             float ref = -INFINITY, l = 0.f;               // the lazy maximum, and this thread's weights' sum relative to it
@@ -992,7 +1036,7 @@ __global__ void __launch_bounds__(C::threads, 1)
             for (int c = 0; c < n; ++c) {
                 const int i = g.i0 + c, t = g.ta + c, m = i % C::metas;
                 if (!wait_warp(&sh.meta_full[m], i / C::metas)) {
-                    ok = false;
+                    out = i;
                     break;
                 }
                 // which of this half's tokens the row attends
@@ -1017,7 +1061,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                 }
                 const bool all = __all_sync(0xffffffffu, see == ~0u || !valid);        // no token to mask in this warp
                 if (!wait_warp(&sh.s_full[i % NB], i / NB)) {
-                    ok = false;
+                    out = i;
                     break;
                 }
                 tc_fence_after();
@@ -1059,7 +1103,12 @@ __global__ void __launch_bounds__(C::threads, 1)
                     const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
                     sh.tops[i & 1][half][row] = mine;
                     meet();                               // both halves have read their scores, too
-                    const float top = fmaxf(mine, sh.tops[i & 1][half ^ 1][row]);
+                    const float theirs = sh.tops[i & 1][half ^ 1][row];
+                    if (__float_as_uint(theirs) == gone) {
+                        out = -2;
+                        break;
+                    }
+                    const float top = fmaxf(mine, theirs);
                     if (top > ref + kLazy) {
                         if (ref != -INFINITY) f = ex2(ref - top);
                         ref = top;
@@ -1096,7 +1145,7 @@ __global__ void __launch_bounds__(C::threads, 1)
                 const bool turned = F8 && (was.x != unit.x || was.y != unit.y);
                 if (c > 0 && __any_sync(0xffffffffu, f != 1.f || turned)) {       // O follows, once the product before it is done
                     if (!wait_warp(&sh.pv_done[(i - 1) % NB], (i - 1) / NB)) {
-                        ok = false;
+                        out = i + 1;
                         break;
                     }
                     tc_fence_after();
@@ -1114,15 +1163,20 @@ __global__ void __launch_bounds__(C::threads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[i % NB])), mbar_arrive(smem_u32(&sh.meta_empty[m]));
             }
-            if (!ok) break;
+            if (out != -1) break;
             // ---- the segment's end: out, or a partial
             const int i = g.i0 + n - 1;
-            if (!wait_warp(&sh.pv_done[i % NB], i / NB) || !wait_warp(&sh.flags_full, seg)) break;
+            if (!wait_warp(&sh.pv_done[i % NB], i / NB) || !wait_warp(&sh.flags_full, seg)) {
+                out = i + 1;
+                break;
+            }
             tc_fence_after();
             if (some) {
                 sh.tops[(i & 1) ^ 1][half][row] = l;      // the sums, where the maxima two tiles back were
                 meet();
-                l = half == 0 ? l + sh.tops[(i & 1) ^ 1][1][row] : sh.tops[(i & 1) ^ 1][0][row] + l;
+                const float theirs = sh.tops[(i & 1) ^ 1][half ^ 1][row];
+                if (__float_as_uint(theirs) == gone) break;
+                l = half == 0 ? l + theirs : theirs + l;
                 meet();
                 const bool whole = g.begins && g.ends;
                 const float by = l == 0.f ? 0.f : (whole ? 1.f / l : 1.f) * (F8 ? 1.f / (1 << (int)kRaise) : 1.f);
@@ -1165,6 +1219,14 @@ __global__ void __launch_bounds__(C::threads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.o_free)), mbar_arrive(smem_u32(&sh.nodes_free));
+        }
+        if (out >= 0) {                                   // segments without rows in this quarter have no exchange
+            bool more = true;
+            while (more && m_tile * kRows + 32 * quarter >= g.r.T * a.G) more = w.next(a, m_tile, g), out = g.i0;
+            if (more) {
+                sh.tops[out & 1][half][row] = __uint_as_float(gone);
+                meet();
+            }
         }
     }
     tc_fence_before();

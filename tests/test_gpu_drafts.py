@@ -334,6 +334,29 @@ def test_tree_captured_replays_with_new_lengths(cuda_lib):
     assert status(ws) == (0, 0)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page,fp8", [(16, 2, 256, 64, False), (16, 2, 256, 5, False), (8, 2, 128, 16, True),
+                                               (16, 2, 256, 5, True), (16, 2, 64, 16, False)])
+@pytest.mark.parametrize("lens,counts", [([30000, 700], [9, 16]), ([150] * 200, [3, 32] * 100)])
+def test_tree_device_timeout_is_reported(cuda_lib, Hq, Hkv, D, page, fp8, lens, counts):
+    """The header's test knob stops every CTA's index warp at its fourth tile: all roles that wait for what it would have named give up
+    within the limit, in the middle of a sequence's tiles and between sequences, and the next call is as if nothing had been."""
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, Hq, Hkv, D, page, fp8, seed=7)
+    cfg = qb.make_paged_config(Hq, Hkv, D, page)
+    ws = qb.tree_workspace(cfg, max(counts))
+    good, good_lse = run_tree(cfg, q, planes, tab, lens, off, parents, max(counts), ws)
+    assert status(ws) == (0, 0)
+    ws.view(torch.int32)[3] = 0x5741171
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    run_tree(cfg, q, planes, tab, lens, off, parents, max(counts), ws)
+    end.record()
+    assert status(ws)[0] == qb.QSA_ERR_DEVICE_TIMEOUT
+    assert begin.elapsed_time(end) < 2 * 250              # one limit of 250 ms for all waits of a CTA, all CTAs at once
+    qb.qsa_workspace_init(ws)
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, parents, max(counts), ws)
+    assert status(ws) == (0, 0) and torch.equal(out, good) and torch.equal(lse, good_lse)
+
+
 # ------------------------------------------------------------------------------------------ accumulated weights
 def run_weights(cfg, q, planes, tab, lens, weights, ws, stream=None, lse=True):
     out = torch.full((q.shape[0], cfg.n_q_heads, cfg.head_dim), 8.0, dtype=torch.bfloat16, device=DEV)
