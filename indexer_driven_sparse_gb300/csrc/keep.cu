@@ -281,11 +281,12 @@ __global__ void __cluster_dims__(kSelectCluster, 1, 1) __launch_bounds__(kSelect
     }
     const int32_t *row = a.table + r * a.ld;
     uint32_t *keys = s.keys + row_at;
-    const int share = (len + kSelectCluster - 1) / kSelectCluster;
-    const int lo = min((int)rank * share, len), hi = min(lo + share, len);    // this CTA's places
+    // this CTA's places, unsigned: a step behind the last place of a row may pass 2^31
+    const uint32_t share = ((uint32_t)len + kSelectCluster - 1) / kSelectCluster;
+    const uint32_t lo = min(rank * share, (uint32_t)len), hi = min(lo + share, (uint32_t)len);
 
     int top = INT32_MIN;
-    for (int j = lo + tid; j < hi; j += kSelectThreads) top = max(top, pos[j]);
+    for (uint32_t j = lo + tid; j < hi; j += kSelectThreads) top = max(top, pos[j]);
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) sums[warp] = (uint32_t)top;
     __syncthreads();
@@ -299,8 +300,8 @@ __global__ void __cluster_dims__(kSelectCluster, 1, 1) __launch_bounds__(kSelect
 
     // ---- the keys, and how many tokens are always kept
     uint32_t always = 0, bad = 0;
-    for (int j = lo + tid; j < hi; j += kSelectThreads) {
-        const int entry = a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size;
+    for (uint32_t j = lo + tid; j < hi; j += kSelectThreads) {
+        const uint32_t entry = a.page_shift >= 0 ? j >> a.page_shift : j / (uint32_t)a.page_size;
         const int page = row[entry], p = pos[j];
         const bool real = (uint32_t)page < (uint32_t)a.n_pages;
         bad |= !real;
@@ -326,7 +327,7 @@ __global__ void __cluster_dims__(kSelectCluster, 1, 1) __launch_bounds__(kSelect
             const int bits = step == 2 ? 10 : kDigit, shift = step == 0 ? 21 : step == 1 ? 10 : 0;
             for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
             __syncthreads();
-            for (int j = lo + tid; j < hi; j += kSelectThreads) {
+            for (uint32_t j = lo + tid; j < hi; j += kSelectThreads) {
                 const uint32_t k = keys[j];
                 if (k != kAlways && (k & known) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
             }
@@ -368,7 +369,7 @@ __global__ void __cluster_dims__(kSelectCluster, 1, 1) __launch_bounds__(kSelect
 
     // ---- keys above and equal, in this CTA and in those before it
     uint32_t above = 0, equal = 0;
-    for (int j = lo + tid; j < hi; j += kSelectThreads) {
+    for (uint32_t j = lo + tid; j < hi; j += kSelectThreads) {
         const uint32_t k = keys[j];
         above += k > key || k == kAlways;
         equal += k == key && k != kAlways;
@@ -380,10 +381,11 @@ __global__ void __cluster_dims__(kSelectCluster, 1, 1) __launch_bounds__(kSelect
     cluster_sum2(mine + 2, rank, passed);
     // tokens kept before place j: keys above + min(need, equal keys); a hole's number is j less those, the filler kept
     // as the x-th of all K has number K - 1 - x from the last
-    for (int j0 = lo; j0 < hi; j0 += kSelectThreads) {
-        const int j = j0 + tid;
-        const uint32_t k = j < hi ? keys[j] : 0u;
-        const bool over = j < hi && (k > key || k == kAlways), same = j < hi && k == key && k != kAlways;
+    for (uint32_t j0 = lo; j0 < hi; j0 += kSelectThreads) {
+        const bool in = j0 + tid < hi;
+        const int j = in ? (int)(j0 + tid) : 0;
+        const uint32_t k = in ? keys[j] : 0u;
+        const bool over = in && (k > key || k == kAlways), same = in && k == key && k != kAlways;
         const uint32_t overs = __ballot_sync(0xffffffffu, over), sames = __ballot_sync(0xffffffffu, same);
         __syncthreads();
         if (lane == 0) sums[2 * warp] = __popc(overs), sums[2 * warp + 1] = __popc(sames);
@@ -396,7 +398,7 @@ __global__ void __cluster_dims__(kSelectCluster, 1, 1) __launch_bounds__(kSelect
         }
         at.x += __popc(overs & ((1u << lane) - 1u));
         at.y += __popc(sames & ((1u << lane) - 1u));
-        if (j < hi) {
+        if (in) {
             const int before = (int)(at.x + min(at.y, need));
             const bool kept = over || (same && at.y < need);
             const int64_t list = r * s.half;

@@ -649,6 +649,30 @@ def test_evict(cuda_lib, lens, budget, first, recent, page, shared, kind):
     check_evict(page, budgets, first, recent, weights, positions, table, lens, ref, planes, result, before)
 
 
+def test_evict_of_a_row_of_all_the_tokens_there_can_be(cuda_lib):
+    """2^31 - 2 tokens, the most that a pool has: three light ones go, the last three take their places."""
+    page, n_pages = 42966, 49981
+    n = page * n_pages
+    assert n == 2 ** 31 - 2
+    weights = torch.ones(1, n, device=DEV)
+    positions = torch.arange(n, dtype=torch.int32, device=DEV)[None]
+    light = [5, 2 ** 30, 2 ** 31 - 10]
+    weights[0, light] = 0.5
+    w_out, p_out = torch.empty_like(weights), torch.empty_like(positions)
+    table, ref = torch.arange(n_pages, dtype=torch.int32, device=DEV)[None], torch.ones(n_pages, dtype=torch.int32, device=DEV)
+    t_out, l_out, r_out = filled(1, n_pages), filled(1), filled(n_pages)
+    ws = qb.keep_workspace(1, n)
+    qb.qsa_evict_tokens(page, ints([n - 3]), 4, 0, weights, positions, table, ints([n]), ref, w_out, p_out, t_out, l_out, r_out, [], ws)
+    assert status(ws) == (0, 0) and l_out.tolist() == [n - 3]
+    assert torch.equal(t_out, table) and torch.equal(r_out, ref)
+    positions[0, light] = ints([n - 3, n - 2, n - 1])
+    positions[0, n - 3:] = -1
+    assert torch.equal(p_out, positions)
+    assert bool((w_out[0, :n - 3] == 1).all()) and not bool(w_out[0, n - 3:].any())
+    del weights, positions, w_out, p_out, ws              # 60 GB that later tests need not work around
+    torch.cuda.empty_cache()
+
+
 def test_evict_rows_out_of_range_are_left(cuda_lib):
     page, lens = 4, [30, 20, 25]
     table, ref = private_pool(lens, page, 2)
