@@ -691,6 +691,63 @@ def test_evict_rows_out_of_range_are_left(cuda_lib):
         assert bool((r_out[mine] == 1).all())
 
 
+def wide_pool(lens, page, seed, shared=0):
+    """private_pool with room for more than 16,384 tokens a row."""
+    table, ref = private_pool(lens, page, seed, shared=shared)
+    wide = np.full((len(lens), max(table.shape[1], 17000 // page)), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    return wide, ref
+
+
+@pytest.mark.parametrize("lens,budget,first,recent,page,shared", [
+    ([10], 0, 0, 0, 4, 0), ([1, 0, 2, 30, 31, 33], 16, 2, 5, 4, 2), ([9000, 5000, 100], 1000, 16, 100, 64, 3),
+    ([64] * 40, 60, 1, 8, 8, 0), ([17000, 40, 20000, 16384, 16385], 12000, 4, 64, 16, 2), ([4080] * 3, 4079, 4, 32, 16, 0)])
+@pytest.mark.parametrize("kind", ["ties", "odd"])
+def test_evict_in_wide_tables(cuda_lib, lens, budget, first, recent, page, shared, kind):
+    """Rows of any length in tables with room for more tokens than one CTA holds in registers."""
+    rng = np.random.default_rng(len(lens) + page)
+    table, ref = wide_pool(lens, page, 2, shared)
+    S, places = len(lens), table.shape[1] * page
+    assert places > 16384
+    w = (rng.integers(0, 3, (S, places)) * 0.5 if kind == "ties" else rng.standard_normal((S, places))).astype(np.float32)
+    if kind == "odd":
+        w.flat[::7], w.flat[1::11], w.flat[2::13], w.flat[4::19] = np.nan, np.inf, -0.0, -np.inf
+    pos = np.stack([rng.permutation(3 * places)[:places] for _ in range(S)])
+    weights, positions = torch.from_numpy(w).to(DEV), ints(pos.tolist())
+    planes = token_planes(len(ref), page, 3)
+    before = [p.clone() for p in planes]
+    budgets = [budget] * S
+    if S > 2:
+        budgets[1] = -1
+    result = run_evict(page, budgets, first, recent, weights, positions, table, lens, ref, planes)
+    check_evict(page, budgets, first, recent, weights, positions, table, lens, ref, planes, result, before)
+
+
+def test_evict_in_wide_tables_leaves_rows_out_of_range_and_bad_pages(cuda_lib):
+    page, lens = 4, [30, 20, 25]
+    table, ref = wide_pool(lens, page, 2)
+    places = table.shape[1] * page
+    weights = torch.rand(3, places, generator=torch.Generator().manual_seed(1)).to(DEV)
+    positions = ints(np.arange(3 * places).reshape(3, -1).tolist())
+    for bad in (-1, places + 1, 2 ** 31 - 1):
+        planes = token_planes(len(ref), page, 3)
+        before = [p.clone() for p in planes]
+        w_out, p_out, t_out, l_out, r_out, ws = run_evict(page, [8] * 3, 1, 2, weights, positions, table, [30, bad, 25], ref, planes)
+        assert status(ws) == (qb.QSA_ERR_DEVICE_BOUNDS, 1) and l_out.tolist() == [8, bad, 8]
+        assert torch.equal(w_out[1], weights[1]) and torch.equal(p_out[1], positions[1])
+        assert np.array_equal(t_out[1].cpu().numpy(), table[1])
+        mine = table[1][table[1] >= 0].tolist()
+        assert all(torch.equal(a[:, mine], b[:, mine]) for a, b in zip(planes, before)) and bool((r_out[mine] == 1).all())
+    broken = table.copy()
+    broken[0, 1], broken[0, 6] = -1, 2 ** 30
+    weights = torch.arange(places, device=DEV, dtype=torch.float32).repeat(3, 1)
+    positions = ints(np.tile(np.arange(places), (3, 1)).tolist())
+    _, p_out, _, l_out, _, ws = run_evict(page, [10] * 3, 0, 0, weights, positions, broken, lens, ref, token_planes(len(ref), page, 3))
+    assert status(ws) == (qb.QSA_ERR_DEVICE_BOUNDS, 0) and l_out.tolist() == [10] * 3
+    for r, n in enumerate(lens):
+        assert sorted(p_out[r, :10].tolist()) == list(range(n - 10, n))
+
+
 def test_accept_moves_nothing_into_shared_pages(cuda_lib):
     """A row forked with its drafts in full pages that both rows name: what would move into them stays, in this row alone;
     a path that is in place already may be kept."""
