@@ -130,20 +130,13 @@ __global__ void __launch_bounds__(kKeepThreads) accept_kernel(KeepArgs a, Accept
     const int32_t *row = a.table + r * a.ld;
     const bool ok = len >= 0 && len <= a.ld * a.page_size && off >= 0 && T >= 0 && T <= QSA_MAX_DRAFT && (int64_t)off + T <= d.N &&
                     T <= len && last >= -1 && last < T;
-    if (ok && tid < T) parent[tid] = d.parent[off + tid];
-    __syncthreads();
+    const int mine = ok && tid < T ? d.parent[off + tid] : -1;
+    if (ok && tid < T) parent[tid] = mine;
+    const bool lost = __syncthreads_or(ok && tid < T && (mine < -1 || mine >= tid)) != 0;     // on the path or not
     if (tid == 0) {
-        int n = ok ? 0 : -1;
-        if (ok)
-            for (int i = last; i >= 0;) {            // upwards; a parent is below its child, so this ends
-                node[n++] = i;
-                const int p = parent[i];
-                if (p < -1 || p >= i) {
-                    n = -1;
-                    break;
-                }
-                i = p;
-            }
+        int n = ok && !lost ? 0 : -1;
+        if (n == 0)
+            for (int i = last; i >= 0; i = parent[i]) node[n++] = i;      // upwards; a parent is below its child, so this ends
         found[0] = n;
         found[1] = 0;
     }

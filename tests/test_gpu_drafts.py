@@ -590,6 +590,23 @@ def test_accept_leaves_rows_out_of_range_as_they_are(cuda_lib, what):
         assert torch.equal(got, w)
 
 
+@pytest.mark.parametrize("parent,last", [([-1, 0, 2, 1], 1), ([-1, 0, -2, 1], 3), ([-1, 0, 1, 7], -1), ([0, -1, 1, -1], 3)])
+def test_accept_leaves_rows_with_any_parent_out_of_range(cuda_lib, parent, last):
+    """A parent out of range that the accepted path does not meet; the row beside it is cut."""
+    page, lens, off = 4, [10, 12], [0, 4, 8]
+    table, ref = private_pool(lens, page, 1)
+    planes = token_planes(len(ref), page, 1)
+    want = [p.clone() for p in planes]
+    t_out, l_out, r_out, ws = filled(2, table.shape[1]), filled(2), filled(len(ref)), qb.keep_workspace(2)
+    positions = ints(np.arange(24).reshape(2, 12).tolist())
+    qb.qsa_accept_drafts(page, ints(off), ints(parent + [-1, 0, 1, 2]), ints([last, 1]), ints(table.tolist()), ints(lens),
+                         ints(ref.tolist()), t_out, l_out, r_out, planes, ws, positions)
+    assert status(ws) == (qb.QSA_ERR_DEVICE_BOUNDS, 0) and l_out.tolist() == [10, 10]
+    want_t, want_r = T.release(table, ref, lens, [10, 10], page)
+    assert np.array_equal(t_out.cpu().numpy(), want_t) and np.array_equal(r_out.cpu().numpy(), want_r)
+    assert positions.flatten().tolist() == list(range(24)) and all(torch.equal(a, b) for a, b in zip(planes, want))
+
+
 # ------------------------------------------------------------------------------------------ evicting
 def run_evict(page, budget, first, recent, weights, positions, table, lens, ref, planes, ws=None):
     S, places = weights.shape
