@@ -1223,6 +1223,35 @@ def test_tree_odd_keys_of_masked_tokens_change_nothing(cuda_lib, value):
     assert torch.equal(out[[0, 3, 4, 5]], good[[0, 3, 4, 5]])
 
 
+@pytest.mark.parametrize("D", [256, 128])
+@pytest.mark.parametrize("page", [8, 3])
+@pytest.mark.parametrize("what", ["code", "inf", "nan"])
+def test_tree_odd_keys_of_masked_tokens_change_nothing_over_fp8_rows(cuda_lib, D, page, what):
+    """A draft's K code or K scale that is not finite, and those of tokens that lie before every window or behind the row's end."""
+    n, T_, Hq, window = 200, 6, 8, 70
+    q, planes, values, tab, table, off, _ = tree_inputs([n], [T_], Hq, 1, D, page, True, seed=4, spare_rows=0)
+    parents = [[-1, 0, 1, -1, 3, 4]]
+    cfg = qb.make_paged_config(Hq, 1, D, page, window=window)
+    ws = qb.tree_workspace(cfg, T_)
+    good, good_lse = run_tree(cfg, q, planes, tab, [n], off, parents, T_, ws)
+    slots = P.slots_of(table[0], n, page)
+    places = [n - T_ + 1, n - T_ - window, 3] + [n] * (n % page != 0)
+    for place in places:
+        slot = int(slots[place]) if place < n else int(slots[n - 1]) + 1
+        if what == "code":
+            planes[0].flatten(0, 1)[slot, 0, D - 1] = 0x7F
+        else:
+            planes[1].flatten(0, 1)[slot, 0, 0] = float(what)
+    out, lse = run_tree(cfg, q, planes, tab, [n], off, parents, T_, ws)
+    seen = [bool(set(places) & set(at)) for at in T.attended(n, parents[0], window)]
+    assert seen == [False, True, True, False, False, False] and status(ws) == (0, 0)
+    for i in range(T_):
+        if seen[i]:
+            assert bool(torch.isnan(out[i]).any())
+        else:
+            assert torch.equal(out[i], good[i]) and torch.equal(lse[i], good_lse[i])
+
+
 # ------------------------------------------------------------------------------------------ limits
 @pytest.mark.parametrize("Hq,Hkv,D,drafts", [(160, 160, 64, 3), (16, 1, 256, 128), (64, 4, 128, 100), (620, 310, 64, 2)])
 def test_tree_of_many_heads_and_drafts(cuda_lib, Hq, Hkv, D, drafts):
