@@ -728,17 +728,21 @@ QSA_API size_t qsa_tree_workspace_size(const qsa_paged_config *cfg, int32_t max_
  * drafted ancestor) has position n - T + d - 1 and attends positions above that - window; the cached tokens' positions
  * are their places.
  *   q [N] rows of n_q_heads x head_dim, q_ld elements apart (a multiple of 8), 16-byte aligned; draft_off [B + 1],
- *   ascending, within [0, N]; parent [N]; max_draft: the most drafted tokens of a sequence, 1 .. QSA_MAX_DRAFT;
+ *   ascending, within [0, N]; parent [N]; max_draft: the most drafted tokens of a sequence, 1 .. QSA_MAX_DRAFT (no more
+ *   than there can be: the GPU is split among that many tokens' rows, so 4 drafts with max_draft 128 take 2 to 4.5 times as
+ *   long as with 4);
  *   out [N][n_q_heads][head_dim] bf16, 16-byte aligned; lse [N][n_q_heads] fp32 or NULL; k_cache, v_cache 16-byte
  *   aligned device memory. Rows of out and lse that no sequence names stay as they were.
  * fp32 scores, softmax and sums; the weights enter the second product as bf16 (each rounded by at most 2^-8 of it, as out
- * itself is). V values that are not finite reach the tokens that attend them, and no others.
+ * itself is). V values that are not finite reach the tokens that attend them, and no others (as that value, or as NaN where
+ * the weight is zero in that many bits).
  * Device checks (QSA_ERR_DEVICE_BOUNDS is recorded): a sequence whose offsets do not ascend within [0, N], or begin below an
  * earlier one's, attends nothing and its rows are not written; one with T > max_draft, T > n or n > table_ld page_size
  * attends nothing (out = 0, lse = -inf); a parent outside [-1, own place) counts as -1; a page outside [0, n_pages) has
  * its tokens left out. A token that attends nothing gets out = 0 and
- * lse = -inf. Results do not depend on timing: the split depends on the lengths, max_draft and the device alone. The first
- * call on a device queries its occupancy and should precede stream capture. */
+ * lse = -inf. Results do not depend on timing: the split depends on the lengths, max_draft and the device alone. A wait inside
+ * the kernel that makes no progress for 250 ms ends the call with QSA_ERR_DEVICE_TIMEOUT. The first call on a device queries
+ * its occupancy and should precede stream capture. */
 QSA_API qsa_status qsa_tree_decode(const qsa_paged_config *cfg, const qsa_bf16 *q, int64_t q_ld,
                                    const int32_t *draft_off, const int32_t *parent, int32_t N, int32_t max_draft,
                                    const qsa_bf16 *k_cache, const qsa_bf16 *v_cache, int64_t n_pages,
@@ -820,7 +824,8 @@ QSA_API qsa_status qsa_accept_drafts_weights(int32_t page_size, const int32_t *d
  * dropping them would free nothing), P tokens; of the others it keeps the heaviest, equal weights by lower place, until
  * K = max(budget[r], P) stay. Only kept tokens at places >= K move: in ascending order into the places below K that
  * dropped tokens held, ascending, in every plane, with their weights and positions. Pages that hold no token any more
- * are given back (ref_out, table_out as in qsa_accept_drafts).
+ * are given back (ref_out, table_out as in qsa_accept_drafts). Rows are cut fastest where tokens_ld is at most 16,384: with
+ * more room another kernel takes about three times as long for rows of 4,000 tokens.
  *   weights [n_rows][tokens_ld] fp32 (a NaN counts as the lightest, -0 as 0), positions [n_rows][tokens_ld] int32;
  *   weights_out, positions_out: other arrays of their shape, 0 and -1 behind a row's new length; budget [n_rows];
  *   first, recent >= 0; the rest as in qsa_accept_drafts.

@@ -66,7 +66,7 @@ struct TreeCfg {
     // tensor memory columns: O, the queries (bf16 rows; with FP8 rows they are in shared memory), buffers of scores
     static constexpr uint32_t t_o = 0, t_q = F8 ? 0u : (uint32_t)D, t_s = D == 256 && !F8 ? 384 : 256, s_cols = SG * kTile;
     static constexpr int buffers = (512 - t_s) / s_cols;
-    // tiles whose slots and scales are known: 4, 6, 8 and 16 of them took 270, 264, 254 and 251 us over 128 ragged sequences of FP8 rows
+    // tiles whose slots and scales are known: 4, 6, 8 and 16 of them took 270, 264, 254 and 251 us over 64 ragged sequences of FP8 rows
     static constexpr int metas = D == 128 ? 16 : 8;
     // 20 warps of 96 registers; the query warps' numbers modulo 4 are the four quarters of tensor memory's lanes
     static constexpr int softmax = 256, q_threads = F8 ? 64 : 128, workers = F8 ? 192 : 160;
@@ -1366,6 +1366,9 @@ cudaError_t launch_as(const TreeArgs &a, int run, cudaStream_t st) {
         return e != cudaSuccess ? e : cudaErrorInvalidDevice;
     }
     TreePlan plan{};
+    // The M tiles that max_draft may need: the host does not know the drafts that there are, and CTAs of M tiles without rows have
+    // nothing to do. 4 drafts in each of 32 sequences of 32,768 tokens, 8 heads a KV head, 2 KV heads: 363 us with max_draft 4, 365
+    // with 16, 416 with 32, 791 with 64, 1,635 with 128.
     plan.m_tiles = m_tiles_of(a.G, a.max_draft);
     plan.ranges = std::max(1, ctas / (a.Hkv * plan.m_tiles));
     // the least length of a part: one sequence of 4,096 tokens took 19.9, 19.2, 20.6 and 24.0 us with 1, 2, 4 and 8 tiles
