@@ -1029,7 +1029,8 @@ __global__ void __launch_bounds__(C::threads, 1)
                 break;
             }
             const int lo = sh.lo[min(node, g.r.T - 1)];
-            const float scale = F8 ? a.scale_log2 * sh.q_scale[seg & 1][F8 ? row : 0] : a.scale_log2;
+            // above zero: a masked token's -infinity times it stays one (queries of zeros have the scale 2^-126)
+            const float scale = F8 ? fmaxf(a.scale_log2 * sh.q_scale[seg & 1][F8 ? row : 0], __uint_as_float(1u)) : a.scale_log2;
             float ref = -INFINITY, l = 0.f;               // the lazy maximum, and this thread's weights' sum relative to it
             float2 unit = make_float2(0.f, 0.f);          // FP8: O is in units of these over 2^kRaise
 #pragma unroll 1

@@ -1252,6 +1252,20 @@ def test_tree_odd_keys_of_masked_tokens_change_nothing_over_fp8_rows(cuda_lib, D
             assert torch.equal(out[i], good[i]) and torch.equal(lse[i], good_lse[i])
 
 
+@pytest.mark.parametrize("Hq,D,fp8", [(8, 256, True), (8, 128, True), (8, 256, False), (4, 64, False)])
+@pytest.mark.parametrize("scale", [0.0, 1e-9, 1e-38])
+def test_tree_queries_of_zeros_take_the_mean(cuda_lib, Hq, D, fp8, scale):
+    """Every score is zero, whatever the scale: masked tokens stay masked beside them."""
+    lens, counts = [150, 70], [5, 3]
+    q, planes, values, tab, table, off, parents = tree_inputs(lens, counts, Hq, 1, D, 16, fp8, seed=4)
+    q[:, 1].zero_()
+    q[3].zero_()
+    cfg = qb.make_paged_config(Hq, 1, D, 16, softmax_scale=scale)
+    ws = qb.tree_workspace(cfg, 5)
+    out, lse = run_tree(cfg, q, planes, tab, lens, off, parents, 5, ws)
+    check_tree(out, lse, q, values, table, lens, off, parents, 16, float(np.float32(scale)) or D ** -0.5, 0, fp8)
+
+
 # ------------------------------------------------------------------------------------------ limits
 @pytest.mark.parametrize("Hq,Hkv,D,drafts", [(160, 160, 64, 3), (16, 1, 256, 128), (64, 4, 128, 100), (620, 310, 64, 2)])
 def test_tree_of_many_heads_and_drafts(cuda_lib, Hq, Hkv, D, drafts):
